@@ -7,6 +7,7 @@
 
 #include "../../include/kda.h"
 #include "kda_internal.h"
+#include "layer.h"
 
 static_assert(KDA_WORKSPACE_BYTES_PER_UNIT == kda::kWsBytesPerUnit, "workspace size in kda.h");
 static_assert(KDA_ERR_TIMEOUT == kda::kErrTimeout && KDA_ERR_RANGE == kda::kErrRange, "device error codes");
@@ -83,8 +84,11 @@ kda_status validate(const void *q, const void *k, const void *v, const void *g, 
     return KDA_OK;
 }
 
-// Memory pool for kda_fwd's workspaces, one per device, created on first use and
-// kept for the life of the process.  Its release threshold keeps freed blocks
+}  // namespace
+
+namespace kda {
+// Memory pool for the workspaces of the library's calls, one per device, created on
+// first use and kept for the life of the process.  Its release threshold keeps freed blocks
 // mapped, so the stream-ordered allocation of a call after the first is cheap;
 // the device's default pool is left untouched.
 cudaMemPool_t workspace_pool(int device) {
@@ -107,9 +111,6 @@ cudaMemPool_t workspace_pool(int device) {
     return pools[device];
 }
 
-}  // namespace
-
-namespace kda {
 // The token recurrence with the gate that has no lower bound (csrc/kda_recur.cu).
 cudaError_t launch_recur(const Params &p, cudaStream_t stream);
 
@@ -124,6 +125,19 @@ cudaError_t sm_count(int &sms) {
     sms = count[dev];
     return e;
 }
+
+// The device error word's address on the current device, looked up once per device.
+cudaError_t device_error_word(int *&err) {
+    static std::atomic<bool> done[kMaxDevices];
+    static int *err_of[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kMaxDevices) return cudaGetSymbolAddress(reinterpret_cast<void **>(&err), g_kda_error);
+    e = once_per_device(done, [&](int d) { return cudaGetSymbolAddress(reinterpret_cast<void **>(&err_of[d]), g_kda_error); });
+    err = err_of[dev];
+    return e;
+}
 }  // namespace kda
 
 namespace {
@@ -132,22 +146,8 @@ namespace {
 // then its scratch, tsplit_scratch_bytes long); pool_sms > 0: the persistent pool kernel
 // on that many SMs (p.ws its ring, pool_scratch_bytes long).
 kda_status launch(kda::Params &p, void *stream, int64_t tsplit = 0, int pool_sms = 0) {
-    // the device error word's address, looked up once per device
-    static std::atomic<bool> done[kda::kMaxDevices];
-    static int *err_of[kda::kMaxDevices];
     int *err = nullptr;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
-    if (kda::once_per_device(done, [&](int d) {
-            return cudaGetSymbolAddress(reinterpret_cast<void **>(&err_of[d < kda::kMaxDevices ? d : 0]),
-                                        g_kda_error);
-        }) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    if (dev < kda::kMaxDevices) {
-        err = err_of[dev];
-    } else if (cudaGetSymbolAddress(reinterpret_cast<void **>(&err), g_kda_error) != cudaSuccess) {
-        return KDA_ERR_CUDA;
-    }
+    if (kda::device_error_word(err) != cudaSuccess) return KDA_ERR_CUDA;
     p.err = err;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     cudaError_t e;
@@ -213,7 +213,7 @@ kda_status kda_fwd(const void *q, const void *k, const void *v, const void *g, c
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     int device = 0;
     if (cudaGetDevice(&device) != cudaSuccess) return KDA_ERR_CUDA;
-    cudaMemPool_t pool = workspace_pool(device);
+    cudaMemPool_t pool = kda::workspace_pool(device);
     if (!pool) return KDA_ERR_CUDA;
     // Few (sequence, head) units on a long fixed-length call: the sequence-parallel path
     int sms = 0;
@@ -283,7 +283,7 @@ kda_status kda_fwd_unbounded(const void *q, const void *k, const void *v, const 
         return kda::launch_recur(p, cs) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     int device = 0;
     if (cudaGetDevice(&device) != cudaSuccess) return KDA_ERR_CUDA;
-    cudaMemPool_t pool = workspace_pool(device);
+    cudaMemPool_t pool = kda::workspace_pool(device);
     if (!pool) return KDA_ERR_CUDA;
     const size_t bytes = tsplit > 0 ? kda::tsplit_scratch_bytes(p, tsplit, sms) : kda::pool_scratch_bytes(p, sms);
     void *ws = nullptr;
@@ -324,7 +324,7 @@ kda_status kda_bwd(const void *q, const void *k, const void *v, const void *g, c
     if (p.n_seqs * p.H > 0) {
         int device = 0;
         if (cudaGetDevice(&device) != cudaSuccess) return KDA_ERR_CUDA;
-        cudaMemPool_t pool = workspace_pool(device);
+        cudaMemPool_t pool = kda::workspace_pool(device);
         if (!pool) return KDA_ERR_CUDA;
         if (cudaMallocFromPoolAsync(&ws, bytes, pool, cs) != cudaSuccess) return KDA_ERR_CUDA;
     }
@@ -381,11 +381,11 @@ const char *kda_status_string(int status) {
     switch (status) {
         case KDA_OK: return "KDA_OK";
         case KDA_ERR_NULL: return "KDA_ERR_NULL: a required pointer is NULL";
-        case KDA_ERR_DTYPE: return "KDA_ERR_DTYPE: bad state dtype";
+        case KDA_ERR_DTYPE: return "KDA_ERR_DTYPE: bad state or element dtype";
         case KDA_ERR_SHAPE: return "KDA_ERR_SHAPE: inconsistent sizes";
-        case KDA_ERR_UNSUPPORTED: return "KDA_ERR_UNSUPPORTED: only K = V = 128 is supported";
-        case KDA_ERR_ALIGN: return "KDA_ERR_ALIGN: tensor pointer not 16-byte aligned";
-        case KDA_ERR_VALUE: return "KDA_ERR_VALUE: lower_bound outside [-5, 0], non-finite scale or workspace too small";
+        case KDA_ERR_UNSUPPORTED: return "KDA_ERR_UNSUPPORTED: only K = V = 128 (delta rule) and 2 to 4 taps (short convolution) are supported";
+        case KDA_ERR_ALIGN: return "KDA_ERR_ALIGN: tensor pointer not aligned (16 bytes; the element for the recurrence, norm and convolution)";
+        case KDA_ERR_VALUE: return "KDA_ERR_VALUE: lower_bound outside [-5, 0], non-finite scale, bad eps or activation, or workspace too small";
         case KDA_ERR_CUDA: return "KDA_ERR_CUDA: CUDA call or launch failed";
         case KDA_ERR_TIMEOUT: return "KDA_ERR_TIMEOUT: a bounded device wait expired";
         case KDA_ERR_RANGE: return "KDA_ERR_RANGE: an fp16 operand (v, state, U, W, T', M; q, k on short steps) exceeded 65504";
@@ -403,6 +403,6 @@ kda_status kda_get_device_status(void *stream) {
     return h == 0 ? KDA_OK : static_cast<kda_status>(h);
 }
 
-int kda_version(void) { return 101; }
+int kda_version(void) { return 102; }
 
 }  // extern "C"

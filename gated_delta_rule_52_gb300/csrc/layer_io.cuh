@@ -1,0 +1,121 @@
+// Typed loads and stores, and the small arithmetic the operators around the delta rule
+// share.  All arithmetic on tensor values is fp32; a value is rounded to its tensor's type
+// once, when it is stored.
+#pragma once
+
+#include <cstdint>
+#include <type_traits>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "layer.h"
+
+namespace kda {
+namespace layer {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f(float v) { return v; }
+template <typename E> __device__ __forceinline__ E from_f(float v);
+template <> __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ float from_f(float v) { return v; }
+
+// V consecutive elements as one register group; loads and stores of V * sizeof(E) bytes
+// (2 to 16, alignment the caller's concern).
+template <typename E, int V> struct alignas(sizeof(E) * V) Pack { E e[V]; };
+
+template <typename E, int V>
+__device__ __forceinline__ Pack<E, V> ld_pack(const E *p) { return *reinterpret_cast<const Pack<E, V> *>(p); }
+template <typename E, int V>
+__device__ __forceinline__ void unpack(const Pack<E, V> &a, float (&f)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = to_f(a.e[j]);
+}
+template <typename E, int V>
+__device__ __forceinline__ void ld_f(const E *p, float (&f)[V]) { unpack<E, V>(ld_pack<E, V>(p), f); }
+template <typename E, int V>
+__device__ __forceinline__ void st_f(E *p, const float (&f)[V]) {
+    Pack<E, V> a;
+#pragma unroll
+    for (int j = 0; j < V; ++j) a.e[j] = from_f<E>(f[j]);
+    *reinterpret_cast<Pack<E, V> *>(p) = a;
+}
+
+// Recurrent state of either type.
+__device__ __forceinline__ float ld_state(const void *p, int type, int64_t at) {
+    return type == kStateBF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[at])
+                              : static_cast<const float *>(p)[at];
+}
+__device__ __forceinline__ void st_state(void *p, int type, int64_t at, float v) {
+    if (type == kStateBF16) static_cast<__nv_bfloat16 *>(p)[at] = __float2bfloat16_rn(v);
+    else static_cast<float *>(p)[at] = v;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// sigma(x) = 1 / (1 + e^-x); e^-x overflows to infinity for very negative x, whose
+// reciprocal is the right 0.
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
+// sigma(x) and its slope sigma(x) sigma(-x) = t / (1 + t)^2, t = e^-|x|: no overflow, and
+// the slope keeps its relative accuracy in both tails.
+__device__ __forceinline__ void sigmoid_slope(float x, float &s, float &slope) {
+    const float t = ex2(-kLog2e * fabsf(x)), r = rcp(1.f + t), tr = t * r;
+    s = x >= 0.f ? r : tr;
+    slope = tr * r;
+}
+
+// First n in [0, N] with cu[n+1] > row (cu non-decreasing, cu[0] = 0): the sequence of a
+// packed row.  The result is at most N - 1 whatever cu holds.
+__device__ __forceinline__ int64_t seq_of_row(const int64_t *cu, int64_t N, int64_t row) {
+    int64_t lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (cu[mid + 1] > row) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+// Rows [lo, hi) of sequence n, clamped to the packed rows.
+template <typename P>
+__device__ __forceinline__ void seq_rows(const P &p, int64_t n, int64_t &lo, int64_t &hi) {
+    if (p.cu_seqlens) {
+        lo = max(p.cu_seqlens[n], (int64_t)0);
+        hi = min(p.cu_seqlens[n + 1], p.rows);
+    } else {
+        lo = n * p.T;
+        hi = lo + p.T;
+    }
+}
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline size_t dtype_bytes(int dtype) { return dtype == kFP32 ? 4 : 2; }
+
+// Calls f with a null pointer of the element type of a dtype code.
+template <typename F>
+auto with_dtype(int dtype, F &&f) {
+    if (dtype == kBF16) return f(static_cast<__nv_bfloat16 *>(nullptr));
+    if (dtype == kFP16) return f(static_cast<__half *>(nullptr));
+    return f(static_cast<float *>(nullptr));
+}
+
+}  // namespace layer
+}  // namespace kda

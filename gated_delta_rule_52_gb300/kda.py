@@ -41,7 +41,8 @@ KDA_STATE_FP32 = 2
 # Every symbol include/kda.h declares.
 EXPORTED = ("kda_fwd", "kda_fwd_ws", "kda_fwd_unbounded", "kda_workspace_size", "kda_workspace_size_pool",
             "kda_status_string", "kda_get_device_status", "kda_version", "kda_fwd_static",
-            "kda_bwd")
+            "kda_bwd", "kda_glr_fwd", "kda_glr_bwd", "kda_layer_norm_fwd", "kda_layer_norm_bwd",
+            "kda_short_conv_fwd", "kda_short_conv_bwd")
 
 # Workspace bytes per (sequence, head) of kda_fwd_ws (KDA_WORKSPACE_BYTES_PER_UNIT).
 WORKSPACE_BYTES_PER_UNIT = 99328
@@ -83,6 +84,18 @@ def lib() -> ctypes.CDLL:
             L.kda_bwd.argtypes = [vp, vp, vp, vp, vp, f, vp, vp, f, ci, vp, ci, vp, vp, vp, i64,
                                   i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp]
             L.kda_bwd.restype = ci
+            L.kda_glr_fwd.argtypes = [vp, vp, vp, i64, i64, i64, vp, i64, ci, vp, vp, f, ci, vp, vp, ci,
+                                      vp, i64, i64, i64, i64, i64, vp, vp]
+            L.kda_glr_bwd.argtypes = [vp, vp, vp, i64, i64, i64, ci, vp, vp, f, ci, vp, ci, vp, vp, i64,
+                                      vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp]
+            L.kda_layer_norm_fwd.argtypes = [vp, i64, vp, vp, f, vp, i64, vp, vp, ci, i64, i64, vp]
+            L.kda_layer_norm_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, ci, i64, i64, vp]
+            L.kda_short_conv_fwd.argtypes = [vp, i64, vp, vp, ci, vp, i64, ci, vp, vp, vp, i64, i64, i64,
+                                             i64, i64, vp]
+            L.kda_short_conv_bwd.argtypes = [vp, i64, vp, vp, ci, ci, vp, vp, i64, vp, vp, i64, i64, i64,
+                                             i64, i64, vp, vp, vp, vp, vp]
+            for name in EXPORTED[-6:]:   # the operators around the delta rule
+                getattr(L, name).restype = ci
             L.kda_workspace_size.argtypes = [i64, i64]
             L.kda_workspace_size.restype = ctypes.c_size_t
             L.kda_workspace_size_pool.argtypes = [i64, i64]

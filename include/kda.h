@@ -276,6 +276,134 @@ kda_status kda_fwd_static(const void *q, const void *k, const void *v, const voi
                           int64_t num_seqs, int64_t B, int64_t T, int64_t H, int64_t K, int64_t V,
                           void *stream);
 
+/*
+ * Operators around the delta rule: what a layer needs beside kda_fwd.  They share these
+ * rules.  Tensors are in one of the element types of kda_dtype, all tensors of a call in
+ * the same one; parameters (A_log, dt_bias, weights, biases), statistics and parameter
+ * gradients are fp32.  The channels of a token are contiguous; a token tensor's rows
+ * (B*T packed token rows) lie a caller-given number of elements apart, so that a slice of
+ * a wider tensor is read in place (inputs may also repeat a row: stride 0).  Written
+ * tensors must not overlap inputs unless stated, and their row stride is at least the
+ * row's width.  Pointers need the alignment of their element only; 16-byte aligned
+ * pointers and strides that are multiples of 16 bytes run the widest loads.  At most
+ * 2^31 - 1 packed rows, and at most 2^31 - 1 elements of a state.  cu_seqlens, num_seqs,
+ * B and T are as for kda_fwd; sequences of no token are allowed (their final state is
+ * their initial state).  Values of one sequence, NaN and infinity included, never reach
+ * another.  The calls are asynchronous on `stream`, take their workspace (if any) from
+ * kda_fwd's pool, and give the same bits for the same inputs every time.  They return
+ * KDA_OK, the argument errors of kda_fwd that apply (nothing enqueued), KDA_ERR_DTYPE for
+ * an unknown element type, or KDA_ERR_CUDA.
+ */
+
+/* Element type of a token tensor of the operators below. */
+typedef enum {
+    KDA_DTYPE_BF16 = 1,
+    KDA_DTYPE_FP32 = 2,
+    KDA_DTYPE_FP16 = 3
+} kda_dtype;
+
+/* Packed rows from one checkpoint of the gated linear recurrence to the next. */
+#define KDA_GLR_CHECKPOINT_ROWS 64
+
+/*
+ * kda_glr_fwd — gated linear recurrence, the delta rule's vector-state sibling: per
+ * channel c of head h, in fp32,
+ *
+ *   h_t = exp(gk_t) h_{t-1} + sigmoid(i_t) x_t,   out_t = h_t
+ *   gk_t = lower_bound * sigmoid(exp(A_log[h]) * (g_t + dt_bias[h][c]))    or, `unbounded`,
+ *   gk_t = -exp(A_log[h]) * softplus(g_t + dt_bias[h][c])
+ *
+ * (kda_fwd's gates).  A token with i = -infinity adds nothing, one with g = -infinity
+ * keeps the state as it is.
+ *   x, i, g        [B*T, H*K] value, input gate logits, gate before activation; rows
+ *                  x_stride, i_stride, g_stride elements apart
+ *   out            [B*T, H*K], rows out_stride apart
+ *   dtype          kda_dtype of x, i, g and out
+ *   A_log fp32 [H], dt_bias fp32 [H, K]; any H and K
+ *   initial_state, final_state   [N, H, K] of state_dtype, or NULL (zero; not written);
+ *                  they may be the same buffer
+ *   checkpoints    fp32 [ceil(B*T / KDA_GLR_CHECKPOINT_ROWS), H, K] or NULL: the state
+ *                  that every 64th packed row starts from (a sequence's first row starts
+ *                  from its initial state), for kda_glr_bwd
+ */
+kda_status kda_glr_fwd(const void *x, const void *i, const void *g, int64_t x_stride, int64_t i_stride,
+                       int64_t g_stride, void *out, int64_t out_stride, int dtype, const float *A_log,
+                       const float *dt_bias, float lower_bound, int unbounded, const void *initial_state,
+                       void *final_state, int state_dtype, const int64_t *cu_seqlens, int64_t num_seqs, int64_t B,
+                       int64_t T, int64_t H, int64_t K, float *checkpoints, void *stream);
+
+/*
+ * kda_glr_bwd — gradients of L = sum(dout * out) + sum(dfinal * final_state) with respect
+ * to kda_glr_fwd's inputs, states recomputed in fp32.
+ *   checkpoints    what kda_glr_fwd left for the same inputs, or NULL (recomputed)
+ *   dout           [B*T, H*K], rows dout_stride apart; dfinal fp32 [N, H, K] or NULL (zero)
+ *   dx, di, dg     [B*T, H*K] of dtype, contiguous
+ *   dA_log [H], ddt_bias [H, K], dinitial_state [N, H, K] (or NULL), fp32
+ */
+kda_status kda_glr_bwd(const void *x, const void *i, const void *g, int64_t x_stride, int64_t i_stride,
+                       int64_t g_stride, int dtype, const float *A_log, const float *dt_bias, float lower_bound,
+                       int unbounded, const void *initial_state, int state_dtype, const float *checkpoints,
+                       const void *dout, int64_t dout_stride, const float *dfinal, const int64_t *cu_seqlens,
+                       int64_t num_seqs, int64_t B, int64_t T, int64_t H, int64_t K, void *dx, void *di, void *dg,
+                       float *dA_log, float *ddt_bias, float *dinitial_state, void *stream);
+
+/*
+ * kda_layer_norm_fwd — out = (x - mean) * rstd * weight + bias over rows of D elements,
+ * rstd = 1 / sqrt(variance + eps), the variance taken about the mean.
+ *   x, out         [rows, D], rows x_stride, out_stride elements apart; out may be x
+ *   weight, bias   fp32 [D], each may be NULL (1, 0)
+ *   mean, rstd     fp32 [rows] or NULL (not written), for kda_layer_norm_bwd
+ * KDA_ERR_VALUE for eps negative or not finite.
+ */
+kda_status kda_layer_norm_fwd(const void *x, int64_t x_stride, const float *weight, const float *bias, float eps,
+                              void *out, int64_t out_stride, float *mean, float *rstd, int dtype, int64_t rows,
+                              int64_t D, void *stream);
+
+/*
+ * kda_layer_norm_bwd — gradients of sum(dout * out) with respect to x, weight and bias.
+ *   dout, x        [rows, D] with their row strides; mean, rstd as the forward wrote them
+ *   dx             [rows, D] of dtype, contiguous
+ *   dweight, dbias fp32 [D], each may be NULL (not wanted)
+ */
+kda_status kda_layer_norm_bwd(const void *dout, int64_t dout_stride, const void *x, int64_t x_stride,
+                              const float *weight, const float *mean, const float *rstd, void *dx, float *dweight,
+                              float *dbias, int dtype, int64_t rows, int64_t D, void *stream);
+
+/* Activation after the short convolution. */
+typedef enum {
+    KDA_ACTIVATION_NONE = 0,
+    KDA_ACTIVATION_SILU = 1
+} kda_activation;
+
+/*
+ * kda_short_conv_fwd — causal depthwise convolution over a sequence's last W rows,
+ *
+ *   y_t[c] = bias[c] + sum_j weight[c][j] * x_{t-(W-1)+j}[c],   out = act(y)
+ *
+ * with 2 <= W <= 4 (else KDA_ERR_UNSUPPORTED); rows before a sequence's first are those of
+ * its initial state.
+ *   x, out         [B*T, D], rows x_stride, out_stride elements apart
+ *   weight         fp32 [D, W]; bias fp32 [D] or NULL
+ *   initial_state, final_state   [N, W-1, D] of dtype, the last W-1 input rows, oldest
+ *                  first, or NULL (zero rows; not written); they may be the same buffer
+ */
+kda_status kda_short_conv_fwd(const void *x, int64_t x_stride, const float *weight, const float *bias, int activation,
+                              void *out, int64_t out_stride, int dtype, const void *initial_state, void *final_state,
+                              const int64_t *cu_seqlens, int64_t num_seqs, int64_t B, int64_t T, int64_t D, int64_t W,
+                              void *stream);
+
+/*
+ * kda_short_conv_bwd — gradients of L = sum(dout * out) + sum(dfinal * final_state).
+ *   dout           [B*T, D], rows dout_stride apart; dfinal fp32 [N, W-1, D] or NULL
+ *   dx             [B*T, D] of dtype, contiguous
+ *   dweight [D, W], dbias [D] (or NULL), dinitial_state [N, W-1, D] (or NULL), fp32
+ */
+kda_status kda_short_conv_bwd(const void *x, int64_t x_stride, const float *weight, const float *bias, int activation,
+                              int dtype, const void *initial_state, const void *dout, int64_t dout_stride,
+                              const float *dfinal, const int64_t *cu_seqlens, int64_t num_seqs, int64_t B, int64_t T,
+                              int64_t D, int64_t W, void *dx, float *dweight, float *dbias, float *dinitial_state,
+                              void *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *kda_status_string(int status);
 
