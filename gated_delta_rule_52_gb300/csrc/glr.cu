@@ -1,46 +1,282 @@
 // Gated linear recurrence, forward: h_t = a_t h_{t-1} + sigma(i_t) x_t per channel, a_t the
 // gate's decay (glr_gate.cuh), h in fp32.
 //
-// One thread per (sequence, channel) walks its tokens; lanes hold neighbouring channels.
-#include "glr_gate.cuh"
+// Two kernels.  Short fixed-length calls (decode steps) run a thread per (sequence, 4
+// channels) over the tokens.  All others run a single pass over tiles of 64 rows
+// (glr_scan.cuh): a thread forms a and sigma(i) x of its 8 rows x 4 channels, folds them
+// into one affine map, the CTA folds the row groups, hands the tile's map on, takes the
+// state that enters the tile, and every thread runs its rows again from its own state with
+// a and sigma(i) x still in registers.  Inputs are read once, by copies into shared memory
+// that run one tile ahead.
+#include "glr_scan.cuh"
+#ifndef GLR_THREADS
+#define GLR_THREADS 128
+#define GLR_CTAS 4
+#endif
 
 namespace kda {
 namespace {
 
 using namespace layer;
 
-template <typename E, bool UB>
-__global__ void __launch_bounds__(256) glr_fwd_serial_kernel(GlrParams p) {
-    const int64_t unit = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (unit >= p.N * p.D) return;
-    const int64_t n = unit / p.D, c = unit % p.D;
-    int64_t lo, hi;
-    seq_rows(p, n, lo, hi);
-    const GateConst gc{expf(p.A_log[c / p.K]), p.dt_bias[c]};
-    float h = p.init ? ld_state(p.init, p.state_type, unit) : 0.f;
-    for (int64_t t = lo; t < hi; ++t) {
-        if (p.checkpoints && t % kGlrCheckpointRows == 0) p.checkpoints[t / kGlrCheckpointRows * p.D + c] = h;
-        const float x = to_f(static_cast<const E *>(p.x)[t * p.xs + c]);
-        const float i = to_f(static_cast<const E *>(p.i)[t * p.is + c]);
-        const float g = to_f(static_cast<const E *>(p.g)[t * p.gs + c]);
-        h = gate_decay<UB>(g, gc, p.lower_bound) * h + sigmoid(i) * x;
-        if (p.out) static_cast<E *>(p.out)[t * p.os + c] = from_f<E>(h);
+template <typename E, int V, bool UB>
+__global__ void __launch_bounds__(128) glr_fwd_step_kernel(GlrParams p) {
+    const int64_t unit = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, per = p.D / V;
+    if (unit >= p.N * per) return;
+    const int64_t n = unit / per, c = unit % per * V;
+    const E *x = static_cast<const E *>(p.x) + n * p.T * p.xs + c;
+    const E *i = static_cast<const E *>(p.i) + n * p.T * p.is + c;
+    const E *g = static_cast<const E *>(p.g) + n * p.T * p.gs + c;
+    E *out = static_cast<E *>(p.out) + n * p.T * p.os + c;
+    const float lb2 = p.lower_bound * kLog2e;
+    GateConst gc[V];
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        gc[v] = gate_const<UB>(p.A_log[(unsigned)(c + v) / (unsigned)p.K], p.dt_bias[c + v]);
+        h[v] = p.init ? ld_state(p.init, p.state_type, n * p.D + c + v) : 0.f;
     }
-    if (p.fin) st_state(p.fin, p.state_type, unit, h);
+    for (int64_t t = 0; t < p.T; ++t) {
+        float xf[V], jf[V], gf[V];
+        ld_f<E, V>(x + t * p.xs, xf);
+        ld_f<E, V>(i + t * p.is, jf);
+        ld_f<E, V>(g + t * p.gs, gf);
+        const int64_t row = n * p.T + t;
+        if (p.checkpoints && row % kGlrCheckpointRows == 0) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) p.checkpoints[row / kGlrCheckpointRows * p.D + c + v] = h[v];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = fmaf(gate_decay<UB>(gf[v], gc[v], lb2), h[v], sigmoid(jf[v]) * xf[v]);
+        if (p.out) st_f<E, V>(out + t * p.os, h);
+    }
+    if (p.fin) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) st_state(p.fin, p.state_type, n * p.D + c + v, h[v]);
+    }
+}
+
+template <int V> using FwdShape = TileShape<V == 4 ? GLR_THREADS : 128, V == 4 ? 16 : 32, V>;
+
+template <typename E, int V>
+struct FwdShared {
+    using S = FwdShape<V>;
+    Pack<E, V> raw[3][S::L][S::THREADS];
+    Pack<GateConst, V> gates[S::THREADS];
+    Pack<float, V> A[S::RG][S::CL], H[S::RG][S::CL];   // maps of the row groups
+    Pack<float, V> h[S::RG][S::CL];                    // states that enter them
+    TileMarks marks;
+};
+
+template <typename E, int V, bool UB>
+__global__ void __launch_bounds__(FwdShape<V>::THREADS, GLR_CTAS) glr_fwd_scan_kernel(GlrParams p, ScanPlan s) {
+    using namespace sm103;
+    using S = FwdShape<V>;
+    constexpr int CL = S::CL, L = S::L, CB = S::CB, RG = S::RG;
+    extern __shared__ __align__(16) unsigned char smem[];
+    FwdShared<E, V> &sh = *reinterpret_cast<FwdShared<E, V> *>(smem);
+    const int tid = threadIdx.x, lane = tid % CL, rg = tid / CL;
+    const float lb2 = p.lower_bound * kLog2e;
+
+    // starts the copies of a tile into this thread's own slots; returns its first sequence
+    auto fetch = [&](const TileWalk &w) {
+        int first = 0;
+        if (w.rt < s.row_tiles) {
+            const int64_t r0 = w.rt * kTileRows + rg * L;
+            const int c = w.cb * CB + lane * V;
+            first = s.first_seq[w.rt];
+            const float *gate = reinterpret_cast<const float *>(s.gates + c);
+            copy_async<float, V == 4 ? 4 : 2>(&sh.gates[tid], gate);
+            if (V == 4) copy_async<float, V == 4 ? 4 : 2>(&sh.gates[tid].e[V / 2], gate + V);
+            if (c < p.D) {
+                const E *x = static_cast<const E *>(p.x) + r0 * p.xs + c, *i = static_cast<const E *>(p.i) + r0 * p.is + c,
+                        *g = static_cast<const E *>(p.g) + r0 * p.gs + c;
+                const int left = (int)min(p.rows - r0, (int64_t)L);
+#pragma unroll
+                for (int r = 0; r < L; ++r, x += p.xs, i += p.is, g += p.gs) {
+                    if (r < left) {
+                        copy_async<E, V>(&sh.raw[0][r][tid], x);
+                        copy_async<E, V>(&sh.raw[1][r][tid], i);
+                        copy_async<E, V>(&sh.raw[2][r][tid], g);
+                    }
+                }
+            }
+        }
+        copies_commit();
+        return first;
+    };
+
+    TileWalk w(s);
+    int first = fetch(w);
+    while (w.rt < s.row_tiles) {
+        const int64_t rt = w.rt, r0 = rt * kTileRows + rg * L;
+        const int c = w.cb * CB + lane * V, block = w.cb * CB;
+        const bool marked = mark_tile(p, rt, first, sh.marks);
+        copies_wait<0>();   // this thread's own copies: no barrier needed
+
+        // decays and inputs, two at a time: neighbouring channels, or rows where V is 1
+        float a[L * V], b[L * V];
+        const int left = c < p.D ? (int)min(p.rows - r0, (int64_t)L) : 0;   // rows of this thread that exist
+        const Pack<GateConst, V> gc = sh.gates[tid];
+#pragma unroll
+        for (int e = 0; e < L * V; e += 2) {
+            const auto at2 = [&](int k) {
+                return make_float2(to_f(sh.raw[k][e / V][tid].e[e % V]), to_f(sh.raw[k][(e + 1) / V][tid].e[(e + 1) % V]));
+            };
+            const float2 a2 = gate_decay2<UB>(at2(2), gc.e[e % V], gc.e[(e + 1) % V], lb2), b2 = mul2(sigmoid2(at2(1)), at2(0));
+            a[e] = a2.x, a[e + 1] = a2.y;
+            b[e] = b2.x, b[e + 1] = b2.y;
+        }
+        w.next();
+        first = fetch(w);   // the slots are free: the next tile's copies run beside the rest
+        if (left < L) {
+#pragma unroll
+            for (int e = 0; e < L * V; ++e)
+                if (e / V >= left) a[e] = 1.f, b[e] = 0.f;
+        }
+        // a row that begins a sequence starts from the initial state instead
+        if (marked) {
+#pragma unroll
+            for (int e = 0; e < L * V; ++e) {
+                const int r = e / V, n = sh.marks.begins[rg * L + r];
+                if (n < 0 || r >= left) continue;
+                const float h0 = p.init ? ld_state(p.init, p.state_type, n * p.D + c + e % V) : 0.f;
+                b[e] = fmaf(a[e], h0, b[e]);
+                a[e] = -0.f;   // depends on nothing before
+                if (r == 0 && rg == 0 && p.checkpoints) p.checkpoints[rt * p.D + c + e % V] = h0;
+            }
+        }
+        Pack<float, V> mA, mH;
+#pragma unroll
+        for (int v = 0; v < V; ++v) mA.e[v] = a[v], mH.e[v] = b[v];
+#pragma unroll
+        for (int e = V; e < L * V; ++e) {
+            const int v = e % V;
+            const Affine m = marked ? then(Affine{mA.e[v], mH.e[v]}, Affine{a[e], b[e]})
+                                    : Affine{mA.e[v] * a[e], fmaf(a[e], mH.e[v], b[e])};
+            mA.e[v] = m.A, mH.e[v] = m.H;
+        }
+        sh.A[rg][lane] = mA;
+        sh.H[rg][lane] = mH;
+        __syncthreads();
+
+        const int64_t group = rt / s.group;
+        const int pos = (int)(rt % s.group);
+        if (tid < CB) {
+            // one thread per channel: the tile's map, handed on
+            if (pos != s.group - 1) {
+                const int ch = tid;
+                Affine t{sh.A[0][ch / V].e[ch % V], sh.H[0][ch / V].e[ch % V]};
+#pragma unroll
+                for (int q = 1; q < RG; ++q) t = then(t, Affine{sh.A[q][ch / V].e[ch % V], sh.H[q][ch / V].e[ch % V]});
+                publish(s.maps + rt * s.width + block + ch, t);
+            }
+        } else if (tid < 2 * CB) {
+            // one thread per channel: the state that enters the tile, from the state after
+            // the previous group and the maps of the group's earlier tiles
+            const int ch = tid - CB;
+            const uint32_t *before = s.states + (group - 1) * s.width + block + ch;
+            const uint32_t h_bits = group > 0 ? peek(before) : 0;
+            const Affine t = join_maps(s.maps + group * s.group * s.width + block + ch, s.width, pos, p.err);
+            float h = apply(t, group > 0 ? __uint_as_float(await(before, h_bits, p.err)) : 0.f);
+#pragma unroll
+            for (int q = 0; q < RG; ++q) {
+                sh.h[q][ch / V].e[ch % V] = h;
+                h = apply(Affine{sh.A[q][ch / V].e[ch % V], sh.H[q][ch / V].e[ch % V]}, h);
+            }
+            if (pos == s.group - 1) publish(s.states + group * s.width + block + ch, h);
+        }
+        __syncthreads();
+
+        if (left > 0) {
+            const Pack<float, V> start = sh.h[rg][lane];
+            float h[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = start.e[v];
+            if (p.checkpoints && rg == 0 && !(marked && sh.marks.begins[0] >= 0)) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) p.checkpoints[rt * p.D + c + v] = h[v];
+            }
+            E *out = static_cast<E *>(p.out) + r0 * p.os + c;
+#pragma unroll
+            for (int r = 0; r < L; ++r, out += p.os) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    h[v] = marked ? apply(Affine{a[r * V + v], b[r * V + v]}, h[v]) : fmaf(a[r * V + v], h[v], b[r * V + v]);
+                if (r < left) {
+                    if (p.out) st_f<E, V>(out, h);
+                    if (marked && p.fin && sh.marks.ends[rg * L + r] >= 0) {
+                        const int64_t n = sh.marks.ends[rg * L + r];
+#pragma unroll
+                        for (int v = 0; v < V; ++v) st_state(p.fin, p.state_type, n * p.D + c + v, h[v]);
+                    }
+                }
+            }
+        }
+    }
+    copies_wait<0>();
+}
+
+// Rows of a fixed-length call up to which the step kernel runs.
+constexpr int64_t kStepMaxT = 16;
+
+bool step_takes(const GlrParams &p) { return !p.cu_seqlens && p.T <= kStepMaxT; }
+
+// 4 channels per thread where every row of x, i, g and out allows loads of 4 elements.
+bool vector_rows(const GlrParams &p) {
+    const size_t n = 4 * dtype_bytes(p.dtype);
+    const void *ptrs[] = {p.x, p.i, p.g, p.out};
+    for (const void *q : ptrs)
+        if (reinterpret_cast<uintptr_t>(q) % n) return false;
+    return p.D % 4 == 0 && p.xs % 4 == 0 && p.is % 4 == 0 && p.gs % 4 == 0 && (!p.out || p.os % 4 == 0);
+}
+
+template <typename E, int V, bool UB>
+cudaError_t run(const GlrParams &p, unsigned char *ws, int sms, cudaStream_t stream) {
+    if (step_takes(p)) {
+        glr_fwd_step_kernel<E, V, UB><<<(unsigned)ceil_div(p.N * (p.D / V), 128), 128, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
+    ScanPlan s = scan_plan(p.rows, p.D, FwdShape<V>::CB, ws, nullptr);
+    const int64_t fill = s.row_tiles * s.width / 2 + s.width;
+    glr_prepare_kernel<UB, false><<<(unsigned)min(ceil_div(fill, 256), (int64_t)sms * 4), 256, 0, stream>>>(p, s);
+    if (s.row_tiles == 0) return cudaGetLastError();
+    auto kernel = glr_fwd_scan_kernel<E, V, UB>;
+    constexpr int bytes = (int)sizeof(FwdShared<E, V>);
+    static std::atomic<bool> done[kMaxDevices];
+    static int per_sm[kMaxDevices];
+    int dev = 0, ctas = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = once_per_device(done, [&](int d) {
+        cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (r == cudaSuccess) r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, FwdShape<V>::THREADS, bytes);
+        if (d < kMaxDevices) per_sm[d] = ctas;
+        return r;
+    });
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) ctas = per_sm[dev];
+    const unsigned grid = (unsigned)min(s.row_tiles * s.blocks, (int64_t)sms * ctas);
+    GlrParams arg = p;
+    void *args[] = {&arg, &s};
+    return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(FwdShape<V>::THREADS), args, bytes, stream);
 }
 
 }  // namespace
 
-size_t glr_fwd_scratch_bytes(const GlrParams &, int) { return 0; }
+size_t glr_fwd_scratch_bytes(const GlrParams &p, int) {
+    if (step_takes(p)) return 0;
+    size_t bytes = 0;
+    scan_plan(p.rows, p.D, vector_rows(p) ? FwdShape<4>::CB : FwdShape<1>::CB, nullptr, &bytes);
+    return bytes;
+}
 
-cudaError_t launch_glr_fwd(const GlrParams &p, unsigned char *, int, cudaStream_t stream) {
-    const unsigned grid = (unsigned)ceil_div(p.N * p.D, 256);
-    with_dtype(p.dtype, [&](auto *tag) {
+cudaError_t launch_glr_fwd(const GlrParams &p, unsigned char *ws, int sms, cudaStream_t stream) {
+    return with_dtype(p.dtype, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
-        if (p.unbounded) glr_fwd_serial_kernel<E, true><<<grid, 256, 0, stream>>>(p);
-        else glr_fwd_serial_kernel<E, false><<<grid, 256, 0, stream>>>(p);
+        if (vector_rows(p)) return p.unbounded ? run<E, 4, true>(p, ws, sms, stream) : run<E, 4, false>(p, ws, sms, stream);
+        return p.unbounded ? run<E, 1, true>(p, ws, sms, stream) : run<E, 1, false>(p, ws, sms, stream);
     });
-    return cudaGetLastError();
 }
 
 }  // namespace kda

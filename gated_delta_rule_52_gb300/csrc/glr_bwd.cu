@@ -19,7 +19,8 @@ __global__ void __launch_bounds__(256) glr_bwd_serial_kernel(GlrParams p, float 
     const int64_t n = unit / p.D, c = unit % p.D;
     int64_t lo, hi;
     seq_rows(p, n, lo, hi);
-    const GateConst gc{expf(p.A_log[c / p.K]), p.dt_bias[c]};
+    const GateConst gc = gate_const<UB>(p.A_log[c / p.K], p.dt_bias[c]);
+    const float lb2 = p.lower_bound * kLog2e;
     const E *xp = static_cast<const E *>(p.x), *ip = static_cast<const E *>(p.i), *gp = static_cast<const E *>(p.g);
     float e = p.dfinal ? p.dfinal[unit] : 0.f, dA_sum = 0.f, ddt_sum = 0.f;
     float start[kGlrCheckpointRows];
@@ -30,12 +31,12 @@ __global__ void __launch_bounds__(256) glr_bwd_serial_kernel(GlrParams p, float 
                                                   : 0.f;
         for (int64_t t = begin; t < end; ++t) {
             start[t - begin] = h;
-            h = gate_decay<UB>(to_f(gp[t * p.gs + c]), gc, p.lower_bound) * h + sigmoid(to_f(ip[t * p.is + c])) * to_f(xp[t * p.xs + c]);
+            h = gate_decay<UB>(to_f(gp[t * p.gs + c]), gc, lb2) * h + sigmoid(to_f(ip[t * p.is + c])) * to_f(xp[t * p.xs + c]);
         }
         for (int64_t t = end - 1; t >= begin; --t) {
             const float x = to_f(xp[t * p.xs + c]);
             float slope, rate, s, ss;
-            const float a = gate_slopes<UB>(to_f(gp[t * p.gs + c]), gc, p.lower_bound, slope, rate);
+            const float a = gate_slopes<UB>(to_f(gp[t * p.gs + c]), gc, lb2, slope, rate);
             sigmoid_slope(to_f(ip[t * p.is + c]), s, ss);
             e += to_f(static_cast<const E *>(p.dout)[t * p.ds + c]);
             const float dl = e * a * start[t - begin], dg = dl * slope;
@@ -77,12 +78,19 @@ __global__ void __launch_bounds__(256) glr_param_grads_kernel(GlrParams p, int64
     if (threadIdx.x == 0) p.dA_log[h] = sums[0];
 }
 
+// The forward run that writes checkpoints only.
+GlrParams states_only(const GlrParams &p) {
+    GlrParams f = p;
+    f.out = f.fin = nullptr;
+    return f;
+}
+
 }  // namespace
 
-size_t glr_bwd_scratch_bytes(const GlrParams &p, int) {
+size_t glr_bwd_scratch_bytes(const GlrParams &p, int sms) {
     const size_t part = (size_t)(p.N * p.D) * sizeof(float);
     const size_t ck = p.checkpoints ? 0 : (size_t)(ceil_div(p.rows, kGlrCheckpointRows) * p.D) * sizeof(float);
-    return 2 * part + ck;
+    return (2 * part + ck + 15) / 16 * 16 + (p.checkpoints ? 0 : glr_fwd_scratch_bytes(states_only(p), sms));
 }
 
 cudaError_t launch_glr_bwd(const GlrParams &p0, unsigned char *ws, int sms, cudaStream_t stream) {
@@ -91,10 +99,9 @@ cudaError_t launch_glr_bwd(const GlrParams &p0, unsigned char *ws, int sms, cuda
     float *dA_part = reinterpret_cast<float *>(ws), *ddt_part = dA_part + units;
     if (units > 0) {
         if (!p.checkpoints) {
-            GlrParams f = p;
-            f.out = f.fin = nullptr;
-            f.checkpoints = p.checkpoints = ddt_part + units;
-            const cudaError_t e = launch_glr_fwd(f, nullptr, sms, stream);
+            p.checkpoints = ddt_part + units;
+            const size_t used = (size_t)(2 * units + ceil_div(p.rows, kGlrCheckpointRows) * p.D) * sizeof(float);
+            const cudaError_t e = launch_glr_fwd(states_only(p), ws + (used + 15) / 16 * 16, sms, stream);
             if (e != cudaSuccess) return e;
         }
         const unsigned grid = (unsigned)ceil_div(units, 256);

@@ -1,0 +1,225 @@
+// What the forward and the backward scan of the gated linear recurrence share: affine maps
+// h -> A h + H and their products, the tiles, and the hand-over of a tile's map to the
+// tiles after it.
+//
+// Both scans cut [rows, D] into tiles of 64 rows (a checkpoint's spacing) and one block of
+// channels, and run as one cooperative launch of persistent CTAs: every CTA takes its tiles
+// in ascending order, a tile waits only for tiles before it, and all CTAs are resident, so
+// the first unfinished tile can always go on.  The tiles of a channel block form groups
+// (scan_plan chooses their size).  A tile publishes its own map; it takes the state that enters it from the state
+// after the previous group and the maps of its own group's earlier tiles, always the same
+// ones in the same order, whatever has arrived first: the same bits every time.
+// A published value is its own flag: the buffers are filled with ones (a NaN that is never
+// published) before the launch.
+#pragma once
+
+#include "glr_gate.cuh"
+#include "sm103.cuh"
+
+namespace kda {
+namespace layer {
+
+constexpr int kTileRows = kGlrCheckpointRows;
+constexpr uint32_t kEmpty = 0xffffffffu;
+
+// An affine map.  A decay is never negative, so A's sign bit marks a map that does not
+// depend on the state that enters it (a sequence begins inside): the state is left out,
+// not multiplied by 0, and NaN and infinity stay within their sequence.
+struct Affine { float A, H; };
+
+__device__ __forceinline__ bool cuts(float A) { return __float_as_int(A) < 0; }
+__device__ __forceinline__ float apply(Affine m, float h) { return cuts(m.A) ? m.H : fmaf(m.A, h, m.H); }
+// First `a`, then `b`.  The product keeps the sign of a's A.
+__device__ __forceinline__ Affine then(Affine a, Affine b) {
+    return cuts(b.A) ? b : Affine{a.A * b.A, fmaf(b.A, a.H, b.H)};
+}
+
+// A NaN is published as the canonical one, so that no value looks empty.
+__device__ __forceinline__ uint32_t bits_to_publish(float v) {
+    return v == v ? __float_as_uint(v) : 0x7fffffffu;
+}
+__device__ __forceinline__ void publish(uint64_t *at, Affine m) {
+    const uint64_t v = (uint64_t)bits_to_publish(m.H) << 32 | bits_to_publish(m.A);
+    asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(at), "l"(v) : "memory");
+}
+__device__ __forceinline__ void publish(uint32_t *at, float h) {
+    asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(at), "r"(bits_to_publish(h)) : "memory");
+}
+__device__ __forceinline__ uint64_t peek(const uint64_t *at) {
+    uint64_t v;
+    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t peek(const uint32_t *at) {
+    uint32_t v;
+    asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ bool empty(uint64_t v) { return (uint32_t)v == kEmpty; }
+__device__ __forceinline__ bool empty(uint32_t v) { return v == kEmpty; }
+
+// Waits for a published value, at most kWaitNs; on expiry reports to the device error word
+// and goes on with what is there.
+constexpr uint64_t kWaitNs = 2000000000ull;
+template <typename U>
+__device__ __forceinline__ U await(const U *at, U v, int *err) {
+    if (!empty(v)) return v;
+    const uint64_t t0 = sm103::globaltimer_ns();
+    while (empty(v = peek(at))) {
+        if (sm103::globaltimer_ns() - t0 > kWaitNs) {
+            atomicExch(err, kErrTimeout);
+            break;
+        }
+    }
+    return v;
+}
+
+// Asynchronous copy of one thread's V elements into its own slot of shared memory (2-byte
+// elements that are alone are copied at once).
+template <typename E, int V>
+__device__ __forceinline__ void copy_async(void *slot, const E *src) {
+    constexpr int n = sizeof(E) * V;
+    static_assert(n == 2 || n == 4 || n == 8 || n == 16, "copy size");
+    if constexpr (n == 2)
+        *reinterpret_cast<E *>(slot) = *src;
+    else if constexpr (n == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm103::smem_u32(slot)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(sm103::smem_u32(slot)), "l"(src), "n"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// How a CTA covers a tile: THREADS threads as CL channel lanes of V channels each by RG row
+// groups of L rows each.
+template <int THREADS_, int CL_, int V_>
+struct TileShape {
+    static constexpr int THREADS = THREADS_, CL = CL_, V = V_;
+    static constexpr int CB = CL * V, RG = THREADS / CL, L = kTileRows / RG;
+    static_assert(RG * L == kTileRows && THREADS >= 2 * CB && CB % 32 == 0, "tile shape");
+};
+
+// Workspace of a scan and its tiles.  Maps [row tile][padded channel], states after a
+// group [group][padded channel], then the first sequence of every row tile.
+struct ScanPlan {
+    int64_t row_tiles, groups, blocks, width;   // width = blocks * channels per block
+    int group;                                  // row tiles per group, a power of two
+    uint64_t *maps;
+    uint32_t *states;
+    int *first_seq;                             // kInside set: the tile lies inside that sequence
+    GateConst *gates;                           // [width]
+};
+constexpr int kInside = INT32_MIN;
+inline ScanPlan scan_plan(int64_t rows, int64_t D, int channels, unsigned char *ws, size_t *bytes) {
+    ScanPlan s;
+    s.row_tiles = ceil_div(rows, kTileRows);
+    s.blocks = ceil_div(D, channels);
+    // The state passes from group to group one at a time, each step about one tile's time
+    // on one SM, while the rest of the GPU works off `group` row tiles of `blocks` tiles; a
+    // tile joins the maps of half a group on average.
+    for (s.group = 4; s.group < 32 && s.group * s.blocks < 512; s.group *= 2) {}
+    s.groups = ceil_div(s.row_tiles, s.group);
+    s.width = s.blocks * channels;
+    s.maps = reinterpret_cast<uint64_t *>(ws);
+    s.states = reinterpret_cast<uint32_t *>(s.maps + s.row_tiles * s.width);
+    s.gates = reinterpret_cast<GateConst *>(s.states + ceil_div(s.groups * s.width, 4) * 4);
+    s.first_seq = reinterpret_cast<int *>(s.gates + s.width);
+    if (bytes) *bytes = (size_t)(reinterpret_cast<unsigned char *>(s.first_seq + s.row_tiles) - ws + 15) / 16 * 16;
+    return s;
+}
+
+// Before a scan: empties the hand-over buffers, folds the gates' constants, finds the first
+// sequence of every row tile.  REVERSE false: final states of sequences without tokens;
+// true: their gradients of the initial state.
+template <bool UB, bool REVERSE>
+__global__ void __launch_bounds__(256) glr_prepare_kernel(GlrParams p, ScanPlan s) {
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    const int64_t words = (s.row_tiles * s.width * 2 + ceil_div(s.groups * s.width, 4) * 4) / 4;
+    uint4 *fill = reinterpret_cast<uint4 *>(s.maps);
+    for (int64_t j = at; j < words; j += step) fill[j] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
+    for (int64_t c = at; c < s.width; c += step)
+        s.gates[c] = c < p.D ? gate_const<UB>(p.A_log[(unsigned)c / (unsigned)p.K], p.dt_bias[c]) : GateConst{0.f, 0.f};
+    for (int64_t t = at; t < s.row_tiles; t += step) {
+        const int64_t r0 = t * kTileRows, n = p.cu_seqlens ? seq_of_row(p.cu_seqlens, p.N, r0) : r0 / p.T;
+        int64_t lo, hi;
+        seq_rows(p, n, lo, hi);
+        s.first_seq[t] = (int)n | (lo < r0 && hi > r0 + kTileRows ? kInside : 0);
+    }
+    if (!p.cu_seqlens) return;
+    if (REVERSE ? !p.dinit : !p.fin) return;
+    // a warp per sequence: one without tokens passes its state through
+    for (int64_t n = at >> 5; n < p.N; n += step >> 5) {
+        int64_t lo, hi;
+        seq_rows(p, n, lo, hi);
+        if (lo < hi) continue;
+        for (int64_t c = n * p.D + (threadIdx.x & 31); c < (n + 1) * p.D; c += 32) {
+            if (REVERSE) p.dinit[c] = p.dfinal ? p.dfinal[c] : 0.f;
+            else st_state(p.fin, p.state_type, c, p.init ? ld_state(p.init, p.state_type, c) : 0.f);
+        }
+    }
+}
+
+// Where sequences begin and end within a tile of rows [r0, r0 + kTileRows): for each row
+// the sequence that it begins (ends), or -1.  Returns false, and writes nothing, where the
+// tile lies inside one sequence.  Called by all threads, whose shared memory it is.
+struct TileMarks { int begins[kTileRows], ends[kTileRows]; };
+
+// n: first_seq of the tile.
+template <typename P>
+__device__ __forceinline__ bool mark_tile(const P &p, int64_t row_tile, int n, TileMarks &m) {
+    if (n & kInside) return false;
+    const int64_t r0 = row_tile * kTileRows, r1 = r0 + kTileRows;
+    __syncthreads();   // the marks of the tile before are read no more
+    if (threadIdx.x < kTileRows) m.begins[threadIdx.x] = m.ends[threadIdx.x] = -1;
+    __syncthreads();
+    for (int64_t k = n + threadIdx.x; k < p.N; k += blockDim.x) {
+        int64_t lo, hi;
+        seq_rows(p, k, lo, hi);
+        if (lo >= r1) break;
+        if (lo >= hi) continue;
+        if (lo >= r0) m.begins[lo - r0] = (int)k;
+        if (hi > r0 && hi <= r1) m.ends[hi - 1 - r0] = (int)k;
+    }
+    __syncthreads();
+    return true;
+}
+
+// The maps of `count` row tiles of a channel, one after the other, as one map.  `at` is the
+// first one's, the next `stride` further on.
+__device__ __forceinline__ Affine join_maps(const uint64_t *at, int64_t stride, int count, int *err) {
+    Affine t{1.f, 0.f};
+    constexpr int kBatch = 8;   // in flight together
+    for (int j0 = 0; j0 < count; j0 += kBatch, at += kBatch * stride) {
+        uint64_t w[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) w[j] = j0 + j < count ? peek(at + j * stride) : 0x3f800000ull;   // (1, 0)
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            w[j] = await(at + j * stride, w[j], err);
+            t = then(t, Affine{__uint_as_float((uint32_t)w[j]), __uint_as_float((uint32_t)(w[j] >> 32))});
+        }
+    }
+    return t;
+}
+
+// Tiles of a persistent CTA: row tile and channel block, stepped by the grid's size.
+struct TileWalk {
+    int64_t rt;
+    int cb, blocks, step_rt, step_cb;
+    __device__ __forceinline__ TileWalk(const ScanPlan &s) {
+        blocks = (int)s.blocks;
+        rt = blockIdx.x / (unsigned)blocks;
+        cb = (int)(blockIdx.x % (unsigned)blocks);
+        step_rt = (int)(gridDim.x / (unsigned)blocks);
+        step_cb = (int)(gridDim.x % (unsigned)blocks);
+    }
+    __device__ __forceinline__ void next() {
+        rt += step_rt;
+        cb += step_cb;
+        if (cb >= blocks) cb -= blocks, ++rt;
+    }
+};
+
+}  // namespace layer
+}  // namespace kda
