@@ -34,6 +34,36 @@ __device__ __forceinline__ Affine then(Affine a, Affine b) {
     return cuts(b.A) ? b : Affine{a.A * b.A, fmaf(b.A, a.H, b.H)};
 }
 
+// V channels at a time, none of whose maps cuts: m <- m then (a, b), and h <- a h + b.
+template <int V>
+__device__ __forceinline__ void then_all(float (&A)[V], float (&H)[V], const float *a, const float *b) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            const float2 a2 = make_float2(a[v], a[v + 1]);
+            const float2 h2 = sm103::fma2(a2, make_float2(H[v], H[v + 1]), make_float2(b[v], b[v + 1]));
+            const float2 m2 = sm103::mul2(a2, make_float2(A[v], A[v + 1]));
+            A[v] = m2.x, A[v + 1] = m2.y, H[v] = h2.x, H[v + 1] = h2.y;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) H[v] = fmaf(a[v], H[v], b[v]), A[v] *= a[v];
+    }
+}
+template <int V>
+__device__ __forceinline__ void apply_all(const float *a, const float *b, float (&h)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            const float2 h2 = sm103::fma2(make_float2(a[v], a[v + 1]), make_float2(h[v], h[v + 1]), make_float2(b[v], b[v + 1]));
+            h[v] = h2.x, h[v + 1] = h2.y;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = fmaf(a[v], h[v], b[v]);
+    }
+}
+
 // A NaN is published as the canonical one, so that no value looks empty.
 __device__ __forceinline__ uint32_t bits_to_publish(float v) {
     return v == v ? __float_as_uint(v) : 0x7fffffffu;
@@ -104,7 +134,7 @@ struct TileShape {
 // group [group][padded channel], then the first sequence of every row tile.
 struct ScanPlan {
     int64_t row_tiles, groups, blocks, width;   // width = blocks * channels per block
-    int group;                                  // row tiles per group, a power of two
+    int group_log2;                             // row tiles per group
     uint64_t *maps;
     uint32_t *states;
     int *first_seq;                             // kInside set: the tile lies inside that sequence
@@ -118,8 +148,8 @@ inline ScanPlan scan_plan(int64_t rows, int64_t D, int channels, unsigned char *
     // The state passes from group to group one at a time, each step about one tile's time
     // on one SM, while the rest of the GPU works off `group` row tiles of `blocks` tiles; a
     // tile joins the maps of half a group on average.
-    for (s.group = 4; s.group < 32 && s.group * s.blocks < 512; s.group *= 2) {}
-    s.groups = ceil_div(s.row_tiles, s.group);
+    for (s.group_log2 = 2; s.group_log2 < 5 && s.blocks << s.group_log2 < 512; ++s.group_log2) {}
+    s.groups = ceil_div(s.row_tiles, int64_t(1) << s.group_log2);
     s.width = s.blocks * channels;
     s.maps = reinterpret_cast<uint64_t *>(ws);
     s.states = reinterpret_cast<uint32_t *>(s.maps + s.row_tiles * s.width);
