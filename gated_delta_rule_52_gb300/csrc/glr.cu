@@ -8,6 +8,8 @@
 // state that enters the tile, and every thread runs its rows again from its own state with
 // a and sigma(i) x still in registers.  Inputs are read once, by copies into shared memory
 // that run one tile ahead.
+#include <algorithm>
+
 #include "glr_scan.cuh"
 
 namespace kda {
@@ -247,24 +249,14 @@ cudaError_t run(const GlrParams &p, unsigned char *ws, int sms, cudaStream_t str
     }
     ScanPlan s = scan_plan(p.rows, p.D, FwdShape<V>::CB, ws, nullptr);
     const int64_t fill = s.row_tiles * s.width / 2 + s.width;
-    glr_prepare_kernel<UB, false><<<(unsigned)min(ceil_div(fill, 256), (int64_t)sms * 4), 256, 0, stream>>>(p, s);
+    glr_prepare_kernel<UB, false><<<(unsigned)std::min(ceil_div(fill, 256), (int64_t)sms * 4), 256, 0, stream>>>(p, s);
     if (s.row_tiles == 0) return cudaGetLastError();
-    auto kernel = glr_fwd_scan_kernel<E, V, UB>;
+    constexpr auto kernel = glr_fwd_scan_kernel<E, V, UB>;
     constexpr int bytes = (int)sizeof(FwdShared<E, V>);
-    static std::atomic<bool> done[kMaxDevices];
-    static int per_sm[kMaxDevices];
-    int dev = 0, ctas = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    int ctas = 0;
+    const cudaError_t e = resident_ctas<kernel>(FwdShape<V>::THREADS, bytes, ctas);
     if (e != cudaSuccess) return e;
-    e = once_per_device(done, [&](int d) {
-        cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (r == cudaSuccess) r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, FwdShape<V>::THREADS, bytes);
-        if (d < kMaxDevices) per_sm[d] = ctas;
-        return r;
-    });
-    if (e != cudaSuccess) return e;
-    if (dev < kMaxDevices) ctas = per_sm[dev];
-    const unsigned grid = (unsigned)min(s.row_tiles * s.blocks, (int64_t)sms * ctas);
+    const unsigned grid = (unsigned)std::min(s.row_tiles * s.blocks, (int64_t)sms * ctas);
     GlrParams arg = p;
     void *args[] = {&arg, &s};
     return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(FwdShape<V>::THREADS), args, bytes, stream);

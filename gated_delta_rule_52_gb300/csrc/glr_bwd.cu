@@ -1,81 +1,283 @@
-// Gated linear recurrence, backward.  With e_t the gradient of h_t,
-//   e_t = dout_t + a_{t+1} e_{t+1}   (e of the last token also takes dfinal)
-//   dx = e s, di = e x s (1 - s), s = sigma(i);   dl = e_t a_t h_{t-1}, the gradient of gk_t;
-//   dg = dl d gk/dg, ddt_bias = sum dg, dA_log = sum dl d gk/dA_log, dinit = a_first e_first.
-// h_{t-1} is recomputed in fp32 from the checkpoints (one state every 64 packed rows).
+// Gated linear recurrence, backward.  With e_t the gradient of h_t and f_t = a_t e_t what
+// passes on to h_{t-1},
+//   e_t = dout_t + f_{t+1}   (of a sequence's last token also + dfinal)
+//   f_t = a_t f_{t+1} + a_t dout_t
+//   dx = e s, di = e x s (1 - s), s = sigma(i);   dl = f_t h_{t-1}, the gradient of gk_t;
+//   dg = dl d gk/dg, ddt_bias = sum dg, dA_log = sum dl d gk/dA_log, dinit = f_first.
 //
-// One thread per (sequence, channel) walks its 64-row blocks from the last to the first.
-#include "glr_gate.cuh"
+// One pass over tiles of 64 rows from the last to the first (glr_scan.cuh).  h_{t-1} is
+// recomputed in fp32: a tile's rows are those of one checkpoint, so the forward states need
+// no other tile.  A thread forms the decays of its 16 elements and folds them forward (from
+// the checkpoint) and backward (into the map that the tile hands on); with the states that
+// enter its rows from both sides it then forms the gradients, the inputs still in shared
+// memory and three values per element in registers.  Inputs are read and gradients written
+// once.  Parameter gradients leave a tile as one partial sum per channel.
+#include <algorithm>
+
+#include "glr_scan.cuh"
 
 namespace kda {
 namespace {
 
 using namespace layer;
 
-template <typename E, bool UB>
-__global__ void __launch_bounds__(256) glr_bwd_serial_kernel(GlrParams p, float *dA_part, float *ddt_part) {
-    const int64_t unit = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (unit >= p.N * p.D) return;
-    const int64_t n = unit / p.D, c = unit % p.D;
-    int64_t lo, hi;
-    seq_rows(p, n, lo, hi);
-    const GateConst gc = gate_const<UB>(p.A_log[c / p.K], p.dt_bias[c]);
+// 16 elements per thread: 4 rows by 4 channels in 16 bits, 8 by 2 in 32 bits (the raw
+// inputs of two tiles in shared memory allow 2 and 3 CTAs per SM), 16 by 1 where rows are
+// not aligned.
+template <typename E, int V> using BwdShape = TileShape<V == 4 ? 256 : 128, V == 1 ? 32 : 16, V>;
+
+template <typename E, int V>
+struct BwdShared {
+    using S = BwdShape<E, V>;
+    Pack<E, V> raw[2][4][S::L][S::THREADS];                  // x, i, g, dout
+    Pack<GateConst, V> gates[2][S::THREADS];
+    Pack<float, V> A[S::RG][S::CL], H[S::RG][S::CL];         // forward maps of the row groups
+    Pack<float, V> B[S::RG][S::CL], F[S::RG][S::CL];         // backward maps
+    Pack<float, V> h[S::RG][S::CL], f[S::RG][S::CL];         // states that enter them
+    Pack<float, V> sum_ddt[S::RG][S::CL], sum_dA[S::RG][S::CL];
+    TileMarks marks;
+};
+
+template <typename E, int V, bool UB>
+__global__ void __launch_bounds__(BwdShape<E, V>::THREADS, V == 4 ? 2 : 3)
+    glr_bwd_scan_kernel(GlrParams p, ScanPlan s, float *part_ddt, float *part_dA) {
+    using namespace sm103;
+    using S = BwdShape<E, V>;
+    constexpr int CL = S::CL, L = S::L, CB = S::CB, RG = S::RG;
+    static_assert(S::THREADS >= 3 * CB && L * V == 16, "roles");
+    extern __shared__ __align__(16) unsigned char smem[];
+    BwdShared<E, V> &sh = *reinterpret_cast<BwdShared<E, V> *>(smem);
+    const int tid = threadIdx.x, lane = tid % CL, rg = tid / CL;
+    const int role = tid / CB, ch = tid % CB;
     const float lb2 = p.lower_bound * kLog2e;
-    const E *xp = static_cast<const E *>(p.x), *ip = static_cast<const E *>(p.i), *gp = static_cast<const E *>(p.g);
-    float e = p.dfinal ? p.dfinal[unit] : 0.f, dA_sum = 0.f, ddt_sum = 0.f;
-    float start[kGlrCheckpointRows];
-    for (int64_t end = hi; end > lo;) {
-        const int64_t begin = max(lo, (end - 1) / kGlrCheckpointRows * kGlrCheckpointRows);
-        float h = begin % kGlrCheckpointRows == 0 ? p.checkpoints[begin / kGlrCheckpointRows * p.D + c]
-                  : p.init                        ? ld_state(p.init, p.state_type, unit)
-                                                  : 0.f;
-        for (int64_t t = begin; t < end; ++t) {
-            start[t - begin] = h;
-            h = gate_decay<UB>(to_f(gp[t * p.gs + c]), gc, lb2) * h + sigmoid(to_f(ip[t * p.is + c])) * to_f(xp[t * p.xs + c]);
+    float checkpoint = 0.f;   // of role 2's channel, fetched with the tile
+
+    // tile number w.rt counts from the last row tile
+    auto fetch = [&](const TileWalk &w, int stage) {
+        int first = 0;
+        if (w.rt < s.row_tiles) {
+            const int64_t rt = s.row_tiles - 1 - w.rt, r0 = rt * kTileRows + rg * L;
+            const int c = w.cb * CB + lane * V;
+            first = s.first_seq[rt];
+            const float *gate = reinterpret_cast<const float *>(s.gates + c);
+            copy_async<float, V == 4 ? 4 : 2 * V>(&sh.gates[stage][tid], gate);
+            if (V == 4) copy_async<float, 4>(&sh.gates[stage][tid].e[V / 2], gate + 4);
+            if (role == 2 && w.cb * CB + ch < p.D) checkpoint = p.checkpoints[rt * p.D + w.cb * CB + ch];
+            if (c < p.D) {
+                const E *x = static_cast<const E *>(p.x) + r0 * p.xs + c, *i = static_cast<const E *>(p.i) + r0 * p.is + c,
+                        *g = static_cast<const E *>(p.g) + r0 * p.gs + c, *d = static_cast<const E *>(p.dout) + r0 * p.ds + c;
+                const int left = (int)min(p.rows - r0, (int64_t)L);
+#pragma unroll
+                for (int r = 0; r < L; ++r, x += p.xs, i += p.is, g += p.gs, d += p.ds) {
+                    if (r < left) {
+                        copy_async<E, V>(&sh.raw[stage][0][r][tid], x);
+                        copy_async<E, V>(&sh.raw[stage][1][r][tid], i);
+                        copy_async<E, V>(&sh.raw[stage][2][r][tid], g);
+                        copy_async<E, V>(&sh.raw[stage][3][r][tid], d);
+                    }
+                }
+            }
         }
-        for (int64_t t = end - 1; t >= begin; --t) {
-            const float x = to_f(xp[t * p.xs + c]);
-            float slope, rate, s, ss;
-            const float a = gate_slopes<UB>(to_f(gp[t * p.gs + c]), gc, lb2, slope, rate);
-            sigmoid_slope(to_f(ip[t * p.is + c]), s, ss);
-            e += to_f(static_cast<const E *>(p.dout)[t * p.ds + c]);
-            const float dl = e * a * start[t - begin], dg = dl * slope;
-            static_cast<E *>(p.dx)[t * p.D + c] = from_f<E>(e * s);
-            static_cast<E *>(p.di)[t * p.D + c] = from_f<E>(e * x * ss);
-            static_cast<E *>(p.dg)[t * p.D + c] = from_f<E>(dg);
-            ddt_sum += dg;
-            dA_sum += dl * rate;
-            e *= a;
+        copies_commit();
+        return first;
+    };
+
+    TileWalk w(s);
+    int next_first = fetch(w, 0);
+    for (int stage = 0; w.rt < s.row_tiles; stage ^= 1) {
+        const int64_t walk = w.rt, rt = s.row_tiles - 1 - walk, r0 = rt * kTileRows + rg * L;
+        const int c = w.cb * CB + lane * V, block = w.cb * CB, first = next_first;
+        const float h_tile = checkpoint;
+        w.next();
+        next_first = fetch(w, stage ^ 1);
+        const bool marked = mark_tile(p, rt, first, sh.marks);
+        copies_wait<1>();   // this thread's own copies: no barrier needed
+
+        const int left = c < p.D ? (int)min(p.rows - r0, (int64_t)L) : 0;   // rows of this thread that exist
+        const Pack<GateConst, V> gc = sh.gates[stage][tid];
+        const auto raw = [&](int k, int e) { return to_f(sh.raw[stage][k][e / V][tid].e[e % V]); };
+        TokenGates tg[L * V];
+        Pack<float, V> mA, mH, mB, mF;
+#pragma unroll
+        for (int v = 0; v < V; ++v) mA.e[v] = mB.e[v] = 1.f, mH.e[v] = mF.e[v] = 0.f;
+        if (!marked && left == L) {
+#pragma unroll
+            for (int e = 0; e < L * V; ++e) {
+                const int v = e % V;
+                float a, si;
+                tg[e] = token_gates<UB>(raw(2, e), raw(1, e), gc.e[v], lb2, a, si);
+                // forward: after the rows before; backward: f = a_0 (dout_0 + a_1 (dout_1 + ...))
+                mH.e[v] = fmaf(a, mH.e[v], si * raw(0, e));
+                mA.e[v] *= a;
+                mF.e[v] = fmaf(mA.e[v], raw(3, e), mF.e[v]);
+            }
+            mB = mA;
+        } else {
+#pragma unroll
+            for (int e = 0; e < L * V; ++e) {
+                const int v = e % V, r = e / V;
+                if (r >= left) continue;
+                float a, si;
+                tg[e] = token_gates<UB>(raw(2, e), raw(1, e), gc.e[v], lb2, a, si);
+                const int begins = marked ? sh.marks.begins[rg * L + r] : -1, ends = marked ? sh.marks.ends[rg * L + r] : -1;
+                const float b = si * raw(0, e);
+                if (begins >= 0) {
+                    const float h0 = p.init ? ld_state(p.init, p.state_type, begins * p.D + c + v) : 0.f;
+                    mA.e[v] = -0.f, mH.e[v] = fmaf(a, h0, b);
+                } else {
+                    mH.e[v] = fmaf(a, mH.e[v], b);
+                    mA.e[v] *= a;
+                }
+                // backward map of rows 0 .. r: the earlier rows' map after this row's
+                float d = raw(3, e);
+                if (ends >= 0 && p.dfinal) d += p.dfinal[ends * p.D + c + v];
+                const Affine m = then(Affine{ends >= 0 ? -0.f : a, a * d}, Affine{mB.e[v], mF.e[v]});
+                mB.e[v] = m.A, mF.e[v] = m.H;
+            }
         }
-        end = begin;
+        sh.A[rg][lane] = mA;
+        sh.H[rg][lane] = mH;
+        sh.B[rg][lane] = mB;
+        sh.F[rg][lane] = mF;
+        __syncthreads();
+
+        const int64_t group = walk >> s.group_log2;
+        const int pos = (int)(walk - (group << s.group_log2)), last = (1 << s.group_log2) - 1;
+        const auto back = [&](int q) { return Affine{sh.B[q][ch / V].e[ch % V], sh.F[q][ch / V].e[ch % V]}; };
+        if (role == 0) {
+            // the tile's backward map, handed on
+            if (pos != last) {
+                Affine t = back(RG - 1);
+#pragma unroll
+                for (int q = RG - 2; q >= 0; --q) t = then(t, back(q));
+                publish(s.maps + walk * s.width + block + ch, t);
+            }
+        } else if (role == 1) {
+            // what enters the tile and its row groups from behind
+            const uint32_t *before = s.states + (group - 1) * s.width + block + ch;
+            const uint32_t f_bits = group > 0 ? peek(before) : 0;
+            const Affine t = join_maps(s.maps + (walk - pos) * s.width + block + ch, s.width, pos, p.err);
+            float f = apply(t, group > 0 ? __uint_as_float(await(before, f_bits, p.err)) : 0.f);
+#pragma unroll
+            for (int q = RG - 1; q >= 0; --q) {
+                sh.f[q][ch / V].e[ch % V] = f;
+                f = apply(back(q), f);
+            }
+            if (pos == last) publish(s.states + group * s.width + block + ch, f);
+        } else if (role == 2) {
+            // the forward states that enter the row groups
+            float h = h_tile;
+#pragma unroll
+            for (int q = 0; q < RG; ++q) {
+                sh.h[q][ch / V].e[ch % V] = h;
+                h = apply(Affine{sh.A[q][ch / V].e[ch % V], sh.H[q][ch / V].e[ch % V]}, h);
+            }
+        }
+        __syncthreads();
+
+        Pack<float, V> ddt, dA;
+#pragma unroll
+        for (int v = 0; v < V; ++v) ddt.e[v] = dA.e[v] = 0.f;
+        if (left > 0) {
+            float start[L * V];   // the states that the rows start from
+            const Pack<float, V> h_in = sh.h[rg][lane];
+            float h[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = h_in.e[v];
+#pragma unroll
+            for (int e = 0; e < L * V; ++e) {
+                const int v = e % V, r = e / V;
+                if (r >= left) break;
+                if (marked && sh.marks.begins[rg * L + r] >= 0)
+                    h[v] = p.init ? ld_state(p.init, p.state_type, sh.marks.begins[rg * L + r] * p.D + c + v) : 0.f;
+                start[e] = h[v];
+                if (r < L - 1) {
+                    const float si = raw(1, e) >= 0.f ? 1.f - tg[e].mi : tg[e].mi, a = UB ? ex2(tg[e].gate) : tg[e].gate;
+                    h[v] = fmaf(a, h[v], si * raw(0, e));
+                }
+            }
+            const Pack<float, V> f_in = sh.f[rg][lane];
+            float f[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = f_in.e[v];
+            const int64_t row_at = (r0 + L - 1) * p.D + c;
+            E *dx = static_cast<E *>(p.dx) + row_at, *di = static_cast<E *>(p.di) + row_at, *dg = static_cast<E *>(p.dg) + row_at;
+#pragma unroll
+            for (int r = L - 1; r >= 0; --r, dx -= p.D, di -= p.D, dg -= p.D) {
+                if (r >= left) continue;
+                const int ends = marked ? sh.marks.ends[rg * L + r] : -1, begins = marked ? sh.marks.begins[rg * L + r] : -1;
+                float ox[V], oi[V], og[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int e = r * V + v;
+                    if (ends >= 0) f[v] = p.dfinal ? p.dfinal[ends * p.D + c + v] : 0.f;
+                    const float grad = raw(3, e) + f[v];
+                    f[v] = (UB ? ex2(tg[e].gate) : tg[e].gate) * grad;
+                    if (begins >= 0 && p.dinit) p.dinit[begins * p.D + c + v] = f[v];
+                    const float mi = tg[e].mi, other = 1.f - mi;
+                    const float gm = grad * mi, go = grad * other;
+                    ox[v] = raw(1, e) >= 0.f ? go : gm;
+                    oi[v] = gm * other * raw(0, e);
+                    const float dl = f[v] * start[e];
+                    float slope, rate;
+                    gate_slopes<UB>(raw(2, e), gc.e[v], p.lower_bound, tg[e], slope, rate);
+                    og[v] = dl * slope;
+                    ddt.e[v] += og[v];
+                    dA.e[v] = fmaf(dl, rate, dA.e[v]);
+                }
+                st_f<E, V>(dx, ox);
+                st_f<E, V>(di, oi);
+                st_f<E, V>(dg, og);
+            }
+        }
+        sh.sum_ddt[rg][lane] = ddt;
+        sh.sum_dA[rg][lane] = dA;
+        __syncthreads();
+        if (role < 2) {
+            const auto &sum = role == 0 ? sh.sum_ddt : sh.sum_dA;
+            float t = 0.f;
+#pragma unroll
+            for (int q = 0; q < RG; ++q) t += sum[q][ch / V].e[ch % V];
+            (role == 0 ? part_ddt : part_dA)[rt * s.width + block + ch] = t;
+        }
     }
-    if (p.dinit) p.dinit[unit] = e;
-    dA_part[unit] = dA_sum;
-    ddt_part[unit] = ddt_sum;
+    copies_wait<0>();
 }
 
-// Sums the partial parameter gradients [parts, D]: ddt_bias per channel, dA_log per head.
-__global__ void __launch_bounds__(256) glr_param_grads_kernel(GlrParams p, int64_t parts, const float *dA_part,
-                                                              const float *ddt_part) {
-    __shared__ float sums[256];
-    const int64_t h = blockIdx.x;
-    float dA = 0.f;
-    for (int64_t k = threadIdx.x; k < p.K; k += 256) {
-        const int64_t c = h * p.K + k;
-        float ddt = 0.f;
-        for (int64_t j = 0; j < parts; ++j) {
-            ddt += ddt_part[j * p.D + c];
-            dA += dA_part[j * p.D + c];
+// Sums the tiles' partial parameter gradients [parts, width] over the tiles, 32 channels
+// per CTA: ddt_bias, and in part_dA's first row dA_log's sums per channel.
+__global__ void __launch_bounds__(1024) glr_param_sum_kernel(GlrParams p, int64_t parts, int64_t width, const float *part_ddt,
+                                                             float *part_dA) {
+    __shared__ float sums[2][32][33];
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    float ddt = 0.f, dA = 0.f;
+    if (c < p.D) {
+#pragma unroll 4
+        for (int64_t j = slice; j < parts; j += 32) {
+            ddt += part_ddt[j * width + c];
+            dA += part_dA[j * width + c];
         }
-        p.ddt_bias[c] = ddt;
     }
-    sums[threadIdx.x] = dA;
+    sums[0][slice][lane] = ddt;
+    sums[1][slice][lane] = dA;
     __syncthreads();
-    for (int w = 128; w; w >>= 1) {
-        if (threadIdx.x < w) sums[threadIdx.x] += sums[threadIdx.x + w];
-        __syncthreads();
+    if (slice < 2 && c < p.D) {
+        float t = 0.f;
+        for (int j = 0; j < 32; ++j) t += sums[slice][j][lane];
+        if (slice == 0) p.ddt_bias[c] = t;
+        else if (parts > 0) part_dA[c] = t;
     }
-    if (threadIdx.x == 0) p.dA_log[h] = sums[0];
+}
+__global__ void __launch_bounds__(128) glr_head_sum_kernel(GlrParams p, bool any, const float *dA) {
+    __shared__ float sums[4];
+    float t = 0.f;
+    if (any)
+        for (int64_t k = threadIdx.x; k < p.K; k += 128) t += dA[blockIdx.x * p.K + k];
+    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = t;
+    __syncthreads();
+    if (threadIdx.x == 0) p.dA_log[blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
 // The forward run that writes checkpoints only.
@@ -85,33 +287,82 @@ GlrParams states_only(const GlrParams &p) {
     return f;
 }
 
+// V channels per thread where every row of the inputs and gradients allows it.
+bool vector_rows(const GlrParams &p) {
+    const size_t V = p.dtype == kFP32 ? 2 : 4, n = V * dtype_bytes(p.dtype);
+    const void *ptrs[] = {p.x, p.i, p.g, p.dout, p.dx, p.di, p.dg};
+    for (const void *q : ptrs)
+        if (reinterpret_cast<uintptr_t>(q) % n) return false;
+    return p.D % V == 0 && p.xs % V == 0 && p.is % V == 0 && p.gs % V == 0 && p.ds % V == 0;
+}
+int block_channels(const GlrParams &p) { return vector_rows(p) && p.dtype != kFP32 ? 64 : 32; }
+
+// Workspace: the scan's, the partial sums, the checkpoints and the forward run's workspace.
+struct BwdPlan {
+    ScanPlan s;
+    float *part_ddt, *part_dA, *checkpoints;
+    unsigned char *fwd;
+    size_t bytes;
+};
+BwdPlan bwd_plan(const GlrParams &p, int sms, unsigned char *ws) {
+    BwdPlan b;
+    size_t at = 0;
+    b.s = scan_plan(p.rows, p.D, block_channels(p), ws, &at);
+    const size_t part = (size_t)(b.s.row_tiles * b.s.width) * sizeof(float);
+    const size_t ck = p.checkpoints ? 0 : ((size_t)(b.s.row_tiles * p.D) * sizeof(float) + 15) / 16 * 16;
+    b.part_ddt = reinterpret_cast<float *>(ws + at);
+    b.part_dA = reinterpret_cast<float *>(ws + at + part);
+    b.checkpoints = reinterpret_cast<float *>(ws + at + 2 * part);
+    b.fwd = ws + at + 2 * part + ck;
+    b.bytes = at + 2 * part + ck + (p.checkpoints ? 0 : glr_fwd_scratch_bytes(states_only(p), sms));
+    return b;
+}
+
+template <typename E, int V, bool UB>
+cudaError_t run(const GlrParams &p, const BwdPlan &b, int sms, cudaStream_t stream) {
+    ScanPlan s = b.s;
+    const int64_t fill = s.row_tiles * s.width / 2 + s.width;
+    glr_prepare_kernel<UB, true><<<(unsigned)std::min(ceil_div(fill, 256), (int64_t)sms * 4), 256, 0, stream>>>(p, s);
+    if (s.row_tiles == 0) return cudaGetLastError();
+    int ctas = 0;
+    constexpr int bytes = (int)sizeof(BwdShared<E, V>);
+    constexpr auto kernel = glr_bwd_scan_kernel<E, V, UB>;
+    const cudaError_t e = resident_ctas<kernel>(BwdShape<E, V>::THREADS, bytes, ctas);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)std::min(s.row_tiles * s.blocks, (int64_t)sms * ctas);
+    GlrParams arg = p;
+    float *ddt = b.part_ddt, *dA = b.part_dA;
+    void *args[] = {&arg, &s, &ddt, &dA};
+    return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(BwdShape<E, V>::THREADS), args,
+                                       bytes, stream);
+}
+
 }  // namespace
 
-size_t glr_bwd_scratch_bytes(const GlrParams &p, int sms) {
-    const size_t part = (size_t)(p.N * p.D) * sizeof(float);
-    const size_t ck = p.checkpoints ? 0 : (size_t)(ceil_div(p.rows, kGlrCheckpointRows) * p.D) * sizeof(float);
-    return (2 * part + ck + 15) / 16 * 16 + (p.checkpoints ? 0 : glr_fwd_scratch_bytes(states_only(p), sms));
-}
+size_t glr_bwd_scratch_bytes(const GlrParams &p, int sms) { return bwd_plan(p, sms, nullptr).bytes; }
 
 cudaError_t launch_glr_bwd(const GlrParams &p0, unsigned char *ws, int sms, cudaStream_t stream) {
     GlrParams p = p0;
-    const int64_t units = p.N * p.D;
-    float *dA_part = reinterpret_cast<float *>(ws), *ddt_part = dA_part + units;
-    if (units > 0) {
+    const BwdPlan b = bwd_plan(p, sms, ws);
+    cudaError_t e = cudaSuccess;
+    if (p.N > 0 && p.D > 0) {
         if (!p.checkpoints) {
-            p.checkpoints = ddt_part + units;
-            const size_t used = (size_t)(2 * units + ceil_div(p.rows, kGlrCheckpointRows) * p.D) * sizeof(float);
-            const cudaError_t e = launch_glr_fwd(states_only(p), ws + (used + 15) / 16 * 16, sms, stream);
+            p.checkpoints = b.checkpoints;
+            e = launch_glr_fwd(states_only(p), b.fwd, sms, stream);
             if (e != cudaSuccess) return e;
         }
-        const unsigned grid = (unsigned)ceil_div(units, 256);
-        with_dtype(p.dtype, [&](auto *tag) {
+        const bool vec = vector_rows(p);
+        e = with_dtype(p.dtype, [&](auto *tag) {
             using E = std::remove_pointer_t<decltype(tag)>;
-            if (p.unbounded) glr_bwd_serial_kernel<E, true><<<grid, 256, 0, stream>>>(p, dA_part, ddt_part);
-            else glr_bwd_serial_kernel<E, false><<<grid, 256, 0, stream>>>(p, dA_part, ddt_part);
+            constexpr int V = sizeof(E) == 4 ? 2 : 4;
+            if (vec) return p.unbounded ? run<E, V, true>(p, b, sms, stream) : run<E, V, false>(p, b, sms, stream);
+            return p.unbounded ? run<E, 1, true>(p, b, sms, stream) : run<E, 1, false>(p, b, sms, stream);
         });
+        if (e != cudaSuccess) return e;
     }
-    glr_param_grads_kernel<<<(unsigned)p.H, 256, 0, stream>>>(p, p.N, dA_part, ddt_part);
+    if (p.D > 0)
+        glr_param_sum_kernel<<<(unsigned)ceil_div(p.D, 32), 1024, 0, stream>>>(p, b.s.row_tiles, b.s.width, b.part_ddt, b.part_dA);
+    glr_head_sum_kernel<<<(unsigned)p.H, 128, 0, stream>>>(p, b.s.row_tiles > 0, b.part_dA);
     return cudaGetLastError();
 }
 

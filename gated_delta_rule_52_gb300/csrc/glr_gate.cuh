@@ -18,14 +18,17 @@ __device__ __forceinline__ GateConst gate_const(float A_log, float dt_bias) {
     return UB ? GateConst{-e, kLog2e * dt_bias} : GateConst{-kLog2e * e, -kLog2e * e * dt_bias};
 }
 
+// 2 log2(e) P(z), P the degree-4 Chebyshev fit of atanh(s) / s over z = s^2 in [0, 1/9]
+// (relative error 8e-9).
+__device__ __forceinline__ float atanh_poly(float z) {
+    return fmaf(z, fmaf(z, fmaf(z, fmaf(z, 0.40647438f, 0.40339801f), 0.57743657f), 0.96179163f), 2.88539004f);
+}
 // log2(1 + t) for t in [0, 1], to fp32 accuracy relative to the result (lg2(1 + t) rounds
 // a small t away, and the sum of many small log decays with it): with s = t / (2 + t),
-// log(1 + t) = 2 atanh(s) = 2 s P(s^2), P the degree-4 Chebyshev fit of atanh(s) / s over
-// s^2 in [0, 1/9] (relative error 8e-9).
+// log(1 + t) = 2 atanh(s).
 __device__ __forceinline__ float log2_1p(float t) {
     const float s = t * rcp(2.f + t), z = s * s;
-    const float q = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 0.40647438f, 0.40339801f), 0.57743657f), 0.96179163f), 2.88539004f);
-    return s * q;
+    return s * atanh_poly(z);
 }
 
 // Decay a = exp(gk) of one token.  Bounded: gk = lb sigma(e (g + bias)), lb2 = lb log2(e);
@@ -66,23 +69,41 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
     const float2 d = add2(make_float2(ex2(m.x), ex2(m.y)), make_float2(1.f, 1.f));
     return make_float2(rcp(d.x), rcp(d.y));
 }
-// The same, with what the derivative needs: slope = d gk / d g, and rate, d gk / d A_log.
+// What the derivatives of one token are formed from, kept between the two halves of the
+// backward pass: `gate` is the decay a (bounded) or its log2 (else), `mg` and `mi` the
+// smaller of sigma(v) and sigma(-v) for the gate's argument and for i.  The smaller one is
+// exact relative to itself, and with it both sigma and its slope m (1 - m).
+struct TokenGates { float gate, mg, mi; };
+
 template <bool UB>
-__device__ __forceinline__ float gate_slopes(float g, GateConst c, float lb2, float &slope, float &rate) {
+__device__ __forceinline__ TokenGates token_gates(float g, float i, GateConst c, float lb2, float &a, float &s) {
+    const float ti = ex2(-kLog2e * fabsf(i)), mi = ti * rcp(1.f + ti);
+    s = i >= 0.f ? 1.f - mi : mi;
     if (UB) {
         const float u2 = fmaf(kLog2e, g, c.k1);
-        const float t = ex2(-fabsf(u2)), r = rcp(1.f + t);
-        const float gk2 = c.k0 * (fmaxf(u2, 0.f) + log2_1p(t));
-        slope = c.k0 * (u2 >= 0.f ? r : t * r);
-        rate = kLn2 * gk2;
-        return ex2(gk2);
+        const float t = ex2(-fabsf(u2)), d1 = 1.f + t, d2 = 2.f + t, r = rcp(d1 * d2);   // both reciprocals
+        const float q = t * d1 * r;                                                     // t / (2 + t)
+        const float gk2 = c.k0 * fmaf(q, atanh_poly(q * q), fmaxf(u2, 0.f));
+        a = ex2(gk2);
+        return {gk2, t * d2 * r, mi};
     }
     const float z2 = fmaf(c.k0, g, c.k1);   // -log2(e) z
-    const float t = ex2(-fabsf(z2)), r = rcp(1.f + t), tr = t * r;
-    const float lsl = lb2 * tr * r;         // lb2 sigma'(z)
-    slope = -lsl * c.k0 * (kLn2 * kLn2);    // lb sigma'(z) e
-    rate = -lsl * z2 * (kLn2 * kLn2);       // lb sigma'(z) z
-    return ex2(lb2 * (z2 <= 0.f ? r : tr));
+    const float t = ex2(-fabsf(z2)), mg = t * rcp(1.f + t);
+    a = ex2(lb2 * (z2 <= 0.f ? 1.f - mg : mg));
+    return {a, mg, mi};
+}
+// slope = d gk / d g, rate = d gk / d A_log, from the same token's kept values.
+template <bool UB>
+__device__ __forceinline__ void gate_slopes(float g, GateConst c, float lb, const TokenGates &k, float &slope, float &rate) {
+    if (UB) {
+        const float u2 = fmaf(kLog2e, g, c.k1);
+        slope = c.k0 * (u2 >= 0.f ? 1.f - k.mg : k.mg);
+        rate = kLn2 * fmaxf(k.gate, -1e30f);   // a decay of 0 times its infinite log is 0
+    } else {
+        const float z2 = fmaf(c.k0, g, c.k1), l = -kLn2 * lb * (k.mg - k.mg * k.mg);   // -ln 2 lb sigma'
+        slope = l * c.k0;
+        rate = l == 0.f ? 0.f : l * z2;       // so is a slope of 0 times an infinite argument
+    }
 }
 
 }  // namespace layer

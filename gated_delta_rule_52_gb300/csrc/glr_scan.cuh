@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(256) glr_prepare_kernel(GlrParams p, ScanPlan 
         seq_rows(p, n, lo, hi);
         s.first_seq[t] = (int)n | (lo < r0 && hi > r0 + kTileRows ? kInside : 0);
     }
-    if (!p.cu_seqlens) return;
+    if (!p.cu_seqlens && p.T > 0) return;
     if (REVERSE ? !p.dinit : !p.fin) return;
     // a warp per sequence: one without tokens passes its state through
     for (int64_t n = at >> 5; n < p.N; n += step >> 5) {
@@ -250,6 +250,27 @@ struct TileWalk {
         if (cb >= blocks) cb -= blocks, ++rt;
     }
 };
+
+// CTAs of a kernel that an SM holds, its dynamic shared memory allowed first; looked up once
+// per device.
+template <auto Kernel>
+cudaError_t resident_ctas(int threads, int smem, int &ctas) {
+    static std::atomic<bool> done[kMaxDevices];
+    static int per_sm[kMaxDevices];
+    int dev = 0;
+    ctas = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = once_per_device(done, [&](int d) {
+        cudaError_t r = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (r == cudaSuccess) r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, Kernel, threads, smem);
+        if (r == cudaSuccess && ctas < 1) r = cudaErrorInvalidConfiguration;
+        if (d < kMaxDevices) per_sm[d] = ctas;
+        return r;
+    });
+    if (dev < kMaxDevices) ctas = per_sm[dev];
+    return e;
+}
 
 }  // namespace layer
 }  // namespace kda

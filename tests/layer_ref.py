@@ -50,7 +50,7 @@ def glr(x, i, g, A_log, dt_bias, lb, seqs, init=None, dout=None, dfinal=None):
     N = len(seqs)
     e = A_log.exp()[:, None]
     u = g + dt_bias
-    gk = -e * torch.nn.functional.softplus(u, threshold=1e6) if lb is None else lb * sig(e * u)
+    gk = -e * torch.nn.functional.softplus(u, threshold=40.0) if lb is None else lb * sig(e * u)
     a, s = gk.exp(), sig(i)
     b = s * x
     start, h, E0, E = (torch.zeros(R, H, K, dtype=torch.float64) for _ in range(4))

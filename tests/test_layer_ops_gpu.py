@@ -143,6 +143,27 @@ def test_glr_masked_tokens(T, lb):
 
 
 @pytest.mark.parametrize("lb", [-5.0, None])
+def test_glr_gradient_at_masked_tokens(lb):
+    # infinite logits have the gradients of very large ones: 0 for the masked token's own
+    d = _glr_inputs(2, 200, 2, 32, BF, None, F, 22)
+    d["i"][:, 1::5] = float("-inf")
+    d["g"][:, 1::3] = float("-inf")
+    d["g"][:, 2::11] = float("inf")
+    got = _glr_run(d, lb)
+    for k in ("i", "g"):
+        d[k] = d[k].float().clamp(-1e4, 1e4)
+    _glr_check(got, _glr_ref(d, lb))
+
+
+@pytest.mark.parametrize("B", [0, 3])
+def test_glr_without_tokens(B):
+    d = _glr_inputs(B, 0, 2, 16, BF, None, F, 23)
+    got = _glr_run(d, -5.0)
+    assert torch.equal(got["final"].cpu(), d["init"]) and torch.equal(got["dinit"].cpu(), d["dfinal"])
+    assert not got["dA_log"].any() and not got["ddt_bias"].any()
+
+
+@pytest.mark.parametrize("lb", [-5.0, None])
 def test_glr_sequences_do_not_reach_each_other(lb):
     lens = (100, 3, 64, 64, 200, 1, 1, 90)
     d = _glr_inputs(1, sum(lens), 2, 40, BF, lens, F, 5)
