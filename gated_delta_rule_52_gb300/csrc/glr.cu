@@ -91,17 +91,10 @@ __global__ void __launch_bounds__(FwdShape<V>::THREADS, kFwdCtas) glr_fwd_scan_k
             copy_async<float, V == 4 ? 4 : 2>(&sh.gates[tid], gate);
             if (V == 4) copy_async<float, V == 4 ? 4 : 2>(&sh.gates[tid].e[V / 2], gate + V);
             if (c < p.D) {
-                const E *x = static_cast<const E *>(p.x) + r0 * p.xs + c, *i = static_cast<const E *>(p.i) + r0 * p.is + c,
-                        *g = static_cast<const E *>(p.g) + r0 * p.gs + c;
                 const int left = (int)min(p.rows - r0, (int64_t)L);
-#pragma unroll
-                for (int r = 0; r < L; ++r, x += p.xs, i += p.is, g += p.gs) {
-                    if (r < left) {
-                        copy_async<E, V>(&sh.raw[0][r][tid], x);
-                        copy_async<E, V>(&sh.raw[1][r][tid], i);
-                        copy_async<E, V>(&sh.raw[2][r][tid], g);
-                    }
-                }
+                copy_rows<E, V, L, S::THREADS>(&sh.raw[0][0][tid], static_cast<const E *>(p.x) + r0 * p.xs + c, p.xs, left);
+                copy_rows<E, V, L, S::THREADS>(&sh.raw[1][0][tid], static_cast<const E *>(p.i) + r0 * p.is + c, p.is, left);
+                copy_rows<E, V, L, S::THREADS>(&sh.raw[2][0][tid], static_cast<const E *>(p.g) + r0 * p.gs + c, p.gs, left);
             }
         }
         copies_commit();

@@ -64,18 +64,15 @@ __global__ void __launch_bounds__(BwdShape<E, V>::THREADS, V == 4 ? 2 : 3)
             if (V == 4) copy_async<float, 4>(&sh.gates[stage][tid].e[V / 2], gate + 4);
             if (role == 2 && w.cb * CB + ch < p.D) checkpoint = p.checkpoints[rt * p.D + w.cb * CB + ch];
             if (c < p.D) {
-                const E *x = static_cast<const E *>(p.x) + r0 * p.xs + c, *i = static_cast<const E *>(p.i) + r0 * p.is + c,
-                        *g = static_cast<const E *>(p.g) + r0 * p.gs + c, *d = static_cast<const E *>(p.dout) + r0 * p.ds + c;
                 const int left = (int)min(p.rows - r0, (int64_t)L);
-#pragma unroll
-                for (int r = 0; r < L; ++r, x += p.xs, i += p.is, g += p.gs, d += p.ds) {
-                    if (r < left) {
-                        copy_async<E, V>(&sh.raw[stage][0][r][tid], x);
-                        copy_async<E, V>(&sh.raw[stage][1][r][tid], i);
-                        copy_async<E, V>(&sh.raw[stage][2][r][tid], g);
-                        copy_async<E, V>(&sh.raw[stage][3][r][tid], d);
-                    }
-                }
+                const auto copy = [&](int k, const void *src, int64_t stride) {
+                    copy_rows<E, V, L, S::THREADS>(&sh.raw[stage][k][0][tid], static_cast<const E *>(src) + r0 * stride + c,
+                                                   stride, left);
+                };
+                copy(0, p.x, p.xs);
+                copy(1, p.i, p.is);
+                copy(2, p.g, p.gs);
+                copy(3, p.dout, p.ds);
             }
         }
         copies_commit();
@@ -192,7 +189,7 @@ __global__ void __launch_bounds__(BwdShape<E, V>::THREADS, V == 4 ? 2 : 3)
                     h[v] = p.init ? ld_state(p.init, p.state_type, sh.marks.begins[rg * L + r] * p.D + c + v) : 0.f;
                 start[e] = h[v];
                 if (r < L - 1) {
-                    const float si = raw(1, e) >= 0.f ? 1.f - tg[e].mi : tg[e].mi, a = UB ? ex2(tg[e].gate) : tg[e].gate;
+                    const float si = raw(1, e) >= 0.f ? 1.f - tg[e].mi : tg[e].mi, a = UB ? exp2_decay(tg[e].gate) : tg[e].gate;
                     h[v] = fmaf(a, h[v], si * raw(0, e));
                 }
             }
@@ -212,7 +209,7 @@ __global__ void __launch_bounds__(BwdShape<E, V>::THREADS, V == 4 ? 2 : 3)
                     const int e = r * V + v;
                     if (ends >= 0) f[v] = p.dfinal ? p.dfinal[ends * p.D + c + v] : 0.f;
                     const float grad = raw(3, e) + f[v];
-                    f[v] = (UB ? ex2(tg[e].gate) : tg[e].gate) * grad;
+                    f[v] = (UB ? exp2_decay(tg[e].gate) : tg[e].gate) * grad;
                     if (begins >= 0 && p.dinit) p.dinit[begins * p.D + c + v] = f[v];
                     const float mi = tg[e].mi, other = 1.f - mi;
                     const float gm = grad * mi, go = grad * other;
@@ -248,25 +245,13 @@ __global__ void __launch_bounds__(BwdShape<E, V>::THREADS, V == 4 ? 2 : 3)
 // per CTA: ddt_bias, and in part_dA's first row dA_log's sums per channel.
 __global__ void __launch_bounds__(1024) glr_param_sum_kernel(GlrParams p, int64_t parts, int64_t width, const float *part_ddt,
                                                              float *part_dA) {
-    __shared__ float sums[2][32][33];
-    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-    float ddt = 0.f, dA = 0.f;
-    if (c < p.D) {
-#pragma unroll 4
-        for (int64_t j = slice; j < parts; j += 32) {
-            ddt += part_ddt[j * width + c];
-            dA += part_dA[j * width + c];
-        }
-    }
-    sums[0][slice][lane] = ddt;
-    sums[1][slice][lane] = dA;
+    const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+    const float ddt = column_sum(part_ddt, parts, width, c, c < p.D);
     __syncthreads();
-    if (slice < 2 && c < p.D) {
-        float t = 0.f;
-        for (int j = 0; j < 32; ++j) t += sums[slice][j][lane];
-        if (slice == 0) p.ddt_bias[c] = t;
-        else if (parts > 0) part_dA[c] = t;
+    const float dA = column_sum(part_dA, parts, width, c, c < p.D);
+    if (threadIdx.x < 32 && c < p.D) {
+        p.ddt_bias[c] = ddt;
+        if (parts > 0) part_dA[c] = dA;   // no other CTA reads this column
     }
 }
 __global__ void __launch_bounds__(128) glr_head_sum_kernel(GlrParams p, bool any, const float *dA) {

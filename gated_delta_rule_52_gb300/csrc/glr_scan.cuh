@@ -14,7 +14,7 @@
 #pragma once
 
 #include "glr_gate.cuh"
-#include "sm103.cuh"
+#include "layer_copy.cuh"
 
 namespace kda {
 namespace layer {
@@ -103,23 +103,6 @@ __device__ __forceinline__ U await(const U *at, U v, int *err) {
     }
     return v;
 }
-
-// Asynchronous copy of one thread's V elements into its own slot of shared memory (2-byte
-// elements that are alone are copied at once).
-template <typename E, int V>
-__device__ __forceinline__ void copy_async(void *slot, const E *src) {
-    constexpr int n = sizeof(E) * V;
-    static_assert(n == 2 || n == 4 || n == 8 || n == 16, "copy size");
-    if constexpr (n == 2)
-        *reinterpret_cast<E *>(slot) = *src;
-    else if constexpr (n == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm103::smem_u32(slot)), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(sm103::smem_u32(slot)), "l"(src), "n"(n) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // How a CTA covers a tile: THREADS threads as CL channel lanes of V channels each by RG row
 // groups of L rows each.

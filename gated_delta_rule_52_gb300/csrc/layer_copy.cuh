@@ -1,0 +1,65 @@
+// Asynchronous copies into a thread's own slots of shared memory, and sums of partial
+// results over CTAs.
+#pragma once
+
+#include "layer_io.cuh"
+#include "sm103.cuh"
+
+namespace kda {
+namespace layer {
+
+// Copies V elements (4, 8 or 16 bytes) of one thread.
+template <typename E, int V>
+__device__ __forceinline__ void copy_async(void *slot, const E *src) {
+    constexpr int n = sizeof(E) * V;
+    static_assert(n == 4 || n == 8 || n == 16, "copy size");
+    if constexpr (n == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm103::smem_u32(slot)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(sm103::smem_u32(slot)), "l"(src), "n"(n) : "memory");
+}
+// Copies `count` <= N groups of V elements, `stride` elements apart, into slots THREADS
+// groups apart.  Single 2-byte elements have no asynchronous copy: they are loaded
+// together, then stored.
+template <typename E, int V, int N, int THREADS>
+__device__ __forceinline__ void copy_rows(Pack<E, V> *slots, const E *src, int64_t stride, int count) {
+    if constexpr (sizeof(E) * V == 2) {
+        E t[N];
+#pragma unroll
+        for (int r = 0; r < N; ++r)
+            if (r < count) t[r] = src[r * stride];
+#pragma unroll
+        for (int r = 0; r < N; ++r)
+            if (r < count) slots[r * THREADS].e[0] = t[r];
+    } else {
+#pragma unroll
+        for (int r = 0; r < N; ++r, src += stride)
+            if (r < count) copy_async<E, V>(slots + r * THREADS, src);
+    }
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Sum over j of part[j * width + c], 32 columns per CTA of 1024 threads, in a fixed order.
+// The threads of the CTA's first warp have the sum of column 32 blockIdx.x + lane.
+__device__ __forceinline__ float column_sum(const float *part, int64_t parts, int64_t width, int64_t c, bool in) {
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    float t = 0.f;
+    if (in) {
+#pragma unroll 4
+        for (int64_t j = slice; j < parts; j += 32) t += part[j * width + c];
+    }
+    sums[slice][lane] = t;
+    __syncthreads();
+    t = sums[lane][slice];   // warp `slice` holds column `slice`'s 32 partial sums
+    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    __syncthreads();
+    if (lane == 0) sums[0][slice] = t;
+    __syncthreads();
+    return sums[0][lane];
+}
+
+}  // namespace layer
+}  // namespace kda

@@ -2,46 +2,118 @@
 //   y = (x - mean) rstd w + b,  rstd = 1 / sqrt(var + eps)
 //   with d = dy w, xh = (x - mean) rstd:  dx = rstd (d - mean(d) - xh mean(d xh)),
 //   dw = sum over rows of dy xh, db = sum over rows of dy
-// Sums are fp32; the variance is the mean square of x - mean (two passes).
+// Sums are fp32; the variance is the mean square of x - mean, formed after the mean from
+// the row that the threads hold in registers.
 //
-// One CTA per row; the weight's gradient by a thread per column and row block.
-#include "layer_io.cuh"
+// Both directions move each value once.  Threads blockDim.x share a row (a warp for short
+// rows, then blockDim.y rows per CTA), EL elements each.  The backward kernel is
+// persistent: a CTA walks its rows with the next ones on their way into shared memory, a
+// thread keeps its columns' weights and their gradients in registers, and one partial sum
+// per CTA and column is left for a second kernel.  Rows too long for that (more than 32768
+// forward, 8192 backward) run kernels that pass over a row again through L2.
+#include <algorithm>
+
+#include "layer_copy.cuh"
 
 namespace kda {
 namespace {
 
 using namespace layer;
 
-constexpr int kThreads = 256;
+constexpr int kMaxWarps = 32;
 
-__device__ float block_sum(float v) {
-    __shared__ float part[kThreads / 32];
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// Sums of K values over the blockDim.x threads of every row of the CTA; all threads of the
+// CTA call it together.  `part`: one warp's sums each; a caller's next call must use
+// another one.
+template <int K>
+__device__ __forceinline__ void row_sums(float (&v)[K], float (&part)[K][kMaxWarps]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return;
+    const int first = threadIdx.y * warps, lane = threadIdx.x & 31;
+    if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) part[k][first + (threadIdx.x >> 5)] = v[k];
+    }
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-    for (int w = 0; w < kThreads / 32; ++w) v += part[w];
-    return v;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        v[k] = lane < warps ? part[k][first + lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    }
 }
 
-template <typename E>
-__global__ void __launch_bounds__(kThreads) norm_fwd_kernel(NormParams p) {
-    const int64_t row = blockIdx.x;
-    const E *x = static_cast<const E *>(p.x) + row * p.xs;
-    E *out = static_cast<E *>(p.out) + row * p.os;
-    float s = 0.f;
-    for (int64_t c = threadIdx.x; c < p.D; c += kThreads) s += to_f(x[c]);
-    const float mean = block_sum(s) / (float)p.D;
-    s = 0.f;
-    for (int64_t c = threadIdx.x; c < p.D; c += kThreads) {
-        const float d = to_f(x[c]) - mean;
-        s += d * d;
+// Column of group k of a thread: groups of V, neighbouring threads side by side.
+template <int V>
+__device__ __forceinline__ int column(int k) { return (k * blockDim.x + threadIdx.x) * V; }
+
+template <int V>
+__device__ __forceinline__ void ld_param(const float *p, int c, float dflt, float (&f)[V]) {
+    if (!p) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[v] = dflt;
+        return;
     }
-    const float rstd = 1.f / sqrtf(block_sum(s) / (float)p.D + p.eps);
-    for (int64_t c = threadIdx.x; c < p.D; c += kThreads) {
-        const float xh = (to_f(x[c]) - mean) * rstd;
-        out[c] = from_f<E>(xh * (p.weight ? p.weight[c] : 1.f) + (p.bias ? p.bias[c] : 0.f));
+    if constexpr (V >= 4) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            const float4 t = *reinterpret_cast<const float4 *>(p + c + v);
+            f[v] = t.x, f[v + 1] = t.y, f[v + 2] = t.z, f[v + 3] = t.w;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[v] = p[c + v];
+    }
+}
+
+template <typename E, int V, int EL>
+__global__ void __launch_bounds__(1024) norm_fwd_kernel(NormParams p) {
+    constexpr int N = EL / V;
+    __shared__ float part[2][1][kMaxWarps];
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const bool live = row < p.rows;
+    const E *x = static_cast<const E *>(p.x) + row * p.xs;
+    Pack<E, V> raw[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (live && column<V>(k) < p.D) raw[k] = ld_pack<E, V>(x + column<V>(k));
+    float s[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if (!live || column<V>(k) >= p.D) continue;
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[0] += to_f(raw[k].e[v]);
+    }
+    row_sums<1>(s, part[0]);
+    const float inv = 1.f / (float)p.D, mean = s[0] * inv;
+    s[0] = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if (!live || column<V>(k) >= p.D) continue;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float d = to_f(raw[k].e[v]) - mean;
+            s[0] = fmaf(d, d, s[0]);
+        }
+    }
+    row_sums<1>(s, part[1]);
+    if (!live) return;
+    const float rstd = 1.f / sqrtf(fmaf(s[0], inv, p.eps));
+    E *out = static_cast<E *>(p.out) + row * p.os;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int c = column<V>(k);
+        if (c >= p.D) continue;
+        float w[V], b[V], y[V];
+        ld_param<V>(p.weight, c, 1.f, w);
+        ld_param<V>(p.bias, c, 0.f, b);
+#pragma unroll
+        for (int v = 0; v < V; ++v) y[v] = fmaf((to_f(raw[k].e[v]) - mean) * rstd, w[v], b[v]);
+        st_f<E, V>(out + c, y);
     }
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mean;
@@ -49,83 +121,290 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_kernel(NormParams p) {
     }
 }
 
+constexpr int kStages = 3;
+
+template <typename E, int V, int EL>
+__global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *part_out) {
+    constexpr int N = EL / V;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float part[2][2][kMaxWarps];
+    __shared__ float2 stats[kStages][kMaxWarps];
+    const int threads = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x, warp = tid >> 5;
+    Pack<E, V> *ring = reinterpret_cast<Pack<E, V> *>(smem);   // [stage][x, dy][group][thread]
+    const auto slot = [&](int stage, int t, int k) -> Pack<E, V> & { return ring[((stage * 2 + t) * N + k) * threads + tid]; };
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < p.rows) {
+            const E *x = static_cast<const E *>(p.x) + row * p.xs, *dy = static_cast<const E *>(p.dout) + row * p.ds;
+            if constexpr (sizeof(E) * V == 2) {
+                E t[2 * N];
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    if (column<V>(k) < p.D) t[2 * k] = x[column<V>(k)], t[2 * k + 1] = dy[column<V>(k)];
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    if (column<V>(k) < p.D) slot(stage, 0, k).e[0] = t[2 * k], slot(stage, 1, k).e[0] = t[2 * k + 1];
+            } else {
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    if (column<V>(k) < p.D) {
+                        copy_async<E, V>(&slot(stage, 0, k), x + column<V>(k));
+                        copy_async<E, V>(&slot(stage, 1, k), dy + column<V>(k));
+                    }
+                }
+            }
+            if ((tid & 31) == 0) {
+                copy_async<float, 1>(&stats[stage][warp].x, p.mean + row);
+                copy_async<float, 1>(&stats[stage][warp].y, p.rstd + row);
+            }
+        }
+        copies_commit();
+    };
+
+    float w[EL], dw[EL], db[EL];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        float t[V] = {};
+        if (column<V>(k) < p.D) ld_param<V>(p.weight, column<V>(k), 1.f, t);
+#pragma unroll
+        for (int v = 0; v < V; ++v) w[k * V + v] = t[v], dw[k * V + v] = db[k * V + v] = 0.f;
+    }
+    const float inv = 1.f / (float)p.D;
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int64_t passes = ceil_div(p.rows - (int64_t)blockIdx.x * blockDim.y, step);
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(row + k * step, k);
+    for (int64_t pass = 0; pass < passes; ++pass, row += step) {
+        const int stage = (int)(pass % kStages);
+        fetch(row + (kStages - 1) * step, (int)((pass + kStages - 1) % kStages));
+        copies_wait<kStages - 1>();
+        __syncwarp();
+        const bool live = row < p.rows;
+        const float2 st = stats[stage][warp];
+        float xh[EL], d[EL], s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const bool in = live && column<V>(k) < p.D;
+            const Pack<E, V> x = slot(stage, 0, k), dy = slot(stage, 1, k);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e = k * V + v;
+                const float g = in ? to_f(dy.e[v]) : 0.f;
+                xh[e] = in ? (to_f(x.e[v]) - st.x) * st.y : 0.f;
+                d[e] = g * w[e];
+                s[0] += d[e];
+                s[1] = fmaf(d[e], xh[e], s[1]);
+                dw[e] = fmaf(g, xh[e], dw[e]);
+                db[e] += g;
+            }
+        }
+        row_sums<2>(s, part[pass & 1]);
+        if (!live) continue;
+        const float m1 = s[0] * inv, m2 = s[1] * inv;
+        E *dx = static_cast<E *>(p.dx) + row * p.D;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (column<V>(k) >= p.D) continue;
+            float o[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = st.y * (d[k * V + v] - fmaf(xh[k * V + v], m2, m1));
+            st_f<E, V>(dx + column<V>(k), o);
+        }
+    }
+    copies_wait<0>();
+    if (!part_out) return;
+    // over the CTA's rows side by side, one after the other
+    float *sums = reinterpret_cast<float *>(smem);   // [2][EL][blockDim.x], over the ring
+    for (int y = 0; y < (int)blockDim.y; ++y) {
+        __syncthreads();
+        if ((int)threadIdx.y != y) continue;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+            float *at = sums + e * blockDim.x + threadIdx.x;
+            if (y > 0) dw[e] += at[0], db[e] += at[EL * blockDim.x];
+            if (y + 1 < (int)blockDim.y) at[0] = dw[e], at[EL * blockDim.x] = db[e];
+        }
+    }
+    if (threadIdx.y == blockDim.y - 1) {
+        float *at = part_out + (int64_t)blockIdx.x * 2 * p.D;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+            const int c = column<V>(e / V) + e % V;
+            if (c < p.D) at[c] = dw[e], at[p.D + c] = db[e];
+        }
+    }
+}
+
+// ---- rows too long for a thread's registers: a CTA per row, several passes
 template <typename E>
-__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(NormParams p) {
+__global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormParams p) {
+    __shared__ float part[2][1][kMaxWarps];
+    const int64_t row = blockIdx.x;
+    const E *x = static_cast<const E *>(p.x) + row * p.xs;
+    E *out = static_cast<E *>(p.out) + row * p.os;
+    float s[1] = {0.f};
+    for (int64_t c = threadIdx.x; c < p.D; c += 1024) s[0] += to_f(x[c]);
+    row_sums<1>(s, part[0]);
+    const float mean = s[0] / (float)p.D;
+    s[0] = 0.f;
+    for (int64_t c = threadIdx.x; c < p.D; c += 1024) {
+        const float d = to_f(x[c]) - mean;
+        s[0] = fmaf(d, d, s[0]);
+    }
+    row_sums<1>(s, part[1]);
+    const float rstd = 1.f / sqrtf(s[0] / (float)p.D + p.eps);
+    for (int64_t c = threadIdx.x; c < p.D; c += 1024)
+        out[c] = from_f<E>(fmaf((to_f(x[c]) - mean) * rstd, p.weight ? p.weight[c] : 1.f, p.bias ? p.bias[c] : 0.f));
+    if (threadIdx.x == 0) {
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+}
+
+template <typename E>
+__global__ void __launch_bounds__(1024) norm_bwd_long_kernel(NormParams p) {
+    __shared__ float part[2][kMaxWarps];
     const int64_t row = blockIdx.x;
     const E *x = static_cast<const E *>(p.x) + row * p.xs, *dy = static_cast<const E *>(p.dout) + row * p.ds;
     const float mean = p.mean[row], rstd = p.rstd[row];
-    float s1 = 0.f, s2 = 0.f;
-    for (int64_t c = threadIdx.x; c < p.D; c += kThreads) {
+    float s[2] = {0.f, 0.f};
+    for (int64_t c = threadIdx.x; c < p.D; c += 1024) {
         const float d = to_f(dy[c]) * (p.weight ? p.weight[c] : 1.f);
-        s1 += d;
-        s2 += d * ((to_f(x[c]) - mean) * rstd);
+        s[0] += d;
+        s[1] = fmaf(d, (to_f(x[c]) - mean) * rstd, s[1]);
     }
-    s1 = block_sum(s1) / (float)p.D;
-    s2 = block_sum(s2) / (float)p.D;
-    for (int64_t c = threadIdx.x; c < p.D; c += kThreads) {
+    row_sums<2>(s, part);
+    const float m1 = s[0] / (float)p.D, m2 = s[1] / (float)p.D;
+    for (int64_t c = threadIdx.x; c < p.D; c += 1024) {
         const float d = to_f(dy[c]) * (p.weight ? p.weight[c] : 1.f), xh = (to_f(x[c]) - mean) * rstd;
-        static_cast<E *>(p.dx)[row * p.D + c] = from_f<E>(rstd * (d - s1 - xh * s2));
+        static_cast<E *>(p.dx)[row * p.D + c] = from_f<E>(rstd * (d - fmaf(xh, m2, m1)));
     }
 }
 
-// Rows per partial sum of the weight's gradient.
-constexpr int64_t kPartRows = 128;
-
+// A thread per column, blockIdx.y a block of rows.
 template <typename E>
-__global__ void __launch_bounds__(kThreads) norm_param_part_kernel(NormParams p, float *dw, float *db) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x, r0 = blockIdx.y * kPartRows;
+__global__ void __launch_bounds__(256) norm_param_part_kernel(NormParams p, int64_t block_rows, float *part_out) {
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x, r0 = blockIdx.y * block_rows;
     if (c >= p.D) return;
     float w = 0.f, b = 0.f;
-    for (int64_t row = r0; row < min(r0 + kPartRows, p.rows); ++row) {
+#pragma unroll 8
+    for (int64_t row = r0; row < min(r0 + block_rows, p.rows); ++row) {
         const float dy = to_f(static_cast<const E *>(p.dout)[row * p.ds + c]);
-        w += dy * ((to_f(static_cast<const E *>(p.x)[row * p.xs + c]) - p.mean[row]) * p.rstd[row]);
+        w = fmaf(dy, (to_f(static_cast<const E *>(p.x)[row * p.xs + c]) - p.mean[row]) * p.rstd[row], w);
         b += dy;
     }
-    dw[blockIdx.y * p.D + c] = w;
-    db[blockIdx.y * p.D + c] = b;
+    part_out[blockIdx.y * 2 * p.D + c] = w;
+    part_out[blockIdx.y * 2 * p.D + p.D + c] = b;
 }
 
-__global__ void __launch_bounds__(kThreads) norm_param_sum_kernel(NormParams p, int64_t parts, const float *dw,
-                                                                  const float *db) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= p.D) return;
-    float w = 0.f, b = 0.f;
-    for (int64_t j = 0; j < parts; ++j) {
-        w += dw[j * p.D + c];
-        b += db[j * p.D + c];
+// part [parts, 2, D] to dweight, dbias.
+__global__ void __launch_bounds__(1024) norm_param_sum_kernel(NormParams p, int64_t parts, const float *part) {
+    const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+    const float t = column_sum(part, parts, 2 * p.D, c, c < 2 * p.D);
+    if (threadIdx.x >= 32) return;
+    if (c < p.D) {
+        if (p.dweight) p.dweight[c] = t;
+    } else if (c < 2 * p.D) {
+        if (p.dbias) p.dbias[c - p.D] = t;
     }
-    if (p.dweight) p.dweight[c] = w;
-    if (p.dbias) p.dbias[c] = b;
 }
 
-// Partial sums: at most 65535 (a grid's y extent), so the rows of a launch are bounded.
-int64_t norm_parts(const NormParams &p) { return ceil_div(p.rows, kPartRows); }
+// ---- host side
+constexpr int64_t kFwdMaxD = 32768, kBwdMaxD = 8192;
+constexpr int64_t kLongParts = 256;
 
-}  // namespace
-
-size_t norm_bwd_scratch_bytes(const NormParams &p, int) {
-    return p.dweight || p.dbias ? (size_t)(2 * norm_parts(p) * p.D) * sizeof(float) : 0;
+// Threads of a row, and rows of a CTA: at most `most` threads, whole warps.
+dim3 row_block(int64_t D, int el, int most) {
+    const int x = (int)(ceil_div(D, 32 * el) * 32);
+    return dim3(x, x >= most ? 1 : most / x);
 }
 
-cudaError_t launch_norm_fwd(const NormParams &p, int, cudaStream_t stream) {
-    with_dtype(p.dtype, [&](auto *tag) {
-        using E = std::remove_pointer_t<decltype(tag)>;
-        norm_fwd_kernel<E><<<(unsigned)p.rows, kThreads, 0, stream>>>(p);
-    });
+// 16-byte groups where every row allows them.
+bool aligned_rows(const NormParams &p, const void *a, int64_t as, const void *b, int64_t bs) {
+    const int64_t V = 16 / (int64_t)dtype_bytes(p.dtype);
+    const void *ptrs[] = {p.x, a, b, p.weight, p.bias};
+    for (const void *q : ptrs)
+        if (reinterpret_cast<uintptr_t>(q) % 16) return false;
+    return p.D % V == 0 && p.xs % V == 0 && as % V == 0 && bs % V == 0;
+}
+
+bool wants_params(const NormParams &p) { return p.dweight || p.dbias; }
+
+// Backward: 16 elements per thread; 8 for rows that then still fit a CTA.
+int bwd_el(const NormParams &p) { return p.D <= 512 * 8 ? 8 : 16; }
+int64_t bwd_grid(const NormParams &p, int sms) {
+    return std::min(ceil_div(p.rows, (int64_t)row_block(p.D, bwd_el(p), 512).y), (int64_t)sms);
+}
+int64_t bwd_parts(const NormParams &p, int sms) {
+    if (p.rows == 0) return 0;
+    return p.D <= kBwdMaxD ? bwd_grid(p, sms) : std::min(ceil_div(p.rows, 64), kLongParts);
+}
+
+template <typename E, int V, int EL>
+cudaError_t run_fwd(const NormParams &p, cudaStream_t stream) {
+    const dim3 block = row_block(p.D, EL, 256);
+    norm_fwd_kernel<E, V, EL><<<(unsigned)ceil_div(p.rows, (int64_t)block.y), block, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
-cudaError_t launch_norm_bwd(const NormParams &p, unsigned char *ws, int, cudaStream_t stream) {
-    const int64_t parts = norm_parts(p);
-    const unsigned cols = (unsigned)ceil_div(p.D, kThreads);
-    float *dw = reinterpret_cast<float *>(ws), *db = dw + parts * p.D;
-    with_dtype(p.dtype, [&](auto *tag) {
-        using E = std::remove_pointer_t<decltype(tag)>;
-        if (p.rows > 0) norm_bwd_kernel<E><<<(unsigned)p.rows, kThreads, 0, stream>>>(p);
-        if ((p.dweight || p.dbias) && p.rows > 0)
-            norm_param_part_kernel<E><<<dim3(cols, (unsigned)parts), kThreads, 0, stream>>>(p, dw, db);
+template <typename E, int V, int EL>
+cudaError_t run_bwd(const NormParams &p, float *part, int sms, cudaStream_t stream) {
+    const dim3 block = row_block(p.D, EL, 512);
+    const int threads = block.x * block.y;
+    const int smem = threads * EL * std::max(kStages * 2 * (int)sizeof(E), block.y > 1 ? 8 : 0);
+    constexpr auto kernel = norm_bwd_kernel<E, V, EL>;
+    static std::atomic<bool> done[kMaxDevices];
+    const cudaError_t e = once_per_device(done, [&](int) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * EL * kStages * 2 * (int)sizeof(E));
     });
-    if (p.dweight || p.dbias) norm_param_sum_kernel<<<cols, kThreads, 0, stream>>>(p, parts, dw, db);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)bwd_grid(p, sms), block, smem, stream>>>(p, part);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t norm_bwd_scratch_bytes(const NormParams &p, int sms) {
+    return wants_params(p) ? (size_t)(bwd_parts(p, sms) * 2 * p.D) * sizeof(float) : 0;
+}
+
+cudaError_t launch_norm_fwd(const NormParams &p, int sms, cudaStream_t stream) {
+    return with_dtype(p.dtype, [&](auto *tag) {
+        using E = std::remove_pointer_t<decltype(tag)>;
+        constexpr int V = 16 / sizeof(E);
+        if (p.D > kFwdMaxD) {
+            norm_fwd_long_kernel<E><<<(unsigned)p.rows, 1024, 0, stream>>>(p);
+            return cudaGetLastError();
+        }
+        // few rows: more threads to each
+        const bool few = p.rows <= 4 * sms && p.D <= 8192;
+        if (aligned_rows(p, p.out, p.os, nullptr, 0)) return few ? run_fwd<E, V, 8>(p, stream) : run_fwd<E, V, 32>(p, stream);
+        return few ? run_fwd<E, 1, 8>(p, stream) : run_fwd<E, 1, 32>(p, stream);
+    });
+}
+
+cudaError_t launch_norm_bwd(const NormParams &p, unsigned char *ws, int sms, cudaStream_t stream) {
+    const int64_t parts = bwd_parts(p, sms);
+    float *part = wants_params(p) ? reinterpret_cast<float *>(ws) : nullptr;
+    const cudaError_t e = with_dtype(p.dtype, [&](auto *tag) {
+        using E = std::remove_pointer_t<decltype(tag)>;
+        constexpr int V = 16 / sizeof(E);
+        if (p.rows == 0) return cudaSuccess;
+        if (p.D > kBwdMaxD) {
+            norm_bwd_long_kernel<E><<<(unsigned)p.rows, 1024, 0, stream>>>(p);
+            if (part)
+                norm_param_part_kernel<E><<<dim3((unsigned)ceil_div(p.D, 256), (unsigned)parts), 256, 0, stream>>>(
+                    p, ceil_div(p.rows, parts), part);
+            return cudaGetLastError();
+        }
+        const bool wide = aligned_rows(p, p.dout, p.ds, p.dx, 0);
+        if (bwd_el(p) == 8) return wide ? run_bwd<E, V, 8>(p, part, sms, stream) : run_bwd<E, 1, 8>(p, part, sms, stream);
+        return wide ? run_bwd<E, V, 16>(p, part, sms, stream) : run_bwd<E, 1, 16>(p, part, sms, stream);
+    });
+    if (e != cudaSuccess) return e;
+    if (part || (wants_params(p) && p.rows == 0))
+        norm_param_sum_kernel<<<(unsigned)ceil_div(2 * p.D, 32), 1024, 0, stream>>>(p, parts, part);
     return cudaGetLastError();
 }
 
