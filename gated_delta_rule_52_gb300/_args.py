@@ -1,5 +1,8 @@
 """Argument checks and marshalling shared by the operators around the delta rule (glr,
-layer_norm, short_conv): element types, token tensors with strided rows, streams."""
+layer_norm, short_conv): element types, token tensors with strided rows, streams.
+
+A decode step's call costs more on the host than on the GPU, so the checks look at a
+contiguous tensor once and take the current stream's handle without building a Stream."""
 from __future__ import annotations
 
 import contextlib
@@ -9,6 +12,17 @@ import torch
 from . import kda
 
 DTYPES = {torch.bfloat16: 1, torch.float32: 2, torch.float16: 3}   # kda_dtype
+STATES = {torch.bfloat16: kda.KDA_STATE_BF16, torch.float32: kda.KDA_STATE_FP32}
+
+_entry = {}
+
+
+def entry(name):
+    """The library's C entry point."""
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = getattr(kda.lib(), name)
+    return f
 
 
 def dtype_code(name, t) -> int:
@@ -20,40 +34,37 @@ def dtype_code(name, t) -> int:
     return code
 
 
-def ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def check(name, t, dtype, shape) -> None:
-    """A contiguous CUDA tensor of this type and shape."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+def tensor(name, t, dtype, shape):
+    """Data pointer of a contiguous CUDA tensor of this type and shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
         kda._check_tensor(name, t, dtype, shape)
+    return t.data_ptr()
 
 
-def rows(name, t, dtype, shape, lead: int) -> int:
+def optional(name, t, dtype, shape):
+    return None if t is None else tensor(name, t, dtype, shape)
+
+
+def rows(name, t, dtype, shape, lead: int, width: int) -> int:
     """Row stride (elements) of a CUDA tensor whose first ``lead`` dimensions index packed
-    rows and whose others are one row's contiguous elements.  A slice of a wider tensor
-    qualifies; rows that are not evenly spaced do not."""
+    rows and whose others are one row's ``width`` contiguous elements.  A slice of a wider
+    tensor qualifies; rows that are not evenly spaced do not."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    size = t.shape
+    if size != shape:
+        raise ValueError(f"{name} has shape {tuple(size)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    width = 1
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
     if t.is_contiguous() or t.numel() == 0:
-        for n in shape[lead:]:
-            width *= n
         return width
-    size, step = t.shape, t.stride()
+    step, inner = t.stride(), 1
     for d in range(len(size) - 1, lead - 1, -1):
-        if size[d] != 1 and step[d] != width:
+        if size[d] != 1 and step[d] != inner:
             raise ValueError(f"{name}: the elements of a row must be contiguous")
-        width *= size[d]
+        inner *= size[d]
     stride, span = None, 0
     for d in range(lead - 1, -1, -1):
         if size[d] == 1:
@@ -68,18 +79,31 @@ def rows(name, t, dtype, shape, lead: int) -> int:
     return width if stride is None else stride
 
 
-def sequences(cu_seqlens) -> int:
-    """Number of sequences of cu_seqlens (0 for None)."""
+def states(initial_state, final_state, shape):
+    """State dtype code and the data pointers of the states (None where absent)."""
+    first = initial_state if initial_state is not None else final_state
+    if first is None:
+        return kda.KDA_STATE_NONE, None, None
+    code = kda.state_dtype_code(initial_state, final_state) if final_state is not initial_state else STATES.get(first.dtype)
+    if code is None:
+        raise ValueError(f"state dtype must be bf16 or fp32, got {first.dtype}")
+    return code, optional("initial_state", initial_state, first.dtype, shape), \
+        optional("final_state", final_state, first.dtype, shape)
+
+
+def sequences(cu_seqlens):
+    """Number of sequences of cu_seqlens and its data pointer (0 and None for None)."""
     if cu_seqlens is None:
-        return 0
+        return 0, None
     kda._check_tensor("cu_seqlens", cu_seqlens, torch.int64)
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must be 1-D with at least 2 entries")
-    return cu_seqlens.numel() - 1
+    return cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
 
 
-def stream_handle(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def stream_handle(stream, t) -> int:
+    """Handle of ``stream``, or of the current stream of the tensor's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def on(stream):
@@ -88,5 +112,5 @@ def on(stream):
 
 
 def done(status: int) -> None:
-    if status != kda.KDA_OK:
+    if status:
         raise kda.KDAError(status, kda.status_string(status))

@@ -26,8 +26,14 @@ constexpr int kLanes = 32, kGroups = 8, kThreads = kLanes * kGroups;
 // packed ones as one row range.
 struct Runs { int64_t count, per_seq; int length; };
 
-// The run of this thread: rows [r0, r1), the first one's sequence n and its rows [lo, hi).
-struct Run { int64_t r0, r1, n, lo, hi; };
+// Rows [r0, r1) of a thread's run, and the part [s0, s1) of them that lies in sequence n,
+// whose rows are [lo, hi).
+struct Run { int64_t r0, r1, s0, s1, n, lo, hi; };
+__device__ __forceinline__ void part_of_run(const ConvParams &p, Run &r) {
+    r.lo = min(r.lo, r.s0);   // no row of the run lies outside, whatever cu_seqlens holds
+    if (r.hi <= r.s0) r.hi = p.rows;
+    r.s1 = min(r.r1, r.hi);
+}
 __device__ __forceinline__ Run run_of(const ConvParams &p, const Runs &runs, int64_t q) {
     Run r;
     if (p.cu_seqlens) {
@@ -35,8 +41,6 @@ __device__ __forceinline__ Run run_of(const ConvParams &p, const Runs &runs, int
         r.r1 = min(r.r0 + runs.length, p.rows);
         r.n = seq_of_row(p.cu_seqlens, p.N, r.r0);
         seq_rows(p, r.n, r.lo, r.hi);
-        r.lo = min(r.lo, r.r0);   // no row of the run lies outside, whatever cu_seqlens holds
-        if (r.hi <= r.r0) r.hi = p.rows;
     } else {
         r.n = runs.per_seq == 1 ? q : q / runs.per_seq;
         r.lo = r.n * p.T;
@@ -44,13 +48,17 @@ __device__ __forceinline__ Run run_of(const ConvParams &p, const Runs &runs, int
         r.r0 = r.lo + (q - r.n * runs.per_seq) * runs.length;
         r.r1 = min(r.r0 + runs.length, r.hi);
     }
+    r.s0 = r.r0;
+    part_of_run(p, r);
     return r;
 }
-// The sequence of row t = r.hi or later.
-__device__ __forceinline__ void next_sequence(const ConvParams &p, Run &r, int64_t t) {
-    while (r.n + 1 < p.N && r.hi <= t) seq_rows(p, ++r.n, r.lo, r.hi);
-    if (r.hi <= t) r.hi = p.rows;   // rows that no sequence claims
-    r.lo = t;
+// The part of the run in the next sequence that has rows; false at the run's end.
+__device__ __forceinline__ bool next_part(const ConvParams &p, Run &r) {
+    if (r.s1 >= r.r1) return false;
+    r.s0 = r.s1;
+    while (r.n + 1 < p.N && r.hi <= r.s0) seq_rows(p, ++r.n, r.lo, r.hi);
+    part_of_run(p, r);
+    return true;
 }
 
 // V channels' weights, w[j][v].
@@ -87,15 +95,27 @@ __device__ __forceinline__ void ld_x(const ConvParams &p, int64_t n, int64_t lo,
     }
 }
 
-// One step of the window: x_{t-(W-1)} .. x_t in xw; y_t.
+// acc += a * b, V channels.
+template <int V>
+__device__ __forceinline__ void fma_all(float (&acc)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            const float2 t = sm103::fma2(make_float2(a[v], a[v + 1]), make_float2(b[v], b[v + 1]), make_float2(acc[v], acc[v + 1]));
+            acc[v] = t.x, acc[v + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(a[v], b[v], acc[v]);
+    }
+}
+// y_t of the window x_{t-(W-1)} .. x_t.
 template <int V, int W>
 __device__ __forceinline__ void taps_sum(const float (&w)[W][V], const float (&b)[V], const float (&xw)[W][V], float (&y)[V]) {
 #pragma unroll
     for (int v = 0; v < V; ++v) y[v] = b[v];
 #pragma unroll
-    for (int j = 0; j < W; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) y[v] = fmaf(w[j][v], xw[j][v], y[v]);
+    for (int j = 0; j < W; ++j) fma_all<V>(y, w[j], xw[j]);
 }
 template <int V, int W>
 __device__ __forceinline__ void shift(float (&xw)[W][V]) {
@@ -106,7 +126,7 @@ __device__ __forceinline__ void shift(float (&xw)[W][V]) {
 }
 
 template <typename E, int V, int W>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvParams p, Runs runs, int channel_blocks) {
+__global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 4) conv_fwd_kernel(ConvParams p, Runs runs, int channel_blocks) {
     const int64_t q = (int64_t)(blockIdx.x / channel_blocks) * kGroups + threadIdx.x / kLanes;
     const int64_t c = ((int64_t)(blockIdx.x % channel_blocks) * kLanes + threadIdx.x % kLanes) * V;
     if (q >= runs.count || c >= p.D) return;
@@ -115,47 +135,40 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvParams p, Runs r
     ld_taps<V, W>(p.weight, c, w);
 #pragma unroll
     for (int v = 0; v < V; ++v) b[v] = p.bias ? p.bias[c + v] : 0.f;
+    do {
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) ld_x<E, V>(p, r.n, r.lo, r.r0 - (W - 1) + j, c, xw[j]);
-    // the final state is the first run's to write: it alone reads the initial state
-    const bool state = p.fin && !p.cu_seqlens && r.r0 == r.lo;
-    float last[W - 1][V];
-    if (state) {
+        for (int j = 0; j < W - 1; ++j) ld_x<E, V>(p, r.n, r.lo, r.s0 - (W - 1) + j, c, xw[j]);
+        // the final state is the first run's to write: it alone reads the initial state
+        if (p.fin && !p.cu_seqlens && r.s0 == r.lo) {
+            float last[W - 1][V];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) ld_x<E, V>(p, r.n, r.lo, r.hi - (W - 1) + j, c, last[j]);
-    }
-    const E *x = static_cast<const E *>(p.x) + r.r0 * p.xs + c;
-    E *out = static_cast<E *>(p.out) + r.r0 * p.os + c;
-    constexpr int kBatch = 8;   // rows on their way together
-    for (int64_t t0 = r.r0; t0 < r.r1; t0 += kBatch) {
-        Pack<E, V> raw[kBatch];
+            for (int j = 0; j < W - 1; ++j) ld_x<E, V>(p, r.n, r.lo, r.hi - (W - 1) + j, c, last[j]);
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k, x += p.xs)
-            if (t0 + k < r.r1) raw[k] = ld_pack<E, V>(x);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k, out += p.os) {
-            const int64_t t = t0 + k;
-            if (t >= r.r1) break;
-            if (t == r.hi) {
-                next_sequence(p, r, t);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) ld_x<E, V>(p, r.n, r.lo, t - (W - 1) + j, c, xw[j]);
-            }
-            unpack<E, V>(raw[k], xw[W - 1]);
-            float y[V];
-            taps_sum<V, W>(w, b, xw, y);
-            if (p.silu) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) y[v] *= sigmoid(y[v]);
-            }
-            st_f<E, V>(out, y);
-            shift<V, W>(xw);
+            for (int j = 0; j < W - 1; ++j) st_f<E, V>(static_cast<E *>(p.fin) + (r.n * (W - 1) + j) * p.D + c, last[j]);
         }
-    }
-    if (state) {
+        const E *x = static_cast<const E *>(p.x) + r.s0 * p.xs + c;
+        E *out = static_cast<E *>(p.out) + r.s0 * p.os + c;
+        constexpr int kBatch = 8;   // rows on their way together
+        for (int left = (int)(r.s1 - r.s0); left > 0; left -= kBatch) {
+            Pack<E, V> raw[kBatch];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) st_f<E, V>(static_cast<E *>(p.fin) + (r.n * (W - 1) + j) * p.D + c, last[j]);
-    }
+            for (int k = 0; k < kBatch; ++k, x += p.xs)
+                if (k < left) raw[k] = ld_pack<E, V>(x);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k, out += p.os) {
+                if (k >= left) break;
+                unpack<E, V>(raw[k], xw[W - 1]);
+                float y[V];
+                taps_sum<V, W>(w, b, xw, y);
+                if (p.silu) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) y[v] *= sigmoid(y[v]);
+                }
+                st_f<E, V>(out, y);
+                shift<V, W>(xw);
+            }
+        }
+    } while (next_part(p, r));
 }
 
 // Final states of packed sequences (and of sequences without tokens): one thread per
@@ -176,10 +189,18 @@ __global__ void __launch_bounds__(kThreads) conv_state_kernel(ConvParams p) {
     }
 }
 
+constexpr int kBatch = 4, kStages = 3;   // rows per copy group, groups of the ring
+
+// With t = u - (W-1), row u's q completes d_t = sum_k w[W-1-k] q_{t+k}: the gradient of
+// input row t, or of a row of the initial state where t comes before the sequence.  So a
+// part [s0, s1) of a run walks u from s0 to s1 + W-2; rows from s1 on add to no parameter,
+// and rows after the sequence have a q of 0 but the final state's gradient.
 template <typename E, int V, int W>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvParams p, Runs runs, int channel_blocks, float *part) {
-    __shared__ float sums[kGroups][W + 1][kLanes * V];
-    const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+__global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 3) conv_bwd_kernel(ConvParams p, Runs runs, int channel_blocks, float *part) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    auto &ring = *reinterpret_cast<Pack<E, V>(*)[kStages][2][kBatch][kThreads]>(smem);   // x, dout
+    auto &sums = *reinterpret_cast<float (*)[kGroups][W + 1][kLanes * V]>(smem);         // after the walk
+    const int tid = threadIdx.x, lane = tid % kLanes, group = tid / kLanes;
     const int64_t block = blockIdx.x / channel_blocks, q = block * kGroups + group;
     const int64_t c0 = (int64_t)(blockIdx.x % channel_blocks) * kLanes * V, c = c0 + lane * V;
     float dw[W][V], db[V];
@@ -191,110 +212,80 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvParams p, Runs r
     }
     if (q < runs.count && c < p.D) {
         Run r = run_of(p, runs, q);
-        float w[W][V], b[V], xw[W][V], qs[W][V];   // qs[k]: q of the row k after the current one
+        float w[W][V], b[V];
         ld_taps<V, W>(p.weight, c, w);
 #pragma unroll
         for (int v = 0; v < V; ++v) b[v] = p.bias ? p.bias[c + v] : 0.f;
-
-        // q of row u, whose input and upstream gradient are given; the window moves on
-        const auto form_q = [&](int64_t u, const float (&x)[V], const float (&dy)[V], float (&out)[V]) {
-            float y[V];
+        do {
+            const int own = (int)(r.s1 - r.s0), real = own + (int)min((int64_t)(W - 1), r.hi - r.s1), all = own + W - 1;
+            const bool first = r.s0 == r.lo;
+            const auto fetch = [&](int j0, int stage) {
+                const E *x = static_cast<const E *>(p.x) + (r.s0 + j0) * p.xs + c, *dy = static_cast<const E *>(p.dout) + (r.s0 + j0) * p.ds + c;
+                copy_rows<E, V, kBatch, kThreads>(&ring[stage][0][0][tid], x, p.xs, real - j0);
+                copy_rows<E, V, kBatch, kThreads>(&ring[stage][1][0][tid], dy, p.ds, real - j0);
+                copies_commit();
+            };
+            float xw[W][V], qs[W][V];   // inputs u-(W-1) .. u and their q
 #pragma unroll
-            for (int v = 0; v < V; ++v) xw[W - 1][v] = x[v];
-            taps_sum<V, W>(w, b, xw, y);
+            for (int k = 0; k < kStages - 1; ++k) fetch(k * kBatch, k);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                out[v] = dy[v];
-                if (p.silu) {
-                    // silu' = s + y s (1 - s) = s (1 + y (1 - s)); 1 - s as sigma(-y)
-                    const float t = ex2(-kLog2e * fabsf(y[v])), rt = rcp(1.f + t), m = t * rt;
-                    const float s = y[v] >= 0.f ? rt : m, o = y[v] >= 0.f ? m : rt;
-                    out[v] *= s * fmaf(y[v], o, 1.f);
-                }
+            for (int j = 0; j < W - 1; ++j) {
+                ld_x<E, V>(p, r.n, r.lo, r.s0 - (W - 1) + j, c, xw[j]);
+#pragma unroll
+                for (int v = 0; v < V; ++v) qs[j][v] = 0.f;
             }
-            if (u < r.r1) {   // rows after the run are another thread's to sum
+            E *dx = static_cast<E *>(p.dx) + (r.s0 - (W - 1)) * p.D + c;
+            int stage = 0;
+            for (int j0 = 0; j0 < all; j0 += kBatch) {
+                fetch(j0 + (kStages - 1) * kBatch, stage == 0 ? kStages - 1 : stage - 1);
+                copies_wait<kStages - 1>();   // this thread's own copies: no barrier needed
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    db[v] += out[v];
+                for (int k = 0; k < kBatch; ++k, dx += p.D) {
+                    const int j = j0 + k;
+                    if (j >= all) break;
+                    float (&qn)[V] = qs[W - 1];
+                    if (j < real) {
+                        unpack<E, V>(ring[stage][0][k][tid], xw[W - 1]);
+                        unpack<E, V>(ring[stage][1][k][tid], qn);
+                        if (p.silu) {
+                            float y[V];
+                            taps_sum<V, W>(w, b, xw, y);
 #pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j][v] = fmaf(out[v], xw[j][v], dw[j][v]);
+                            for (int v = 0; v < V; ++v) {   // silu' = s (1 + y (1 - s))
+                                const float s = sigmoid(y[v]);
+                                qn[v] *= s * fmaf(y[v], 1.f - s, 1.f);
+                            }
+                        }
+                        if (j < own) {
+#pragma unroll
+                            for (int v = 0; v < V; ++v) db[v] += qn[v];
+#pragma unroll
+                            for (int i = 0; i < W; ++i) fma_all<V>(dw[i], qn, xw[i]);
+                        }
+                        shift<V, W>(xw);
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) qn[v] = 0.f;
+                    }
+                    float d[V];
+#pragma unroll
+                    for (int v = 0; v < V; ++v) d[v] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < W; ++i) fma_all<V>(d, w[W - 1 - i], qs[i]);
+                    if (p.dfinal && r.s0 + j >= r.hi) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) d[v] += p.dfinal[(r.n * (W - 1) + (r.s0 + j - r.hi)) * p.D + c + v];
+                    }
+                    if (j >= W - 1) st_f<E, V>(dx, d);
+                    else if (first && p.dinit) st_f<float, V>(p.dinit + (r.n * (W - 1) + j) * p.D + c, d);
+                    shift<V, W>(qs);
                 }
+                stage = stage + 1 == kStages ? 0 : stage + 1;
             }
-            shift<V, W>(xw);
-        };
-        // window and q at row t; where t begins its sequence, the initial state's gradient
-        const auto start = [&](int64_t t) {
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) ld_x<E, V>(p, r.n, r.lo, t - (W - 1) + j, c, xw[j]);
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) qs[k][v] = 0.f;
-                if (t + k < r.hi) {
-                    float x[V], dy[V];
-                    ld_f<E, V>(static_cast<const E *>(p.x) + (t + k) * p.xs + c, x);
-                    ld_f<E, V>(static_cast<const E *>(p.dout) + (t + k) * p.ds + c, dy);
-                    form_q(t + k, x, dy, qs[k]);
-                }
-            }
-            if (t != r.lo || !p.dinit) return;
-#pragma unroll
-            for (int m = 0; m < W - 1; ++m) {   // state row m is input row lo - (W-1) + m
-                const int64_t j = m - (r.hi - r.lo);
-                float d[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    d[v] = p.dfinal && j >= 0 ? p.dfinal[(r.n * (W - 1) + j) * p.D + c + v] : 0.f;
-#pragma unroll
-                    for (int i = 0; i <= m; ++i) d[v] = fmaf(w[i][v], qs[m - i][v], d[v]);
-                }
-                st_f<float, V>(p.dinit + (r.n * (W - 1) + m) * p.D + c, d);
-            }
-        };
-        start(r.r0);
-        const E *x = static_cast<const E *>(p.x) + (r.r0 + W - 1) * p.xs + c;
-        const E *dy = static_cast<const E *>(p.dout) + (r.r0 + W - 1) * p.ds + c;
-        E *dx = static_cast<E *>(p.dx) + r.r0 * p.D + c;
-        constexpr int kBatch = 4;   // rows on their way together
-        for (int64_t t0 = r.r0; t0 < r.r1; t0 += kBatch) {
-            Pack<E, V> rx[kBatch], rd[kBatch];   // rows W-1 ahead
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k, x += p.xs, dy += p.ds) {
-                const int64_t u = t0 + k + W - 1;
-                if (t0 + k < r.r1 && u < p.rows) rx[k] = ld_pack<E, V>(x), rd[k] = ld_pack<E, V>(dy);
-            }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k, dx += p.D) {
-                const int64_t t = t0 + k, u = t + W - 1;
-                if (t >= r.r1) break;
-                if (t == r.hi) {
-                    next_sequence(p, r, t);
-                    start(t);
-                }
-#pragma unroll
-                for (int v = 0; v < V; ++v) qs[W - 1][v] = 0.f;
-                if (u < r.hi) {
-                    float xf[V], df[V];
-                    unpack<E, V>(rx[k], xf);
-                    unpack<E, V>(rd[k], df);
-                    form_q(u, xf, df, qs[W - 1]);
-                }
-                float d[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    d[v] = 0.f;
-#pragma unroll
-                    for (int i = 0; i < W; ++i) d[v] = fmaf(w[W - 1 - i][v], qs[i][v], d[v]);
-                }
-                if (p.dfinal && u >= r.hi) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) d[v] += p.dfinal[(r.n * (W - 1) + u - r.hi) * p.D + c + v];
-                }
-                st_f<E, V>(dx, d);
-                shift<V, W>(qs);
-            }
-        }
+        } while (next_part(p, r));
     }
+    copies_wait<0>();
+    __syncthreads();
     // over the CTA's runs, in order
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -396,8 +387,15 @@ cudaError_t launch_conv_bwd(const ConvParams &p, unsigned char *ws, int sms, cud
     const cudaError_t e = with_shape(p, [&](auto *tag, auto V, auto W) {
         using E = std::remove_pointer_t<decltype(tag)>;
         const int64_t blocks = ceil_div(p.D, kLanes * V);
-        if (p.rows > 0)
-            conv_bwd_kernel<E, V, W><<<(unsigned)(run_blocks(runs) * blocks), kThreads, 0, stream>>>(p, runs, (int)blocks, part);
+        if (p.rows == 0) return cudaSuccess;
+        constexpr auto kernel = conv_bwd_kernel<E, V, W>;
+        constexpr int smem = (int)std::max(sizeof(Pack<E, V>) * kStages * 2 * kBatch * kThreads, sizeof(float) * kGroups * (W + 1) * kLanes * V);
+        static std::atomic<bool> done[kMaxDevices];
+        const cudaError_t e = once_per_device(done, [&](int) {
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        });
+        if (e != cudaSuccess) return e;
+        kernel<<<(unsigned)(run_blocks(runs) * blocks), kThreads, smem, stream>>>(p, runs, (int)blocks, part);
         return cudaGetLastError();
     });
     if (e != cudaSuccess) return e;

@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import torch
 
-from . import _args, kda
+from . import _args
 
 # Packed rows from one checkpoint to the next (KDA_GLR_CHECKPOINT_ROWS).
 CHECKPOINT_ROWS = 64
@@ -24,15 +24,17 @@ def checkpoint_shape(B: int, T: int, H: int, K: int) -> tuple:
     return (-(-B * T // CHECKPOINT_ROWS), H, K)
 
 
-def _check(x, i, g, A_log, dt_bias, cu_seqlens):
+def _check(x, i, g, A_log, dt_bias):
     dt = _args.dtype_code("x", x)
     if x.dim() != 4:
         raise ValueError("x must be [B, T, H, K]")
-    B, T, H, K = shape = x.shape
-    strides = [_args.rows(n, t, x.dtype, shape, 2) for n, t in (("x", x), ("i", i), ("g", g))]
-    _args.check("A_log", A_log, torch.float32, (H,))
-    _args.check("dt_bias", dt_bias, torch.float32, (H, K))
-    return dt, shape, strides, _args.sequences(cu_seqlens)
+    shape = x.shape
+    B, T, H, K = shape
+    D, dtype, rows = H * K, x.dtype, _args.rows
+    f32 = torch.float32
+    return (dt, shape, D, rows("x", x, dtype, shape, 2, D), rows("i", i, dtype, shape, 2, D),
+            rows("g", g, dtype, shape, 2, D), _args.tensor("A_log", A_log, f32, (H,)),
+            _args.tensor("dt_bias", dt_bias, f32, (H, K)))
 
 
 def glr_fwd(x, i, g, out, A_log, dt_bias, lower_bound, initial_state=None, final_state=None,
@@ -41,20 +43,15 @@ def glr_fwd(x, i, g, out, A_log, dt_bias, lower_bound, initial_state=None, final
     ``initial_state`` itself) in place, asynchronously on ``stream`` (default: the current
     torch stream).  ``checkpoints`` (fp32, ``checkpoint_shape``) takes the states that
     ``glr_bwd`` starts from."""
-    dt, (B, T, H, K), strides, num_seqs = _check(x, i, g, A_log, dt_bias, cu_seqlens)
-    out_stride = _args.rows("out", out, x.dtype, x.shape, 2)
-    N = num_seqs or B
-    code = kda.state_dtype_code(initial_state, final_state)
-    for name, s in (("initial_state", initial_state), ("final_state", final_state)):
-        if s is not None:
-            _args.check(name, s, s.dtype, (N, H, K))
-    if checkpoints is not None:
-        _args.check("checkpoints", checkpoints, torch.float32, checkpoint_shape(B, T, H, K))
-    p = _args.ptr
-    _args.done(kda.lib().kda_glr_fwd(
-        p(x), p(i), p(g), *strides, p(out), out_stride, dt, p(A_log), p(dt_bias), lower_bound or 0.0,
-        lower_bound is None, p(initial_state), p(final_state), code, p(cu_seqlens), num_seqs, B, T, H, K,
-        p(checkpoints), _args.stream_handle(stream)))
+    dt, shape, D, xs, is_, gs, pA, pt = _check(x, i, g, A_log, dt_bias)
+    B, T, H, K = shape
+    out_stride = _args.rows("out", out, x.dtype, shape, 2, D)
+    num_seqs, cu = _args.sequences(cu_seqlens)
+    code, init, fin = _args.states(initial_state, final_state, (num_seqs or B, H, K))
+    ck = None if checkpoints is None else _args.tensor("checkpoints", checkpoints, torch.float32, checkpoint_shape(B, T, H, K))
+    _args.done(_args.entry("kda_glr_fwd")(
+        x.data_ptr(), i.data_ptr(), g.data_ptr(), xs, is_, gs, out.data_ptr(), out_stride, dt, pA, pt, lower_bound or 0.0,
+        lower_bound is None, init, fin, code, cu, num_seqs, B, T, H, K, ck, _args.stream_handle(stream, x)))
 
 
 def glr_bwd(x, i, g, A_log, dt_bias, lower_bound, dout, initial_state=None, dfinal=None,
@@ -63,26 +60,23 @@ def glr_bwd(x, i, g, A_log, dt_bias, lower_bound, dout, initial_state=None, dfin
     ``dfinal`` fp32 [N,H,K] or None; ``checkpoints`` as ``glr_fwd`` left them for these
     inputs, or None (the states are recomputed).  Returns a dict of new tensors: dx, di, dg
     in the inputs' type, and fp32 dA_log, ddt_bias and dinit (None unless ``want_dinit``)."""
-    dt, (B, T, H, K), strides, num_seqs = _check(x, i, g, A_log, dt_bias, cu_seqlens)
-    dout_stride = _args.rows("dout", dout, x.dtype, x.shape, 2)
-    N = num_seqs or B
-    code = kda.state_dtype_code(initial_state, None)
-    if initial_state is not None:
-        _args.check("initial_state", initial_state, initial_state.dtype, (N, H, K))
-    if dfinal is not None:
-        _args.check("dfinal", dfinal, torch.float32, (N, H, K))
-    if checkpoints is not None:
-        _args.check("checkpoints", checkpoints, torch.float32, checkpoint_shape(B, T, H, K))
+    dt, shape, D, xs, is_, gs, pA, pt = _check(x, i, g, A_log, dt_bias)
+    B, T, H, K = shape
+    ds = _args.rows("dout", dout, x.dtype, shape, 2, D)
+    num_seqs, cu = _args.sequences(cu_seqlens)
+    state, f32 = (num_seqs or B, H, K), torch.float32
+    code, init, _ = _args.states(initial_state, None, state)
+    dfin = _args.optional("dfinal", dfinal, f32, state)
+    ck = None if checkpoints is None else _args.tensor("checkpoints", checkpoints, f32, checkpoint_shape(B, T, H, K))
     with _args.on(stream):
         dev = x.device
-        r = {k: torch.empty((B, T, H, K), dtype=x.dtype, device=dev) for k in ("dx", "di", "dg")}
-        r["dA_log"] = torch.empty((H,), dtype=torch.float32, device=dev)
-        r["ddt_bias"] = torch.empty((H, K), dtype=torch.float32, device=dev)
-        r["dinit"] = torch.empty((N, H, K), dtype=torch.float32, device=dev) if want_dinit else None
-    p = _args.ptr
-    _args.done(kda.lib().kda_glr_bwd(
-        p(x), p(i), p(g), *strides, dt, p(A_log), p(dt_bias), lower_bound or 0.0, lower_bound is None,
-        p(initial_state), code, p(checkpoints), p(dout), dout_stride, p(dfinal), p(cu_seqlens), num_seqs,
-        B, T, H, K, p(r["dx"]), p(r["di"]), p(r["dg"]), p(r["dA_log"]), p(r["ddt_bias"]), p(r["dinit"]),
-        _args.stream_handle(stream)))
-    return r
+        dx, di, dg = (torch.empty(shape, dtype=x.dtype, device=dev) for _ in range(3))
+        dA_log = torch.empty((H,), dtype=f32, device=dev)
+        ddt_bias = torch.empty((H, K), dtype=f32, device=dev)
+        dinit = torch.empty(state, dtype=f32, device=dev) if want_dinit else None
+    _args.done(_args.entry("kda_glr_bwd")(
+        x.data_ptr(), i.data_ptr(), g.data_ptr(), xs, is_, gs, dt, pA, pt, lower_bound or 0.0, lower_bound is None, init,
+        code, ck, dout.data_ptr(), ds, dfin, cu, num_seqs, B, T, H, K, dx.data_ptr(), di.data_ptr(), dg.data_ptr(),
+        dA_log.data_ptr(), ddt_bias.data_ptr(), None if dinit is None else dinit.data_ptr(),
+        _args.stream_handle(stream, x)))
+    return {"dx": dx, "di": di, "dg": dg, "dA_log": dA_log, "ddt_bias": ddt_bias, "dinit": dinit}

@@ -11,26 +11,24 @@ from __future__ import annotations
 
 import torch
 
-from . import _args, kda
+from . import _args
 
 ACTIVATIONS = {None: 0, "silu": 1}   # kda_activation
 
 
-def _check(x, weight, bias, activation, cu_seqlens):
-    dt = _args.dtype_code("x", x)
-    if x.dim() != 3:
+def _check(x, weight, bias, activation):
+    dt, shape = _args.dtype_code("x", x), x.shape
+    if len(shape) != 3:
         raise ValueError("x must be [B, T, D]")
-    B, T, D = x.shape
+    D, f32 = shape[2], torch.float32
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a [D, W] tensor")
     W = weight.shape[1]
-    _args.check("weight", weight, torch.float32, (D, W))
-    if bias is not None:
-        _args.check("bias", bias, torch.float32, (D,))
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be None or 'silu', got {activation!r}")
-    return dt, (B, T, D, W), _args.rows("x", x, x.dtype, x.shape, 2), ACTIVATIONS[activation], \
-        _args.sequences(cu_seqlens)
+    return (dt, shape, W, _args.rows("x", x, x.dtype, shape, 2, D), act, _args.tensor("weight", weight, f32, (D, W)),
+            _args.optional("bias", bias, f32, (D,)))
 
 
 def short_conv_fwd(x, weight, bias, out, activation="silu", initial_state=None, final_state=None,
@@ -38,15 +36,16 @@ def short_conv_fwd(x, weight, bias, out, activation="silu", initial_state=None, 
     """Writes ``out`` (like ``x``) and, where given, ``final_state`` [N, W-1, D] (which may
     be ``initial_state`` itself) in place, asynchronously on ``stream`` (default: the
     current torch stream)."""
-    dt, (B, T, D, W), stride, act, num_seqs = _check(x, weight, bias, activation, cu_seqlens)
-    out_stride = _args.rows("out", out, x.dtype, x.shape, 2)
-    for name, s in (("initial_state", initial_state), ("final_state", final_state)):
-        if s is not None:
-            _args.check(name, s, x.dtype, (num_seqs or B, W - 1, D))
-    p = _args.ptr
-    _args.done(kda.lib().kda_short_conv_fwd(p(x), stride, p(weight), p(bias), act, p(out), out_stride, dt,
-                                            p(initial_state), p(final_state), p(cu_seqlens), num_seqs, B, T, D, W,
-                                            _args.stream_handle(stream)))
+    dt, shape, W, stride, act, pw, pb = _check(x, weight, bias, activation)
+    B, T, D = shape
+    out_stride = _args.rows("out", out, x.dtype, shape, 2, D)
+    num_seqs, cu = _args.sequences(cu_seqlens)
+    state = (num_seqs or B, W - 1, D)
+    _args.done(_args.entry("kda_short_conv_fwd")(
+        x.data_ptr(), stride, pw, pb, act, out.data_ptr(), out_stride, dt,
+        _args.optional("initial_state", initial_state, x.dtype, state),
+        _args.optional("final_state", final_state, x.dtype, state), cu, num_seqs, B, T, D, W,
+        _args.stream_handle(stream, x)))
 
 
 def short_conv_bwd(x, weight, bias, dout, activation="silu", initial_state=None, dfinal=None,
@@ -54,22 +53,21 @@ def short_conv_bwd(x, weight, bias, dout, activation="silu", initial_state=None,
     """Gradients of L = sum(dout * out) + sum(dfinal * final_state); ``dfinal`` fp32
     [N, W-1, D] or None.  Returns a dict of new tensors: dx (x's type, contiguous), and fp32
     dweight, dbias (None without a bias) and dinit (None unless ``want_dinit``)."""
-    dt, (B, T, D, W), stride, act, num_seqs = _check(x, weight, bias, activation, cu_seqlens)
-    dout_stride = _args.rows("dout", dout, x.dtype, x.shape, 2)
-    N = num_seqs or B
-    if initial_state is not None:
-        _args.check("initial_state", initial_state, x.dtype, (N, W - 1, D))
-    if dfinal is not None:
-        _args.check("dfinal", dfinal, torch.float32, (N, W - 1, D))
+    dt, shape, W, stride, act, pw, pb = _check(x, weight, bias, activation)
+    B, T, D = shape
+    dout_stride = _args.rows("dout", dout, x.dtype, shape, 2, D)
+    num_seqs, cu = _args.sequences(cu_seqlens)
+    state, f32 = (num_seqs or B, W - 1, D), torch.float32
+    init = _args.optional("initial_state", initial_state, x.dtype, state)
+    dfin = _args.optional("dfinal", dfinal, f32, state)
     with _args.on(stream):
         dev = x.device
-        r = {"dx": torch.empty((B, T, D), dtype=x.dtype, device=dev),
-             "dweight": torch.empty((D, W), dtype=torch.float32, device=dev),
-             "dbias": None if bias is None else torch.empty((D,), dtype=torch.float32, device=dev),
-             "dinit": torch.empty((N, W - 1, D), dtype=torch.float32, device=dev) if want_dinit else None}
-    p = _args.ptr
-    _args.done(kda.lib().kda_short_conv_bwd(p(x), stride, p(weight), p(bias), act, dt, p(initial_state), p(dout),
-                                            dout_stride, p(dfinal), p(cu_seqlens), num_seqs, B, T, D, W, p(r["dx"]),
-                                            p(r["dweight"]), p(r["dbias"]), p(r["dinit"]),
-                                            _args.stream_handle(stream)))
-    return r
+        dx = torch.empty(shape, dtype=x.dtype, device=dev)
+        dw = torch.empty((D, W), dtype=f32, device=dev)
+        db = None if bias is None else torch.empty((D,), dtype=f32, device=dev)
+        dinit = torch.empty(state, dtype=f32, device=dev) if want_dinit else None
+    _args.done(_args.entry("kda_short_conv_bwd")(
+        x.data_ptr(), stride, pw, pb, act, dt, init, dout.data_ptr(), dout_stride, dfin, cu, num_seqs, B, T, D, W,
+        dx.data_ptr(), dw.data_ptr(), None if db is None else db.data_ptr(), None if dinit is None else dinit.data_ptr(),
+        _args.stream_handle(stream, x)))
+    return {"dx": dx, "dweight": dw, "dbias": db, "dinit": dinit}

@@ -2,6 +2,7 @@
 at least one invalid argument (or has no work), so nothing touches a device; and the 64-bit
 references' gradients against differentiation of their formulas."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -155,7 +156,7 @@ class _SaysGpu(torch.Tensor):                                      # a CPU tenso
 def test_row_strides():
     def stride(t, lead):
         f = t.as_subclass(_SaysGpu)
-        return _args.rows("t", f, t.dtype, t.shape, lead)
+        return _args.rows("t", f, t.dtype, t.shape, lead, math.prod(t.shape[lead:]))
 
     t = torch.zeros(3, 5, 4, 8)
     assert stride(t, 2) == 32
