@@ -27,11 +27,11 @@ __global__ void __launch_bounds__(128) glr_fwd_step_kernel(GlrParams p) {
     const E *g = static_cast<const E *>(p.g) + n * p.T * p.gs + c;
     E *out = static_cast<E *>(p.out) + n * p.T * p.os + c;
     const float lb2 = p.lower_bound * kLog2e;
-    GateConst gc[V];
-    float h[V];
+    float k0[V], k1[V], h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        gc[v] = gate_const<UB>(p.A_log[(unsigned)(c + v) / (unsigned)p.K], p.dt_bias[c + v]);
+        const GateConst gc = gate_const<UB>(p.A_log[(unsigned)(c + v) / (unsigned)p.K], p.dt_bias[c + v]);
+        k0[v] = gc.k0, k1[v] = gc.k1;
         h[v] = p.init ? ld_state(p.init, p.state_type, n * p.D + c + v) : 0.f;
     }
     for (int64_t t = 0; t < p.T; ++t) {
@@ -44,8 +44,11 @@ __global__ void __launch_bounds__(128) glr_fwd_step_kernel(GlrParams p) {
 #pragma unroll
             for (int v = 0; v < V; ++v) p.checkpoints[row / kGlrCheckpointRows * p.D + c + v] = h[v];
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = fmaf(gate_decay<UB>(gf[v], gc[v], lb2), h[v], sigmoid(jf[v]) * xf[v]);
+        float a[V], b[V];
+        gate_decay_n<UB, V>(a, gf, k0, k1, lb2);
+        sigmoid_n<V>(b, jf);
+        mul_n<V>(b, b, xf);
+        fma_n<V>(h, a, h, b);
         if (p.out) st_f<E, V>(out + t * p.os, h);
     }
     if (p.fin) {
@@ -109,18 +112,21 @@ __global__ void __launch_bounds__(FwdShape<V>::THREADS, kFwdCtas) glr_fwd_scan_k
         const bool marked = mark_tile(p, rt, first, sh.marks);
         copies_wait<0>();   // this thread's own copies: no barrier needed
 
-        // decays and inputs, two at a time: neighbouring channels, or rows where V is 1
         float a[L * V], b[L * V];
         const int left = c < p.D ? (int)min(p.rows - r0, (int64_t)L) : 0;   // rows of this thread that exist
-        const Pack<GateConst, V> gc = sh.gates[tid];
+        constexpr int n = kGateWidth<V>;
+        const ChunkGates<V> gc(sh.gates[tid]);
 #pragma unroll
-        for (int e = 0; e < L * V; e += 2) {
-            const auto at2 = [&](int k) {
-                return make_float2(to_f(sh.raw[k][e / V][tid].e[e % V]), to_f(sh.raw[k][(e + 1) / V][tid].e[(e + 1) % V]));
-            };
-            const float2 a2 = gate_decay2<UB>(at2(2), gc.e[e % V], gc.e[(e + 1) % V], lb2), b2 = mul2(sigmoid2(at2(1)), at2(0));
-            a[e] = a2.x, a[e + 1] = a2.y;
-            b[e] = b2.x, b[e + 1] = b2.y;
+        for (int e = 0; e < L * V; e += n) {
+            float x[n], i[n], g[n], ac[n], bc[n];
+            ld_chunk<E, V, S::THREADS>(&sh.raw[0][0][tid], e, x);
+            ld_chunk<E, V, S::THREADS>(&sh.raw[1][0][tid], e, i);
+            ld_chunk<E, V, S::THREADS>(&sh.raw[2][0][tid], e, g);
+            gate_decay_n<UB, n>(ac, g, gc.k0, gc.k1, lb2);
+            sigmoid_n<n>(bc, i);
+            mul_n<n>(bc, bc, x);
+#pragma unroll
+            for (int j = 0; j < n; ++j) a[e + j] = ac[j], b[e + j] = bc[j];
         }
         w.next();
         first = fetch(w);   // the slots are free: the next tile's copies run beside the rest
@@ -146,7 +152,11 @@ __global__ void __launch_bounds__(FwdShape<V>::THREADS, kFwdCtas) glr_fwd_scan_k
         for (int v = 0; v < V; ++v) mA.e[v] = a[v], mH.e[v] = b[v];
         if (!marked) {
 #pragma unroll
-            for (int r = 1; r < L; ++r) then_all<V>(mA.e, mH.e, a + r * V, b + r * V);
+            for (int r = 1; r < L; ++r) {
+                const auto &ar = reinterpret_cast<const float (&)[V]>(a[r * V]);
+                fma_n<V>(mH.e, ar, mH.e, reinterpret_cast<const float (&)[V]>(b[r * V]));
+                mul_n<V>(mA.e, ar, mA.e);
+            }
         } else {
 #pragma unroll
             for (int e = V; e < L * V; ++e) {
@@ -199,7 +209,7 @@ __global__ void __launch_bounds__(FwdShape<V>::THREADS, kFwdCtas) glr_fwd_scan_k
             if (!marked) {
 #pragma unroll
                 for (int r = 0; r < L; ++r, out += p.os) {
-                    apply_all<V>(a + r * V, b + r * V, h);
+                    fma_n<V>(h, reinterpret_cast<const float (&)[V]>(a[r * V]), h, reinterpret_cast<const float (&)[V]>(b[r * V]));
                     if (r < left && p.out) st_f<E, V>(out, h);
                 }
             } else {

@@ -91,47 +91,57 @@ __global__ void __launch_bounds__(BwdShape<E, V>::THREADS, V == 4 ? 2 : 3)
         copies_wait<1>();   // this thread's own copies: no barrier needed
 
         const int left = c < p.D ? (int)min(p.rows - r0, (int64_t)L) : 0;   // rows of this thread that exist
-        const Pack<GateConst, V> gc = sh.gates[stage][tid];
-        const auto raw = [&](int k, int e) { return to_f(sh.raw[stage][k][e / V][tid].e[e % V]); };
-        TokenGates tg[L * V];
+        const ChunkGates<V> gc(sh.gates[stage][tid]);
+        const auto raw = [&](int k) { return &sh.raw[stage][k][0][tid]; };
+        constexpr int n = kGateWidth<V>;
+        float a[L][V], mg[L][V], mi[L][V];   // kept for the second half
         Pack<float, V> mA, mH, mB, mF;
 #pragma unroll
         for (int v = 0; v < V; ++v) mA.e[v] = mB.e[v] = 1.f, mH.e[v] = mF.e[v] = 0.f;
-        if (!marked && left == L) {
 #pragma unroll
-            for (int e = 0; e < L * V; ++e) {
-                const int v = e % V;
-                float a, si;
-                tg[e] = token_gates<UB>(raw(2, e), raw(1, e), gc.e[v], lb2, a, si);
-                // forward: after the rows before; backward: f = a_0 (dout_0 + a_1 (dout_1 + ...))
-                mH.e[v] = fmaf(a, mH.e[v], si * raw(0, e));
-                mA.e[v] *= a;
-                mF.e[v] = fmaf(mA.e[v], raw(3, e), mF.e[v]);
+        for (int e = 0; e < L * V; e += n) {
+            float x[n], i[n], g[n], d[n], ac[n], s[n], mgc[n], mic[n];
+            ld_chunk<E, V, S::THREADS>(raw(0), e, x);
+            ld_chunk<E, V, S::THREADS>(raw(1), e, i);
+            ld_chunk<E, V, S::THREADS>(raw(2), e, g);
+            ld_chunk<E, V, S::THREADS>(raw(3), e, d);
+            token_gates_n<UB, n>(ac, s, mgc, mic, g, i, gc.k0, gc.k1, lb2);
+            mul_n<n>(s, s, x);
+#pragma unroll
+            for (int j = 0; j < n; ++j) {
+                const int r = (e + j) / V, v = (e + j) % V;
+                a[r][v] = ac[j], mg[r][v] = mgc[j], mi[r][v] = mic[j];
             }
-            mB = mA;
-        } else {
+            if (!marked && left == L) {
+                // forward: after the rows before; backward: f = a_0 (dout_0 + a_1 (dout_1 + ...))
 #pragma unroll
-            for (int e = 0; e < L * V; ++e) {
-                const int v = e % V, r = e / V;
-                if (r >= left) continue;
-                float a, si;
-                tg[e] = token_gates<UB>(raw(2, e), raw(1, e), gc.e[v], lb2, a, si);
-                const int begins = marked ? sh.marks.begins[rg * L + r] : -1, ends = marked ? sh.marks.ends[rg * L + r] : -1;
-                const float b = si * raw(0, e);
-                if (begins >= 0) {
-                    const float h0 = p.init ? ld_state(p.init, p.state_type, begins * p.D + c + v) : 0.f;
-                    mA.e[v] = -0.f, mH.e[v] = fmaf(a, h0, b);
-                } else {
-                    mH.e[v] = fmaf(a, mH.e[v], b);
-                    mA.e[v] *= a;
+                for (int j = 0; j < n; j += V) {
+                    const auto &ar = reinterpret_cast<const float (&)[V]>(ac[j]);
+                    fma_n<V>(mH.e, ar, mH.e, reinterpret_cast<const float (&)[V]>(s[j]));
+                    mul_n<V>(mA.e, ar, mA.e);
+                    fma_n<V>(mF.e, mA.e, reinterpret_cast<const float (&)[V]>(d[j]), mF.e);
                 }
-                // backward map of rows 0 .. r: the earlier rows' map after this row's
-                float d = raw(3, e);
-                if (ends >= 0 && p.dfinal) d += p.dfinal[ends * p.D + c + v];
-                const Affine m = then(Affine{ends >= 0 ? -0.f : a, a * d}, Affine{mB.e[v], mF.e[v]});
-                mB.e[v] = m.A, mF.e[v] = m.H;
+            } else {
+#pragma unroll
+                for (int j = 0; j < n; ++j) {
+                    const int r = (e + j) / V, v = (e + j) % V;
+                    if (r >= left) continue;
+                    const int begins = marked ? sh.marks.begins[rg * L + r] : -1, ends = marked ? sh.marks.ends[rg * L + r] : -1;
+                    if (begins >= 0) {
+                        const float h0 = p.init ? ld_state(p.init, p.state_type, begins * p.D + c + v) : 0.f;
+                        mA.e[v] = -0.f, mH.e[v] = fmaf(ac[j], h0, s[j]);
+                    } else {
+                        mH.e[v] = fmaf(ac[j], mH.e[v], s[j]);
+                        mA.e[v] *= ac[j];
+                    }
+                    // backward map of rows 0 .. r: the earlier rows' map after this row's
+                    const float dt = ends >= 0 && p.dfinal ? d[j] + p.dfinal[ends * p.D + c + v] : d[j];
+                    const Affine m = then(Affine{ends >= 0 ? -0.f : ac[j], ac[j] * dt}, Affine{mB.e[v], mF.e[v]});
+                    mB.e[v] = m.A, mF.e[v] = m.H;
+                }
             }
         }
+        if (!marked && left == L) mB = mA;
         sh.A[rg][lane] = mA;
         sh.H[rg][lane] = mH;
         sh.B[rg][lane] = mB;
@@ -176,55 +186,66 @@ __global__ void __launch_bounds__(BwdShape<E, V>::THREADS, V == 4 ? 2 : 3)
 #pragma unroll
         for (int v = 0; v < V; ++v) ddt.e[v] = dA.e[v] = 0.f;
         if (left > 0) {
-            float start[L * V];   // the states that the rows start from
-            const Pack<float, V> h_in = sh.h[rg][lane];
-            float h[V];
+            float start[L][V], h[V], f[V];   // the states that the rows start from
+            const Pack<float, V> h_in = sh.h[rg][lane], f_in = sh.f[rg][lane];
+            const auto &k0 = reinterpret_cast<const float (&)[V]>(gc.k0), &k1 = reinterpret_cast<const float (&)[V]>(gc.k1);
 #pragma unroll
-            for (int v = 0; v < V; ++v) h[v] = h_in.e[v];
+            for (int v = 0; v < V; ++v) h[v] = h_in.e[v], f[v] = f_in.e[v];
 #pragma unroll
-            for (int e = 0; e < L * V; ++e) {
-                const int v = e % V, r = e / V;
-                if (r >= left) break;
-                if (marked && sh.marks.begins[rg * L + r] >= 0)
-                    h[v] = p.init ? ld_state(p.init, p.state_type, sh.marks.begins[rg * L + r] * p.D + c + v) : 0.f;
-                start[e] = h[v];
-                if (r < L - 1) {
-                    const float si = raw(1, e) >= 0.f ? 1.f - tg[e].mi : tg[e].mi, a = UB ? exp2_decay(tg[e].gate) : tg[e].gate;
-                    h[v] = fmaf(a, h[v], si * raw(0, e));
+            for (int r = 0; r < L; ++r) {
+                if (marked && r < left && sh.marks.begins[rg * L + r] >= 0) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        h[v] = p.init ? ld_state(p.init, p.state_type, sh.marks.begins[rg * L + r] * p.D + c + v) : 0.f;
                 }
-            }
-            const Pack<float, V> f_in = sh.f[rg][lane];
-            float f[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) f[v] = f_in.e[v];
+                for (int v = 0; v < V; ++v) start[r][v] = h[v];
+                if (r == L - 1) break;
+                float x[V], i[V], s[V];
+                unpack<E, V>(*(raw(0) + r * S::THREADS), x);
+                unpack<E, V>(*(raw(1) + r * S::THREADS), i);
+                fma_n<V>(s, mi[r], -1.f, 1.f);
+#pragma unroll
+                for (int v = 0; v < V; ++v) s[v] = i[v] >= 0.f ? s[v] : mi[r][v];
+                mul_n<V>(s, s, x);
+                fma_n<V>(h, a[r], h, s);
+            }
             const int64_t row_at = (r0 + L - 1) * p.D + c;
             E *dx = static_cast<E *>(p.dx) + row_at, *di = static_cast<E *>(p.di) + row_at, *dg = static_cast<E *>(p.dg) + row_at;
 #pragma unroll
             for (int r = L - 1; r >= 0; --r, dx -= p.D, di -= p.D, dg -= p.D) {
                 if (r >= left) continue;
-                const int ends = marked ? sh.marks.ends[rg * L + r] : -1, begins = marked ? sh.marks.begins[rg * L + r] : -1;
-                float ox[V], oi[V], og[V];
+                if (marked && sh.marks.ends[rg * L + r] >= 0) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const int e = r * V + v;
-                    if (ends >= 0) f[v] = p.dfinal ? p.dfinal[ends * p.D + c + v] : 0.f;
-                    const float grad = raw(3, e) + f[v];
-                    f[v] = (UB ? exp2_decay(tg[e].gate) : tg[e].gate) * grad;
-                    if (begins >= 0 && p.dinit) p.dinit[begins * p.D + c + v] = f[v];
-                    const float mi = tg[e].mi, other = 1.f - mi;
-                    const float gm = grad * mi, go = grad * other;
-                    ox[v] = raw(1, e) >= 0.f ? go : gm;
-                    oi[v] = gm * other * raw(0, e);
-                    const float dl = f[v] * start[e];
-                    float slope, rate;
-                    gate_slopes<UB>(raw(2, e), gc.e[v], p.lower_bound, tg[e], slope, rate);
-                    og[v] = dl * slope;
-                    ddt.e[v] += og[v];
-                    dA.e[v] = fmaf(dl, rate, dA.e[v]);
+                    for (int v = 0; v < V; ++v) f[v] = p.dfinal ? p.dfinal[sh.marks.ends[rg * L + r] * p.D + c + v] : 0.f;
                 }
-                st_f<E, V>(dx, ox);
-                st_f<E, V>(di, oi);
-                st_f<E, V>(dg, og);
+                float x[V], i[V], g[V], grad[V], gm[V], go[V], o[V], slope[V], rate[V];
+                unpack<E, V>(*(raw(0) + r * S::THREADS), x);
+                unpack<E, V>(*(raw(1) + r * S::THREADS), i);
+                unpack<E, V>(*(raw(2) + r * S::THREADS), g);
+                unpack<E, V>(*(raw(3) + r * S::THREADS), grad);
+                add_n<V>(grad, grad, f);
+                mul_n<V>(f, a[r], grad);
+                if (marked && p.dinit && sh.marks.begins[rg * L + r] >= 0) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) p.dinit[sh.marks.begins[rg * L + r] * p.D + c + v] = f[v];
+                }
+                fma_n<V>(o, mi[r], -1.f, 1.f);
+                mul_n<V>(gm, grad, mi[r]);
+                mul_n<V>(go, grad, o);
+                float out[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) out[v] = i[v] >= 0.f ? go[v] : gm[v];
+                st_f<E, V>(dx, out);
+                mul_n<V>(out, gm, o);
+                mul_n<V>(out, out, x);
+                st_f<E, V>(di, out);
+                gate_slopes_n<UB, V>(slope, rate, g, mg[r], k0, k1, p.lower_bound);
+                mul_n<V>(o, f, start[r]);        // the gradient of gk
+                mul_n<V>(out, o, slope);
+                st_f<E, V>(dg, out);
+                add_n<V>(ddt.e, ddt.e, out);
+                fma_n<V>(dA.e, o, rate, dA.e);
             }
         }
         sh.sum_ddt[rg][lane] = ddt;

@@ -34,36 +34,6 @@ __device__ __forceinline__ Affine then(Affine a, Affine b) {
     return cuts(b.A) ? b : Affine{a.A * b.A, fmaf(b.A, a.H, b.H)};
 }
 
-// V channels at a time, none of whose maps cuts: m <- m then (a, b), and h <- a h + b.
-template <int V>
-__device__ __forceinline__ void then_all(float (&A)[V], float (&H)[V], const float *a, const float *b) {
-    if constexpr (V % 2 == 0) {
-#pragma unroll
-        for (int v = 0; v < V; v += 2) {
-            const float2 a2 = make_float2(a[v], a[v + 1]);
-            const float2 h2 = sm103::fma2(a2, make_float2(H[v], H[v + 1]), make_float2(b[v], b[v + 1]));
-            const float2 m2 = sm103::mul2(a2, make_float2(A[v], A[v + 1]));
-            A[v] = m2.x, A[v + 1] = m2.y, H[v] = h2.x, H[v + 1] = h2.y;
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) H[v] = fmaf(a[v], H[v], b[v]), A[v] *= a[v];
-    }
-}
-template <int V>
-__device__ __forceinline__ void apply_all(const float *a, const float *b, float (&h)[V]) {
-    if constexpr (V % 2 == 0) {
-#pragma unroll
-        for (int v = 0; v < V; v += 2) {
-            const float2 h2 = sm103::fma2(make_float2(a[v], a[v + 1]), make_float2(h[v], h[v + 1]), make_float2(b[v], b[v + 1]));
-            h[v] = h2.x, h[v + 1] = h2.y;
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = fmaf(a[v], h[v], b[v]);
-    }
-}
-
 // A NaN is published as the canonical one, so that no value looks empty.
 __device__ __forceinline__ uint32_t bits_to_publish(float v) {
     return v == v ? __float_as_uint(v) : 0x7fffffffu;
@@ -111,6 +81,29 @@ struct TileShape {
     static constexpr int THREADS = THREADS_, CL = CL_, V = V_;
     static constexpr int CB = CL * V, RG = THREADS / CL, L = kTileRows / RG;
     static_assert(RG * L == kTileRows && THREADS >= 2 * CB && CB % 32 == 0, "tile shape");
+};
+
+// Gates are formed for this many elements at a time: a row's V, or two rows where V is 1.
+template <int V> constexpr int kGateWidth = V == 1 ? 2 : V;
+
+// Elements [e, e + n) of a thread's rows, V per row, from its slots in shared memory.
+template <typename E, int V, int THREADS, int n>
+__device__ __forceinline__ void ld_chunk(const Pack<E, V> *slots, int e, float (&f)[n]) {
+    if constexpr (n == V) {
+        unpack<E, V>(slots[e / V * THREADS], f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < n; ++j) f[j] = to_f(slots[(e + j) / V * THREADS].e[(e + j) % V]);
+    }
+}
+// A thread's gate constants as arrays over a chunk.
+template <int V>
+struct ChunkGates {
+    float k0[kGateWidth<V>], k1[kGateWidth<V>];
+    __device__ __forceinline__ ChunkGates(const Pack<GateConst, V> &g) {
+#pragma unroll
+        for (int j = 0; j < kGateWidth<V>; ++j) k0[j] = g.e[j % V].k0, k1[j] = g.e[j % V].k1;
+    }
 };
 
 // Workspace of a scan and its tiles.  Maps [row tile][padded channel], states after a

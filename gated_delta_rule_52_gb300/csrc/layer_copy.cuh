@@ -41,6 +41,13 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// Lets a kernel use this much dynamic shared memory; set once per device.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<bool> done[kMaxDevices];
+    return once_per_device(done, [&](int) { return cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+}
+
 // Sum over j of part[j * width + c], 32 columns per CTA of 1024 threads, in a fixed order.
 // The threads of the CTA's first warp have the sum of column 32 blockIdx.x + lane.
 __device__ __forceinline__ float column_sum(const float *part, int64_t parts, int64_t width, int64_t c, bool in) {

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include "layer.h"
+#include "sm103.cuh"
 
 namespace kda {
 namespace layer {
@@ -31,19 +32,99 @@ template <typename E, int V> struct alignas(sizeof(E) * V) Pack { E e[V]; };
 
 template <typename E, int V>
 __device__ __forceinline__ Pack<E, V> ld_pack(const E *p) { return *reinterpret_cast<const Pack<E, V> *>(p); }
+// 16-bit values are converted two at a time.
 template <typename E, int V>
 __device__ __forceinline__ void unpack(const Pack<E, V> &a, float (&f)[V]) {
+    if constexpr (sizeof(E) == 2 && V % 2 == 0) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = to_f(a.e[j]);
+        for (int j = 0; j < V; j += 2) {
+            const uint32_t w = reinterpret_cast<const uint32_t *>(a.e)[j / 2];
+            if constexpr (std::is_same_v<E, __nv_bfloat16>) {
+                f[j] = __uint_as_float(w << 16);
+                f[j + 1] = __uint_as_float(w & 0xffff0000u);
+            } else {
+                const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                f[j] = t.x, f[j + 1] = t.y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = to_f(a.e[j]);
+    }
 }
 template <typename E, int V>
 __device__ __forceinline__ void ld_f(const E *p, float (&f)[V]) { unpack<E, V>(ld_pack<E, V>(p), f); }
 template <typename E, int V>
 __device__ __forceinline__ void st_f(E *p, const float (&f)[V]) {
     Pack<E, V> a;
+    if constexpr (sizeof(E) == 2 && V % 2 == 0) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) a.e[j] = from_f<E>(f[j]);
+        for (int j = 0; j < V; j += 2) {
+            uint32_t w;
+            if constexpr (std::is_same_v<E, __nv_bfloat16>) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(f[j + 1]), "f"(f[j]));
+            else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(f[j + 1]), "f"(f[j]));
+            reinterpret_cast<uint32_t *>(a.e)[j / 2] = w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) a.e[j] = from_f<E>(f[j]);
+    }
     *reinterpret_cast<Pack<E, V> *>(p) = a;
+}
+
+// Arithmetic on n values, two per instruction where n is even.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+template <int n>
+__device__ __forceinline__ void fma_n(float (&r)[n], const float (&a)[n], const float (&b)[n], const float (&c)[n]) {   // a b + c
+    if constexpr (n % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < n; j += 2) {
+            const float2 t = sm103::fma2(make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]), make_float2(c[j], c[j + 1]));
+            r[j] = t.x, r[j + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < n; ++j) r[j] = fmaf(a[j], b[j], c[j]);
+    }
+}
+template <int n>
+__device__ __forceinline__ void fma_n(float (&r)[n], const float (&a)[n], float b, float c) {
+    if constexpr (n % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < n; j += 2) {
+            const float2 t = sm103::fma2(make_float2(a[j], a[j + 1]), both(b), both(c));
+            r[j] = t.x, r[j + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < n; ++j) r[j] = fmaf(a[j], b, c);
+    }
+}
+template <int n>
+__device__ __forceinline__ void mul_n(float (&r)[n], const float (&a)[n], const float (&b)[n]) {
+    if constexpr (n % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < n; j += 2) {
+            const float2 t = sm103::mul2(make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]));
+            r[j] = t.x, r[j + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < n; ++j) r[j] = a[j] * b[j];
+    }
+}
+template <int n>
+__device__ __forceinline__ void add_n(float (&r)[n], const float (&a)[n], const float (&b)[n]) {
+    if constexpr (n % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < n; j += 2) {
+            const float2 t = sm103::add2(make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]));
+            r[j] = t.x, r[j + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < n; ++j) r[j] = a[j] + b[j];
+    }
 }
 
 // Recurrent state of either type.
@@ -70,14 +151,15 @@ __device__ __forceinline__ float rcp(float x) {
 // sigma(x) = 1 / (1 + e^-x); e^-x overflows to infinity for very negative x, whose
 // reciprocal is the right 0.
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
-// sigma(x) and its slope sigma(x) sigma(-x) = t / (1 + t)^2, t = e^-|x|: no overflow, and
-// the slope keeps its relative accuracy in both tails.
-__device__ __forceinline__ void sigmoid_slope(float x, float &s, float &slope) {
-    const float t = ex2(-kLog2e * fabsf(x)), r = rcp(1.f + t), tr = t * r;
-    s = x >= 0.f ? r : tr;
-    slope = tr * r;
+template <int n>
+__device__ __forceinline__ void sigmoid_n(float (&s)[n], const float (&x)[n]) {
+    fma_n<n>(s, x, -kLog2e, 0.f);
+#pragma unroll
+    for (int j = 0; j < n; ++j) s[j] = ex2(s[j]);
+    fma_n<n>(s, s, 1.f, 1.f);
+#pragma unroll
+    for (int j = 0; j < n; ++j) s[j] = rcp(s[j]);
 }
-
 // First n in [0, N] with cu[n+1] > row (cu non-decreasing, cu[0] = 0): the sequence of a
 // packed row.  The result is at most N - 1 whatever cu holds.
 __device__ __forceinline__ int64_t seq_of_row(const int64_t *cu, int64_t N, int64_t row) {

@@ -9,7 +9,7 @@
 // rows, then blockDim.y rows per CTA), EL elements each.  The backward kernel is
 // persistent: a CTA walks its rows with the next ones on their way into shared memory, a
 // thread keeps its columns' weights and their gradients in registers, and one partial sum
-// per CTA and column is left for a second kernel.  Rows too long for that (more than 32768
+// per CTA and column is left for a second kernel.  Rows too long for that (more than 16384
 // forward, 8192 backward) run kernels that pass over a row again through L2.
 #include <algorithm>
 
@@ -22,29 +22,51 @@ using namespace layer;
 
 constexpr int kMaxWarps = 32;
 
-// Sums of K values over the blockDim.x threads of every row of the CTA; all threads of the
-// CTA call it together.  `part`: one warp's sums each; a caller's next call must use
-// another one.
-template <int K>
-__device__ __forceinline__ void row_sums(float (&v)[K], float (&part)[K][kMaxWarps]) {
+// Sum of one value over the blockDim.x threads of every row of the CTA; all threads of the
+// CTA call it together.  `part`: one warp's sum each; a caller's next call must use another.
+__device__ __forceinline__ float row_sum(float v, float (&part)[kMaxWarps]) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int o = 16; o; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     const int warps = blockDim.x >> 5;
-    if (warps == 1) return;
+    if (warps == 1) return v;
     const int first = threadIdx.y * warps, lane = threadIdx.x & 31;
-    if (lane == 0) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) part[k][first + (threadIdx.x >> 5)] = v[k];
-    }
+    if (lane == 0) part[first + (threadIdx.x >> 5)] = v;
     __syncthreads();
+    v = lane < warps ? part[first + lane] : 0.f;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        v[k] = lane < warps ? part[k][first + lane] : 0.f;
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// The same for two values, at most 16 warps per row: one half of the lanes sums a, the
+// other b, half the shuffles of two sums.
+__device__ __forceinline__ void row_sum2(float &a, float &b, float (&part)[2][kMaxWarps]) {
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const bool low = lane < 16;
+    float v = (low ? a : b) + __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (warps > 1) {
+        const int first = threadIdx.y * warps, k = lane >> 4, l = lane & 15;
+        if (l == 0) part[k][first + (threadIdx.x >> 5)] = v;
+        __syncthreads();
+        v = l < warps ? part[k][first + l] : 0.f;
+#pragma unroll
+        for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     }
+    a = __shfl_sync(0xffffffffu, v, 0);
+    b = __shfl_sync(0xffffffffu, v, 16);
+}
+template <int n>
+__device__ __forceinline__ float lane_sum(const float (&v)[n]) {
+    float t[2] = {0.f, 0.f};
+    if constexpr (n % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < n; j += 2) add_n<2>(t, t, reinterpret_cast<const float (&)[2]>(v[j]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < n; ++j) t[0] += v[j];
+    }
+    return t[0] + t[1];
 }
 
 // Column of group k of a thread: groups of V, neighbouring threads side by side.
@@ -71,49 +93,51 @@ __device__ __forceinline__ void ld_param(const float *p, int c, float dflt, floa
 }
 
 template <typename E, int V, int EL>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(NormParams p) {
+__global__ void __launch_bounds__(EL == 32 ? 512 : 1024) norm_fwd_kernel(NormParams p) {
     constexpr int N = EL / V;
-    __shared__ float part[2][1][kMaxWarps];
+    __shared__ float part[2][kMaxWarps];
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = row < p.rows;
     const E *x = static_cast<const E *>(p.x) + row * p.xs;
-    Pack<E, V> raw[N];
+    float f[N][V];
+    {
+        Pack<E, V> raw[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-        if (live && column<V>(k) < p.D) raw[k] = ld_pack<E, V>(x + column<V>(k));
-    float s[1] = {0.f};
+        for (int k = 0; k < N; ++k)
+            if (live && column<V>(k) < p.D) raw[k] = ld_pack<E, V>(x + column<V>(k));
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        if (!live || column<V>(k) >= p.D) continue;
+        for (int k = 0; k < N; ++k) {
+            if (live && column<V>(k) < p.D) unpack<E, V>(raw[k], f[k]);
+            else
 #pragma unroll
-        for (int v = 0; v < V; ++v) s[0] += to_f(raw[k].e[v]);
-    }
-    row_sums<1>(s, part[0]);
-    const float inv = 1.f / (float)p.D, mean = s[0] * inv;
-    s[0] = 0.f;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        if (!live || column<V>(k) >= p.D) continue;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float d = to_f(raw[k].e[v]) - mean;
-            s[0] = fmaf(d, d, s[0]);
+                for (int v = 0; v < V; ++v) f[k][v] = 0.f;
         }
     }
-    row_sums<1>(s, part[1]);
+    const float inv = 1.f / (float)p.D;
+    const float mean = row_sum(lane_sum(reinterpret_cast<const float (&)[EL]>(f)), part[0]) * inv;
+    float sq[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) sq[v] = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if (column<V>(k) >= p.D) continue;
+        fma_n<V>(f[k], f[k], 1.f, -mean);
+        fma_n<V>(sq, f[k], f[k], sq);
+    }
+    const float var = row_sum(lane_sum(sq), part[1]) * inv;
     if (!live) return;
-    const float rstd = 1.f / sqrtf(fmaf(s[0], inv, p.eps));
+    const float rstd = 1.f / sqrtf(var + p.eps);
     E *out = static_cast<E *>(p.out) + row * p.os;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         const int c = column<V>(k);
         if (c >= p.D) continue;
-        float w[V], b[V], y[V];
+        float w[V], b[V];
         ld_param<V>(p.weight, c, 1.f, w);
         ld_param<V>(p.bias, c, 0.f, b);
-#pragma unroll
-        for (int v = 0; v < V; ++v) y[v] = fmaf((to_f(raw[k].e[v]) - mean) * rstd, w[v], b[v]);
-        st_f<E, V>(out + c, y);
+        fma_n<V>(f[k], f[k], rstd, 0.f);
+        fma_n<V>(f[k], f[k], w, b);
+        st_f<E, V>(out + c, f[k]);
     }
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mean;
@@ -162,6 +186,15 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *p
         copies_commit();
     };
 
+    // columns that do not exist stay 0 in every slot
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if (column<V>(k) < p.D) continue;
+        for (int j = 0; j < 2 * kStages; ++j) {
+            const float zero[V] = {};
+            st_f<E, V>(&slot(j / 2, j % 2, k).e[0], zero);
+        }
+    }
     float w[EL], dw[EL], db[EL];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -172,45 +205,47 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *p
     }
     const float inv = 1.f / (float)p.D;
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int64_t passes = ceil_div(p.rows - (int64_t)blockIdx.x * blockDim.y, step);
+    const int passes = (int)ceil_div(p.rows - (int64_t)blockIdx.x * blockDim.y, step);
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) fetch(row + k * step, k);
-    for (int64_t pass = 0; pass < passes; ++pass, row += step) {
-        const int stage = (int)(pass % kStages);
-        fetch(row + (kStages - 1) * step, (int)((pass + kStages - 1) % kStages));
+    for (int pass = 0, stage = 0; pass < passes; ++pass, row += step) {
+        fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
         copies_wait<kStages - 1>();
         __syncwarp();
         const bool live = row < p.rows;
         const float2 st = stats[stage][warp];
-        float xh[EL], d[EL], s[2] = {0.f, 0.f};
+        float xh[EL], d[EL], s1 = 0.f, s2 = 0.f;
+        if (live) {
+            float t[EL];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const bool in = live && column<V>(k) < p.D;
-            const Pack<E, V> x = slot(stage, 0, k), dy = slot(stage, 1, k);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int e = k * V + v;
-                const float g = in ? to_f(dy.e[v]) : 0.f;
-                xh[e] = in ? (to_f(x.e[v]) - st.x) * st.y : 0.f;
-                d[e] = g * w[e];
-                s[0] += d[e];
-                s[1] = fmaf(d[e], xh[e], s[1]);
-                dw[e] = fmaf(g, xh[e], dw[e]);
-                db[e] += g;
+            for (int k = 0; k < N; ++k) {
+                unpack<E, V>(slot(stage, 0, k), reinterpret_cast<float (&)[V]>(xh[k * V]));
+                unpack<E, V>(slot(stage, 1, k), reinterpret_cast<float (&)[V]>(d[k * V]));
             }
+            fma_n<EL>(xh, xh, 1.f, -st.x);
+            fma_n<EL>(xh, xh, st.y, 0.f);
+            fma_n<EL>(dw, d, xh, dw);
+            add_n<EL>(db, db, d);
+            mul_n<EL>(d, d, w);
+            mul_n<EL>(t, d, xh);
+            s1 = lane_sum(d);
+            s2 = lane_sum(t);
         }
-        row_sums<2>(s, part[pass & 1]);
+        row_sum2(s1, s2, part[pass & 1]);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
         if (!live) continue;
-        const float m1 = s[0] * inv, m2 = s[1] * inv;
+        // rstd (d - m1 - xh m2)
+        fma_n<EL>(xh, xh, -st.y * s2 * inv, -st.y * s1 * inv);
+        const float r = st.y;
+#pragma unroll
+        for (int e = 0; e < EL; e += 2) {
+            const float2 o = sm103::fma2(make_float2(d[e], d[e + 1]), both(r), make_float2(xh[e], xh[e + 1]));
+            d[e] = o.x, d[e + 1] = o.y;
+        }
         E *dx = static_cast<E *>(p.dx) + row * p.D;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            if (column<V>(k) >= p.D) continue;
-            float o[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) o[v] = st.y * (d[k * V + v] - fmaf(xh[k * V + v], m2, m1));
-            st_f<E, V>(dx + column<V>(k), o);
-        }
+        for (int k = 0; k < N; ++k)
+            if (column<V>(k) < p.D) st_f<E, V>(dx + column<V>(k), reinterpret_cast<const float (&)[V]>(d[k * V]));
     }
     copies_wait<0>();
     if (!part_out) return;
@@ -239,21 +274,19 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *p
 // ---- rows too long for a thread's registers: a CTA per row, several passes
 template <typename E>
 __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormParams p) {
-    __shared__ float part[2][1][kMaxWarps];
+    __shared__ float part[2][kMaxWarps];
     const int64_t row = blockIdx.x;
     const E *x = static_cast<const E *>(p.x) + row * p.xs;
     E *out = static_cast<E *>(p.out) + row * p.os;
-    float s[1] = {0.f};
-    for (int64_t c = threadIdx.x; c < p.D; c += 1024) s[0] += to_f(x[c]);
-    row_sums<1>(s, part[0]);
-    const float mean = s[0] / (float)p.D;
-    s[0] = 0.f;
+    float s = 0.f;
+    for (int64_t c = threadIdx.x; c < p.D; c += 1024) s += to_f(x[c]);
+    const float mean = row_sum(s, part[0]) / (float)p.D;
+    s = 0.f;
     for (int64_t c = threadIdx.x; c < p.D; c += 1024) {
         const float d = to_f(x[c]) - mean;
-        s[0] = fmaf(d, d, s[0]);
+        s = fmaf(d, d, s);
     }
-    row_sums<1>(s, part[1]);
-    const float rstd = 1.f / sqrtf(s[0] / (float)p.D + p.eps);
+    const float rstd = 1.f / sqrtf(row_sum(s, part[1]) / (float)p.D + p.eps);
     for (int64_t c = threadIdx.x; c < p.D; c += 1024)
         out[c] = from_f<E>(fmaf((to_f(x[c]) - mean) * rstd, p.weight ? p.weight[c] : 1.f, p.bias ? p.bias[c] : 0.f));
     if (threadIdx.x == 0) {
@@ -268,14 +301,13 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(NormParams p) {
     const int64_t row = blockIdx.x;
     const E *x = static_cast<const E *>(p.x) + row * p.xs, *dy = static_cast<const E *>(p.dout) + row * p.ds;
     const float mean = p.mean[row], rstd = p.rstd[row];
-    float s[2] = {0.f, 0.f};
+    float s1 = 0.f, s2 = 0.f;
     for (int64_t c = threadIdx.x; c < p.D; c += 1024) {
         const float d = to_f(dy[c]) * (p.weight ? p.weight[c] : 1.f);
-        s[0] += d;
-        s[1] = fmaf(d, (to_f(x[c]) - mean) * rstd, s[1]);
+        s1 += d;
+        s2 = fmaf(d, (to_f(x[c]) - mean) * rstd, s2);
     }
-    row_sums<2>(s, part);
-    const float m1 = s[0] / (float)p.D, m2 = s[1] / (float)p.D;
+    const float m1 = row_sum(s1, part[0]) / (float)p.D, m2 = row_sum(s2, part[1]) / (float)p.D;
     for (int64_t c = threadIdx.x; c < p.D; c += 1024) {
         const float d = to_f(dy[c]) * (p.weight ? p.weight[c] : 1.f), xh = (to_f(x[c]) - mean) * rstd;
         static_cast<E *>(p.dx)[row * p.D + c] = from_f<E>(rstd * (d - fmaf(xh, m2, m1)));
@@ -311,7 +343,7 @@ __global__ void __launch_bounds__(1024) norm_param_sum_kernel(NormParams p, int6
 }
 
 // ---- host side
-constexpr int64_t kFwdMaxD = 32768, kBwdMaxD = 8192;
+constexpr int64_t kFwdMaxD = 16384, kBwdMaxD = 8192;
 constexpr int64_t kLongParts = 256;
 
 // Threads of a row, and rows of a CTA: at most `most` threads, whole warps.
@@ -354,10 +386,7 @@ cudaError_t run_bwd(const NormParams &p, float *part, int sms, cudaStream_t stre
     const int threads = block.x * block.y;
     const int smem = threads * EL * std::max(kStages * 2 * (int)sizeof(E), block.y > 1 ? 8 : 0);
     constexpr auto kernel = norm_bwd_kernel<E, V, EL>;
-    static std::atomic<bool> done[kMaxDevices];
-    const cudaError_t e = once_per_device(done, [&](int) {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * EL * kStages * 2 * (int)sizeof(E));
-    });
+    const cudaError_t e = allow_smem<kernel>(512 * EL * kStages * 2 * (int)sizeof(E));
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)bwd_grid(p, sms), block, smem, stream>>>(p, part);
     return cudaGetLastError();

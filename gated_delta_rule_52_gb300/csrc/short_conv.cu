@@ -95,27 +95,13 @@ __device__ __forceinline__ void ld_x(const ConvParams &p, int64_t n, int64_t lo,
     }
 }
 
-// acc += a * b, V channels.
-template <int V>
-__device__ __forceinline__ void fma_all(float (&acc)[V], const float (&a)[V], const float (&b)[V]) {
-    if constexpr (V % 2 == 0) {
-#pragma unroll
-        for (int v = 0; v < V; v += 2) {
-            const float2 t = sm103::fma2(make_float2(a[v], a[v + 1]), make_float2(b[v], b[v + 1]), make_float2(acc[v], acc[v + 1]));
-            acc[v] = t.x, acc[v + 1] = t.y;
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = fmaf(a[v], b[v], acc[v]);
-    }
-}
 // y_t of the window x_{t-(W-1)} .. x_t.
 template <int V, int W>
 __device__ __forceinline__ void taps_sum(const float (&w)[W][V], const float (&b)[V], const float (&xw)[W][V], float (&y)[V]) {
 #pragma unroll
     for (int v = 0; v < V; ++v) y[v] = b[v];
 #pragma unroll
-    for (int j = 0; j < W; ++j) fma_all<V>(y, w[j], xw[j]);
+    for (int j = 0; j < W; ++j) fma_n<V>(y, w[j], xw[j], y);
 }
 template <int V, int W>
 __device__ __forceinline__ void shift(float (&xw)[W][V]) {
@@ -125,10 +111,15 @@ __device__ __forceinline__ void shift(float (&xw)[W][V]) {
         for (int v = 0; v < V; ++v) xw[j][v] = xw[j + 1][v];
 }
 
+constexpr int kBatch = 4, kStages = 3;   // rows per copy group, groups of a thread's ring
+
 template <typename E, int V, int W>
-__global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 4) conv_fwd_kernel(ConvParams p, Runs runs, int channel_blocks) {
-    const int64_t q = (int64_t)(blockIdx.x / channel_blocks) * kGroups + threadIdx.x / kLanes;
-    const int64_t c = ((int64_t)(blockIdx.x % channel_blocks) * kLanes + threadIdx.x % kLanes) * V;
+__global__ void __launch_bounds__(kThreads, 3) conv_fwd_kernel(ConvParams p, Runs runs, int channel_blocks) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    auto &ring = *reinterpret_cast<Pack<E, V>(*)[kStages][kBatch][kThreads]>(smem);
+    const int tid = threadIdx.x;
+    const int64_t q = (int64_t)(blockIdx.x / channel_blocks) * kGroups + tid / kLanes;
+    const int64_t c = ((int64_t)(blockIdx.x % channel_blocks) * kLanes + tid % kLanes) * V;
     if (q >= runs.count || c >= p.D) return;
     Run r = run_of(p, runs, q);
     float w[W][V], b[V], xw[W][V];
@@ -136,6 +127,13 @@ __global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 4) conv_fwd_kernel(Conv
 #pragma unroll
     for (int v = 0; v < V; ++v) b[v] = p.bias ? p.bias[c + v] : 0.f;
     do {
+        const int own = (int)(r.s1 - r.s0);
+        const auto fetch = [&](int j0, int stage) {
+            copy_rows<E, V, kBatch, kThreads>(&ring[stage][0][tid], static_cast<const E *>(p.x) + (r.s0 + j0) * p.xs + c, p.xs, own - j0);
+            copies_commit();
+        };
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) fetch(k * kBatch, k);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) ld_x<E, V>(p, r.n, r.lo, r.s0 - (W - 1) + j, c, xw[j]);
         // the final state is the first run's to write: it alone reads the initial state
@@ -146,29 +144,33 @@ __global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 4) conv_fwd_kernel(Conv
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) st_f<E, V>(static_cast<E *>(p.fin) + (r.n * (W - 1) + j) * p.D + c, last[j]);
         }
-        const E *x = static_cast<const E *>(p.x) + r.s0 * p.xs + c;
         E *out = static_cast<E *>(p.out) + r.s0 * p.os + c;
-        constexpr int kBatch = 8;   // rows on their way together
-        for (int left = (int)(r.s1 - r.s0); left > 0; left -= kBatch) {
-            Pack<E, V> raw[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k, x += p.xs)
-                if (k < left) raw[k] = ld_pack<E, V>(x);
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k, out += p.os) {
-                if (k >= left) break;
-                unpack<E, V>(raw[k], xw[W - 1]);
-                float y[V];
-                taps_sum<V, W>(w, b, xw, y);
-                if (p.silu) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) y[v] *= sigmoid(y[v]);
-                }
-                st_f<E, V>(out, y);
-                shift<V, W>(xw);
+        const auto row = [&](int k, int stage) {
+            unpack<E, V>(ring[stage][k][tid], xw[W - 1]);
+            float y[V], s[V];
+            taps_sum<V, W>(w, b, xw, y);
+            if (p.silu) {
+                sigmoid_n<V>(s, y);
+                mul_n<V>(y, y, s);
             }
+            st_f<E, V>(out, y);
+            out += p.os;
+            shift<V, W>(xw);
+        };
+        for (int j0 = 0, stage = 0; j0 < own; j0 += kBatch) {
+            fetch(j0 + (kStages - 1) * kBatch, stage == 0 ? kStages - 1 : stage - 1);
+            copies_wait<kStages - 1>();   // this thread's own copies: no barrier needed
+            if (j0 + kBatch <= own) {
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) row(k, stage);
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < own - j0; ++k) row(k, stage);
+            }
+            stage = stage + 1 == kStages ? 0 : stage + 1;
         }
     } while (next_part(p, r));
+    copies_wait<0>();
 }
 
 // Final states of packed sequences (and of sequences without tokens): one thread per
@@ -188,8 +190,6 @@ __global__ void __launch_bounds__(kThreads) conv_state_kernel(ConvParams p) {
         st_f<E, 1>(static_cast<E *>(p.fin) + (n * (p.W - 1) + j) * p.D + c, f);
     }
 }
-
-constexpr int kBatch = 4, kStages = 3;   // rows per copy group, groups of the ring
 
 // With t = u - (W-1), row u's q completes d_t = sum_k w[W-1-k] q_{t+k}: the gradient of
 // input row t, or of a row of the initial state where t comes before the sequence.  So a
@@ -235,50 +235,71 @@ __global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 3) conv_bwd_kernel(Conv
                 for (int v = 0; v < V; ++v) qs[j][v] = 0.f;
             }
             E *dx = static_cast<E *>(p.dx) + (r.s0 - (W - 1)) * p.D + c;
-            int stage = 0;
-            for (int j0 = 0; j0 < all; j0 += kBatch) {
+            // q of the row in slot k, whose window is complete
+            const auto form_q = [&](int k, int stage) {
+                float (&qn)[V] = qs[W - 1];
+                unpack<E, V>(ring[stage][0][k][tid], xw[W - 1]);
+                unpack<E, V>(ring[stage][1][k][tid], qn);
+                if (p.silu) {   // silu' = s (1 + y (1 - s))
+                    float y[V], s[V], o[V], one[V];
+                    taps_sum<V, W>(w, b, xw, y);
+                    sigmoid_n<V>(s, y);
+                    fma_n<V>(o, s, -1.f, 1.f);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) one[v] = 1.f;
+                    fma_n<V>(o, y, o, one);
+                    mul_n<V>(s, s, o);
+                    mul_n<V>(qn, qn, s);
+                }
+            };
+            const auto add_params = [&]() {
+                add_n<V>(db, db, qs[W - 1]);
+#pragma unroll
+                for (int i = 0; i < W; ++i) fma_n<V>(dw[i], qs[W - 1], xw[i], dw[i]);
+            };
+            const auto form_d = [&](float (&d)[V]) {
+                mul_n<V>(d, w[W - 1], qs[0]);
+#pragma unroll
+                for (int i = 1; i < W; ++i) fma_n<V>(d, w[W - 1 - i], qs[i], d);
+            };
+            for (int j0 = 0, stage = 0; j0 < all; j0 += kBatch) {
                 fetch(j0 + (kStages - 1) * kBatch, stage == 0 ? kStages - 1 : stage - 1);
                 copies_wait<kStages - 1>();   // this thread's own copies: no barrier needed
+                if (j0 >= W - 1 && j0 + kBatch <= own) {
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k, dx += p.D) {
-                    const int j = j0 + k;
-                    if (j >= all) break;
-                    float (&qn)[V] = qs[W - 1];
-                    if (j < real) {
-                        unpack<E, V>(ring[stage][0][k][tid], xw[W - 1]);
-                        unpack<E, V>(ring[stage][1][k][tid], qn);
-                        if (p.silu) {
-                            float y[V];
-                            taps_sum<V, W>(w, b, xw, y);
-#pragma unroll
-                            for (int v = 0; v < V; ++v) {   // silu' = s (1 + y (1 - s))
-                                const float s = sigmoid(y[v]);
-                                qn[v] *= s * fmaf(y[v], 1.f - s, 1.f);
-                            }
-                        }
-                        if (j < own) {
-#pragma unroll
-                            for (int v = 0; v < V; ++v) db[v] += qn[v];
-#pragma unroll
-                            for (int i = 0; i < W; ++i) fma_all<V>(dw[i], qn, xw[i]);
-                        }
+                    for (int k = 0; k < kBatch; ++k, dx += p.D) {
+                        float d[V];
+                        form_q(k, stage);
+                        add_params();
+                        form_d(d);
+                        st_f<E, V>(dx, d);
                         shift<V, W>(xw);
-                    } else {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) qn[v] = 0.f;
+                        shift<V, W>(qs);
                     }
-                    float d[V];
+                } else {
+                    // the part's first and last rows
+                    const int n = min(kBatch, all - j0);
+#pragma unroll 1
+                    for (int k = 0; k < n; ++k, dx += p.D) {
+                        const int j = j0 + k;
+                        if (j < real) {
+                            form_q(k, stage);
+                            if (j < own) add_params();
+                        } else {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) d[v] = 0.f;
+                            for (int v = 0; v < V; ++v) qs[W - 1][v] = 0.f;
+                        }
+                        float d[V];
+                        form_d(d);
+                        if (p.dfinal && r.s0 + j >= r.hi) {
 #pragma unroll
-                    for (int i = 0; i < W; ++i) fma_all<V>(d, w[W - 1 - i], qs[i]);
-                    if (p.dfinal && r.s0 + j >= r.hi) {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) d[v] += p.dfinal[(r.n * (W - 1) + (r.s0 + j - r.hi)) * p.D + c + v];
+                            for (int v = 0; v < V; ++v) d[v] += p.dfinal[(r.n * (W - 1) + (r.s0 + j - r.hi)) * p.D + c + v];
+                        }
+                        if (j >= W - 1) st_f<E, V>(dx, d);
+                        else if (first && p.dinit) st_f<float, V>(p.dinit + (r.n * (W - 1) + j) * p.D + c, d);
+                        shift<V, W>(xw);
+                        shift<V, W>(qs);
                     }
-                    if (j >= W - 1) st_f<E, V>(dx, d);
-                    else if (first && p.dinit) st_f<float, V>(p.dinit + (r.n * (W - 1) + j) * p.D + c, d);
-                    shift<V, W>(qs);
                 }
                 stage = stage + 1 == kStages ? 0 : stage + 1;
             }
@@ -371,8 +392,13 @@ cudaError_t launch_conv_fwd(const ConvParams &p, int sms, cudaStream_t stream) {
     return with_shape(p, [&](auto *tag, auto V, auto W) {
         using E = std::remove_pointer_t<decltype(tag)>;
         const int64_t blocks = ceil_div(p.D, kLanes * V);
-        if (p.rows > 0)
-            conv_fwd_kernel<E, V, W><<<(unsigned)(run_blocks(runs) * blocks), kThreads, 0, stream>>>(p, runs, (int)blocks);
+        if (p.rows > 0) {
+            constexpr auto kernel = conv_fwd_kernel<E, V, W>;
+            constexpr int smem = (int)sizeof(Pack<E, V>) * kStages * kBatch * kThreads;
+            const cudaError_t e = allow_smem<kernel>(smem);
+            if (e != cudaSuccess) return e;
+            kernel<<<(unsigned)(run_blocks(runs) * blocks), kThreads, smem, stream>>>(p, runs, (int)blocks);
+        }
         if (p.fin && (p.cu_seqlens || p.T == 0))
             conv_state_kernel<E><<<(unsigned)ceil_div(p.N * p.D, kThreads), kThreads, 0, stream>>>(p);
         return cudaGetLastError();
@@ -390,10 +416,7 @@ cudaError_t launch_conv_bwd(const ConvParams &p, unsigned char *ws, int sms, cud
         if (p.rows == 0) return cudaSuccess;
         constexpr auto kernel = conv_bwd_kernel<E, V, W>;
         constexpr int smem = (int)std::max(sizeof(Pack<E, V>) * kStages * 2 * kBatch * kThreads, sizeof(float) * kGroups * (W + 1) * kLanes * V);
-        static std::atomic<bool> done[kMaxDevices];
-        const cudaError_t e = once_per_device(done, [&](int) {
-            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        });
+        const cudaError_t e = allow_smem<kernel>(smem);
         if (e != cudaSuccess) return e;
         kernel<<<(unsigned)(run_blocks(runs) * blocks), kThreads, smem, stream>>>(p, runs, (int)blocks, part);
         return cudaGetLastError();
