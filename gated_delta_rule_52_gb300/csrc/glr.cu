@@ -57,47 +57,50 @@ __global__ void __launch_bounds__(128) glr_fwd_step_kernel(GlrParams p) {
     }
 }
 
-// 8 rows by 4 channels per thread, or 16 rows by 1 where rows are not aligned, 5 CTAs per
-// SM.  Measured on 8192 x 8192 bf16: 119 us, with 4 CTAs 120 us, with 256 threads of 4 rows
-// (3 CTAs) 133 us (twice the per-thread work of a tile).
-template <int V> using FwdShape = TileShape<128, V == 4 ? 16 : 32, V>;
+// 8 rows by 4 channels per thread, 5 CTAs per SM.  Measured on 8192 x 8192 bf16: 118 us,
+// with 4 CTAs 120 us, with 256 threads of 4 rows (3 CTAs) 133 us (twice the per-thread work
+// of a tile), with two tiles in flight per CTA, the next one's map handed on before the
+// current one's state is taken (3 CTAs), 163 us (12 warps per SM are too few).
+using FwdShape = TileShape<128, 16, 4>;
 constexpr int kFwdCtas = 5;
 
-template <typename E, int V>
+template <typename E>
 struct FwdShared {
-    using S = FwdShape<V>;
-    Pack<E, V> raw[3][S::L][S::THREADS];
-    Pack<GateConst, V> gates[S::THREADS];
-    Pack<float, V> A[S::RG][S::CL], H[S::RG][S::CL];   // maps of the row groups
-    Pack<float, V> h[S::RG][S::CL];                    // states that enter them
+    using S = FwdShape;
+    Pack<E, S::V> raw[3][S::L][S::THREADS];               // x, i, g
+    Pack<GateConst, S::V> gates[S::THREADS];
+    Pack<float, S::V> A[S::RG][S::CL], H[S::RG][S::CL];   // maps of the row groups
+    Pack<float, S::V> h[S::RG][S::CL];                    // states that enter them
     TileMarks marks;
 };
 
-template <typename E, int V, bool UB>
-__global__ void __launch_bounds__(FwdShape<V>::THREADS, kFwdCtas) glr_fwd_scan_kernel(GlrParams p, ScanPlan s) {
-    using namespace sm103;
-    using S = FwdShape<V>;
-    constexpr int CL = S::CL, L = S::L, CB = S::CB, RG = S::RG;
+template <typename E, bool WIDE, bool UB>
+__global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas) glr_fwd_scan_kernel(GlrParams p, ScanPlan s) {
+    using S = FwdShape;
+    constexpr int CL = S::CL, V = S::V, L = S::L, CB = S::CB, RG = S::RG;
     extern __shared__ __align__(16) unsigned char smem[];
-    FwdShared<E, V> &sh = *reinterpret_cast<FwdShared<E, V> *>(smem);
+    FwdShared<E> &sh = *reinterpret_cast<FwdShared<E> *>(smem);
     const int tid = threadIdx.x, lane = tid % CL, rg = tid / CL;
     const float lb2 = p.lower_bound * kLog2e;
+    const int D = (int)p.D;
 
     // starts the copies of a tile into this thread's own slots; returns its first sequence
-    auto fetch = [&](const TileWalk &w) {
+    const auto fetch = [&](const TileWalk &w) {
         int first = 0;
         if (w.rt < s.row_tiles) {
             const int64_t r0 = w.rt * kTileRows + rg * L;
             const int c = w.cb * CB + lane * V;
             first = s.first_seq[w.rt];
-            const float *gate = reinterpret_cast<const float *>(s.gates + c);
-            copy_async<float, V == 4 ? 4 : 2>(&sh.gates[tid], gate);
-            if (V == 4) copy_async<float, V == 4 ? 4 : 2>(&sh.gates[tid].e[V / 2], gate + V);
-            if (c < p.D) {
+            copy_gates<V>(&sh.gates[tid], s.gates + c);
+            if (c < D) {
                 const int left = (int)min(p.rows - r0, (int64_t)L);
-                copy_rows<E, V, L, S::THREADS>(&sh.raw[0][0][tid], static_cast<const E *>(p.x) + r0 * p.xs + c, p.xs, left);
-                copy_rows<E, V, L, S::THREADS>(&sh.raw[1][0][tid], static_cast<const E *>(p.i) + r0 * p.is + c, p.is, left);
-                copy_rows<E, V, L, S::THREADS>(&sh.raw[2][0][tid], static_cast<const E *>(p.g) + r0 * p.gs + c, p.gs, left);
+                const auto copy = [&](int k, const void *src, int64_t stride) {
+                    copy_rows<E, V, WIDE, L, S::THREADS>(&sh.raw[k][0][tid], static_cast<const E *>(src) + r0 * stride + c, stride,
+                                                         left, D - c);
+                };
+                copy(0, p.x, p.xs);
+                copy(1, p.i, p.is);
+                copy(2, p.g, p.gs);
             }
         }
         copies_commit();
@@ -108,60 +111,65 @@ __global__ void __launch_bounds__(FwdShape<V>::THREADS, kFwdCtas) glr_fwd_scan_k
     int first = fetch(w);
     while (w.rt < s.row_tiles) {
         const int64_t rt = w.rt, r0 = rt * kTileRows + rg * L;
-        const int c = w.cb * CB + lane * V, block = w.cb * CB;
+        const int block = w.cb * CB, c = block + lane * V;
         const bool marked = mark_tile(p, rt, first, sh.marks);
+        const bool plain = !marked && (rt + 1) * kTileRows <= p.rows;   // every row inside one sequence
         copies_wait<0>();   // this thread's own copies: no barrier needed
 
-        float a[L * V], b[L * V];
-        const int left = c < p.D ? (int)min(p.rows - r0, (int64_t)L) : 0;   // rows of this thread that exist
-        constexpr int n = kGateWidth<V>;
-        const ChunkGates<V> gc(sh.gates[tid]);
+        float a[L][V], b[L][V];
+        {
+            const ChannelGates<V> gc(sh.gates[tid]);
 #pragma unroll
-        for (int e = 0; e < L * V; e += n) {
-            float x[n], i[n], g[n], ac[n], bc[n];
-            ld_chunk<E, V, S::THREADS>(&sh.raw[0][0][tid], e, x);
-            ld_chunk<E, V, S::THREADS>(&sh.raw[1][0][tid], e, i);
-            ld_chunk<E, V, S::THREADS>(&sh.raw[2][0][tid], e, g);
-            gate_decay_n<UB, n>(ac, g, gc.k0, gc.k1, lb2);
-            sigmoid_n<n>(bc, i);
-            mul_n<n>(bc, bc, x);
-#pragma unroll
-            for (int j = 0; j < n; ++j) a[e + j] = ac[j], b[e + j] = bc[j];
+            for (int r = 0; r < L; ++r) {
+                float x[V], i[V], g[V];
+                unpack<E, V>(sh.raw[0][r][tid], x);
+                unpack<E, V>(sh.raw[1][r][tid], i);
+                unpack<E, V>(sh.raw[2][r][tid], g);
+                gate_decay_n<UB, V>(a[r], g, gc.k0, gc.k1, lb2);
+                sigmoid_n<V>(b[r], i);
+                mul_n<V>(b[r], b[r], x);
+            }
         }
         w.next();
         first = fetch(w);   // the slots are free: the next tile's copies run beside the rest
-        if (left < L) {
-#pragma unroll
-            for (int e = 0; e < L * V; ++e)
-                if (e / V >= left) a[e] = 1.f, b[e] = 0.f;
-        }
-        // a row that begins a sequence starts from the initial state instead
-        if (marked) {
-#pragma unroll
-            for (int e = 0; e < L * V; ++e) {
-                const int r = e / V, n = sh.marks.begins[rg * L + r];
-                if (n < 0 || r >= left) continue;
-                const float h0 = p.init ? ld_state(p.init, p.state_type, n * p.D + c + e % V) : 0.f;
-                b[e] = fmaf(a[e], h0, b[e]);
-                a[e] = -0.f;   // depends on nothing before
-                if (r == 0 && rg == 0 && p.checkpoints) p.checkpoints[rt * p.D + c + e % V] = h0;
-            }
-        }
         Pack<float, V> mA, mH;
+        if (plain) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) mA.e[v] = a[v], mH.e[v] = b[v];
-        if (!marked) {
+            for (int v = 0; v < V; ++v) mA.e[v] = a[0][v], mH.e[v] = b[0][v];
 #pragma unroll
             for (int r = 1; r < L; ++r) {
-                const auto &ar = reinterpret_cast<const float (&)[V]>(a[r * V]);
-                fma_n<V>(mH.e, ar, mH.e, reinterpret_cast<const float (&)[V]>(b[r * V]));
-                mul_n<V>(mA.e, ar, mA.e);
+                fma_n<V>(mH.e, a[r], mH.e, b[r]);
+                mul_n<V>(mA.e, a[r], mA.e);
             }
         } else {
+            if (r0 + L > p.rows) {
 #pragma unroll
-            for (int e = V; e < L * V; ++e) {
-                const Affine m = then(Affine{mA.e[e % V], mH.e[e % V]}, Affine{a[e], b[e]});
-                mA.e[e % V] = m.A, mH.e[e % V] = m.H;
+                for (int r = 0; r < L; ++r)
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        if (r0 + r >= p.rows) a[r][v] = 1.f, b[r][v] = 0.f;
+            }
+            if (marked) {
+#pragma unroll
+                for (int r = 0; r < L; ++r) {
+                    const int n = sh.marks.begins[rg * L + r];
+                    if (n < 0) continue;
+                    // a row that begins a sequence starts from the initial state instead
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float h0 = p.init && c + v < D ? ld_state(p.init, p.state_type, n * p.D + c + v) : 0.f;
+                        b[r][v] = fmaf(a[r][v], h0, b[r][v]);
+                        a[r][v] = -0.f;   // depends on nothing before
+                        if (r == 0 && rg == 0 && p.checkpoints && c + v < D) p.checkpoints[rt * p.D + c + v] = h0;
+                    }
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                Affine m{a[0][v], b[0][v]};
+#pragma unroll
+                for (int r = 1; r < L; ++r) m = then(m, Affine{a[r][v], b[r][v]});
+                mA.e[v] = m.A, mH.e[v] = m.H;
             }
         }
         sh.A[rg][lane] = mA;
@@ -170,19 +178,24 @@ __global__ void __launch_bounds__(FwdShape<V>::THREADS, kFwdCtas) glr_fwd_scan_k
 
         const int64_t group = rt >> s.group_log2;
         const int pos = (int)(rt - (group << s.group_log2)), last = (1 << s.group_log2) - 1;
+        const int ch = tid % CB;
+        const auto map = [&](int q) { return Affine{sh.A[q][ch / V].e[ch % V], sh.H[q][ch / V].e[ch % V]}; };
         if (tid < CB) {
             // one thread per channel: the tile's map, handed on
             if (pos != last) {
-                const int ch = tid;
-                Affine t{sh.A[0][ch / V].e[ch % V], sh.H[0][ch / V].e[ch % V]};
+                Affine t = map(0);
+                if (plain) {
 #pragma unroll
-                for (int q = 1; q < RG; ++q) t = then(t, Affine{sh.A[q][ch / V].e[ch % V], sh.H[q][ch / V].e[ch % V]});
+                    for (int q = 1; q < RG; ++q) t = joined<false>(t, map(q));
+                } else {
+#pragma unroll
+                    for (int q = 1; q < RG; ++q) t = joined<true>(t, map(q));
+                }
                 publish(s.maps + rt * s.width + block + ch, t);
             }
-        } else if (tid < 2 * CB) {
+        } else {
             // one thread per channel: the state that enters the tile, from the state after
             // the previous group and the maps of the group's earlier tiles
-            const int ch = tid - CB;
             const uint32_t *before = s.states + (group - 1) * s.width + block + ch;
             const uint32_t h_bits = group > 0 ? peek(before) : 0;
             const Affine t = join_maps(s.maps + (rt - pos) * s.width + block + ch, s.width, pos, p.err);
@@ -190,39 +203,37 @@ __global__ void __launch_bounds__(FwdShape<V>::THREADS, kFwdCtas) glr_fwd_scan_k
 #pragma unroll
             for (int q = 0; q < RG; ++q) {
                 sh.h[q][ch / V].e[ch % V] = h;
-                h = apply(Affine{sh.A[q][ch / V].e[ch % V], sh.H[q][ch / V].e[ch % V]}, h);
+                h = plain ? applied<false>(map(q), h) : applied<true>(map(q), h);
             }
             if (pos == last) publish(s.states + group * s.width + block + ch, h);
         }
         __syncthreads();
 
-        if (left > 0) {
+        const int cols = D - c;
+        if (cols > 0) {
             const Pack<float, V> start = sh.h[rg][lane];
             float h[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) h[v] = start.e[v];
-            if (p.checkpoints && rg == 0 && !(marked && sh.marks.begins[0] >= 0)) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) p.checkpoints[rt * p.D + c + v] = h[v];
-            }
+            if (p.checkpoints && rg == 0 && !(marked && sh.marks.begins[0] >= 0)) st_cols<float, V, false>(p.checkpoints + rt * p.D + c, h, cols);
             E *out = static_cast<E *>(p.out) + r0 * p.os + c;
-            if (!marked) {
+            if (plain) {
 #pragma unroll
                 for (int r = 0; r < L; ++r, out += p.os) {
-                    fma_n<V>(h, reinterpret_cast<const float (&)[V]>(a[r * V]), h, reinterpret_cast<const float (&)[V]>(b[r * V]));
-                    if (r < left && p.out) st_f<E, V>(out, h);
+                    fma_n<V>(h, a[r], h, b[r]);
+                    if (p.out) st_cols<E, V, WIDE>(out, h, cols);
                 }
             } else {
 #pragma unroll
                 for (int r = 0; r < L; ++r, out += p.os) {
+                    if (r0 + r >= p.rows) break;
 #pragma unroll
-                    for (int v = 0; v < V; ++v) h[v] = apply(Affine{a[r * V + v], b[r * V + v]}, h[v]);
-                    if (r >= left) continue;
-                    if (p.out) st_f<E, V>(out, h);
-                    const int n = sh.marks.ends[rg * L + r];
-                    if (n < 0 || !p.fin) continue;
+                    for (int v = 0; v < V; ++v) h[v] = apply(Affine{a[r][v], b[r][v]}, h[v]);
+                    if (p.out) st_cols<E, V, WIDE>(out, h, cols);
+                    const int n = marked && p.fin ? sh.marks.ends[rg * L + r] : -1;
 #pragma unroll
-                    for (int v = 0; v < V; ++v) st_state(p.fin, p.state_type, n * p.D + c + v, h[v]);
+                    for (int v = 0; v < V; ++v)
+                        if (n >= 0 && v < cols) st_state(p.fin, p.state_type, n * p.D + c + v, h[v]);
                 }
             }
         }
@@ -235,7 +246,7 @@ constexpr int64_t kStepMaxT = 16;
 
 bool step_takes(const GlrParams &p) { return !p.cu_seqlens && p.T <= kStepMaxT; }
 
-// 4 channels per thread where every row of x, i, g and out allows loads of 4 elements.
+// Whether every row of x, i, g and out allows loads of 4 elements.
 bool vector_rows(const GlrParams &p) {
     const size_t n = 4 * dtype_bytes(p.dtype);
     const void *ptrs[] = {p.x, p.i, p.g, p.out};
@@ -244,25 +255,26 @@ bool vector_rows(const GlrParams &p) {
     return p.D % 4 == 0 && p.xs % 4 == 0 && p.is % 4 == 0 && p.gs % 4 == 0 && (!p.out || p.os % 4 == 0);
 }
 
-template <typename E, int V, bool UB>
+template <typename E, bool WIDE, bool UB>
 cudaError_t run(const GlrParams &p, unsigned char *ws, int sms, cudaStream_t stream) {
     if (step_takes(p)) {
+        constexpr int V = WIDE ? 4 : 1;
         glr_fwd_step_kernel<E, V, UB><<<(unsigned)ceil_div(p.N * (p.D / V), 128), 128, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    ScanPlan s = scan_plan(p.rows, p.D, FwdShape<V>::CB, ws, nullptr);
+    ScanPlan s = scan_plan(p.rows, p.D, FwdShape::CB, ws, nullptr);
     const int64_t fill = s.row_tiles * s.width / 2 + s.width;
     glr_prepare_kernel<UB, false><<<(unsigned)std::min(ceil_div(fill, 256), (int64_t)sms * 4), 256, 0, stream>>>(p, s);
     if (s.row_tiles == 0) return cudaGetLastError();
-    constexpr auto kernel = glr_fwd_scan_kernel<E, V, UB>;
-    constexpr int bytes = (int)sizeof(FwdShared<E, V>);
+    constexpr auto kernel = glr_fwd_scan_kernel<E, WIDE, UB>;
+    constexpr int bytes = (int)sizeof(FwdShared<E>);
     int ctas = 0;
-    const cudaError_t e = resident_ctas<kernel>(FwdShape<V>::THREADS, bytes, ctas);
+    const cudaError_t e = resident_ctas<kernel>(FwdShape::THREADS, bytes, ctas);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)std::min(s.row_tiles * s.blocks, (int64_t)sms * ctas);
     GlrParams arg = p;
     void *args[] = {&arg, &s};
-    return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(FwdShape<V>::THREADS), args, bytes, stream);
+    return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(FwdShape::THREADS), args, bytes, stream);
 }
 
 }  // namespace
@@ -270,15 +282,15 @@ cudaError_t run(const GlrParams &p, unsigned char *ws, int sms, cudaStream_t str
 size_t glr_fwd_scratch_bytes(const GlrParams &p, int) {
     if (step_takes(p)) return 0;
     size_t bytes = 0;
-    scan_plan(p.rows, p.D, vector_rows(p) ? FwdShape<4>::CB : FwdShape<1>::CB, nullptr, &bytes);
+    scan_plan(p.rows, p.D, FwdShape::CB, nullptr, &bytes);
     return bytes;
 }
 
 cudaError_t launch_glr_fwd(const GlrParams &p, unsigned char *ws, int sms, cudaStream_t stream) {
     return with_dtype(p.dtype, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
-        if (vector_rows(p)) return p.unbounded ? run<E, 4, true>(p, ws, sms, stream) : run<E, 4, false>(p, ws, sms, stream);
-        return p.unbounded ? run<E, 1, true>(p, ws, sms, stream) : run<E, 1, false>(p, ws, sms, stream);
+        if (vector_rows(p)) return p.unbounded ? run<E, true, true>(p, ws, sms, stream) : run<E, true, false>(p, ws, sms, stream);
+        return p.unbounded ? run<E, false, true>(p, ws, sms, stream) : run<E, false, false>(p, ws, sms, stream);
     });
 }
 

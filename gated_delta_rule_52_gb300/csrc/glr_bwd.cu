@@ -22,52 +22,49 @@ namespace {
 using namespace layer;
 
 // 16 elements per thread: 4 rows by 4 channels in 16 bits, 8 by 2 in 32 bits (the raw
-// inputs of two tiles in shared memory allow 2 and 3 CTAs per SM), 16 by 1 where rows are
-// not aligned.
-template <typename E, int V> using BwdShape = TileShape<V == 4 ? 256 : 128, V == 1 ? 32 : 16, V>;
+// inputs of two tiles in shared memory allow 2 and 3 CTAs per SM).
+template <typename E> using BwdShape = TileShape<sizeof(E) == 2 ? 256 : 128, 16, sizeof(E) == 2 ? 4 : 2>;
 
-template <typename E, int V>
+template <typename E>
 struct BwdShared {
-    using S = BwdShape<E, V>;
-    Pack<E, V> raw[2][4][S::L][S::THREADS];                  // x, i, g, dout
-    Pack<GateConst, V> gates[2][S::THREADS];
-    Pack<float, V> A[S::RG][S::CL], H[S::RG][S::CL];         // forward maps of the row groups
-    Pack<float, V> B[S::RG][S::CL], F[S::RG][S::CL];         // backward maps
-    Pack<float, V> h[S::RG][S::CL], f[S::RG][S::CL];         // states that enter them
-    Pack<float, V> sum_ddt[S::RG][S::CL], sum_dA[S::RG][S::CL];
+    using S = BwdShape<E>;
+    Pack<E, S::V> raw[2][4][S::L][S::THREADS];                     // x, i, g, dout
+    Pack<GateConst, S::V> gates[2][S::THREADS];
+    Pack<float, S::V> A[S::RG][S::CL], H[S::RG][S::CL];            // forward maps of the row groups
+    Pack<float, S::V> B[S::RG][S::CL], F[S::RG][S::CL];            // backward maps
+    // states that enter them, and over each thread's own two its sums of parameter gradients
+    Pack<float, S::V> h[S::RG][S::CL], f[S::RG][S::CL];
     TileMarks marks;
 };
 
-template <typename E, int V, bool UB>
-__global__ void __launch_bounds__(BwdShape<E, V>::THREADS, V == 4 ? 2 : 3)
+template <typename E, bool WIDE, bool UB>
+__global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
     glr_bwd_scan_kernel(GlrParams p, ScanPlan s, float *part_ddt, float *part_dA) {
-    using namespace sm103;
-    using S = BwdShape<E, V>;
-    constexpr int CL = S::CL, L = S::L, CB = S::CB, RG = S::RG;
+    using S = BwdShape<E>;
+    constexpr int CL = S::CL, V = S::V, L = S::L, CB = S::CB, RG = S::RG;
+    constexpr bool EXACT = sizeof(E) == 4;
     static_assert(S::THREADS >= 3 * CB && L * V == 16, "roles");
     extern __shared__ __align__(16) unsigned char smem[];
-    BwdShared<E, V> &sh = *reinterpret_cast<BwdShared<E, V> *>(smem);
+    BwdShared<E> &sh = *reinterpret_cast<BwdShared<E> *>(smem);
     const int tid = threadIdx.x, lane = tid % CL, rg = tid / CL;
-    const int role = tid / CB, ch = tid % CB;
+    const int role = tid / CB, ch = tid % CB, D = (int)p.D;
     const float lb2 = p.lower_bound * kLog2e;
     float checkpoint = 0.f;   // of role 2's channel, fetched with the tile
 
     // tile number w.rt counts from the last row tile
-    auto fetch = [&](const TileWalk &w, int stage) {
+    const auto fetch = [&](const TileWalk &w, int stage) {
         int first = 0;
         if (w.rt < s.row_tiles) {
             const int64_t rt = s.row_tiles - 1 - w.rt, r0 = rt * kTileRows + rg * L;
             const int c = w.cb * CB + lane * V;
             first = s.first_seq[rt];
-            const float *gate = reinterpret_cast<const float *>(s.gates + c);
-            copy_async<float, V == 4 ? 4 : 2 * V>(&sh.gates[stage][tid], gate);
-            if (V == 4) copy_async<float, 4>(&sh.gates[stage][tid].e[V / 2], gate + 4);
-            if (role == 2 && w.cb * CB + ch < p.D) checkpoint = p.checkpoints[rt * p.D + w.cb * CB + ch];
-            if (c < p.D) {
+            copy_gates<V>(&sh.gates[stage][tid], s.gates + c);
+            if (role == 2 && w.cb * CB + ch < D) checkpoint = p.checkpoints[rt * p.D + w.cb * CB + ch];
+            if (c < D) {
                 const int left = (int)min(p.rows - r0, (int64_t)L);
                 const auto copy = [&](int k, const void *src, int64_t stride) {
-                    copy_rows<E, V, L, S::THREADS>(&sh.raw[stage][k][0][tid], static_cast<const E *>(src) + r0 * stride + c,
-                                                   stride, left);
+                    copy_rows<E, V, WIDE, L, S::THREADS>(&sh.raw[stage][k][0][tid], static_cast<const E *>(src) + r0 * stride + c,
+                                                         stride, left, D - c);
                 };
                 copy(0, p.x, p.xs);
                 copy(1, p.i, p.is);
@@ -83,65 +80,61 @@ __global__ void __launch_bounds__(BwdShape<E, V>::THREADS, V == 4 ? 2 : 3)
     int next_first = fetch(w, 0);
     for (int stage = 0; w.rt < s.row_tiles; stage ^= 1) {
         const int64_t walk = w.rt, rt = s.row_tiles - 1 - walk, r0 = rt * kTileRows + rg * L;
-        const int c = w.cb * CB + lane * V, block = w.cb * CB, first = next_first;
+        const int c = w.cb * CB + lane * V, block = w.cb * CB, cols = D - c, first = next_first;
         const float h_tile = checkpoint;
         w.next();
         next_first = fetch(w, stage ^ 1);
         const bool marked = mark_tile(p, rt, first, sh.marks);
+        const bool plain = !marked && (rt + 1) * kTileRows <= p.rows;        // every row inside one sequence
+        const int left = cols > 0 ? (int)min(p.rows - r0, (int64_t)L) : 0;   // rows of this thread that exist
         copies_wait<1>();   // this thread's own copies: no barrier needed
 
-        const int left = c < p.D ? (int)min(p.rows - r0, (int64_t)L) : 0;   // rows of this thread that exist
-        const ChunkGates<V> gc(sh.gates[stage][tid]);
-        const auto raw = [&](int k) { return &sh.raw[stage][k][0][tid]; };
-        constexpr int n = kGateWidth<V>;
-        float a[L][V], mg[L][V], mi[L][V];   // kept for the second half
+        const ChannelGates<V> gc(sh.gates[stage][tid]);
+        const auto raw = [&](int k, int r, float (&f)[V]) { unpack<E, V>(sh.raw[stage][k][r][tid], f); };
+        float a[L][V], kept_g[L][V], kept_i[L][V];   // for the second half
         Pack<float, V> mA, mH, mB, mF;
 #pragma unroll
         for (int v = 0; v < V; ++v) mA.e[v] = mB.e[v] = 1.f, mH.e[v] = mF.e[v] = 0.f;
+        if (plain) {
 #pragma unroll
-        for (int e = 0; e < L * V; e += n) {
-            float x[n], i[n], g[n], d[n], ac[n], s[n], mgc[n], mic[n];
-            ld_chunk<E, V, S::THREADS>(raw(0), e, x);
-            ld_chunk<E, V, S::THREADS>(raw(1), e, i);
-            ld_chunk<E, V, S::THREADS>(raw(2), e, g);
-            ld_chunk<E, V, S::THREADS>(raw(3), e, d);
-            token_gates_n<UB, n>(ac, s, mgc, mic, g, i, gc.k0, gc.k1, lb2);
-            mul_n<n>(s, s, x);
-#pragma unroll
-            for (int j = 0; j < n; ++j) {
-                const int r = (e + j) / V, v = (e + j) % V;
-                a[r][v] = ac[j], mg[r][v] = mgc[j], mi[r][v] = mic[j];
-            }
-            if (!marked && left == L) {
+            for (int r = 0; r < L; ++r) {
+                float x[V], i[V], g[V], d[V], sx[V];
+                raw(0, r, x), raw(1, r, i), raw(2, r, g), raw(3, r, d);
+                token_gates_n<UB, EXACT, V>(a[r], sx, kept_g[r], kept_i[r], g, i, gc.k0, gc.k1, lb2);
+                mul_n<V>(sx, sx, x);
                 // forward: after the rows before; backward: f = a_0 (dout_0 + a_1 (dout_1 + ...))
+                fma_n<V>(mH.e, a[r], mH.e, sx);
+                mul_n<V>(mA.e, a[r], mA.e);
+                fma_n<V>(mF.e, mA.e, d, mF.e);
+            }
+            mB = mA;
+        } else {
+#pragma unroll 1
+            for (int r = 0; r < left; ++r) {
+                float x[V], i[V], g[V], d[V], sx[V], ar[V], kg[V], ki[V];
+                raw(0, r, x), raw(1, r, i), raw(2, r, g), raw(3, r, d);
+                token_gates_n<UB, EXACT, V>(ar, sx, kg, ki, g, i, gc.k0, gc.k1, lb2);
+                mul_n<V>(sx, sx, x);
+                const int begins = marked ? sh.marks.begins[rg * L + r] : -1, ends = marked ? sh.marks.ends[rg * L + r] : -1;
 #pragma unroll
-                for (int j = 0; j < n; j += V) {
-                    const auto &ar = reinterpret_cast<const float (&)[V]>(ac[j]);
-                    fma_n<V>(mH.e, ar, mH.e, reinterpret_cast<const float (&)[V]>(s[j]));
-                    mul_n<V>(mA.e, ar, mA.e);
-                    fma_n<V>(mF.e, mA.e, reinterpret_cast<const float (&)[V]>(d[j]), mF.e);
-                }
-            } else {
+                for (int v = 0; v < V; ++v) {
 #pragma unroll
-                for (int j = 0; j < n; ++j) {
-                    const int r = (e + j) / V, v = (e + j) % V;
-                    if (r >= left) continue;
-                    const int begins = marked ? sh.marks.begins[rg * L + r] : -1, ends = marked ? sh.marks.ends[rg * L + r] : -1;
+                    for (int k = 0; k < L; ++k)
+                        if (k == r) a[k][v] = ar[v], kept_g[k][v] = kg[v], kept_i[k][v] = ki[v];
                     if (begins >= 0) {
-                        const float h0 = p.init ? ld_state(p.init, p.state_type, begins * p.D + c + v) : 0.f;
-                        mA.e[v] = -0.f, mH.e[v] = fmaf(ac[j], h0, s[j]);
+                        const float h0 = p.init && v < cols ? ld_state(p.init, p.state_type, begins * p.D + c + v) : 0.f;
+                        mA.e[v] = -0.f, mH.e[v] = fmaf(ar[v], h0, sx[v]);
                     } else {
-                        mH.e[v] = fmaf(ac[j], mH.e[v], s[j]);
-                        mA.e[v] *= ac[j];
+                        mH.e[v] = fmaf(ar[v], mH.e[v], sx[v]);
+                        mA.e[v] *= ar[v];
                     }
                     // backward map of rows 0 .. r: the earlier rows' map after this row's
-                    const float dt = ends >= 0 && p.dfinal ? d[j] + p.dfinal[ends * p.D + c + v] : d[j];
-                    const Affine m = then(Affine{ends >= 0 ? -0.f : ac[j], ac[j] * dt}, Affine{mB.e[v], mF.e[v]});
+                    const float dt = ends >= 0 && p.dfinal && v < cols ? d[v] + p.dfinal[ends * p.D + c + v] : d[v];
+                    const Affine m = then(Affine{ends >= 0 ? -0.f : ar[v], ar[v] * dt}, Affine{mB.e[v], mF.e[v]});
                     mB.e[v] = m.A, mF.e[v] = m.H;
                 }
             }
         }
-        if (!marked && left == L) mB = mA;
         sh.A[rg][lane] = mA;
         sh.H[rg][lane] = mH;
         sh.B[rg][lane] = mB;
@@ -151,12 +144,18 @@ __global__ void __launch_bounds__(BwdShape<E, V>::THREADS, V == 4 ? 2 : 3)
         const int64_t group = walk >> s.group_log2;
         const int pos = (int)(walk - (group << s.group_log2)), last = (1 << s.group_log2) - 1;
         const auto back = [&](int q) { return Affine{sh.B[q][ch / V].e[ch % V], sh.F[q][ch / V].e[ch % V]}; };
+        const auto ahead = [&](int q) { return Affine{sh.A[q][ch / V].e[ch % V], sh.H[q][ch / V].e[ch % V]}; };
         if (role == 0) {
             // the tile's backward map, handed on
             if (pos != last) {
                 Affine t = back(RG - 1);
+                if (plain) {
 #pragma unroll
-                for (int q = RG - 2; q >= 0; --q) t = then(t, back(q));
+                    for (int q = RG - 2; q >= 0; --q) t = joined<false>(t, back(q));
+                } else {
+#pragma unroll
+                    for (int q = RG - 2; q >= 0; --q) t = joined<true>(t, back(q));
+                }
                 publish(s.maps + walk * s.width + block + ch, t);
             }
         } else if (role == 1) {
@@ -168,7 +167,7 @@ __global__ void __launch_bounds__(BwdShape<E, V>::THREADS, V == 4 ? 2 : 3)
 #pragma unroll
             for (int q = RG - 1; q >= 0; --q) {
                 sh.f[q][ch / V].e[ch % V] = f;
-                f = apply(back(q), f);
+                f = plain ? applied<false>(back(q), f) : applied<true>(back(q), f);
             }
             if (pos == last) publish(s.states + group * s.width + block + ch, f);
         } else if (role == 2) {
@@ -177,7 +176,7 @@ __global__ void __launch_bounds__(BwdShape<E, V>::THREADS, V == 4 ? 2 : 3)
 #pragma unroll
             for (int q = 0; q < RG; ++q) {
                 sh.h[q][ch / V].e[ch % V] = h;
-                h = apply(Affine{sh.A[q][ch / V].e[ch % V], sh.H[q][ch / V].e[ch % V]}, h);
+                h = plain ? applied<false>(ahead(q), h) : applied<true>(ahead(q), h);
             }
         }
         __syncthreads();
@@ -185,74 +184,83 @@ __global__ void __launch_bounds__(BwdShape<E, V>::THREADS, V == 4 ? 2 : 3)
         Pack<float, V> ddt, dA;
 #pragma unroll
         for (int v = 0; v < V; ++v) ddt.e[v] = dA.e[v] = 0.f;
-        if (left > 0) {
-            float start[L][V], h[V], f[V];   // the states that the rows start from
-            const Pack<float, V> h_in = sh.h[rg][lane], f_in = sh.f[rg][lane];
-            const auto &k0 = reinterpret_cast<const float (&)[V]>(gc.k0), &k1 = reinterpret_cast<const float (&)[V]>(gc.k1);
+        float h[V], f[V];
+        const Pack<float, V> h_in = sh.h[rg][lane], f_in = sh.f[rg][lane];
 #pragma unroll
-            for (int v = 0; v < V; ++v) h[v] = h_in.e[v], f[v] = f_in.e[v];
+        for (int v = 0; v < V; ++v) h[v] = h_in.e[v], f[v] = f_in.e[v];
+        const int64_t row_at = r0 * p.D + c;
+        // the state after a row from the one before it
+        const auto advance = [&](int r, const float (&ar)[V], const float (&ki)[V]) {
+            float x[V], i[V], si[V], o[V];
+            raw(0, r, x);
+            if (EXACT) raw(1, r, i);
+            input_gates_n<EXACT, V>(si, o, i, ki);
+            mul_n<V>(si, si, x);
+            fma_n<V>(h, ar, h, si);
+        };
+        // the gradients of a row from its state `start` and what comes from behind
+        const auto row = [&](int r, const float (&ar)[V], const float (&kg)[V], const float (&ki)[V], const float (&start)[V]) {
+            float x[V], i[V], g[V], grad[V], si[V], o[V], out[V], slope[V], rate[V];
+            raw(0, r, x), raw(2, r, g), raw(3, r, grad);
+            if (EXACT) raw(1, r, i);
+            add_n<V>(grad, grad, f);
+            mul_n<V>(f, ar, grad);
+            input_gates_n<EXACT, V>(si, o, i, ki);
+            mul_n<V>(out, grad, si);
+            st_cols<E, V, WIDE>(static_cast<E *>(p.dx) + row_at + r * p.D, out, cols);
+            mul_n<V>(out, out, o);
+            mul_n<V>(out, out, x);
+            st_cols<E, V, WIDE>(static_cast<E *>(p.di) + row_at + r * p.D, out, cols);
+            gate_slopes_n<UB, V>(slope, rate, g, kg, gc.k0, gc.k1, p.lower_bound);
+            mul_n<V>(o, f, start);        // the gradient of gk
+            mul_n<V>(out, o, slope);
+            st_cols<E, V, WIDE>(static_cast<E *>(p.dg) + row_at + r * p.D, out, cols);
+            add_n<V>(ddt.e, ddt.e, out);
+            fma_n<V>(dA.e, o, rate, dA.e);
+        };
+        if (plain) {
+            if (cols > 0) {
+                float start[L][V];   // the states that the rows start from
+#pragma unroll
+                for (int r = 0; r < L; ++r) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) start[r][v] = h[v];
+                    if (r < L - 1) advance(r, a[r], kept_i[r]);
+                }
+#pragma unroll
+                for (int r = L - 1; r >= 0; --r) row(r, a[r], kept_g[r], kept_i[r], start[r]);
+            }
+        } else {
+            float start[L][V];
 #pragma unroll
             for (int r = 0; r < L; ++r) {
-                if (marked && r < left && sh.marks.begins[rg * L + r] >= 0) {
+                if (r >= left) break;
+                const int begins = marked ? sh.marks.begins[rg * L + r] : -1;
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        h[v] = p.init ? ld_state(p.init, p.state_type, sh.marks.begins[rg * L + r] * p.D + c + v) : 0.f;
+                for (int v = 0; v < V; ++v) {
+                    if (begins >= 0) h[v] = p.init && v < cols ? ld_state(p.init, p.state_type, begins * p.D + c + v) : 0.f;
+                    start[r][v] = h[v];
                 }
-#pragma unroll
-                for (int v = 0; v < V; ++v) start[r][v] = h[v];
-                if (r == L - 1) break;
-                float x[V], i[V], s[V];
-                unpack<E, V>(*(raw(0) + r * S::THREADS), x);
-                unpack<E, V>(*(raw(1) + r * S::THREADS), i);
-                fma_n<V>(s, mi[r], -1.f, 1.f);
-#pragma unroll
-                for (int v = 0; v < V; ++v) s[v] = i[v] >= 0.f ? s[v] : mi[r][v];
-                mul_n<V>(s, s, x);
-                fma_n<V>(h, a[r], h, s);
+                advance(r, a[r], kept_i[r]);
             }
-            const int64_t row_at = (r0 + L - 1) * p.D + c;
-            E *dx = static_cast<E *>(p.dx) + row_at, *di = static_cast<E *>(p.di) + row_at, *dg = static_cast<E *>(p.dg) + row_at;
 #pragma unroll
-            for (int r = L - 1; r >= 0; --r, dx -= p.D, di -= p.D, dg -= p.D) {
+            for (int r = L - 1; r >= 0; --r) {
                 if (r >= left) continue;
-                if (marked && sh.marks.ends[rg * L + r] >= 0) {
+                const int ends = marked ? sh.marks.ends[rg * L + r] : -1, begins = marked ? sh.marks.begins[rg * L + r] : -1;
 #pragma unroll
-                    for (int v = 0; v < V; ++v) f[v] = p.dfinal ? p.dfinal[sh.marks.ends[rg * L + r] * p.D + c + v] : 0.f;
-                }
-                float x[V], i[V], g[V], grad[V], gm[V], go[V], o[V], slope[V], rate[V];
-                unpack<E, V>(*(raw(0) + r * S::THREADS), x);
-                unpack<E, V>(*(raw(1) + r * S::THREADS), i);
-                unpack<E, V>(*(raw(2) + r * S::THREADS), g);
-                unpack<E, V>(*(raw(3) + r * S::THREADS), grad);
-                add_n<V>(grad, grad, f);
-                mul_n<V>(f, a[r], grad);
-                if (marked && p.dinit && sh.marks.begins[rg * L + r] >= 0) {
+                for (int v = 0; v < V; ++v)
+                    if (ends >= 0) f[v] = p.dfinal && v < cols ? p.dfinal[ends * p.D + c + v] : 0.f;
+                row(r, a[r], kept_g[r], kept_i[r], start[r]);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) p.dinit[sh.marks.begins[rg * L + r] * p.D + c + v] = f[v];
-                }
-                fma_n<V>(o, mi[r], -1.f, 1.f);
-                mul_n<V>(gm, grad, mi[r]);
-                mul_n<V>(go, grad, o);
-                float out[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) out[v] = i[v] >= 0.f ? go[v] : gm[v];
-                st_f<E, V>(dx, out);
-                mul_n<V>(out, gm, o);
-                mul_n<V>(out, out, x);
-                st_f<E, V>(di, out);
-                gate_slopes_n<UB, V>(slope, rate, g, mg[r], k0, k1, p.lower_bound);
-                mul_n<V>(o, f, start[r]);        // the gradient of gk
-                mul_n<V>(out, o, slope);
-                st_f<E, V>(dg, out);
-                add_n<V>(ddt.e, ddt.e, out);
-                fma_n<V>(dA.e, o, rate, dA.e);
+                for (int v = 0; v < V; ++v)
+                    if (begins >= 0 && p.dinit && v < cols) p.dinit[begins * p.D + c + v] = f[v];
             }
         }
-        sh.sum_ddt[rg][lane] = ddt;
-        sh.sum_dA[rg][lane] = dA;
+        sh.h[rg][lane] = ddt;
+        sh.f[rg][lane] = dA;
         __syncthreads();
         if (role < 2) {
-            const auto &sum = role == 0 ? sh.sum_ddt : sh.sum_dA;
+            const auto &sum = role == 0 ? sh.h : sh.f;
             float t = 0.f;
 #pragma unroll
             for (int q = 0; q < RG; ++q) t += sum[q][ch / V].e[ch % V];
@@ -293,7 +301,7 @@ GlrParams states_only(const GlrParams &p) {
     return f;
 }
 
-// V channels per thread where every row of the inputs and gradients allows it.
+// Whether every row of the inputs and gradients allows loads of a thread's V elements.
 bool vector_rows(const GlrParams &p) {
     const size_t V = p.dtype == kFP32 ? 2 : 4, n = V * dtype_bytes(p.dtype);
     const void *ptrs[] = {p.x, p.i, p.g, p.dout, p.dx, p.di, p.dg};
@@ -301,7 +309,7 @@ bool vector_rows(const GlrParams &p) {
         if (reinterpret_cast<uintptr_t>(q) % n) return false;
     return p.D % V == 0 && p.xs % V == 0 && p.is % V == 0 && p.gs % V == 0 && p.ds % V == 0;
 }
-int block_channels(const GlrParams &p) { return vector_rows(p) && p.dtype != kFP32 ? 64 : 32; }
+int block_channels(const GlrParams &p) { return p.dtype == kFP32 ? BwdShape<float>::CB : BwdShape<__half>::CB; }
 
 // Workspace: the scan's, the partial sums, the checkpoints and the forward run's workspace.
 struct BwdPlan {
@@ -324,22 +332,22 @@ BwdPlan bwd_plan(const GlrParams &p, int sms, unsigned char *ws) {
     return b;
 }
 
-template <typename E, int V, bool UB>
+template <typename E, bool WIDE, bool UB>
 cudaError_t run(const GlrParams &p, const BwdPlan &b, int sms, cudaStream_t stream) {
     ScanPlan s = b.s;
     const int64_t fill = s.row_tiles * s.width / 2 + s.width;
     glr_prepare_kernel<UB, true><<<(unsigned)std::min(ceil_div(fill, 256), (int64_t)sms * 4), 256, 0, stream>>>(p, s);
     if (s.row_tiles == 0) return cudaGetLastError();
     int ctas = 0;
-    constexpr int bytes = (int)sizeof(BwdShared<E, V>);
-    constexpr auto kernel = glr_bwd_scan_kernel<E, V, UB>;
-    const cudaError_t e = resident_ctas<kernel>(BwdShape<E, V>::THREADS, bytes, ctas);
+    constexpr int bytes = (int)sizeof(BwdShared<E>);
+    constexpr auto kernel = glr_bwd_scan_kernel<E, WIDE, UB>;
+    const cudaError_t e = resident_ctas<kernel>(BwdShape<E>::THREADS, bytes, ctas);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)std::min(s.row_tiles * s.blocks, (int64_t)sms * ctas);
     GlrParams arg = p;
     float *ddt = b.part_ddt, *dA = b.part_dA;
     void *args[] = {&arg, &s, &ddt, &dA};
-    return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(BwdShape<E, V>::THREADS), args,
+    return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(BwdShape<E>::THREADS), args,
                                        bytes, stream);
 }
 
@@ -360,9 +368,8 @@ cudaError_t launch_glr_bwd(const GlrParams &p0, unsigned char *ws, int sms, cuda
         const bool vec = vector_rows(p);
         e = with_dtype(p.dtype, [&](auto *tag) {
             using E = std::remove_pointer_t<decltype(tag)>;
-            constexpr int V = sizeof(E) == 4 ? 2 : 4;
-            if (vec) return p.unbounded ? run<E, V, true>(p, b, sms, stream) : run<E, V, false>(p, b, sms, stream);
-            return p.unbounded ? run<E, 1, true>(p, b, sms, stream) : run<E, 1, false>(p, b, sms, stream);
+            if (vec) return p.unbounded ? run<E, true, true>(p, b, sms, stream) : run<E, true, false>(p, b, sms, stream);
+            return p.unbounded ? run<E, false, true>(p, b, sms, stream) : run<E, false, false>(p, b, sms, stream);
         });
         if (e != cudaSuccess) return e;
     }

@@ -89,23 +89,32 @@ __device__ __forceinline__ void gate_decay_n(float (&a)[n], const float (&g)[n],
     exp2_decay_n<n>(a, x);
 }
 
-// The same and sigma(i) of n tokens or channels, with what their derivatives are formed
-// from later: mg and mi, the smaller of sigma(v) and sigma(-v) for the gate's argument and
-// for i.  The smaller one is exact relative to itself, and with it both sigma and its slope
-// m (1 - m).
-template <bool UB, int n>
-__device__ __forceinline__ void token_gates_n(float (&a)[n], float (&s)[n], float (&mg)[n], float (&mi)[n], const float (&g)[n],
-                                              const float (&i)[n], const float (&k0)[n], const float (&k1)[n], float lb2) {
+// The same and sigma(i) of n tokens or channels, with two values each that their derivatives
+// are formed from later, kept_g and kept_i.  EXACT (tensors in 32 bits): the smaller of
+// sigma(v) and sigma(-v), which is exact relative to itself, and with it sigma and its slope
+// m (1 - m) at any v.  Else (tensors in 16 bits): sigma(v) itself; 1 - sigma is then off by
+// 2^-24, below the rounding of a 16-bit gradient while 1 - sigma is above 2^-13.  (The gate
+// without a lower bound keeps the smaller one in either case: its softplus needs it.)
+template <bool UB, bool EXACT, int n>
+__device__ __forceinline__ void token_gates_n(float (&a)[n], float (&s)[n], float (&kept_g)[n], float (&kept_i)[n],
+                                              const float (&g)[n], const float (&i)[n], const float (&k0)[n],
+                                              const float (&k1)[n], float lb2) {
     float t[n], d[n], o[n], u[n], x[n];
+    if (EXACT) {
 #pragma unroll
-    for (int j = 0; j < n; ++j) t[j] = ex2(-kLog2e * fabsf(i[j]));
-    fma_n<n>(d, t, 1.f, 1.f);
+        for (int j = 0; j < n; ++j) t[j] = ex2(-kLog2e * fabsf(i[j]));
+        fma_n<n>(d, t, 1.f, 1.f);
 #pragma unroll
-    for (int j = 0; j < n; ++j) d[j] = rcp(d[j]);
-    mul_n<n>(mi, t, d);
-    fma_n<n>(o, mi, -1.f, 1.f);
+        for (int j = 0; j < n; ++j) d[j] = rcp(d[j]);
+        mul_n<n>(kept_i, t, d);
+        fma_n<n>(o, kept_i, -1.f, 1.f);
 #pragma unroll
-    for (int j = 0; j < n; ++j) s[j] = i[j] >= 0.f ? o[j] : mi[j];
+        for (int j = 0; j < n; ++j) s[j] = i[j] >= 0.f ? o[j] : kept_i[j];
+    } else {
+        sigmoid_n<n>(s, i);
+#pragma unroll
+        for (int j = 0; j < n; ++j) kept_i[j] = s[j];
+    }
     if (UB) {
         float q[n], z[n];
 #pragma unroll
@@ -119,7 +128,7 @@ __device__ __forceinline__ void token_gates_n(float (&a)[n], float (&s)[n], floa
 #pragma unroll
         for (int j = 0; j < n; ++j) x[j] = rcp(x[j]);   // both reciprocals
         mul_n<n>(x, t, x);
-        mul_n<n>(mg, x, o);                             // t / (1 + t)
+        mul_n<n>(kept_g, x, o);                         // t / (1 + t)
         mul_n<n>(d, x, d);                              // t / (2 + t)
         mul_n<n>(z, d, d);
         atanh_poly_n<n>(q, z);
@@ -127,39 +136,58 @@ __device__ __forceinline__ void token_gates_n(float (&a)[n], float (&s)[n], floa
         mul_n<n>(x, k0, x);
     } else {
         fma_n<n>(u, k0, g, k1);                         // -log2(e) z
+        if (EXACT) {
 #pragma unroll
-        for (int j = 0; j < n; ++j) t[j] = ex2(-fabsf(u[j]));
-        fma_n<n>(d, t, 1.f, 1.f);
+            for (int j = 0; j < n; ++j) t[j] = ex2(-fabsf(u[j]));
+            fma_n<n>(d, t, 1.f, 1.f);
 #pragma unroll
-        for (int j = 0; j < n; ++j) d[j] = rcp(d[j]);
-        mul_n<n>(mg, t, d);
-        fma_n<n>(o, mg, -1.f, 1.f);
+            for (int j = 0; j < n; ++j) d[j] = rcp(d[j]);
+            mul_n<n>(kept_g, t, d);
+            fma_n<n>(o, kept_g, -1.f, 1.f);
 #pragma unroll
-        for (int j = 0; j < n; ++j) x[j] = u[j] <= 0.f ? o[j] : mg[j];
+            for (int j = 0; j < n; ++j) x[j] = u[j] <= 0.f ? o[j] : kept_g[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < n; ++j) t[j] = ex2(u[j]);
+            fma_n<n>(d, t, 1.f, 1.f);
+#pragma unroll
+            for (int j = 0; j < n; ++j) x[j] = kept_g[j] = rcp(d[j]);
+        }
         fma_n<n>(x, x, lb2, 0.f);
     }
     exp2_decay_n<n>(a, x);
 }
 
-// slope = d gk / d g and rate = d gk / d A_log from the kept mg.
+// sigma(i), sigma(-i) from kept_i.
+template <bool EXACT, int n>
+__device__ __forceinline__ void input_gates_n(float (&s)[n], float (&o)[n], const float (&i)[n], const float (&kept)[n]) {
+    fma_n<n>(o, kept, -1.f, 1.f);
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+        const float m = kept[j], r = o[j];
+        s[j] = !EXACT || i[j] < 0.f ? m : r;
+        o[j] = !EXACT || i[j] < 0.f ? r : m;
+    }
+}
+// slope = d gk / d g and rate = d gk / d A_log from kept_g.
 template <bool UB, int n>
-__device__ __forceinline__ void gate_slopes_n(float (&slope)[n], float (&rate)[n], const float (&g)[n], const float (&mg)[n],
+__device__ __forceinline__ void gate_slopes_n(float (&slope)[n], float (&rate)[n], const float (&g)[n], const float (&kept)[n],
                                               const float (&k0)[n], const float (&k1)[n], float lb) {
     float u[n];
     if (UB) {
-        // softplus once more: log(1 + t) = -log(1 - mg) = 2 atanh(mg / (2 - mg))
+        // softplus once more: log(1 + t) = -log(1 - m) = 2 atanh(m / (2 - m))
         float o[n], s[n], z[n], q[n];
 #pragma unroll
         for (int j = 0; j < n; ++j) z[j] = kLog2e;
         fma_n<n>(u, z, g, k1);
-        fma_n<n>(o, mg, -1.f, 1.f);
+        fma_n<n>(o, kept, -1.f, 1.f);
 #pragma unroll
-        for (int j = 0; j < n; ++j) o[j] = u[j] >= 0.f ? o[j] : mg[j], u[j] = fmaxf(u[j], 0.f);
+        for (int j = 0; j < n; ++j) o[j] = u[j] >= 0.f ? o[j] : kept[j], u[j] = fmaxf(u[j], 0.f);
         mul_n<n>(slope, k0, o);
-        fma_n<n>(s, mg, -1.f, 2.f);
+        fma_n<n>(s, kept, -1.f, 2.f);
 #pragma unroll
         for (int j = 0; j < n; ++j) s[j] = rcp(s[j]);
-        mul_n<n>(s, mg, s);
+        mul_n<n>(s, kept, s);
         mul_n<n>(z, s, s);
         atanh_poly_n<n>(q, z);
         fma_n<n>(u, s, q, u);
@@ -169,13 +197,13 @@ __device__ __forceinline__ void gate_slopes_n(float (&slope)[n], float (&rate)[n
     } else {
         float l[n], o[n];
         fma_n<n>(u, k0, g, k1);
-        fma_n<n>(o, mg, -1.f, 1.f);
-        mul_n<n>(l, mg, o);
+        fma_n<n>(o, kept, -1.f, 1.f);
+        mul_n<n>(l, kept, o);
         fma_n<n>(l, l, -kLn2 * lb, 0.f);                                    // -ln 2 lb sigma'
         mul_n<n>(slope, l, k0);
         mul_n<n>(rate, l, u);
 #pragma unroll
-        for (int j = 0; j < n; ++j) rate[j] = mg[j] == 0.f ? 0.f : rate[j];  // so is a slope of 0 times an infinite argument
+        for (int j = 0; j < n; ++j) rate[j] = l[j] == 0.f ? 0.f : rate[j];  // so is a slope of 0 times an infinite argument
     }
 }
 

@@ -83,29 +83,6 @@ struct TileShape {
     static_assert(RG * L == kTileRows && THREADS >= 2 * CB && CB % 32 == 0, "tile shape");
 };
 
-// Gates are formed for this many elements at a time: a row's V, or two rows where V is 1.
-template <int V> constexpr int kGateWidth = V == 1 ? 2 : V;
-
-// Elements [e, e + n) of a thread's rows, V per row, from its slots in shared memory.
-template <typename E, int V, int THREADS, int n>
-__device__ __forceinline__ void ld_chunk(const Pack<E, V> *slots, int e, float (&f)[n]) {
-    if constexpr (n == V) {
-        unpack<E, V>(slots[e / V * THREADS], f);
-    } else {
-#pragma unroll
-        for (int j = 0; j < n; ++j) f[j] = to_f(slots[(e + j) / V * THREADS].e[(e + j) % V]);
-    }
-}
-// A thread's gate constants as arrays over a chunk.
-template <int V>
-struct ChunkGates {
-    float k0[kGateWidth<V>], k1[kGateWidth<V>];
-    __device__ __forceinline__ ChunkGates(const Pack<GateConst, V> &g) {
-#pragma unroll
-        for (int j = 0; j < kGateWidth<V>; ++j) k0[j] = g.e[j % V].k0, k1[j] = g.e[j % V].k1;
-    }
-};
-
 // Workspace of a scan and its tiles.  Maps [row tile][padded channel], states after a
 // group [group][padded channel], then the first sequence of every row tile.
 struct ScanPlan {
@@ -124,7 +101,7 @@ inline ScanPlan scan_plan(int64_t rows, int64_t D, int channels, unsigned char *
     // The state passes from group to group one at a time, each step about one tile's time
     // on one SM, while the rest of the GPU works off `group` row tiles of `blocks` tiles; a
     // tile joins the maps of half a group on average.
-    for (s.group_log2 = 2; s.group_log2 < 5 && s.blocks << s.group_log2 < 512; ++s.group_log2) {}
+    for (s.group_log2 = 2; s.group_log2 < 5 && s.blocks << s.group_log2 < 256; ++s.group_log2) {}
     s.groups = ceil_div(s.row_tiles, int64_t(1) << s.group_log2);
     s.width = s.blocks * channels;
     s.maps = reinterpret_cast<uint64_t *>(ws);
@@ -147,7 +124,7 @@ __global__ void __launch_bounds__(256) glr_prepare_kernel(GlrParams p, ScanPlan 
     for (int64_t c = at; c < s.width; c += step)
         s.gates[c] = c < p.D ? gate_const<UB>(p.A_log[(unsigned)c / (unsigned)p.K], p.dt_bias[c]) : GateConst{0.f, 0.f};
     for (int64_t t = at; t < s.row_tiles; t += step) {
-        const int64_t r0 = t * kTileRows, n = p.cu_seqlens ? seq_of_row(p.cu_seqlens, p.N, r0) : r0 / p.T;
+        const int64_t r0 = t * kTileRows, n = p.cu_seqlens ? seq_of_row(p.cu_seqlens, p.N, r0) : (unsigned)r0 / (unsigned)p.T;
         int64_t lo, hi;
         seq_rows(p, n, lo, hi);
         s.first_seq[t] = (int)n | (lo < r0 && hi > r0 + kTileRows ? kInside : 0);
@@ -165,6 +142,29 @@ __global__ void __launch_bounds__(256) glr_prepare_kernel(GlrParams p, ScanPlan 
         }
     }
 }
+
+// A thread's gate constants, one array each.
+template <int V>
+struct ChannelGates {
+    float k0[V], k1[V];
+    __device__ __forceinline__ ChannelGates(const Pack<GateConst, V> &g) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) k0[v] = g.e[v].k0, k1[v] = g.e[v].k1;
+    }
+};
+template <int V>
+__device__ __forceinline__ void copy_gates(Pack<GateConst, V> *slot, const GateConst *src) {
+#pragma unroll
+    for (int v = 0; v < V; v += 2) copy_async<16>(&slot->e[v], src + v);
+}
+
+// One map after the other where neither cuts.
+template <bool CUTS>
+__device__ __forceinline__ Affine joined(Affine a, Affine b) {
+    return CUTS ? then(a, b) : Affine{a.A * b.A, fmaf(b.A, a.H, b.H)};
+}
+template <bool CUTS>
+__device__ __forceinline__ float applied(Affine m, float h) { return CUTS ? apply(m, h) : fmaf(m.A, h, m.H); }
 
 // Where sequences begin and end within a tile of rows [r0, r0 + kTileRows): for each row
 // the sequence that it begins (ends), or -1.  Returns false, and writes nothing, where the

@@ -8,10 +8,9 @@
 namespace kda {
 namespace layer {
 
-// Copies V elements (4, 8 or 16 bytes) of one thread.
-template <typename E, int V>
-__device__ __forceinline__ void copy_async(void *slot, const E *src) {
-    constexpr int n = sizeof(E) * V;
+// Copies n bytes (4, 8 or 16) of one thread.
+template <int n>
+__device__ __forceinline__ void copy_async(void *slot, const void *src) {
     static_assert(n == 4 || n == 8 || n == 16, "copy size");
     if constexpr (n == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm103::smem_u32(slot)), "l"(src) : "memory");
@@ -19,22 +18,57 @@ __device__ __forceinline__ void copy_async(void *slot, const E *src) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(sm103::smem_u32(slot)), "l"(src), "n"(n) : "memory");
 }
 // Copies `count` <= N groups of V elements, `stride` elements apart, into slots THREADS
-// groups apart.  Single 2-byte elements have no asynchronous copy: they are loaded
-// together, then stored.
-template <typename E, int V, int N, int THREADS>
-__device__ __forceinline__ void copy_rows(Pack<E, V> *slots, const E *src, int64_t stride, int count) {
-    if constexpr (sizeof(E) * V == 2) {
-        E t[N];
-#pragma unroll
-        for (int r = 0; r < N; ++r)
-            if (r < count) t[r] = src[r * stride];
-#pragma unroll
-        for (int r = 0; r < N; ++r)
-            if (r < count) slots[r * THREADS].e[0] = t[r];
-    } else {
+// groups apart.  WIDE: every group is aligned to its size and whole.  Else its first `cols`
+// elements are copied one by one; 2-byte elements have no asynchronous copy: they are
+// loaded together, then stored.
+template <typename E, int V, bool WIDE, int N, int THREADS>
+__device__ __forceinline__ void copy_rows(Pack<E, V> *slots, const E *src, int64_t stride, int count, int cols) {
+    if constexpr (WIDE) {
 #pragma unroll
         for (int r = 0; r < N; ++r, src += stride)
-            if (r < count) copy_async<E, V>(slots + r * THREADS, src);
+            if (r < count) copy_async<sizeof(E) * V>(slots + r * THREADS, src);
+    } else if constexpr (sizeof(E) == 4) {
+#pragma unroll
+        for (int r = 0; r < N; ++r, src += stride) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (r < count && v < cols) copy_async<4>(&slots[r * THREADS].e[v], src + v);
+        }
+    } else {
+        constexpr int G = 4;   // rows in registers together
+#pragma unroll
+        for (int r0 = 0; r0 < N; r0 += G) {
+            Pack<E, V> t[G];
+#pragma unroll
+            for (int r = 0; r < G; ++r, src += stride) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (r0 + r < count && v < cols) t[r].e[v] = src[v];
+            }
+#pragma unroll
+            for (int r = 0; r < G; ++r)
+                if (r0 + r < count) slots[(r0 + r) * THREADS] = t[r];
+        }
+    }
+}
+// Stores V values, or the first `cols` of them one by one.
+template <typename E, int V, bool WIDE>
+__device__ __forceinline__ void st_cols(E *p, const float (&f)[V], int cols) {
+    if constexpr (WIDE) {
+        st_f<E, V>(p, f);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (v < cols) p[v] = from_f<E>(f[v]);
+    }
+}
+template <typename E, int V, bool WIDE>
+__device__ __forceinline__ void ld_cols(const E *p, float (&f)[V], int cols) {
+    if constexpr (WIDE) {
+        ld_f<E, V>(p, f);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[v] = v < cols ? to_f(p[v]) : 0.f;
     }
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }

@@ -173,14 +173,14 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *p
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
                     if (column<V>(k) < p.D) {
-                        copy_async<E, V>(&slot(stage, 0, k), x + column<V>(k));
-                        copy_async<E, V>(&slot(stage, 1, k), dy + column<V>(k));
+                        copy_async<sizeof(E) * V>(&slot(stage, 0, k), x + column<V>(k));
+                        copy_async<sizeof(E) * V>(&slot(stage, 1, k), dy + column<V>(k));
                     }
                 }
             }
             if ((tid & 31) == 0) {
-                copy_async<float, 1>(&stats[stage][warp].x, p.mean + row);
-                copy_async<float, 1>(&stats[stage][warp].y, p.rstd + row);
+                copy_async<4>(&stats[stage][warp].x, p.mean + row);
+                copy_async<4>(&stats[stage][warp].y, p.rstd + row);
             }
         }
         copies_commit();

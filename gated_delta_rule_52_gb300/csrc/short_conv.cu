@@ -61,11 +61,15 @@ __device__ __forceinline__ bool next_part(const ConvParams &p, Run &r) {
     return true;
 }
 
-// V channels' weights, w[j][v].
-template <int V, int W>
-__device__ __forceinline__ void ld_taps(const float *weight, int64_t c, float (&w)[W][V]) {
+// V channels per thread.  WIDE: every row allows loads of V elements; else they are moved
+// one by one, and a thread's last channels may not exist.
+constexpr int V = 4;
+
+// A thread's weights, w[j][v].
+template <bool WIDE, int W>
+__device__ __forceinline__ void ld_taps(const float *weight, int64_t c, int cols, float (&w)[W][V]) {
     float t[V * W];
-    if constexpr (V == 4) {
+    if constexpr (WIDE) {
 #pragma unroll
         for (int k = 0; k < W; ++k) {
             const float4 f = reinterpret_cast<const float4 *>(weight + c * W)[k];
@@ -73,7 +77,7 @@ __device__ __forceinline__ void ld_taps(const float *weight, int64_t c, float (&
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < V * W; ++k) t[k] = weight[c * W + k];
+        for (int k = 0; k < V * W; ++k) t[k] = k < cols * W ? weight[c * W + k] : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < W; ++j)
@@ -82,13 +86,13 @@ __device__ __forceinline__ void ld_taps(const float *weight, int64_t c, float (&
 }
 
 // Input row t of sequence n that begins at lo, counting the initial state's rows.
-template <typename E, int V>
-__device__ __forceinline__ void ld_x(const ConvParams &p, int64_t n, int64_t lo, int64_t t, int64_t c, float (&f)[V]) {
+template <typename E, int V, bool WIDE>
+__device__ __forceinline__ void ld_x(const ConvParams &p, int64_t n, int64_t lo, int64_t t, int64_t c, int cols, float (&f)[V]) {
     const int64_t j = t - lo + p.W - 1;
     if (t >= lo) {
-        ld_f<E, V>(static_cast<const E *>(p.x) + t * p.xs + c, f);
+        ld_cols<E, V, WIDE>(static_cast<const E *>(p.x) + t * p.xs + c, f, cols);
     } else if (p.init && j >= 0) {
-        ld_f<E, V>(static_cast<const E *>(p.init) + (n * (p.W - 1) + j) * p.D + c, f);
+        ld_cols<E, V, WIDE>(static_cast<const E *>(p.init) + (n * (p.W - 1) + j) * p.D + c, f, cols);
     } else {
 #pragma unroll
         for (int v = 0; v < V; ++v) f[v] = 0.f;
@@ -96,14 +100,14 @@ __device__ __forceinline__ void ld_x(const ConvParams &p, int64_t n, int64_t lo,
 }
 
 // y_t of the window x_{t-(W-1)} .. x_t.
-template <int V, int W>
+template <int W>
 __device__ __forceinline__ void taps_sum(const float (&w)[W][V], const float (&b)[V], const float (&xw)[W][V], float (&y)[V]) {
 #pragma unroll
     for (int v = 0; v < V; ++v) y[v] = b[v];
 #pragma unroll
     for (int j = 0; j < W; ++j) fma_n<V>(y, w[j], xw[j], y);
 }
-template <int V, int W>
+template <int W>
 __device__ __forceinline__ void shift(float (&xw)[W][V]) {
 #pragma unroll
     for (int j = 0; j + 1 < W; ++j)
@@ -113,49 +117,50 @@ __device__ __forceinline__ void shift(float (&xw)[W][V]) {
 
 constexpr int kBatch = 4, kStages = 3;   // rows per copy group, groups of a thread's ring
 
-template <typename E, int V, int W>
+template <typename E, bool WIDE, int W>
 __global__ void __launch_bounds__(kThreads, 3) conv_fwd_kernel(ConvParams p, Runs runs, int channel_blocks) {
     extern __shared__ __align__(16) unsigned char smem[];
     auto &ring = *reinterpret_cast<Pack<E, V>(*)[kStages][kBatch][kThreads]>(smem);
     const int tid = threadIdx.x;
     const int64_t q = (int64_t)(blockIdx.x / channel_blocks) * kGroups + tid / kLanes;
     const int64_t c = ((int64_t)(blockIdx.x % channel_blocks) * kLanes + tid % kLanes) * V;
-    if (q >= runs.count || c >= p.D) return;
+    const int cols = (int)min(p.D - c, (int64_t)V);
+    if (q >= runs.count || cols <= 0) return;
     Run r = run_of(p, runs, q);
     float w[W][V], b[V], xw[W][V];
-    ld_taps<V, W>(p.weight, c, w);
+    ld_taps<WIDE, W>(p.weight, c, cols, w);
 #pragma unroll
-    for (int v = 0; v < V; ++v) b[v] = p.bias ? p.bias[c + v] : 0.f;
+    for (int v = 0; v < V; ++v) b[v] = p.bias && v < cols ? p.bias[c + v] : 0.f;
     do {
         const int own = (int)(r.s1 - r.s0);
         const auto fetch = [&](int j0, int stage) {
-            copy_rows<E, V, kBatch, kThreads>(&ring[stage][0][tid], static_cast<const E *>(p.x) + (r.s0 + j0) * p.xs + c, p.xs, own - j0);
+            copy_rows<E, V, WIDE, kBatch, kThreads>(&ring[stage][0][tid], static_cast<const E *>(p.x) + (r.s0 + j0) * p.xs + c, p.xs, own - j0, cols);
             copies_commit();
         };
 #pragma unroll
         for (int k = 0; k < kStages - 1; ++k) fetch(k * kBatch, k);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) ld_x<E, V>(p, r.n, r.lo, r.s0 - (W - 1) + j, c, xw[j]);
+        for (int j = 0; j < W - 1; ++j) ld_x<E, V, WIDE>(p, r.n, r.lo, r.s0 - (W - 1) + j, c, cols, xw[j]);
         // the final state is the first run's to write: it alone reads the initial state
         if (p.fin && !p.cu_seqlens && r.s0 == r.lo) {
             float last[W - 1][V];
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) ld_x<E, V>(p, r.n, r.lo, r.hi - (W - 1) + j, c, last[j]);
+            for (int j = 0; j < W - 1; ++j) ld_x<E, V, WIDE>(p, r.n, r.lo, r.hi - (W - 1) + j, c, cols, last[j]);
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) st_f<E, V>(static_cast<E *>(p.fin) + (r.n * (W - 1) + j) * p.D + c, last[j]);
+            for (int j = 0; j < W - 1; ++j) st_cols<E, V, WIDE>(static_cast<E *>(p.fin) + (r.n * (W - 1) + j) * p.D + c, last[j], cols);
         }
         E *out = static_cast<E *>(p.out) + r.s0 * p.os + c;
         const auto row = [&](int k, int stage) {
             unpack<E, V>(ring[stage][k][tid], xw[W - 1]);
             float y[V], s[V];
-            taps_sum<V, W>(w, b, xw, y);
+            taps_sum<W>(w, b, xw, y);
             if (p.silu) {
                 sigmoid_n<V>(s, y);
                 mul_n<V>(y, y, s);
             }
-            st_f<E, V>(out, y);
+            st_cols<E, V, WIDE>(out, y, cols);
             out += p.os;
-            shift<V, W>(xw);
+            shift<W>(xw);
         };
         for (int j0 = 0, stage = 0; j0 < own; j0 += kBatch) {
             fetch(j0 + (kStages - 1) * kBatch, stage == 0 ? kStages - 1 : stage - 1);
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) conv_state_kernel(ConvParams p) {
     hi = max(lo, hi);
     for (int j = 0; j < p.W - 1; ++j) {   // row j is read at or after row j: in order is safe in place
         float f[1];
-        ld_x<E, 1>(p, n, lo, hi - (p.W - 1) + j, c, f);
+        ld_x<E, 1, true>(p, n, lo, hi - (p.W - 1) + j, c, 1, f);
         st_f<E, 1>(static_cast<E *>(p.fin) + (n * (p.W - 1) + j) * p.D + c, f);
     }
 }
@@ -195,8 +200,8 @@ __global__ void __launch_bounds__(kThreads) conv_state_kernel(ConvParams p) {
 // input row t, or of a row of the initial state where t comes before the sequence.  So a
 // part [s0, s1) of a run walks u from s0 to s1 + W-2; rows from s1 on add to no parameter,
 // and rows after the sequence have a q of 0 but the final state's gradient.
-template <typename E, int V, int W>
-__global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 3) conv_bwd_kernel(ConvParams p, Runs runs, int channel_blocks, float *part) {
+template <typename E, bool WIDE, int W>
+__global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvParams p, Runs runs, int channel_blocks, float *part) {
     extern __shared__ __align__(16) unsigned char smem[];
     auto &ring = *reinterpret_cast<Pack<E, V>(*)[kStages][2][kBatch][kThreads]>(smem);   // x, dout
     auto &sums = *reinterpret_cast<float (*)[kGroups][W + 1][kLanes * V]>(smem);         // after the walk
@@ -210,19 +215,20 @@ __global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 3) conv_bwd_kernel(Conv
 #pragma unroll
         for (int j = 0; j < W; ++j) dw[j][v] = 0.f;
     }
-    if (q < runs.count && c < p.D) {
+    const int cols = (int)min(p.D - c, (int64_t)V);
+    if (q < runs.count && cols > 0) {
         Run r = run_of(p, runs, q);
         float w[W][V], b[V];
-        ld_taps<V, W>(p.weight, c, w);
+        ld_taps<WIDE, W>(p.weight, c, cols, w);
 #pragma unroll
-        for (int v = 0; v < V; ++v) b[v] = p.bias ? p.bias[c + v] : 0.f;
+        for (int v = 0; v < V; ++v) b[v] = p.bias && v < cols ? p.bias[c + v] : 0.f;
         do {
             const int own = (int)(r.s1 - r.s0), real = own + (int)min((int64_t)(W - 1), r.hi - r.s1), all = own + W - 1;
             const bool first = r.s0 == r.lo;
             const auto fetch = [&](int j0, int stage) {
                 const E *x = static_cast<const E *>(p.x) + (r.s0 + j0) * p.xs + c, *dy = static_cast<const E *>(p.dout) + (r.s0 + j0) * p.ds + c;
-                copy_rows<E, V, kBatch, kThreads>(&ring[stage][0][0][tid], x, p.xs, real - j0);
-                copy_rows<E, V, kBatch, kThreads>(&ring[stage][1][0][tid], dy, p.ds, real - j0);
+                copy_rows<E, V, WIDE, kBatch, kThreads>(&ring[stage][0][0][tid], x, p.xs, real - j0, cols);
+                copy_rows<E, V, WIDE, kBatch, kThreads>(&ring[stage][1][0][tid], dy, p.ds, real - j0, cols);
                 copies_commit();
             };
             float xw[W][V], qs[W][V];   // inputs u-(W-1) .. u and their q
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 3) conv_bwd_kernel(Conv
             for (int k = 0; k < kStages - 1; ++k) fetch(k * kBatch, k);
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) {
-                ld_x<E, V>(p, r.n, r.lo, r.s0 - (W - 1) + j, c, xw[j]);
+                ld_x<E, V, WIDE>(p, r.n, r.lo, r.s0 - (W - 1) + j, c, cols, xw[j]);
 #pragma unroll
                 for (int v = 0; v < V; ++v) qs[j][v] = 0.f;
             }
@@ -242,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 3) conv_bwd_kernel(Conv
                 unpack<E, V>(ring[stage][1][k][tid], qn);
                 if (p.silu) {   // silu' = s (1 + y (1 - s))
                     float y[V], s[V], o[V], one[V];
-                    taps_sum<V, W>(w, b, xw, y);
+                    taps_sum<W>(w, b, xw, y);
                     sigmoid_n<V>(s, y);
                     fma_n<V>(o, s, -1.f, 1.f);
 #pragma unroll
@@ -272,9 +278,9 @@ __global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 3) conv_bwd_kernel(Conv
                         form_q(k, stage);
                         add_params();
                         form_d(d);
-                        st_f<E, V>(dx, d);
-                        shift<V, W>(xw);
-                        shift<V, W>(qs);
+                        st_cols<E, V, WIDE>(dx, d, cols);
+                        shift<W>(xw);
+                        shift<W>(qs);
                     }
                 } else {
                     // the part's first and last rows
@@ -293,12 +299,13 @@ __global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 3) conv_bwd_kernel(Conv
                         form_d(d);
                         if (p.dfinal && r.s0 + j >= r.hi) {
 #pragma unroll
-                            for (int v = 0; v < V; ++v) d[v] += p.dfinal[(r.n * (W - 1) + (r.s0 + j - r.hi)) * p.D + c + v];
+                            for (int v = 0; v < V; ++v)
+                                if (v < cols) d[v] += p.dfinal[(r.n * (W - 1) + (r.s0 + j - r.hi)) * p.D + c + v];
                         }
-                        if (j >= W - 1) st_f<E, V>(dx, d);
-                        else if (first && p.dinit) st_f<float, V>(p.dinit + (r.n * (W - 1) + j) * p.D + c, d);
-                        shift<V, W>(xw);
-                        shift<V, W>(qs);
+                        if (j >= W - 1) st_cols<E, V, WIDE>(dx, d, cols);
+                        else if (first && p.dinit) st_cols<float, V, WIDE>(p.dinit + (r.n * (W - 1) + j) * p.D + c, d, cols);
+                        shift<W>(xw);
+                        shift<W>(qs);
                     }
                 }
                 stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -345,7 +352,7 @@ __global__ void __launch_bounds__(1024) conv_param_sum_kernel(ConvParams p, int6
 }
 
 // ---- host side
-// 4 channels per thread where every row allows loads of 4 elements.
+// Whether every row allows loads of 4 elements.
 bool vector_rows(const ConvParams &p) {
     const size_t n = 4 * dtype_bytes(p.dtype);
     const void *ptrs[] = {p.x, p.out, p.init, p.fin, p.dout, p.dx};
@@ -358,7 +365,7 @@ bool vector_rows(const ConvParams &p) {
 // Runs as long as leaves about 1024 threads per SM, 8 to 64 rows: every run reads W-1 rows
 // of its neighbour's again.
 Runs plan_runs(const ConvParams &p, int sms) {
-    const int64_t lanes = ceil_div(p.D, vector_rows(p) ? 4 : 1);
+    const int64_t lanes = ceil_div(p.D, V);
     Runs r;
     for (r.length = 64; r.length > 8 && ceil_div(p.rows, r.length) * lanes < (int64_t)sms * 1024; r.length /= 2) {}
     r.per_seq = p.cu_seqlens ? 0 : ceil_div(p.T, r.length);
@@ -367,17 +374,17 @@ Runs plan_runs(const ConvParams &p, int sms) {
 }
 int64_t run_blocks(const Runs &r) { return ceil_div(r.count, kGroups); }
 
-// Calls f(null E pointer, integral_constant V, integral_constant W).
+// Calls f(null E pointer, bool_constant WIDE, integral_constant W).
 template <typename F>
 cudaError_t with_shape(const ConvParams &p, F &&f) {
-    const bool vec = vector_rows(p);
+    const bool wide = vector_rows(p);
     return with_dtype(p.dtype, [&](auto *tag) {
         const auto with_w = [&](auto v) {
             if (p.W == 2) return f(tag, v, std::integral_constant<int, 2>{});
             if (p.W == 3) return f(tag, v, std::integral_constant<int, 3>{});
             return f(tag, v, std::integral_constant<int, 4>{});
         };
-        return vec ? with_w(std::integral_constant<int, 4>{}) : with_w(std::integral_constant<int, 1>{});
+        return wide ? with_w(std::true_type{}) : with_w(std::false_type{});
     });
 }
 
@@ -389,11 +396,11 @@ size_t conv_bwd_scratch_bytes(const ConvParams &p, int sms) {
 
 cudaError_t launch_conv_fwd(const ConvParams &p, int sms, cudaStream_t stream) {
     const Runs runs = plan_runs(p, sms);
-    return with_shape(p, [&](auto *tag, auto V, auto W) {
+    return with_shape(p, [&](auto *tag, auto WIDE, auto W) {
         using E = std::remove_pointer_t<decltype(tag)>;
         const int64_t blocks = ceil_div(p.D, kLanes * V);
         if (p.rows > 0) {
-            constexpr auto kernel = conv_fwd_kernel<E, V, W>;
+            constexpr auto kernel = conv_fwd_kernel<E, WIDE, W>;
             constexpr int smem = (int)sizeof(Pack<E, V>) * kStages * kBatch * kThreads;
             const cudaError_t e = allow_smem<kernel>(smem);
             if (e != cudaSuccess) return e;
@@ -410,11 +417,11 @@ cudaError_t launch_conv_bwd(const ConvParams &p, unsigned char *ws, int sms, cud
     float *part = reinterpret_cast<float *>(ws);
     if (p.dinit && p.N > 0 && (p.cu_seqlens || p.T == 0))
         conv_empty_kernel<<<(unsigned)ceil_div(p.N, kGroups), kThreads, 0, stream>>>(p);
-    const cudaError_t e = with_shape(p, [&](auto *tag, auto V, auto W) {
+    const cudaError_t e = with_shape(p, [&](auto *tag, auto WIDE, auto W) {
         using E = std::remove_pointer_t<decltype(tag)>;
         const int64_t blocks = ceil_div(p.D, kLanes * V);
         if (p.rows == 0) return cudaSuccess;
-        constexpr auto kernel = conv_bwd_kernel<E, V, W>;
+        constexpr auto kernel = conv_bwd_kernel<E, WIDE, W>;
         constexpr int smem = (int)std::max(sizeof(Pack<E, V>) * kStages * 2 * kBatch * kThreads, sizeof(float) * kGroups * (W + 1) * kLanes * V);
         const cudaError_t e = allow_smem<kernel>(smem);
         if (e != cudaSuccess) return e;
