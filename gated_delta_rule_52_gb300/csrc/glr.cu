@@ -59,9 +59,9 @@ __global__ void __launch_bounds__(128) glr_fwd_step_kernel(GlrParams p) {
 
 // 8 rows by 4 channels per thread, 5 CTAs per SM.  Measured on 8192 x 8192 bf16: 118 us,
 // with 4 CTAs 120 us, with 256 threads of 4 rows (3 CTAs) 133 us (twice the per-thread work
-// of a tile), with two tiles in flight per CTA, the next one's map handed on before the
+// of a tile), with tiles of 32 rows (7 CTAs) 131 us, with two tiles in flight per CTA, the next one's map handed on before the
 // current one's state is taken (3 CTAs), 163 us (12 warps per SM are too few).
-using FwdShape = TileShape<128, 16, 4>;
+using FwdShape = TileShape<kGlrCheckpointRows, 128, 16, 4>;
 constexpr int kFwdCtas = 5;
 
 template <typename E>
@@ -71,7 +71,7 @@ struct FwdShared {
     Pack<GateConst, S::V> gates[S::THREADS];
     Pack<float, S::V> A[S::RG][S::CL], H[S::RG][S::CL];   // maps of the row groups
     Pack<float, S::V> h[S::RG][S::CL];                    // states that enter them
-    TileMarks marks;
+    TileMarks<S::ROWS> marks;
 };
 
 template <typename E, bool WIDE, bool UB>
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas) glr_fwd_scan_kern
     const auto fetch = [&](const TileWalk &w) {
         int first = 0;
         if (w.rt < s.row_tiles) {
-            const int64_t r0 = w.rt * kTileRows + rg * L;
+            const int64_t r0 = w.rt * S::ROWS + rg * L;
             const int c = w.cb * CB + lane * V;
             first = s.first_seq[w.rt];
             copy_gates<V>(&sh.gates[tid], s.gates + c);
@@ -110,10 +110,10 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas) glr_fwd_scan_kern
     TileWalk w(s);
     int first = fetch(w);
     while (w.rt < s.row_tiles) {
-        const int64_t rt = w.rt, r0 = rt * kTileRows + rg * L;
+        const int64_t rt = w.rt, r0 = rt * S::ROWS + rg * L;
         const int block = w.cb * CB, c = block + lane * V;
         const bool marked = mark_tile(p, rt, first, sh.marks);
-        const bool plain = !marked && (rt + 1) * kTileRows <= p.rows;   // every row inside one sequence
+        const bool plain = !marked && (rt + 1) * S::ROWS <= p.rows;   // every row inside one sequence
         copies_wait<0>();   // this thread's own copies: no barrier needed
 
         float a[L][V], b[L][V];
@@ -262,7 +262,7 @@ cudaError_t run(const GlrParams &p, unsigned char *ws, int sms, cudaStream_t str
         glr_fwd_step_kernel<E, V, UB><<<(unsigned)ceil_div(p.N * (p.D / V), 128), 128, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    ScanPlan s = scan_plan(p.rows, p.D, FwdShape::CB, ws, nullptr);
+    ScanPlan s = scan_plan<FwdShape>(p.rows, p.D, ws, nullptr);
     const int64_t fill = s.row_tiles * s.width / 2 + s.width;
     glr_prepare_kernel<UB, false><<<(unsigned)std::min(ceil_div(fill, 256), (int64_t)sms * 4), 256, 0, stream>>>(p, s);
     if (s.row_tiles == 0) return cudaGetLastError();
@@ -282,7 +282,7 @@ cudaError_t run(const GlrParams &p, unsigned char *ws, int sms, cudaStream_t str
 size_t glr_fwd_scratch_bytes(const GlrParams &p, int) {
     if (step_takes(p)) return 0;
     size_t bytes = 0;
-    scan_plan(p.rows, p.D, FwdShape::CB, nullptr, &bytes);
+    scan_plan<FwdShape>(p.rows, p.D, nullptr, &bytes);
     return bytes;
 }
 

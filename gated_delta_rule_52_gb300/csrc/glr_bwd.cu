@@ -23,7 +23,7 @@ using namespace layer;
 
 // 16 elements per thread: 4 rows by 4 channels in 16 bits, 8 by 2 in 32 bits (the raw
 // inputs of two tiles in shared memory allow 2 and 3 CTAs per SM).
-template <typename E> using BwdShape = TileShape<sizeof(E) == 2 ? 256 : 128, 16, sizeof(E) == 2 ? 4 : 2>;
+template <typename E> using BwdShape = TileShape<kGlrCheckpointRows, sizeof(E) == 2 ? 256 : 128, 16, sizeof(E) == 2 ? 4 : 2>;
 
 template <typename E>
 struct BwdShared {
@@ -34,7 +34,7 @@ struct BwdShared {
     Pack<float, S::V> B[S::RG][S::CL], F[S::RG][S::CL];            // backward maps
     // states that enter them, and over each thread's own two its sums of parameter gradients
     Pack<float, S::V> h[S::RG][S::CL], f[S::RG][S::CL];
-    TileMarks marks;
+    TileMarks<S::ROWS> marks;
 };
 
 template <typename E, bool WIDE, bool UB>
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
     const auto fetch = [&](const TileWalk &w, int stage) {
         int first = 0;
         if (w.rt < s.row_tiles) {
-            const int64_t rt = s.row_tiles - 1 - w.rt, r0 = rt * kTileRows + rg * L;
+            const int64_t rt = s.row_tiles - 1 - w.rt, r0 = rt * S::ROWS + rg * L;
             const int c = w.cb * CB + lane * V;
             first = s.first_seq[rt];
             copy_gates<V>(&sh.gates[stage][tid], s.gates + c);
@@ -79,13 +79,13 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
     TileWalk w(s);
     int next_first = fetch(w, 0);
     for (int stage = 0; w.rt < s.row_tiles; stage ^= 1) {
-        const int64_t walk = w.rt, rt = s.row_tiles - 1 - walk, r0 = rt * kTileRows + rg * L;
+        const int64_t walk = w.rt, rt = s.row_tiles - 1 - walk, r0 = rt * S::ROWS + rg * L;
         const int c = w.cb * CB + lane * V, block = w.cb * CB, cols = D - c, first = next_first;
         const float h_tile = checkpoint;
         w.next();
         next_first = fetch(w, stage ^ 1);
         const bool marked = mark_tile(p, rt, first, sh.marks);
-        const bool plain = !marked && (rt + 1) * kTileRows <= p.rows;        // every row inside one sequence
+        const bool plain = !marked && (rt + 1) * S::ROWS <= p.rows;        // every row inside one sequence
         const int left = cols > 0 ? (int)min(p.rows - r0, (int64_t)L) : 0;   // rows of this thread that exist
         copies_wait<1>();   // this thread's own copies: no barrier needed
 
@@ -309,7 +309,6 @@ bool vector_rows(const GlrParams &p) {
         if (reinterpret_cast<uintptr_t>(q) % n) return false;
     return p.D % V == 0 && p.xs % V == 0 && p.is % V == 0 && p.gs % V == 0 && p.ds % V == 0;
 }
-int block_channels(const GlrParams &p) { return p.dtype == kFP32 ? BwdShape<float>::CB : BwdShape<__half>::CB; }
 
 // Workspace: the scan's, the partial sums, the checkpoints and the forward run's workspace.
 struct BwdPlan {
@@ -321,7 +320,7 @@ struct BwdPlan {
 BwdPlan bwd_plan(const GlrParams &p, int sms, unsigned char *ws) {
     BwdPlan b;
     size_t at = 0;
-    b.s = scan_plan(p.rows, p.D, block_channels(p), ws, &at);
+    b.s = p.dtype == kFP32 ? scan_plan<BwdShape<float>>(p.rows, p.D, ws, &at) : scan_plan<BwdShape<__half>>(p.rows, p.D, ws, &at);
     const size_t part = (size_t)(b.s.row_tiles * b.s.width) * sizeof(float);
     const size_t ck = p.checkpoints ? 0 : ((size_t)(b.s.row_tiles * p.D) * sizeof(float) + 15) / 16 * 16;
     b.part_ddt = reinterpret_cast<float *>(ws + at);

@@ -19,7 +19,6 @@
 namespace kda {
 namespace layer {
 
-constexpr int kTileRows = kGlrCheckpointRows;
 constexpr uint32_t kEmpty = 0xffffffffu;
 
 // An affine map.  A decay is never negative, so A's sign bit marks a map that does not
@@ -76,34 +75,36 @@ __device__ __forceinline__ U await(const U *at, U v, int *err) {
 
 // How a CTA covers a tile: THREADS threads as CL channel lanes of V channels each by RG row
 // groups of L rows each.
-template <int THREADS_, int CL_, int V_>
+template <int ROWS_, int THREADS_, int CL_, int V_>
 struct TileShape {
-    static constexpr int THREADS = THREADS_, CL = CL_, V = V_;
-    static constexpr int CB = CL * V, RG = THREADS / CL, L = kTileRows / RG;
-    static_assert(RG * L == kTileRows && THREADS >= 2 * CB && CB % 32 == 0, "tile shape");
+    static constexpr int ROWS = ROWS_, THREADS = THREADS_, CL = CL_, V = V_;
+    static constexpr int CB = CL * V, RG = THREADS / CL, L = ROWS / RG;
+    static_assert(RG * L == ROWS && THREADS >= 2 * CB && CB % 32 == 0, "tile shape");
 };
 
 // Workspace of a scan and its tiles.  Maps [row tile][padded channel], states after a
 // group [group][padded channel], then the first sequence of every row tile.
 struct ScanPlan {
     int64_t row_tiles, groups, blocks, width;   // width = blocks * channels per block
-    int group_log2;                             // row tiles per group
+    int tile_rows, group_log2;                  // rows per tile, log2 of row tiles per group
     uint64_t *maps;
     uint32_t *states;
     int *first_seq;                             // kInside set: the tile lies inside that sequence
     GateConst *gates;                           // [width]
 };
 constexpr int kInside = INT32_MIN;
-inline ScanPlan scan_plan(int64_t rows, int64_t D, int channels, unsigned char *ws, size_t *bytes) {
+template <typename S>
+ScanPlan scan_plan(int64_t rows, int64_t D, unsigned char *ws, size_t *bytes) {
     ScanPlan s;
-    s.row_tiles = ceil_div(rows, kTileRows);
-    s.blocks = ceil_div(D, channels);
+    s.tile_rows = S::ROWS;
+    s.row_tiles = ceil_div(rows, S::ROWS);
+    s.blocks = ceil_div(D, S::CB);
     // The state passes from group to group one at a time, each step about one tile's time
     // on one SM, while the rest of the GPU works off `group` row tiles of `blocks` tiles; a
     // tile joins the maps of half a group on average.
     for (s.group_log2 = 2; s.group_log2 < 5 && s.blocks << s.group_log2 < 256; ++s.group_log2) {}
     s.groups = ceil_div(s.row_tiles, int64_t(1) << s.group_log2);
-    s.width = s.blocks * channels;
+    s.width = s.blocks * S::CB;
     s.maps = reinterpret_cast<uint64_t *>(ws);
     s.states = reinterpret_cast<uint32_t *>(s.maps + s.row_tiles * s.width);
     s.gates = reinterpret_cast<GateConst *>(s.states + ceil_div(s.groups * s.width, 4) * 4);
@@ -124,10 +125,10 @@ __global__ void __launch_bounds__(256) glr_prepare_kernel(GlrParams p, ScanPlan 
     for (int64_t c = at; c < s.width; c += step)
         s.gates[c] = c < p.D ? gate_const<UB>(p.A_log[(unsigned)c / (unsigned)p.K], p.dt_bias[c]) : GateConst{0.f, 0.f};
     for (int64_t t = at; t < s.row_tiles; t += step) {
-        const int64_t r0 = t * kTileRows, n = p.cu_seqlens ? seq_of_row(p.cu_seqlens, p.N, r0) : (unsigned)r0 / (unsigned)p.T;
+        const int64_t r0 = t * s.tile_rows, n = p.cu_seqlens ? seq_of_row(p.cu_seqlens, p.N, r0) : (unsigned)r0 / (unsigned)p.T;
         int64_t lo, hi;
         seq_rows(p, n, lo, hi);
-        s.first_seq[t] = (int)n | (lo < r0 && hi > r0 + kTileRows ? kInside : 0);
+        s.first_seq[t] = (int)n | (lo < r0 && hi > r0 + s.tile_rows ? kInside : 0);
     }
     if (!p.cu_seqlens && p.T > 0) return;
     if (REVERSE ? !p.dinit : !p.fin) return;
@@ -166,18 +167,18 @@ __device__ __forceinline__ Affine joined(Affine a, Affine b) {
 template <bool CUTS>
 __device__ __forceinline__ float applied(Affine m, float h) { return CUTS ? apply(m, h) : fmaf(m.A, h, m.H); }
 
-// Where sequences begin and end within a tile of rows [r0, r0 + kTileRows): for each row
+// Where sequences begin and end within a tile of rows [r0, r0 + ROWS): for each row
 // the sequence that it begins (ends), or -1.  Returns false, and writes nothing, where the
 // tile lies inside one sequence.  Called by all threads, whose shared memory it is.
-struct TileMarks { int begins[kTileRows], ends[kTileRows]; };
+template <int ROWS> struct TileMarks { int begins[ROWS], ends[ROWS]; };
 
 // n: first_seq of the tile.
-template <typename P>
-__device__ __forceinline__ bool mark_tile(const P &p, int64_t row_tile, int n, TileMarks &m) {
+template <typename P, int ROWS>
+__device__ __forceinline__ bool mark_tile(const P &p, int64_t row_tile, int n, TileMarks<ROWS> &m) {
     if (n & kInside) return false;
-    const int64_t r0 = row_tile * kTileRows, r1 = r0 + kTileRows;
+    const int64_t r0 = row_tile * ROWS, r1 = r0 + ROWS;
     __syncthreads();   // the marks of the tile before are read no more
-    if (threadIdx.x < kTileRows) m.begins[threadIdx.x] = m.ends[threadIdx.x] = -1;
+    if (threadIdx.x < ROWS) m.begins[threadIdx.x] = m.ends[threadIdx.x] = -1;
     __syncthreads();
     for (int64_t k = n + threadIdx.x; k < p.N; k += blockDim.x) {
         int64_t lo, hi;

@@ -24,9 +24,13 @@ __device__ __forceinline__ void copy_async(void *slot, const void *src) {
 template <typename E, int V, bool WIDE, int N, int THREADS>
 __device__ __forceinline__ void copy_rows(Pack<E, V> *slots, const E *src, int64_t stride, int count, int cols) {
     if constexpr (WIDE) {
+        if (count >= N) {
 #pragma unroll
-        for (int r = 0; r < N; ++r, src += stride)
-            if (r < count) copy_async<sizeof(E) * V>(slots + r * THREADS, src);
+            for (int r = 0; r < N; ++r, src += stride) copy_async<sizeof(E) * V>(slots + r * THREADS, src);
+        } else {
+#pragma unroll 1
+            for (int r = 0; r < count; ++r, src += stride) copy_async<sizeof(E) * V>(slots + r * THREADS, src);
+        }
     } else if constexpr (sizeof(E) == 4) {
 #pragma unroll
         for (int r = 0; r < N; ++r, src += stride) {

@@ -87,18 +87,12 @@ __device__ __forceinline__ void fma_n(float (&r)[n], const float (&a)[n], const 
         for (int j = 0; j < n; ++j) r[j] = fmaf(a[j], b[j], c[j]);
     }
 }
+// With the same b and c for all: an immediate operand costs nothing, a register pair of
+// constants two moves.
 template <int n>
 __device__ __forceinline__ void fma_n(float (&r)[n], const float (&a)[n], float b, float c) {
-    if constexpr (n % 2 == 0) {
 #pragma unroll
-        for (int j = 0; j < n; j += 2) {
-            const float2 t = sm103::fma2(make_float2(a[j], a[j + 1]), both(b), both(c));
-            r[j] = t.x, r[j + 1] = t.y;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < n; ++j) r[j] = fmaf(a[j], b, c);
-    }
+    for (int j = 0; j < n; ++j) r[j] = fmaf(a[j], b, c);
 }
 template <int n>
 __device__ __forceinline__ void mul_n(float (&r)[n], const float (&a)[n], const float (&b)[n]) {

@@ -94,6 +94,7 @@ __device__ __forceinline__ void ld_param(const float *p, int c, float dflt, floa
 
 template <typename E, int V, int EL>
 __global__ void __launch_bounds__(EL == 32 ? 512 : 1024) norm_fwd_kernel(NormParams p) {
+    const int D = (int)p.D;
     constexpr int N = EL / V;
     __shared__ float part[2][kMaxWarps];
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -104,10 +105,10 @@ __global__ void __launch_bounds__(EL == 32 ? 512 : 1024) norm_fwd_kernel(NormPar
         Pack<E, V> raw[N];
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            if (live && column<V>(k) < p.D) raw[k] = ld_pack<E, V>(x + column<V>(k));
+            if (live && column<V>(k) < D) raw[k] = ld_pack<E, V>(x + column<V>(k));
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            if (live && column<V>(k) < p.D) unpack<E, V>(raw[k], f[k]);
+            if (live && column<V>(k) < D) unpack<E, V>(raw[k], f[k]);
             else
 #pragma unroll
                 for (int v = 0; v < V; ++v) f[k][v] = 0.f;
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(EL == 32 ? 512 : 1024) norm_fwd_kernel(NormPar
     for (int v = 0; v < V; ++v) sq[v] = 0.f;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        if (column<V>(k) >= p.D) continue;
+        if (column<V>(k) >= D) continue;
         fma_n<V>(f[k], f[k], 1.f, -mean);
         fma_n<V>(sq, f[k], f[k], sq);
     }
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(EL == 32 ? 512 : 1024) norm_fwd_kernel(NormPar
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         const int c = column<V>(k);
-        if (c >= p.D) continue;
+        if (c >= D) continue;
         float w[V], b[V];
         ld_param<V>(p.weight, c, 1.f, w);
         ld_param<V>(p.bias, c, 0.f, b);
@@ -149,6 +150,7 @@ constexpr int kStages = 3;
 
 template <typename E, int V, int EL>
 __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *part_out) {
+    const int D = (int)p.D;
     constexpr int N = EL / V;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float part[2][2][kMaxWarps];
@@ -165,14 +167,14 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *p
                 E t[2 * N];
 #pragma unroll
                 for (int k = 0; k < N; ++k)
-                    if (column<V>(k) < p.D) t[2 * k] = x[column<V>(k)], t[2 * k + 1] = dy[column<V>(k)];
+                    if (column<V>(k) < D) t[2 * k] = x[column<V>(k)], t[2 * k + 1] = dy[column<V>(k)];
 #pragma unroll
                 for (int k = 0; k < N; ++k)
-                    if (column<V>(k) < p.D) slot(stage, 0, k).e[0] = t[2 * k], slot(stage, 1, k).e[0] = t[2 * k + 1];
+                    if (column<V>(k) < D) slot(stage, 0, k).e[0] = t[2 * k], slot(stage, 1, k).e[0] = t[2 * k + 1];
             } else {
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    if (column<V>(k) < p.D) {
+                    if (column<V>(k) < D) {
                         copy_async<sizeof(E) * V>(&slot(stage, 0, k), x + column<V>(k));
                         copy_async<sizeof(E) * V>(&slot(stage, 1, k), dy + column<V>(k));
                     }
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *p
     // columns that do not exist stay 0 in every slot
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        if (column<V>(k) < p.D) continue;
+        if (column<V>(k) < D) continue;
         for (int j = 0; j < 2 * kStages; ++j) {
             const float zero[V] = {};
             st_f<E, V>(&slot(j / 2, j % 2, k).e[0], zero);
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *p
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         float t[V] = {};
-        if (column<V>(k) < p.D) ld_param<V>(p.weight, column<V>(k), 1.f, t);
+        if (column<V>(k) < D) ld_param<V>(p.weight, column<V>(k), 1.f, t);
 #pragma unroll
         for (int v = 0; v < V; ++v) w[k * V + v] = t[v], dw[k * V + v] = db[k * V + v] = 0.f;
     }
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *p
         E *dx = static_cast<E *>(p.dx) + row * p.D;
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            if (column<V>(k) < p.D) st_f<E, V>(dx + column<V>(k), reinterpret_cast<const float (&)[V]>(d[k * V]));
+            if (column<V>(k) < D) st_f<E, V>(dx + column<V>(k), reinterpret_cast<const float (&)[V]>(d[k * V]));
     }
     copies_wait<0>();
     if (!part_out) return;
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *p
 #pragma unroll
         for (int e = 0; e < EL; ++e) {
             const int c = column<V>(e / V) + e % V;
-            if (c < p.D) at[c] = dw[e], at[p.D + c] = db[e];
+            if (c < D) at[c] = dw[e], at[p.D + c] = db[e];
         }
     }
 }
