@@ -84,14 +84,11 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas) glr_fwd_scan_kern
     const float lb2 = p.lower_bound * kLog2e;
     const int D = (int)p.D;
 
-    // starts the copies of a tile into this thread's own slots; returns its first sequence
+    // starts the copies of a tile's inputs into this thread's own slots
     const auto fetch = [&](const TileWalk &w) {
-        int first = 0;
         if (w.rt < s.row_tiles) {
             const int64_t r0 = w.rt * S::ROWS + rg * L;
             const int c = w.cb * CB + lane * V;
-            first = s.first_seq[w.rt];
-            copy_gates<V>(&sh.gates[tid], s.gates + c);
             if (c < D) {
                 const int left = (int)min(p.rows - r0, (int64_t)L);
                 const auto copy = [&](int k, const void *src, int64_t stride) {
@@ -103,12 +100,23 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas) glr_fwd_scan_kern
                 copy(2, p.g, p.gs);
             }
         }
+    };
+    // and of what the scan's first part has left for the tile; returns its first sequence
+    const auto fetch_plan = [&](const TileWalk &w) {
+        int first = 0;
+        if (w.rt < s.row_tiles) {
+            first = s.first_seq[w.rt];
+            copy_gates<V>(&sh.gates[tid], s.gates + w.cb * CB + lane * V);
+        }
         copies_commit();
         return first;
     };
 
     TileWalk w(s);
-    int first = fetch(w);
+    fetch(w);
+    prepare_scan<UB, false>(p, s);
+    cooperative_groups::this_grid().sync();
+    int first = fetch_plan(w);
     while (w.rt < s.row_tiles) {
         const int64_t rt = w.rt, r0 = rt * S::ROWS + rg * L;
         const int block = w.cb * CB, c = block + lane * V;
@@ -131,7 +139,8 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas) glr_fwd_scan_kern
             }
         }
         w.next();
-        first = fetch(w);   // the slots are free: the next tile's copies run beside the rest
+        fetch(w);   // the slots are free: the next tile's copies run beside the rest
+        first = fetch_plan(w);
         Pack<float, V> mA, mH;
         if (plain) {
 #pragma unroll
@@ -263,15 +272,12 @@ cudaError_t run(const GlrParams &p, unsigned char *ws, int sms, cudaStream_t str
         return cudaGetLastError();
     }
     ScanPlan s = scan_plan<FwdShape>(p.rows, p.D, ws, nullptr);
-    const int64_t fill = s.row_tiles * s.width / 2 + s.width;
-    glr_prepare_kernel<UB, false><<<(unsigned)std::min(ceil_div(fill, 256), (int64_t)sms * 4), 256, 0, stream>>>(p, s);
-    if (s.row_tiles == 0) return cudaGetLastError();
     constexpr auto kernel = glr_fwd_scan_kernel<E, WIDE, UB>;
     constexpr int bytes = (int)sizeof(FwdShared<E>);
     int ctas = 0;
     const cudaError_t e = resident_ctas<kernel>(FwdShape::THREADS, bytes, ctas);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)std::min(s.row_tiles * s.blocks, (int64_t)sms * ctas);
+    const unsigned grid = (unsigned)std::max(std::min(s.row_tiles * s.blocks, (int64_t)sms * ctas), (int64_t)1);
     GlrParams arg = p;
     void *args[] = {&arg, &s};
     return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(FwdShape::THREADS), args, bytes, stream);

@@ -53,12 +53,9 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
 
     // tile number w.rt counts from the last row tile
     const auto fetch = [&](const TileWalk &w, int stage) {
-        int first = 0;
         if (w.rt < s.row_tiles) {
             const int64_t rt = s.row_tiles - 1 - w.rt, r0 = rt * S::ROWS + rg * L;
             const int c = w.cb * CB + lane * V;
-            first = s.first_seq[rt];
-            copy_gates<V>(&sh.gates[stage][tid], s.gates + c);
             if (role == 2 && w.cb * CB + ch < D) checkpoint = p.checkpoints[rt * p.D + w.cb * CB + ch];
             if (c < D) {
                 const int left = (int)min(p.rows - r0, (int64_t)L);
@@ -72,18 +69,30 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
                 copy(3, p.dout, p.ds);
             }
         }
+    };
+    // and of what the scan's first part has left for the tile; returns its first sequence
+    const auto fetch_plan = [&](const TileWalk &w, int stage) {
+        int first = 0;
+        if (w.rt < s.row_tiles) {
+            first = s.first_seq[s.row_tiles - 1 - w.rt];
+            copy_gates<V>(&sh.gates[stage][tid], s.gates + w.cb * CB + lane * V);
+        }
         copies_commit();
         return first;
     };
 
     TileWalk w(s);
-    int next_first = fetch(w, 0);
+    fetch(w, 0);
+    prepare_scan<UB, true>(p, s);
+    cooperative_groups::this_grid().sync();
+    int next_first = fetch_plan(w, 0);
     for (int stage = 0; w.rt < s.row_tiles; stage ^= 1) {
         const int64_t walk = w.rt, rt = s.row_tiles - 1 - walk, r0 = rt * S::ROWS + rg * L;
         const int c = w.cb * CB + lane * V, block = w.cb * CB, cols = D - c, first = next_first;
         const float h_tile = checkpoint;
         w.next();
-        next_first = fetch(w, stage ^ 1);
+        fetch(w, stage ^ 1);
+        next_first = fetch_plan(w, stage ^ 1);
         const bool marked = mark_tile(p, rt, first, sh.marks);
         const bool plain = !marked && (rt + 1) * S::ROWS <= p.rows;        // every row inside one sequence
         const int left = cols > 0 ? (int)min(p.rows - r0, (int64_t)L) : 0;   // rows of this thread that exist
@@ -270,10 +279,45 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
     copies_wait<0>();
 }
 
-// Sums the tiles' partial parameter gradients [parts, width] over the tiles, 32 channels
-// per CTA: ddt_bias, and in part_dA's first row dA_log's sums per channel.
-__global__ void __launch_bounds__(1024) glr_param_sum_kernel(GlrParams p, int64_t parts, int64_t width, const float *part_ddt,
-                                                             float *part_dA) {
+// Sums the tiles' partial parameter gradients [parts, width] over the tiles: a CTA per head
+// of at most 512 channels, ddt_bias per channel and dA_log; 1024 threads, as many slices of
+// the parts as they allow.
+constexpr int64_t kMaxHead = 512;
+__global__ void __launch_bounds__(1024) glr_head_grads_kernel(GlrParams p, int64_t parts, int64_t width, const float *part_ddt,
+                                                              const float *part_dA) {
+    __shared__ float sums[2][1024];
+    const int K = (int)p.K, lanes = (K + 31) / 32 * 32, slices = lanes > 0 ? 1024 / lanes : 0;
+    const int k = lanes > 0 ? threadIdx.x % lanes : 0, slice = lanes > 0 ? threadIdx.x / lanes : 0;
+    const int64_t c = blockIdx.x * p.K + k;
+    float ddt = 0.f, dA = 0.f;
+    if (k < K && slice < slices) {
+#pragma unroll 8
+        for (int64_t j = slice; j < parts; j += slices) {
+            ddt += part_ddt[j * width + c];
+            dA += part_dA[j * width + c];
+        }
+    }
+    sums[0][threadIdx.x] = ddt;
+    sums[1][threadIdx.x] = dA;
+    __syncthreads();
+    ddt = dA = 0.f;
+    if (threadIdx.x < K) {
+        for (int j = 0; j < slices; ++j) ddt += sums[0][j * lanes + k], dA += sums[1][j * lanes + k];
+        p.ddt_bias[c] = ddt;
+    }
+    __syncthreads();
+    for (int o = 16; o; o >>= 1) dA += __shfl_xor_sync(0xffffffffu, dA, o);
+    if ((threadIdx.x & 31) == 0) sums[0][threadIdx.x >> 5] = dA;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int j = 1; j < 32; ++j) dA += sums[0][j];
+        p.dA_log[blockIdx.x] = dA;
+    }
+}
+// Wider heads: the sums per channel first, 32 channels per CTA, those of dA_log left in
+// part_dA's first row; then a CTA per head.
+__global__ void __launch_bounds__(kSumThreads) glr_param_sum_kernel(GlrParams p, int64_t parts, int64_t width, const float *part_ddt,
+                                                                    float *part_dA) {
     const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     const float ddt = column_sum(part_ddt, parts, width, c, c < p.D);
     __syncthreads();
@@ -334,15 +378,12 @@ BwdPlan bwd_plan(const GlrParams &p, int sms, unsigned char *ws) {
 template <typename E, bool WIDE, bool UB>
 cudaError_t run(const GlrParams &p, const BwdPlan &b, int sms, cudaStream_t stream) {
     ScanPlan s = b.s;
-    const int64_t fill = s.row_tiles * s.width / 2 + s.width;
-    glr_prepare_kernel<UB, true><<<(unsigned)std::min(ceil_div(fill, 256), (int64_t)sms * 4), 256, 0, stream>>>(p, s);
-    if (s.row_tiles == 0) return cudaGetLastError();
     int ctas = 0;
     constexpr int bytes = (int)sizeof(BwdShared<E>);
     constexpr auto kernel = glr_bwd_scan_kernel<E, WIDE, UB>;
     const cudaError_t e = resident_ctas<kernel>(BwdShape<E>::THREADS, bytes, ctas);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)std::min(s.row_tiles * s.blocks, (int64_t)sms * ctas);
+    const unsigned grid = (unsigned)std::max(std::min(s.row_tiles * s.blocks, (int64_t)sms * ctas), (int64_t)1);
     GlrParams arg = p;
     float *ddt = b.part_ddt, *dA = b.part_dA;
     void *args[] = {&arg, &s, &ddt, &dA};
@@ -372,8 +413,11 @@ cudaError_t launch_glr_bwd(const GlrParams &p0, unsigned char *ws, int sms, cuda
         });
         if (e != cudaSuccess) return e;
     }
-    if (p.D > 0)
-        glr_param_sum_kernel<<<(unsigned)ceil_div(p.D, 32), 1024, 0, stream>>>(p, b.s.row_tiles, b.s.width, b.part_ddt, b.part_dA);
+    if (p.K <= kMaxHead) {
+        glr_head_grads_kernel<<<(unsigned)p.H, 1024, 0, stream>>>(p, b.s.row_tiles, b.s.width, b.part_ddt, b.part_dA);
+        return cudaGetLastError();
+    }
+    glr_param_sum_kernel<<<(unsigned)ceil_div(p.D, 32), kSumThreads, 0, stream>>>(p, b.s.row_tiles, b.s.width, b.part_ddt, b.part_dA);
     glr_head_sum_kernel<<<(unsigned)p.H, 128, 0, stream>>>(p, b.s.row_tiles > 0, b.part_dA);
     return cudaGetLastError();
 }

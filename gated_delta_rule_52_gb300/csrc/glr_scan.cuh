@@ -13,6 +13,8 @@
 // published) before the launch.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "glr_gate.cuh"
 #include "layer_copy.cuh"
 
@@ -57,15 +59,13 @@ __device__ __forceinline__ uint32_t peek(const uint32_t *at) {
 __device__ __forceinline__ bool empty(uint64_t v) { return (uint32_t)v == kEmpty; }
 __device__ __forceinline__ bool empty(uint32_t v) { return v == kEmpty; }
 
-// Waits for a published value, at most kWaitNs; on expiry reports to the device error word
-// and goes on with what is there.
-constexpr uint64_t kWaitNs = 2000000000ull;
+// Waits for a published value, at most kWaitPolls loads (some seconds); on expiry reports to
+// the device error word and goes on with what is there.
+constexpr int kWaitPolls = 1 << 22;
 template <typename U>
 __device__ __forceinline__ U await(const U *at, U v, int *err) {
-    if (!empty(v)) return v;
-    const uint64_t t0 = sm103::globaltimer_ns();
-    while (empty(v = peek(at))) {
-        if (sm103::globaltimer_ns() - t0 > kWaitNs) {
+    for (int polls = 0; empty(v); v = peek(at)) {
+        if (++polls > kWaitPolls) {
             atomicExch(err, kErrTimeout);
             break;
         }
@@ -113,12 +113,13 @@ ScanPlan scan_plan(int64_t rows, int64_t D, unsigned char *ws, size_t *bytes) {
     return s;
 }
 
-// Before a scan: empties the hand-over buffers, folds the gates' constants, finds the first
-// sequence of every row tile.  REVERSE false: final states of sequences without tokens;
-// true: their gradients of the initial state.
+// The first part of a scan kernel, before its grid-wide barrier: empties the hand-over
+// buffers, folds the gates' constants, finds the first sequence of every row tile.  REVERSE
+// false: final states of sequences without tokens; true: their gradients of the initial
+// state.  (As a kernel of its own it cost 4 us and a launch.)
 template <bool UB, bool REVERSE>
-__global__ void __launch_bounds__(256) glr_prepare_kernel(GlrParams p, ScanPlan s) {
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+__device__ __forceinline__ void prepare_scan(const GlrParams &p, const ScanPlan &s) {
+    const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
     const int64_t words = (s.row_tiles * s.width * 2 + ceil_div(s.groups * s.width, 4) * 4) / 4;
     uint4 *fill = reinterpret_cast<uint4 *>(s.maps);
     for (int64_t j = at; j < words; j += step) fill[j] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);

@@ -86,24 +86,24 @@ cudaError_t allow_smem(int bytes) {
     return once_per_device(done, [&](int) { return cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
 }
 
-// Sum over j of part[j * width + c], 32 columns per CTA of 1024 threads, in a fixed order.
-// The threads of the CTA's first warp have the sum of column 32 blockIdx.x + lane.
+// Sum over j of part[j * width + c], 32 columns per CTA of kSumThreads threads, in a fixed
+// order.  The threads of the CTA's first warp have the sum of column 32 blockIdx.x + lane.
+constexpr int kSumThreads = 256;
 __device__ __forceinline__ float column_sum(const float *part, int64_t parts, int64_t width, int64_t c, bool in) {
-    __shared__ float sums[32][33];
+    constexpr int kSlices = kSumThreads / 32;
+    __shared__ float sums[kSlices][32];
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     float t = 0.f;
     if (in) {
-#pragma unroll 4
-        for (int64_t j = slice; j < parts; j += 32) t += part[j * width + c];
+#pragma unroll 8
+        for (int64_t j = slice; j < parts; j += kSlices) t += part[j * width + c];
     }
     sums[slice][lane] = t;
     __syncthreads();
-    t = sums[lane][slice];   // warp `slice` holds column `slice`'s 32 partial sums
-    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    __syncthreads();
-    if (lane == 0) sums[0][slice] = t;
-    __syncthreads();
-    return sums[0][lane];
+    t = 0.f;
+#pragma unroll
+    for (int j = 0; j < kSlices; ++j) t += sums[j][lane];
+    return t;
 }
 
 }  // namespace layer

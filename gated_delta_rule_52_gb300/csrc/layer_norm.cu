@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(256) norm_param_part_kernel(NormParams p, int6
 }
 
 // part [parts, 2, D] to dweight, dbias.
-__global__ void __launch_bounds__(1024) norm_param_sum_kernel(NormParams p, int64_t parts, const float *part) {
+__global__ void __launch_bounds__(kSumThreads) norm_param_sum_kernel(NormParams p, int64_t parts, const float *part) {
     const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     const float t = column_sum(part, parts, 2 * p.D, c, c < 2 * p.D);
     if (threadIdx.x >= 32) return;
@@ -435,7 +435,7 @@ cudaError_t launch_norm_bwd(const NormParams &p, unsigned char *ws, int sms, cud
     });
     if (e != cudaSuccess) return e;
     if (part || (wants_params(p) && p.rows == 0))
-        norm_param_sum_kernel<<<(unsigned)ceil_div(2 * p.D, 32), 1024, 0, stream>>>(p, parts, part);
+        norm_param_sum_kernel<<<(unsigned)ceil_div(2 * p.D, 32), kSumThreads, 0, stream>>>(p, parts, part);
     return cudaGetLastError();
 }
 

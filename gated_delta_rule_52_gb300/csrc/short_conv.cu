@@ -115,6 +115,19 @@ __device__ __forceinline__ void shift(float (&xw)[W][V]) {
         for (int v = 0; v < V; ++v) xw[j][v] = xw[j + 1][v];
 }
 
+// Calls f with every state element of the packed sequences without tokens, which no run
+// comes to: sequence n is CTA n's.
+template <typename F>
+__device__ __forceinline__ void each_empty(const ConvParams &p, F &&f) {
+    for (int64_t n = blockIdx.x; n < p.N; n += gridDim.x) {
+        int64_t lo, hi;
+        seq_rows(p, n, lo, hi);
+        if (lo < hi) continue;
+        const int64_t size = (p.W - 1) * p.D;
+        for (int64_t k = n * size + threadIdx.x; k < (n + 1) * size; k += blockDim.x) f(k);
+    }
+}
+
 constexpr int kBatch = 4, kStages = 3;   // rows per copy group, groups of a thread's ring
 
 template <typename E, bool WIDE, int W>
@@ -125,6 +138,8 @@ __global__ void __launch_bounds__(kThreads, 3) conv_fwd_kernel(ConvParams p, Run
     const int64_t q = (int64_t)(blockIdx.x / channel_blocks) * kGroups + tid / kLanes;
     const int64_t c = ((int64_t)(blockIdx.x % channel_blocks) * kLanes + tid % kLanes) * V;
     const int cols = (int)min(p.D - c, (int64_t)V);
+    if (p.cu_seqlens && p.fin)
+        each_empty(p, [&](int64_t k) { static_cast<E *>(p.fin)[k] = p.init ? static_cast<const E *>(p.init)[k] : from_f<E>(0.f); });
     if (q >= runs.count || cols <= 0) return;
     Run r = run_of(p, runs, q);
     float w[W][V], b[V], xw[W][V];
@@ -141,14 +156,6 @@ __global__ void __launch_bounds__(kThreads, 3) conv_fwd_kernel(ConvParams p, Run
         for (int k = 0; k < kStages - 1; ++k) fetch(k * kBatch, k);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) ld_x<E, V, WIDE>(p, r.n, r.lo, r.s0 - (W - 1) + j, c, cols, xw[j]);
-        // the final state is the first run's to write: it alone reads the initial state
-        if (p.fin && !p.cu_seqlens && r.s0 == r.lo) {
-            float last[W - 1][V];
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) ld_x<E, V, WIDE>(p, r.n, r.lo, r.hi - (W - 1) + j, c, cols, last[j]);
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) st_cols<E, V, WIDE>(static_cast<E *>(p.fin) + (r.n * (W - 1) + j) * p.D + c, last[j], cols);
-        }
         E *out = static_cast<E *>(p.out) + r.s0 * p.os + c;
         const auto row = [&](int k, int stage) {
             unpack<E, V>(ring[stage][k][tid], xw[W - 1]);
@@ -174,13 +181,17 @@ __global__ void __launch_bounds__(kThreads, 3) conv_fwd_kernel(ConvParams p, Run
             }
             stage = stage + 1 == kStages ? 0 : stage + 1;
         }
+        // the window after a sequence's last row is its final state
+        if (p.fin && r.s1 == r.hi) {
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) st_cols<E, V, WIDE>(static_cast<E *>(p.fin) + (r.n * (W - 1) + j) * p.D + c, xw[j], cols);
+        }
     } while (next_part(p, r));
     copies_wait<0>();
 }
 
-// Final states of packed sequences (and of sequences without tokens): one thread per
-// (sequence, channel), after the convolution, so that a final state may be the initial
-// state's own buffer.
+// Final states of calls whose final state is the initial state's own buffer, which several
+// runs read: one thread per (sequence, channel), after the convolution.
 template <typename E>
 __global__ void __launch_bounds__(kThreads) conv_state_kernel(ConvParams p) {
     const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -208,6 +219,8 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvParams p, Run
     const int tid = threadIdx.x, lane = tid % kLanes, group = tid / kLanes;
     const int64_t block = blockIdx.x / channel_blocks, q = block * kGroups + group;
     const int64_t c0 = (int64_t)(blockIdx.x % channel_blocks) * kLanes * V, c = c0 + lane * V;
+    // a sequence without tokens passes the final state's gradient to the initial state
+    if (p.cu_seqlens && p.dinit) each_empty(p, [&](int64_t k) { p.dinit[k] = p.dfinal ? p.dfinal[k] : 0.f; });
     float dw[W][V], db[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -331,18 +344,13 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvParams p, Run
     }
 }
 
-// Sequences without tokens pass the final state's gradient to the initial state.
+// The same for a call without any token.
 __global__ void __launch_bounds__(kThreads) conv_empty_kernel(ConvParams p) {
-    const int64_t n = (int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes, row = (p.W - 1) * p.D;
-    if (n >= p.N) return;
-    int64_t lo, hi;
-    seq_rows(p, n, lo, hi);
-    if (lo < hi) return;
-    for (int64_t k = n * row + threadIdx.x % kLanes; k < (n + 1) * row; k += kLanes) p.dinit[k] = p.dfinal ? p.dfinal[k] : 0.f;
+    each_empty(p, [&](int64_t k) { p.dinit[k] = p.dfinal ? p.dfinal[k] : 0.f; });
 }
 
 // part [parts, W+1, D] to dweight [D, W] and dbias [D].
-__global__ void __launch_bounds__(1024) conv_param_sum_kernel(ConvParams p, int64_t parts, const float *part) {
+__global__ void __launch_bounds__(kSumThreads) conv_param_sum_kernel(ConvParams p, int64_t parts, const float *part) {
     const int64_t width = (p.W + 1) * p.D, k = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     const float t = column_sum(part, parts, width, k, k < width);
     if (threadIdx.x >= 32 || k >= width) return;
@@ -394,9 +402,13 @@ size_t conv_bwd_scratch_bytes(const ConvParams &p, int sms) {
     return (size_t)(run_blocks(plan_runs(p, sms)) * (p.W + 1) * p.D) * sizeof(float);
 }
 
-cudaError_t launch_conv_fwd(const ConvParams &p, int sms, cudaStream_t stream) {
+cudaError_t launch_conv_fwd(const ConvParams &p0, int sms, cudaStream_t stream) {
+    ConvParams p = p0;
     const Runs runs = plan_runs(p, sms);
-    return with_shape(p, [&](auto *tag, auto WIDE, auto W) {
+    // the convolution writes the final states unless it may still read them as initial ones
+    const bool apart = p.fin && (p.rows == 0 || (p.fin == p.init && (p.cu_seqlens || runs.per_seq > 1)));
+    if (apart) p.fin = nullptr;
+    return with_shape(p0, [&](auto *tag, auto WIDE, auto W) {
         using E = std::remove_pointer_t<decltype(tag)>;
         const int64_t blocks = ceil_div(p.D, kLanes * V);
         if (p.rows > 0) {
@@ -406,8 +418,7 @@ cudaError_t launch_conv_fwd(const ConvParams &p, int sms, cudaStream_t stream) {
             if (e != cudaSuccess) return e;
             kernel<<<(unsigned)(run_blocks(runs) * blocks), kThreads, smem, stream>>>(p, runs, (int)blocks);
         }
-        if (p.fin && (p.cu_seqlens || p.T == 0))
-            conv_state_kernel<E><<<(unsigned)ceil_div(p.N * p.D, kThreads), kThreads, 0, stream>>>(p);
+        if (apart) conv_state_kernel<E><<<(unsigned)ceil_div(p.N * p.D, kThreads), kThreads, 0, stream>>>(p0);
         return cudaGetLastError();
     });
 }
@@ -415,8 +426,8 @@ cudaError_t launch_conv_fwd(const ConvParams &p, int sms, cudaStream_t stream) {
 cudaError_t launch_conv_bwd(const ConvParams &p, unsigned char *ws, int sms, cudaStream_t stream) {
     const Runs runs = plan_runs(p, sms);
     float *part = reinterpret_cast<float *>(ws);
-    if (p.dinit && p.N > 0 && (p.cu_seqlens || p.T == 0))
-        conv_empty_kernel<<<(unsigned)ceil_div(p.N, kGroups), kThreads, 0, stream>>>(p);
+    if (p.rows == 0 && p.dinit && p.N > 0)
+        conv_empty_kernel<<<(unsigned)std::min(p.N, (int64_t)sms), kThreads, 0, stream>>>(p);
     const cudaError_t e = with_shape(p, [&](auto *tag, auto WIDE, auto W) {
         using E = std::remove_pointer_t<decltype(tag)>;
         const int64_t blocks = ceil_div(p.D, kLanes * V);
@@ -429,7 +440,7 @@ cudaError_t launch_conv_bwd(const ConvParams &p, unsigned char *ws, int sms, cud
         return cudaGetLastError();
     });
     if (e != cudaSuccess) return e;
-    conv_param_sum_kernel<<<(unsigned)ceil_div((p.W + 1) * p.D, 32), 1024, 0, stream>>>(p, run_blocks(runs), part);
+    conv_param_sum_kernel<<<(unsigned)ceil_div((p.W + 1) * p.D, 32), kSumThreads, 0, stream>>>(p, run_blocks(runs), part);
     return cudaGetLastError();
 }
 
