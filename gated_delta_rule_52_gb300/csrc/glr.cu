@@ -67,38 +67,44 @@ constexpr int kFwdCtas = 5;
 template <typename E>
 struct FwdShared {
     using S = FwdShape;
-    Pack<E, S::V> raw[3][S::L][S::THREADS];               // x, i, g
-    Pack<GateConst, S::V> gates[S::THREADS];
+    Pack<E, S::V> raw[3][S::ROWS][S::CL];                 // x, i, g
+    Pack<GateConst, S::V> gates[S::CL];
     Pack<float, S::V> A[S::RG][S::CL], H[S::RG][S::CL];   // maps of the row groups
     Pack<float, S::V> h[S::RG][S::CL];                    // states that enter them
     TileMarks<S::ROWS> marks;
+    uint64_t arrived;                                     // of a tile's copies
 };
 
-template <typename E, bool WIDE, bool UB>
-__global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas) glr_fwd_scan_kernel(GlrParams p, ScanPlan s) {
+template <typename E, bool TMA, bool UB>
+__global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas)
+    glr_fwd_scan_kernel(GlrParams p, ScanPlan s, const __grid_constant__ ScanMaps maps) {
+    using namespace sm103;
     using S = FwdShape;
     constexpr int CL = S::CL, V = S::V, L = S::L, CB = S::CB, RG = S::RG;
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(128) unsigned char smem[];
     FwdShared<E> &sh = *reinterpret_cast<FwdShared<E> *>(smem);
     const int tid = threadIdx.x, lane = tid % CL, rg = tid / CL;
     const float lb2 = p.lower_bound * kLog2e;
     const int D = (int)p.D;
 
-    // starts the copies of a tile's inputs into this thread's own slots
+    // starts the copies of a tile's inputs
     const auto fetch = [&](const TileWalk &w) {
-        if (w.rt < s.row_tiles) {
-            const int64_t r0 = w.rt * S::ROWS + rg * L;
-            const int c = w.cb * CB + lane * V;
-            if (c < D) {
-                const int left = (int)min(p.rows - r0, (int64_t)L);
-                const auto copy = [&](int k, const void *src, int64_t stride) {
-                    copy_rows<E, V, WIDE, L, S::THREADS>(&sh.raw[k][0][tid], static_cast<const E *>(src) + r0 * stride + c, stride,
-                                                         left, D - c);
-                };
-                copy(0, p.x, p.xs);
-                copy(1, p.i, p.is);
-                copy(2, p.g, p.gs);
+        if (w.rt >= s.row_tiles) return;
+        if constexpr (TMA) {
+            if (tid == 0) {
+                mbar_arrive_expect_tx(&sh.arrived, sizeof(sh.raw) + sizeof(sh.gates));
+#pragma unroll
+                for (int k = 0; k < 3; ++k) tma_tile(sh.raw[k], maps.m[k], &sh.arrived, w.cb * CB, (int)w.rt * S::ROWS);
             }
+        } else {
+            const int64_t r0 = w.rt * S::ROWS + rg * L;
+            const int c = w.cb * CB + lane * V, left = (int)min(p.rows - r0, (int64_t)L);
+            const auto copy = [&](int k, const void *src, int64_t stride) {
+                copy_rows<E, V, false, L, CL>(&sh.raw[k][rg * L][lane], static_cast<const E *>(src) + r0 * stride + c, stride, left, D - c);
+            };
+            copy(0, p.x, p.xs);
+            copy(1, p.i, p.is);
+            copy(2, p.g, p.gs);
         }
     };
     // and of what the scan's first part has left for the tile; returns its first sequence
@@ -106,41 +112,59 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas) glr_fwd_scan_kern
         int first = 0;
         if (w.rt < s.row_tiles) {
             first = s.first_seq[w.rt];
-            copy_gates<V>(&sh.gates[tid], s.gates + w.cb * CB + lane * V);
+            const GateConst *gates = s.gates + w.cb * CB;
+            if constexpr (TMA) {
+                if (tid == 0) bulk_load(smem_u32(sh.gates), gates, sizeof(sh.gates), smem_u32(&sh.arrived));
+            } else {
+                if (tid < CB / 2) copy_async<16>(&sh.gates[0].e[0] + 2 * tid, gates + 2 * tid);
+            }
         }
-        copies_commit();
+        if constexpr (!TMA) copies_commit();
         return first;
     };
+    const auto copies_arrive = [&](uint32_t parity) {
+        if constexpr (TMA) {
+            if (!mbar_wait(&sh.arrived, parity, kCopyWaitNs)) atomicExch(p.err, kErrTimeout);
+        } else {
+            copies_wait<0>();
+            __syncthreads();
+        }
+    };
 
+    if (TMA && tid == 0) {
+        mbar_init(&sh.arrived, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
     TileWalk w(s);
     fetch(w);
     prepare_scan<UB, false>(p, s);
+    if (TMA) fence_proxy_async_global();   // the gates are read by bulk copies
     cooperative_groups::this_grid().sync();
+    if (TMA) fence_proxy_async_global();
     int first = fetch_plan(w);
-    while (w.rt < s.row_tiles) {
+    for (uint32_t parity = 0; w.rt < s.row_tiles; parity ^= 1) {
         const int64_t rt = w.rt, r0 = rt * S::ROWS + rg * L;
         const int block = w.cb * CB, c = block + lane * V;
         const bool marked = mark_tile(p, rt, first, sh.marks);
         const bool plain = !marked && (rt + 1) * S::ROWS <= p.rows;   // every row inside one sequence
-        copies_wait<0>();   // this thread's own copies: no barrier needed
+        copies_arrive(parity);
 
         float a[L][V], b[L][V];
         {
-            const ChannelGates<V> gc(sh.gates[tid]);
+            const ChannelGates<V> gc(sh.gates[lane]);
 #pragma unroll
             for (int r = 0; r < L; ++r) {
                 float x[V], i[V], g[V];
-                unpack<E, V>(sh.raw[0][r][tid], x);
-                unpack<E, V>(sh.raw[1][r][tid], i);
-                unpack<E, V>(sh.raw[2][r][tid], g);
+                unpack<E, V>(sh.raw[0][rg * L + r][lane], x);
+                unpack<E, V>(sh.raw[1][rg * L + r][lane], i);
+                unpack<E, V>(sh.raw[2][rg * L + r][lane], g);
                 gate_decay_n<UB, V>(a[r], g, gc.k0, gc.k1, lb2);
                 sigmoid_n<V>(b[r], i);
                 mul_n<V>(b[r], b[r], x);
             }
         }
         w.next();
-        fetch(w);   // the slots are free: the next tile's copies run beside the rest
-        first = fetch_plan(w);
         Pack<float, V> mA, mH;
         if (plain) {
 #pragma unroll
@@ -184,21 +208,23 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas) glr_fwd_scan_kern
         sh.A[rg][lane] = mA;
         sh.H[rg][lane] = mH;
         __syncthreads();
+        fetch(w);   // the inputs are in registers: the next tile's copies run beside the rest
+        first = fetch_plan(w);
 
         const int64_t group = rt >> s.group_log2;
         const int pos = (int)(rt - (group << s.group_log2)), last = (1 << s.group_log2) - 1;
         const int ch = tid % CB;
-        const auto map = [&](int q) { return Affine{sh.A[q][ch / V].e[ch % V], sh.H[q][ch / V].e[ch % V]}; };
         if (tid < CB) {
             // one thread per channel: the tile's map, handed on
             if (pos != last) {
-                Affine t = map(0);
+                const GroupMaps<RG, CL, V> maps(sh.A, sh.H, ch);
+                Affine t = maps.m[0];
                 if (plain) {
 #pragma unroll
-                    for (int q = 1; q < RG; ++q) t = joined<false>(t, map(q));
+                    for (int q = 1; q < RG; ++q) t = joined<false>(t, maps.m[q]);
                 } else {
 #pragma unroll
-                    for (int q = 1; q < RG; ++q) t = joined<true>(t, map(q));
+                    for (int q = 1; q < RG; ++q) t = joined<true>(t, maps.m[q]);
                 }
                 publish(s.maps + rt * s.width + block + ch, t);
             }
@@ -209,10 +235,11 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas) glr_fwd_scan_kern
             const uint32_t h_bits = group > 0 ? peek(before) : 0;
             const Affine t = join_maps(s.maps + (rt - pos) * s.width + block + ch, s.width, pos, p.err);
             float h = apply(t, group > 0 ? __uint_as_float(await(before, h_bits, p.err)) : 0.f);
+            const GroupMaps<RG, CL, V> maps(sh.A, sh.H, ch);
 #pragma unroll
             for (int q = 0; q < RG; ++q) {
                 sh.h[q][ch / V].e[ch % V] = h;
-                h = plain ? applied<false>(map(q), h) : applied<true>(map(q), h);
+                h = plain ? applied<false>(maps.m[q], h) : applied<true>(maps.m[q], h);
             }
             if (pos == last) publish(s.states + group * s.width + block + ch, h);
         }
@@ -230,7 +257,7 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas) glr_fwd_scan_kern
 #pragma unroll
                 for (int r = 0; r < L; ++r, out += p.os) {
                     fma_n<V>(h, a[r], h, b[r]);
-                    if (p.out) st_cols<E, V, WIDE>(out, h, cols);
+                    if (p.out) st_cols<E, V, TMA>(out, h, cols);
                 }
             } else {
 #pragma unroll
@@ -238,7 +265,7 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas) glr_fwd_scan_kern
                     if (r0 + r >= p.rows) break;
 #pragma unroll
                     for (int v = 0; v < V; ++v) h[v] = apply(Affine{a[r][v], b[r][v]}, h[v]);
-                    if (p.out) st_cols<E, V, WIDE>(out, h, cols);
+                    if (p.out) st_cols<E, V, TMA>(out, h, cols);
                     const int n = marked && p.fin ? sh.marks.ends[rg * L + r] : -1;
 #pragma unroll
                     for (int v = 0; v < V; ++v)
@@ -247,7 +274,6 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas) glr_fwd_scan_kern
             }
         }
     }
-    copies_wait<0>();
 }
 
 // Rows of a fixed-length call up to which the step kernel runs.
@@ -255,31 +281,35 @@ constexpr int64_t kStepMaxT = 16;
 
 bool step_takes(const GlrParams &p) { return !p.cu_seqlens && p.T <= kStepMaxT; }
 
-// Whether every row of x, i, g and out allows loads of 4 elements.
-bool vector_rows(const GlrParams &p) {
-    const size_t n = 4 * dtype_bytes(p.dtype);
-    const void *ptrs[] = {p.x, p.i, p.g, p.out};
-    for (const void *q : ptrs)
-        if (reinterpret_cast<uintptr_t>(q) % n) return false;
-    return p.D % 4 == 0 && p.xs % 4 == 0 && p.is % 4 == 0 && p.gs % 4 == 0 && (!p.out || p.os % 4 == 0);
+// Rows that tensor maps take, and 16-byte stores of the step kernel's and the scan's groups.
+bool aligned_rows(const GlrParams &p) {
+    const size_t e = dtype_bytes(p.dtype);
+    return tma_rows(p.x, p.xs, p.D, e) && tma_rows(p.i, p.is, p.D, e) && tma_rows(p.g, p.gs, p.D, e) &&
+           (!p.out || tma_rows(p.out, p.os, p.D, e));
 }
 
-template <typename E, bool WIDE, bool UB>
+template <typename E, bool TMA, bool UB>
 cudaError_t run(const GlrParams &p, unsigned char *ws, int sms, cudaStream_t stream) {
     if (step_takes(p)) {
-        constexpr int V = WIDE ? 4 : 1;
+        constexpr int V = TMA ? 4 : 1;
         glr_fwd_step_kernel<E, V, UB><<<(unsigned)ceil_div(p.N * (p.D / V), 128), 128, 0, stream>>>(p);
         return cudaGetLastError();
     }
     ScanPlan s = scan_plan<FwdShape>(p.rows, p.D, ws, nullptr);
-    constexpr auto kernel = glr_fwd_scan_kernel<E, WIDE, UB>;
+    ScanMaps maps{};
+    if (TMA && p.rows > 0 &&
+        !(encode_tile_map<FwdShape>(maps.m[0], p.x, p.xs, p.rows, p.D, p.dtype) &&
+          encode_tile_map<FwdShape>(maps.m[1], p.i, p.is, p.rows, p.D, p.dtype) &&
+          encode_tile_map<FwdShape>(maps.m[2], p.g, p.gs, p.rows, p.D, p.dtype)))
+        return cudaErrorUnknown;
+    constexpr auto kernel = glr_fwd_scan_kernel<E, TMA, UB>;
     constexpr int bytes = (int)sizeof(FwdShared<E>);
     int ctas = 0;
     const cudaError_t e = resident_ctas<kernel>(FwdShape::THREADS, bytes, ctas);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)std::max(std::min(s.row_tiles * s.blocks, (int64_t)sms * ctas), (int64_t)1);
     GlrParams arg = p;
-    void *args[] = {&arg, &s};
+    void *args[] = {&arg, &s, &maps};
     return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(FwdShape::THREADS), args, bytes, stream);
 }
 
@@ -295,7 +325,7 @@ size_t glr_fwd_scratch_bytes(const GlrParams &p, int) {
 cudaError_t launch_glr_fwd(const GlrParams &p, unsigned char *ws, int sms, cudaStream_t stream) {
     return with_dtype(p.dtype, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
-        if (vector_rows(p)) return p.unbounded ? run<E, true, true>(p, ws, sms, stream) : run<E, true, false>(p, ws, sms, stream);
+        if (aligned_rows(p)) return p.unbounded ? run<E, true, true>(p, ws, sms, stream) : run<E, true, false>(p, ws, sms, stream);
         return p.unbounded ? run<E, false, true>(p, ws, sms, stream) : run<E, false, false>(p, ws, sms, stream);
     });
 }

@@ -28,46 +28,53 @@ template <typename E> using BwdShape = TileShape<kGlrCheckpointRows, sizeof(E) =
 template <typename E>
 struct BwdShared {
     using S = BwdShape<E>;
-    Pack<E, S::V> raw[2][4][S::L][S::THREADS];                     // x, i, g, dout
-    Pack<GateConst, S::V> gates[2][S::THREADS];
+    Pack<E, S::V> raw[2][4][S::ROWS][S::CL];                       // x, i, g, dout
+    Pack<GateConst, S::V> gates[2][S::CL];
     Pack<float, S::V> A[S::RG][S::CL], H[S::RG][S::CL];            // forward maps of the row groups
     Pack<float, S::V> B[S::RG][S::CL], F[S::RG][S::CL];            // backward maps
     // states that enter them, and over each thread's own two its sums of parameter gradients
     Pack<float, S::V> h[S::RG][S::CL], f[S::RG][S::CL];
     TileMarks<S::ROWS> marks;
+    uint64_t arrived[2];                                           // of a tile's copies
 };
 
-template <typename E, bool WIDE, bool UB>
+template <typename E, bool TMA, bool UB>
 __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
-    glr_bwd_scan_kernel(GlrParams p, ScanPlan s, float *part_ddt, float *part_dA) {
+    glr_bwd_scan_kernel(GlrParams p, ScanPlan s, const __grid_constant__ ScanMaps maps, float *part_ddt, float *part_dA) {
+    using namespace sm103;
     using S = BwdShape<E>;
     constexpr int CL = S::CL, V = S::V, L = S::L, CB = S::CB, RG = S::RG;
     constexpr bool EXACT = sizeof(E) == 4;
     static_assert(S::THREADS >= 3 * CB && L * V == 16, "roles");
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(128) unsigned char smem[];
     BwdShared<E> &sh = *reinterpret_cast<BwdShared<E> *>(smem);
     const int tid = threadIdx.x, lane = tid % CL, rg = tid / CL;
     const int role = tid / CB, ch = tid % CB, D = (int)p.D;
     const float lb2 = p.lower_bound * kLog2e;
     float checkpoint = 0.f;   // of role 2's channel, fetched with the tile
 
-    // tile number w.rt counts from the last row tile
+    // starts the copies of a tile's inputs; tile number w.rt counts from the last row tile
     const auto fetch = [&](const TileWalk &w, int stage) {
-        if (w.rt < s.row_tiles) {
-            const int64_t rt = s.row_tiles - 1 - w.rt, r0 = rt * S::ROWS + rg * L;
-            const int c = w.cb * CB + lane * V;
-            if (role == 2 && w.cb * CB + ch < D) checkpoint = p.checkpoints[rt * p.D + w.cb * CB + ch];
-            if (c < D) {
-                const int left = (int)min(p.rows - r0, (int64_t)L);
-                const auto copy = [&](int k, const void *src, int64_t stride) {
-                    copy_rows<E, V, WIDE, L, S::THREADS>(&sh.raw[stage][k][0][tid], static_cast<const E *>(src) + r0 * stride + c,
-                                                         stride, left, D - c);
-                };
-                copy(0, p.x, p.xs);
-                copy(1, p.i, p.is);
-                copy(2, p.g, p.gs);
-                copy(3, p.dout, p.ds);
+        if (w.rt >= s.row_tiles) return;
+        const int64_t rt = s.row_tiles - 1 - w.rt;
+        if (role == 2 && w.cb * CB + ch < D) checkpoint = p.checkpoints[rt * p.D + w.cb * CB + ch];
+        if constexpr (TMA) {
+            if (tid == 0) {
+                mbar_arrive_expect_tx(&sh.arrived[stage], sizeof(sh.raw[0]) + sizeof(sh.gates[0]));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tma_tile(sh.raw[stage][k], maps.m[k], &sh.arrived[stage], w.cb * CB, (int)rt * S::ROWS);
             }
+        } else {
+            const int64_t r0 = rt * S::ROWS + rg * L;
+            const int c = w.cb * CB + lane * V, left = (int)min(p.rows - r0, (int64_t)L);
+            const auto copy = [&](int k, const void *src, int64_t stride) {
+                copy_rows<E, V, false, L, CL>(&sh.raw[stage][k][rg * L][lane], static_cast<const E *>(src) + r0 * stride + c, stride,
+                                              left, D - c);
+            };
+            copy(0, p.x, p.xs);
+            copy(1, p.i, p.is);
+            copy(2, p.g, p.gs);
+            copy(3, p.dout, p.ds);
         }
     };
     // and of what the scan's first part has left for the tile; returns its first sequence
@@ -75,17 +82,39 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
         int first = 0;
         if (w.rt < s.row_tiles) {
             first = s.first_seq[s.row_tiles - 1 - w.rt];
-            copy_gates<V>(&sh.gates[stage][tid], s.gates + w.cb * CB + lane * V);
+            const GateConst *gates = s.gates + w.cb * CB;
+            if constexpr (TMA) {
+                if (tid == 0) bulk_load(smem_u32(sh.gates[stage]), gates, sizeof(sh.gates[0]), smem_u32(&sh.arrived[stage]));
+            } else {
+                if (tid < CB / 2) copy_async<16>(&sh.gates[stage][0].e[0] + 2 * tid, gates + 2 * tid);
+            }
         }
-        copies_commit();
+        if constexpr (!TMA) copies_commit();
         return first;
     };
+    const auto copies_arrive = [&](int stage, uint32_t parity) {
+        if constexpr (TMA) {
+            if (!mbar_wait(&sh.arrived[stage], parity, kCopyWaitNs)) atomicExch(p.err, kErrTimeout);
+        } else {
+            copies_wait<1>();
+            __syncthreads();
+        }
+    };
 
+    if (TMA && tid == 0) {
+        mbar_init(&sh.arrived[0], 1);
+        mbar_init(&sh.arrived[1], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
     TileWalk w(s);
     fetch(w, 0);
     prepare_scan<UB, true>(p, s);
+    if (TMA) fence_proxy_async_global();   // the gates are read by bulk copies
     cooperative_groups::this_grid().sync();
+    if (TMA) fence_proxy_async_global();
     int next_first = fetch_plan(w, 0);
+    uint32_t parity = 0;   // of stage 0's copies; stage 1's turn comes in between
     for (int stage = 0; w.rt < s.row_tiles; stage ^= 1) {
         const int64_t walk = w.rt, rt = s.row_tiles - 1 - walk, r0 = rt * S::ROWS + rg * L;
         const int c = w.cb * CB + lane * V, block = w.cb * CB, cols = D - c, first = next_first;
@@ -96,10 +125,11 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
         const bool marked = mark_tile(p, rt, first, sh.marks);
         const bool plain = !marked && (rt + 1) * S::ROWS <= p.rows;        // every row inside one sequence
         const int left = cols > 0 ? (int)min(p.rows - r0, (int64_t)L) : 0;   // rows of this thread that exist
-        copies_wait<1>();   // this thread's own copies: no barrier needed
+        copies_arrive(stage, parity);
+        parity ^= stage;
 
-        const ChannelGates<V> gc(sh.gates[stage][tid]);
-        const auto raw = [&](int k, int r, float (&f)[V]) { unpack<E, V>(sh.raw[stage][k][r][tid], f); };
+        const ChannelGates<V> gc(sh.gates[stage][lane]);
+        const auto raw = [&](int k, int r, float (&f)[V]) { unpack<E, V>(sh.raw[stage][k][rg * L + r][lane], f); };
         float a[L][V], kept_g[L][V], kept_i[L][V];   // for the second half
         Pack<float, V> mA, mH, mB, mF;
 #pragma unroll
@@ -152,18 +182,17 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
 
         const int64_t group = walk >> s.group_log2;
         const int pos = (int)(walk - (group << s.group_log2)), last = (1 << s.group_log2) - 1;
-        const auto back = [&](int q) { return Affine{sh.B[q][ch / V].e[ch % V], sh.F[q][ch / V].e[ch % V]}; };
-        const auto ahead = [&](int q) { return Affine{sh.A[q][ch / V].e[ch % V], sh.H[q][ch / V].e[ch % V]}; };
         if (role == 0) {
             // the tile's backward map, handed on
             if (pos != last) {
-                Affine t = back(RG - 1);
+                const GroupMaps<RG, CL, V> back(sh.B, sh.F, ch);
+                Affine t = back.m[RG - 1];
                 if (plain) {
 #pragma unroll
-                    for (int q = RG - 2; q >= 0; --q) t = joined<false>(t, back(q));
+                    for (int q = RG - 2; q >= 0; --q) t = joined<false>(t, back.m[q]);
                 } else {
 #pragma unroll
-                    for (int q = RG - 2; q >= 0; --q) t = joined<true>(t, back(q));
+                    for (int q = RG - 2; q >= 0; --q) t = joined<true>(t, back.m[q]);
                 }
                 publish(s.maps + walk * s.width + block + ch, t);
             }
@@ -173,19 +202,21 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
             const uint32_t f_bits = group > 0 ? peek(before) : 0;
             const Affine t = join_maps(s.maps + (walk - pos) * s.width + block + ch, s.width, pos, p.err);
             float f = apply(t, group > 0 ? __uint_as_float(await(before, f_bits, p.err)) : 0.f);
+            const GroupMaps<RG, CL, V> back(sh.B, sh.F, ch);
 #pragma unroll
             for (int q = RG - 1; q >= 0; --q) {
                 sh.f[q][ch / V].e[ch % V] = f;
-                f = plain ? applied<false>(back(q), f) : applied<true>(back(q), f);
+                f = plain ? applied<false>(back.m[q], f) : applied<true>(back.m[q], f);
             }
             if (pos == last) publish(s.states + group * s.width + block + ch, f);
         } else if (role == 2) {
             // the forward states that enter the row groups
+            const GroupMaps<RG, CL, V> fore(sh.A, sh.H, ch);
             float h = h_tile;
 #pragma unroll
             for (int q = 0; q < RG; ++q) {
                 sh.h[q][ch / V].e[ch % V] = h;
-                h = plain ? applied<false>(ahead(q), h) : applied<true>(ahead(q), h);
+                h = plain ? applied<false>(fore.m[q], h) : applied<true>(fore.m[q], h);
             }
         }
         __syncthreads();
@@ -216,14 +247,14 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
             mul_n<V>(f, ar, grad);
             input_gates_n<EXACT, V>(si, o, i, ki);
             mul_n<V>(out, grad, si);
-            st_cols<E, V, WIDE>(static_cast<E *>(p.dx) + row_at + r * p.D, out, cols);
+            st_cols<E, V, TMA>(static_cast<E *>(p.dx) + row_at + r * p.D, out, cols);
             mul_n<V>(out, out, o);
             mul_n<V>(out, out, x);
-            st_cols<E, V, WIDE>(static_cast<E *>(p.di) + row_at + r * p.D, out, cols);
+            st_cols<E, V, TMA>(static_cast<E *>(p.di) + row_at + r * p.D, out, cols);
             gate_slopes_n<UB, V>(slope, rate, g, kg, gc.k0, gc.k1, p.lower_bound);
             mul_n<V>(o, f, start);        // the gradient of gk
             mul_n<V>(out, o, slope);
-            st_cols<E, V, WIDE>(static_cast<E *>(p.dg) + row_at + r * p.D, out, cols);
+            st_cols<E, V, TMA>(static_cast<E *>(p.dg) + row_at + r * p.D, out, cols);
             add_n<V>(ddt.e, ddt.e, out);
             fma_n<V>(dA.e, o, rate, dA.e);
         };
@@ -276,7 +307,6 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
             (role == 0 ? part_ddt : part_dA)[rt * s.width + block + ch] = t;
         }
     }
-    copies_wait<0>();
 }
 
 // Sums the tiles' partial parameter gradients [parts, width] over the tiles: a CTA per head
@@ -345,13 +375,11 @@ GlrParams states_only(const GlrParams &p) {
     return f;
 }
 
-// Whether every row of the inputs and gradients allows loads of a thread's V elements.
-bool vector_rows(const GlrParams &p) {
-    const size_t V = p.dtype == kFP32 ? 2 : 4, n = V * dtype_bytes(p.dtype);
-    const void *ptrs[] = {p.x, p.i, p.g, p.dout, p.dx, p.di, p.dg};
-    for (const void *q : ptrs)
-        if (reinterpret_cast<uintptr_t>(q) % n) return false;
-    return p.D % V == 0 && p.xs % V == 0 && p.is % V == 0 && p.gs % V == 0 && p.ds % V == 0;
+// Rows that tensor maps take, and gradients that allow stores of a thread's groups.
+bool aligned_rows(const GlrParams &p) {
+    const size_t e = dtype_bytes(p.dtype);
+    return tma_rows(p.x, p.xs, p.D, e) && tma_rows(p.i, p.is, p.D, e) && tma_rows(p.g, p.gs, p.D, e) && tma_rows(p.dout, p.ds, p.D, e) &&
+           tma_rows(p.dx, p.D, p.D, e) && tma_rows(p.di, p.D, p.D, e) && tma_rows(p.dg, p.D, p.D, e);
 }
 
 // Workspace: the scan's, the partial sums, the checkpoints and the forward run's workspace.
@@ -375,18 +403,24 @@ BwdPlan bwd_plan(const GlrParams &p, int sms, unsigned char *ws) {
     return b;
 }
 
-template <typename E, bool WIDE, bool UB>
+template <typename E, bool TMA, bool UB>
 cudaError_t run(const GlrParams &p, const BwdPlan &b, int sms, cudaStream_t stream) {
     ScanPlan s = b.s;
+    using S = BwdShape<E>;
+    ScanMaps maps{};
+    if (TMA && p.rows > 0 &&
+        !(encode_tile_map<S>(maps.m[0], p.x, p.xs, p.rows, p.D, p.dtype) && encode_tile_map<S>(maps.m[1], p.i, p.is, p.rows, p.D, p.dtype) &&
+          encode_tile_map<S>(maps.m[2], p.g, p.gs, p.rows, p.D, p.dtype) && encode_tile_map<S>(maps.m[3], p.dout, p.ds, p.rows, p.D, p.dtype)))
+        return cudaErrorUnknown;
     int ctas = 0;
     constexpr int bytes = (int)sizeof(BwdShared<E>);
-    constexpr auto kernel = glr_bwd_scan_kernel<E, WIDE, UB>;
+    constexpr auto kernel = glr_bwd_scan_kernel<E, TMA, UB>;
     const cudaError_t e = resident_ctas<kernel>(BwdShape<E>::THREADS, bytes, ctas);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)std::max(std::min(s.row_tiles * s.blocks, (int64_t)sms * ctas), (int64_t)1);
     GlrParams arg = p;
     float *ddt = b.part_ddt, *dA = b.part_dA;
-    void *args[] = {&arg, &s, &ddt, &dA};
+    void *args[] = {&arg, &s, &maps, &ddt, &dA};
     return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(BwdShape<E>::THREADS), args,
                                        bytes, stream);
 }
@@ -405,7 +439,7 @@ cudaError_t launch_glr_bwd(const GlrParams &p0, unsigned char *ws, int sms, cuda
             e = launch_glr_fwd(states_only(p), b.fwd, sms, stream);
             if (e != cudaSuccess) return e;
         }
-        const bool vec = vector_rows(p);
+        const bool vec = aligned_rows(p);
         e = with_dtype(p.dtype, [&](auto *tag) {
             using E = std::remove_pointer_t<decltype(tag)>;
             if (vec) return p.unbounded ? run<E, true, true>(p, b, sms, stream) : run<E, true, false>(p, b, sms, stream);

@@ -40,18 +40,16 @@ __device__ __forceinline__ void copy_rows(Pack<E, V> *slots, const E *src, int64
         }
     } else {
         constexpr int G = 4;   // rows in registers together
+        E t[G * V];
 #pragma unroll
         for (int r0 = 0; r0 < N; r0 += G) {
-            Pack<E, V> t[G];
 #pragma unroll
-            for (int r = 0; r < G; ++r, src += stride) {
+            for (int k = 0; k < G * V; ++k)
+                if (r0 + k / V < count && k % V < cols) t[k] = src[k / V * stride + k % V];
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (r0 + r < count && v < cols) t[r].e[v] = src[v];
-            }
-#pragma unroll
-            for (int r = 0; r < G; ++r)
-                if (r0 + r < count) slots[(r0 + r) * THREADS] = t[r];
+            for (int k = 0; k < G * V; ++k)
+                if (r0 + k / V < count && k % V < cols) slots[(r0 + k / V) * THREADS].e[k % V] = t[k];
+            src += G * stride;
         }
     }
 }
