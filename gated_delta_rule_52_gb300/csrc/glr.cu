@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas)
             if (tid == 0) {
                 mbar_arrive_expect_tx(&sh.arrived, sizeof(sh.raw) + sizeof(sh.gates));
 #pragma unroll
-                for (int k = 0; k < 3; ++k) tma_tile(sh.raw[k], maps.m[k], &sh.arrived, w.cb * CB, (int)w.rt * S::ROWS);
+                for (int k = 0; k < 3; ++k) tma_box(sh.raw[k], maps.m[k], &sh.arrived, w.cb * CB, (int)w.rt * S::ROWS);
             }
         } else {
             const int64_t r0 = w.rt * S::ROWS + rg * L;
@@ -298,9 +298,9 @@ cudaError_t run(const GlrParams &p, unsigned char *ws, int sms, cudaStream_t str
     ScanPlan s = scan_plan<FwdShape>(p.rows, p.D, ws, nullptr);
     ScanMaps maps{};
     if (TMA && p.rows > 0 &&
-        !(encode_tile_map<FwdShape>(maps.m[0], p.x, p.xs, p.rows, p.D, p.dtype) &&
-          encode_tile_map<FwdShape>(maps.m[1], p.i, p.is, p.rows, p.D, p.dtype) &&
-          encode_tile_map<FwdShape>(maps.m[2], p.g, p.gs, p.rows, p.D, p.dtype)))
+        !(encode_tile_map(maps.m[0], p.x, p.xs, p.rows, p.D, p.dtype, FwdShape::CB, FwdShape::ROWS) &&
+          encode_tile_map(maps.m[1], p.i, p.is, p.rows, p.D, p.dtype, FwdShape::CB, FwdShape::ROWS) &&
+          encode_tile_map(maps.m[2], p.g, p.gs, p.rows, p.D, p.dtype, FwdShape::CB, FwdShape::ROWS)))
         return cudaErrorUnknown;
     constexpr auto kernel = glr_fwd_scan_kernel<E, TMA, UB>;
     constexpr int bytes = (int)sizeof(FwdShared<E>);

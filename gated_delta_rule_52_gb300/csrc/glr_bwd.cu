@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
             if (tid == 0) {
                 mbar_arrive_expect_tx(&sh.arrived[stage], sizeof(sh.raw[0]) + sizeof(sh.gates[0]));
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tma_tile(sh.raw[stage][k], maps.m[k], &sh.arrived[stage], w.cb * CB, (int)rt * S::ROWS);
+                for (int k = 0; k < 4; ++k) tma_box(sh.raw[stage][k], maps.m[k], &sh.arrived[stage], w.cb * CB, (int)rt * S::ROWS);
             }
         } else {
             const int64_t r0 = rt * S::ROWS + rg * L;
@@ -409,8 +409,8 @@ cudaError_t run(const GlrParams &p, const BwdPlan &b, int sms, cudaStream_t stre
     using S = BwdShape<E>;
     ScanMaps maps{};
     if (TMA && p.rows > 0 &&
-        !(encode_tile_map<S>(maps.m[0], p.x, p.xs, p.rows, p.D, p.dtype) && encode_tile_map<S>(maps.m[1], p.i, p.is, p.rows, p.D, p.dtype) &&
-          encode_tile_map<S>(maps.m[2], p.g, p.gs, p.rows, p.D, p.dtype) && encode_tile_map<S>(maps.m[3], p.dout, p.ds, p.rows, p.D, p.dtype)))
+        !(encode_tile_map(maps.m[0], p.x, p.xs, p.rows, p.D, p.dtype, S::CB, S::ROWS) && encode_tile_map(maps.m[1], p.i, p.is, p.rows, p.D, p.dtype, S::CB, S::ROWS) &&
+          encode_tile_map(maps.m[2], p.g, p.gs, p.rows, p.D, p.dtype, S::CB, S::ROWS) && encode_tile_map(maps.m[3], p.dout, p.ds, p.rows, p.D, p.dtype, S::CB, S::ROWS)))
         return cudaErrorUnknown;
     int ctas = 0;
     constexpr int bytes = (int)sizeof(BwdShared<E>);

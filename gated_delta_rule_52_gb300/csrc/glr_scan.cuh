@@ -16,7 +16,6 @@
 #include <cooperative_groups.h>
 
 #include "glr_gate.cuh"
-#include "kda_chunk.cuh"
 #include "layer_copy.cuh"
 
 namespace kda {
@@ -156,37 +155,10 @@ struct ChannelGates {
     }
 };
 
-// Tensor maps of the token tensors [rows, D], boxes of a tile's rows by its channels: one
-// thread loads a tile with one instruction per tensor.  (With 8 bytes per thread and row
-// the copies' own issue was a fifth of a tile's time: 119 us forward and 289 us backward on
-// 8192 x 8192 bf16.)
+// Tensor maps of a scan's inputs: one thread loads a tile with one instruction per tensor.
+// (With 8 bytes per thread and row the copies' own issue was a fifth of a tile's time:
+// 119 us forward and 289 us backward on 8192 x 8192 bf16.)
 struct ScanMaps { CUtensorMap m[4]; };
-
-__device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap &map, uint64_t *bar, int c, int row) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-            sm103::smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(&map)), "r"(sm103::smem_u32(bar)), "r"(c), "r"(row)
-        : "memory");
-}
-
-// A tensor map's demands: 16-byte aligned rows, no row over another.
-inline bool tma_rows(const void *ptr, int64_t stride, int64_t D, size_t elem) {
-    return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && stride * elem % 16 == 0 && D * elem % 16 == 0 && stride >= D;
-}
-template <typename S>
-bool encode_tile_map(CUtensorMap &map, const void *ptr, int64_t stride, int64_t rows, int64_t D, int dtype) {
-    const auto encode = chunk::encode_fn();
-    if (!encode) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * dtype_bytes(dtype)};
-    const cuuint32_t box[2] = {S::CB, S::ROWS}, step[2] = {1, 1};
-    const CUtensorMapDataType type = dtype == kBF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                     : dtype == kFP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-    return encode(&map, type, 2, const_cast<void *>(ptr), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-constexpr uint64_t kCopyWaitNs = 2000000000ull;
 
 // One map after the other where neither cuts.
 template <bool CUTS>

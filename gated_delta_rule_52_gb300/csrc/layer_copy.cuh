@@ -2,6 +2,7 @@
 // results over CTAs.
 #pragma once
 
+#include "kda_chunk.cuh"
 #include "layer_io.cuh"
 #include "sm103.cuh"
 
@@ -76,6 +77,34 @@ __device__ __forceinline__ void ld_cols(const E *p, float (&f)[V], int cols) {
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Tensor maps of token tensors [rows, D]: boxes of `box_rows` rows by `box_cols` channels,
+// dense in shared memory, zeros where the tensor has no elements.
+__device__ __forceinline__ void tma_box(void *dst, const CUtensorMap &map, uint64_t *bar, int c, int row) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            sm103::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(&map)), "r"(sm103::smem_u32(bar)), "r"(c), "r"(row)
+        : "memory");
+}
+constexpr uint64_t kCopyWaitNs = 2000000000ull;
+
+// A tensor map's demands: 16-byte aligned rows, no row over another.
+inline bool tma_rows(const void *ptr, int64_t stride, int64_t D, size_t elem) {
+    return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && stride * elem % 16 == 0 && D * elem % 16 == 0 && stride >= D;
+}
+inline bool encode_tile_map(CUtensorMap &map, const void *ptr, int64_t stride, int64_t rows, int64_t D, int dtype, int box_cols,
+                            int box_rows) {
+    const auto encode = chunk::encode_fn();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * dtype_bytes(dtype)};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    const CUtensorMapDataType type = dtype == kBF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                     : dtype == kFP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    return encode(&map, type, 2, const_cast<void *>(ptr), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Lets a kernel use this much dynamic shared memory; set once per device.
 template <auto Kernel>

@@ -131,7 +131,7 @@ __device__ __forceinline__ void each_empty(const ConvParams &p, F &&f) {
 constexpr int kBatch = 4, kStages = 3;   // rows per copy group, groups of a thread's ring
 
 template <typename E, bool WIDE, int W>
-__global__ void __launch_bounds__(kThreads, 3) conv_fwd_kernel(ConvParams p, Runs runs, int channel_blocks) {
+__global__ void __launch_bounds__(kThreads, 4) conv_fwd_kernel(ConvParams p, Runs runs, int channel_blocks) {
     extern __shared__ __align__(16) unsigned char smem[];
     auto &ring = *reinterpret_cast<Pack<E, V>(*)[kStages][kBatch][kThreads]>(smem);
     const int tid = threadIdx.x;
