@@ -7,7 +7,7 @@
 #include "../../include/kda.h"
 #include "layer.h"
 
-static_assert(KDA_DTYPE_BF16 == kda::kBF16 && KDA_DTYPE_FP32 == kda::kFP32 && KDA_DTYPE_FP16 == kda::kFP16,
+static_assert((int)KDA_DTYPE_BF16 == kda::kBF16 && (int)KDA_DTYPE_FP32 == kda::kFP32 && (int)KDA_DTYPE_FP16 == kda::kFP16,
               "element types of include/kda.h");
 static_assert(KDA_GLR_CHECKPOINT_ROWS == kda::kGlrCheckpointRows, "checkpoint spacing of include/kda.h");
 

@@ -103,6 +103,10 @@ def _glr_check(got, want):
     (1, 1023, 2, 128, BF, F, None, "slice"),
     (2, 1100, 1, 96, F, None, -5.0, "dense"),
     (1, 5000, 1, 20, BF, F, None, "dense"),
+    (2, 200, 1, 600, BF, F, -5.0, "dense"),        # one wide head
+    (1, 130, 40, 3, F, BF, None, "dense"),         # many narrow ones
+    (1, 4500, 1, 8, HF, F, -5.0, "slice"),         # few channels, many tiles
+    (1, 2100, 2, 29, HF, F, None, "odd"),
 ])
 def test_glr(B, T, H, K, dt, sd, lb, how):
     d = _glr_inputs(B, T, H, K, dt, None, sd, T + H)
@@ -455,3 +459,23 @@ def test_offsets_beyond_32_bits():
     _status()
     for a, b in zip(*outs):
         assert torch.allclose(a.float(), b.float(), rtol=2.0 ** -7, atol=0)   # two roundings to bf16
+
+
+# ------------------------------------------------------------------ together
+def test_block_trains_and_serves():
+    from gated_delta_rule_52_gb300 import block
+    gen = _gen(0)
+    blocks = [block.Block(kind, 128, gen) for kind in ("glr", "kda")]
+    losses = block.train(blocks, 25, 2, 200, gen)
+    assert all(b < a for a, b in zip(losses[::8], losses[8::8])), losses
+    u = torch.randn(2, 90, 128, generator=gen).to("cuda", BF)
+    whole, stepped = block.serve(blocks, u, 90), block.serve(blocks, u, 70)
+    _status()
+    # both round every operator's output to bf16 (2^-9 each, a dozen in a row), the delta
+    # rule's chunked form besides holds its operands in fp16
+    assert float((whole.float() - stepped.float()).norm()) <= 2.0 ** -6 * float(whole.float().norm())
+    # and what was trained is what is served
+    h = u
+    for b in blocks:
+        h = b.train(h)
+    assert float((whole.float() - h.float()).norm()) <= 2.0 ** -6 * float(whole.float().norm())
