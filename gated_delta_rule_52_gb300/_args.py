@@ -5,8 +5,6 @@ A decode step's call costs more on the host than on the GPU, so the checks look 
 contiguous tensor once and take the current stream's handle without building a Stream."""
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import kda
@@ -106,9 +104,13 @@ def stream_handle(stream, t) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
-def on(stream):
-    """Allocates what a call returns on the stream that writes it."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def new(stream, t, *shapes):
+    """New contiguous tensors of ``t``'s type and device, allocated on the stream that writes
+    them (None for a shape of None)."""
+    if stream is None:
+        return [None if s is None else t.new_empty(s) for s in shapes]
+    with torch.cuda.stream(stream):
+        return new(None, t, *shapes)
 
 
 def done(status: int) -> None:

@@ -68,12 +68,8 @@ def glr_bwd(x, i, g, A_log, dt_bias, lower_bound, dout, initial_state=None, dfin
     code, init, _ = _args.states(initial_state, None, state)
     dfin = _args.optional("dfinal", dfinal, f32, state)
     ck = None if checkpoints is None else _args.tensor("checkpoints", checkpoints, f32, checkpoint_shape(B, T, H, K))
-    with _args.on(stream):
-        dev = x.device
-        dx, di, dg = (torch.empty(shape, dtype=x.dtype, device=dev) for _ in range(3))
-        dA_log = torch.empty((H,), dtype=f32, device=dev)
-        ddt_bias = torch.empty((H, K), dtype=f32, device=dev)
-        dinit = torch.empty(state, dtype=f32, device=dev) if want_dinit else None
+    dx, di, dg = _args.new(stream, x, shape, shape, shape)
+    dA_log, ddt_bias, dinit = _args.new(stream, A_log, (H,), (H, K), state if want_dinit else None)
     _args.done(_args.entry("kda_glr_bwd")(
         x.data_ptr(), i.data_ptr(), g.data_ptr(), xs, is_, gs, dt, pA, pt, lower_bound or 0.0, lower_bound is None, init,
         code, ck, dout.data_ptr(), ds, dfin, cu, num_seqs, B, T, H, K, dx.data_ptr(), di.data_ptr(), dg.data_ptr(),

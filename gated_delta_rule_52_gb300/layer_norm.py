@@ -47,10 +47,9 @@ def layer_norm_bwd(dout, x, weight, mean, rstd, want_params=None, stream=None) -
     pm, pr = _args.tensor("mean", mean, f32, row), _args.tensor("rstd", rstd, f32, row)
     if want_params is None:
         want_params = weight is not None
-    with _args.on(stream):
-        dx = torch.empty(shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty((D,), dtype=f32, device=x.device) if want_params else None
-        db = torch.empty((D,), dtype=f32, device=x.device) if want_params else None
+    dx, = _args.new(stream, x, shape)
+    param = (D,) if want_params else None
+    dw, db = _args.new(stream, mean, param, param)
     _args.done(_args.entry("kda_layer_norm_bwd")(
         dout.data_ptr(), dout_stride, x.data_ptr(), stride, pw, pm, pr, dx.data_ptr(),
         dw.data_ptr() if want_params else None, db.data_ptr() if want_params else None, dt, math.prod(row), D,

@@ -60,12 +60,8 @@ def short_conv_bwd(x, weight, bias, dout, activation="silu", initial_state=None,
     state, f32 = (num_seqs or B, W - 1, D), torch.float32
     init = _args.optional("initial_state", initial_state, x.dtype, state)
     dfin = _args.optional("dfinal", dfinal, f32, state)
-    with _args.on(stream):
-        dev = x.device
-        dx = torch.empty(shape, dtype=x.dtype, device=dev)
-        dw = torch.empty((D, W), dtype=f32, device=dev)
-        db = None if bias is None else torch.empty((D,), dtype=f32, device=dev)
-        dinit = torch.empty(state, dtype=f32, device=dev) if want_dinit else None
+    dx, = _args.new(stream, x, shape)
+    dw, db, dinit = _args.new(stream, weight, (D, W), None if bias is None else (D,), state if want_dinit else None)
     _args.done(_args.entry("kda_short_conv_bwd")(
         x.data_ptr(), stride, pw, pb, act, dt, init, dout.data_ptr(), dout_stride, dfin, cu, num_seqs, B, T, D, W,
         dx.data_ptr(), dw.data_ptr(), None if db is None else db.data_ptr(), None if dinit is None else dinit.data_ptr(),
