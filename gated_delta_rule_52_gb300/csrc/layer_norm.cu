@@ -146,7 +146,80 @@ __global__ void __launch_bounds__(EL == 32 ? 512 : 1024) norm_fwd_kernel(NormPar
     }
 }
 
-constexpr int kStages = 3;
+constexpr int kStages = 3;   // rows of a copy ring
+
+// Many rows: persistent CTAs, the next two rows on their way into the threads' own slots of
+// shared memory, the weights in registers.
+template <typename E, int V, int EL>
+__global__ void __launch_bounds__(256, 2) norm_fwd_stream_kernel(NormParams p) {
+    const int D = (int)p.D;
+    constexpr int N = EL / V;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float part[4][kMaxWarps];
+    const int threads = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x;
+    Pack<E, V> *ring = reinterpret_cast<Pack<E, V> *>(smem);   // [stage][group][thread]
+    const auto slot = [&](int stage, int k) -> Pack<E, V> & { return ring[(stage * N + k) * threads + tid]; };
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    const auto fetch = [&](int64_t row, int stage) {
+        if (row < p.rows) {
+            const E *x = static_cast<const E *>(p.x) + row * p.xs;
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (column<V>(k) < D) copy_async<sizeof(E) * V>(&slot(stage, k), x + column<V>(k));
+        }
+        copies_commit();
+    };
+    float w[N][V], b[N][V];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) w[k][v] = b[k][v] = 0.f;
+        if (column<V>(k) >= D) {   // columns that do not exist stay 0 in every slot
+            for (int stage = 0; stage < kStages; ++stage) st_f<E, V>(&slot(stage, k).e[0], w[k]);
+            continue;
+        }
+        ld_param<V>(p.weight, column<V>(k), 1.f, w[k]);
+        ld_param<V>(p.bias, column<V>(k), 0.f, b[k]);
+    }
+    const float inv = 1.f / (float)D;
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int passes = (int)ceil_div(p.rows - (int64_t)blockIdx.x * blockDim.y, step);
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(row + k * step, k);
+    for (int pass = 0, stage = 0; pass < passes; ++pass, row += step) {
+        fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+        copies_wait<kStages - 1>();   // this thread's own copies: no barrier needed
+        float f[N][V];
+#pragma unroll
+        for (int k = 0; k < N; ++k) unpack<E, V>(slot(stage, k), f[k]);
+        const float mean = row_sum(lane_sum(reinterpret_cast<const float (&)[EL]>(f)), part[2 * (pass & 1)]) * inv;
+        float sq[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) sq[v] = 0.f;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (column<V>(k) >= D) continue;
+            fma_n<V>(f[k], f[k], 1.f, -mean);
+            fma_n<V>(sq, f[k], f[k], sq);
+        }
+        const float rstd = 1.f / sqrtf(fmaf(row_sum(lane_sum(sq), part[2 * (pass & 1) + 1]), inv, p.eps));
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        if (row >= p.rows) continue;
+        E *out = static_cast<E *>(p.out) + row * p.os;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (column<V>(k) >= D) continue;
+            fma_n<V>(f[k], f[k], rstd, 0.f);
+            fma_n<V>(f[k], f[k], w[k], b[k]);
+            st_f<E, V>(out + column<V>(k), f[k]);
+        }
+        if (threadIdx.x == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+    }
+    copies_wait<0>();
+}
 
 template <typename E, int V, int EL>
 __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *part_out) {
@@ -383,6 +456,17 @@ cudaError_t run_fwd(const NormParams &p, cudaStream_t stream) {
 }
 
 template <typename E, int V, int EL>
+cudaError_t run_fwd_stream(const NormParams &p, int sms, cudaStream_t stream) {
+    const dim3 block = row_block(p.D, EL, 256);
+    constexpr auto kernel = norm_fwd_stream_kernel<E, V, EL>;
+    const cudaError_t e = allow_smem<kernel>(256 * EL * kStages * (int)sizeof(E));
+    if (e != cudaSuccess) return e;
+    const int64_t grid = std::min(ceil_div(p.rows, (int64_t)block.y), (int64_t)sms * 2);
+    kernel<<<(unsigned)grid, block, block.x * block.y * EL * kStages * (int)sizeof(E), stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename E, int V, int EL>
 cudaError_t run_bwd(const NormParams &p, float *part, int sms, cudaStream_t stream) {
     const dim3 block = row_block(p.D, EL, 512);
     const int threads = block.x * block.y;
@@ -408,10 +492,18 @@ cudaError_t launch_norm_fwd(const NormParams &p, int sms, cudaStream_t stream) {
             norm_fwd_long_kernel<E><<<(unsigned)p.rows, 1024, 0, stream>>>(p);
             return cudaGetLastError();
         }
-        // few rows: more threads to each
-        const bool few = p.rows <= 4 * sms && p.D <= 8192;
-        if (aligned_rows(p, p.out, p.os, nullptr, 0)) return few ? run_fwd<E, V, 8>(p, stream) : run_fwd<E, V, 32>(p, stream);
-        return few ? run_fwd<E, 1, 8>(p, stream) : run_fwd<E, 1, 32>(p, stream);
+        // elements per thread: a warp to a short row; of longer ones many, or few where few
+        // rows leave most of the GPU idle
+        const int el = p.D <= 256 ? 8 : p.D <= 512 ? 16 : p.rows <= 4 * sms && p.D <= 8192 ? 8 : 32;
+        const bool aligned = aligned_rows(p, p.out, p.os, nullptr, 0);
+        // many rows: the streaming kernel.  8192 x 8192 bf16: 50 us against 62 us; in 32 bits
+        // its ring and registers leave too few bytes on their way: 96 us against 84 us
+        if constexpr (sizeof(E) == 2) {
+            if (aligned && p.D > 512 && p.D <= 256 * 32 && p.rows >= 8 * sms * (int64_t)row_block(p.D, 32, 256).y)
+                return run_fwd_stream<E, V, 32>(p, sms, stream);
+        }
+        if (aligned) return el == 8 ? run_fwd<E, V, 8>(p, stream) : el == 16 ? run_fwd<E, V, 16>(p, stream) : run_fwd<E, V, 32>(p, stream);
+        return el == 8 ? run_fwd<E, 1, 8>(p, stream) : el == 16 ? run_fwd<E, 1, 16>(p, stream) : run_fwd<E, 1, 32>(p, stream);
     });
 }
 
