@@ -346,63 +346,118 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *p
     }
 }
 
-// ---- rows too long for a thread's registers: a CTA per row, several passes
-template <typename E>
-__global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormParams p) {
+// ---- rows too long for a thread's registers: a CTA per row, several passes (the later ones
+// through L2), V elements at a time
+constexpr int kLongThreads = 512;
+
+template <typename E, int V>
+__global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(NormParams p) {
     __shared__ float part[2][kMaxWarps];
+    const int D = (int)p.D, c0 = threadIdx.x * V;
+    constexpr int kStep = kLongThreads * V;
     const int64_t row = blockIdx.x;
     const E *x = static_cast<const E *>(p.x) + row * p.xs;
     E *out = static_cast<E *>(p.out) + row * p.os;
-    float s = 0.f;
-    for (int64_t c = threadIdx.x; c < p.D; c += 1024) s += to_f(x[c]);
-    const float mean = row_sum(s, part[0]) / (float)p.D;
-    s = 0.f;
-    for (int64_t c = threadIdx.x; c < p.D; c += 1024) {
-        const float d = to_f(x[c]) - mean;
-        s = fmaf(d, d, s);
+    const float inv = 1.f / (float)D;
+    float s[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = 0.f;
+#pragma unroll 4
+    for (int64_t c = c0; c < D; c += kStep) {
+        float f[V];
+        ld_f<E, V>(x + c, f);
+        add_n<V>(s, s, f);
     }
-    const float rstd = 1.f / sqrtf(row_sum(s, part[1]) / (float)p.D + p.eps);
-    for (int64_t c = threadIdx.x; c < p.D; c += 1024)
-        out[c] = from_f<E>(fmaf((to_f(x[c]) - mean) * rstd, p.weight ? p.weight[c] : 1.f, p.bias ? p.bias[c] : 0.f));
+    const float mean = row_sum(lane_sum(s), part[0]) * inv;
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = 0.f;
+#pragma unroll 4
+    for (int64_t c = c0; c < D; c += kStep) {
+        float f[V];
+        ld_f<E, V>(x + c, f);
+        fma_n<V>(f, f, 1.f, -mean);
+        fma_n<V>(s, f, f, s);
+    }
+    const float rstd = 1.f / sqrtf(fmaf(row_sum(lane_sum(s), part[1]), inv, p.eps));
+#pragma unroll 2
+    for (int64_t c = c0; c < D; c += kStep) {
+        float f[V], w[V], b[V];
+        ld_f<E, V>(x + c, f);
+        ld_param<V>(p.weight, (int)c, 1.f, w);
+        ld_param<V>(p.bias, (int)c, 0.f, b);
+        fma_n<V>(f, f, 1.f, -mean);
+        fma_n<V>(f, f, rstd, 0.f);
+        fma_n<V>(f, f, w, b);
+        st_f<E, V>(out + c, f);
+    }
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
 }
 
-template <typename E>
-__global__ void __launch_bounds__(1024) norm_bwd_long_kernel(NormParams p) {
+template <typename E, int V>
+__global__ void __launch_bounds__(kLongThreads) norm_bwd_long_kernel(NormParams p) {
     __shared__ float part[2][kMaxWarps];
+    const int D = (int)p.D, c0 = threadIdx.x * V;
+    constexpr int kStep = kLongThreads * V;
     const int64_t row = blockIdx.x;
     const E *x = static_cast<const E *>(p.x) + row * p.xs, *dy = static_cast<const E *>(p.dout) + row * p.ds;
-    const float mean = p.mean[row], rstd = p.rstd[row];
-    float s1 = 0.f, s2 = 0.f;
-    for (int64_t c = threadIdx.x; c < p.D; c += 1024) {
-        const float d = to_f(dy[c]) * (p.weight ? p.weight[c] : 1.f);
-        s1 += d;
-        s2 = fmaf(d, (to_f(x[c]) - mean) * rstd, s2);
+    E *dx = static_cast<E *>(p.dx) + row * p.D;
+    const float mean = p.mean[row], rstd = p.rstd[row], inv = 1.f / (float)D;
+    float s1[V], s2[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) s1[v] = s2[v] = 0.f;
+#pragma unroll 2
+    for (int64_t c = c0; c < D; c += kStep) {
+        float f[V], d[V], w[V];
+        ld_f<E, V>(x + c, f);
+        ld_f<E, V>(dy + c, d);
+        ld_param<V>(p.weight, (int)c, 1.f, w);
+        fma_n<V>(f, f, 1.f, -mean);
+        fma_n<V>(f, f, rstd, 0.f);
+        mul_n<V>(d, d, w);
+        add_n<V>(s1, s1, d);
+        fma_n<V>(s2, d, f, s2);
     }
-    const float m1 = row_sum(s1, part[0]) / (float)p.D, m2 = row_sum(s2, part[1]) / (float)p.D;
-    for (int64_t c = threadIdx.x; c < p.D; c += 1024) {
-        const float d = to_f(dy[c]) * (p.weight ? p.weight[c] : 1.f), xh = (to_f(x[c]) - mean) * rstd;
-        static_cast<E *>(p.dx)[row * p.D + c] = from_f<E>(rstd * (d - fmaf(xh, m2, m1)));
+    const float m1 = row_sum(lane_sum(s1), part[0]) * inv, m2 = row_sum(lane_sum(s2), part[1]) * inv;
+#pragma unroll 2
+    for (int64_t c = c0; c < D; c += kStep) {
+        float f[V], d[V], w[V];
+        ld_f<E, V>(x + c, f);
+        ld_f<E, V>(dy + c, d);
+        ld_param<V>(p.weight, (int)c, 1.f, w);
+        fma_n<V>(f, f, 1.f, -mean);
+        fma_n<V>(f, f, rstd, 0.f);
+        mul_n<V>(d, d, w);
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] = rstd * (d[v] - fmaf(f[v], m2, m1));
+        st_f<E, V>(dx + c, d);
     }
 }
 
-// A thread per column, blockIdx.y a block of rows.
-template <typename E>
-__global__ void __launch_bounds__(256) norm_param_part_kernel(NormParams p, int64_t block_rows, float *part_out) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x, r0 = blockIdx.y * block_rows;
+// A thread per V columns, blockIdx.y a block of rows.
+template <typename E, int V>
+__global__ void __launch_bounds__(128) norm_param_part_kernel(NormParams p, int64_t block_rows, float *part_out) {
+    const int64_t c = ((int64_t)blockIdx.x * 128 + threadIdx.x) * V, r0 = blockIdx.y * block_rows, r1 = min(r0 + block_rows, p.rows);
     if (c >= p.D) return;
-    float w = 0.f, b = 0.f;
-#pragma unroll 8
-    for (int64_t row = r0; row < min(r0 + block_rows, p.rows); ++row) {
-        const float dy = to_f(static_cast<const E *>(p.dout)[row * p.ds + c]);
-        w = fmaf(dy, (to_f(static_cast<const E *>(p.x)[row * p.xs + c]) - p.mean[row]) * p.rstd[row], w);
-        b += dy;
+    float w[V], b[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) w[v] = b[v] = 0.f;
+    const E *x = static_cast<const E *>(p.x) + c, *dy = static_cast<const E *>(p.dout) + c;
+#pragma unroll 4
+    for (int64_t row = r0; row < r1; ++row) {
+        float f[V], d[V];
+        ld_f<E, V>(x + row * p.xs, f);
+        ld_f<E, V>(dy + row * p.ds, d);
+        fma_n<V>(f, f, 1.f, -p.mean[row]);
+        fma_n<V>(f, f, p.rstd[row], 0.f);
+        fma_n<V>(w, d, f, w);
+        add_n<V>(b, b, d);
     }
-    part_out[blockIdx.y * 2 * p.D + c] = w;
-    part_out[blockIdx.y * 2 * p.D + p.D + c] = b;
+    float *at = part_out + blockIdx.y * 2 * p.D + c;
+#pragma unroll
+    for (int v = 0; v < V; ++v) at[v] = w[v], at[p.D + v] = b[v];
 }
 
 // part [parts, 2, D] to dweight, dbias.
@@ -489,7 +544,8 @@ cudaError_t launch_norm_fwd(const NormParams &p, int sms, cudaStream_t stream) {
         using E = std::remove_pointer_t<decltype(tag)>;
         constexpr int V = 16 / sizeof(E);
         if (p.D > kFwdMaxD) {
-            norm_fwd_long_kernel<E><<<(unsigned)p.rows, 1024, 0, stream>>>(p);
+            if (aligned_rows(p, p.out, p.os, nullptr, 0)) norm_fwd_long_kernel<E, V><<<(unsigned)p.rows, kLongThreads, 0, stream>>>(p);
+            else norm_fwd_long_kernel<E, 1><<<(unsigned)p.rows, kLongThreads, 0, stream>>>(p);
             return cudaGetLastError();
         }
         // elements per thread: a warp to a short row; of longer ones many, or few where few
@@ -514,14 +570,18 @@ cudaError_t launch_norm_bwd(const NormParams &p, unsigned char *ws, int sms, cud
         using E = std::remove_pointer_t<decltype(tag)>;
         constexpr int V = 16 / sizeof(E);
         if (p.rows == 0) return cudaSuccess;
-        if (p.D > kBwdMaxD) {
-            norm_bwd_long_kernel<E><<<(unsigned)p.rows, 1024, 0, stream>>>(p);
-            if (part)
-                norm_param_part_kernel<E><<<dim3((unsigned)ceil_div(p.D, 256), (unsigned)parts), 256, 0, stream>>>(
-                    p, ceil_div(p.rows, parts), part);
-            return cudaGetLastError();
-        }
         const bool wide = aligned_rows(p, p.dout, p.ds, p.dx, 0);
+        if (p.D > kBwdMaxD) {
+            const auto run_long = [&](auto v) {
+                constexpr int LV = decltype(v)::value;
+                norm_bwd_long_kernel<E, LV><<<(unsigned)p.rows, kLongThreads, 0, stream>>>(p);
+                if (part)
+                    norm_param_part_kernel<E, LV><<<dim3((unsigned)ceil_div(p.D, 128 * LV), (unsigned)parts), 128, 0, stream>>>(
+                        p, ceil_div(p.rows, parts), part);
+                return cudaGetLastError();
+            };
+            return wide ? run_long(std::integral_constant<int, V>{}) : run_long(std::integral_constant<int, 1>{});
+        }
         if (bwd_el(p) == 8) return wide ? run_bwd<E, V, 8>(p, part, sms, stream) : run_bwd<E, 1, 8>(p, part, sms, stream);
         return wide ? run_bwd<E, V, 16>(p, part, sms, stream) : run_bwd<E, 1, 16>(p, part, sms, stream);
     });
