@@ -9,8 +9,9 @@
 // rows, then blockDim.y rows per CTA), EL elements each.  The backward kernel is
 // persistent: a CTA walks its rows with the next ones on their way into shared memory, a
 // thread keeps its columns' weights and their gradients in registers, and one partial sum
-// per CTA and column is left for a second kernel.  Rows too long for that (more than 16384
-// forward, 8192 backward) run kernels that pass over a row again through L2.
+// per CTA and column is left for a second kernel.  The forward kernel for many 16-bit rows
+// walks them likewise.  Rows too long for registers (more than 16384 forward; backward 8192,
+// or 4096 unaligned in 16 bits) run kernels that pass over a row again through L2.
 #include <algorithm>
 
 #include "layer_copy.cuh"
@@ -498,9 +499,16 @@ int bwd_el(const NormParams &p) { return p.D <= 512 * 8 ? 8 : 16; }
 int64_t bwd_grid(const NormParams &p, int sms) {
     return std::min(ceil_div(p.rows, (int64_t)row_block(p.D, bwd_el(p), 512).y), (int64_t)sms);
 }
+// Rows of more than 8192 elements, and of more than 4096 in 16 bits that are not aligned:
+// their 2-byte elements pass through registers on the way to the ring, and with 16 of them
+// per thread that spills.  8192 rows of 8191 bf16: 595 us, in several passes 313 us; of
+// 4097: 524 and 177; but of 1537, at 8 per thread: 52 and 75.
+bool long_rows(const NormParams &p) {
+    return p.D > kBwdMaxD || (p.D > 4096 && p.dtype != kFP32 && !aligned_rows(p, p.dout, p.ds, p.dx, 0));
+}
 int64_t bwd_parts(const NormParams &p, int sms) {
     if (p.rows == 0) return 0;
-    return p.D <= kBwdMaxD ? bwd_grid(p, sms) : std::min(ceil_div(p.rows, 64), kLongParts);
+    return !long_rows(p) ? bwd_grid(p, sms) : std::min(ceil_div(p.rows, 64), kLongParts);
 }
 
 template <typename E, int V, int EL>
@@ -559,7 +567,9 @@ cudaError_t launch_norm_fwd(const NormParams &p, int sms, cudaStream_t stream) {
                 return run_fwd_stream<E, V, 32>(p, sms, stream);
         }
         if (aligned) return el == 8 ? run_fwd<E, V, 8>(p, stream) : el == 16 ? run_fwd<E, V, 16>(p, stream) : run_fwd<E, V, 32>(p, stream);
-        return el == 8 ? run_fwd<E, 1, 8>(p, stream) : el == 16 ? run_fwd<E, 1, 16>(p, stream) : run_fwd<E, 1, 32>(p, stream);
+        // single elements: at most 16 to a thread.  8192 x 8191 bf16: 134 us, 167 with 32, 199
+        // with 8; 8192 x 1537: 31, 42 with 32
+        return el == 8 ? run_fwd<E, 1, 8>(p, stream) : run_fwd<E, 1, 16>(p, stream);
     });
 }
 
@@ -571,7 +581,7 @@ cudaError_t launch_norm_bwd(const NormParams &p, unsigned char *ws, int sms, cud
         constexpr int V = 16 / sizeof(E);
         if (p.rows == 0) return cudaSuccess;
         const bool wide = aligned_rows(p, p.dout, p.ds, p.dx, 0);
-        if (p.D > kBwdMaxD) {
+        if (long_rows(p)) {
             const auto run_long = [&](auto v) {
                 constexpr int LV = decltype(v)::value;
                 norm_bwd_long_kernel<E, LV><<<(unsigned)p.rows, kLongThreads, 0, stream>>>(p);
@@ -583,7 +593,9 @@ cudaError_t launch_norm_bwd(const NormParams &p, unsigned char *ws, int sms, cud
             return wide ? run_long(std::integral_constant<int, V>{}) : run_long(std::integral_constant<int, 1>{});
         }
         if (bwd_el(p) == 8) return wide ? run_bwd<E, V, 8>(p, part, sms, stream) : run_bwd<E, 1, 8>(p, part, sms, stream);
-        return wide ? run_bwd<E, V, 16>(p, part, sms, stream) : run_bwd<E, 1, 16>(p, part, sms, stream);
+        if constexpr (sizeof(E) == 4)
+            if (!wide) return run_bwd<E, 1, 16>(p, part, sms, stream);
+        return run_bwd<E, V, 16>(p, part, sms, stream);
     });
     if (e != cudaSuccess) return e;
     if (part || (wants_params(p) && p.rows == 0))

@@ -261,7 +261,8 @@ def test_glr_in_a_cuda_graph():
 @pytest.mark.parametrize("rows,D,dt,how,affine", [
     (1, 1, F, "dense", True), (3, 2, BF, "dense", True), (7, 33, HF, "odd", True), (1, 129, F, "odd", True),
     (64, 64, BF, "dense", False), (5, 1000, HF, "slice", True), (200, 256, BF, "dense", True),
-    (2, 1537, F, "dense", True), (9, 4096, BF, "slice", True), (300, 2049, BF, "odd", True),
+    (2, 1537, F, "dense", True), (9, 4096, BF, "slice", True), (300, 2049, BF, "odd", True), (70, 4097, BF, "odd", True), (3, 8191, HF, "odd", True),
+    (5, 8191, F, "odd", True), (2, 15001, BF, "odd", True),
     (3, 8192, BF, "dense", True), (4, 16384, HF, "dense", True), (2, 16385, F, "dense", False),
     (2, 70001, BF, "dense", True), (1300, 24, F, "dense", True), (0, 64, BF, "dense", True),
 ])
