@@ -64,10 +64,10 @@ __global__ void __launch_bounds__(128) glr_fwd_step_kernel(GlrParams p) {
 using FwdShape = TileShape<kGlrCheckpointRows, 128, 16, 4>;
 constexpr int kFwdCtas = 5;
 
-template <typename E>
+template <typename E, bool TMA>
 struct FwdShared {
     using S = FwdShape;
-    Pack<E, S::V> raw[3][S::ROWS][S::CL];                 // x, i, g
+    RawTile<E, S, TMA> raw[3];                            // x, i, g
     Pack<GateConst, S::V> gates[S::CL];
     Pack<float, S::V> A[S::RG][S::CL], H[S::RG][S::CL];   // maps of the row groups
     Pack<float, S::V> h[S::RG][S::CL];                    // states that enter them
@@ -77,12 +77,12 @@ struct FwdShared {
 
 template <typename E, bool TMA, bool UB>
 __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas)
-    glr_fwd_scan_kernel(GlrParams p, ScanPlan s, const __grid_constant__ ScanMaps maps) {
+    glr_fwd_scan_kernel(GlrParams p, ScanPlan s, const __grid_constant__ ScanMaps<3 * RawTile<E, FwdShape, TMA>::PHASES> maps) {
     using namespace sm103;
     using S = FwdShape;
     constexpr int CL = S::CL, V = S::V, L = S::L, CB = S::CB, RG = S::RG;
     extern __shared__ __align__(128) unsigned char smem[];
-    FwdShared<E> &sh = *reinterpret_cast<FwdShared<E> *>(smem);
+    FwdShared<E, TMA> &sh = *reinterpret_cast<FwdShared<E, TMA> *>(smem);
     const int tid = threadIdx.x, lane = tid % CL, rg = tid / CL;
     const float lb2 = p.lower_bound * kLog2e;
     const int D = (int)p.D;
@@ -90,21 +90,11 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas)
     // starts the copies of a tile's inputs
     const auto fetch = [&](const TileWalk &w) {
         if (w.rt >= s.row_tiles) return;
-        if constexpr (TMA) {
-            if (tid == 0) {
-                mbar_arrive_expect_tx(&sh.arrived, sizeof(sh.raw) + sizeof(sh.gates));
-#pragma unroll
-                for (int k = 0; k < 3; ++k) tma_box(sh.raw[k], maps.m[k], &sh.arrived, w.cb * CB, (int)w.rt * S::ROWS);
-            }
-        } else {
-            const int64_t r0 = w.rt * S::ROWS + rg * L;
-            const int c = w.cb * CB + lane * V, left = (int)min(p.rows - r0, (int64_t)L);
-            const auto copy = [&](int k, const void *src, int64_t stride) {
-                copy_rows<E, V, false, L, CL>(&sh.raw[k][rg * L][lane], static_cast<const E *>(src) + r0 * stride + c, stride, left, D - c);
-            };
-            copy(0, p.x, p.xs);
-            copy(1, p.i, p.is);
-            copy(2, p.g, p.gs);
+        if (TMA || maps.boxed) {
+            fetch_boxes(sh.raw, maps, w.rt * S::ROWS, w.cb * CB, sizeof(sh.gates), &sh.arrived);
+        } else if constexpr (!TMA) {
+            fetch_rows<E, S, 3>(sh.raw, {p.x, p.i, p.g}, {p.xs, p.is, p.gs}, p.rows, p.D, w.rt * S::ROWS, w.cb * CB,
+                             tid == 0 ? sizeof(sh.gates) : 0, &sh.arrived);
         }
     };
     // and of what the scan's first part has left for the tile; returns its first sequence
@@ -113,52 +103,42 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas)
         if (w.rt < s.row_tiles) {
             first = s.first_seq[w.rt];
             const GateConst *gates = s.gates + w.cb * CB;
-            if constexpr (TMA) {
-                if (tid == 0) bulk_load(smem_u32(sh.gates), gates, sizeof(sh.gates), smem_u32(&sh.arrived));
-            } else {
-                if (tid < CB / 2) copy_async<16>(&sh.gates[0].e[0] + 2 * tid, gates + 2 * tid);
-            }
+            if (tid == 0) bulk_load(smem_u32(sh.gates), gates, sizeof(sh.gates), smem_u32(&sh.arrived));
         }
-        if constexpr (!TMA) copies_commit();
         return first;
     };
-    const auto copies_arrive = [&](uint32_t parity) {
-        if constexpr (TMA) {
-            if (!mbar_wait(&sh.arrived, parity, kCopyWaitNs)) atomicExch(p.err, kErrTimeout);
-        } else {
-            copies_wait<0>();
-            __syncthreads();
-        }
-    };
+    const RowStart<E> starts[3] = {{p.x, p.xs}, {p.i, p.is}, {p.g, p.gs}};
 
-    if (TMA && tid == 0) {
-        mbar_init(&sh.arrived, 1);
+    if (tid == 0) {
+        mbar_init(&sh.arrived, TMA || maps.boxed ? 1 : S::THREADS);
         fence_mbar_init();
     }
     __syncthreads();
     TileWalk w(s);
     fetch(w);
     prepare_scan<UB, false>(p, s);
-    if (TMA) fence_proxy_async_global();   // the gates are read by bulk copies
+    fence_proxy_async_global();   // the gates are read by bulk copies
     cooperative_groups::this_grid().sync();
-    if (TMA) fence_proxy_async_global();
+    fence_proxy_async_global();
     int first = fetch_plan(w);
     for (uint32_t parity = 0; w.rt < s.row_tiles; parity ^= 1) {
         const int64_t rt = w.rt, r0 = rt * S::ROWS + rg * L;
         const int block = w.cb * CB, c = block + lane * V;
         const bool marked = mark_tile(p, rt, first, sh.marks);
         const bool plain = !marked && (rt + 1) * S::ROWS <= p.rows;   // every row inside one sequence
-        copies_arrive(parity);
+        if (!mbar_wait(&sh.arrived, parity, kCopyWaitNs)) atomicExch(p.err, kErrTimeout);
 
         float a[L][V], b[L][V];
         {
             const ChannelGates<V> gc(sh.gates[lane]);
+            const auto raw = [&](int k, int r, float (&f)[V]) {
+                const int row = rg * L + r;
+                unpack<E, V>(TMA ? sh.raw[k].at(row, lane) : pick<E, V>(sh.raw[k].row(row), starts[k][row] + lane * V), f);
+            };
 #pragma unroll
             for (int r = 0; r < L; ++r) {
                 float x[V], i[V], g[V];
-                unpack<E, V>(sh.raw[0][rg * L + r][lane], x);
-                unpack<E, V>(sh.raw[1][rg * L + r][lane], i);
-                unpack<E, V>(sh.raw[2][rg * L + r][lane], g);
+                raw(0, r, x), raw(1, r, i), raw(2, r, g);
                 gate_decay_n<UB, V>(a[r], g, gc.k0, gc.k1, lb2);
                 sigmoid_n<V>(b[r], i);
                 mul_n<V>(b[r], b[r], x);
@@ -296,14 +276,16 @@ cudaError_t run(const GlrParams &p, unsigned char *ws, int sms, cudaStream_t str
         return cudaGetLastError();
     }
     ScanPlan s = scan_plan<FwdShape>(p.rows, p.D, ws, nullptr);
-    ScanMaps maps{};
-    if (TMA && p.rows > 0 &&
-        !(encode_tile_map(maps.m[0], p.x, p.xs, p.rows, p.D, p.dtype, FwdShape::CB, FwdShape::ROWS) &&
-          encode_tile_map(maps.m[1], p.i, p.is, p.rows, p.D, p.dtype, FwdShape::CB, FwdShape::ROWS) &&
-          encode_tile_map(maps.m[2], p.g, p.gs, p.rows, p.D, p.dtype, FwdShape::CB, FwdShape::ROWS)))
+    using Raw = RawTile<E, FwdShape, TMA>;
+    ScanMaps<3 * Raw::PHASES> maps{};
+    maps.boxed = p.rows >= Raw::PHASES && p.xs >= p.D && p.is >= p.D && p.gs >= p.D;
+    if (maps.boxed &&
+        !(encode_maps<Raw>(maps, 0, p.x, p.xs, p.rows, p.D, p.dtype) &&
+          encode_maps<Raw>(maps, 1, p.i, p.is, p.rows, p.D, p.dtype) &&
+          encode_maps<Raw>(maps, 2, p.g, p.gs, p.rows, p.D, p.dtype)))
         return cudaErrorUnknown;
     constexpr auto kernel = glr_fwd_scan_kernel<E, TMA, UB>;
-    constexpr int bytes = (int)sizeof(FwdShared<E>);
+    constexpr int bytes = (int)sizeof(FwdShared<E, TMA>);
     int ctas = 0;
     const cudaError_t e = resident_ctas<kernel>(FwdShape::THREADS, bytes, ctas);
     if (e != cudaSuccess) return e;

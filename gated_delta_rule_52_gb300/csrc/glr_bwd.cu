@@ -25,10 +25,10 @@ using namespace layer;
 // inputs of two tiles in shared memory allow 2 and 3 CTAs per SM).
 template <typename E> using BwdShape = TileShape<kGlrCheckpointRows, sizeof(E) == 2 ? 256 : 128, 16, sizeof(E) == 2 ? 4 : 2>;
 
-template <typename E>
+template <typename E, bool TMA>
 struct BwdShared {
     using S = BwdShape<E>;
-    Pack<E, S::V> raw[2][4][S::ROWS][S::CL];                       // x, i, g, dout
+    RawTile<E, S, TMA> raw[2][4];                                  // x, i, g, dout
     Pack<GateConst, S::V> gates[2][S::CL];
     Pack<float, S::V> A[S::RG][S::CL], H[S::RG][S::CL];            // forward maps of the row groups
     Pack<float, S::V> B[S::RG][S::CL], F[S::RG][S::CL];            // backward maps
@@ -39,15 +39,15 @@ struct BwdShared {
 };
 
 template <typename E, bool TMA, bool UB>
-__global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
-    glr_bwd_scan_kernel(GlrParams p, ScanPlan s, const __grid_constant__ ScanMaps maps, float *part_ddt, float *part_dA) {
+__global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 || !TMA ? 2 : 3)
+    glr_bwd_scan_kernel(GlrParams p, ScanPlan s, const __grid_constant__ ScanMaps<4 * RawTile<E, BwdShape<E>, TMA>::PHASES> maps, float *part_ddt, float *part_dA) {
     using namespace sm103;
     using S = BwdShape<E>;
     constexpr int CL = S::CL, V = S::V, L = S::L, CB = S::CB, RG = S::RG;
     constexpr bool EXACT = sizeof(E) == 4;
     static_assert(S::THREADS >= 3 * CB && L * V == 16, "roles");
     extern __shared__ __align__(128) unsigned char smem[];
-    BwdShared<E> &sh = *reinterpret_cast<BwdShared<E> *>(smem);
+    BwdShared<E, TMA> &sh = *reinterpret_cast<BwdShared<E, TMA> *>(smem);
     const int tid = threadIdx.x, lane = tid % CL, rg = tid / CL;
     const int role = tid / CB, ch = tid % CB, D = (int)p.D;
     const float lb2 = p.lower_bound * kLog2e;
@@ -58,23 +58,11 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
         if (w.rt >= s.row_tiles) return;
         const int64_t rt = s.row_tiles - 1 - w.rt;
         if (role == 2 && w.cb * CB + ch < D) checkpoint = p.checkpoints[rt * p.D + w.cb * CB + ch];
-        if constexpr (TMA) {
-            if (tid == 0) {
-                mbar_arrive_expect_tx(&sh.arrived[stage], sizeof(sh.raw[0]) + sizeof(sh.gates[0]));
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tma_box(sh.raw[stage][k], maps.m[k], &sh.arrived[stage], w.cb * CB, (int)rt * S::ROWS);
-            }
-        } else {
-            const int64_t r0 = rt * S::ROWS + rg * L;
-            const int c = w.cb * CB + lane * V, left = (int)min(p.rows - r0, (int64_t)L);
-            const auto copy = [&](int k, const void *src, int64_t stride) {
-                copy_rows<E, V, false, L, CL>(&sh.raw[stage][k][rg * L][lane], static_cast<const E *>(src) + r0 * stride + c, stride,
-                                              left, D - c);
-            };
-            copy(0, p.x, p.xs);
-            copy(1, p.i, p.is);
-            copy(2, p.g, p.gs);
-            copy(3, p.dout, p.ds);
+        if (TMA || maps.boxed) {
+            fetch_boxes(sh.raw[stage], maps, rt * S::ROWS, w.cb * CB, sizeof(sh.gates[0]), &sh.arrived[stage]);
+        } else if constexpr (!TMA) {
+            fetch_rows<E, S, 4>(sh.raw[stage], {p.x, p.i, p.g, p.dout}, {p.xs, p.is, p.gs, p.ds}, p.rows, p.D, rt * S::ROWS, w.cb * CB,
+                             tid == 0 ? sizeof(sh.gates[0]) : 0, &sh.arrived[stage]);
         }
     };
     // and of what the scan's first part has left for the tile; returns its first sequence
@@ -83,36 +71,24 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
         if (w.rt < s.row_tiles) {
             first = s.first_seq[s.row_tiles - 1 - w.rt];
             const GateConst *gates = s.gates + w.cb * CB;
-            if constexpr (TMA) {
-                if (tid == 0) bulk_load(smem_u32(sh.gates[stage]), gates, sizeof(sh.gates[0]), smem_u32(&sh.arrived[stage]));
-            } else {
-                if (tid < CB / 2) copy_async<16>(&sh.gates[stage][0].e[0] + 2 * tid, gates + 2 * tid);
-            }
+            if (tid == 0) bulk_load(smem_u32(sh.gates[stage]), gates, sizeof(sh.gates[0]), smem_u32(&sh.arrived[stage]));
         }
-        if constexpr (!TMA) copies_commit();
         return first;
     };
-    const auto copies_arrive = [&](int stage, uint32_t parity) {
-        if constexpr (TMA) {
-            if (!mbar_wait(&sh.arrived[stage], parity, kCopyWaitNs)) atomicExch(p.err, kErrTimeout);
-        } else {
-            copies_wait<1>();
-            __syncthreads();
-        }
-    };
+    const RowStart<E> starts[4] = {{p.x, p.xs}, {p.i, p.is}, {p.g, p.gs}, {p.dout, p.ds}};
 
-    if (TMA && tid == 0) {
-        mbar_init(&sh.arrived[0], 1);
-        mbar_init(&sh.arrived[1], 1);
+    if (tid == 0) {
+        mbar_init(&sh.arrived[0], TMA || maps.boxed ? 1 : S::THREADS);
+        mbar_init(&sh.arrived[1], TMA || maps.boxed ? 1 : S::THREADS);
         fence_mbar_init();
     }
     __syncthreads();
     TileWalk w(s);
     fetch(w, 0);
     prepare_scan<UB, true>(p, s);
-    if (TMA) fence_proxy_async_global();   // the gates are read by bulk copies
+    fence_proxy_async_global();   // the gates are read by bulk copies
     cooperative_groups::this_grid().sync();
-    if (TMA) fence_proxy_async_global();
+    fence_proxy_async_global();
     int next_first = fetch_plan(w, 0);
     uint32_t parity = 0;   // of stage 0's copies; stage 1's turn comes in between
     for (int stage = 0; w.rt < s.row_tiles; stage ^= 1) {
@@ -125,11 +101,24 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 ? 2 : 3)
         const bool marked = mark_tile(p, rt, first, sh.marks);
         const bool plain = !marked && (rt + 1) * S::ROWS <= p.rows;        // every row inside one sequence
         const int left = cols > 0 ? (int)min(p.rows - r0, (int64_t)L) : 0;   // rows of this thread that exist
-        copies_arrive(stage, parity);
+        if (!mbar_wait(&sh.arrived[stage], parity, kCopyWaitNs)) atomicExch(p.err, kErrTimeout);
         parity ^= stage;
+        if constexpr (!TMA) {
+            // each row to its aligned place; the lanes of a row are in one warp
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                Pack<E, V> t[L];
+#pragma unroll
+                for (int r = 0; r < L; ++r) t[r] = pick<E, V>(sh.raw[stage][k].row(rg * L + r), starts[k][rg * L + r] + lane * V);
+                __syncwarp();
+#pragma unroll
+                for (int r = 0; r < L; ++r) sh.raw[stage][k].at(rg * L + r, lane) = t[r];
+            }
+            fence_proxy_async_smem();   // before the copies that follow this tile
+        }
 
         const ChannelGates<V> gc(sh.gates[stage][lane]);
-        const auto raw = [&](int k, int r, float (&f)[V]) { unpack<E, V>(sh.raw[stage][k][rg * L + r][lane], f); };
+        const auto raw = [&](int k, int r, float (&f)[V]) { unpack<E, V>(sh.raw[stage][k].at(rg * L + r, lane), f); };
         float a[L][V], kept_g[L][V], kept_i[L][V];   // for the second half
         Pack<float, V> mA, mH, mB, mF;
 #pragma unroll
@@ -407,13 +396,17 @@ template <typename E, bool TMA, bool UB>
 cudaError_t run(const GlrParams &p, const BwdPlan &b, int sms, cudaStream_t stream) {
     ScanPlan s = b.s;
     using S = BwdShape<E>;
-    ScanMaps maps{};
-    if (TMA && p.rows > 0 &&
-        !(encode_tile_map(maps.m[0], p.x, p.xs, p.rows, p.D, p.dtype, S::CB, S::ROWS) && encode_tile_map(maps.m[1], p.i, p.is, p.rows, p.D, p.dtype, S::CB, S::ROWS) &&
-          encode_tile_map(maps.m[2], p.g, p.gs, p.rows, p.D, p.dtype, S::CB, S::ROWS) && encode_tile_map(maps.m[3], p.dout, p.ds, p.rows, p.D, p.dtype, S::CB, S::ROWS)))
+    using Raw = RawTile<E, S, TMA>;
+    ScanMaps<4 * Raw::PHASES> maps{};
+    maps.boxed = p.rows >= Raw::PHASES && p.xs >= p.D && p.is >= p.D && p.gs >= p.D && p.ds >= p.D;
+    if (maps.boxed &&
+        !(encode_maps<Raw>(maps, 0, p.x, p.xs, p.rows, p.D, p.dtype) &&
+          encode_maps<Raw>(maps, 1, p.i, p.is, p.rows, p.D, p.dtype) &&
+          encode_maps<Raw>(maps, 2, p.g, p.gs, p.rows, p.D, p.dtype) &&
+          encode_maps<Raw>(maps, 3, p.dout, p.ds, p.rows, p.D, p.dtype)))
         return cudaErrorUnknown;
     int ctas = 0;
-    constexpr int bytes = (int)sizeof(BwdShared<E>);
+    constexpr int bytes = (int)sizeof(BwdShared<E, TMA>);
     constexpr auto kernel = glr_bwd_scan_kernel<E, TMA, UB>;
     const cudaError_t e = resident_ctas<kernel>(BwdShape<E>::THREADS, bytes, ctas);
     if (e != cudaSuccess) return e;

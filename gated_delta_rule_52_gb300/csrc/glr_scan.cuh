@@ -82,6 +82,122 @@ struct TileShape {
     static_assert(RG * L == ROWS && THREADS >= 2 * CB && CB % 32 == 0, "tile shape");
 };
 
+// One input of a tile in shared memory.  From aligned rows (TMA) a box of a tensor map.
+// Other rows come as whole 16-byte granules, so that a row begins at its first element's
+// place in a granule (RowStart) and takes up to one granule more.  PHASES rows apart that
+// place is the same: these rows lie together, and a tensor map of theirs has a legal pitch.
+template <typename E, typename S, bool TMA>
+struct RawTile {
+    static constexpr int PHASES = TMA ? 1 : 16 / (int)sizeof(E), PITCH = S::CB + (TMA ? 0 : PHASES), EACH = S::ROWS / PHASES;
+    E e[PHASES][EACH][PITCH];
+    __device__ __forceinline__ E *row(int r) { return e[r % PHASES][r / PHASES]; }
+    __device__ __forceinline__ Pack<E, S::V> &at(int r, int lane) { return *reinterpret_cast<Pack<E, S::V> *>(row(r) + lane * S::V); }
+};
+template <typename E>
+struct RowStart {
+    uint32_t first, step;
+    __device__ __forceinline__ RowStart(const void *p, int64_t stride)
+        : first((uint32_t)(reinterpret_cast<uintptr_t>(p) / sizeof(E))), step((uint32_t)stride) {}
+    // of a row of a tile (tiles begin at multiples of 64 rows)
+    __device__ __forceinline__ int operator[](int row) const { return (first + (uint32_t)row * step) & (16 / sizeof(E) - 1); }
+};
+// Tensor maps of a tile's N inputs.  Not `boxed`: without them (rows that overlap, as of a
+// broadcast tensor, and too few rows for the phases).
+template <int N>
+struct ScanMaps {
+    CUtensorMap m[N];
+    int boxed;
+};
+// The maps begin at a whole granule, which is inside the allocation, and end with the rows'
+// last element: nothing else is read.
+template <typename Raw, int N>
+bool encode_maps(ScanMaps<N> &maps, int k, const void *ptr, int64_t stride, int64_t rows, int64_t D, int dtype) {
+    const int64_t e = (int64_t)dtype_bytes(dtype);
+    for (int ph = 0; ph < Raw::PHASES; ++ph) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(ptr) + ph * stride * e, floor = at / 16 * 16;
+        if (!encode_tile_map(maps.m[k * Raw::PHASES + ph], reinterpret_cast<const void *>(floor), Raw::PHASES * stride,
+                             (rows - ph + Raw::PHASES - 1) / Raw::PHASES, (int64_t)(at - floor) / e + D, dtype, Raw::PITCH, Raw::EACH))
+            return false;
+    }
+    return true;
+}
+// Starts the boxes of a tile, by one thread or, of several phases, one to a lane of the CTA's
+// first warp; `bytes` more are to arrive with them.  (Copies of 8 bytes per thread and row
+// took a fifth of a tile's time to issue: 119 us forward and 289 us backward on 8192 x 8192
+// bf16.)
+template <typename Raw, int N, int M>
+__device__ __forceinline__ void fetch_boxes(Raw (&raw)[N], const ScanMaps<M> &maps, int64_t r0, int c, uint32_t bytes, uint64_t *arrived) {
+    static_assert(M == N * Raw::PHASES && M <= 32, "a box per lane");
+    if constexpr (Raw::PHASES == 1) {
+        if (threadIdx.x != 0) return;
+        sm103::mbar_arrive_expect_tx(arrived, bytes + sizeof(raw));
+#pragma unroll
+        for (int k = 0; k < N; ++k) tma_box(raw[k].e, maps.m[k], arrived, c, (int)r0);
+        return;
+    }
+    if (threadIdx.x >= 32) return;
+    if (threadIdx.x == 0) sm103::mbar_arrive_expect_tx(arrived, bytes + sizeof(raw));
+    __syncwarp();
+    if (threadIdx.x < M)
+        tma_box(raw[threadIdx.x / Raw::PHASES].e[threadIdx.x % Raw::PHASES], maps.m[threadIdx.x], arrived, c, (int)(r0 / Raw::PHASES));
+}
+// V elements from any place of a row in shared memory.
+template <typename E, int V>
+__device__ __forceinline__ Pack<E, V> pick(const E *row, int at) {
+    Pack<E, V> t;
+    if constexpr (sizeof(E) == 4) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) t.e[v] = row[at + v];
+    } else {
+        static_assert(V == 4, "two words");
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(row) + (at >> 1);
+        const uint32_t w0 = w[0], w1 = w[1], w2 = w[2], by = (at & 1) * 16;
+        uint32_t *to = reinterpret_cast<uint32_t *>(t.e);
+        to[0] = __funnelshift_r(w0, w1, by);
+        to[1] = __funnelshift_r(w1, w2, by);
+    }
+    return t;
+}
+// Without maps: bulk copies of a tile's rows, one or two to a thread, which all arrive at
+// `arrived`, this one with `bytes` more.  What a granule holds before the tensor's first
+// element or after its last one is not read: the elements there are copied by themselves.
+template <typename E, typename S, int N>
+__device__ __forceinline__ void fetch_rows(RawTile<E, S, false> (&raw)[N], const void *const (&src)[N], const int64_t (&stride)[N],
+                                           int64_t rows, int64_t D, int64_t r0, int c, uint32_t bytes, uint64_t *arrived) {
+    constexpr int PER = (N * S::ROWS + S::THREADS - 1) / S::THREADS;
+    const int n = (int)min(D - c, (int64_t)S::CB);
+    uintptr_t from[PER];
+    uint32_t to[PER], size[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        const int j = threadIdx.x + u * S::THREADS, k = j / S::ROWS, row = j % S::ROWS;
+        size[u] = 0;
+        if (k >= N || r0 + row >= rows) continue;
+        uintptr_t begin = 0;
+        int64_t step = 0;
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+            if (q == k) begin = reinterpret_cast<uintptr_t>(src[q]), step = stride[q];
+        const uintptr_t end = begin + ((rows - 1) * step + D) * sizeof(E), a = begin + ((r0 + row) * step + c) * sizeof(E);
+        const uintptr_t z = a + n * sizeof(E), floor = a / 16 * 16, ceil = (z + 15) / 16 * 16;
+        const uintptr_t lo = floor < begin ? floor + 16 : floor, hi = ceil > end ? ceil - 16 : ceil;
+        const uint32_t slot = sm103::smem_u32(raw[k].row(row));
+        if (lo > a || hi < z) {
+            for (int m = 0; m < n; ++m) {
+                const uintptr_t at = a + m * sizeof(E);
+                if (at < lo || at >= hi) raw[k].row(row)[(a - floor) / sizeof(E) + m] = *reinterpret_cast<const E *>(at);
+            }
+            sm103::fence_proxy_async_smem();
+        }
+        if (hi > lo) from[u] = lo, to[u] = slot + (uint32_t)(lo - floor), size[u] = (uint32_t)(hi - lo);
+        bytes += size[u];
+    }
+    sm103::mbar_arrive_expect_tx(arrived, bytes);
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+        if (size[u]) sm103::bulk_load(to[u], reinterpret_cast<const void *>(from[u]), size[u], sm103::smem_u32(arrived));
+}
+
 // Workspace of a scan and its tiles.  Maps [row tile][padded channel], states after a
 // group [group][padded channel], then the first sequence of every row tile.
 struct ScanPlan {
@@ -154,11 +270,6 @@ struct ChannelGates {
         for (int v = 0; v < V; ++v) k0[v] = g.e[v].k0, k1[v] = g.e[v].k1;
     }
 };
-
-// Tensor maps of a scan's inputs: one thread loads a tile with one instruction per tensor.
-// (With 8 bytes per thread and row the copies' own issue was a fifth of a tile's time:
-// 119 us forward and 289 us backward on 8192 x 8192 bf16.)
-struct ScanMaps { CUtensorMap m[4]; };
 
 // One map after the other where neither cuts.
 template <bool CUTS>
