@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas)
         if (TMA || maps.boxed) {
             fetch_boxes(sh.raw, maps, w.rt * S::ROWS, w.cb * CB, sizeof(sh.gates), &sh.arrived);
         } else if constexpr (!TMA) {
-            fetch_rows<E, S, 3>(sh.raw, {p.x, p.i, p.g}, {p.xs, p.is, p.gs}, p.rows, p.D, w.rt * S::ROWS, w.cb * CB,
-                             tid == 0 ? sizeof(sh.gates) : 0, &sh.arrived);
+            fetch_elements<E, S, 3>(sh.raw, {p.x, p.i, p.g}, {p.xs, p.is, p.gs}, p.rows, p.D, w.rt * S::ROWS, w.cb * CB,
+                                    tid == 0 ? sizeof(sh.gates) : 0, &sh.arrived);
         }
     };
     // and of what the scan's first part has left for the tile; returns its first sequence
@@ -132,8 +132,7 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas)
         {
             const ChannelGates<V> gc(sh.gates[lane]);
             const auto raw = [&](int k, int r, float (&f)[V]) {
-                const int row = rg * L + r;
-                unpack<E, V>(TMA ? sh.raw[k].at(row, lane) : pick<E, V>(sh.raw[k].row(row), starts[k][row] + lane * V), f);
+                unpack<E, V>(TMA ? sh.raw[k].at(rg, r, lane) : pick<E, V>(sh.raw[k].row(rg, r), starts[k][rg * L + r] + lane * V), f);
             };
 #pragma unroll
             for (int r = 0; r < L; ++r) {

@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 || !TMA ?
         if (TMA || maps.boxed) {
             fetch_boxes(sh.raw[stage], maps, rt * S::ROWS, w.cb * CB, sizeof(sh.gates[0]), &sh.arrived[stage]);
         } else if constexpr (!TMA) {
-            fetch_rows<E, S, 4>(sh.raw[stage], {p.x, p.i, p.g, p.dout}, {p.xs, p.is, p.gs, p.ds}, p.rows, p.D, rt * S::ROWS, w.cb * CB,
-                             tid == 0 ? sizeof(sh.gates[0]) : 0, &sh.arrived[stage]);
+            fetch_elements<E, S, 4>(sh.raw[stage], {p.x, p.i, p.g, p.dout}, {p.xs, p.is, p.gs, p.ds}, p.rows, p.D, rt * S::ROWS,
+                                    w.cb * CB, tid == 0 ? sizeof(sh.gates[0]) : 0, &sh.arrived[stage]);
         }
     };
     // and of what the scan's first part has left for the tile; returns its first sequence
@@ -109,16 +109,16 @@ __global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 || !TMA ?
             for (int k = 0; k < 4; ++k) {
                 Pack<E, V> t[L];
 #pragma unroll
-                for (int r = 0; r < L; ++r) t[r] = pick<E, V>(sh.raw[stage][k].row(rg * L + r), starts[k][rg * L + r] + lane * V);
+                for (int r = 0; r < L; ++r) t[r] = pick<E, V>(sh.raw[stage][k].row(rg, r), starts[k][rg * L + r] + lane * V);
                 __syncwarp();
 #pragma unroll
-                for (int r = 0; r < L; ++r) sh.raw[stage][k].at(rg * L + r, lane) = t[r];
+                for (int r = 0; r < L; ++r) sh.raw[stage][k].at(rg, r, lane) = t[r];
             }
             fence_proxy_async_smem();   // before the copies that follow this tile
         }
 
         const ChannelGates<V> gc(sh.gates[stage][lane]);
-        const auto raw = [&](int k, int r, float (&f)[V]) { unpack<E, V>(sh.raw[stage][k].at(rg * L + r, lane), f); };
+        const auto raw = [&](int k, int r, float (&f)[V]) { unpack<E, V>(sh.raw[stage][k].at(rg, r, lane), f); };
         float a[L][V], kept_g[L][V], kept_i[L][V];   // for the second half
         Pack<float, V> mA, mH, mB, mF;
 #pragma unroll

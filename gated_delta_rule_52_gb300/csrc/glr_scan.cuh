@@ -90,8 +90,12 @@ template <typename E, typename S, bool TMA>
 struct RawTile {
     static constexpr int PHASES = TMA ? 1 : 16 / (int)sizeof(E), PITCH = S::CB + (TMA ? 0 : PHASES), EACH = S::ROWS / PHASES;
     E e[PHASES][EACH][PITCH];
-    __device__ __forceinline__ E *row(int r) { return e[r % PHASES][r / PHASES]; }
-    __device__ __forceinline__ Pack<E, S::V> &at(int r, int lane) { return *reinterpret_cast<Pack<E, S::V> *>(row(r) + lane * S::V); }
+    static_assert(S::L % PHASES == 0 || PHASES % S::L == 0, "a row group's phases follow each other");
+    // row r of a row group
+    __device__ __forceinline__ E *row(int rg, int r) {
+        return &e[rg * S::L % PHASES][rg * S::L / PHASES][0] + (r % PHASES * EACH + r / PHASES) * PITCH;
+    }
+    __device__ __forceinline__ Pack<E, S::V> &at(int rg, int r, int lane) { return *reinterpret_cast<Pack<E, S::V> *>(row(rg, r) + lane * S::V); }
 };
 template <typename E>
 struct RowStart {
@@ -158,44 +162,23 @@ __device__ __forceinline__ Pack<E, V> pick(const E *row, int at) {
     }
     return t;
 }
-// Without maps: bulk copies of a tile's rows, one or two to a thread, which all arrive at
-// `arrived`, this one with `bytes` more.  What a granule holds before the tensor's first
-// element or after its last one is not read: the elements there are copied by themselves.
+// Without maps: the elements one by one.  Every thread arrives, with `bytes` more to come.
 template <typename E, typename S, int N>
-__device__ __forceinline__ void fetch_rows(RawTile<E, S, false> (&raw)[N], const void *const (&src)[N], const int64_t (&stride)[N],
-                                           int64_t rows, int64_t D, int64_t r0, int c, uint32_t bytes, uint64_t *arrived) {
-    constexpr int PER = (N * S::ROWS + S::THREADS - 1) / S::THREADS;
-    const int n = (int)min(D - c, (int64_t)S::CB);
-    uintptr_t from[PER];
-    uint32_t to[PER], size[PER];
+__device__ __forceinline__ void fetch_elements(RawTile<E, S, false> (&raw)[N], const void *const (&src)[N], const int64_t (&stride)[N],
+                                               int64_t rows, int64_t D, int64_t r0, int c, uint32_t bytes, uint64_t *arrived) {
+    using Raw = RawTile<E, S, false>;
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-        const int j = threadIdx.x + u * S::THREADS, k = j / S::ROWS, row = j % S::ROWS;
-        size[u] = 0;
-        if (k >= N || r0 + row >= rows) continue;
-        uintptr_t begin = 0;
-        int64_t step = 0;
-#pragma unroll
-        for (int q = 0; q < N; ++q)
-            if (q == k) begin = reinterpret_cast<uintptr_t>(src[q]), step = stride[q];
-        const uintptr_t end = begin + ((rows - 1) * step + D) * sizeof(E), a = begin + ((r0 + row) * step + c) * sizeof(E);
-        const uintptr_t z = a + n * sizeof(E), floor = a / 16 * 16, ceil = (z + 15) / 16 * 16;
-        const uintptr_t lo = floor < begin ? floor + 16 : floor, hi = ceil > end ? ceil - 16 : ceil;
-        const uint32_t slot = sm103::smem_u32(raw[k].row(row));
-        if (lo > a || hi < z) {
-            for (int m = 0; m < n; ++m) {
-                const uintptr_t at = a + m * sizeof(E);
-                if (at < lo || at >= hi) raw[k].row(row)[(a - floor) / sizeof(E) + m] = *reinterpret_cast<const E *>(at);
-            }
-            sm103::fence_proxy_async_smem();
+    for (int k = 0; k < N; ++k) {
+        const RowStart<E> start(src[k], stride[k]);
+#pragma unroll 4
+        for (int j = threadIdx.x; j < S::ROWS * S::CB; j += S::THREADS) {
+            const int row = j / S::CB, m = j % S::CB;
+            if (r0 + row < rows && c + m < D)
+                raw[k].e[row % Raw::PHASES][row / Raw::PHASES][start[row] + m] = static_cast<const E *>(src[k])[(r0 + row) * stride[k] + c + m];
         }
-        if (hi > lo) from[u] = lo, to[u] = slot + (uint32_t)(lo - floor), size[u] = (uint32_t)(hi - lo);
-        bytes += size[u];
     }
+    sm103::fence_proxy_async_smem();
     sm103::mbar_arrive_expect_tx(arrived, bytes);
-#pragma unroll
-    for (int u = 0; u < PER; ++u)
-        if (size[u]) sm103::bulk_load(to[u], reinterpret_cast<const void *>(from[u]), size[u], sm103::smem_u32(arrived));
 }
 
 // Workspace of a scan and its tiles.  Maps [row tile][padded channel], states after a

@@ -107,6 +107,8 @@ def _glr_check(got, want):
     (1, 130, 40, 3, F, BF, None, "dense"),         # many narrow ones
     (1, 4500, 1, 8, HF, F, -5.0, "slice"),         # few channels, many tiles
     (1, 2100, 2, 29, HF, F, None, "odd"),
+    (1, 200, 1, 65, BF, F, -5.0, "dense"),         # unaligned, one channel in the last block
+    (1, 200, 5, 26, BF, F, None, "dense"),         # rows of 4-byte alignment
 ])
 def test_glr(B, T, H, K, dt, sd, lb, how):
     d = _glr_inputs(B, T, H, K, dt, None, sd, T + H)
@@ -119,6 +121,9 @@ def test_glr(B, T, H, K, dt, sd, lb, how):
     ((1,) * 37 + (0, 300), 3, 24, HF, F, -5.0),
     ((0, 0, 0), 2, 16, BF, F, None),               # sequences without tokens only
     ((900, 3, 1200, 130, 129, 128, 127), 2, 33, BF, F, None),
+    ((2, 3), 1, 33, BF, F, -5.0),                  # fewer unaligned rows than 16 bytes have elements
+    ((1, 70), 3, 33, F, None, -5.0),
+    ((65, 7, 0, 191), 5, 51, HF, BF, -5.0),
 ])
 def test_glr_ragged(lens, H, K, dt, sd, lb):
     d = _glr_inputs(1, sum(lens), H, K, dt, lens, sd, len(lens))
