@@ -18,12 +18,20 @@ __device__ __forceinline__ void copy_async(void *slot, const void *src) {
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(sm103::smem_u32(slot)), "l"(src), "n"(n) : "memory");
 }
+// What a thread's slot holds of a row: its V elements, or the 4-byte words around V 16-bit
+// elements whose row may begin inside a word.
+template <int N>
+struct Words { uint32_t w[N]; };
+template <typename E, int V, bool WIDE>
+using RowSlot = std::conditional_t<WIDE || sizeof(E) == 4, Pack<E, V>, Words<V / 2 + 1>>;
 // Copies `count` <= N groups of V elements, `stride` elements apart, into slots THREADS
 // groups apart.  WIDE: every group is aligned to its size and whole.  Else its first `cols`
-// elements are copied one by one; 2-byte elements have no asynchronous copy: they are
-// loaded together, then stored.
+// <= V elements are copied: 4-byte ones one by one, 2-byte ones, which have no asynchronous
+// copy, as words, the last one no further than the elements go.  (Loaded and stored one by
+// one they held up every group of rows: the convolution of 16384 x 4095 bf16 took 183 us
+// forward and, of 8192 x 4095, 240 us backward; with words 100 us both.)
 template <typename E, int V, bool WIDE, int N, int THREADS>
-__device__ __forceinline__ void copy_rows(Pack<E, V> *slots, const E *src, int64_t stride, int count, int cols) {
+__device__ __forceinline__ void copy_rows(RowSlot<E, V, WIDE> *slots, const E *src, int64_t stride, int count, int cols) {
     if constexpr (WIDE) {
         if (count >= N) {
 #pragma unroll
@@ -40,20 +48,35 @@ __device__ __forceinline__ void copy_rows(Pack<E, V> *slots, const E *src, int64
                 if (r < count && v < cols) copy_async<4>(&slots[r * THREADS].e[v], src + v);
         }
     } else {
-        constexpr int G = 4;   // rows in registers together
-        E t[G * V];
 #pragma unroll
-        for (int r0 = 0; r0 < N; r0 += G) {
+        for (int r = 0; r < N; ++r, src += stride) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(src), word = at & ~(uintptr_t)3;
+            const int bytes = 2 * cols + (int)(at & 2);
 #pragma unroll
-            for (int k = 0; k < G * V; ++k)
-                if (r0 + k / V < count && k % V < cols) t[k] = src[k / V * stride + k % V];
-#pragma unroll
-            for (int k = 0; k < G * V; ++k)
-                if (r0 + k / V < count && k % V < cols) slots[(r0 + k / V) * THREADS].e[k % V] = t[k];
-            src += G * stride;
+            for (int k = 0; k < V / 2 + 1; ++k)
+                if (r < count && 4 * k < bytes)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sm103::smem_u32(&slots[r * THREADS].w[k])),
+                                 "l"(word + 4 * k), "r"(min(bytes - 4 * k, 4))
+                                 : "memory");
         }
     }
 }
+// The elements of a slot; `odd`: its row begins in the middle of a word.
+template <typename E, int V>
+__device__ __forceinline__ void take(const Pack<E, V> &slot, int, float (&f)[V]) { unpack<E, V>(slot, f); }
+template <typename E, int V>
+__device__ __forceinline__ void take(const Words<V / 2 + 1> &slot, int odd, float (&f)[V]) {
+    Pack<E, V> t;
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) reinterpret_cast<uint32_t *>(t.e)[k] = __funnelshift_r(slot.w[k], slot.w[k + 1], 16 * odd);
+    unpack<E, V>(t, f);
+}
+// Whether the rows of 16-bit elements from p on begin in the middle of a word.
+struct RowParity {
+    int first, step;
+    __device__ __forceinline__ RowParity(const void *p, int64_t stride) : first((int)(reinterpret_cast<uintptr_t>(p) >> 1 & 1)), step((int)(stride & 1)) {}
+    __device__ __forceinline__ int operator[](int r) const { return first ^ (step & r & 1); }
+};
 // Stores V values, or the first `cols` of them one by one.
 template <typename E, int V, bool WIDE>
 __device__ __forceinline__ void st_cols(E *p, const float (&f)[V], int cols) {

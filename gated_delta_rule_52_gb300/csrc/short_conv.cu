@@ -130,10 +130,12 @@ __device__ __forceinline__ void each_empty(const ConvParams &p, F &&f) {
 
 constexpr int kBatch = 4, kStages = 3;   // rows per copy group, groups of a thread's ring
 
+// 16384 x 4096 fp16, W = 4: 56 us, 4.8 TB/s, issue at 62% (a plain copy of the same bytes
+// 47 us).
 template <typename E, bool WIDE, int W>
 __global__ void __launch_bounds__(kThreads, 4) conv_fwd_kernel(ConvParams p, Runs runs, int channel_blocks) {
     extern __shared__ __align__(16) unsigned char smem[];
-    auto &ring = *reinterpret_cast<Pack<E, V>(*)[kStages][kBatch][kThreads]>(smem);
+    auto &ring = *reinterpret_cast<RowSlot<E, V, WIDE>(*)[kStages][kBatch][kThreads]>(smem);
     const int tid = threadIdx.x;
     const int64_t q = (int64_t)(blockIdx.x / channel_blocks) * kGroups + tid / kLanes;
     const int64_t c = ((int64_t)(blockIdx.x % channel_blocks) * kLanes + tid % kLanes) * V;
@@ -157,8 +159,9 @@ __global__ void __launch_bounds__(kThreads, 4) conv_fwd_kernel(ConvParams p, Run
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) ld_x<E, V, WIDE>(p, r.n, r.lo, r.s0 - (W - 1) + j, c, cols, xw[j]);
         E *out = static_cast<E *>(p.out) + r.s0 * p.os + c;
+        const RowParity odd(static_cast<const E *>(p.x) + r.s0 * p.xs + c, p.xs);   // batches begin at even rows
         const auto row = [&](int k, int stage) {
-            unpack<E, V>(ring[stage][k][tid], xw[W - 1]);
+            take<E, V>(ring[stage][k][tid], odd[k], xw[W - 1]);
             float y[V], s[V];
             taps_sum<W>(w, b, xw, y);
             if (p.silu) {
@@ -211,10 +214,13 @@ __global__ void __launch_bounds__(kThreads) conv_state_kernel(ConvParams p) {
 // input row t, or of a row of the initial state where t comes before the sequence.  So a
 // part [s0, s1) of a run walks u from s0 to s1 + W-2; rows from s1 on add to no parameter,
 // and rows after the sequence have a q of 0 but the final state's gradient.
+// 8192 x 8192 bf16, W = 4: 100 us, 4.0 TB/s; bound by issue and dependent arithmetic at the
+// 16 warps per SM that its windows' registers leave.  2 channels per thread: 123 us; a ring
+// filled by tensor maps: 102 us, and the forward pass's call of one token 16 us instead of 9.
 template <typename E, bool WIDE, int W>
 __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvParams p, Runs runs, int channel_blocks, float *part) {
     extern __shared__ __align__(16) unsigned char smem[];
-    auto &ring = *reinterpret_cast<Pack<E, V>(*)[kStages][2][kBatch][kThreads]>(smem);   // x, dout
+    auto &ring = *reinterpret_cast<RowSlot<E, V, WIDE>(*)[kStages][2][kBatch][kThreads]>(smem);   // x, dout
     auto &sums = *reinterpret_cast<float (*)[kGroups][W + 1][kLanes * V]>(smem);         // after the walk
     const int tid = threadIdx.x, lane = tid % kLanes, group = tid / kLanes;
     const int64_t block = blockIdx.x / channel_blocks, q = block * kGroups + group;
@@ -254,11 +260,12 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvParams p, Run
                 for (int v = 0; v < V; ++v) qs[j][v] = 0.f;
             }
             E *dx = static_cast<E *>(p.dx) + (r.s0 - (W - 1)) * p.D + c;
+            const RowParity x_odd(static_cast<const E *>(p.x) + r.s0 * p.xs + c, p.xs), d_odd(static_cast<const E *>(p.dout) + r.s0 * p.ds + c, p.ds);
             // q of the row in slot k, whose window is complete
             const auto form_q = [&](int k, int stage) {
                 float (&qn)[V] = qs[W - 1];
-                unpack<E, V>(ring[stage][0][k][tid], xw[W - 1]);
-                unpack<E, V>(ring[stage][1][k][tid], qn);
+                take<E, V>(ring[stage][0][k][tid], x_odd[k], xw[W - 1]);
+                take<E, V>(ring[stage][1][k][tid], d_odd[k], qn);
                 if (p.silu) {   // silu' = s (1 + y (1 - s))
                     float y[V], s[V], o[V], one[V];
                     taps_sum<W>(w, b, xw, y);
@@ -413,7 +420,7 @@ cudaError_t launch_conv_fwd(const ConvParams &p0, int sms, cudaStream_t stream) 
         const int64_t blocks = ceil_div(p.D, kLanes * V);
         if (p.rows > 0) {
             constexpr auto kernel = conv_fwd_kernel<E, WIDE, W>;
-            constexpr int smem = (int)sizeof(Pack<E, V>) * kStages * kBatch * kThreads;
+            constexpr int smem = (int)sizeof(RowSlot<E, V, WIDE>) * kStages * kBatch * kThreads;
             const cudaError_t e = allow_smem<kernel>(smem);
             if (e != cudaSuccess) return e;
             kernel<<<(unsigned)(run_blocks(runs) * blocks), kThreads, smem, stream>>>(p, runs, (int)blocks);
@@ -433,7 +440,7 @@ cudaError_t launch_conv_bwd(const ConvParams &p, unsigned char *ws, int sms, cud
         const int64_t blocks = ceil_div(p.D, kLanes * V);
         if (p.rows == 0) return cudaSuccess;
         constexpr auto kernel = conv_bwd_kernel<E, WIDE, W>;
-        constexpr int smem = (int)std::max(sizeof(Pack<E, V>) * kStages * 2 * kBatch * kThreads, sizeof(float) * kGroups * (W + 1) * kLanes * V);
+        constexpr int smem = (int)std::max(sizeof(RowSlot<E, V, WIDE>) * kStages * 2 * kBatch * kThreads, sizeof(float) * kGroups * (W + 1) * kLanes * V);
         const cudaError_t e = allow_smem<kernel>(smem);
         if (e != cudaSuccess) return e;
         kernel<<<(unsigned)(run_blocks(runs) * blocks), kThreads, smem, stream>>>(p, runs, (int)blocks, part);

@@ -383,6 +383,8 @@ def _conv_check(got, want):
     (3, 2, 40, 4, BF, None, True, None, "dense"),
     (1, 5, 1, 2, F, None, False, "silu", "dense"),
     (2, 33, 77, 3, BF, None, True, "silu", "odd"),
+    (2, 71, 66, 4, HF, None, True, "silu", "odd"),
+    (1, 20, 131, 3, BF, (7, 0, 13), True, None, "dense"),
     (1, 64, 128, 4, HF, None, False, "silu", "slice"),
     (4, 65, 129, 2, F, None, True, None, "odd"),
     (1, 1000, 200, 4, BF, None, True, "silu", "dense"),
