@@ -7,7 +7,7 @@
 //
 // One pass over tiles of 64 rows from the last to the first (glr_scan.cuh).  h_{t-1} is
 // recomputed in fp32: a tile's rows are those of one checkpoint, so the forward states need
-// no other tile.  A thread forms the decays of its 16 elements and folds them forward (from
+// no other tile.  A thread forms the decays of its elements and folds them forward (from
 // the checkpoint) and backward (into the map that the tile hands on); with the states that
 // enter its rows from both sides it then forms the gradients, the inputs still in shared
 // memory and three values per element in registers.  Inputs are read and gradients written
@@ -21,17 +21,20 @@ namespace {
 
 using namespace layer;
 
-// 16 elements per thread: 4 rows by 4 channels in 16 bits, 8 by 2 in 32 bits (the raw
-// inputs of two tiles in shared memory allow 2 and 3 CTAs per SM; 2 also in 32 bits with
-// unaligned rows, which take more of it: that alone is 171 us instead of 147 on 20011 x 836).
+// 16 bits: 4 rows by 4 channels per thread, 2 CTAs per SM (the raw inputs of two tiles each
+// in shared memory).  32 bits: 8 rows by 2 channels and 3 CTAs of 128 threads (20011 x 836:
+// 146 us; 2 CTAs of 256: 149; 8192 x 8192: 323 and 340).  There the granules of unaligned
+// rows leave room for 2 CTAs only, so they have 256 threads of 4 rows: 20011 x 847 176 us,
+// with 128 threads 201.
 // 8192 x 8192 bf16: 235 us, 4.0 TB/s; what bounds it is issue, 70 instructions per element
-// between barriers, at 55% of the slots.  Unaligned rows: 8192 x 3937 bf16 264 us (aligned
-// 3968: 130 us), 20011 x 847 fp32 201 us; element-wise copies took 475 and 214 us.
-template <typename E> using BwdShape = TileShape<kGlrCheckpointRows, sizeof(E) == 2 ? 256 : 128, 16, sizeof(E) == 2 ? 4 : 2>;
+// between barriers, at 55% of the slots.  Unaligned: 8192 x 3937 bf16 264 us (aligned 3968:
+// 130 us); element-wise copies took 475 us, and 214 us on 20011 x 847 fp32.
+template <typename E, bool TMA>
+using BwdShape = TileShape<kGlrCheckpointRows, sizeof(E) == 2 || !TMA ? 256 : 128, 16, sizeof(E) == 2 ? 4 : 2>;
 
 template <typename E, bool TMA>
 struct BwdShared {
-    using S = BwdShape<E>;
+    using S = BwdShape<E, TMA>;
     RawTile<E, S, TMA> raw[2][4];                                  // x, i, g, dout
     Pack<GateConst, S::V> gates[2][S::CL];
     Pack<float, S::V> A[S::RG][S::CL], H[S::RG][S::CL];            // forward maps of the row groups
@@ -43,13 +46,14 @@ struct BwdShared {
 };
 
 template <typename E, bool TMA, bool UB>
-__global__ void __launch_bounds__(BwdShape<E>::THREADS, sizeof(E) == 2 || !TMA ? 2 : 3)
-    glr_bwd_scan_kernel(GlrParams p, ScanPlan s, const __grid_constant__ ScanMaps<4 * RawTile<E, BwdShape<E>, TMA>::PHASES> maps, float *part_ddt, float *part_dA) {
+__global__ void __launch_bounds__(BwdShape<E, TMA>::THREADS, sizeof(E) == 2 || !TMA ? 2 : 3)
+    glr_bwd_scan_kernel(GlrParams p, ScanPlan s, const __grid_constant__ ScanMaps<4 * RawTile<E, BwdShape<E, TMA>, TMA>::PHASES> maps,
+                        float *part_ddt, float *part_dA) {
     using namespace sm103;
-    using S = BwdShape<E>;
+    using S = BwdShape<E, TMA>;
     constexpr int CL = S::CL, V = S::V, L = S::L, CB = S::CB, RG = S::RG;
     constexpr bool EXACT = sizeof(E) == 4;
-    static_assert(S::THREADS >= 3 * CB && L * V == 16, "roles");
+    static_assert(S::THREADS >= 3 * CB, "roles");
     extern __shared__ __align__(128) unsigned char smem[];
     BwdShared<E, TMA> &sh = *reinterpret_cast<BwdShared<E, TMA> *>(smem);
     const int tid = threadIdx.x, lane = tid % CL, rg = tid / CL;
@@ -386,7 +390,7 @@ struct BwdPlan {
 BwdPlan bwd_plan(const GlrParams &p, int sms, unsigned char *ws) {
     BwdPlan b;
     size_t at = 0;
-    b.s = p.dtype == kFP32 ? scan_plan<BwdShape<float>>(p.rows, p.D, ws, &at) : scan_plan<BwdShape<__half>>(p.rows, p.D, ws, &at);
+    b.s = p.dtype == kFP32 ? scan_plan<BwdShape<float, true>>(p.rows, p.D, ws, &at) : scan_plan<BwdShape<__half, true>>(p.rows, p.D, ws, &at);
     const size_t part = (size_t)(b.s.row_tiles * b.s.width) * sizeof(float);
     const size_t ck = p.checkpoints ? 0 : ((size_t)(b.s.row_tiles * p.D) * sizeof(float) + 15) / 16 * 16;
     b.part_ddt = reinterpret_cast<float *>(ws + at);
@@ -400,7 +404,7 @@ BwdPlan bwd_plan(const GlrParams &p, int sms, unsigned char *ws) {
 template <typename E, bool TMA, bool UB>
 cudaError_t run(const GlrParams &p, const BwdPlan &b, int sms, cudaStream_t stream) {
     ScanPlan s = b.s;
-    using S = BwdShape<E>;
+    using S = BwdShape<E, TMA>;
     using Raw = RawTile<E, S, TMA>;
     ScanMaps<4 * Raw::PHASES> maps{};
     maps.boxed = p.rows >= Raw::PHASES && p.xs >= p.D && p.is >= p.D && p.gs >= p.D && p.ds >= p.D;
@@ -413,13 +417,13 @@ cudaError_t run(const GlrParams &p, const BwdPlan &b, int sms, cudaStream_t stre
     int ctas = 0;
     constexpr int bytes = (int)sizeof(BwdShared<E, TMA>);
     constexpr auto kernel = glr_bwd_scan_kernel<E, TMA, UB>;
-    const cudaError_t e = resident_ctas<kernel>(BwdShape<E>::THREADS, bytes, ctas);
+    const cudaError_t e = resident_ctas<kernel>(BwdShape<E, TMA>::THREADS, bytes, ctas);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)std::max(std::min(s.row_tiles * s.blocks, (int64_t)sms * ctas), (int64_t)1);
     GlrParams arg = p;
     float *ddt = b.part_ddt, *dA = b.part_dA;
     void *args[] = {&arg, &s, &maps, &ddt, &dA};
-    return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(BwdShape<E>::THREADS), args,
+    return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(BwdShape<E, TMA>::THREADS), args,
                                        bytes, stream);
 }
 

@@ -87,7 +87,8 @@ struct TileShape {
 // place in a granule (RowStart) and takes up to one granule more.  PHASES rows apart that
 // place is the same: these rows lie together, and a tensor map of theirs has a legal pitch.
 // (A bulk copy per row instead was as fast in the 16-bit backward pass, but 115 us against
-// 99 in the forward one, 8192 x 3937 bf16, and 238 against 201 on 20011 x 847 fp32 backward.)
+// 99 in the forward one, 8192 x 3937 bf16, and 238 against then 201 on 20011 x 847 fp32
+// backward.)
 template <typename E, typename S, bool TMA>
 struct RawTile {
     static constexpr int PHASES = TMA ? 1 : 16 / (int)sizeof(E), PITCH = S::CB + (TMA ? 0 : PHASES), EACH = S::ROWS / PHASES;
