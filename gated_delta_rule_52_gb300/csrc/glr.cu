@@ -57,12 +57,17 @@ __global__ void __launch_bounds__(128) glr_fwd_step_kernel(GlrParams p) {
     }
 }
 
-// 8 rows by 4 channels per thread, 5 CTAs per SM.  Measured on 8192 x 8192 bf16: 118 us,
-// with 4 CTAs 120 us, with 256 threads of 4 rows (3 CTAs) 133 us (twice the per-thread work
-// of a tile), with tiles of 32 rows (7 CTAs) 131 us, with two tiles in flight per CTA, the next one's map handed on before the
-// current one's state is taken (3 CTAs), 163 us (12 warps per SM are too few).
+// 8 rows by 4 channels per thread.  16 bits: 5 CTAs per SM, 8192 x 8192 bf16 103 us, 5.2 TB/s
+// (4 CTAs: 107; 3 CTAs of 256 threads with 4 rows: 131; before the tensor maps, at then 118 us,
+// tiles of 32 rows on 7 CTAs 131, and two tiles in flight per CTA, the next one's map handed
+// on before the current one's state is taken, on 3 CTAs 163).  What bounds it: the barriers
+// between a tile's phases, issue at 57% of the slots.  In 32 bits shared memory holds 4 CTAs,
+// 3 of unaligned rows, and the threads have that many more registers: 8192 x 3937 106 us, 114
+// with the registers of 5.  Unaligned 16-bit rows: 8192 x 3937 94 us (aligned 3968: 59 us;
+// element-wise copies 165 us).
 using FwdShape = TileShape<kGlrCheckpointRows, 128, 16, 4>;
-constexpr int kFwdCtas = 5;
+template <typename E, bool TMA>
+constexpr int kFwdCtas = sizeof(E) == 2 ? 5 : TMA ? 4 : 3;
 
 template <typename E, bool TMA>
 struct FwdShared {
@@ -76,7 +81,7 @@ struct FwdShared {
 };
 
 template <typename E, bool TMA, bool UB>
-__global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas)
+__global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas<E, TMA>)
     glr_fwd_scan_kernel(GlrParams p, ScanPlan s, const __grid_constant__ ScanMaps<3 * RawTile<E, FwdShape, TMA>::PHASES> maps) {
     using namespace sm103;
     using S = FwdShape;
