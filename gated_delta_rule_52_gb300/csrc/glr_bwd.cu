@@ -10,8 +10,9 @@
 // no other tile.  A thread forms the decays of its elements and folds them forward (from
 // the checkpoint) and backward (into the map that the tile hands on); with the states that
 // enter its rows from both sides it then forms the gradients, the inputs still in shared
-// memory and three values per element in registers.  Inputs are read and gradients written
-// once.  Parameter gradients leave a tile as one partial sum per channel.
+// memory and three values per element in registers.  The slopes of saturated gates are exact
+// relative to themselves: no 1 - sigma is taken of a sigma near 1.  Inputs are read and
+// gradients written once.  Parameter gradients leave a tile as one partial sum per channel.
 #include <algorithm>
 
 #include "glr_scan.cuh"
@@ -24,11 +25,12 @@ using namespace layer;
 // 16 bits: 4 rows by 4 channels per thread, 2 CTAs per SM (the raw inputs of two tiles each
 // in shared memory).  32 bits: 8 rows by 2 channels and 3 CTAs of 128 threads (20011 x 836:
 // 146 us; 2 CTAs of 256: 149; 8192 x 8192: 323 and 340).  There the granules of unaligned
-// rows leave room for 2 CTAs only, so they have 256 threads of 4 rows: 20011 x 847 176 us,
+// rows leave room for 2 CTAs only, so they have 256 threads of 4 rows: 20011 x 847 175 us,
 // with 128 threads 201.
-// 8192 x 8192 bf16: 235 us, 4.0 TB/s; what bounds it is issue, 70 instructions per element
-// between barriers, at 55% of the slots.  Unaligned: 8192 x 3937 bf16 264 us (aligned 3968:
-// 130 us); element-wise copies took 475 us, and 214 us on 20011 x 847 fp32.
+// 8192 x 8192 bf16: 237 us, 4.0 TB/s (235 with 1 - sigma(i) in place of sigma(-i)); what bounds
+// it is issue, 70 instructions per element between barriers, at 55% of the slots.  Unaligned:
+// 8192 x 3937 bf16 262 us (aligned 3968: 130 us); element-wise copies took 475 us, and 214 us
+// on 20011 x 847 fp32.
 template <typename E, bool TMA>
 using BwdShape = TileShape<kGlrCheckpointRows, sizeof(E) == 2 || !TMA ? 256 : 128, 16, sizeof(E) == 2 ? 4 : 2>;
 
@@ -52,7 +54,6 @@ __global__ void __launch_bounds__(BwdShape<E, TMA>::THREADS, sizeof(E) == 2 || !
     using namespace sm103;
     using S = BwdShape<E, TMA>;
     constexpr int CL = S::CL, V = S::V, L = S::L, CB = S::CB, RG = S::RG;
-    constexpr bool EXACT = sizeof(E) == 4;
     static_assert(S::THREADS >= 3 * CB, "roles");
     extern __shared__ __align__(128) unsigned char smem[];
     BwdShared<E, TMA> &sh = *reinterpret_cast<BwdShared<E, TMA> *>(smem);
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(BwdShape<E, TMA>::THREADS, sizeof(E) == 2 || !
 
         const ChannelGates<V> gc(sh.gates[stage][lane]);
         const auto raw = [&](int k, int r, float (&f)[V]) { unpack<E, V>(sh.raw[stage][k].at(rg, r, lane), f); };
-        float a[L][V], kept_g[L][V], kept_i[L][V];   // for the second half
+        float a[L][V], si[L][V], kept[L][V];   // for the second half: decays, sigma(i), the gates' slopes
         Pack<float, V> mA, mH, mB, mF;
 #pragma unroll
         for (int v = 0; v < V; ++v) mA.e[v] = mB.e[v] = 1.f, mH.e[v] = mF.e[v] = 0.f;
@@ -137,8 +138,9 @@ __global__ void __launch_bounds__(BwdShape<E, TMA>::THREADS, sizeof(E) == 2 || !
             for (int r = 0; r < L; ++r) {
                 float x[V], i[V], g[V], d[V], sx[V];
                 raw(0, r, x), raw(1, r, i), raw(2, r, g), raw(3, r, d);
-                token_gates_n<UB, EXACT, V>(a[r], sx, kept_g[r], kept_i[r], g, i, gc.k0, gc.k1, lb2);
-                mul_n<V>(sx, sx, x);
+                sigmoid_n<V>(si[r], i);
+                decay_and_kept_n<UB, V>(a[r], kept[r], g, gc.k0, gc.k1, lb2);
+                mul_n<V>(sx, si[r], x);
                 // forward: after the rows before; backward: f = a_0 (dout_0 + a_1 (dout_1 + ...))
                 fma_n<V>(mH.e, a[r], mH.e, sx);
                 mul_n<V>(mA.e, a[r], mA.e);
@@ -148,16 +150,17 @@ __global__ void __launch_bounds__(BwdShape<E, TMA>::THREADS, sizeof(E) == 2 || !
         } else {
 #pragma unroll 1
             for (int r = 0; r < left; ++r) {
-                float x[V], i[V], g[V], d[V], sx[V], ar[V], kg[V], ki[V];
+                float x[V], i[V], g[V], d[V], sx[V], ar[V], sr[V], kr[V];
                 raw(0, r, x), raw(1, r, i), raw(2, r, g), raw(3, r, d);
-                token_gates_n<UB, EXACT, V>(ar, sx, kg, ki, g, i, gc.k0, gc.k1, lb2);
-                mul_n<V>(sx, sx, x);
+                sigmoid_n<V>(sr, i);
+                decay_and_kept_n<UB, V>(ar, kr, g, gc.k0, gc.k1, lb2);
+                mul_n<V>(sx, sr, x);
                 const int begins = marked ? sh.marks.begins[rg * L + r] : -1, ends = marked ? sh.marks.ends[rg * L + r] : -1;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
 #pragma unroll
                     for (int k = 0; k < L; ++k)
-                        if (k == r) a[k][v] = ar[v], kept_g[k][v] = kg[v], kept_i[k][v] = ki[v];
+                        if (k == r) a[k][v] = ar[v], si[k][v] = sr[v], kept[k][v] = kr[v];
                     if (begins >= 0) {
                         const float h0 = p.init && v < cols ? ld_state(p.init, p.state_type, begins * p.D + c + v) : 0.f;
                         mA.e[v] = -0.f, mH.e[v] = fmaf(ar[v], h0, sx[v]);
@@ -228,28 +231,26 @@ __global__ void __launch_bounds__(BwdShape<E, TMA>::THREADS, sizeof(E) == 2 || !
         for (int v = 0; v < V; ++v) h[v] = h_in.e[v], f[v] = f_in.e[v];
         const int64_t row_at = r0 * p.D + c;
         // the state after a row from the one before it
-        const auto advance = [&](int r, const float (&ar)[V], const float (&ki)[V]) {
-            float x[V], i[V], si[V], o[V];
+        const auto advance = [&](int r) {
+            float x[V];
             raw(0, r, x);
-            if (EXACT) raw(1, r, i);
-            input_gates_n<EXACT, V>(si, o, i, ki);
-            mul_n<V>(si, si, x);
-            fma_n<V>(h, ar, h, si);
+            mul_n<V>(x, si[r], x);
+            fma_n<V>(h, a[r], h, x);
         };
         // the gradients of a row from its state `start` and what comes from behind
-        const auto row = [&](int r, const float (&ar)[V], const float (&kg)[V], const float (&ki)[V], const float (&start)[V]) {
-            float x[V], i[V], g[V], grad[V], si[V], o[V], out[V], slope[V], rate[V];
+        const auto row = [&](int r, const float (&start)[V]) {
+            float x[V], i[V], g[V], grad[V], o[V], out[V], slope[V], rate[V];
             raw(0, r, x), raw(2, r, g), raw(3, r, grad);
-            if (EXACT) raw(1, r, i);
             add_n<V>(grad, grad, f);
-            mul_n<V>(f, ar, grad);
-            input_gates_n<EXACT, V>(si, o, i, ki);
-            mul_n<V>(out, grad, si);
+            mul_n<V>(f, a[r], grad);
+            mul_n<V>(out, grad, si[r]);
             st_cols<E, V, TMA>(static_cast<E *>(p.dx) + row_at + r * p.D, out, cols);
+            raw(1, r, i);
+            sigmoid_n<V>(o, i, kLog2e);   // sigma(-i) anew, exact relative to itself as 1 - sigma(i) is not
             mul_n<V>(out, out, o);
             mul_n<V>(out, out, x);
             st_cols<E, V, TMA>(static_cast<E *>(p.di) + row_at + r * p.D, out, cols);
-            gate_slopes_n<UB, V>(slope, rate, g, kg, gc.k0, gc.k1, p.lower_bound);
+            gate_slopes_n<UB, V>(slope, rate, g, kept[r], gc.k0, gc.k1, p.lower_bound);
             mul_n<V>(o, f, start);        // the gradient of gk
             mul_n<V>(out, o, slope);
             st_cols<E, V, TMA>(static_cast<E *>(p.dg) + row_at + r * p.D, out, cols);
@@ -258,15 +259,22 @@ __global__ void __launch_bounds__(BwdShape<E, TMA>::THREADS, sizeof(E) == 2 || !
         };
         if (plain) {
             if (cols > 0) {
-                float start[L][V];   // the states that the rows start from
+                // The states that the rows start from; of 4 rows over the thread's own maps, which
+                // nobody reads any more, as registers are short.
+                Pack<float, V> *const slots[4] = {&sh.A[rg][lane], &sh.H[rg][lane], &sh.B[rg][lane], &sh.F[rg][lane]};
+                float start[L][V];
 #pragma unroll
                 for (int r = 0; r < L; ++r) {
 #pragma unroll
                     for (int v = 0; v < V; ++v) start[r][v] = h[v];
-                    if (r < L - 1) advance(r, a[r], kept_i[r]);
+                    if constexpr (L == 4) st_f<float, V>(slots[r]->e, h);
+                    if (r < L - 1) advance(r);
                 }
 #pragma unroll
-                for (int r = L - 1; r >= 0; --r) row(r, a[r], kept_g[r], kept_i[r], start[r]);
+                for (int r = L - 1; r >= 0; --r) {
+                    if constexpr (L == 4) ld_f<float, V>(slots[r]->e, start[r]);
+                    row(r, start[r]);
+                }
             }
         } else {
             float start[L][V];
@@ -279,7 +287,7 @@ __global__ void __launch_bounds__(BwdShape<E, TMA>::THREADS, sizeof(E) == 2 || !
                     if (begins >= 0) h[v] = p.init && v < cols ? ld_state(p.init, p.state_type, begins * p.D + c + v) : 0.f;
                     start[r][v] = h[v];
                 }
-                advance(r, a[r], kept_i[r]);
+                advance(r);
             }
 #pragma unroll
             for (int r = L - 1; r >= 0; --r) {
@@ -288,7 +296,7 @@ __global__ void __launch_bounds__(BwdShape<E, TMA>::THREADS, sizeof(E) == 2 || !
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     if (ends >= 0) f[v] = p.dfinal && v < cols ? p.dfinal[ends * p.D + c + v] : 0.f;
-                row(r, a[r], kept_g[r], kept_i[r], start[r]);
+                row(r, start[r]);
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     if (begins >= 0 && p.dinit && v < cols) p.dinit[begins * p.D + c + v] = f[v];
@@ -302,7 +310,7 @@ __global__ void __launch_bounds__(BwdShape<E, TMA>::THREADS, sizeof(E) == 2 || !
             float t = 0.f;
 #pragma unroll
             for (int q = 0; q < RG; ++q) t += sum[q][ch / V].e[ch % V];
-            (role == 0 ? part_ddt : part_dA)[rt * s.width + block + ch] = t;
+            (role == 0 ? part_ddt : part_dA)[rt * s.width + block + ch] = role == 0 ? t : t * rate_unit<UB>(p.lower_bound);
         }
     }
 }

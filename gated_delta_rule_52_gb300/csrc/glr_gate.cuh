@@ -1,6 +1,8 @@
 // The gates of the gated linear recurrence and their derivatives.
 #pragma once
 
+#include <cfloat>
+
 #include "layer_io.cuh"
 #include "sm103.cuh"
 
@@ -89,34 +91,15 @@ __device__ __forceinline__ void gate_decay_n(float (&a)[n], const float (&g)[n],
     exp2_decay_n<n>(a, x);
 }
 
-// The same and sigma(i) of n tokens or channels, with two values each that their derivatives
-// are formed from later, kept_g and kept_i.  EXACT (tensors in 32 bits): the smaller of
-// sigma(v) and sigma(-v), which is exact relative to itself, and with it sigma and its slope
-// m (1 - m) at any v.  Else (tensors in 16 bits): sigma(v) itself; 1 - sigma is then off by
-// 2^-24, below the rounding of a 16-bit gradient while 1 - sigma is above 2^-13.  (The gate
-// without a lower bound keeps the smaller one in either case: its softplus needs it.)
-template <bool UB, bool EXACT, int n>
-__device__ __forceinline__ void token_gates_n(float (&a)[n], float (&s)[n], float (&kept_g)[n], float (&kept_i)[n],
-                                              const float (&g)[n], const float (&i)[n], const float (&k0)[n],
-                                              const float (&k1)[n], float lb2) {
-    float t[n], d[n], o[n], u[n], x[n];
-    if (EXACT) {
-#pragma unroll
-        for (int j = 0; j < n; ++j) t[j] = ex2(-kLog2e * fabsf(i[j]));
-        fma_n<n>(d, t, 1.f, 1.f);
-#pragma unroll
-        for (int j = 0; j < n; ++j) d[j] = rcp(d[j]);
-        mul_n<n>(kept_i, t, d);
-        fma_n<n>(o, kept_i, -1.f, 1.f);
-#pragma unroll
-        for (int j = 0; j < n; ++j) s[j] = i[j] >= 0.f ? o[j] : kept_i[j];
-    } else {
-        sigmoid_n<n>(s, i);
-#pragma unroll
-        for (int j = 0; j < n; ++j) kept_i[j] = s[j];
-    }
+// The decays of n tokens or channels again, with what their derivatives are formed from
+// later.  Bounded: sigma(z) sigma(-z), with sigma(-z) = e^-z sigma(z), exact relative to itself;
+// 1 - sigma(z) would be 1% off at z = 12 and 0 from z = 17 on.  Else sigma(-|g + bias|).
+template <bool UB, int n>
+__device__ __forceinline__ void decay_and_kept_n(float (&a)[n], float (&kept)[n], const float (&g)[n], const float (&k0)[n],
+                                                 const float (&k1)[n], float lb2) {
+    float u[n], o[n], x[n];
     if (UB) {
-        float q[n], z[n];
+        float t[n], d[n], q[n], z[n];
 #pragma unroll
         for (int j = 0; j < n; ++j) z[j] = kLog2e;
         fma_n<n>(u, z, g, k1);
@@ -128,7 +111,7 @@ __device__ __forceinline__ void token_gates_n(float (&a)[n], float (&s)[n], floa
 #pragma unroll
         for (int j = 0; j < n; ++j) x[j] = rcp(x[j]);   // both reciprocals
         mul_n<n>(x, t, x);
-        mul_n<n>(kept_g, x, o);                         // t / (1 + t)
+        mul_n<n>(kept, x, o);                           // t / (1 + t)
         mul_n<n>(d, x, d);                              // t / (2 + t)
         mul_n<n>(z, d, d);
         atanh_poly_n<n>(q, z);
@@ -136,40 +119,23 @@ __device__ __forceinline__ void token_gates_n(float (&a)[n], float (&s)[n], floa
         mul_n<n>(x, k0, x);
     } else {
         fma_n<n>(u, k0, g, k1);                         // -log2(e) z
-        if (EXACT) {
+        // e^-z held finite: sigma(z) is 0 from 2^126 on, and the product then 0 too, not
+        // infinity times 0.  NaN stays.
 #pragma unroll
-            for (int j = 0; j < n; ++j) t[j] = ex2(-fabsf(u[j]));
-            fma_n<n>(d, t, 1.f, 1.f);
+        for (int j = 0; j < n; ++j) u[j] = min_nan(ex2(u[j]), FLT_MAX);
+        fma_n<n>(x, u, 1.f, 1.f);
 #pragma unroll
-            for (int j = 0; j < n; ++j) d[j] = rcp(d[j]);
-            mul_n<n>(kept_g, t, d);
-            fma_n<n>(o, kept_g, -1.f, 1.f);
-#pragma unroll
-            for (int j = 0; j < n; ++j) x[j] = u[j] <= 0.f ? o[j] : kept_g[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < n; ++j) t[j] = ex2(u[j]);
-            fma_n<n>(d, t, 1.f, 1.f);
-#pragma unroll
-            for (int j = 0; j < n; ++j) x[j] = kept_g[j] = rcp(d[j]);
-        }
+        for (int j = 0; j < n; ++j) x[j] = rcp(x[j]);
+        mul_n<n>(o, u, x);
+        mul_n<n>(kept, x, o);
         fma_n<n>(x, x, lb2, 0.f);
     }
     exp2_decay_n<n>(a, x);
 }
 
-// sigma(i), sigma(-i) from kept_i.
-template <bool EXACT, int n>
-__device__ __forceinline__ void input_gates_n(float (&s)[n], float (&o)[n], const float (&i)[n], const float (&kept)[n]) {
-    fma_n<n>(o, kept, -1.f, 1.f);
-#pragma unroll
-    for (int j = 0; j < n; ++j) {
-        const float m = kept[j], r = o[j];
-        s[j] = !EXACT || i[j] < 0.f ? m : r;
-        o[j] = !EXACT || i[j] < 0.f ? r : m;
-    }
-}
-// slope = d gk / d g and rate = d gk / d A_log from kept_g.
+// slope = d gk / d g and rate, which times rate_unit is d gk / d A_log, from what was kept.
+template <bool UB>
+__device__ __forceinline__ float rate_unit(float lb) { return UB ? kLn2 : -kLn2 * lb; }
 template <bool UB, int n>
 __device__ __forceinline__ void gate_slopes_n(float (&slope)[n], float (&rate)[n], const float (&g)[n], const float (&kept)[n],
                                               const float (&k0)[n], const float (&k1)[n], float lb) {
@@ -193,17 +159,14 @@ __device__ __forceinline__ void gate_slopes_n(float (&slope)[n], float (&rate)[n
         fma_n<n>(u, s, q, u);
         mul_n<n>(u, k0, u);
 #pragma unroll
-        for (int j = 0; j < n; ++j) rate[j] = kLn2 * fmaxf(u[j], -1e30f);   // a decay of 0 times its infinite log is 0
+        for (int j = 0; j < n; ++j) rate[j] = fmaxf(u[j], -1e30f);   // a decay of 0 times its infinite log is 0
     } else {
-        float l[n], o[n];
-        fma_n<n>(u, k0, g, k1);
-        fma_n<n>(o, kept, -1.f, 1.f);
-        mul_n<n>(l, kept, o);
-        fma_n<n>(l, l, -kLn2 * lb, 0.f);                                    // -ln 2 lb sigma'
-        mul_n<n>(slope, l, k0);
-        mul_n<n>(rate, l, u);
+        fma_n<n>(u, k0, g, k1);                                      // -log2(e) z
+        fma_n<n>(slope, k0, rate_unit<UB>(lb), 0.f);
+        mul_n<n>(slope, slope, kept);
+        mul_n<n>(rate, kept, u);
 #pragma unroll
-        for (int j = 0; j < n; ++j) rate[j] = l[j] == 0.f ? 0.f : rate[j];  // so is a slope of 0 times an infinite argument
+        for (int j = 0; j < n; ++j) rate[j] = kept[j] == 0.f ? 0.f : rate[j];   // so is a slope of 0 times an infinite argument
     }
 }
 

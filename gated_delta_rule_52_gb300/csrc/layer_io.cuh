@@ -141,13 +141,20 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// The smaller of two values, NaN where one is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
 // sigma(x) = 1 / (1 + e^-x); e^-x overflows to infinity for very negative x, whose
 // reciprocal is the right 0.
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
+// (sigma(-x) with kLog2e as the scale.)
 template <int n>
-__device__ __forceinline__ void sigmoid_n(float (&s)[n], const float (&x)[n]) {
-    fma_n<n>(s, x, -kLog2e, 0.f);
+__device__ __forceinline__ void sigmoid_n(float (&s)[n], const float (&x)[n], float scale = -kLog2e) {
+    fma_n<n>(s, x, scale, 0.f);
 #pragma unroll
     for (int j = 0; j < n; ++j) s[j] = ex2(s[j]);
     fma_n<n>(s, s, 1.f, 1.f);
