@@ -30,11 +30,11 @@ def _check(x, i, g, A_log, dt_bias):
         raise ValueError("x must be [B, T, H, K]")
     shape = x.shape
     B, T, H, K = shape
-    D, dtype, rows = H * K, x.dtype, _args.rows
+    D, dtype, rows, dev = H * K, x.dtype, _args.rows, _args.device("x", x)
     f32 = torch.float32
-    return (dt, shape, D, rows("x", x, dtype, shape, 2, D), rows("i", i, dtype, shape, 2, D),
-            rows("g", g, dtype, shape, 2, D), _args.tensor("A_log", A_log, f32, (H,)),
-            _args.tensor("dt_bias", dt_bias, f32, (H, K)))
+    return (dev, dt, shape, D, rows("x", x, dtype, shape, 2, D, dev), rows("i", i, dtype, shape, 2, D, dev),
+            rows("g", g, dtype, shape, 2, D, dev), _args.tensor("A_log", A_log, f32, (H,), dev),
+            _args.tensor("dt_bias", dt_bias, f32, (H, K), dev))
 
 
 def glr_fwd(x, i, g, out, A_log, dt_bias, lower_bound, initial_state=None, final_state=None,
@@ -43,15 +43,15 @@ def glr_fwd(x, i, g, out, A_log, dt_bias, lower_bound, initial_state=None, final
     ``initial_state`` itself) in place, asynchronously on ``stream`` (default: the current
     torch stream).  ``checkpoints`` (fp32, ``checkpoint_shape``) takes the states that
     ``glr_bwd`` starts from."""
-    dt, shape, D, xs, is_, gs, pA, pt = _check(x, i, g, A_log, dt_bias)
+    dev, dt, shape, D, xs, is_, gs, pA, pt = _check(x, i, g, A_log, dt_bias)
     B, T, H, K = shape
-    out_stride = _args.rows("out", out, x.dtype, shape, 2, D)
-    num_seqs, cu = _args.sequences(cu_seqlens)
-    code, init, fin = _args.states(initial_state, final_state, (num_seqs or B, H, K))
-    ck = None if checkpoints is None else _args.tensor("checkpoints", checkpoints, torch.float32, checkpoint_shape(B, T, H, K))
+    out_stride = _args.rows("out", out, x.dtype, shape, 2, D, dev)
+    num_seqs, cu = _args.sequences(cu_seqlens, dev)
+    code, init, fin = _args.states(initial_state, final_state, (num_seqs or B, H, K), dev)
+    ck = None if checkpoints is None else _args.tensor("checkpoints", checkpoints, torch.float32, checkpoint_shape(B, T, H, K), dev)
     _args.done(_args.entry("kda_glr_fwd")(
         x.data_ptr(), i.data_ptr(), g.data_ptr(), xs, is_, gs, out.data_ptr(), out_stride, dt, pA, pt, lower_bound or 0.0,
-        lower_bound is None, init, fin, code, cu, num_seqs, B, T, H, K, ck, _args.stream_handle(stream, x)))
+        lower_bound is None, init, fin, code, cu, num_seqs, B, T, H, K, ck, _args.stream_handle(stream, dev)))
 
 
 def glr_bwd(x, i, g, A_log, dt_bias, lower_bound, dout, initial_state=None, dfinal=None,
@@ -60,19 +60,19 @@ def glr_bwd(x, i, g, A_log, dt_bias, lower_bound, dout, initial_state=None, dfin
     ``dfinal`` fp32 [N,H,K] or None; ``checkpoints`` as ``glr_fwd`` left them for these
     inputs, or None (the states are recomputed).  Returns a dict of new tensors: dx, di, dg
     in the inputs' type, and fp32 dA_log, ddt_bias and dinit (None unless ``want_dinit``)."""
-    dt, shape, D, xs, is_, gs, pA, pt = _check(x, i, g, A_log, dt_bias)
+    dev, dt, shape, D, xs, is_, gs, pA, pt = _check(x, i, g, A_log, dt_bias)
     B, T, H, K = shape
-    ds = _args.rows("dout", dout, x.dtype, shape, 2, D)
-    num_seqs, cu = _args.sequences(cu_seqlens)
+    ds = _args.rows("dout", dout, x.dtype, shape, 2, D, dev)
+    num_seqs, cu = _args.sequences(cu_seqlens, dev)
     state, f32 = (num_seqs or B, H, K), torch.float32
-    code, init, _ = _args.states(initial_state, None, state)
-    dfin = _args.optional("dfinal", dfinal, f32, state)
-    ck = None if checkpoints is None else _args.tensor("checkpoints", checkpoints, f32, checkpoint_shape(B, T, H, K))
+    code, init, _ = _args.states(initial_state, None, state, dev)
+    dfin = _args.optional("dfinal", dfinal, f32, state, dev)
+    ck = None if checkpoints is None else _args.tensor("checkpoints", checkpoints, f32, checkpoint_shape(B, T, H, K), dev)
     dx, di, dg = _args.new(stream, x, shape, shape, shape)
     dA_log, ddt_bias, dinit = _args.new(stream, A_log, (H,), (H, K), state if want_dinit else None)
     _args.done(_args.entry("kda_glr_bwd")(
         x.data_ptr(), i.data_ptr(), g.data_ptr(), xs, is_, gs, dt, pA, pt, lower_bound or 0.0, lower_bound is None, init,
         code, ck, dout.data_ptr(), ds, dfin, cu, num_seqs, B, T, H, K, dx.data_ptr(), di.data_ptr(), dg.data_ptr(),
         dA_log.data_ptr(), ddt_bias.data_ptr(), None if dinit is None else dinit.data_ptr(),
-        _args.stream_handle(stream, x)))
+        _args.stream_handle(stream, dev)))
     return {"dx": dx, "di": di, "dg": dg, "dA_log": dA_log, "ddt_bias": ddt_bias, "dinit": dinit}

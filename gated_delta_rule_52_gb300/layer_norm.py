@@ -19,32 +19,32 @@ def _shape(x):
     dt, shape = _args.dtype_code("x", x), x.shape
     if not shape:
         raise ValueError("x must have at least one dimension")
-    D, lead = shape[-1], len(shape) - 1
-    return dt, shape, lead, D, _args.rows("x", x, x.dtype, shape, lead, D)
+    D, lead, dev = shape[-1], len(shape) - 1, _args.device("x", x)
+    return dev, dt, shape, lead, D, _args.rows("x", x, x.dtype, shape, lead, D, dev)
 
 
 def layer_norm_fwd(x, weight, bias, eps, out, mean=None, rstd=None, stream=None) -> None:
     """Writes ``out`` (like ``x``, and may be ``x``) and, where given, ``mean`` and ``rstd``
     (fp32, one value per row), asynchronously on ``stream`` (default: the current torch
     stream)."""
-    dt, shape, lead, D, stride = _shape(x)
-    out_stride = _args.rows("out", out, x.dtype, shape, lead, D)
+    dev, dt, shape, lead, D, stride = _shape(x)
+    out_stride = _args.rows("out", out, x.dtype, shape, lead, D, dev)
     f32, row, param = torch.float32, shape[:-1], (D,)
     _args.done(_args.entry("kda_layer_norm_fwd")(
-        x.data_ptr(), stride, _args.optional("weight", weight, f32, param), _args.optional("bias", bias, f32, param), eps,
-        out.data_ptr(), out_stride, _args.optional("mean", mean, f32, row), _args.optional("rstd", rstd, f32, row), dt,
-        math.prod(row), D, _args.stream_handle(stream, x)))
+        x.data_ptr(), stride, _args.optional("weight", weight, f32, param, dev), _args.optional("bias", bias, f32, param, dev), eps,
+        out.data_ptr(), out_stride, _args.optional("mean", mean, f32, row, dev), _args.optional("rstd", rstd, f32, row, dev), dt,
+        math.prod(row), D, _args.stream_handle(stream, dev)))
 
 
 def layer_norm_bwd(dout, x, weight, mean, rstd, want_params=None, stream=None) -> dict:
     """Gradients of sum(dout * out), with ``mean`` and ``rstd`` as the forward wrote them.
     Returns a dict of new tensors: dx (like x, contiguous), and fp32 dweight and dbias
     (None unless ``want_params``, by default where there is a weight)."""
-    dt, shape, lead, D, stride = _shape(x)
-    dout_stride = _args.rows("dout", dout, x.dtype, shape, lead, D)
+    dev, dt, shape, lead, D, stride = _shape(x)
+    dout_stride = _args.rows("dout", dout, x.dtype, shape, lead, D, dev)
     f32, row = torch.float32, shape[:-1]
-    pw = _args.optional("weight", weight, f32, (D,))
-    pm, pr = _args.tensor("mean", mean, f32, row), _args.tensor("rstd", rstd, f32, row)
+    pw = _args.optional("weight", weight, f32, (D,), dev)
+    pm, pr = _args.tensor("mean", mean, f32, row, dev), _args.tensor("rstd", rstd, f32, row, dev)
     if want_params is None:
         want_params = weight is not None
     dx, = _args.new(stream, x, shape)
@@ -53,5 +53,5 @@ def layer_norm_bwd(dout, x, weight, mean, rstd, want_params=None, stream=None) -
     _args.done(_args.entry("kda_layer_norm_bwd")(
         dout.data_ptr(), dout_stride, x.data_ptr(), stride, pw, pm, pr, dx.data_ptr(),
         dw.data_ptr() if want_params else None, db.data_ptr() if want_params else None, dt, math.prod(row), D,
-        _args.stream_handle(stream, x)))
+        _args.stream_handle(stream, dev)))
     return {"dx": dx, "dweight": dw, "dbias": db}

@@ -27,8 +27,9 @@ def _check(x, weight, bias, activation):
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be None or 'silu', got {activation!r}")
-    return (dt, shape, W, _args.rows("x", x, x.dtype, shape, 2, D), act, _args.tensor("weight", weight, f32, (D, W)),
-            _args.optional("bias", bias, f32, (D,)))
+    dev = _args.device("x", x)
+    return (dev, dt, shape, W, _args.rows("x", x, x.dtype, shape, 2, D, dev), act,
+            _args.tensor("weight", weight, f32, (D, W), dev), _args.optional("bias", bias, f32, (D,), dev))
 
 
 def short_conv_fwd(x, weight, bias, out, activation="silu", initial_state=None, final_state=None,
@@ -36,16 +37,16 @@ def short_conv_fwd(x, weight, bias, out, activation="silu", initial_state=None, 
     """Writes ``out`` (like ``x``) and, where given, ``final_state`` [N, W-1, D] (which may
     be ``initial_state`` itself) in place, asynchronously on ``stream`` (default: the
     current torch stream)."""
-    dt, shape, W, stride, act, pw, pb = _check(x, weight, bias, activation)
+    dev, dt, shape, W, stride, act, pw, pb = _check(x, weight, bias, activation)
     B, T, D = shape
-    out_stride = _args.rows("out", out, x.dtype, shape, 2, D)
-    num_seqs, cu = _args.sequences(cu_seqlens)
+    out_stride = _args.rows("out", out, x.dtype, shape, 2, D, dev)
+    num_seqs, cu = _args.sequences(cu_seqlens, dev)
     state = (num_seqs or B, W - 1, D)
     _args.done(_args.entry("kda_short_conv_fwd")(
         x.data_ptr(), stride, pw, pb, act, out.data_ptr(), out_stride, dt,
-        _args.optional("initial_state", initial_state, x.dtype, state),
-        _args.optional("final_state", final_state, x.dtype, state), cu, num_seqs, B, T, D, W,
-        _args.stream_handle(stream, x)))
+        _args.optional("initial_state", initial_state, x.dtype, state, dev),
+        _args.optional("final_state", final_state, x.dtype, state, dev), cu, num_seqs, B, T, D, W,
+        _args.stream_handle(stream, dev)))
 
 
 def short_conv_bwd(x, weight, bias, dout, activation="silu", initial_state=None, dfinal=None,
@@ -53,17 +54,17 @@ def short_conv_bwd(x, weight, bias, dout, activation="silu", initial_state=None,
     """Gradients of L = sum(dout * out) + sum(dfinal * final_state); ``dfinal`` fp32
     [N, W-1, D] or None.  Returns a dict of new tensors: dx (x's type, contiguous), and fp32
     dweight, dbias (None without a bias) and dinit (None unless ``want_dinit``)."""
-    dt, shape, W, stride, act, pw, pb = _check(x, weight, bias, activation)
+    dev, dt, shape, W, stride, act, pw, pb = _check(x, weight, bias, activation)
     B, T, D = shape
-    dout_stride = _args.rows("dout", dout, x.dtype, shape, 2, D)
-    num_seqs, cu = _args.sequences(cu_seqlens)
+    dout_stride = _args.rows("dout", dout, x.dtype, shape, 2, D, dev)
+    num_seqs, cu = _args.sequences(cu_seqlens, dev)
     state, f32 = (num_seqs or B, W - 1, D), torch.float32
-    init = _args.optional("initial_state", initial_state, x.dtype, state)
-    dfin = _args.optional("dfinal", dfinal, f32, state)
+    init = _args.optional("initial_state", initial_state, x.dtype, state, dev)
+    dfin = _args.optional("dfinal", dfinal, f32, state, dev)
     dx, = _args.new(stream, x, shape)
     dw, db, dinit = _args.new(stream, weight, (D, W), None if bias is None else (D,), state if want_dinit else None)
     _args.done(_args.entry("kda_short_conv_bwd")(
         x.data_ptr(), stride, pw, pb, act, dt, init, dout.data_ptr(), dout_stride, dfin, cu, num_seqs, B, T, D, W,
         dx.data_ptr(), dw.data_ptr(), None if db is None else db.data_ptr(), None if dinit is None else dinit.data_ptr(),
-        _args.stream_handle(stream, x)))
+        _args.stream_handle(stream, dev)))
     return {"dx": dx, "dweight": dw, "dbias": db, "dinit": dinit}

@@ -289,10 +289,11 @@ kda_status kda_fwd_static(const void *q, const void *k, const void *v, const voi
  * 2^31 - 1 packed rows, and at most 2^31 - 1 elements of a state.  cu_seqlens, num_seqs,
  * B and T are as for kda_fwd; sequences of no token are allowed (their final state is
  * their initial state).  Values of one sequence, NaN and infinity included, never reach
- * another.  The calls are asynchronous on `stream`, take their workspace (if any) from
- * kda_fwd's pool, and give the same bits for the same inputs every time.  They return
- * KDA_OK, the argument errors of kda_fwd that apply (nothing enqueued), KDA_ERR_DTYPE for
- * an unknown element type, or KDA_ERR_CUDA.
+ * another.  Tensors, cu_seqlens and `stream` are on the current device (the library does
+ * not look where a pointer lies).  The calls are asynchronous on `stream`, take their
+ * workspace (if any) from kda_fwd's pool, and give the same bits for the same inputs every
+ * time.  They return KDA_OK, the argument errors of kda_fwd that apply (nothing enqueued),
+ * KDA_ERR_DTYPE for an unknown element type, or KDA_ERR_CUDA.
  */
 
 /* Element type of a token tensor of the operators below. */
