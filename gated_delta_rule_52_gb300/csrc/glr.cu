@@ -78,6 +78,7 @@ struct FwdShared {
     Pack<float, S::V> h[S::RG][S::CL];                    // states that enter them
     TileMarks<S::ROWS> marks;
     uint64_t arrived;                                     // of a tile's copies
+    int late;
 };
 
 template <typename E, bool TMA, bool UB>
@@ -112,10 +113,12 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas<E, TMA>)
         }
         return first;
     };
+    const Waits waits{p.err, &sh.late};
     const RowStart<E> starts[3] = {{p.x, p.xs}, {p.i, p.is}, {p.g, p.gs}};
 
     if (tid == 0) {
         mbar_init(&sh.arrived, TMA || maps.boxed ? 1 : S::THREADS);
+        sh.late = 0;
         fence_mbar_init();
     }
     __syncthreads();
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas<E, TMA>)
         const int block = w.cb * CB, c = block + lane * V;
         const bool marked = mark_tile(p, rt, first, sh.marks);
         const bool plain = !marked && (rt + 1) * S::ROWS <= p.rows;   // every row inside one sequence
-        if (!mbar_wait(&sh.arrived, parity, kCopyWaitNs)) atomicExch(p.err, kErrTimeout);
+        wait_copies(&sh.arrived, parity, waits);
 
         float a[L][V], b[L][V];
         {
@@ -217,8 +220,8 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas<E, TMA>)
             // the previous group and the maps of the group's earlier tiles
             const uint32_t *before = s.states + (group - 1) * s.width + block + ch;
             const uint32_t h_bits = group > 0 ? peek(before) : 0;
-            const Affine t = join_maps(s.maps + (rt - pos) * s.width + block + ch, s.width, pos, p.err);
-            float h = apply(t, group > 0 ? __uint_as_float(await(before, h_bits, p.err)) : 0.f);
+            const Affine t = join_maps(s.maps + (rt - pos) * s.width + block + ch, s.width, pos, waits);
+            float h = apply(t, group > 0 ? __uint_as_float(await(waits, before, h_bits)) : 0.f);
             const GroupMaps<RG, CL, V> maps(sh.A, sh.H, ch);
 #pragma unroll
             for (int q = 0; q < RG; ++q) {

@@ -25,11 +25,11 @@ using namespace layer;
 // 16 bits: 4 rows by 4 channels per thread, 2 CTAs per SM (the raw inputs of two tiles each
 // in shared memory).  32 bits: 8 rows by 2 channels and 3 CTAs of 128 threads (20011 x 836:
 // 146 us; 2 CTAs of 256: 149; 8192 x 8192: 323 and 340).  There the granules of unaligned
-// rows leave room for 2 CTAs only, so they have 256 threads of 4 rows: 20011 x 847 175 us,
+// rows leave room for 2 CTAs only, so they have 256 threads of 4 rows: 20011 x 847 172 us,
 // with 128 threads 201.
-// 8192 x 8192 bf16: 237 us, 4.0 TB/s (235 with 1 - sigma(i) in place of sigma(-i)); what bounds
-// it is issue, 70 instructions per element between barriers, at 55% of the slots.  Unaligned:
-// 8192 x 3937 bf16 262 us (aligned 3968: 130 us); element-wise copies took 475 us, and 214 us
+// 8192 x 8192 bf16: 230 us, 4.1 TB/s; what bounds it is issue, 70 instructions per element
+// between barriers, at 55% of the slots.  Unaligned: 8192 x 3937 bf16 253 us (aligned 3936:
+// 126 us); element-wise copies took 475 us, and 214 us
 // on 20011 x 847 fp32.
 template <typename E, bool TMA>
 using BwdShape = TileShape<kGlrCheckpointRows, sizeof(E) == 2 || !TMA ? 256 : 128, 16, sizeof(E) == 2 ? 4 : 2>;
@@ -45,6 +45,7 @@ struct BwdShared {
     Pack<float, S::V> h[S::RG][S::CL], f[S::RG][S::CL];
     TileMarks<S::ROWS> marks;
     uint64_t arrived[2];                                           // of a tile's copies
+    int late;
 };
 
 template <typename E, bool TMA, bool UB>
@@ -84,11 +85,13 @@ __global__ void __launch_bounds__(BwdShape<E, TMA>::THREADS, sizeof(E) == 2 || !
         }
         return first;
     };
+    const Waits waits{p.err, &sh.late};
     const RowStart<E> starts[4] = {{p.x, p.xs}, {p.i, p.is}, {p.g, p.gs}, {p.dout, p.ds}};
 
     if (tid == 0) {
         mbar_init(&sh.arrived[0], TMA || maps.boxed ? 1 : S::THREADS);
         mbar_init(&sh.arrived[1], TMA || maps.boxed ? 1 : S::THREADS);
+        sh.late = 0;
         fence_mbar_init();
     }
     __syncthreads();
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(BwdShape<E, TMA>::THREADS, sizeof(E) == 2 || !
         const bool marked = mark_tile(p, rt, first, sh.marks);
         const bool plain = !marked && (rt + 1) * S::ROWS <= p.rows;        // every row inside one sequence
         const int left = cols > 0 ? (int)min(p.rows - r0, (int64_t)L) : 0;   // rows of this thread that exist
-        if (!mbar_wait(&sh.arrived[stage], parity, kCopyWaitNs)) atomicExch(p.err, kErrTimeout);
+        wait_copies(&sh.arrived[stage], parity, waits);
         parity ^= stage;
         if constexpr (!TMA) {
             // each row to its aligned place, as it is read several times (15 us of 185 on
@@ -201,8 +204,8 @@ __global__ void __launch_bounds__(BwdShape<E, TMA>::THREADS, sizeof(E) == 2 || !
             // what enters the tile and its row groups from behind
             const uint32_t *before = s.states + (group - 1) * s.width + block + ch;
             const uint32_t f_bits = group > 0 ? peek(before) : 0;
-            const Affine t = join_maps(s.maps + (walk - pos) * s.width + block + ch, s.width, pos, p.err);
-            float f = apply(t, group > 0 ? __uint_as_float(await(before, f_bits, p.err)) : 0.f);
+            const Affine t = join_maps(s.maps + (walk - pos) * s.width + block + ch, s.width, pos, waits);
+            float f = apply(t, group > 0 ? __uint_as_float(await(waits, before, f_bits)) : 0.f);
             const GroupMaps<RG, CL, V> back(sh.B, sh.F, ch);
 #pragma unroll
             for (int q = RG - 1; q >= 0; --q) {

@@ -59,18 +59,45 @@ __device__ __forceinline__ uint32_t peek(const uint32_t *at) {
 __device__ __forceinline__ bool empty(uint64_t v) { return (uint32_t)v == kEmpty; }
 __device__ __forceinline__ bool empty(uint32_t v) { return v == kEmpty; }
 
-// Waits for a published value, at most kWaitPolls loads (some seconds); on expiry reports to
-// the device error word and goes on with what is there.
-constexpr int kWaitPolls = 1 << 22;
-template <typename U>
-__device__ __forceinline__ U await(const U *at, U v, int *err) {
-    for (int polls = 0; empty(v); v = peek(at)) {
-        if (++polls > kWaitPolls) {
-            atomicExch(err, kErrTimeout);
-            break;
-        }
+// What the waits of a CTA report to: the device error word, and a flag in the CTA's shared
+// memory (0 at first) that its first expired wait sets.  After that its waits are short, so
+// that the kernel ends soon however much is missing.  On expiry a wait goes on with what is
+// there.
+struct Waits { int *err; volatile int *late; };
+__device__ __forceinline__ void expire(const Waits &w) {
+    atomicExch(w.err, kErrTimeout);
+    *w.late = 1;
+}
+
+// Waits until `all_there`, which looks again at what is missing, says so; at most kWaitPolls
+// looks (about a second).  One loop for all the values of a batch: one for each of them took
+// 237 us in the backward pass of 8192 x 8192 bf16, so 230.
+constexpr int kWaitPolls = 1 << 22, kLatePolls = 1 << 10;
+template <typename F>
+__device__ __forceinline__ void await(const Waits &w, F &&all_there) {
+    for (int polls = 0; !all_there(); ++polls) {
+        if (polls < kWaitPolls && !(polls > kLatePolls && *w.late)) continue;
+        expire(w);
+        break;
     }
+}
+// One published value, of which v is the first look.
+template <typename U>
+__device__ __forceinline__ U await(const Waits &w, const U *at, U v) {
+    if (empty(v)) await(w, [&] { return !empty(v = peek(at)); });
     return v;
+}
+
+// Waits for a tile's copies.
+constexpr uint64_t kCopyWaitNs = 2000000000ull, kLateCopyNs = 1000000ull;
+__device__ __forceinline__ void wait_copies(uint64_t *arrived, uint32_t parity, const Waits &w) {
+    if (sm103::mbar_try_wait(arrived, parity)) return;
+    const uint64_t end = sm103::globaltimer_ns() + (*w.late ? kLateCopyNs : kCopyWaitNs);
+    while (!sm103::mbar_try_wait(arrived, parity)) {
+        if (sm103::globaltimer_ns() < end) continue;
+        expire(w);
+        break;
+    }
 }
 
 // How a CTA covers a tile: THREADS threads as CL channel lanes of V channels each by RG row
@@ -303,16 +330,29 @@ __device__ __forceinline__ bool mark_tile(const P &p, int64_t row_tile, int n, T
 
 // The maps of `count` row tiles of a channel, one after the other, as one map.  `at` is the
 // first one's, the next `stride` further on.
-__device__ __forceinline__ Affine join_maps(const uint64_t *at, int64_t stride, int count, int *err) {
+__device__ __forceinline__ Affine join_maps(const uint64_t *at, int64_t stride, int count, const Waits &waits) {
     Affine t{1.f, 0.f};
     constexpr int kBatch = 8;   // in flight together
     for (int j0 = 0; j0 < count; j0 += kBatch, at += kBatch * stride) {
         uint64_t w[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) w[j] = j0 + j < count ? peek(at + j * stride) : 0x3f800000ull;   // (1, 0)
+        bool there = true;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) there &= !empty(w[j]);
+        if (!there) {
+            await(waits, [&] {
+                bool all = true;
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    if (empty(w[j])) w[j] = peek(at + j * stride);
+                    all &= !empty(w[j]);
+                }
+                return all;
+            });
+        }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            w[j] = await(at + j * stride, w[j], err);
             t = then(t, Affine{__uint_as_float((uint32_t)w[j]), __uint_as_float((uint32_t)(w[j] >> 32))});
         }
     }

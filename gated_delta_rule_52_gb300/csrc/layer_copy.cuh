@@ -110,7 +110,6 @@ __device__ __forceinline__ void tma_box(void *dst, const CUtensorMap &map, uint6
         "l"(reinterpret_cast<uint64_t>(&map)), "r"(sm103::smem_u32(bar)), "r"(c), "r"(row)
         : "memory");
 }
-constexpr uint64_t kCopyWaitNs = 2000000000ull;
 
 // A tensor map's demands: 16-byte aligned rows, no row over another.
 inline bool tma_rows(const void *ptr, int64_t stride, int64_t D, size_t elem) {
