@@ -12,6 +12,7 @@ from a prefill to single tokens.  The task is to give back the input of three to
 from __future__ import annotations
 
 import argparse
+import functools
 import os
 import sys
 
@@ -27,6 +28,31 @@ EPS = 1e-5
 LOWER_BOUND = -5.0
 
 
+class _FirstOrder(torch.autograd.Function):
+    """The first ``n`` tensors as they are, tied to the others; has no derivative."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the operators have first derivatives only")
+
+
+def first_order(backward):
+    """For a backward pass in kernels, which autograd cannot see into: under create_graph the
+    gradients depend on what they were formed from, so that differentiating them again is an
+    error and not a sum without their terms.  (autograd's once_differentiable does so only
+    where ``dout`` has a graph of its own.)"""
+    @functools.wraps(backward)
+    def run(ctx, dout):
+        with torch.no_grad():
+            grads = backward(ctx, dout)
+        return _FirstOrder.apply(len(grads), *grads, dout, *ctx.saved_tensors) if torch.is_grad_enabled() else grads
+    return run
+
+
 class Norm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias):
@@ -36,6 +62,7 @@ class Norm(torch.autograd.Function):
         return out
 
     @staticmethod
+    @first_order
     def backward(ctx, dout):
         x, weight, mean, rstd = ctx.saved_tensors
         r = layer_norm.layer_norm_bwd(dout.contiguous(), x, weight, mean, rstd)
@@ -51,6 +78,7 @@ class Conv(torch.autograd.Function):
         return out
 
     @staticmethod
+    @first_order
     def backward(ctx, dout):
         x, weight, bias = ctx.saved_tensors
         r = short_conv.short_conv_bwd(x, weight, bias, dout.contiguous(), want_dinit=False)
@@ -67,6 +95,7 @@ class Recurrence(torch.autograd.Function):
         return out
 
     @staticmethod
+    @first_order
     def backward(ctx, dout):
         *inputs, ck = ctx.saved_tensors
         r = glr.glr_bwd(*inputs, LOWER_BOUND, dout.contiguous(), checkpoints=ck, want_dinit=False)
@@ -83,6 +112,7 @@ class DeltaRule(torch.autograd.Function):
         return out
 
     @staticmethod
+    @first_order
     def backward(ctx, dout):
         q, k, v, g, beta, A_log, dt_bias = ctx.saved_tensors
         r = kda.kda_bwd(q, k, v, g, beta, 128 ** -0.5, A_log, dt_bias, LOWER_BOUND, dout.contiguous(), want_dinit=False)
