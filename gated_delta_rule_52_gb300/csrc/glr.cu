@@ -61,9 +61,9 @@ __global__ void __launch_bounds__(128) glr_fwd_step_kernel(GlrParams p) {
 // (4 CTAs: 107; 3 CTAs of 256 threads with 4 rows: 131; before the tensor maps, at then 118 us,
 // tiles of 32 rows on 7 CTAs 131, and two tiles in flight per CTA, the next one's map handed
 // on before the current one's state is taken, on 3 CTAs 163).  What bounds it: the barriers
-// between a tile's phases, issue at 57% of the slots.  In 32 bits shared memory holds 4 CTAs,
-// 3 of unaligned rows, and the threads have that many more registers: 8192 x 3937 106 us, 114
-// with the registers of 5.  Unaligned 16-bit rows: 8192 x 3937 94 us (aligned 3968: 59 us;
+// between a tile's phases, issue at 58% of the slots.  In 32 bits shared memory holds 4 CTAs,
+// 3 of unaligned rows, and the threads have that many more registers: 8192 x 3937 105 us, 114
+// with the registers of 5.  Unaligned 16-bit rows: 8192 x 3937 94 us (aligned 3968: 58 us;
 // element-wise copies 165 us).
 using FwdShape = TileShape<kGlrCheckpointRows, 128, 16, 4>;
 template <typename E, bool TMA>
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas<E, TMA>)
             // the previous group and the maps of the group's earlier tiles
             const uint32_t *before = s.states + (group - 1) * s.width + block + ch;
             const uint32_t h_bits = group > 0 ? peek(before) : 0;
-            const Affine t = join_maps(s.maps + (rt - pos) * s.width + block + ch, s.width, pos, waits);
+            const Affine t = join_maps<4>(s.maps + (rt - pos) * s.width + block + ch, s.width, pos, waits);
             float h = apply(t, group > 0 ? __uint_as_float(await(waits, before, h_bits)) : 0.f);
             const GroupMaps<RG, CL, V> maps(sh.A, sh.H, ch);
 #pragma unroll
@@ -263,7 +263,10 @@ __global__ void __launch_bounds__(FwdShape::THREADS, kFwdCtas<E, TMA>)
     }
 }
 
-// Rows of a fixed-length call up to which the step kernel runs.
+// Rows of a fixed-length call up to which the step kernel runs.  In a CUDA graph, step and scan:
+// 8 x 4 x 128 channels bf16, 16 rows 7.1 and 7.7 us, 24 rows 9.8 and 7.9; 64 sequences of 64 x
+// 128, 16 rows 13.3 and 22.6 us.  (With many sequences the step kernel stays ahead for longer,
+// 33.9 and 44.7 us at 32 rows; with few, where the call is short, it does not.)
 constexpr int64_t kStepMaxT = 16;
 
 bool step_takes(const GlrParams &p) { return !p.cu_seqlens && p.T <= kStepMaxT; }

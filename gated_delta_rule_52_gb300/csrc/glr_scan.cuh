@@ -329,10 +329,13 @@ __device__ __forceinline__ bool mark_tile(const P &p, int64_t row_tile, int n, T
 }
 
 // The maps of `count` row tiles of a channel, one after the other, as one map.  `at` is the
-// first one's, the next `stride` further on.
+// first one's, the next `stride` further on; kBatch are in flight together.  Forward 4: 8
+// spill there (8192 x 8192 bf16 101.5 and 103.6 us, without a lower bound 111.8 and 114.7),
+// though they help where channels are few (65536 x 256: 48.5 and 45.3 us).  Backward 8: 230
+// and 243 us, 65536 x 1024 270 and 293.
+template <int kBatch = 8>
 __device__ __forceinline__ Affine join_maps(const uint64_t *at, int64_t stride, int count, const Waits &waits) {
     Affine t{1.f, 0.f};
-    constexpr int kBatch = 8;   // in flight together
     for (int j0 = 0; j0 < count; j0 += kBatch, at += kBatch * stride) {
         uint64_t w[kBatch];
 #pragma unroll
