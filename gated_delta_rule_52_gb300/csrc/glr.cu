@@ -57,11 +57,11 @@ __global__ void __launch_bounds__(128) glr_fwd_step_kernel(GlrParams p) {
     }
 }
 
-// 8 rows by 4 channels per thread.  16 bits: 5 CTAs per SM, 8192 x 8192 bf16 103 us, 5.2 TB/s
+// 8 rows by 4 channels per thread.  16 bits: 5 CTAs per SM, 8192 x 8192 bf16 101 us, 5.3 TB/s
 // (4 CTAs: 107; 3 CTAs of 256 threads with 4 rows: 131; before the tensor maps, at then 118 us,
 // tiles of 32 rows on 7 CTAs 131, and two tiles in flight per CTA, the next one's map handed
 // on before the current one's state is taken, on 3 CTAs 163).  What bounds it: the barriers
-// between a tile's phases, issue at 58% of the slots.  In 32 bits shared memory holds 4 CTAs,
+// between a tile's phases, issue at 57% of the slots.  In 32 bits shared memory holds 4 CTAs,
 // 3 of unaligned rows, and the threads have that many more registers: 8192 x 3937 105 us, 114
 // with the registers of 5.  Unaligned 16-bit rows: 8192 x 3937 94 us (aligned 3968: 58 us;
 // element-wise copies 165 us).

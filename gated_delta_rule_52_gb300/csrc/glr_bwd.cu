@@ -23,14 +23,13 @@ namespace {
 using namespace layer;
 
 // 16 bits: 4 rows by 4 channels per thread, 2 CTAs per SM (the raw inputs of two tiles each
-// in shared memory).  32 bits: 8 rows by 2 channels and 3 CTAs of 128 threads (20011 x 836:
-// 146 us; 2 CTAs of 256: 149; 8192 x 8192: 323 and 340).  There the granules of unaligned
-// rows leave room for 2 CTAs only, so they have 256 threads of 4 rows: 20011 x 847 172 us,
-// with 128 threads 201.
-// 8192 x 8192 bf16: 230 us, 4.1 TB/s; what bounds it is issue, 70 instructions per element
-// between barriers, at 55% of the slots.  Unaligned: 8192 x 3937 bf16 253 us (aligned 3936:
-// 126 us); element-wise copies took 475 us, and 214 us
-// on 20011 x 847 fp32.
+// in shared memory).  32 bits: 8 rows by 2 channels and 3 CTAs of 128 threads (65536 x 1024:
+// 326 us, 2 CTAs of 256 363; 8192 x 8192: 315 and 309, without a lower bound 318 and 340).
+// There the granules of unaligned rows leave room for 2 CTAs only, so they have 256 threads of
+// 4 rows: 20011 x 847 171 us, with 128 threads 190.
+// 8192 x 8192 bf16: 228 us, 4.1 TB/s; what bounds it is issue, 75 instructions per element
+// between barriers, at 59% of the slots.  Unaligned: 8192 x 3937 bf16 250 us (aligned 3968:
+// 125 us); element-wise copies took 475 us, and 214 us on 20011 x 847 fp32.
 template <typename E, bool TMA>
 using BwdShape = TileShape<kGlrCheckpointRows, sizeof(E) == 2 || !TMA ? 256 : 128, 16, sizeof(E) == 2 ? 4 : 2>;
 
