@@ -299,6 +299,41 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
         : "memory");
 }
 
+// Instruction descriptor of the block-scaled tcgen05.mma kind::mxf8f6f4 (fp32 D, K = 32 8-bit
+// elements, both operands K-major, scales are powers of two).  Types: 0 = e4m3, 1 = e5m2.
+// `sf` (0 to 3) is the byte of the scale words that this MMA takes, of both operands.
+__host__ __device__ constexpr uint32_t idesc_mx8(int M, int N, int a_type, int b_type, int sf) {
+    return ((uint32_t)sf << 4)               // byte of B's scale words
+           | ((uint32_t)a_type << 7)         // A format
+           | ((uint32_t)b_type << 10)        // B format
+           | ((uint32_t)(N >> 3) << 17)      // N / 8
+           | (1u << 23)                      // scales: 8 bits of exponent
+           | ((uint32_t)(M >> 4) << 24)      // M / 16
+           | ((uint32_t)sf << 29);           // byte of A's scale words
+}
+
+// Shared-memory descriptor without swizzle of 8-row by 16-byte core matrices `sbo` bytes apart.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t sbo) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1u << 46;
+}
+
+// Copies 32 rows of 16 bytes from shared memory into 4 TMEM columns, the same for each of the
+// 4 groups of 32 lanes.  Scales of 128 rows: row r is word r / 32 of row r % 32, one byte per
+// 32-element (here: 128-element) block of K.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// D[tmem] (+)= (A scaled)[smem] * (B scaled)[smem]^T, 8-bit elements; issued by one thread.
+__device__ __forceinline__ void mma_mx8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t a_scales, uint32_t b_scales, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
 // Arrives once on `bar` when all previously issued MMAs of this thread finish.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile(

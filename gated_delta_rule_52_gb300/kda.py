@@ -42,7 +42,8 @@ KDA_STATE_FP32 = 2
 EXPORTED = ("kda_fwd", "kda_fwd_ws", "kda_fwd_unbounded", "kda_workspace_size", "kda_workspace_size_pool",
             "kda_status_string", "kda_get_device_status", "kda_version", "kda_fwd_static",
             "kda_bwd", "kda_glr_fwd", "kda_glr_bwd", "kda_layer_norm_fwd", "kda_layer_norm_bwd",
-            "kda_short_conv_fwd", "kda_short_conv_bwd")
+            "kda_short_conv_fwd", "kda_short_conv_bwd", "kda_rms_norm_fwd", "kda_rms_norm_bwd",
+            "kda_fp8_quantize", "kda_fp8_dequantize", "kda_fp8_matmul")
 
 # Workspace bytes per (sequence, head) of kda_fwd_ws (KDA_WORKSPACE_BYTES_PER_UNIT).
 WORKSPACE_BYTES_PER_UNIT = 99328
@@ -94,7 +95,12 @@ def lib() -> ctypes.CDLL:
                                              i64, i64, vp]
             L.kda_short_conv_bwd.argtypes = [vp, i64, vp, vp, ci, ci, vp, vp, i64, vp, vp, i64, i64, i64,
                                              i64, i64, vp, vp, vp, vp, vp]
-            for name in EXPORTED[-6:]:   # the operators around the delta rule
+            L.kda_rms_norm_fwd.argtypes = [vp, i64, vp, i64, vp, f, vp, i64, ci, vp, i64, vp, i64, vp, ci, i64, i64, vp]
+            L.kda_rms_norm_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, vp, vp, ci, i64, i64, vp]
+            L.kda_fp8_quantize.argtypes = [vp, i64, ci, vp, i64, vp, i64, vp, i64, vp, i64, ci, ci, i64, i64, vp]
+            L.kda_fp8_dequantize.argtypes = [vp, i64, ci, vp, i64, ci, vp, i64, ci, i64, i64, vp]
+            L.kda_fp8_matmul.argtypes = [vp, i64, ci, vp, i64, ci, vp, i64, ci, vp, i64, ci, vp, i64, vp, i64, ci, i64, i64, i64, vp]
+            for name in EXPORTED[EXPORTED.index("kda_glr_fwd"):]:   # the operators around the delta rule
                 getattr(L, name).restype = ci
             L.kda_workspace_size.argtypes = [i64, i64]
             L.kda_workspace_size.restype = ctypes.c_size_t

@@ -1,0 +1,79 @@
+"""RMS norm over the last axis with the residual's addition, forward and backward (C entry
+points kda_rms_norm_fwd and kda_rms_norm_bwd of include/kda.h):
+
+    h = x + residual (rounded to x's type),   out = h * rstd * weight,
+    rstd = 1 / sqrt(mean(h^2) + eps)
+
+``x`` and ``residual`` are [..., D] in bf16, fp16 or fp32, rows evenly spaced (a slice of a
+wider tensor qualifies); ``weight`` is fp32 [D] or None; ``rstd`` is fp32.  The output is of
+x's type, or in 8 bits with a scale for each block of 128 columns, as ``fp8.matmul`` reads it
+(``fp8.empty`` makes such a pair).
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import _args, fp8
+
+
+def _shape(x):
+    dt, shape = _args.dtype_code("x", x), x.shape
+    if not shape:
+        raise ValueError("x must have at least one dimension")
+    D, lead, dev = shape[-1], len(shape) - 1, _args.device("x", x)
+    return dev, dt, shape, lead, D, _args.rows("x", x, x.dtype, shape, lead, D, dev)
+
+
+def _maybe_rows(name, t, x, shape, lead, D, dev):
+    """Data pointer and row stride of an optional tensor like ``x``."""
+    return (None, 0) if t is None else (t.data_ptr(), _args.rows(name, t, x.dtype, shape, lead, D, dev))
+
+
+def rms_norm_fwd(x, weight, eps, out, residual=None, residual_out=None, rstd=None, scales=None, stream=None) -> None:
+    """Writes ``out`` [..., D] and, where given, ``residual_out`` (the sum h, like ``x``) and
+    ``rstd`` (fp32, one value per row), asynchronously on ``stream`` (default: the current torch
+    stream).  ``out`` is of x's type (it may be ``x`` or ``residual``), or torch.float8_e4m3fn
+    or torch.float8_e5m2 with ``scales`` [..., ceil(D/128)] of torch.float8_e8m0fnu;
+    ``residual_out`` may be ``x`` or ``residual``."""
+    dev, dt, shape, lead, D, stride = _shape(x)
+    code, f32 = fp8.DTYPES.get(out.dtype) if isinstance(out, torch.Tensor) else None, torch.float32
+    if code is None:
+        if scales is not None:
+            raise ValueError("scales belong to an 8-bit out")
+        code, out_stride, ps, ss = dt, _args.rows("out", out, x.dtype, shape, lead, D, dev), None, 0
+    else:
+        if scales is None:
+            raise ValueError("an 8-bit out needs scales")
+        out_stride = _args.rows("out", out, out.dtype, shape, lead, D, dev)
+        ss = _args.rows("scales", scales, fp8.SCALE, (*shape[:-1], fp8.blocks(D)), lead, fp8.blocks(D), dev)
+        ps = scales.data_ptr()
+    if residual_out is not None and residual is None:
+        raise ValueError("residual_out needs a residual")
+    pr, rs = _maybe_rows("residual", residual, x, shape, lead, D, dev)
+    po, ros = _maybe_rows("residual_out", residual_out, x, shape, lead, D, dev)
+    _args.done(_args.entry("kda_rms_norm_fwd")(
+        x.data_ptr(), stride, pr, rs, _args.optional("weight", weight, f32, (D,), dev), eps, out.data_ptr(), out_stride, code,
+        ps, ss, po, ros, _args.optional("rstd", rstd, f32, shape[:-1], dev), dt, math.prod(shape[:-1]), D,
+        _args.stream_handle(stream, dev)))
+
+
+def rms_norm_bwd(dout, x, weight, rstd, dresidual=None, want_dweight=None, stream=None) -> dict:
+    """Gradients of sum(dout * out) + sum(dresidual * residual_out); ``x`` is the sum h that was
+    normed and ``rstd`` what the forward wrote.  Returns a dict of new tensors: dx (like x,
+    contiguous: the gradient of the forward's x and of its residual) and fp32 dweight (None
+    unless ``want_dweight``, by default where there is a weight)."""
+    dev, dt, shape, lead, D, stride = _shape(x)
+    dout_stride = _args.rows("dout", dout, x.dtype, shape, lead, D, dev)
+    pd, ds = _maybe_rows("dresidual", dresidual, x, shape, lead, D, dev)
+    f32 = torch.float32
+    pw, pr = _args.optional("weight", weight, f32, (D,), dev), _args.tensor("rstd", rstd, f32, shape[:-1], dev)
+    if want_dweight is None:
+        want_dweight = weight is not None
+    dx, = _args.new(stream, x, shape)
+    dw, = _args.new(stream, rstd, (D,) if want_dweight else None)
+    _args.done(_args.entry("kda_rms_norm_bwd")(
+        dout.data_ptr(), dout_stride, x.data_ptr(), stride, pw, pr, pd, ds, dx.data_ptr(), None if dw is None else dw.data_ptr(),
+        dt, math.prod(shape[:-1]), D, _args.stream_handle(stream, dev)))
+    return {"dx": dx, "dweight": dw}

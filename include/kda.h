@@ -300,7 +300,9 @@ kda_status kda_fwd_static(const void *q, const void *k, const void *v, const voi
 typedef enum {
     KDA_DTYPE_BF16 = 1,
     KDA_DTYPE_FP32 = 2,
-    KDA_DTYPE_FP16 = 3
+    KDA_DTYPE_FP16 = 3,
+    KDA_DTYPE_E4M3 = 4,      /* 8 bits, only where an argument below says so */
+    KDA_DTYPE_E5M2 = 5
 } kda_dtype;
 
 /* Packed rows from one checkpoint of the gated linear recurrence to the next. */
@@ -404,6 +406,93 @@ kda_status kda_short_conv_bwd(const void *x, int64_t x_stride, const float *weig
                               const float *dfinal, const int64_t *cu_seqlens, int64_t num_seqs, int64_t B, int64_t T,
                               int64_t D, int64_t W, void *dx, float *dweight, float *dbias, float *dinitial_state,
                               void *stream);
+
+/* Elements of a row (and of a tile's columns) that share a scale in an 8-bit tensor. */
+#define KDA_FP8_BLOCK 128
+
+/*
+ * 8-bit tensors.  A tensor [rows, cols] in e4m3 (magnitudes up to 448) or e5m2 (57344) has a
+ * scale for each block of 128 neighbours along a row (the last one may be shorter): bytes
+ * [rows, ceil(cols/128)], or where a call's `tile` argument is not 0 one for each tile of 128
+ * rows by 128 columns, [ceil(rows/128), ceil(cols/128)].  A byte b stands for the scale
+ * 2^(b - 127), 255 for NaN; the element q stands for q times its scale.  Row strides of the
+ * scales are in bytes, like those of the 8-bit elements.
+ *
+ * What the library writes has the smallest power of two with which the block's largest
+ * finite magnitude stays in range (at least 2^-126; 2^0 for a block whose magnitudes are all
+ * below 2^-126), and elements rounded to the nearest value, halves to even.  NaN stays NaN;
+ * infinities become NaN in e4m3 and stay infinities in e5m2.
+ */
+
+/*
+ * kda_rms_norm_fwd — RMS norm over rows of D elements, with the residual's addition:
+ *
+ *   h = x + residual, rounded to dtype;  out = h * rstd * weight,
+ *   rstd = 1 / sqrt(mean(h^2) + eps)
+ *
+ *   x, residual    [rows, D] of dtype, rows x_stride, residual_stride elements apart;
+ *                  residual may be NULL (h = x)
+ *   weight         fp32 [D] or NULL (1)
+ *   out            [rows, D] of out_dtype: dtype (then it may be x or residual), or
+ *                  KDA_DTYPE_E4M3 or KDA_DTYPE_E5M2 with `scales` [rows, ceil(D/128)]
+ *   residual_out   [rows, D] of dtype: takes h (it may be x or residual), or NULL
+ *   rstd           fp32 [rows] or NULL (not written), for kda_rms_norm_bwd
+ * KDA_ERR_VALUE for eps negative or not finite; KDA_ERR_NULL for residual_out without a
+ * residual, or 8-bit outputs without scales.
+ */
+kda_status kda_rms_norm_fwd(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, const float *weight,
+                            float eps, void *out, int64_t out_stride, int out_dtype, void *scales, int64_t scales_stride,
+                            void *residual_out, int64_t residual_out_stride, float *rstd, int dtype, int64_t rows, int64_t D,
+                            void *stream);
+
+/*
+ * kda_rms_norm_bwd — gradients of sum(dout * out) + sum(dresidual * residual_out).
+ *   dout, x        [rows, D] with their row strides; x is the normed sum h (residual_out)
+ *   rstd           as the forward wrote it
+ *   dresidual      [rows, D] of dtype, or NULL (zero)
+ *   dx             [rows, D] of dtype, contiguous: the gradient of x and of the residual
+ *   dweight        fp32 [D] or NULL (not wanted)
+ */
+kda_status kda_rms_norm_bwd(const void *dout, int64_t dout_stride, const void *x, int64_t x_stride, const float *weight,
+                            const float *rstd, const void *dresidual, int64_t dresidual_stride, void *dx, float *dweight,
+                            int dtype, int64_t rows, int64_t D, void *stream);
+
+/*
+ * kda_fp8_quantize — x in 8 bits, its transpose, or both from one pass over x.
+ *   x              [rows, cols] of dtype, rows x_stride elements apart
+ *   q, scales      [rows, cols] of q_dtype with its scales, or both NULL
+ *   qt, scales_t   [cols, rows] of q_dtype with its scales, whose blocks lie along the columns
+ *                  of x (with `tile` its tiles are those of q, transposed), or both NULL
+ *   q_dtype        KDA_DTYPE_E4M3 or KDA_DTYPE_E5M2
+ * For kda_fp8_matmul, rows of q and qt start at multiples of 16 bytes and rows of scales at
+ * multiples of 4; this call takes any.
+ */
+kda_status kda_fp8_quantize(const void *x, int64_t x_stride, int dtype, void *q, int64_t q_stride, void *scales,
+                            int64_t scales_stride, void *qt, int64_t qt_stride, void *scales_t, int64_t scales_t_stride,
+                            int q_dtype, int tile, int64_t rows, int64_t cols, void *stream);
+
+/* kda_fp8_dequantize — the values that an 8-bit tensor stands for, [rows, cols] of dtype. */
+kda_status kda_fp8_dequantize(const void *q, int64_t q_stride, int q_dtype, const void *scales, int64_t scales_stride, int tile,
+                              void *out, int64_t out_stride, int dtype, int64_t rows, int64_t cols, void *stream);
+
+/*
+ * kda_fp8_matmul — product of two 8-bit tensors whose rows hold what is summed over:
+ *
+ *   out[m, n] = add[m, n] + sum_k a[m, k] b[n, k]
+ *
+ * of the values that they stand for, summed in fp32 and rounded to dtype once.
+ *   a, a_scales    [M, K] of a_dtype (e4m3 or e5m2) with its scales; b, b_scales [N, K]
+ *                  likewise.  Rows start at multiples of 16 bytes, rows of scales at multiples
+ *                  of 4 (else KDA_ERR_ALIGN); what lies between two rows is not read
+ *   out            [M, N] of dtype, rows out_stride elements apart
+ *   add            [M, N] of dtype, rows add_stride apart (it may be out), or NULL (zero)
+ * A projection y = x W^T takes a = x, b = W; its gradients dx = dy W and dW = dy^T x take the
+ * transposed tensors of kda_fp8_quantize: a = dy, b = W^T, and a = dy^T, b = x^T.
+ */
+kda_status kda_fp8_matmul(const void *a, int64_t a_stride, int a_dtype, const void *a_scales, int64_t a_scales_stride, int a_tile,
+                          const void *b, int64_t b_stride, int b_dtype, const void *b_scales, int64_t b_scales_stride, int b_tile,
+                          void *out, int64_t out_stride, const void *add, int64_t add_stride, int dtype, int64_t M, int64_t N,
+                          int64_t K, void *stream);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *kda_status_string(int status);
