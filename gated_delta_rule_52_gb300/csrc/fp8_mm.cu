@@ -5,6 +5,7 @@
 // block take the same byte.  4 blocks' bytes of a row are one 4-byte word, the unit in which
 // scales are loaded and put into TMEM.
 #include <algorithm>
+#include <cstdlib>
 #include <cuda.h>
 
 #include "kda_chunk.cuh"
@@ -20,7 +21,38 @@ using namespace sm103;
 
 constexpr uint64_t kWait = 2000000000ull;   // 2 s per wait
 constexpr int kRows = 128;                  // rows of b per tile: the MMA's M, TMEM's lanes
-constexpr int kScaleStages = 4;
+constexpr int kScaleStages = 8, kAhead = 4;   // groups of 4 blocks' scales: places, and on their way
+
+// Waits of the pipelines.  Reading the GPU's timer takes longer than a stage does, so it is read
+// once in many tries only.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint64_t limit = kWait) {
+    uint64_t t0 = 0;
+    for (uint32_t tries = 0;; ++tries) {
+        if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+        if (tries % 1024 == 1023) {
+            const uint64_t now = globaltimer_ns();
+            if (!t0) t0 = now;
+            else if (now - t0 > limit) return false;
+        }
+    }
+}
+
+// wait_for by a whole warp.
+template <bool CLUSTER>
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64_t limit = kWait) {
+    return __all_sync(0xffffffffu, wait_for<CLUSTER>(bar, parity, limit));
+}
+
+// A place in a ring of N slots and the parity of its turn.
+template <int N>
+struct Slot {
+    int at = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) at = 0, turn ^= 1;
+    }
+};
 
 struct MatmulArgs {
     CUtensorMap a, b;
@@ -36,17 +68,33 @@ __device__ __forceinline__ void copy_word(uint32_t dst, const uint8_t *src, int 
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// The scale words of rows row0 .. row0 + n (of blocks 4 group .. 4 group + 3) to `dst`, as the
-// tensor cores want them: rows 128 c + 32 w + i at byte 512 c + 16 i + 4 w.
-__device__ __forceinline__ void copy_scales(uint32_t dst, const Fp8Operand &o, int64_t row0, int n, int group, int blocks, int lane) {
-    const int bytes = min(4, blocks - 4 * group);
-    for (int r = lane; r < n; r += 32) {
-        const int64_t row = row0 + r;
-        const bool in = row < o.rows;
-        const uint8_t *src = o.s + (in ? (o.tile ? row / kFp8Block : row) * o.s_stride + 4 * group : 0);
-        copy_word(dst + (r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4, src, in ? bytes : 0);
+// Scale words of N rows from row0 on, 4 blocks of K at a time, on their way to shared memory as the
+// tensor cores want them: rows 128 c + 32 w + i at byte 512 c + 16 i + 4 w.  A lane has rows i =
+// lane of every c and w; where they are is worked out once for a tile.
+template <int N>
+struct ScaleRows {
+    static constexpr int kWords = (N + 31) / 32;
+    const uint8_t *row[kWords];
+    uint32_t in;   // which of them exist
+    __device__ __forceinline__ void set(const Fp8Operand &o, int64_t row0, int lane) {
+        in = 0;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            const int64_t r = row0 + 32 * w + lane;
+            const bool some = 32 * w + lane < N && r < o.rows;
+            row[w] = o.s + (some ? (o.tile ? r / kFp8Block : r) * o.s_stride : 0);
+            in |= (uint32_t)some << w;
+        }
     }
-}
+    // The next 4 blocks, `bytes` (1 to 4) of which there are.
+    __device__ __forceinline__ void copy(uint32_t dst, int bytes, int lane) {
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            copy_word(dst + (w >> 2) * 512 + lane * 16 + (w & 3) * 4, row[w], in >> w & 1 ? bytes : 0);
+            if (in >> w & 1) row[w] += 4;
+        }
+    }
+};
 
 // ---- one tile of 128 rows of b by BT rows of a per cluster of `split` CTAs, which share K and
 // join their sums through distributed shared memory.
@@ -96,7 +144,7 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
         int i = 0;
         for (int k = k0; k < k1; ++k, ++i) {
             const int st = i % S::kStages, turn = i / S::kStages;
-            if (turn > 0 && !mbar_wait(&empty[st], (turn - 1) & 1, kWait)) {
+            if (turn > 0 && !wait_for<false>(&empty[st], (turn - 1) & 1)) {
                 ok = false;
                 break;
             }
@@ -107,7 +155,7 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
         }
         // the copies end before the CTA does
         for (int j = max(0, i - S::kStages); j < i; ++j)
-            if (!mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1, kWait)) ok = false;
+            if (!wait_for<false>(&full[j % S::kStages], (j / S::kStages) & 1)) ok = false;
     } else if (warp == 1 && lane == 0) {
         int i = 0, g = -1, sets = 0;
         for (int k = k0; ok && k < k1; ++k, ++i) {
@@ -115,7 +163,7 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
             if (k / 4 != g) {
                 g = k / 4;
                 const int ss = sets % kScaleStages;
-                if (!mbar_wait(&sfull[ss], (sets / kScaleStages) & 1, kWait)) {
+                if (!wait_for<false>(&sfull[ss], (sets / kScaleStages) & 1)) {
                     ok = false;
                     break;
                 }
@@ -126,7 +174,7 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
                 mma_commit(&sempty[ss]);
                 ++sets;
             }
-            if (!mbar_wait(&full[st], (i / S::kStages) & 1, kWait)) {
+            if (!wait_for<false>(&full[st], (i / S::kStages) & 1)) {
                 ok = false;
                 break;
             }
@@ -141,19 +189,26 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
         }
         mma_commit(&done);
     } else if (warp == 2) {
-        // kScaleStages - 1 groups on their way; a group is handed over when the copies before
-        // the last kScaleStages - 2 have arrived
+        // kAhead groups on their way while the ones before are handed over
         const int g0 = k0 / 4, groups = k1 > k0 ? (k1 - 1) / 4 - g0 + 1 : 0;
-        constexpr int kAhead = kScaleStages - 2;
+        ScaleRows<kRows> rows_b;
+        ScaleRows<BT> rows_a;
+        rows_b.set(p.b, n0, lane);
+        rows_a.set(p.a, m0, lane);
+#pragma unroll
+        for (int w = 0; w < rows_b.kWords; ++w) rows_b.row[w] += rows_b.in >> w & 1 ? 4 * g0 : 0;
+#pragma unroll
+        for (int w = 0; w < rows_a.kWords; ++w) rows_a.row[w] += rows_a.in >> w & 1 ? 4 * g0 : 0;
         for (int i = 0; i < groups + kAhead; ++i) {
             if (i < groups) {
                 const int ss = i % kScaleStages, turn = i / kScaleStages;
-                if (turn > 0 && !mbar_wait(&sempty[ss], (turn - 1) & 1, kWait)) ok = false;
+                if (turn > 0 && !wait_for<false>(&sempty[ss], (turn - 1) & 1)) ok = false;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const uint32_t at = smem_u32(scales + ss * S::kScaleStage);
-                copy_scales(at, p.b, n0, kRows, g0 + i, blocks, lane);
-                copy_scales(at + 512, p.a, m0, BT, g0 + i, blocks, lane);
+                const int bytes = min(4, blocks - 4 * (g0 + i));
+                rows_b.copy(at, bytes, lane);
+                rows_a.copy(at + 512, bytes, lane);
             }
             copies_commit();
             if (i >= kAhead) {
@@ -165,7 +220,7 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
         copies_wait<0>();
     }
     __syncwarp();
-    if (!mbar_wait(&done, 0, 2 * kWait)) ok = false;
+    if (!wait_for<false>(&done, 0, 2 * kWait)) ok = false;
     if (!ok && p.err) atomicExch(p.err, kErrTimeout);
     __syncthreads();   // the ring is free: every copy and MMA has ended
     tc_fence_after();
@@ -209,6 +264,276 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
     if (split > 1) cluster_sync();   // the others have read this CTA's sums
 }
 
+// ---- tiles of 256 rows of a by BN rows of b, persistent pairs of CTAs.
+//
+// A pair shares its tiles: each CTA loads its 128 rows of a and half of the rows of b, one
+// thread of the first CTA issues the MMAs of both (cta_group::2), which halves what shared
+// memory has to deliver for b.  Warp 0 loads tiles, warp 2 scales, warp 1 issues, warps 4 to 11
+// empty the accumulators; two of these in TMEM, so that a tile's MMAs run while the one before
+// is stored.  fp32 outputs take K in segments whose sums are added in registers: the tensor
+// cores cut an accumulator at each step, which over a long K would cost more than fp32's own
+// rounding.
+constexpr int kPairThreads = 384, kStoreWarps = 8;
+constexpr int kSegment = 32;                // blocks of K per segment of an fp32 output
+
+template <int BN>
+struct PairShape {
+    static constexpr int kStage = (kRows + BN / 2) * kFp8Block;
+    static constexpr int kScaleB = BN <= 128 ? 512 : 1024;
+    static constexpr int kScaleStage = 512 + kScaleB;
+    static constexpr int kStaging = kStoreWarps * 32 * 17 * 4;
+    static constexpr int kStages = (227 * 1024 - 2048 - kStaging - kScaleStage * kScaleStages) / kStage;
+    static constexpr int kSmem = 1024 + kStage * kStages + kScaleStage * kScaleStages + kStaging;
+    static constexpr int kSet = 4 + kScaleB / 128;
+    static constexpr int kBuffers = 2 * BN + 2 * kSet <= 512 ? 2 : 1;
+    static constexpr int kCols = kBuffers * BN + 2 * kSet <= 256 ? 256 : 512;
+    static_assert(kSmem <= 227 * 1024 && BN % 32 == 0 && kBuffers * BN + 2 * kSet <= 512, "fits an SM");
+};
+
+// Tile t of a grid of `down` x `across`: 8 tiles down, then across, so that the tiles in flight
+// share rows of both operands in L2.
+__device__ __forceinline__ void tile_at(int64_t t, int64_t down, int64_t across, int64_t &i, int64_t &j) {
+    const int64_t band = t / (8 * across), first = band * 8, high = min(down - first, (int64_t)8), in = t - band * 8 * across;
+    i = first + in % high;
+    j = in / high;
+}
+
+template <typename E, int BN>
+__global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_constant__ MatmulArgs args, int wide) {
+    using S = PairShape<BN>;
+    constexpr bool kSums = sizeof(E) == 4;
+    extern __shared__ unsigned char raw[];
+    unsigned char *ring = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    unsigned char *scales = ring + S::kStage * S::kStages;
+    float *staging = reinterpret_cast<float *>(scales + S::kScaleStage * kScaleStages);
+    __shared__ uint64_t full[S::kStages], empty[S::kStages], sfull[kScaleStages], sempty[kScaleStages], tfull[S::kBuffers], tempty[S::kBuffers];
+    __shared__ uint32_t tmem_base;
+    const MatmulParams &p = args.p;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int64_t down = ceil_div(p.a.rows, 2 * kRows), across = ceil_div(p.b.rows, BN), tiles = down * across;
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int blocks = (int)ceil_div(p.K, kFp8Block);
+    const int segment = kSums ? kSegment : blocks;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+        for (int i = 0; i < kScaleStages; ++i) mbar_init(&sfull[i], 64), mbar_init(&sempty[i], 1);
+        for (int i = 0; i < S::kBuffers; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 2 * kStoreWarps);
+        fence_mbar_init();
+    }
+    if (warp == 3) tmem_alloc_pair(&tmem_base, S::kCols);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t acc = tmem_base, sf = acc + S::kBuffers * BN;
+    bool ok = true;
+    if (warp == 0) {
+        // ---- tiles of both operands; the bytes of both CTAs count on the first one's barrier
+        const bool issuer = elect_one();
+        Slot<S::kStages> slot;
+        int loads = 0;
+        const uint32_t bars = mapa_shared(smem_u32(full), 0);
+        for (int64_t t = pair; ok && t < tiles; t += pairs) {
+            int64_t i, j;
+            tile_at(t, down, across, i, j);
+            const int ra = (int)(i * 2 * kRows + rank * kRows), rb = (int)(j * BN + rank * (BN / 2));
+            for (int k = 0; k < blocks; ++k) {
+                // (a wait for the turn before the first returns at once)
+                if (!warp_wait<false>(&empty[slot.at], slot.turn ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                unsigned char *at = ring + slot.at * S::kStage;
+                if (issuer) {
+                    if (rank == 0) mbar_arrive_expect_tx(&full[slot.at], 2 * S::kStage);
+                    tma_load_2d_pair(at, &args.a, bars + 8 * slot.at, k * kFp8Block, ra);
+                    tma_load_2d_pair(at + kRows * kFp8Block, &args.b, bars + 8 * slot.at, k * kFp8Block, rb);
+                }
+                slot.next();
+                loads = min(loads + 1, S::kStages);
+            }
+        }
+        if (rank == 0)   // the copies end before the CTAs do
+            for (int m = 0; m < loads; ++m) {
+                slot.at = slot.at == 0 ? S::kStages - 1 : slot.at - 1;
+                if (slot.at == S::kStages - 1) slot.turn ^= 1;
+                if (!warp_wait<false>(&full[slot.at], slot.turn)) ok = false;
+            }
+    } else if (warp == 1 && rank == 0) {
+        // ---- MMAs of the pair
+        const bool issuer = elect_one();
+        Slot<S::kStages> slot;
+        Slot<kScaleStages> scale;
+        Slot<S::kBuffers> sum;
+        const uint64_t a0 = sdesc_sw128(smem_u32(ring), 16, 1024), s0 = sdesc_plain(smem_u32(scales), 128);
+        const uint32_t idesc = idesc_mx8(2 * kRows, BN, p.a.dtype == kE5M2, p.b.dtype == kE5M2, 0);
+        for (int64_t t = pair; ok && t < tiles; t += pairs) {
+            for (int k0 = 0; ok && k0 < blocks; k0 += segment) {
+                if (!warp_wait<false>(&tempty[sum.at], sum.turn ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t to = acc + sum.at * BN;
+                const int k1 = min(blocks, k0 + segment);
+                for (int k = k0; k < k1; ++k) {
+                    const uint32_t set = sf + (scale.at & 1) * S::kSet;
+                    if (k % 4 == 0) {
+                        if (!warp_wait<true>(&sfull[scale.at], scale.turn)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t from = s0 + scale.at * (S::kScaleStage >> 4);
+                        if (issuer) {
+#pragma unroll
+                            for (int c = 0; c < S::kScaleStage / 512; ++c) tmem_copy_scales_pair(set + 4 * c, from + 32 * c);
+                            mma_commit_pair(&sempty[scale.at]);
+                        }
+                    }
+                    if (!warp_wait<false>(&full[slot.at], slot.turn)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = a0 + slot.at * (S::kStage >> 4), bd = ad + (kRows * kFp8Block >> 4);
+                    const uint32_t id = idesc | (k & 3) << 4 | (uint32_t)(k & 3) << 29;
+                    if (issuer) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) mma_mx8_pair(to, ad + 2 * q, bd + 2 * q, id, set, set + 4, k != k0 || q > 0);
+                        mma_commit_pair(&empty[slot.at]);
+                    }
+                    slot.next();
+                    if (k % 4 == 3 || k == blocks - 1) scale.next();
+                }
+                if (issuer) mma_commit_pair(&tfull[sum.at]);
+                sum.next();
+            }
+        }
+    } else if (warp == 2) {
+        // ---- scales: of this CTA's rows of a, and of all rows of b
+        const int groups = (int)ceil_div(blocks, 4);
+        const int64_t mine = pair < tiles ? (tiles - pair - 1) / pairs + 1 : 0;
+        ScaleRows<kRows> rows_a;
+        ScaleRows<BN> rows_b;
+        int64_t t = pair;
+        int g = 0;
+        Slot<kScaleStages> in, out;
+        const uint32_t bars = mapa_shared(smem_u32(sfull), 0);
+        const int64_t all = mine * groups;
+        for (int64_t n = 0; n < all + kAhead; ++n) {
+            if (n < all) {
+                if (g == 0) {
+                    int64_t i, j;
+                    tile_at(t, down, across, i, j);
+                    rows_a.set(p.a, i * 2 * kRows + rank * kRows, lane);
+                    rows_b.set(p.b, j * BN, lane);
+                }
+                ok = wait_for<false>(&sempty[in.at], in.turn ^ 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint32_t at = smem_u32(scales + in.at * S::kScaleStage);
+                const int bytes = min(4, blocks - 4 * g);
+                rows_a.copy(at, bytes, lane);
+                rows_b.copy(at + 512, bytes, lane);
+                in.next();
+                if (++g == groups) g = 0, t += pairs;
+            }
+            copies_commit();
+            if (n >= kAhead) {
+                copies_wait<kAhead>();
+                fence_proxy_async_smem();
+                mbar_arrive_remote(bars + 8 * out.at);
+                out.next();
+            }
+        }
+        copies_wait<0>();
+    } else if (warp >= 4) {
+        // ---- accumulators to out: lanes 32 (warp % 4) .. + 31, one half of the columns
+        const int part = warp & 3, half = (warp - 4) >> 2;
+        constexpr int kHalf = BN / 2;
+        float *own = staging + (warp - 4) * 32 * 17;
+        Slot<S::kBuffers> sum;
+        const uint32_t bars = mapa_shared(smem_u32(tempty), 0);
+        for (int64_t t = pair; ok && t < tiles; t += pairs) {
+            int64_t ti, tj;
+            tile_at(t, down, across, ti, tj);
+            const int64_t m0 = ti * 2 * kRows + rank * kRows + part * 32, n0 = tj * BN + half * kHalf;
+            float f[kSums ? kHalf : 16];
+            for (int k = 0; k < blocks; k += segment) {
+                const int buf = sum.at;
+                ok = wait_for<false>(&tfull[buf], sum.turn);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                sum.next();
+                tc_fence_after();
+                const bool last = k + segment >= blocks;
+                const uint32_t from = tmem_addr(acc, part * 32, buf * BN + half * kHalf);
+                if constexpr (kSums) {
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += 16) {
+                        float r[16];
+                        tmem_ld16(from + c, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) f[c + e] = k == 0 ? r[e] : f[c + e] + r[e];
+                    }
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive_remote(bars + 8 * buf);
+                    if (!last) continue;
+                }
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 16) {
+                    // 16 columns through shared memory: rows of 16 neighbours to store
+                    if constexpr (!kSums) {
+                        tmem_ld16(from + c, f);
+                        tmem_ld_wait();
+                        if (c + 16 >= kHalf) {
+                            tc_fence_before();
+                            if (lane == 0) mbar_arrive_remote(bars + 8 * buf);
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) own[lane * 17 + e] = f[kSums ? c + e : e];
+                    __syncwarp();
+                    constexpr int V = 16 / sizeof(E), G = 16 / V;   // elements of a store, stores of a row
+#pragma unroll 1
+                    for (int u = 0; u < G; ++u) {
+                        const int row = u * (32 / G) + lane / G, col = lane % G * V;
+                        const int64_t m = m0 + row, nn = n0 + c + col;
+                        if (m >= p.a.rows || nn >= p.b.rows) continue;
+                        float o[V];
+#pragma unroll
+                        for (int e = 0; e < V; ++e) o[e] = own[row * 17 + col + e];
+                        E *to = static_cast<E *>(p.out) + m * p.os + nn;
+                        const E *plus = p.add ? static_cast<const E *>(p.add) + m * p.as + nn : nullptr;
+                        if (wide && nn + V <= p.b.rows) {
+                            if (plus) {
+                                float a[V];
+                                ld_f<E, V>(plus, a);
+                                add_n<V>(o, o, a);
+                            }
+                            st_f<E, V>(to, o);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+                                if (nn + e < p.b.rows) to[e] = from_f<E>(plus ? o[e] + to_f(plus[e]) : o[e]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    if (!ok && p.err) atomicExch(p.err, kErrTimeout);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // nothing of the pair is still to arrive at the other CTA
+    if (warp == 3) tmem_dealloc_pair(acc, S::kCols);
+}
+
 bool encode_operand(CUtensorMap &map, const Fp8Operand &o, int64_t K, int box_rows) {
     const auto encode = chunk::encode_fn();
     if (!encode) return false;
@@ -239,6 +564,31 @@ cudaError_t run_tile(MatmulArgs &args, int split, cudaStream_t stream) {
     return cudaLaunchKernelEx(&c, kernel, args, split);
 }
 
+template <typename E, int BN>
+cudaError_t run_pair(MatmulArgs &args, int sms, cudaStream_t stream) {
+    using S = PairShape<BN>;
+    constexpr auto kernel = mm_pair_kernel<E, BN>;
+    cudaError_t e = allow_smem<kernel>(S::kSmem);
+    if (e != cudaSuccess) return e;
+    MatmulParams &p = args.p;
+    if (!encode_operand(args.a, p.a, p.K, kRows) || !encode_operand(args.b, p.b, p.K, BN / 2)) return cudaErrorInvalidValue;
+    constexpr int V = 16 / sizeof(E);
+    const int wide = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.os % V == 0 &&
+                     (!p.add || (reinterpret_cast<uintptr_t>(p.add) % 16 == 0 && p.as % V == 0));
+    const int64_t tiles = ceil_div(p.a.rows, 2 * kRows) * ceil_div(p.b.rows, BN);
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(2 * (unsigned)std::min(tiles, (int64_t)sms / 2));
+    c.blockDim = dim3(kPairThreads);
+    c.dynamicSmemBytes = S::kSmem;
+    c.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, args, wide);
+}
+
 // out = add, where K is 0.
 template <typename E>
 __global__ void __launch_bounds__(256) mm_add_kernel(MatmulParams p) {
@@ -260,6 +610,15 @@ cudaError_t launch_matmul(const MatmulParams &p, int sms, cudaStream_t stream) {
         MatmulArgs args;
         args.p = p;
         if (!encode_operand(args.b, p.b, p.K, kRows)) return cudaErrorInvalidValue;
+        if (p.a.rows > 256) {
+            const char *bn = getenv("MM_BN");
+            switch (bn ? atoi(bn) : 224) {
+                case 128: return run_pair<E, 128>(args, sms, stream);
+                case 192: return run_pair<E, 192>(args, sms, stream);
+                case 256: return run_pair<E, 256>(args, sms, stream);
+                default: return run_pair<E, 224>(args, sms, stream);
+            }
+        }
         const int64_t M = p.a.rows, tiles = ceil_div(p.b.rows, kRows), blocks = ceil_div(p.K, kFp8Block);
         const int bt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
         const int64_t all = tiles * ceil_div(M, bt);
