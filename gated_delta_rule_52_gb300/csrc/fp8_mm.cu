@@ -55,7 +55,7 @@ struct Slot {
 };
 
 struct MatmulArgs {
-    CUtensorMap a, b;
+    CUtensorMap a, b, out;
     MatmulParams p;
 };
 
@@ -276,12 +276,15 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
 constexpr int kPairThreads = 384, kStoreWarps = 8;
 constexpr int kSegment = 32;                // blocks of K per segment of an fp32 output
 
+// A store warp's buffer: 32 rows of 64 bytes for a tensor store, or 32 x 17 fp32.
+constexpr int kStoreBuffer = 2560;
+
 template <int BN>
 struct PairShape {
     static constexpr int kStage = (kRows + BN / 2) * kFp8Block;
     static constexpr int kScaleB = BN <= 128 ? 512 : 1024;
     static constexpr int kScaleStage = 512 + kScaleB;
-    static constexpr int kStaging = kStoreWarps * 32 * 17 * 4;
+    static constexpr int kStaging = kStoreWarps * kStoreBuffer;
     static constexpr int kStages = (227 * 1024 - 2048 - kStaging - kScaleStage * kScaleStages) / kStage;
     static constexpr int kSmem = 1024 + kStage * kStages + kScaleStage * kScaleStages + kStaging;
     static constexpr int kSet = 4 + kScaleB / 128;
@@ -298,6 +301,41 @@ __device__ __forceinline__ void tile_at(int64_t t, int64_t down, int64_t across,
     j = in / high;
 }
 
+// The first n of V neighbours (the others 0), in one load where all exist.
+template <typename E, int V>
+__device__ __forceinline__ Pack<E, V> ld_row(const E *p, int n) {
+    if (n >= V) return ld_pack<E, V>(p);
+    Pack<E, V> r;
+#pragma unroll
+    for (int e = 0; e < V; ++e) r.e[e] = e < n ? p[e] : from_f<E>(0.f);
+    return r;
+}
+
+// 16 columns of 32 rows (one to a lane) to out, with the addend, by single elements: neighbouring
+// lanes take neighbouring columns.  `own`: 32 x 17 fp32 of shared memory.
+template <typename E>
+__device__ __forceinline__ void st_narrow(const MatmulParams &p, const float (&r)[16], float *own, int64_t m0, int64_t n0, int lane) {
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) own[lane * 17 + e] = r[e];
+    __syncwarp();
+    const int64_t n = n0 + (lane & 15), m = m0 + (lane >> 4);
+    const int rows = n < p.b.rows ? (int)min(max(p.a.rows - m, (int64_t)0), (int64_t)32) : 0;
+    E *to = static_cast<E *>(p.out) + m * p.os + n;
+    const E *plus = static_cast<const E *>(p.add) + m * p.as + n;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float a[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = p.add && 16 * h + 2 * i < rows ? to_f(plus[(16 * h + 2 * i) * p.as]) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = 16 * h + 2 * i;
+            if (row < rows) to[row * p.os] = from_f<E>(own[(row + (lane >> 4)) * 17 + (lane & 15)] + a[i]);
+        }
+    }
+}
+
 template <typename E, int BN>
 __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_constant__ MatmulArgs args, int wide) {
     using S = PairShape<BN>;
@@ -305,7 +343,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     extern __shared__ unsigned char raw[];
     unsigned char *ring = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     unsigned char *scales = ring + S::kStage * S::kStages;
-    float *staging = reinterpret_cast<float *>(scales + S::kScaleStage * kScaleStages);
+    unsigned char *staging = scales + S::kScaleStage * kScaleStages;   // 512-byte aligned
     __shared__ uint64_t full[S::kStages], empty[S::kStages], sfull[kScaleStages], sempty[kScaleStages], tfull[S::kBuffers], tempty[S::kBuffers];
     __shared__ uint32_t tmem_base;
     const MatmulParams &p = args.p;
@@ -377,6 +415,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                 tc_fence_after();
                 const uint32_t to = acc + sum.at * BN;
                 const int k1 = min(blocks, k0 + segment);
+                bool ready = false;   // this lane has seen the next stage full
                 for (int k = k0; k < k1; ++k) {
                     const uint32_t set = sf + (scale.at & 1) * S::kSet;
                     if (k % 4 == 0) {
@@ -392,19 +431,21 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                             mma_commit_pair(&sempty[scale.at]);
                         }
                     }
-                    if (!warp_wait<false>(&full[slot.at], slot.turn)) {
+                    if (!__all_sync(0xffffffffu, ready) && !warp_wait<false>(&full[slot.at], slot.turn)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint64_t ad = a0 + slot.at * (S::kStage >> 4), bd = ad + (kRows * kFp8Block >> 4);
                     const uint32_t id = idesc | (k & 3) << 4 | (uint32_t)(k & 3) << 29;
+                    const int here = slot.at;
+                    slot.next();
+                    ready = mbar_try_wait(&full[slot.at], slot.turn);   // its answer is looked at after the MMAs' issue
                     if (issuer) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) mma_mx8_pair(to, ad + 2 * q, bd + 2 * q, id, set, set + 4, k != k0 || q > 0);
-                        mma_commit_pair(&empty[slot.at]);
+                        mma_commit_pair(&empty[here]);
                     }
-                    slot.next();
                     if (k % 4 == 3 || k == blocks - 1) scale.next();
                 }
                 if (issuer) mma_commit_pair(&tfull[sum.at]);
@@ -452,79 +493,124 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     } else if (warp >= 4) {
         // ---- accumulators to out: lanes 32 (warp % 4) .. + 31, one half of the columns
         const int part = warp & 3, half = (warp - 4) >> 2;
-        constexpr int kHalf = BN / 2;
-        float *own = staging + (warp - 4) * 32 * 17;
+        constexpr int kMost = (BN / 2 + 31) / 32 * 32;      // of the first half; the second may be shorter
+        constexpr int V = 16 / sizeof(E);
+        const int cols = half ? BN - kMost : kMost;
+        unsigned char *own = staging + (warp - 4) * kStoreBuffer;
         Slot<S::kBuffers> sum;
         const uint32_t bars = mapa_shared(smem_u32(tempty), 0);
         for (int64_t t = pair; ok && t < tiles; t += pairs) {
             int64_t ti, tj;
             tile_at(t, down, across, ti, tj);
-            const int64_t m0 = ti * 2 * kRows + rank * kRows + part * 32, n0 = tj * BN + half * kHalf;
-            float f[kSums ? kHalf : 16];
+            const int64_t m0 = ti * 2 * kRows + rank * kRows + part * 32, n0 = tj * BN + half * kMost;
+            const int64_t left = p.b.rows - n0;              // columns of out from here on
+            const E *plus = p.add ? static_cast<const E *>(p.add) + (m0 + lane) * p.as + n0 : nullptr;
+            const bool my_row = m0 + lane < p.a.rows;
+            // this lane's row: fp32, or 16-bit values that begin as the addend's
+            float f[kSums ? kMost : 1];
+            Pack<E, V> o[kSums ? 1 : kMost / V];
+            if constexpr (!kSums) {
+                if (wide && plus) {
+#pragma unroll
+                    for (int c = 0; c < kMost; c += V)
+                        if (c < cols) o[c / V] = ld_row<E, V>(plus + c, my_row ? (int)min(left - c, (int64_t)V) : 0);
+                }
+            }
             for (int k = 0; k < blocks; k += segment) {
                 const int buf = sum.at;
-                ok = wait_for<false>(&tfull[buf], sum.turn);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = warp_wait<false>(&tfull[buf], sum.turn);
                 if (!ok) break;
                 sum.next();
                 tc_fence_after();
-                const bool last = k + segment >= blocks;
-                const uint32_t from = tmem_addr(acc, part * 32, buf * BN + half * kHalf);
+                const uint32_t from = tmem_addr(acc, part * 32, buf * BN + half * kMost);
                 if constexpr (kSums) {
 #pragma unroll
-                    for (int c = 0; c < kHalf; c += 16) {
+                    for (int c = 0; c < kMost; c += 32) {
+                        if (c >= cols) break;
+                        float r[32];
+                        tmem_ld32(from + c, r);
+                        tmem_ld_wait();
+                        if (k == 0) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) f[c + e] = r[e];
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) f[c + e] += r[e];
+                        }
+                    }
+                } else if (wide) {
+#pragma unroll
+                    for (int c = 0; c < kMost; c += 32) {
+                        if (c >= cols) break;
+                        float r[32];
+                        tmem_ld32(from + c, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; e += V) {
+                            float (&v)[V] = reinterpret_cast<float (&)[V]>(r[e]);
+                            if (plus) {
+                                float a[V];
+                                unpack<E, V>(o[(c + e) / V], a);
+                                add_n<V>(v, v, a);
+                            }
+                            st_f<E, V>(o[(c + e) / V].e, v);
+                        }
+                    }
+                } else {
+                    // rows that no wide access fits: 16 columns at a time through shared memory
+#pragma unroll 1
+                    for (int c = 0; c < cols; c += 16) {
                         float r[16];
                         tmem_ld16(from + c, r);
                         tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) f[c + e] = k == 0 ? r[e] : f[c + e] + r[e];
+                        st_narrow<E>(p, r, reinterpret_cast<float *>(own), m0, n0 + c, lane);
                     }
-                    tc_fence_before();
-                    if (lane == 0) mbar_arrive_remote(bars + 8 * buf);
-                    if (!last) continue;
                 }
+                tc_fence_before();
+                if (lane == 0) mbar_arrive_remote(bars + 8 * buf);
+            }
+            if (!ok) break;
+            if constexpr (kSums) {
+                if (!wide) {
 #pragma unroll
-                for (int c = 0; c < kHalf; c += 16) {
-                    // 16 columns through shared memory: rows of 16 neighbours to store
-                    if constexpr (!kSums) {
-                        tmem_ld16(from + c, f);
-                        tmem_ld_wait();
-                        if (c + 16 >= kHalf) {
-                            tc_fence_before();
-                            if (lane == 0) mbar_arrive_remote(bars + 8 * buf);
+                    for (int c = 0; c < kMost; c += 16)
+                        if (c < cols) st_narrow<E>(p, reinterpret_cast<float (&)[16]>(f[c]), reinterpret_cast<float *>(own), m0, n0 + c, lane);
+                }
+            }
+            if (!wide || m0 >= p.a.rows) continue;
+            // 64 bytes of every row to the buffer (16-byte piece j of row r at j ^ (r / 2 % 4), the
+            // 64-byte swizzle), and from there by a tensor store, which leaves out what is outside
+            constexpr int kStep = 64 / sizeof(E);
+#pragma unroll
+            for (int c = 0; c < kMost; c += kStep) {
+                if (c >= cols || c >= left) break;
+                if (lane == 0) bulk_wait_read0();
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    Pack<E, V> piece;
+                    if constexpr (kSums) {
+                        float (&v)[V] = reinterpret_cast<float (&)[V]>(f[c + j * V]);
+                        if (plus) {
+                            float a[V];
+                            unpack<E, V>(ld_row<E, V>(plus + c + j * V, my_row ? (int)min(left - c - j * V, (int64_t)V) : 0), a);
+                            add_n<V>(v, v, a);
                         }
+                        st_f<E, V>(piece.e, v);
+                    } else {
+                        piece = o[c / V + j];
                     }
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) own[lane * 17 + e] = f[kSums ? c + e : e];
-                    __syncwarp();
-                    constexpr int V = 16 / sizeof(E), G = 16 / V;   // elements of a store, stores of a row
-#pragma unroll 1
-                    for (int u = 0; u < G; ++u) {
-                        const int row = u * (32 / G) + lane / G, col = lane % G * V;
-                        const int64_t m = m0 + row, nn = n0 + c + col;
-                        if (m >= p.a.rows || nn >= p.b.rows) continue;
-                        float o[V];
-#pragma unroll
-                        for (int e = 0; e < V; ++e) o[e] = own[row * 17 + col + e];
-                        E *to = static_cast<E *>(p.out) + m * p.os + nn;
-                        const E *plus = p.add ? static_cast<const E *>(p.add) + m * p.as + nn : nullptr;
-                        if (wide && nn + V <= p.b.rows) {
-                            if (plus) {
-                                float a[V];
-                                ld_f<E, V>(plus, a);
-                                add_n<V>(o, o, a);
-                            }
-                            st_f<E, V>(to, o);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < V; ++e)
-                                if (nn + e < p.b.rows) to[e] = from_f<E>(plus ? o[e] + to_f(plus[e]) : o[e]);
-                        }
-                    }
+                    *reinterpret_cast<Pack<E, V> *>(own + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = piece;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&args.out, own, (int)(n0 + c), (int)m0);
+                    bulk_commit();
                 }
             }
         }
+        if (lane == 0) bulk_wait0();
     }
     if (!ok && p.err) atomicExch(p.err, kErrTimeout);
     __syncwarp();
@@ -542,6 +628,20 @@ bool encode_operand(CUtensorMap &map, const Fp8Operand &o, int64_t K, int box_ro
     return encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(o.q), dims, strides, box, step,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// out for tensor stores of 64 bytes by 32 rows.
+bool encode_out(CUtensorMap &map, const MatmulParams &p) {
+    const auto encode = chunk::encode_fn();
+    if (!encode) return false;
+    const size_t e = dtype_bytes(p.dtype);
+    const cuuint64_t dims[2] = {(cuuint64_t)p.b.rows, (cuuint64_t)p.a.rows}, strides[1] = {(cuuint64_t)p.os * e};
+    const cuuint32_t box[2] = {(cuuint32_t)(64 / e), 32}, step[2] = {1, 1};
+    const CUtensorMapDataType type = p.dtype == kBF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                     : p.dtype == kFP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    return encode(&map, type, 2, p.out, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename E, int BT>
@@ -575,6 +675,7 @@ cudaError_t run_pair(MatmulArgs &args, int sms, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(E);
     const int wide = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.os % V == 0 &&
                      (!p.add || (reinterpret_cast<uintptr_t>(p.add) % 16 == 0 && p.as % V == 0));
+    if (wide && !encode_out(args.out, p)) return cudaErrorInvalidValue;
     const int64_t tiles = ceil_div(p.a.rows, 2 * kRows) * ceil_div(p.b.rows, BN);
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3(2 * (unsigned)std::min(tiles, (int64_t)sms / 2));

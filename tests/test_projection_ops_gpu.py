@@ -68,6 +68,11 @@ MM = [  # M, N, K, a, b, a_tile, b_tile, dtype, add
     (300, 100, 4097, E5, E4, False, False, F, True),
     (513, 700, 256, E4, E4, False, True, BF, False),
     (1100, 520, 1200, E4, E5, True, True, F, False),
+    (400, 264, 640, E4, E4, False, True, BF, True),
+    (700, 1000, 384, E5, E4, False, False, HF, True),
+    (520, 1032, 4300, E4, E4, False, False, F, True),        # fp32 sums of several segments
+    (2049, 513, 130, E4, E4, False, True, BF, True),
+    (1537, 2048, 256, E4, E4, True, True, HF, False),
 ]
 
 
