@@ -353,9 +353,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int blocks = (int)ceil_div(p.K, kFp8Block);
     const int segment = kSums ? kSegment : blocks;
+    const int groups = (int)ceil_div(blocks, 4);                       // of scales per tile
+    const int64_t all = pair < tiles ? ((tiles - pair - 1) / pairs + 1) * groups : 0;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-        for (int i = 0; i < kScaleStages; ++i) mbar_init(&sfull[i], 64), mbar_init(&sempty[i], 1);
+        for (int i = 0; i < kScaleStages; ++i) mbar_init(&sfull[i], rank == 0 ? 33 : 32), mbar_init(&sempty[i], 1);
         for (int i = 0; i < S::kBuffers; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 2 * kStoreWarps);
         fence_mbar_init();
     }
@@ -452,17 +454,24 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                 sum.next();
             }
         }
+    } else if (warp == 1) {
+        // ---- the second CTA's scales are there: told to the first by a warp that has no copies on
+        // their way, because a release for the cluster waits for all of a thread's
+        Slot<kScaleStages> scale;
+        const uint32_t bars = mapa_shared(smem_u32(sfull), 0);
+        for (int64_t n = 0; n < all; ++n) {
+            ok = warp_wait<false>(&sfull[scale.at], scale.turn);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_remote(bars + 8 * scale.at);
+            scale.next();
+        }
     } else if (warp == 2) {
         // ---- scales: of this CTA's rows of a, and of all rows of b
-        const int groups = (int)ceil_div(blocks, 4);
-        const int64_t mine = pair < tiles ? (tiles - pair - 1) / pairs + 1 : 0;
         ScaleRows<kRows> rows_a;
         ScaleRows<BN> rows_b;
         int64_t t = pair;
         int g = 0;
         Slot<kScaleStages> in, out;
-        const uint32_t bars = mapa_shared(smem_u32(sfull), 0);
-        const int64_t all = mine * groups;
         for (int64_t n = 0; n < all + kAhead; ++n) {
             if (n < all) {
                 if (g == 0) {
@@ -485,7 +494,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
             if (n >= kAhead) {
                 copies_wait<kAhead>();
                 fence_proxy_async_smem();
-                mbar_arrive_remote(bars + 8 * out.at);
+                mbar_arrive(&sfull[out.at]);
                 out.next();
             }
         }
