@@ -54,14 +54,20 @@ struct Slot {
     }
 };
 
+// Tiles of a pair kernel's call: the first `full` are one item of work each; each of the `rest`
+// after them is `split` items, equal parts of K, whose sums meet in the workspace.
+struct Plan {
+    int64_t full, rest;
+    int split;
+    float *parts;          // [rest][split][2][kStoreWarps][kMost][32]
+    unsigned *arrived;     // [rest][2][kStoreWarps], zero at the start
+};
+
 struct MatmulArgs {
     CUtensorMap a, b, out;
     MatmulParams p;
+    Plan plan;
 };
-
-__device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap &map, uint64_t *bar, int k, int row) {
-    tma_box(dst, map, bar, k, row);
-}
 
 // Asynchronous copy of up to 4 bytes (the rest zero) into shared memory.
 __device__ __forceinline__ void copy_word(uint32_t dst, const uint8_t *src, int bytes) {
@@ -76,13 +82,13 @@ struct ScaleRows {
     static constexpr int kWords = (N + 31) / 32;
     const uint8_t *row[kWords];
     uint32_t in;   // which of them exist
-    __device__ __forceinline__ void set(const Fp8Operand &o, int64_t row0, int lane) {
+    __device__ __forceinline__ void set(const Fp8Operand &o, int64_t row0, int block, int lane) {   // from this block on
         in = 0;
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
             const int64_t r = row0 + 32 * w + lane;
             const bool some = 32 * w + lane < N && r < o.rows;
-            row[w] = o.s + (some ? (o.tile ? r / kFp8Block : r) * o.s_stride : 0);
+            row[w] = o.s + (some ? (o.tile ? r / kFp8Block : r) * o.s_stride + block : 0);
             in |= (uint32_t)some << w;
         }
     }
@@ -96,18 +102,18 @@ struct ScaleRows {
     }
 };
 
-// ---- one tile of 128 rows of b by BT rows of a per cluster of `split` CTAs, which share K and
-// join their sums through distributed shared memory.
+// ---- few rows of a: one tile of 128 rows of b by BT rows of a per cluster of `split` CTAs, which
+// share K and join their sums through distributed shared memory.  The rows of b, of which nearly
+// all bytes are, lie along the MMA's M, so that tiles are full however few rows a has.  Two CTAs
+// per SM keep about 170 KB of loads in flight.
 template <int BT>
 struct TileShape {
     static constexpr int kStage = (kRows + BT) * kFp8Block;
-    static constexpr int kStages = BT <= 16 ? 6 : BT <= 32 ? 5 : BT <= 64 ? 4 : BT <= 128 ? 3 : 4;
-    static constexpr int kScaleA = BT <= 128 ? 512 : 1024;
-    static constexpr int kScaleStage = 512 + kScaleA;
+    static constexpr int kScaleStage = 1024;
+    static constexpr int kStages = (113 * 1024 - 2048 - kScaleStage * kScaleStages) / kStage;
     static constexpr int kSmem = 1024 + kStage * kStages + kScaleStage * kScaleStages;
-    // TMEM columns: the accumulator, and two sets of scales
-    static constexpr int kSet = 4 + kScaleA / 128;
-    static constexpr int kCols = BT + 2 * kSet <= 32 ? 32 : BT + 2 * kSet <= 64 ? 64 : BT + 2 * kSet <= 128 ? 128 : BT + 2 * kSet <= 256 ? 256 : 512;
+    static constexpr int kSet = 8;                     // TMEM columns of scales
+    static constexpr int kCols = BT + 2 * kSet <= 32 ? 32 : BT + 2 * kSet <= 64 ? 64 : 128;
     static_assert(BT * kRows * 4 <= kStage * kStages, "the sums fit the ring");
 };
 
@@ -120,18 +126,30 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
     __shared__ uint64_t full[S::kStages], empty[S::kStages], sfull[kScaleStages], sempty[kScaleStages], done;
     __shared__ uint32_t tmem_base;
     const MatmulParams &p = args.p;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = blockIdx.x % split;
     const int64_t tile = blockIdx.x / split, across = ceil_div(p.b.rows, kRows), m0 = tile / across * BT, n0 = tile % across * kRows;
     const int blocks = (int)ceil_div(p.K, kFp8Block);
     const int k0 = (int)((int64_t)blocks * rank / split), k1 = (int)((int64_t)blocks * (rank + 1) / split);
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-        for (int i = 0; i < kScaleStages; ++i) mbar_init(&sfull[i], 32), mbar_init(&sempty[i], 1);
-        mbar_init(&done, 1);
-        fence_mbar_init();
-    }
-    if (warp == 3) {
+    const int early = min(k1 - k0, S::kStages);        // loads that wait for nothing
+    bool ok = true, issuer = false;
+    const auto load = [&](int k, int at) {
+        unsigned char *to = ring + at * S::kStage;
+        mbar_arrive_expect_tx(&full[at], S::kStage);
+        tma_box(to, args.b, &full[at], k * kFp8Block, (int)n0);
+        tma_box(to + kRows * kFp8Block, args.a, &full[at], k * kFp8Block, (int)m0);
+    };
+    if (warp == 0) {
+        issuer = elect_one();
+        if (issuer) {
+            for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+            for (int i = 0; i < kScaleStages; ++i) mbar_init(&sfull[i], 32), mbar_init(&sempty[i], 1);
+            mbar_init(&done, 1);
+            fence_mbar_init();
+            for (int i = 0; i < early; ++i) load(k0 + i, i);
+        }
+    } else if (warp == 1) {
+        issuer = elect_one();
         tmem_alloc(&tmem_base, S::kCols);
         tmem_relinquish();
     }
@@ -139,82 +157,76 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
     __syncthreads();
     tc_fence_after();
     const uint32_t acc = tmem_base, sf = acc + BT;
-    bool ok = true;
-    if (warp == 0 && lane == 0) {
-        int i = 0;
-        for (int k = k0; k < k1; ++k, ++i) {
-            const int st = i % S::kStages, turn = i / S::kStages;
-            if (turn > 0 && !wait_for<false>(&empty[st], (turn - 1) & 1)) {
-                ok = false;
-                break;
-            }
-            unsigned char *at = ring + st * S::kStage;
-            mbar_arrive_expect_tx(&full[st], S::kStage);
-            tma_tile(at, args.b, &full[st], k * kFp8Block, (int)n0);
-            tma_tile(at + kRows * kFp8Block, args.a, &full[st], k * kFp8Block, (int)m0);
+    if (warp == 0) {
+        Slot<S::kStages> slot;
+        for (int k = k0 + early; k < k1; ++k) {
+            ok = warp_wait<false>(&empty[slot.at], slot.turn);
+            if (!ok) break;
+            if (issuer) load(k, slot.at);
+            slot.next();
         }
-        // the copies end before the CTA does
-        for (int j = max(0, i - S::kStages); j < i; ++j)
-            if (!wait_for<false>(&full[j % S::kStages], (j / S::kStages) & 1)) ok = false;
-    } else if (warp == 1 && lane == 0) {
-        int i = 0, g = -1, sets = 0;
-        for (int k = k0; ok && k < k1; ++k, ++i) {
-            const int st = i % S::kStages;
-            if (k / 4 != g) {
-                g = k / 4;
-                const int ss = sets % kScaleStages;
-                if (!wait_for<false>(&sfull[ss], (sets / kScaleStages) & 1)) {
-                    ok = false;
-                    break;
-                }
+        // the copies end before the CTA does: the last loads of all slots, in order
+        if (early < S::kStages) slot.at = 0;
+        for (int i = 0; i < early; ++i) {
+            if (!warp_wait<false>(&full[slot.at], early < S::kStages ? 0 : slot.turn)) ok = false;
+            slot.next();
+        }
+    } else if (warp == 1) {
+        Slot<S::kStages> slot;
+        Slot<kScaleStages> scale;
+        const uint64_t b0 = sdesc_sw128(smem_u32(ring), 16, 1024), s0 = sdesc_plain(smem_u32(scales), 128);
+        const uint32_t idesc = idesc_mx8(kRows, BT, p.b.dtype == kE5M2, p.a.dtype == kE5M2, 0);
+        for (int k = k0; k < k1; ++k) {
+            const uint32_t set = sf + (scale.at & 1) * S::kSet;
+            if (k % 4 == 0 || k == k0) {
+                ok = warp_wait<false>(&sfull[scale.at], scale.turn);
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t from = smem_u32(scales + ss * S::kScaleStage), to = sf + (sets & 1) * S::kSet;
-                tmem_copy_scales(to, sdesc_plain(from, 128));
-                for (int c = 0; c < S::kScaleA / 512; ++c) tmem_copy_scales(to + 4 + 4 * c, sdesc_plain(from + 512 + 512 * c, 128));
-                mma_commit(&sempty[ss]);
-                ++sets;
+                const uint64_t from = s0 + scale.at * (S::kScaleStage >> 4);
+                if (issuer) {
+                    tmem_copy_scales(set, from);
+                    tmem_copy_scales(set + 4, from + 32);
+                    mma_commit(&sempty[scale.at]);
+                }
             }
-            if (!wait_for<false>(&full[st], (i / S::kStages) & 1)) {
-                ok = false;
-                break;
-            }
+            ok = warp_wait<false>(&full[slot.at], slot.turn);
+            if (!ok) break;
             tc_fence_after();
-            const uint32_t set = sf + ((sets - 1) & 1) * S::kSet, at = smem_u32(ring + st * S::kStage);
-            const uint32_t idesc = idesc_mx8(kRows, BT, p.b.dtype == kE5M2, p.a.dtype == kE5M2, k & 3);
+            const uint64_t bd = b0 + slot.at * (S::kStage >> 4), ad = bd + (kRows * kFp8Block >> 4);
+            const uint32_t id = idesc | (k & 3) << 4 | (uint32_t)(k & 3) << 29;
+            if (issuer) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                mma_mx8(acc, sdesc_sw128(at + 32 * q, 16, 1024), sdesc_sw128(at + kRows * kFp8Block + 32 * q, 16, 1024), idesc, set,
-                        set + 4, i > 0 || q > 0);
-            mma_commit(&empty[st]);
+                for (int q = 0; q < 4; ++q) mma_mx8(acc, bd + 2 * q, ad + 2 * q, id, set, set + 4, k != k0 || q > 0);
+                mma_commit(&empty[slot.at]);
+            }
+            slot.next();
+            if (k % 4 == 3) scale.next();
         }
-        mma_commit(&done);
+        if (issuer) mma_commit(&done);
     } else if (warp == 2) {
         // kAhead groups on their way while the ones before are handed over
-        const int g0 = k0 / 4, groups = k1 > k0 ? (k1 - 1) / 4 - g0 + 1 : 0;
+        const int g0 = k0 / 4, groups = (k1 - 1) / 4 - g0 + 1;
         ScaleRows<kRows> rows_b;
         ScaleRows<BT> rows_a;
-        rows_b.set(p.b, n0, lane);
-        rows_a.set(p.a, m0, lane);
-#pragma unroll
-        for (int w = 0; w < rows_b.kWords; ++w) rows_b.row[w] += rows_b.in >> w & 1 ? 4 * g0 : 0;
-#pragma unroll
-        for (int w = 0; w < rows_a.kWords; ++w) rows_a.row[w] += rows_a.in >> w & 1 ? 4 * g0 : 0;
+        rows_b.set(p.b, n0, 4 * g0, lane);
+        rows_a.set(p.a, m0, 4 * g0, lane);
+        Slot<kScaleStages> in, out;
         for (int i = 0; i < groups + kAhead; ++i) {
             if (i < groups) {
-                const int ss = i % kScaleStages, turn = i / kScaleStages;
-                if (turn > 0 && !wait_for<false>(&sempty[ss], (turn - 1) & 1)) ok = false;
-                ok = __all_sync(0xffffffffu, ok);
+                ok = warp_wait<false>(&sempty[in.at], in.turn ^ 1);
                 if (!ok) break;
-                const uint32_t at = smem_u32(scales + ss * S::kScaleStage);
+                const uint32_t at = smem_u32(scales + in.at * S::kScaleStage);
                 const int bytes = min(4, blocks - 4 * (g0 + i));
                 rows_b.copy(at, bytes, lane);
                 rows_a.copy(at + 512, bytes, lane);
+                in.next();
             }
             copies_commit();
             if (i >= kAhead) {
                 copies_wait<kAhead>();
                 fence_proxy_async_smem();
-                mbar_arrive(&sfull[(i - kAhead) % kScaleStages]);
+                mbar_arrive(&sfull[out.at]);
+                out.next();
             }
         }
         copies_wait<0>();
@@ -228,38 +240,32 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
     float *sums = reinterpret_cast<float *>(ring);
     for (int c = 0; c < BT; c += 16) {
         float r[16];
-        if (k1 > k0) {
-            tmem_ld16(tmem_addr(acc, warp * 32, c), r);
-            tmem_ld_wait();
-        }
+        tmem_ld16(tmem_addr(acc, warp * 32, c), r);
+        tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sums[(c + j) * kRows + threadIdx.x] = k1 > k0 ? r[j] : 0.f;
+        for (int j = 0; j < 16; ++j) sums[(c + j) * kRows + threadIdx.x] = r[j];
     }
     tc_fence_before();
     if (split > 1) cluster_sync();
     else __syncthreads();
-    if (warp == 3) tmem_dealloc(acc, S::kCols);
+    if (warp == 1) tmem_dealloc(acc, S::kCols);
     // each CTA's part of the tile's rows of a
-    const int c0 = BT * rank / split, c1 = BT * (rank + 1) / split;
+    const int c0 = BT * rank / split, c1 = (int)min((int64_t)(BT * (rank + 1) / split), p.a.rows - m0);
     const int64_t n = n0 + threadIdx.x;
-    const uint32_t mine = smem_u32(sums);
+    const uint32_t mine = smem_u32(sums) + threadIdx.x * 4;
+#pragma unroll 2
     for (int c = c0; c < c1; ++c) {
         const int64_t m = m0 + c;
-        if (m >= p.a.rows) break;
-        float t = 0.f;
-        if (split == 1) {
-            t = sums[c * kRows + threadIdx.x];
-        } else {
-            for (int q = 0; q < split; ++q) {
-                float v;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(mine + (c * kRows + threadIdx.x) * 4, q)) : "memory");
-                t += v;
-            }
-        }
-        if (n < p.b.rows) {
-            if (p.add) t += to_f(static_cast<const E *>(p.add)[m * p.as + n]);
-            static_cast<E *>(p.out)[m * p.os + n] = from_f<E>(t);
-        }
+        float v[8], t = 0.f;
+        if (p.add && n < p.b.rows) t = to_f(static_cast<const E *>(p.add)[m * p.as + n]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < split) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[q]) : "r"(mapa_shared(mine + c * kRows * 4, q)) : "memory");
+        float u = v[0];
+#pragma unroll
+        for (int q = 1; q < 8; ++q)
+            if (q < split) u += v[q];
+        if (n < p.b.rows) static_cast<E *>(p.out)[m * p.os + n] = from_f<E>(p.add ? u + t : u);
     }
     if (split > 1) cluster_sync();   // the others have read this CTA's sums
 }
@@ -288,9 +294,9 @@ struct PairShape {
     static constexpr int kStages = (227 * 1024 - 2048 - kStaging - kScaleStage * kScaleStages) / kStage;
     static constexpr int kSmem = 1024 + kStage * kStages + kScaleStage * kScaleStages + kStaging;
     static constexpr int kSet = 4 + kScaleB / 128;
-    static constexpr int kBuffers = 2 * BN + 2 * kSet <= 512 ? 2 : 1;
-    static constexpr int kCols = kBuffers * BN + 2 * kSet <= 256 ? 256 : 512;
-    static_assert(kSmem <= 227 * 1024 && BN % 32 == 0 && kBuffers * BN + 2 * kSet <= 512, "fits an SM");
+    static constexpr int kBuffers = 2, kCols = 512;
+    static constexpr int kMost = (BN / 2 + 31) / 32 * 32;   // columns of a store warp, at most
+    static_assert(kSmem <= 227 * 1024 && BN % 32 == 0 && kBuffers * BN + 2 * kSet <= kCols, "fits an SM");
 };
 
 // Tile t of a grid of `down` x `across`: 8 tiles down, then across, so that the tiles in flight
@@ -336,6 +342,26 @@ __device__ __forceinline__ void st_narrow(const MatmulParams &p, const float (&r
     }
 }
 
+// One item of a plan: blocks [k0, k1) of a tile.
+struct Item {
+    int64_t i, j, rest;    // the tile's place; its number among the shared ones, or -1
+    int k0, k1, part;
+    __device__ __forceinline__ Item(const Plan &plan, int64_t n, int64_t down, int64_t across, int blocks) {
+        int64_t t = n;
+        rest = -1, part = 0, k0 = 0, k1 = blocks;
+        if (n >= plan.full) {
+            rest = (n - plan.full) % plan.rest;
+            part = (int)((n - plan.full) / plan.rest);
+            t = plan.full + rest;
+            if (plan.split == 1) rest = -1;
+            const int groups = (blocks + 3) / 4;     // parts begin at a group of 4 blocks
+            k0 = 4 * (int)((int64_t)groups * part / plan.split);
+            k1 = min(4 * (int)((int64_t)groups * (part + 1) / plan.split), blocks);
+        }
+        tile_at(t, down, across, i, j);
+    }
+};
+
 template <typename E, int BN>
 __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_constant__ MatmulArgs args, int wide) {
     using S = PairShape<BN>;
@@ -349,12 +375,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     const MatmulParams &p = args.p;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const int64_t down = ceil_div(p.a.rows, 2 * kRows), across = ceil_div(p.b.rows, BN), tiles = down * across;
+    const Plan &plan = args.plan;
+    const int64_t down = ceil_div(p.a.rows, 2 * kRows), across = ceil_div(p.b.rows, BN), items = plan.full + plan.rest * plan.split;
     const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int blocks = (int)ceil_div(p.K, kFp8Block);
     const int segment = kSums ? kSegment : blocks;
-    const int groups = (int)ceil_div(blocks, 4);                       // of scales per tile
-    const int64_t all = pair < tiles ? ((tiles - pair - 1) / pairs + 1) * groups : 0;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         for (int i = 0; i < kScaleStages; ++i) mbar_init(&sfull[i], rank == 0 ? 33 : 32), mbar_init(&sempty[i], 1);
@@ -374,11 +399,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         Slot<S::kStages> slot;
         int loads = 0;
         const uint32_t bars = mapa_shared(smem_u32(full), 0);
-        for (int64_t t = pair; ok && t < tiles; t += pairs) {
-            int64_t i, j;
-            tile_at(t, down, across, i, j);
-            const int ra = (int)(i * 2 * kRows + rank * kRows), rb = (int)(j * BN + rank * (BN / 2));
-            for (int k = 0; k < blocks; ++k) {
+        for (int64_t t = pair; ok && t < items; t += pairs) {
+            const Item item(plan, t, down, across, blocks);
+            const int ra = (int)(item.i * 2 * kRows + rank * kRows), rb = (int)(item.j * BN + rank * (BN / 2));
+            for (int k = item.k0; k < item.k1; ++k) {
                 // (a wait for the turn before the first returns at once)
                 if (!warp_wait<false>(&empty[slot.at], slot.turn ^ 1)) {
                     ok = false;
@@ -408,15 +432,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         Slot<S::kBuffers> sum;
         const uint64_t a0 = sdesc_sw128(smem_u32(ring), 16, 1024), s0 = sdesc_plain(smem_u32(scales), 128);
         const uint32_t idesc = idesc_mx8(2 * kRows, BN, p.a.dtype == kE5M2, p.b.dtype == kE5M2, 0);
-        for (int64_t t = pair; ok && t < tiles; t += pairs) {
-            for (int k0 = 0; ok && k0 < blocks; k0 += segment) {
+        for (int64_t t = pair; ok && t < items; t += pairs) {
+            const Item item(plan, t, down, across, blocks);
+            for (int k0 = item.k0; ok && k0 < item.k1; k0 += segment) {
                 if (!warp_wait<false>(&tempty[sum.at], sum.turn ^ 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t to = acc + sum.at * BN;
-                const int k1 = min(blocks, k0 + segment);
+                const int k1 = min(item.k1, k0 + segment);
                 bool ready = false;   // this lane has seen the next stage full
                 for (int k = k0; k < k1; ++k) {
                     const uint32_t set = sf + (scale.at & 1) * S::kSet;
@@ -459,73 +484,92 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         // their way, because a release for the cluster waits for all of a thread's
         Slot<kScaleStages> scale;
         const uint32_t bars = mapa_shared(smem_u32(sfull), 0);
-        for (int64_t n = 0; n < all; ++n) {
-            ok = warp_wait<false>(&sfull[scale.at], scale.turn);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_remote(bars + 8 * scale.at);
-            scale.next();
+        for (int64_t t = pair; ok && t < items; t += pairs) {
+            const Item item(plan, t, down, across, blocks);
+            for (int k = item.k0; k < item.k1; k += 4) {
+                ok = warp_wait<false>(&sfull[scale.at], scale.turn);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_remote(bars + 8 * scale.at);
+                scale.next();
+            }
         }
     } else if (warp == 2) {
-        // ---- scales: of this CTA's rows of a, and of all rows of b
+        // ---- scales: of this CTA's rows of a, and of all rows of b; kAhead groups of 4 blocks are on
+        // their way while the ones before are handed over
         ScaleRows<kRows> rows_a;
         ScaleRows<BN> rows_b;
-        int64_t t = pair;
-        int g = 0;
         Slot<kScaleStages> in, out;
-        for (int64_t n = 0; n < all + kAhead; ++n) {
-            if (n < all) {
-                if (g == 0) {
-                    int64_t i, j;
-                    tile_at(t, down, across, i, j);
-                    rows_a.set(p.a, i * 2 * kRows + rank * kRows, lane);
-                    rows_b.set(p.b, j * BN, lane);
-                }
-                ok = wait_for<false>(&sempty[in.at], in.turn ^ 1);
-                ok = __all_sync(0xffffffffu, ok);
+        int waiting = 0;                                  // groups on their way
+        const auto hand_over = [&]() {
+            fence_proxy_async_smem();
+            mbar_arrive(&sfull[out.at]);
+            out.next();
+            --waiting;
+        };
+        for (int64_t t = pair; ok && t < items; t += pairs) {
+            const Item item(plan, t, down, across, blocks);
+            rows_a.set(p.a, item.i * 2 * kRows + rank * kRows, item.k0, lane);
+            rows_b.set(p.b, item.j * BN, item.k0, lane);
+            for (int k = item.k0; k < item.k1; k += 4) {
+                ok = warp_wait<false>(&sempty[in.at], in.turn ^ 1);
                 if (!ok) break;
                 const uint32_t at = smem_u32(scales + in.at * S::kScaleStage);
-                const int bytes = min(4, blocks - 4 * g);
+                const int bytes = min(4, blocks - k);
                 rows_a.copy(at, bytes, lane);
                 rows_b.copy(at + 512, bytes, lane);
                 in.next();
-                if (++g == groups) g = 0, t += pairs;
-            }
-            copies_commit();
-            if (n >= kAhead) {
-                copies_wait<kAhead>();
-                fence_proxy_async_smem();
-                mbar_arrive(&sfull[out.at]);
-                out.next();
+                copies_commit();
+                if (++waiting > kAhead) {
+                    copies_wait<kAhead>();
+                    hand_over();
+                }
             }
         }
         copies_wait<0>();
+        while (ok && waiting > 0) hand_over();
     } else if (warp >= 4) {
         // ---- accumulators to out: lanes 32 (warp % 4) .. + 31, one half of the columns
         const int part = warp & 3, half = (warp - 4) >> 2;
-        constexpr int kMost = (BN / 2 + 31) / 32 * 32;      // of the first half; the second may be shorter
+        constexpr int kMost = S::kMost;                  // of the first half; the second may be shorter
         constexpr int V = 16 / sizeof(E);
         const int cols = half ? BN - kMost : kMost;
         unsigned char *own = staging + (warp - 4) * kStoreBuffer;
         Slot<S::kBuffers> sum;
         const uint32_t bars = mapa_shared(smem_u32(tempty), 0);
-        for (int64_t t = pair; ok && t < tiles; t += pairs) {
-            int64_t ti, tj;
-            tile_at(t, down, across, ti, tj);
-            const int64_t m0 = ti * 2 * kRows + rank * kRows + part * 32, n0 = tj * BN + half * kMost;
+        for (int64_t t = pair; ok && t < items; t += pairs) {
+            const Item item(plan, t, down, across, blocks);
+            const int64_t m0 = item.i * 2 * kRows + rank * kRows + part * 32, n0 = item.j * BN + half * kMost;
             const int64_t left = p.b.rows - n0;              // columns of out from here on
             const E *plus = p.add ? static_cast<const E *>(p.add) + (m0 + lane) * p.as + n0 : nullptr;
-            const bool my_row = m0 + lane < p.a.rows;
+            const bool my_row = m0 + lane < p.a.rows, shared = item.rest >= 0;
+            float *parts = shared ? plan.parts + (((item.rest * plan.split) * 2 + rank) * kStoreWarps + (warp - 4)) * (kMost * 32) + lane : nullptr;
+            constexpr int kPart = 2 * kStoreWarps * kMost * 32;      // from one part of a tile to the next
             // this lane's row: fp32, or 16-bit values that begin as the addend's
             float f[kSums ? kMost : 1];
             Pack<E, V> o[kSums ? 1 : kMost / V];
-            if constexpr (!kSums) {
-                if (wide && plus) {
+            const auto take_addend = [&]() {
+                if constexpr (!kSums) {
 #pragma unroll
                     for (int c = 0; c < kMost; c += V)
                         if (c < cols) o[c / V] = ld_row<E, V>(plus + c, my_row ? (int)min(left - c, (int64_t)V) : 0);
                 }
-            }
-            for (int k = 0; k < blocks; k += segment) {
+            };
+            const auto round_off = [&](int c, float (&r)[32]) {      // 32 columns to o, with the addend there
+                if constexpr (!kSums) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += V) {
+                        float (&v)[V] = reinterpret_cast<float (&)[V]>(r[e]);
+                        if (plus) {
+                            float a[V];
+                            unpack<E, V>(o[(c + e) / V], a);
+                            add_n<V>(v, v, a);
+                        }
+                        st_f<E, V>(o[(c + e) / V].e, v);
+                    }
+                }
+            };
+            if (wide && plus && !shared) take_addend();
+            for (int k = item.k0; k < item.k1; k += segment) {
                 const int buf = sum.at;
                 ok = warp_wait<false>(&tfull[buf], sum.turn);
                 if (!ok) break;
@@ -539,7 +583,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                         float r[32];
                         tmem_ld32(from + c, r);
                         tmem_ld_wait();
-                        if (k == 0) {
+                        if (k == item.k0) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e) f[c + e] = r[e];
                         } else {
@@ -547,22 +591,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                             for (int e = 0; e < 32; ++e) f[c + e] += r[e];
                         }
                     }
-                } else if (wide) {
+                } else if (shared || wide) {
 #pragma unroll
                     for (int c = 0; c < kMost; c += 32) {
                         if (c >= cols) break;
                         float r[32];
                         tmem_ld32(from + c, r);
                         tmem_ld_wait();
+                        if (shared) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += V) {
-                            float (&v)[V] = reinterpret_cast<float (&)[V]>(r[e]);
-                            if (plus) {
-                                float a[V];
-                                unpack<E, V>(o[(c + e) / V], a);
-                                add_n<V>(v, v, a);
-                            }
-                            st_f<E, V>(o[(c + e) / V].e, v);
+                            for (int e = 0; e < 32; ++e) parts[item.part * kPart + (c + e) * 32] = r[e];
+                        } else {
+                            round_off(c, r);
                         }
                     }
                 } else {
@@ -579,6 +619,51 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                 if (lane == 0) mbar_arrive_remote(bars + 8 * buf);
             }
             if (!ok) break;
+            if (shared) {
+                // the last of the tile's parts to arrive adds them all up, in the order of K
+                if constexpr (kSums) {
+#pragma unroll
+                    for (int c = 0; c < kMost; ++c)
+                        if (c < cols) parts[item.part * kPart + c * 32] = f[c];
+                }
+                __threadfence();
+                __syncwarp();
+                unsigned before = 0;
+                if (lane == 0) before = atomicAdd(plan.arrived + (item.rest * 2 + rank) * kStoreWarps + (warp - 4), 1u);
+                before = __shfl_sync(0xffffffffu, before, 0);
+                if (before + 1 != (unsigned)plan.split) continue;
+                __threadfence();
+                if (wide && plus) take_addend();
+                const auto add_up = [&](int c, auto &r) {
+                    constexpr int n = sizeof(r) / sizeof(float);
+#pragma unroll
+                    for (int e = 0; e < n; ++e) r[e] = __ldcg(parts + (c + e) * 32);
+#pragma unroll 1
+                    for (int q = 1; q < plan.split; ++q)
+#pragma unroll
+                        for (int e = 0; e < n; ++e) r[e] += __ldcg(parts + q * kPart + (c + e) * 32);
+                };
+                if constexpr (kSums) {
+#pragma unroll
+                    for (int c = 0; c < kMost; c += 32)
+                        if (c < cols) add_up(c, reinterpret_cast<float (&)[32]>(f[c]));
+                } else if (wide) {
+#pragma unroll
+                    for (int c = 0; c < kMost; c += 32) {
+                        if (c >= cols) break;
+                        float r[32];
+                        add_up(c, r);
+                        round_off(c, r);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < cols; c += 16) {
+                        float r[16];
+                        add_up(c, r);
+                        st_narrow<E>(p, r, reinterpret_cast<float *>(own), m0, n0 + c, lane);
+                    }
+                }
+            }
             if constexpr (kSums) {
                 if (!wide) {
 #pragma unroll
@@ -653,23 +738,33 @@ bool encode_out(CUtensorMap &map, const MatmulParams &p) {
                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+cudaLaunchConfig_t cluster_launch(cudaLaunchAttribute &at, int64_t grid, int threads, int smem, int cluster, cudaStream_t stream) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cluster, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return c;
+}
+
 template <typename E, int BT>
-cudaError_t run_tile(MatmulArgs &args, int split, cudaStream_t stream) {
+cudaError_t run_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
     using S = TileShape<BT>;
     constexpr auto kernel = mm_tile_kernel<E, BT>;
-    cudaError_t e = allow_smem<kernel>(S::kSmem);
+    const cudaError_t e = allow_smem<kernel>(S::kSmem);
     if (e != cudaSuccess) return e;
-    if (!encode_operand(args.a, args.p.a, args.p.K, BT)) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)(ceil_div(args.p.b.rows, kRows) * ceil_div(args.p.a.rows, BT) * split));
-    c.blockDim = dim3(128);
-    c.dynamicSmemBytes = S::kSmem;
-    c.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = split, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
-    c.attrs = at;
-    c.numAttrs = 1;
+    const MatmulParams &p = args.p;
+    if (!encode_operand(args.a, p.a, p.K, BT) || !encode_operand(args.b, p.b, p.K, kRows)) return cudaErrorInvalidValue;
+    // as many parts of K as two CTAs per SM hold, of 4 blocks or more
+    const int64_t tiles = ceil_div(p.b.rows, kRows) * ceil_div(p.a.rows, BT), blocks = ceil_div(p.K, kFp8Block);
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= 2 * sms && blocks >= 8 * split) split *= 2;
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t c = cluster_launch(at, tiles * split, 128, S::kSmem, split, stream);
     return cudaLaunchKernelEx(&c, kernel, args, split);
 }
 
@@ -679,24 +774,60 @@ cudaError_t run_pair(MatmulArgs &args, int sms, cudaStream_t stream) {
     constexpr auto kernel = mm_pair_kernel<E, BN>;
     cudaError_t e = allow_smem<kernel>(S::kSmem);
     if (e != cudaSuccess) return e;
-    MatmulParams &p = args.p;
+    const MatmulParams &p = args.p;
     if (!encode_operand(args.a, p.a, p.K, kRows) || !encode_operand(args.b, p.b, p.K, BN / 2)) return cudaErrorInvalidValue;
     constexpr int V = 16 / sizeof(E);
     const int wide = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.os % V == 0 &&
                      (!p.add || (reinterpret_cast<uintptr_t>(p.add) % 16 == 0 && p.as % V == 0));
     if (wide && !encode_out(args.out, p)) return cudaErrorInvalidValue;
-    const int64_t tiles = ceil_div(p.a.rows, 2 * kRows) * ceil_div(p.b.rows, BN);
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3(2 * (unsigned)std::min(tiles, (int64_t)sms / 2));
-    c.blockDim = dim3(kPairThreads);
-    c.dynamicSmemBytes = S::kSmem;
-    c.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
-    c.attrs = at;
-    c.numAttrs = 1;
+    if (args.plan.split > 1 && (e = cudaMemsetAsync(args.plan.arrived, 0, args.plan.rest * 2 * kStoreWarps * 4, stream)) != cudaSuccess) return e;
+    cudaLaunchAttribute at;
+    const int64_t items = args.plan.full + args.plan.rest * args.plan.split;
+    const cudaLaunchConfig_t c = cluster_launch(at, 2 * std::min(items, (int64_t)sms / 2), kPairThreads, S::kSmem, 2, stream);
     return cudaLaunchKernelEx(&c, kernel, args, wide);
+}
+
+// How a product is computed: rows of a per tile (tile kernel) or of b (pair kernel), and the plan.
+struct Choice {
+    int bt, bn;
+    Plan plan;
+    size_t arrived_bytes, part_bytes;
+};
+// Time of a block of K of a pair's tile of BN rows of b, in ns (8192 x 8192 x 8192).
+int block_ns(int bn) { return bn == 128 ? 272 : bn == 192 ? 298 : 318; }
+
+Choice choose(const MatmulParams &p, int sms) {
+    Choice c = {};
+    if (p.a.rows <= 64) {
+        c.bt = p.a.rows <= 16 ? 16 : p.a.rows <= 32 ? 32 : 64;
+        return c;
+    }
+    const int64_t pairs = sms / 2, blocks = ceil_div(p.K, kFp8Block), groups = ceil_div(blocks, 4);
+    double best = 0;
+    const char *only = getenv("MM_BN"), *sp = getenv("MM_SPLIT");
+    for (int bn : {224, 192, 128}) {
+        if (only && atoi(only) != bn) continue;
+        const int64_t tiles = ceil_div(p.a.rows, 2 * kRows) * ceil_div(p.b.rows, bn), full = tiles / pairs * pairs, rest = tiles - full;
+        // the tiles of the last, partial round: whole, or shared by several pairs, which costs
+        // about 8 blocks' time for the parts' way through L2, and one for each part
+        const double t = block_ns(bn);
+        int split = 1;
+        double tail = rest ? blocks : 0;
+        for (int s = 2; rest && s <= pairs / rest && s <= groups / 2 && s <= 16; ++s) {
+            const double w = (double)blocks / s + 8 + s;
+            if (w < tail) tail = w, split = s;
+        }
+        if (sp && rest) split = atoi(sp);
+        const double cost = t * (full / pairs * blocks + tail);
+        if (c.bn && cost >= best) continue;
+        best = cost;
+        c.bn = bn;
+        c.plan = Plan{full, rest, split, nullptr, nullptr};
+        const int64_t most = (bn / 2 + 31) / 32 * 32;
+        c.arrived_bytes = split > 1 ? (size_t)ceil_div(rest * 2 * kStoreWarps * 4, 256) * 256 : 0;
+        c.part_bytes = split > 1 ? (size_t)(rest * split) * 2 * kStoreWarps * most * 32 * 4 : 0;
+    }
+    return c;
 }
 
 // out = add, where K is 0.
@@ -710,36 +841,34 @@ __global__ void __launch_bounds__(256) mm_add_kernel(MatmulParams p) {
 
 }  // namespace
 
-cudaError_t launch_matmul(const MatmulParams &p, int sms, cudaStream_t stream) {
+size_t matmul_scratch_bytes(const MatmulParams &p, int sms) {
+    if (p.K == 0) return 0;
+    const Choice c = choose(p, sms);
+    return c.arrived_bytes + c.part_bytes;
+}
+
+cudaError_t launch_matmul(const MatmulParams &p, unsigned char *ws, int sms, cudaStream_t stream) {
     return with_dtype(p.dtype, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
         if (p.K == 0) {
             mm_add_kernel<E><<<(unsigned)std::min(ceil_div(p.a.rows * p.b.rows, 256), (int64_t)sms * 8), 256, 0, stream>>>(p);
             return cudaGetLastError();
         }
+        const Choice c = choose(p, sms);
         MatmulArgs args;
         args.p = p;
-        if (!encode_operand(args.b, p.b, p.K, kRows)) return cudaErrorInvalidValue;
-        if (p.a.rows > 256) {
-            const char *bn = getenv("MM_BN");
-            switch (bn ? atoi(bn) : 224) {
-                case 128: return run_pair<E, 128>(args, sms, stream);
-                case 192: return run_pair<E, 192>(args, sms, stream);
-                case 256: return run_pair<E, 256>(args, sms, stream);
-                default: return run_pair<E, 224>(args, sms, stream);
-            }
+        args.plan = c.plan;
+        args.plan.arrived = reinterpret_cast<unsigned *>(ws);
+        args.plan.parts = reinterpret_cast<float *>(ws + c.arrived_bytes);
+        switch (c.bt) {
+            case 16: return run_tile<E, 16>(args, sms, stream);
+            case 32: return run_tile<E, 32>(args, sms, stream);
+            case 64: return run_tile<E, 64>(args, sms, stream);
         }
-        const int64_t M = p.a.rows, tiles = ceil_div(p.b.rows, kRows), blocks = ceil_div(p.K, kFp8Block);
-        const int bt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-        const int64_t all = tiles * ceil_div(M, bt);
-        int split = 1;
-        while (split < 8 && all * split < sms && blocks >= 8 * split) split *= 2;
-        switch (bt) {
-            case 16: return run_tile<E, 16>(args, split, stream);
-            case 32: return run_tile<E, 32>(args, split, stream);
-            case 64: return run_tile<E, 64>(args, split, stream);
-            case 128: return run_tile<E, 128>(args, split, stream);
-            default: return run_tile<E, 256>(args, split, stream);
+        switch (c.bn) {
+            case 128: return run_pair<E, 128>(args, sms, stream);
+            case 192: return run_pair<E, 192>(args, sms, stream);
+            default: return run_pair<E, 224>(args, sms, stream);
         }
     });
 }

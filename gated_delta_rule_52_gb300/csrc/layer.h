@@ -159,6 +159,7 @@ struct MatmulParams {
     int64_t K;
     int *err;
 };
-cudaError_t launch_matmul(const MatmulParams &p, int sms, cudaStream_t stream);
+size_t matmul_scratch_bytes(const MatmulParams &p, int sms);
+cudaError_t launch_matmul(const MatmulParams &p, unsigned char *ws, int sms, cudaStream_t stream);
 
 }  // namespace kda
