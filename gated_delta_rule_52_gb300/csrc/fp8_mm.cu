@@ -29,8 +29,8 @@ template <bool CLUSTER>
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint64_t limit = kWait) {
     uint64_t t0 = 0;
     for (uint32_t tries = 0;; ++tries) {
-        if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-        if (tries % 1024 == 1023) {
+        if (CLUSTER ? mbar_test_wait_cluster(bar, parity) : mbar_test_wait(bar, parity)) return true;
+        if (tries % 4096 == 4095) {
             const uint64_t now = globaltimer_ns();
             if (!t0) t0 = now;
             else if (now - t0 > limit) return false;
@@ -57,7 +57,7 @@ struct Slot {
 // Tiles of a pair kernel's call: the first `full` are one item of work each; each of the `rest`
 // after them is `split` items, equal parts of K, whose sums meet in the workspace.
 struct Plan {
-    int64_t full, rest;
+    uint32_t full, rest;
     int split;
     float *parts;          // [rest][split][2][kStoreWarps][kMost][32]
     unsigned *arrived;     // [rest][2][kStoreWarps], zero at the start
@@ -128,9 +128,11 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
     const MatmulParams &p = args.p;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = blockIdx.x % split;
-    const int64_t tile = blockIdx.x / split, across = ceil_div(p.b.rows, kRows), m0 = tile / across * BT, n0 = tile % across * kRows;
+    const uint32_t tile = blockIdx.x / split, across = (uint32_t)ceil_div(p.b.rows, kRows);
+    const int64_t m0 = (int64_t)(tile / across) * BT, n0 = (int64_t)(tile % across) * kRows;
     const int blocks = (int)ceil_div(p.K, kFp8Block);
-    const int k0 = (int)((int64_t)blocks * rank / split), k1 = (int)((int64_t)blocks * (rank + 1) / split);
+    const int each = blocks / split, more = blocks - each * split;
+    const int k0 = each * rank + min(rank, more), k1 = k0 + each + (rank < more);
     const int early = min(k1 - k0, S::kStages);        // loads that wait for nothing
     bool ok = true, issuer = false;
     const auto load = [&](int k, int at) {
@@ -301,10 +303,10 @@ struct PairShape {
 
 // Tile t of a grid of `down` x `across`: 8 tiles down, then across, so that the tiles in flight
 // share rows of both operands in L2.
-__device__ __forceinline__ void tile_at(int64_t t, int64_t down, int64_t across, int64_t &i, int64_t &j) {
-    const int64_t band = t / (8 * across), first = band * 8, high = min(down - first, (int64_t)8), in = t - band * 8 * across;
-    i = first + in % high;
+__device__ __forceinline__ void tile_at(uint32_t t, uint32_t down, uint32_t across, uint32_t &i, uint32_t &j) {
+    const uint32_t band = t / (8 * across), first = band * 8, high = min(down - first, 8u), in = t - band * 8 * across;
     j = in / high;
+    i = first + in - j * high;
 }
 
 // The first n of V neighbours (the others 0), in one load where all exist.
@@ -344,19 +346,20 @@ __device__ __forceinline__ void st_narrow(const MatmulParams &p, const float (&r
 
 // One item of a plan: blocks [k0, k1) of a tile.
 struct Item {
-    int64_t i, j, rest;    // the tile's place; its number among the shared ones, or -1
-    int k0, k1, part;
-    __device__ __forceinline__ Item(const Plan &plan, int64_t n, int64_t down, int64_t across, int blocks) {
-        int64_t t = n;
+    uint32_t i, j;         // the tile's place
+    int rest, part;        // its number among the shared ones, or -1, and which of its parts
+    int k0, k1;
+    __device__ __forceinline__ Item(const Plan &plan, uint32_t n, uint32_t down, uint32_t across, int blocks) {
+        uint32_t t = n;
         rest = -1, part = 0, k0 = 0, k1 = blocks;
-        if (n >= plan.full) {
-            rest = (n - plan.full) % plan.rest;
-            part = (int)((n - plan.full) / plan.rest);
+        if (plan.split > 1 && n >= plan.full) {
+            part = (n - plan.full) / plan.rest;
+            rest = n - plan.full - part * plan.rest;
             t = plan.full + rest;
-            if (plan.split == 1) rest = -1;
-            const int groups = (blocks + 3) / 4;     // parts begin at a group of 4 blocks
-            k0 = 4 * (int)((int64_t)groups * part / plan.split);
-            k1 = min(4 * (int)((int64_t)groups * (part + 1) / plan.split), blocks);
+            // a round number of groups of 4 blocks for each part, one more for the first ones
+            const int groups = (blocks + 3) / 4, each = groups / plan.split, more = groups - each * plan.split;
+            k0 = 4 * (each * part + min(part, more));
+            k1 = min(k0 + 4 * (each + (part < more)), blocks);
         }
         tile_at(t, down, across, i, j);
     }
@@ -376,8 +379,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const Plan &plan = args.plan;
-    const int64_t down = ceil_div(p.a.rows, 2 * kRows), across = ceil_div(p.b.rows, BN), items = plan.full + plan.rest * plan.split;
-    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const uint32_t down = (uint32_t)ceil_div(p.a.rows, 2 * kRows), across = (uint32_t)ceil_div(p.b.rows, BN), items = plan.full + plan.rest * plan.split;
+    const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int blocks = (int)ceil_div(p.K, kFp8Block);
     const int segment = kSums ? kSegment : blocks;
     if (threadIdx.x == 0) {
@@ -399,9 +402,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         Slot<S::kStages> slot;
         int loads = 0;
         const uint32_t bars = mapa_shared(smem_u32(full), 0);
-        for (int64_t t = pair; ok && t < items; t += pairs) {
+        for (uint32_t t = pair; ok && t < items; t += pairs) {
             const Item item(plan, t, down, across, blocks);
-            const int ra = (int)(item.i * 2 * kRows + rank * kRows), rb = (int)(item.j * BN + rank * (BN / 2));
+            const int ra = (int)(item.i * (2 * kRows) + rank * kRows), rb = (int)(item.j * BN + rank * (BN / 2));
             for (int k = item.k0; k < item.k1; ++k) {
                 // (a wait for the turn before the first returns at once)
                 if (!warp_wait<false>(&empty[slot.at], slot.turn ^ 1)) {
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         Slot<S::kBuffers> sum;
         const uint64_t a0 = sdesc_sw128(smem_u32(ring), 16, 1024), s0 = sdesc_plain(smem_u32(scales), 128);
         const uint32_t idesc = idesc_mx8(2 * kRows, BN, p.a.dtype == kE5M2, p.b.dtype == kE5M2, 0);
-        for (int64_t t = pair; ok && t < items; t += pairs) {
+        for (uint32_t t = pair; ok && t < items; t += pairs) {
             const Item item(plan, t, down, across, blocks);
             for (int k0 = item.k0; ok && k0 < item.k1; k0 += segment) {
                 if (!warp_wait<false>(&tempty[sum.at], sum.turn ^ 1)) {
@@ -467,7 +470,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                     const uint32_t id = idesc | (k & 3) << 4 | (uint32_t)(k & 3) << 29;
                     const int here = slot.at;
                     slot.next();
-                    ready = mbar_try_wait(&full[slot.at], slot.turn);   // its answer is looked at after the MMAs' issue
+                    ready = mbar_test_wait(&full[slot.at], slot.turn);   // its answer is looked at after the MMAs' issue
                     if (issuer) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) mma_mx8_pair(to, ad + 2 * q, bd + 2 * q, id, set, set + 4, k != k0 || q > 0);
@@ -484,7 +487,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         // their way, because a release for the cluster waits for all of a thread's
         Slot<kScaleStages> scale;
         const uint32_t bars = mapa_shared(smem_u32(sfull), 0);
-        for (int64_t t = pair; ok && t < items; t += pairs) {
+        for (uint32_t t = pair; ok && t < items; t += pairs) {
             const Item item(plan, t, down, across, blocks);
             for (int k = item.k0; k < item.k1; k += 4) {
                 ok = warp_wait<false>(&sfull[scale.at], scale.turn);
@@ -506,10 +509,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
             out.next();
             --waiting;
         };
-        for (int64_t t = pair; ok && t < items; t += pairs) {
+        for (uint32_t t = pair; ok && t < items; t += pairs) {
             const Item item(plan, t, down, across, blocks);
-            rows_a.set(p.a, item.i * 2 * kRows + rank * kRows, item.k0, lane);
-            rows_b.set(p.b, item.j * BN, item.k0, lane);
+            rows_a.set(p.a, (int64_t)item.i * (2 * kRows) + rank * kRows, item.k0, lane);
+            rows_b.set(p.b, (int64_t)item.j * BN, item.k0, lane);
             for (int k = item.k0; k < item.k1; k += 4) {
                 ok = warp_wait<false>(&sempty[in.at], in.turn ^ 1);
                 if (!ok) break;
@@ -536,13 +539,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         unsigned char *own = staging + (warp - 4) * kStoreBuffer;
         Slot<S::kBuffers> sum;
         const uint32_t bars = mapa_shared(smem_u32(tempty), 0);
-        for (int64_t t = pair; ok && t < items; t += pairs) {
+        for (uint32_t t = pair; ok && t < items; t += pairs) {
             const Item item(plan, t, down, across, blocks);
-            const int64_t m0 = item.i * 2 * kRows + rank * kRows + part * 32, n0 = item.j * BN + half * kMost;
+            const int64_t m0 = (int64_t)item.i * (2 * kRows) + rank * kRows + part * 32, n0 = (int64_t)item.j * BN + half * kMost;
             const int64_t left = p.b.rows - n0;              // columns of out from here on
             const E *plus = p.add ? static_cast<const E *>(p.add) + (m0 + lane) * p.as + n0 : nullptr;
             const bool my_row = m0 + lane < p.a.rows, shared = item.rest >= 0;
-            float *parts = shared ? plan.parts + (((item.rest * plan.split) * 2 + rank) * kStoreWarps + (warp - 4)) * (kMost * 32) + lane : nullptr;
+            float *parts = shared ? plan.parts + ((int64_t)(item.rest * plan.split * 2 + rank) * kStoreWarps + (warp - 4)) * (kMost * 32) + lane : nullptr;
             constexpr int kPart = 2 * kStoreWarps * kMost * 32;      // from one part of a tile to the next
             // this lane's row: fp32, or 16-bit values that begin as the addend's
             float f[kSums ? kMost : 1];
@@ -782,7 +785,7 @@ cudaError_t run_pair(MatmulArgs &args, int sms, cudaStream_t stream) {
     if (wide && !encode_out(args.out, p)) return cudaErrorInvalidValue;
     if (args.plan.split > 1 && (e = cudaMemsetAsync(args.plan.arrived, 0, args.plan.rest * 2 * kStoreWarps * 4, stream)) != cudaSuccess) return e;
     cudaLaunchAttribute at;
-    const int64_t items = args.plan.full + args.plan.rest * args.plan.split;
+    const int64_t items = args.plan.full + (int64_t)args.plan.rest * args.plan.split;
     const cudaLaunchConfig_t c = cluster_launch(at, 2 * std::min(items, (int64_t)sms / 2), kPairThreads, S::kSmem, 2, stream);
     return cudaLaunchKernelEx(&c, kernel, args, wide);
 }
@@ -822,7 +825,7 @@ Choice choose(const MatmulParams &p, int sms) {
         if (c.bn && cost >= best) continue;
         best = cost;
         c.bn = bn;
-        c.plan = Plan{full, rest, split, nullptr, nullptr};
+        c.plan = Plan{(uint32_t)full, (uint32_t)rest, split, nullptr, nullptr};
         const int64_t most = (bn / 2 + 31) / 32 * 32;
         c.arrived_bytes = split > 1 ? (size_t)ceil_div(rest * 2 * kStoreWarps * 4, 256) * 256 : 0;
         c.part_bytes = split > 1 ? (size_t)(rest * split) * 2 * kStoreWarps * most * 32 * 4 : 0;
