@@ -29,6 +29,17 @@ __device__ __forceinline__ int scale_byte(float top, bool e5m2) {
 // 1 / scale, from 2^-120 to 2^126.
 __device__ __forceinline__ float inverse_scale(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
 
+// Values times the inverse of a scale.
+template <int n>
+__device__ __forceinline__ void scale_n(float (&f)[n], float inv) {
+    const float2 s = both(inv);
+#pragma unroll
+    for (int j = 0; j < n; j += 2) {
+        const float2 t = sm103::mul2(make_float2(f[j], f[j + 1]), s);
+        f[j] = t.x, f[j + 1] = t.y;
+    }
+}
+
 // Two values to 8 bits each (a in the low byte), rounded to nearest even.
 template <bool E5M2>
 __device__ __forceinline__ uint32_t pair_to_fp8(float a, float b) {

@@ -16,106 +16,158 @@ using namespace layer;
 constexpr int kTile = kFp8Block;
 constexpr int kQuantThreads = 256;
 
-// Thread t: columns 8 (t % 16) .. + 7 of rows 64 h + 4 (t / 16) + i.
+// 8 neighbours as they are in memory, two 16-bit elements to a word.  Their magnitudes compare like
+// the integers that their bits are; with kShift added infinity and NaN leave the positive signed
+// numbers, so that a signed maximum passes over them.
+template <typename E>
+struct Eight {
+    static constexpr int kWords = sizeof(E) * 2;
+    static constexpr bool kPairs = sizeof(E) == 2;
+    static constexpr uint32_t kMask = kPairs ? 0x7fff7fffu : 0x7fffffffu;
+    static constexpr uint32_t kShift = std::is_same_v<E, __half> ? 0x04000400u : kPairs ? 0x00800080u : 0x00800000u;   // 0
+    static constexpr uint32_t kSigns = kPairs ? 0x80008000u : 0x80000000u;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void load(const E *p) {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4) {
+            const uint4 t = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint32_t *>(p) + i);
+            w[i] = t.x, w[i + 1] = t.y, w[i + 2] = t.z, w[i + 3] = t.w;
+        }
+    }
+    __device__ __forceinline__ void load(const E *p, int n) {   // the first n, zeros behind them
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j >= n) continue;
+            if constexpr (kPairs) w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[j] << (16 * (j & 1));
+            else w[j] = reinterpret_cast<const uint32_t *>(p)[j];
+        }
+    }
+    __device__ __forceinline__ void values(float (&f)[8]) const {
+        if constexpr (kPairs) {
+            unpack<E, 8>(*reinterpret_cast<const Pack<E, 8> *>(w), f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
+        }
+    }
+    __device__ __forceinline__ float value(int i, int j) const {   // element j of word i
+        if constexpr (std::is_same_v<E, __nv_bfloat16>) return __uint_as_float(j ? w[i] & 0xffff0000u : w[i] << 16);
+        else if constexpr (kPairs) return to_f(reinterpret_cast<const E *>(w)[2 * i + j]);
+        else return __uint_as_float(w[i]);
+    }
+    __device__ __forceinline__ uint32_t magnitude(int i) const { return (w[i] & kMask) + kShift; }
+};
+template <typename E>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    if constexpr (sizeof(E) == 2) return __vmaxs2(a, b);
+    else return (uint32_t)max((int)a, (int)b);
+}
+// The number that a shifted magnitude (of 16 bits: the low half of a word) is.
+template <typename E>
+__device__ __forceinline__ float number(uint32_t m) {
+    if constexpr (sizeof(E) == 2) return to_f(__builtin_bit_cast(E, (uint16_t)(m - (Eight<E>::kShift & 0xffffu))));
+    else return __uint_as_float(m - Eight<E>::kShift);
+}
+
+// Thread t: columns 8 (t % 16) .. + 7 of rows 64 h + 4 (t / 16) + i, kept as they are loaded.
 template <typename E, bool E5M2, bool WIDE>
-__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(QuantParams p) {
-    __shared__ float tops[8][kTile];
-    __shared__ float warp_top[kTile / 32];
+__global__ void __launch_bounds__(kQuantThreads, sizeof(E) == 2 ? 4 : 2) quantize_kernel(QuantParams p) {
+    using Group = Eight<E>;
+    constexpr int kWords = Group::kWords;
+    __shared__ uint32_t tops[8][kWords * 16];
+    __shared__ uint32_t warp_top[4];
     __shared__ uint8_t col_scale[kTile];
     __shared__ uint32_t turned[kTile * kTile / 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
-    const int64_t across = ceil_div(p.cols, kTile), br = blockIdx.x / across, bc = blockIdx.x - br * across;
-    const int64_t r0 = br * kTile, c0 = bc * kTile;
-    const int64_t c = c0 + 8 * cg;
-    const int cols = (int)min(max(p.cols - c, (int64_t)0), (int64_t)8);
-    float v[2][4][8];
+    const uint32_t across = (uint32_t)ceil_div(p.cols, kTile), br = blockIdx.x / across, bc = blockIdx.x - br * across;
+    const int64_t r0 = (int64_t)br * kTile, c0 = (int64_t)bc * kTile, c = c0 + 8 * cg;
+    const int cols = (int)min(max(p.cols - c, (int64_t)0), (int64_t)8), rows = (int)min(p.rows - r0, (int64_t)kTile);
+    Group v[2][4];
+    {
+        const E *at = static_cast<const E *>(p.x) + (r0 + 4 * rg) * p.xs + c;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 64 * h + 4 * rg + i, n = r < rows ? cols : 0;
+                if (WIDE && n == 8) v[h][i].load(at + (64 * h + i) * p.xs);
+                else v[h][i].load(at + (64 * h + i) * p.xs, n);
+            }
+    }
+    uint32_t row_top[2][4], col_top[kWords], any = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) col_top[w] = Group::kShift;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t r = r0 + 64 * h + 4 * rg + i;
-            const E *at = static_cast<const E *>(p.x) + r * p.xs + c;
+            uint32_t t = Group::kShift;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[h][i][j] = 0.f;
-            if (r < p.rows) {
-                constexpr int V = 16 / sizeof(E);
-                if (WIDE && cols == 8) {
-#pragma unroll
-                    for (int j = 0; j < 8; j += V) ld_f<E, V>(at + j, reinterpret_cast<float (&)[V]>(v[h][i][j]));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < cols) v[h][i][j] = to_f(at[j]);
-                }
+            for (int w = 0; w < kWords; ++w) {
+                const uint32_t m = v[h][i].magnitude(w);
+                any |= m;
+                t = larger<E>(t, m);
+                col_top[w] = larger<E>(col_top[w], m);
             }
+            row_top[h][i] = Group::kPairs ? larger<E>(t, t >> 16) : t;
         }
-    bool special = false;
-    float row_top[2][4], col_top[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) col_top[j] = 0.f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float t = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float a = finite_abs(v[h][i][j], special);
-                t = fmaxf(t, a);
-                col_top[j] = fmaxf(col_top[j], a);
-            }
-            row_top[h][i] = t;
-        }
+    const bool special = (any & Group::kSigns) != 0;   // this thread holds infinities or NaN
     if (p.qt || p.tile) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float t = fmaxf(col_top[j], __shfl_xor_sync(0xffffffffu, col_top[j], 16));
-            if (lane < 16) tops[warp][8 * cg + j] = t;
+        for (int w = 0; w < kWords; ++w) {
+            const uint32_t t = larger<E>(col_top[w], __shfl_xor_sync(0xffffffffu, col_top[w], 16));
+            if (lane < 16) tops[warp][cg * kWords + w] = t;
         }
         __syncthreads();
         if (threadIdx.x < kTile) {
-            float t = 0.f;
+            // column threadIdx.x: half a word of a 16-bit type
+            const int word = Group::kPairs ? threadIdx.x >> 1 : threadIdx.x;
+            uint32_t t = tops[0][word];
 #pragma unroll
-            for (int w = 0; w < 8; ++w) t = fmaxf(t, tops[w][threadIdx.x]);
+            for (int w = 1; w < 8; ++w) t = larger<E>(t, tops[w][word]);
+            if (Group::kPairs) t = threadIdx.x & 1 ? t >> 16 : t & 0xffffu;
             if (p.tile) {
-#pragma unroll
-                for (int o = 16; o; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+                t = __reduce_max_sync(0xffffffffu, t);   // positive: kShift or more
                 if (lane == 0) warp_top[warp] = t;
             } else {
-                col_scale[threadIdx.x] = (uint8_t)scale_byte(t, E5M2);
+                col_scale[threadIdx.x] = (uint8_t)scale_byte(number<E>(t), E5M2);
             }
         }
         __syncthreads();
     }
     int tile_scale = 0;
     if (p.tile) {
-        tile_scale = scale_byte(fmaxf(fmaxf(warp_top[0], warp_top[1]), fmaxf(warp_top[2], warp_top[3])), E5M2);
+        tile_scale = scale_byte(number<E>(max(max(warp_top[0], warp_top[1]), max(warp_top[2], warp_top[3]))), E5M2);
         if (threadIdx.x == 0) {
             if (p.q) p.s[br * p.ss + bc] = (uint8_t)tile_scale;
             if (p.qt) p.st[bc * p.sts + br] = (uint8_t)tile_scale;
         }
     }
     if (p.q) {
-        const bool whole = WIDE && cols == 8 && p.qs % 8 == 0 && reinterpret_cast<uintptr_t>(p.q) % 8 == 0;
+        const bool whole = cols == 8 && p.qs % 8 == 0 && reinterpret_cast<uintptr_t>(p.q) % 8 == 0;
+        uint8_t *first = static_cast<uint8_t *>(p.q) + (r0 + 4 * rg) * p.qs + c;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 int e = tile_scale;
                 if (!p.tile) {
-                    float t = row_top[h][i];
+                    uint32_t t = row_top[h][i];
 #pragma unroll
-                    for (int o = 8; o; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                    e = scale_byte(t, E5M2);
+                    for (int o = 8; o; o >>= 1) t = larger<E>(t, __shfl_xor_sync(0xffffffffu, t, o));
+                    e = scale_byte(number<E>(t), E5M2);
                 }
-                const int64_t r = r0 + 64 * h + 4 * rg + i;
-                if (r >= p.rows || cols == 0) continue;
-                if (!p.tile && cg == 0) p.s[r * p.ss + bc] = (uint8_t)e;
-                const float inv = inverse_scale(e);
+                const int r = 64 * h + 4 * rg + i;
+                if (r >= rows || cols == 0) continue;
+                if (!p.tile && cg == 0) p.s[(r0 + r) * p.ss + bc] = (uint8_t)e;
                 float f[8];
-                fma_n<8>(f, v[h][i], inv, 0.f);
+                v[h][i].values(f);
+                scale_n(f, inverse_scale(e));
                 const uint32_t lo = quad_to_fp8<E5M2>(f[0], f[1], f[2], f[3], special), hi = quad_to_fp8<E5M2>(f[4], f[5], f[6], f[7], special);
-                uint8_t *at = static_cast<uint8_t *>(p.q) + r * p.qs + c;
+                uint8_t *at = first + (64 * h + i) * p.qs;
                 if (whole) {
                     *reinterpret_cast<uint2 *>(at) = make_uint2(lo, hi);
                 } else {
@@ -129,26 +181,39 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(QuantParams p) 
     // four rows of a column are one word; word w of column c stands at place w + 2 (c / 8) of
     // its line, so that a warp's words lie in 32 banks
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int col = 8 * cg + j;
-        const float inv = inverse_scale(p.tile ? tile_scale : col_scale[col]);
+    for (int w = 0; w < kWords; ++w) {
+        constexpr int n = Group::kPairs ? 2 : 1;          // columns of a word
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            turned[col * 32 + ((16 * h + rg + 2 * cg) & 31)] =
-                quad_to_fp8<E5M2>(v[h][0][j] * inv, v[h][1][j] * inv, v[h][2][j] * inv, v[h][3][j] * inv, special);
+        for (int j = 0; j < n; ++j) {
+            const int col = 8 * cg + n * w + j;
+            const float inv = inverse_scale(p.tile ? tile_scale : col_scale[col]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                turned[col * 32 + ((16 * h + rg + 2 * cg) & 31)] =
+                    quad_to_fp8<E5M2>(v[h][0].value(w, j) * inv, v[h][1].value(w, j) * inv, v[h][2].value(w, j) * inv, v[h][3].value(w, j) * inv, special);
+        }
     }
     __syncthreads();
-    const bool words = p.qts % 4 == 0 && reinterpret_cast<uintptr_t>(p.qt) % 4 == 0;
-    const int rows = (int)min(p.rows - r0 - 4 * lane, (int64_t)4);
-    for (int col = warp; col < kTile && c0 + col < p.cols; col += 8) {
-        const uint32_t w = turned[col * 32 + ((lane + 2 * (col >> 3)) & 31)];
-        uint8_t *at = static_cast<uint8_t *>(p.qt) + (c0 + col) * p.qts + r0 + 4 * lane;
-        if (words && rows == 4) {
-            *reinterpret_cast<uint32_t *>(at) = w;
+    // 8 lanes to a column, 16 rows each
+    const bool words = p.qts % 16 == 0 && reinterpret_cast<uintptr_t>(p.qt) % 16 == 0;
+    const int w0 = 4 * (lane & 7), n = min(rows - 4 * w0, 16);
+#pragma unroll
+    for (int k = 0; k < kTile / 32; ++k) {
+        const int col = 32 * k + 4 * warp + (lane >> 3);
+        if (c0 + col >= p.cols) continue;
+        const int turn = 2 * (col >> 3);
+        const uint2 a = *reinterpret_cast<const uint2 *>(&turned[col * 32 + ((w0 + turn) & 31)]);
+        const uint2 b = *reinterpret_cast<const uint2 *>(&turned[col * 32 + ((w0 + 2 + turn) & 31)]);
+        uint8_t *at = static_cast<uint8_t *>(p.qt) + (c0 + col) * p.qts + r0 + 4 * w0;
+        if (words && n == 16) {
+            *reinterpret_cast<uint4 *>(at) = make_uint4(a.x, a.y, b.x, b.y);
         } else {
-            for (int j = 0; j < rows; ++j) at[j] = (uint8_t)(w >> (8 * j));
+            const uint32_t t[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (j < n) at[j] = (uint8_t)(t[j / 4] >> (8 * (j & 3)));
         }
-        if (!p.tile && lane == 0) p.st[(c0 + col) * p.sts + br] = col_scale[col];
+        if (!p.tile && (lane & 7) == 0) p.st[(c0 + col) * p.sts + br] = col_scale[col];
     }
 }
 

@@ -6,8 +6,14 @@
 // what the output belongs to, and the backward pass starts from it.  8-bit outputs have a scale
 // for each block of 128 columns (fp8_io.cuh).
 //
-// A CTA takes a row; a warp takes blocks of 128 columns of it, 4 columns to a lane.
+// Both directions move each value once.  Forward, the threads blockDim.x share a row (blockDim.y
+// rows per CTA), each with 8 to 32 of its elements in registers from the load to the store.
+// Backward, CTAs are persistent: a thread's columns stay the same, so that its weights and their
+// gradients stay in registers, and the next rows are on their way into shared memory.  Rows that
+// are not aligned, or too long for registers, take kernels of their own.
 #include <algorithm>
+#include <initializer_list>
+#include <utility>
 
 #include "fp8_io.cuh"
 #include "layer_copy.cuh"
@@ -31,6 +37,232 @@ __device__ __forceinline__ float cta_sum(float v, float (&part)[32]) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+
+// ---- rows in registers: N groups of V = 16 bytes to a thread, neighbouring threads side by side
+
+// Sum over the blockDim.x threads of every row of the CTA; all threads of the CTA call it together.
+__device__ __forceinline__ float row_sum(float v, float (&part)[32]) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return v;
+    const int first = threadIdx.y * warps, lane = threadIdx.x & 31;
+    if (lane == 0) part[first + (threadIdx.x >> 5)] = v;
+    __syncthreads();
+    v = lane < warps ? part[first + lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <int V>
+__device__ __forceinline__ int column(int k) { return (k * blockDim.x + threadIdx.x) * V; }
+
+// A group of 8-bit outputs: V values that with those of the 128 / V threads around make a block.
+template <bool E5M2, int V>
+__device__ __forceinline__ void st_group_fp8(uint8_t *at, uint8_t *scale, float (&f)[V], bool in) {
+    bool special = false;
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) top = fmaxf(top, finite_abs(f[j], special));
+#pragma unroll
+    for (int o = 64 / V; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (!in) return;
+    const int e = scale_byte(top, E5M2);
+    if (threadIdx.x % (128 / V) == 0) *scale = (uint8_t)e;
+    scale_n(f, inverse_scale(e));
+    Pack<uint32_t, V / 4> w;
+#pragma unroll
+    for (int j = 0; j < V; j += 4) w.e[j / 4] = quad_to_fp8<E5M2>(f[j], f[j + 1], f[j + 2], f[j + 3], special);
+    *reinterpret_cast<Pack<uint32_t, V / 4> *>(at) = w;
+}
+
+// OUT: 0 = out in E, 4, 5 = in 8 bits (kE4M3, kE5M2).
+template <typename E, int EL, int OUT>
+__global__ void __launch_bounds__(512) rms_fwd_row_kernel(RmsParams p) {
+    constexpr int V = 16 / sizeof(E), N = EL / V;
+    __shared__ float part[32];
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int D = row < p.rows ? (int)p.D : 0;            // rows behind the last take part in the barriers only
+    const E *x = static_cast<const E *>(p.x) + row * p.xs;
+    Pack<E, V> h[N], r[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (column<V>(k) < D) h[k] = ld_pack<E, V>(x + column<V>(k));
+    if (p.res) {
+        const E *res = static_cast<const E *>(p.res) + row * p.rs;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (column<V>(k) < D) r[k] = ld_pack<E, V>(res + column<V>(k));
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            float a[V], b[V];
+            unpack<E, V>(h[k], a);
+            unpack<E, V>(r[k], b);
+            add_n<V>(a, a, b);
+            st_f<E, V>(h[k].e, a);
+        }
+        if (p.res_out) {
+            E *sum = static_cast<E *>(p.res_out) + row * p.ros;
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (column<V>(k) < D) *reinterpret_cast<Pack<E, V> *>(sum + column<V>(k)) = h[k];
+        }
+    }
+    float s[V], t = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if (column<V>(k) >= D) continue;
+        float a[V];
+        unpack<E, V>(h[k], a);
+        fma_n<V>(s, a, a, s);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) t += s[j];
+    const float rstd = 1.f / sqrtf(row_sum(t, part) / (float)(int)p.D + p.eps);
+    if (threadIdx.x == 0 && D && p.rstd) p.rstd[row] = rstd;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int c = column<V>(k);
+        const bool in = c < D;
+        if (OUT == 0 && !in) continue;
+        float a[V], w[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) a[j] = 0.f;
+        if (in) {
+            unpack<E, V>(h[k], a);
+            scale_n(a, rstd);
+            if (p.weight) {
+#pragma unroll
+                for (int j = 0; j < V; j += 4) ld_f<float, 4>(p.weight + c + j, reinterpret_cast<float (&)[4]>(w[j]));
+                mul_n<V>(a, a, w);
+            }
+        }
+        if constexpr (OUT == 0) st_f<E, V>(static_cast<E *>(p.out) + row * p.os + c, a);
+        else st_group_fp8<OUT == kE5M2, V>(static_cast<uint8_t *>(p.out) + row * p.os + c, p.scales + row * p.ss + c / kFp8Block, a, in);
+    }
+}
+
+// ---- backward, persistent
+constexpr int kBwdThreads = 512;
+// Rows of a thread in its ring: up to 4, in 192 KB.
+template <typename E, int EL>
+constexpr int kBwdStages = std::min(4, 192 * 1024 / (kBwdThreads * EL * 3 * (int)sizeof(E)));
+
+template <typename E, int EL>
+__global__ void __launch_bounds__(kBwdThreads, 1) rms_bwd_row_kernel(RmsParams p, float *part_out) {
+    constexpr int V = 16 / sizeof(E), N = EL / V, kStages = kBwdStages<E, EL>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float part[2][32];
+    const int D = (int)p.D, threads = blockDim.x * blockDim.y, me = threadIdx.y * blockDim.x + threadIdx.x, tensors = p.dres ? 3 : 2;
+    const float inv = 1.f / (float)D;
+    // slot of group k of a tensor in a stage
+    Pack<E, V> *ring = reinterpret_cast<Pack<E, V> *>(smem) + me;
+    const auto slot = [&](int stage, int tensor, int k) { return ring + ((stage * 3 + tensor) * N + k) * threads; };
+    const int64_t step = (int64_t)gridDim.x * blockDim.y, first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int64_t turns = ceil_div(p.rows - (int64_t)blockIdx.x * blockDim.y, step);   // of every row of the CTA
+    const auto request = [&](int64_t turn, int stage) {
+        const int64_t row = first + turn * step;
+        if (turn < turns && row < p.rows) {
+            const E *from[3] = {static_cast<const E *>(p.x) + row * p.xs, static_cast<const E *>(p.dout) + row * p.ds,
+                                static_cast<const E *>(p.dres) + row * p.drs};
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+                if (t >= tensors) break;
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    if (column<V>(k) < D) copy_async<16>(slot(stage, t, k), from[t] + column<V>(k));
+            }
+        }
+        copies_commit();
+    };
+    float w[EL], dw[EL];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = column<V>(k) + j;
+            w[k * V + j] = p.weight && c < D ? p.weight[c] : 1.f;
+            dw[k * V + j] = 0.f;
+        }
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) request(i, i);
+    int stage = 0;
+    for (int64_t turn = 0; turn < turns; ++turn) {
+        request(turn + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+        copies_wait<kStages - 1>();
+        const int64_t row = first + turn * step;
+        const bool real = row < p.rows;
+        const float rstd = real ? p.rstd[row] : 0.f;
+        float s[V], t = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] = 0.f;
+        float hat[EL], d[EL];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            float (&h)[V] = reinterpret_cast<float (&)[V]>(hat[k * V]), (&g)[V] = reinterpret_cast<float (&)[V]>(d[k * V]);
+            float (&ww)[V] = reinterpret_cast<float (&)[V]>(w[k * V]), (&dd)[V] = reinterpret_cast<float (&)[V]>(dw[k * V]);
+            if (real && column<V>(k) < D) {
+                unpack<E, V>(*slot(stage, 0, k), h);
+                unpack<E, V>(*slot(stage, 1, k), g);
+                scale_n(h, rstd);
+                fma_n<V>(dd, g, h, dd);
+                mul_n<V>(g, g, ww);
+                fma_n<V>(s, g, h, s);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) h[j] = g[j] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) t += s[j];
+        const float mean = row_sum(t, part[turn & 1]) * inv;
+        if (real) {
+            E *dx = static_cast<E *>(p.dx) + row * p.D;
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                if (column<V>(k) >= D) continue;
+                float f[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) f[j] = fmaf(-mean, hat[k * V + j], d[k * V + j]);
+                scale_n(f, rstd);
+                if (p.dres) {
+                    float a[V];
+                    unpack<E, V>(*slot(stage, 2, k), a);
+                    add_n<V>(f, f, a);
+                }
+                st_f<E, V>(dx + column<V>(k), f);
+            }
+        }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    copies_wait<0>();
+    if (!part_out) return;
+    // over the CTA's rows side by side, one after the other
+    float *sums = reinterpret_cast<float *>(smem);   // [EL][blockDim.x], over the ring
+    for (int y = 0; y < (int)blockDim.y; ++y) {
+        __syncthreads();
+        if ((int)threadIdx.y != y) continue;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+            float *at = sums + e * blockDim.x + threadIdx.x;
+            if (y > 0) dw[e] += *at;
+            if (y + 1 < (int)blockDim.y) *at = dw[e];
+        }
+    }
+    if (threadIdx.y == blockDim.y - 1) {
+        float *at = part_out + (int64_t)blockIdx.x * p.D;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+            const int c = column<V>(e / V) + e % V;
+            if (c < D) at[c] = dw[e];
+        }
+    }
+}
+
+// ---- rows that are not aligned, or too long for registers: a warp takes blocks of 128 columns, 4
+// columns to a lane, and passes over them twice (the second time through L1 and L2)
 
 // A lane's 4 columns of a block: neighbours where rows are aligned, else 32 apart.
 template <bool WIDE>
@@ -184,38 +416,90 @@ __global__ void __launch_bounds__(kSumThreads) rms_weight_sum_kernel(RmsParams p
     if (threadIdx.x < 32 && c < p.D) p.dweight[c] = t;
 }
 
-// Groups of 4 elements where every row allows them.
-bool wide_rows(const RmsParams &p, std::initializer_list<std::pair<const void *, int64_t>> tensors) {
-    const size_t group = 4 * dtype_bytes(p.dtype);
+// Groups of n elements where every row allows them.
+bool aligned_rows(const RmsParams &p, int n, std::initializer_list<std::pair<const void *, int64_t>> tensors) {
+    const size_t bytes = n * dtype_bytes(p.dtype);
     for (const auto &t : tensors)
-        if (t.first && (reinterpret_cast<uintptr_t>(t.first) % group || t.second % 4)) return false;
+        if (t.first && (reinterpret_cast<uintptr_t>(t.first) % bytes || t.second % n)) return false;
     return reinterpret_cast<uintptr_t>(p.weight) % 16 == 0;
 }
+dim3 row_block(int64_t D, int el, int most) {
+    const int x = (int)(ceil_div(D, 32 * el) * 32);
+    return dim3(x, x >= most ? 1 : most / x);
+}
 
-int64_t weight_parts(const RmsParams &p) { return std::min(ceil_div(p.rows, 64), (int64_t)256); }
+constexpr int64_t kFwdMaxD = 16384, kBwdMaxD = 8192;
+
+bool fwd_in_registers(const RmsParams &p) {
+    const int V = 16 / (int)dtype_bytes(p.dtype);
+    return p.D <= kFwdMaxD && p.D % V == 0 && aligned_rows(p, V, {{p.x, p.xs}, {p.res, p.rs}, {p.res_out, p.ros}}) &&
+           (p.out_dtype == p.dtype ? aligned_rows(p, V, {{p.out, p.os}})
+                                   : reinterpret_cast<uintptr_t>(p.out) % V == 0 && p.os % V == 0);
+}
+bool bwd_in_registers(const RmsParams &p) {
+    const int V = 16 / (int)dtype_bytes(p.dtype);
+    return p.D <= kBwdMaxD && p.D % V == 0 && aligned_rows(p, V, {{p.x, p.xs}, {p.dout, p.ds}, {p.dres, p.drs}, {p.dx, p.D}});
+}
+int bwd_el(const RmsParams &p) { return p.D <= kBwdThreads * 8 ? 8 : 16; }
+int64_t bwd_grid(const RmsParams &p, int sms) {
+    return std::min(ceil_div(p.rows, (int64_t)row_block(p.D, bwd_el(p), kBwdThreads).y), (int64_t)sms);
+}
+int64_t weight_parts(const RmsParams &p, int sms) {
+    if (p.rows == 0) return 0;
+    return bwd_in_registers(p) ? bwd_grid(p, sms) : std::min(ceil_div(p.rows, 64), (int64_t)256);
+}
+
+template <typename E, int EL>
+cudaError_t run_fwd(const RmsParams &p, cudaStream_t stream) {
+    const dim3 block = row_block(p.D, EL, 256);
+    const unsigned grid = (unsigned)ceil_div(p.rows, (int64_t)block.y);
+    if (p.out_dtype == p.dtype) rms_fwd_row_kernel<E, EL, 0><<<grid, block, 0, stream>>>(p);
+    else if (p.out_dtype == kE4M3) rms_fwd_row_kernel<E, EL, kE4M3><<<grid, block, 0, stream>>>(p);
+    else rms_fwd_row_kernel<E, EL, kE5M2><<<grid, block, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename E, int EL>
+cudaError_t run_bwd(const RmsParams &p, float *part, int sms, cudaStream_t stream) {
+    const dim3 block = row_block(p.D, EL, kBwdThreads);
+    const int threads = block.x * block.y, smem = std::max(threads * EL * 3 * kBwdStages<E, EL> * (int)sizeof(E), (int)block.x * EL * 4);
+    constexpr auto kernel = rms_bwd_row_kernel<E, EL>;
+    const cudaError_t e = allow_smem<kernel>(kBwdThreads * EL * 3 * kBwdStages<E, EL> * (int)sizeof(E));
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)bwd_grid(p, sms), block, smem, stream>>>(p, part);
+    return cudaGetLastError();
+}
 
 }  // namespace
 
-size_t rms_bwd_scratch_bytes(const RmsParams &p, int) { return p.dweight ? (size_t)(weight_parts(p) * p.D) * sizeof(float) : 0; }
+size_t rms_bwd_scratch_bytes(const RmsParams &p, int sms) { return p.dweight ? (size_t)(weight_parts(p, sms) * p.D) * sizeof(float) : 0; }
 
-cudaError_t launch_rms_fwd(const RmsParams &p, int, cudaStream_t stream) {
+cudaError_t launch_rms_fwd(const RmsParams &p, int sms, cudaStream_t stream) {
     return with_dtype(p.dtype, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
-        const bool wide = wide_rows(p, {{p.x, p.xs}, {p.res, p.rs}, {p.res_out, p.ros}}) &&
-                          (p.out_dtype != p.dtype || wide_rows(p, {{p.out, p.os}}));
+        if (fwd_in_registers(p)) {
+            // elements per thread: a warp to a short row; of longer ones many, or few where few
+            // rows leave most of the GPU idle
+            if (p.D <= 256 || (p.rows <= 4 * sms && p.D <= 4096)) return run_fwd<E, 8>(p, stream);
+            if (p.D <= 512 || (p.rows <= 4 * sms && p.D <= 8192)) return run_fwd<E, 16>(p, stream);
+            return run_fwd<E, 32>(p, stream);
+        }
+        const bool wide = aligned_rows(p, 4, {{p.x, p.xs}, {p.res, p.rs}, {p.res_out, p.ros}}) &&
+                          (p.out_dtype != p.dtype || aligned_rows(p, 4, {{p.out, p.os}}));
         if (wide) rms_fwd_kernel<E, true><<<(unsigned)p.rows, kRowThreads, 0, stream>>>(p);
         else rms_fwd_kernel<E, false><<<(unsigned)p.rows, kRowThreads, 0, stream>>>(p);
         return cudaGetLastError();
     });
 }
 
-cudaError_t launch_rms_bwd(const RmsParams &p, unsigned char *ws, int, cudaStream_t stream) {
-    float *part = reinterpret_cast<float *>(ws);
-    const int64_t parts = weight_parts(p);
+cudaError_t launch_rms_bwd(const RmsParams &p, unsigned char *ws, int sms, cudaStream_t stream) {
+    float *part = p.dweight ? reinterpret_cast<float *>(ws) : nullptr;
+    const int64_t parts = weight_parts(p, sms);
     const cudaError_t e = with_dtype(p.dtype, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
         if (p.rows == 0) return cudaSuccess;
-        if (wide_rows(p, {{p.x, p.xs}, {p.dout, p.ds}, {p.dres, p.drs}, {p.dx, p.D}}))
+        if (bwd_in_registers(p)) return bwd_el(p) == 8 ? run_bwd<E, 8>(p, part, sms, stream) : run_bwd<E, 16>(p, part, sms, stream);
+        if (aligned_rows(p, 4, {{p.x, p.xs}, {p.dout, p.ds}, {p.dres, p.drs}, {p.dx, p.D}}))
             rms_bwd_kernel<E, true><<<(unsigned)p.rows, kRowThreads, 0, stream>>>(p);
         else rms_bwd_kernel<E, false><<<(unsigned)p.rows, kRowThreads, 0, stream>>>(p);
         if (p.dweight)

@@ -138,6 +138,36 @@ def test_quantize(rows, cols, dt, to, how, tile):
         assert torch.equal(back.cpu().double(), want), name
 
 
+@pytest.mark.parametrize("to", [E4, E5])
+@pytest.mark.parametrize("dt", [BF, HF, F])
+def test_quantize_what_is_not_finite(dt, to):
+    """Infinities and NaN take no part in a scale and stay in their places; blocks of nothing
+    else; magnitudes below the normal numbers."""
+    g = _gen(7)
+    x = torch.randn(140, 300, generator=g).to(dt)
+    inf, nan = float("inf"), float("nan")
+    x[0, 5], x[1, 130], x[2, 299], x[130, 0] = inf, -inf, nan, -nan
+    x[3], x[4, :128], x[5, 128:] = nan, inf, -inf
+    x[:, 77] = inf
+    x[6] = 0
+    if dt != HF:
+        x[8, :128] = 2.0 ** -128                                # in e5m2 and e4m3 below a scale's reach: 0
+    if dt == F:
+        x[9, :128] = torch.randn(128, generator=g) * 2.0 ** -120
+    q, s = fp8.empty(140, 300, to)
+    qt, st = fp8.empty(300, 140, to)
+    fp8.quantize(x.cuda(), q, s, qt=qt, scales_t=st)
+    tq, ts = fp8.empty(140, 300, to, True)
+    fp8.quantize(x.cuda(), tq, ts, tile=True)
+    _status()
+    z = torch.where(x.abs() < 2.0 ** -126, 0, x).double()       # what is not normal counts as 0
+    for name, got, gs, src, tile in (("q", q, s, z, False), ("qt", qt, st, z.T, False), ("tile", tq, ts, z, True)):
+        want, e = ref.quantized(src, to, tile)
+        assert torch.equal(gs.cpu().view(torch.uint8), ref.bytes_of(e)), name
+        have = ref.values(got, gs)
+        assert torch.equal(have.isnan(), want.isnan()) and torch.equal(have.nan_to_num(nan=0, posinf=inf), want.nan_to_num(nan=0, posinf=inf)), name
+
+
 # ------------------------------------------------------------------ norm
 def _close8(name, q, s, y, err):
     """8-bit values of y, known to within err: the scale of some block within that, and the
@@ -155,7 +185,10 @@ RMS = [  # rows, D, dtype, out8, residual, weight, how
     (1, 1, BF, None, False, True, "dense"), (2, 128, BF, E4, True, True, "dense"), (3, 130, HF, E5, True, True, "dense"),
     (5, 1000, F, E4, False, True, "slice"), (4, 2048, BF, None, True, True, "slice"), (7, 777, BF, E4, True, False, "odd"),
     (2, 8192, BF, E4, True, True, "dense"), (3, 1537, HF, None, False, True, "odd"), (2, 16385, F, None, True, True, "dense"),
-    (2, 20000, BF, E4, True, True, "dense"), (33, 64, F, None, True, False, "dense"), (700, 512, BF, E5, True, True, "dense"),
+    (2, 20000, BF, E4, True, True, "dense"), (9, 136, BF, E4, True, True, "slice"), (17, 264, BF, E5, False, True, "dense"),
+    (11, 1096, HF, E4, True, True, "dense"), (5, 4100, F, E4, True, True, "dense"), (3, 16384, BF, E4, True, True, "dense"),
+    (600, 8192, BF, E5, True, True, "dense"), (400, 520, F, None, True, True, "dense"), (1000, 8184, BF, None, False, False, "dense"),
+    (170, 7000, F, None, True, True, "dense"), (33, 64, F, None, True, False, "dense"), (700, 512, BF, E5, True, True, "dense"),
 ]
 
 
