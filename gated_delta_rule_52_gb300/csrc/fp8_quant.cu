@@ -62,8 +62,10 @@ struct Eight {
 };
 template <typename E>
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
-    if constexpr (sizeof(E) == 2) return __vmaxs2(a, b);
-    else return (uint32_t)max((int)a, (int)b);
+    uint32_t r;
+    if constexpr (sizeof(E) == 2) asm("max.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else r = (uint32_t)max((int)a, (int)b);
+    return r;
 }
 // The number that a shifted magnitude (of 16 bits: the low half of a word) is.
 template <typename E>

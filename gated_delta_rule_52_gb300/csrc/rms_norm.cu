@@ -144,37 +144,41 @@ __global__ void __launch_bounds__(512) rms_fwd_row_kernel(RmsParams p) {
     }
 }
 
-// ---- backward, persistent
+// ---- backward, persistent: blockDim.y rows at once, each with a ring and a barrier of its own, so
+// that one row's sums form while another is stored
+
 constexpr int kBwdThreads = 512;
-// Rows of a thread in its ring: up to 4, in 192 KB.
-template <typename E, int EL>
-constexpr int kBwdStages = std::min(4, 192 * 1024 / (kBwdThreads * EL * 3 * (int)sizeof(E)));
+// Most elements per thread, and rows in its ring (up to 4, in 192 KB).
+template <typename E> constexpr int kBwdMost = sizeof(E) == 4 ? 16 : 32;
+template <typename E, int EL> constexpr int kBwdStages = std::min(4, 192 * 1024 / (kBwdThreads * EL * 3 * (int)sizeof(E)));
 
 template <typename E, int EL>
 __global__ void __launch_bounds__(kBwdThreads, 1) rms_bwd_row_kernel(RmsParams p, float *part_out) {
     constexpr int V = 16 / sizeof(E), N = EL / V, kStages = kBwdStages<E, EL>;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float part[2][32];
-    const int D = (int)p.D, threads = blockDim.x * blockDim.y, me = threadIdx.y * blockDim.x + threadIdx.x, tensors = p.dres ? 3 : 2;
+    const int D = (int)p.D, threads = blockDim.x * blockDim.y, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const bool more = p.dres != nullptr;
     const float inv = 1.f / (float)D;
-    // slot of group k of a tensor in a stage
-    Pack<E, V> *ring = reinterpret_cast<Pack<E, V> *>(smem) + me;
-    const auto slot = [&](int stage, int tensor, int k) { return ring + ((stage * 3 + tensor) * N + k) * threads; };
-    const int64_t step = (int64_t)gridDim.x * blockDim.y, first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int64_t turns = ceil_div(p.rows - (int64_t)blockIdx.x * blockDim.y, step);   // of every row of the CTA
-    const auto request = [&](int64_t turn, int stage) {
-        const int64_t row = first + turn * step;
-        if (turn < turns && row < p.rows) {
-            const E *from[3] = {static_cast<const E *>(p.x) + row * p.xs, static_cast<const E *>(p.dout) + row * p.ds,
-                                static_cast<const E *>(p.dres) + row * p.drs};
+    // group k of tensor t of stage s is ring[((3 s + t) N + k) threads]
+    Pack<E, V> *ring = reinterpret_cast<Pack<E, V> *>(smem) + threadIdx.y * blockDim.x + threadIdx.x;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    int64_t ahead = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;      // the next row to ask for
+    const auto request = [&](int stage) {
+        if (ahead < p.rows) {
+            const E *h = static_cast<const E *>(p.x) + ahead * p.xs, *g = static_cast<const E *>(p.dout) + ahead * p.ds;
+            const E *r = static_cast<const E *>(p.dres) + ahead * p.drs;
+            Pack<E, V> *to = ring + stage * 3 * N * threads;
 #pragma unroll
-            for (int t = 0; t < 3; ++t) {
-                if (t >= tensors) break;
-#pragma unroll
-                for (int k = 0; k < N; ++k)
-                    if (column<V>(k) < D) copy_async<16>(slot(stage, t, k), from[t] + column<V>(k));
+            for (int k = 0; k < N; ++k) {
+                const int c = column<V>(k);
+                if (c >= D) continue;
+                copy_async<16>(to + k * threads, h + c);
+                copy_async<16>(to + (N + k) * threads, g + c);
+                if (more) copy_async<16>(to + (2 * N + k) * threads, r + c);
             }
         }
+        ahead += step;
         copies_commit();
     };
     float w[EL], dw[EL];
@@ -187,53 +191,67 @@ __global__ void __launch_bounds__(kBwdThreads, 1) rms_bwd_row_kernel(RmsParams p
             dw[k * V + j] = 0.f;
         }
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) request(i, i);
-    int stage = 0;
-    for (int64_t turn = 0; turn < turns; ++turn) {
-        request(turn + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+    for (int i = 0; i < kStages - 1; ++i) request(i);
+    int stage = 0, turn = 0;
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    float next = row < p.rows ? p.rstd[row] : 0.f;
+    for (; row < p.rows; row += step) {
+        request(stage == 0 ? kStages - 1 : stage - 1);
+        const float rstd = next;
+        if (row + step < p.rows) next = p.rstd[row + step];
         copies_wait<kStages - 1>();
-        const int64_t row = first + turn * step;
-        const bool real = row < p.rows;
-        const float rstd = real ? p.rstd[row] : 0.f;
+        const Pack<E, V> *at = ring + stage * 3 * N * threads;
         float s[V], t = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) s[j] = 0.f;
-        float hat[EL], d[EL];
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            float (&h)[V] = reinterpret_cast<float (&)[V]>(hat[k * V]), (&g)[V] = reinterpret_cast<float (&)[V]>(d[k * V]);
+            if (column<V>(k) >= D) continue;
+            float h[V], g[V];
             float (&ww)[V] = reinterpret_cast<float (&)[V]>(w[k * V]), (&dd)[V] = reinterpret_cast<float (&)[V]>(dw[k * V]);
-            if (real && column<V>(k) < D) {
-                unpack<E, V>(*slot(stage, 0, k), h);
-                unpack<E, V>(*slot(stage, 1, k), g);
-                scale_n(h, rstd);
-                fma_n<V>(dd, g, h, dd);
-                mul_n<V>(g, g, ww);
-                fma_n<V>(s, g, h, s);
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) h[j] = g[j] = 0.f;
-            }
+            unpack<E, V>(at[k * threads], h);
+            unpack<E, V>(at[(N + k) * threads], g);
+            scale_n(h, rstd);
+            fma_n<V>(dd, g, h, dd);
+            mul_n<V>(g, g, ww);
+            fma_n<V>(s, g, h, s);
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) t += s[j];
-        const float mean = row_sum(t, part[turn & 1]) * inv;
-        if (real) {
-            E *dx = static_cast<E *>(p.dx) + row * p.D;
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                if (column<V>(k) >= D) continue;
+        for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (warps > 1) {
+            float *sums = part[turn] + threadIdx.y * warps;
+            if (lane == 0) sums[threadIdx.x >> 5] = t;
+            sm103::named_bar(1 + threadIdx.y, blockDim.x);
+            t = lane < warps ? sums[lane] : 0.f;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            turn ^= 1;
+        }
+        // dx = rstd d - (rstd^2 mean) h + dresidual
+        const float mean = t * inv, c2 = -rstd * rstd * mean;
+        E *dx = static_cast<E *>(p.dx) + row * p.D;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (column<V>(k) >= D) continue;
+            float h[V], g[V];
+            unpack<E, V>(at[k * threads], h);
+            unpack<E, V>(at[(N + k) * threads], g);
+            scale_n(h, c2);
+            if (more) {
                 float f[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) f[j] = fmaf(-mean, hat[k * V + j], d[k * V + j]);
-                scale_n(f, rstd);
-                if (p.dres) {
-                    float a[V];
-                    unpack<E, V>(*slot(stage, 2, k), a);
-                    add_n<V>(f, f, a);
-                }
-                st_f<E, V>(dx + column<V>(k), f);
+                unpack<E, V>(at[(2 * N + k) * threads], f);
+                add_n<V>(h, h, f);
             }
+            mul_n<V>(g, g, reinterpret_cast<float (&)[V]>(w[k * V]));
+            const float2 r = both(rstd);
+#pragma unroll
+            for (int j = 0; j < V; j += 2) {
+                const float2 o = sm103::fma2(make_float2(g[j], g[j + 1]), r, make_float2(h[j], h[j + 1]));
+                g[j] = o.x, g[j + 1] = o.y;
+            }
+            st_f<E, V>(dx + column<V>(k), g);
         }
         stage = stage + 1 == kStages ? 0 : stage + 1;
     }
@@ -410,10 +428,23 @@ __global__ void __launch_bounds__(128) rms_weight_part_kernel(RmsParams p, int64
     part[blockIdx.y * p.D + c] = s;
 }
 
-__global__ void __launch_bounds__(kSumThreads) rms_weight_sum_kernel(RmsParams p, int64_t parts, const float *part) {
-    const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
-    const float t = column_sum(part, parts, p.D, c, c < p.D);
-    if (threadIdx.x < 32 && c < p.D) p.dweight[c] = t;
+// 32 columns per CTA, the parts in 32 slices, in a fixed order.  (8 slices took 7 us of 152 parts.)
+__global__ void __launch_bounds__(1024) rms_weight_sum_kernel(RmsParams p, int64_t parts, const float *part) {
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    float t = 0.f;
+    if (c < p.D) {
+#pragma unroll 8
+        for (int64_t j = slice; j < parts; j += 32) t += part[j * p.D + c];
+    }
+    sums[slice][lane] = t;
+    __syncthreads();
+    t = sums[lane][slice];             // warp `slice` adds up column `slice`
+#pragma unroll
+    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    const int64_t mine = (int64_t)blockIdx.x * 32 + slice;
+    if (lane == 0 && mine < p.D) p.dweight[mine] = t;
 }
 
 // Groups of n elements where every row allows them.
@@ -428,7 +459,8 @@ dim3 row_block(int64_t D, int el, int most) {
     return dim3(x, x >= most ? 1 : most / x);
 }
 
-constexpr int64_t kFwdMaxD = 16384, kBwdMaxD = 8192;
+constexpr int64_t kFwdMaxD = 16384;
+int64_t bwd_most(const RmsParams &p) { return kBwdThreads * (p.dtype == kFP32 ? kBwdMost<float> : kBwdMost<__half>); }
 
 bool fwd_in_registers(const RmsParams &p) {
     const int V = 16 / (int)dtype_bytes(p.dtype);
@@ -438,12 +470,23 @@ bool fwd_in_registers(const RmsParams &p) {
 }
 bool bwd_in_registers(const RmsParams &p) {
     const int V = 16 / (int)dtype_bytes(p.dtype);
-    return p.D <= kBwdMaxD && p.D % V == 0 && aligned_rows(p, V, {{p.x, p.xs}, {p.dout, p.ds}, {p.dres, p.drs}, {p.dx, p.D}});
+    return p.D <= bwd_most(p) && p.D % V == 0 && aligned_rows(p, V, {{p.x, p.xs}, {p.dout, p.ds}, {p.dres, p.drs}, {p.dx, p.D}});
 }
-int bwd_el(const RmsParams &p) { return p.D <= kBwdThreads * 8 ? 8 : 16; }
-int64_t bwd_grid(const RmsParams &p, int sms) {
-    return std::min(ceil_div(p.rows, (int64_t)row_block(p.D, bwd_el(p), kBwdThreads).y), (int64_t)sms);
+// Elements per thread: a warp to a short row; many of longer ones, as each row costs a thread about
+// 150 instructions beside those of its elements.
+int bwd_el(const RmsParams &p) {
+    const int most = p.dtype == kFP32 ? kBwdMost<float> : kBwdMost<__half>;
+    return p.D <= 256 ? 8 : p.D <= 512 || most == 16 ? 16 : 32;
 }
+// Rows side by side have barriers of their own, of which a CTA has 15 beside the common one; no
+// more of them than leaves every SM a row.
+dim3 bwd_block(const RmsParams &p, int sms) {
+    dim3 block = row_block(p.D, bwd_el(p), kBwdThreads);
+    if (block.x > 32) block.y = std::min(block.y, 15u);
+    block.y = (unsigned)std::min((int64_t)block.y, std::max(ceil_div(p.rows, sms), (int64_t)1));
+    return block;
+}
+int64_t bwd_grid(const RmsParams &p, int sms) { return std::min(ceil_div(p.rows, (int64_t)bwd_block(p, sms).y), (int64_t)sms); }
 int64_t weight_parts(const RmsParams &p, int sms) {
     if (p.rows == 0) return 0;
     return bwd_in_registers(p) ? bwd_grid(p, sms) : std::min(ceil_div(p.rows, 64), (int64_t)256);
@@ -461,12 +504,13 @@ cudaError_t run_fwd(const RmsParams &p, cudaStream_t stream) {
 
 template <typename E, int EL>
 cudaError_t run_bwd(const RmsParams &p, float *part, int sms, cudaStream_t stream) {
-    const dim3 block = row_block(p.D, EL, kBwdThreads);
-    const int threads = block.x * block.y, smem = std::max(threads * EL * 3 * kBwdStages<E, EL> * (int)sizeof(E), (int)block.x * EL * 4);
+    const dim3 block = bwd_block(p, sms);
+    constexpr int kBytes = EL * 3 * kBwdStages<E, EL> * (int)sizeof(E);   // of a thread's ring
     constexpr auto kernel = rms_bwd_row_kernel<E, EL>;
-    const cudaError_t e = allow_smem<kernel>(kBwdThreads * EL * 3 * kBwdStages<E, EL> * (int)sizeof(E));
+    const cudaError_t e = allow_smem<kernel>(kBwdThreads * kBytes);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)bwd_grid(p, sms), block, smem, stream>>>(p, part);
+    static_assert(kBytes >= EL * 4, "the sums fit the ring");
+    kernel<<<(unsigned)bwd_grid(p, sms), block, block.x * block.y * kBytes, stream>>>(p, part);
     return cudaGetLastError();
 }
 
@@ -498,7 +542,12 @@ cudaError_t launch_rms_bwd(const RmsParams &p, unsigned char *ws, int sms, cudaS
     const cudaError_t e = with_dtype(p.dtype, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
         if (p.rows == 0) return cudaSuccess;
-        if (bwd_in_registers(p)) return bwd_el(p) == 8 ? run_bwd<E, 8>(p, part, sms, stream) : run_bwd<E, 16>(p, part, sms, stream);
+        if (bwd_in_registers(p)) {
+            const int el = bwd_el(p);
+            if (el == 8) return run_bwd<E, 8>(p, part, sms, stream);
+            if (el == 16) return run_bwd<E, 16>(p, part, sms, stream);
+            if constexpr (sizeof(E) == 2) return run_bwd<E, 32>(p, part, sms, stream);
+        }
         if (aligned_rows(p, 4, {{p.x, p.xs}, {p.dout, p.ds}, {p.dres, p.drs}, {p.dx, p.D}}))
             rms_bwd_kernel<E, true><<<(unsigned)p.rows, kRowThreads, 0, stream>>>(p);
         else rms_bwd_kernel<E, false><<<(unsigned)p.rows, kRowThreads, 0, stream>>>(p);
@@ -507,7 +556,7 @@ cudaError_t launch_rms_bwd(const RmsParams &p, unsigned char *ws, int sms, cudaS
         return cudaGetLastError();
     });
     if (e != cudaSuccess || !p.dweight) return e;
-    rms_weight_sum_kernel<<<(unsigned)ceil_div(p.D, 32), kSumThreads, 0, stream>>>(p, parts, part);
+    rms_weight_sum_kernel<<<(unsigned)ceil_div(p.D, 32), 1024, 0, stream>>>(p, parts, part);
     return cudaGetLastError();
 }
 
