@@ -279,8 +279,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) rms_bwd_row_kernel(RmsParams p
     }
 }
 
-// ---- rows that are not aligned, or too long for registers: a warp takes blocks of 128 columns, 4
-// columns to a lane, and passes over them twice (the second time through L1 and L2)
+// ---- rows that are not aligned: a warp takes blocks of 128 columns, 4 columns 32 apart to a lane, NB
+// blocks that it keeps in registers; blockDim.x threads to a row, blockDim.y rows per CTA
 
 // A lane's 4 columns of a block: neighbours where rows are aligned, else 32 apart.
 template <bool WIDE>
@@ -333,6 +333,123 @@ __device__ __forceinline__ void st_block_fp8(uint8_t *p, uint8_t *scale, int64_t
     }
 }
 
+
+template <typename E, int NB, int OUT>
+__global__ void __launch_bounds__(512) rms_fwd_odd_kernel(RmsParams p) {
+    __shared__ float part[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int64_t D = row < p.rows ? p.D : 0;
+    const E *x = static_cast<const E *>(p.x) + row * p.xs, *res = static_cast<const E *>(p.res) + row * p.rs;
+    E *sum = static_cast<E *>(p.res_out) + row * p.ros;
+    float h[NB][4], s = 0.f;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) ld_block<E, false>(x, (int64_t)(warp + k * warps) * kFp8Block, D, lane, h[k]);
+    if (p.res) {
+        float f[NB][4];   // all of them before the first store, which may be over them
+#pragma unroll
+        for (int k = 0; k < NB; ++k) ld_block<E, false>(res, (int64_t)(warp + k * warps) * kFp8Block, D, lane, f[k]);
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[k][j] = to_f(from_f<E>(h[k][j] + f[k][j]));
+        if (p.res_out) {
+#pragma unroll
+            for (int k = 0; k < NB; ++k) st_block<E, false>(sum, (int64_t)(warp + k * warps) * kFp8Block, D, lane, h[k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = fmaf(h[k][j], h[k][j], s);
+    const float rstd = 1.f / sqrtf(row_sum(s, part) / (float)(int)p.D + p.eps);
+    if (D == 0) return;
+    if (threadIdx.x == 0 && p.rstd) p.rstd[row] = rstd;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+        const int64_t b = warp + k * warps, c0 = b * kFp8Block;
+        if (c0 >= D) break;
+        float w[4];
+        if (p.weight) ld_block<float, false>(p.weight, c0, D, lane, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[k][j] *= p.weight ? rstd * w[j] : rstd;
+        if constexpr (OUT == 0) st_block<E, false>(static_cast<E *>(p.out) + row * p.os, c0, D, lane, h[k]);
+        else st_block_fp8<OUT == kE5M2, false>(static_cast<uint8_t *>(p.out) + row * p.os, p.scales + row * p.ss + b, c0, D, lane, h[k], false);
+    }
+}
+
+// Persistent, like the aligned rows' kernel, with the weights and their gradients in registers; the
+// next row's loads are left to the other CTAs of the SM.
+template <typename E, int NB>
+__global__ void __launch_bounds__(512) rms_bwd_odd_kernel(RmsParams p, float *part_out) {
+    __shared__ float part[2][32];
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const float inv = 1.f / (float)(int)p.D;
+    float w[NB][4], dw[NB][4];
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[k][j] = 1.f, dw[k][j] = 0.f;
+        if (p.weight) ld_block<float, false>(p.weight, (int64_t)(warp + k * warps) * kFp8Block, p.D, lane, w[k]);
+    }
+    int turn = 0;
+    for (int64_t first = (int64_t)blockIdx.x * blockDim.y; first < p.rows; first += (int64_t)gridDim.x * blockDim.y) {
+        const int64_t row = first + threadIdx.y, D = row < p.rows ? p.D : 0;
+        const E *x = static_cast<const E *>(p.x) + row * p.xs, *dy = static_cast<const E *>(p.dout) + row * p.ds;
+        const E *dres = static_cast<const E *>(p.dres) + row * p.drs;
+        float h[NB][4], g[NB][4], s = 0.f;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) ld_block<E, false>(x, (int64_t)(warp + k * warps) * kFp8Block, D, lane, h[k]);
+#pragma unroll
+        for (int k = 0; k < NB; ++k) ld_block<E, false>(dy, (int64_t)(warp + k * warps) * kFp8Block, D, lane, g[k]);
+        const float rstd = D ? p.rstd[row] : 0.f;
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[k][j] *= rstd;
+                dw[k][j] = fmaf(g[k][j], h[k][j], dw[k][j]);
+                g[k][j] *= w[k][j];
+                s = fmaf(g[k][j], h[k][j], s);
+            }
+        float f[NB][4];
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[k][j] = 0.f;
+            if (p.dres) ld_block<E, false>(dres, (int64_t)(warp + k * warps) * kFp8Block, D, lane, f[k]);
+        }
+        const float mean = row_sum(s, part[turn]) * inv;
+        turn ^= 1;
+        E *dx = static_cast<E *>(p.dx) + row * p.D;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[k][j] = fmaf(rstd, fmaf(-mean, h[k][j], g[k][j]), f[k][j]);
+            st_block<E, false>(dx, (int64_t)(warp + k * warps) * kFp8Block, D, lane, f[k]);
+        }
+    }
+    if (!part_out) return;
+    // over the CTA's rows side by side, one after the other
+    float *sums = reinterpret_cast<float *>(smem);   // [4 NB][blockDim.x]
+    for (int y = 0; y < (int)blockDim.y; ++y) {
+        __syncthreads();
+        if ((int)threadIdx.y != y) continue;
+#pragma unroll
+        for (int e = 0; e < 4 * NB; ++e) {
+            float *at = sums + e * blockDim.x + threadIdx.x;
+            if (y > 0) dw[e / 4][e % 4] += *at;
+            if (y + 1 < (int)blockDim.y) *at = dw[e / 4][e % 4];
+        }
+    }
+    if (threadIdx.y == blockDim.y - 1) {
+#pragma unroll
+        for (int k = 0; k < NB; ++k) st_block<float, false>(part_out + (int64_t)blockIdx.x * p.D, (int64_t)(warp + k * warps) * kFp8Block, p.D, lane, dw[k]);
+    }
+}
+
+// ---- rows too long for registers: a CTA each, two passes (the second through L1 and L2)
 template <typename E, bool WIDE>
 __global__ void __launch_bounds__(kRowThreads) rms_fwd_kernel(RmsParams p) {
     __shared__ float part[32];
@@ -487,9 +604,35 @@ dim3 bwd_block(const RmsParams &p, int sms) {
     return block;
 }
 int64_t bwd_grid(const RmsParams &p, int sms) { return std::min(ceil_div(p.rows, (int64_t)bwd_block(p, sms).y), (int64_t)sms); }
+// Rows that are not aligned: 4 blocks of 128 to a warp, 2 where few rows leave most of the GPU idle.
+int odd_blocks(const RmsParams &p, int sms) { return p.D <= 2 * 128 || p.rows <= 4 * sms ? 2 : 4; }
+dim3 odd_block(const RmsParams &p, int nb, int most) {
+    const int x = 32 * (int)ceil_div(ceil_div(p.D, kFp8Block), nb);
+    return dim3(x, x >= most ? 1 : most / x);
+}
+// Longer ones pass over a row twice: 8192 x 8191 bf16 to 8 bits takes 140 us so, and 270 us with 8
+// blocks to a warp in registers, of which too few warps fit.
+constexpr int64_t kOddFwdMaxD = 4096, kOddBwdMaxD = 8192;
+// Backward: as many CTAs as the registers let an SM hold (16 warps)
+dim3 odd_bwd_block(const RmsParams &p) { return odd_block(p, 4, 256); }
+int64_t odd_bwd_grid(const RmsParams &p, int sms) {
+    const dim3 block = odd_bwd_block(p);
+    return std::min(ceil_div(p.rows, (int64_t)block.y), (int64_t)sms * std::max(512 / (int)(block.x * block.y), 1));
+}
 int64_t weight_parts(const RmsParams &p, int sms) {
     if (p.rows == 0) return 0;
-    return bwd_in_registers(p) ? bwd_grid(p, sms) : std::min(ceil_div(p.rows, 64), (int64_t)256);
+    if (bwd_in_registers(p)) return bwd_grid(p, sms);
+    return p.D <= kOddBwdMaxD ? odd_bwd_grid(p, sms) : std::min(ceil_div(p.rows, 64), (int64_t)256);
+}
+
+template <typename E, int NB>
+cudaError_t run_fwd_odd(const RmsParams &p, cudaStream_t stream) {
+    const dim3 block = odd_block(p, NB, 256);
+    const unsigned grid = (unsigned)ceil_div(p.rows, (int64_t)block.y);
+    if (p.out_dtype == p.dtype) rms_fwd_odd_kernel<E, NB, 0><<<grid, block, 0, stream>>>(p);
+    else if (p.out_dtype == kE4M3) rms_fwd_odd_kernel<E, NB, kE4M3><<<grid, block, 0, stream>>>(p);
+    else rms_fwd_odd_kernel<E, NB, kE5M2><<<grid, block, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename E, int EL>
@@ -528,6 +671,9 @@ cudaError_t launch_rms_fwd(const RmsParams &p, int sms, cudaStream_t stream) {
             if (p.D <= 512 || (p.rows <= 4 * sms && p.D <= 8192)) return run_fwd<E, 16>(p, stream);
             return run_fwd<E, 32>(p, stream);
         }
+        if (p.D <= kOddFwdMaxD) {
+            return odd_blocks(p, sms) == 2 ? run_fwd_odd<E, 2>(p, stream) : run_fwd_odd<E, 4>(p, stream);
+        }
         const bool wide = aligned_rows(p, 4, {{p.x, p.xs}, {p.res, p.rs}, {p.res_out, p.ros}}) &&
                           (p.out_dtype != p.dtype || aligned_rows(p, 4, {{p.out, p.os}}));
         if (wide) rms_fwd_kernel<E, true><<<(unsigned)p.rows, kRowThreads, 0, stream>>>(p);
@@ -547,6 +693,11 @@ cudaError_t launch_rms_bwd(const RmsParams &p, unsigned char *ws, int sms, cudaS
             if (el == 8) return run_bwd<E, 8>(p, part, sms, stream);
             if (el == 16) return run_bwd<E, 16>(p, part, sms, stream);
             if constexpr (sizeof(E) == 2) return run_bwd<E, 32>(p, part, sms, stream);
+        }
+        if (p.D <= kOddBwdMaxD) {
+            const dim3 block = odd_bwd_block(p);
+            rms_bwd_odd_kernel<E, 4><<<(unsigned)odd_bwd_grid(p, sms), block, 16 * block.x * 4, stream>>>(p, part);
+            return cudaGetLastError();
         }
         if (aligned_rows(p, 4, {{p.x, p.xs}, {p.dout, p.ds}, {p.dres, p.drs}, {p.dx, p.D}}))
             rms_bwd_kernel<E, true><<<(unsigned)p.rows, kRowThreads, 0, stream>>>(p);

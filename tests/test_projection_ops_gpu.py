@@ -188,7 +188,9 @@ RMS = [  # rows, D, dtype, out8, residual, weight, how
     (2, 20000, BF, E4, True, True, "dense"), (9, 136, BF, E4, True, True, "slice"), (17, 264, BF, E5, False, True, "dense"),
     (11, 1096, HF, E4, True, True, "dense"), (5, 4100, F, E4, True, True, "dense"), (3, 16384, BF, E4, True, True, "dense"),
     (600, 8192, BF, E5, True, True, "dense"), (400, 520, F, None, True, True, "dense"), (1000, 8184, BF, None, False, False, "dense"),
-    (170, 7000, F, None, True, True, "dense"), (33, 64, F, None, True, False, "dense"), (700, 512, BF, E5, True, True, "dense"),
+    (170, 7000, F, None, True, True, "dense"), (9, 4099, BF, E4, True, True, "odd"), (700, 1537, HF, E5, True, True, "dense"),
+    (3, 9001, HF, None, True, True, "dense"), (2, 16383, F, E4, True, True, "odd"), (2, 20001, BF, None, True, True, "odd"),
+    (650, 260, BF, None, True, True, "odd"), (5, 8192, BF, E4, True, True, "odd"), (33, 64, F, None, True, False, "dense"), (700, 512, BF, E5, True, True, "dense"),
 ]
 
 
