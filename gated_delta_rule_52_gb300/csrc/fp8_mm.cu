@@ -54,19 +54,9 @@ struct Slot {
     }
 };
 
-// Tiles of a pair kernel's call: the first `full` are one item of work each; each of the `rest`
-// after them is `split` items, equal parts of K, whose sums meet in the workspace.
-struct Plan {
-    uint32_t full, rest;
-    int split;
-    float *parts;          // [rest][split][2][kStoreWarps][kMost][32]
-    unsigned *arrived;     // [rest][2][kStoreWarps], zero at the start
-};
-
 struct MatmulArgs {
     CUtensorMap a, b, out;
     MatmulParams p;
-    Plan plan;
 };
 
 // Asynchronous copy of up to 4 bytes (the rest zero) into shared memory.
@@ -272,22 +262,24 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
     if (split > 1) cluster_sync();   // the others have read this CTA's sums
 }
 
-// ---- tiles of 256 rows of a by BN rows of b, persistent pairs of CTAs.
+// ---- tiles of 256 rows of a by BN rows of b, each of a pair of CTAs.
 //
-// A pair shares its tiles: each CTA loads its 128 rows of a and half of the rows of b, one
-// thread of the first CTA issues the MMAs of both (cta_group::2), which halves what shared
-// memory has to deliver for b.  Warp 0 loads tiles, warp 2 scales, warp 1 issues, warps 4 to 11
-// empty the accumulators; two of these in TMEM, so that a tile's MMAs run while the one before
-// is stored.  fp32 outputs take K in segments whose sums are added in registers: the tensor
-// cores cut an accumulator at each step, which over a long K would cost more than fp32's own
-// rounding.
+// Each CTA of a pair loads its 128 rows of a and half of the rows of b, one thread of the first CTA
+// issues the MMAs of both (cta_group::2), which halves what shared memory has to deliver for b.
+// Warp 0 loads tiles, warp 2 scales, warp 1 issues, warps 4 to 11 empty the accumulators.
+//   SPLIT = 1: pairs are persistent and walk the tiles, with two accumulators in TMEM, so that a
+// tile's MMAs run while the one before is stored.  fp32 outputs take K in segments whose sums are
+// added in registers: the tensor cores cut an accumulator at each step, which over a long K would
+// cost more than fp32's own rounding.
+//   SPLIT = 2, 4: few tiles; a cluster of SPLIT pairs shares a tile's K and joins the sums through
+// distributed shared memory, each pair for its part of the columns.
 constexpr int kPairThreads = 384, kStoreWarps = 8;
-constexpr int kSegment = 32;                // blocks of K per segment of an fp32 output
+constexpr int kSegment = 64;                // blocks of K per segment of an fp32 output
 
 // A store warp's buffer: 32 rows of 64 bytes for a tensor store, or 32 x 17 fp32.
 constexpr int kStoreBuffer = 2560;
 
-template <int BN>
+template <int BN, int SPLIT>
 struct PairShape {
     static constexpr int kStage = (kRows + BN / 2) * kFp8Block;
     static constexpr int kScaleB = BN <= 128 ? 512 : 1024;
@@ -296,9 +288,12 @@ struct PairShape {
     static constexpr int kStages = (227 * 1024 - 2048 - kStaging - kScaleStage * kScaleStages) / kStage;
     static constexpr int kSmem = 1024 + kStage * kStages + kScaleStage * kScaleStages + kStaging;
     static constexpr int kSet = 4 + kScaleB / 128;
-    static constexpr int kBuffers = 2, kCols = 512;
+    static constexpr int kBuffers = SPLIT > 1 ? 1 : 2, kCols = 512;
     static constexpr int kMost = (BN / 2 + 31) / 32 * 32;   // columns of a store warp, at most
+    static constexpr int kSlice = kMost / SPLIT;            // SPLIT > 1: those that a pair finishes
     static_assert(kSmem <= 227 * 1024 && BN % 32 == 0 && kBuffers * BN + 2 * kSet <= kCols, "fits an SM");
+    static_assert(SPLIT == 1 || (BN % 64 == 0 && kSlice % 16 == 0 && (SPLIT - 1) * kStoreWarps * kSlice * 128 <= kStage * kStages),
+                  "the other pairs' sums fit the ring");
 };
 
 // Tile t of a grid of `down` x `across`: 8 tiles down, then across, so that the tiles in flight
@@ -319,56 +314,51 @@ __device__ __forceinline__ Pack<E, V> ld_row(const E *p, int n) {
     return r;
 }
 
-// 16 columns of 32 rows (one to a lane) to out, with the addend, by single elements: neighbouring
-// lanes take neighbouring columns.  `own`: 32 x 17 fp32 of shared memory.
+// 16 columns at a time of 32 rows (one to a lane) to out, with the addend, by single elements:
+// neighbouring lanes take neighbouring columns.  The addend of the next 16 is on its way while these
+// are stored.  `own`: 32 x 17 fp32 of shared memory.
 template <typename E>
-__device__ __forceinline__ void st_narrow(const MatmulParams &p, const float (&r)[16], float *own, int64_t m0, int64_t n0, int lane) {
-    __syncwarp();
+struct NarrowRows {
+    const MatmulParams &p;
+    float *own;
+    int64_t m, n0;
+    int lane, rows;
+    float a[16];
+    __device__ __forceinline__ NarrowRows(const MatmulParams &p, float *own, int64_t m0, int64_t n0, int lane)
+        : p(p), own(own), m(m0 + (lane >> 4)), n0(n0), lane(lane), rows((int)min(max(p.a.rows - m, (int64_t)0), (int64_t)32)) {}
+    __device__ __forceinline__ void take_addend(int c) {
+        const int64_t n = n0 + c + (lane & 15);
+        const E *plus = static_cast<const E *>(p.add) + m * p.as + n;
+        const int some = p.add && n < p.b.rows ? rows : 0;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) own[lane * 17 + e] = r[e];
-    __syncwarp();
-    const int64_t n = n0 + (lane & 15), m = m0 + (lane >> 4);
-    const int rows = n < p.b.rows ? (int)min(max(p.a.rows - m, (int64_t)0), (int64_t)32) : 0;
-    E *to = static_cast<E *>(p.out) + m * p.os + n;
-    const E *plus = static_cast<const E *>(p.add) + m * p.as + n;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float a[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = p.add && 16 * h + 2 * i < rows ? to_f(plus[(16 * h + 2 * i) * p.as]) : 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int row = 16 * h + 2 * i;
-            if (row < rows) to[row * p.os] = from_f<E>(own[(row + (lane >> 4)) * 17 + (lane & 15)] + a[i]);
-        }
+        for (int i = 0; i < 16; ++i) a[i] = 2 * i < some ? to_f(plus[2 * i * p.as]) : 0.f;
     }
-}
-
-// One item of a plan: blocks [k0, k1) of a tile.
-struct Item {
-    uint32_t i, j;         // the tile's place
-    int rest, part;        // its number among the shared ones, or -1, and which of its parts
-    int k0, k1;
-    __device__ __forceinline__ Item(const Plan &plan, uint32_t n, uint32_t down, uint32_t across, int blocks) {
-        uint32_t t = n;
-        rest = -1, part = 0, k0 = 0, k1 = blocks;
-        if (plan.split > 1 && n >= plan.full) {
-            part = (n - plan.full) / plan.rest;
-            rest = n - plan.full - part * plan.rest;
-            t = plan.full + rest;
-            // a round number of groups of 4 blocks for each part, one more for the first ones
-            const int groups = (blocks + 3) / 4, each = groups / plan.split, more = groups - each * plan.split;
-            k0 = 4 * (each * part + min(part, more));
-            k1 = min(k0 + 4 * (each + (part < more)), blocks);
+    // Columns c .. + 15, of which the addend was taken; `next`: it is taken for those behind them.
+    __device__ __forceinline__ void store(const float (&r)[16], int c, bool next) {
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) own[lane * 17 + e] = r[e];
+        __syncwarp();
+        const int64_t n = n0 + c + (lane & 15);
+        const int some = n < p.b.rows ? rows : 0;
+        E *to = static_cast<E *>(p.out) + m * p.os + n;
+        E o[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float v = own[(2 * i + (lane >> 4)) * 17 + (lane & 15)];
+            o[i] = from_f<E>(p.add ? v + a[i] : v);
         }
-        tile_at(t, down, across, i, j);
+        if (next) take_addend(c + 16);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (2 * i < some) to[2 * i * p.os] = o[i];
     }
 };
 
-template <typename E, int BN>
+template <typename E, int BN, int SPLIT>
 __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_constant__ MatmulArgs args, int wide) {
-    using S = PairShape<BN>;
-    constexpr bool kSums = sizeof(E) == 4;
+    using S = PairShape<BN, SPLIT>;
+    constexpr bool kSums = sizeof(E) == 4 && SPLIT == 1;
     extern __shared__ unsigned char raw[];
     unsigned char *ring = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     unsigned char *scales = ring + S::kStage * S::kStages;
@@ -377,11 +367,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     __shared__ uint32_t tmem_base;
     const MatmulParams &p = args.p;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
-    const Plan &plan = args.plan;
-    const uint32_t down = (uint32_t)ceil_div(p.a.rows, 2 * kRows), across = (uint32_t)ceil_div(p.b.rows, BN), items = plan.full + plan.rest * plan.split;
-    const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int blocks = (int)ceil_div(p.K, kFp8Block);
+    // this CTA's place in its pair, the pair's first CTA in the cluster, both as a mask
+    const uint32_t in_cluster = cluster_ctarank(), rank = in_cluster & 1, first = in_cluster & ~1u;
+    const uint16_t both_ctas = (uint16_t)(3u << first);
+    const int part = SPLIT > 1 ? first >> 1 : 0;
+    const uint32_t down = (uint32_t)ceil_div(p.a.rows, 2 * kRows), across = (uint32_t)ceil_div(p.b.rows, BN), tiles = down * across;
+    const uint32_t pair = blockIdx.x / (2 * SPLIT), pairs = gridDim.x / (2 * SPLIT);
+    // blocks of K: all, or this pair's part, which begins at a group of 4
+    const int blocks = (int)ceil_div(p.K, kFp8Block), groups = (blocks + 3) / 4, each = groups / SPLIT, over = groups - each * SPLIT;
+    const int k_begin = SPLIT > 1 ? 4 * (each * part + min(part, over)) : 0;
+    const int k_end = SPLIT > 1 ? min(k_begin + 4 * (each + (part < over)), blocks) : blocks;
     const int segment = kSums ? kSegment : blocks;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
@@ -401,11 +396,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         const bool issuer = elect_one();
         Slot<S::kStages> slot;
         int loads = 0;
-        const uint32_t bars = mapa_shared(smem_u32(full), 0);
-        for (uint32_t t = pair; ok && t < items; t += pairs) {
-            const Item item(plan, t, down, across, blocks);
-            const int ra = (int)(item.i * (2 * kRows) + rank * kRows), rb = (int)(item.j * BN + rank * (BN / 2));
-            for (int k = item.k0; k < item.k1; ++k) {
+        const uint32_t bars = mapa_shared(smem_u32(full), first);
+        for (uint32_t t = pair; ok && t < tiles; t += pairs) {
+            uint32_t ti, tj;
+            tile_at(t, down, across, ti, tj);
+            const int ra = (int)(ti * (2 * kRows) + rank * kRows), rb = (int)(tj * BN + rank * (BN / 2));
+            for (int k = k_begin; k < k_end; ++k) {
                 // (a wait for the turn before the first returns at once)
                 if (!warp_wait<false>(&empty[slot.at], slot.turn ^ 1)) {
                     ok = false;
@@ -435,16 +431,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         Slot<S::kBuffers> sum;
         const uint64_t a0 = sdesc_sw128(smem_u32(ring), 16, 1024), s0 = sdesc_plain(smem_u32(scales), 128);
         const uint32_t idesc = idesc_mx8(2 * kRows, BN, p.a.dtype == kE5M2, p.b.dtype == kE5M2, 0);
-        for (uint32_t t = pair; ok && t < items; t += pairs) {
-            const Item item(plan, t, down, across, blocks);
-            for (int k0 = item.k0; ok && k0 < item.k1; k0 += segment) {
+        for (uint32_t t = pair; ok && t < tiles; t += pairs) {
+            uint32_t ti, tj;
+            tile_at(t, down, across, ti, tj);
+            for (int k0 = k_begin; ok && k0 < k_end; k0 += segment) {
                 if (!warp_wait<false>(&tempty[sum.at], sum.turn ^ 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t to = acc + sum.at * BN;
-                const int k1 = min(item.k1, k0 + segment);
+                const int k1 = min(k_end, k0 + segment);
                 bool ready = false;   // this lane has seen the next stage full
                 for (int k = k0; k < k1; ++k) {
                     const uint32_t set = sf + (scale.at & 1) * S::kSet;
@@ -458,7 +455,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                         if (issuer) {
 #pragma unroll
                             for (int c = 0; c < S::kScaleStage / 512; ++c) tmem_copy_scales_pair(set + 4 * c, from + 32 * c);
-                            mma_commit_pair(&sempty[scale.at]);
+                            mma_commit_pair(&sempty[scale.at], both_ctas);
                         }
                     }
                     if (!__all_sync(0xffffffffu, ready) && !warp_wait<false>(&full[slot.at], slot.turn)) {
@@ -474,11 +471,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                     if (issuer) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) mma_mx8_pair(to, ad + 2 * q, bd + 2 * q, id, set, set + 4, k != k0 || q > 0);
-                        mma_commit_pair(&empty[here]);
+                        mma_commit_pair(&empty[here], both_ctas);
                     }
                     if (k % 4 == 3 || k == blocks - 1) scale.next();
                 }
-                if (issuer) mma_commit_pair(&tfull[sum.at]);
+                if (issuer) mma_commit_pair(&tfull[sum.at], both_ctas);
                 sum.next();
             }
         }
@@ -486,10 +483,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         // ---- the second CTA's scales are there: told to the first by a warp that has no copies on
         // their way, because a release for the cluster waits for all of a thread's
         Slot<kScaleStages> scale;
-        const uint32_t bars = mapa_shared(smem_u32(sfull), 0);
-        for (uint32_t t = pair; ok && t < items; t += pairs) {
-            const Item item(plan, t, down, across, blocks);
-            for (int k = item.k0; k < item.k1; k += 4) {
+        const uint32_t bars = mapa_shared(smem_u32(sfull), first);
+        for (uint32_t t = pair; ok && t < tiles; t += pairs) {
+            uint32_t ti, tj;
+            tile_at(t, down, across, ti, tj);
+            for (int k = k_begin; k < k_end; k += 4) {
                 ok = warp_wait<false>(&sfull[scale.at], scale.turn);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_remote(bars + 8 * scale.at);
@@ -509,11 +507,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
             out.next();
             --waiting;
         };
-        for (uint32_t t = pair; ok && t < items; t += pairs) {
-            const Item item(plan, t, down, across, blocks);
-            rows_a.set(p.a, (int64_t)item.i * (2 * kRows) + rank * kRows, item.k0, lane);
-            rows_b.set(p.b, (int64_t)item.j * BN, item.k0, lane);
-            for (int k = item.k0; k < item.k1; k += 4) {
+        for (uint32_t t = pair; ok && t < tiles; t += pairs) {
+            uint32_t ti, tj;
+            tile_at(t, down, across, ti, tj);
+            rows_a.set(p.a, (int64_t)ti * (2 * kRows) + rank * kRows, k_begin, lane);
+            rows_b.set(p.b, (int64_t)tj * BN, k_begin, lane);
+            for (int k = k_begin; k < k_end; k += 4) {
                 ok = warp_wait<false>(&sempty[in.at], in.turn ^ 1);
                 if (!ok) break;
                 const uint32_t at = smem_u32(scales + in.at * S::kScaleStage);
@@ -531,183 +530,213 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         copies_wait<0>();
         while (ok && waiting > 0) hand_over();
     } else if (warp >= 4) {
-        // ---- accumulators to out: lanes 32 (warp % 4) .. + 31, one half of the columns
-        const int part = warp & 3, half = (warp - 4) >> 2;
-        constexpr int kMost = S::kMost;                  // of the first half; the second may be shorter
-        constexpr int V = 16 / sizeof(E);
-        const int cols = half ? BN - kMost : kMost;
-        unsigned char *own = staging + (warp - 4) * kStoreBuffer;
-        Slot<S::kBuffers> sum;
-        const uint32_t bars = mapa_shared(smem_u32(tempty), 0);
-        for (uint32_t t = pair; ok && t < items; t += pairs) {
-            const Item item(plan, t, down, across, blocks);
-            const int64_t m0 = (int64_t)item.i * (2 * kRows) + rank * kRows + part * 32, n0 = (int64_t)item.j * BN + half * kMost;
-            const int64_t left = p.b.rows - n0;              // columns of out from here on
-            const E *plus = p.add ? static_cast<const E *>(p.add) + (m0 + lane) * p.as + n0 : nullptr;
-            const bool my_row = m0 + lane < p.a.rows, shared = item.rest >= 0;
-            float *parts = shared ? plan.parts + ((int64_t)(item.rest * plan.split * 2 + rank) * kStoreWarps + (warp - 4)) * (kMost * 32) + lane : nullptr;
-            constexpr int kPart = 2 * kStoreWarps * kMost * 32;      // from one part of a tile to the next
-            // this lane's row: fp32, or 16-bit values that begin as the addend's
-            float f[kSums ? kMost : 1];
-            Pack<E, V> o[kSums ? 1 : kMost / V];
-            const auto take_addend = [&]() {
+        if constexpr (SPLIT > 1) {
+            ok = warp_wait<false>(&tfull[0], 0);
+            tc_fence_after();
+        } else {
+            // ---- accumulators to out: lanes 32 (warp % 4) .. + 31, one half of the columns
+            const int quarter = warp & 3, half = (warp - 4) >> 2;
+            constexpr int kMost = S::kMost;              // of the first half; the second may be shorter
+            constexpr int V = 16 / sizeof(E);
+            const int cols = half ? BN - kMost : kMost;
+            unsigned char *own = staging + (warp - 4) * kStoreBuffer;
+            Slot<S::kBuffers> sum;
+            const uint32_t bars = mapa_shared(smem_u32(tempty), first);
+            for (uint32_t t = pair; ok && t < tiles; t += pairs) {
+                uint32_t ti, tj;
+                tile_at(t, down, across, ti, tj);
+                const int64_t m0 = (int64_t)ti * (2 * kRows) + rank * kRows + quarter * 32, n0 = (int64_t)tj * BN + half * kMost;
+                const int64_t left = p.b.rows - n0;          // columns of out from here on
+                const E *plus = p.add ? static_cast<const E *>(p.add) + (m0 + lane) * p.as + n0 : nullptr;
+                const bool my_row = m0 + lane < p.a.rows;
+                NarrowRows<E> narrow(p, reinterpret_cast<float *>(own), m0, n0, lane);
+                // this lane's row: fp32, or 16-bit values that begin as the addend's
+                float f[kSums ? kMost : 1];
+                Pack<E, V> o[kSums ? 1 : kMost / V];
                 if constexpr (!kSums) {
+                    if (wide && plus) {
 #pragma unroll
-                    for (int c = 0; c < kMost; c += V)
-                        if (c < cols) o[c / V] = ld_row<E, V>(plus + c, my_row ? (int)min(left - c, (int64_t)V) : 0);
-                }
-            };
-            const auto round_off = [&](int c, float (&r)[32]) {      // 32 columns to o, with the addend there
-                if constexpr (!kSums) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += V) {
-                        float (&v)[V] = reinterpret_cast<float (&)[V]>(r[e]);
-                        if (plus) {
-                            float a[V];
-                            unpack<E, V>(o[(c + e) / V], a);
-                            add_n<V>(v, v, a);
-                        }
-                        st_f<E, V>(o[(c + e) / V].e, v);
+                        for (int c = 0; c < kMost; c += V)
+                            if (c < cols) o[c / V] = ld_row<E, V>(plus + c, my_row ? (int)min(left - c, (int64_t)V) : 0);
                     }
                 }
-            };
-            if (wide && plus && !shared) take_addend();
-            for (int k = item.k0; k < item.k1; k += segment) {
-                const int buf = sum.at;
-                ok = warp_wait<false>(&tfull[buf], sum.turn);
-                if (!ok) break;
-                sum.next();
-                tc_fence_after();
-                const uint32_t from = tmem_addr(acc, part * 32, buf * BN + half * kMost);
-                if constexpr (kSums) {
-#pragma unroll
-                    for (int c = 0; c < kMost; c += 32) {
-                        if (c >= cols) break;
-                        float r[32];
-                        tmem_ld32(from + c, r);
-                        tmem_ld_wait();
-                        if (k == item.k0) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) f[c + e] = r[e];
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) f[c + e] += r[e];
-                        }
-                    }
-                } else if (shared || wide) {
-#pragma unroll
-                    for (int c = 0; c < kMost; c += 32) {
-                        if (c >= cols) break;
-                        float r[32];
-                        tmem_ld32(from + c, r);
-                        tmem_ld_wait();
-                        if (shared) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) parts[item.part * kPart + (c + e) * 32] = r[e];
-                        } else {
-                            round_off(c, r);
-                        }
-                    }
-                } else {
-                    // rows that no wide access fits: 16 columns at a time through shared memory
-#pragma unroll 1
-                    for (int c = 0; c < cols; c += 16) {
-                        float r[16];
-                        tmem_ld16(from + c, r);
-                        tmem_ld_wait();
-                        st_narrow<E>(p, r, reinterpret_cast<float *>(own), m0, n0 + c, lane);
-                    }
-                }
-                tc_fence_before();
-                if (lane == 0) mbar_arrive_remote(bars + 8 * buf);
-            }
-            if (!ok) break;
-            if (shared) {
-                // the last of the tile's parts to arrive adds them all up, in the order of K
-                if constexpr (kSums) {
-#pragma unroll
-                    for (int c = 0; c < kMost; ++c)
-                        if (c < cols) parts[item.part * kPart + c * 32] = f[c];
-                }
-                __threadfence();
-                __syncwarp();
-                unsigned before = 0;
-                if (lane == 0) before = atomicAdd(plan.arrived + (item.rest * 2 + rank) * kStoreWarps + (warp - 4), 1u);
-                before = __shfl_sync(0xffffffffu, before, 0);
-                if (before + 1 != (unsigned)plan.split) continue;
-                __threadfence();
-                if (wide && plus) take_addend();
-                const auto add_up = [&](int c, auto &r) {
-                    constexpr int n = sizeof(r) / sizeof(float);
-#pragma unroll
-                    for (int e = 0; e < n; ++e) r[e] = __ldcg(parts + (c + e) * 32);
-#pragma unroll 1
-                    for (int q = 1; q < plan.split; ++q)
-#pragma unroll
-                        for (int e = 0; e < n; ++e) r[e] += __ldcg(parts + q * kPart + (c + e) * 32);
-                };
-                if constexpr (kSums) {
-#pragma unroll
-                    for (int c = 0; c < kMost; c += 32)
-                        if (c < cols) add_up(c, reinterpret_cast<float (&)[32]>(f[c]));
-                } else if (wide) {
-#pragma unroll
-                    for (int c = 0; c < kMost; c += 32) {
-                        if (c >= cols) break;
-                        float r[32];
-                        add_up(c, r);
-                        round_off(c, r);
-                    }
-                } else {
-#pragma unroll 1
-                    for (int c = 0; c < cols; c += 16) {
-                        float r[16];
-                        add_up(c, r);
-                        st_narrow<E>(p, r, reinterpret_cast<float *>(own), m0, n0 + c, lane);
-                    }
-                }
-            }
-            if constexpr (kSums) {
-                if (!wide) {
-#pragma unroll
-                    for (int c = 0; c < kMost; c += 16)
-                        if (c < cols) st_narrow<E>(p, reinterpret_cast<float (&)[16]>(f[c]), reinterpret_cast<float *>(own), m0, n0 + c, lane);
-                }
-            }
-            if (!wide || m0 >= p.a.rows) continue;
-            // 64 bytes of every row to the buffer (16-byte piece j of row r at j ^ (r / 2 % 4), the
-            // 64-byte swizzle), and from there by a tensor store, which leaves out what is outside
-            constexpr int kStep = 64 / sizeof(E);
-#pragma unroll
-            for (int c = 0; c < kMost; c += kStep) {
-                if (c >= cols || c >= left) break;
-                if (lane == 0) bulk_wait_read0();
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    Pack<E, V> piece;
+                if (!wide) narrow.take_addend(0);
+                for (int k = 0; k < blocks; k += segment) {
+                    const int buf = sum.at;
+                    ok = warp_wait<false>(&tfull[buf], sum.turn);
+                    if (!ok) break;
+                    sum.next();
+                    tc_fence_after();
+                    const uint32_t from = tmem_addr(acc, quarter * 32, buf * BN + half * kMost);
                     if constexpr (kSums) {
-                        float (&v)[V] = reinterpret_cast<float (&)[V]>(f[c + j * V]);
-                        if (plus) {
-                            float a[V];
-                            unpack<E, V>(ld_row<E, V>(plus + c + j * V, my_row ? (int)min(left - c - j * V, (int64_t)V) : 0), a);
-                            add_n<V>(v, v, a);
+#pragma unroll
+                        for (int c = 0; c < kMost; c += 16) {
+                            if (c >= cols) break;
+                            float r[16];
+                            tmem_ld16(from + c, r);
+                            tmem_ld_wait();
+                            if (k == 0) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) f[c + e] = r[e];
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) f[c + e] += r[e];
+                            }
                         }
-                        st_f<E, V>(piece.e, v);
+                    } else if (wide) {
+#pragma unroll
+                        for (int c = 0; c < kMost; c += 32) {
+                            if (c >= cols) break;
+                            float r[32];
+                            tmem_ld32(from + c, r);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; e += V) {
+                                float (&v)[V] = reinterpret_cast<float (&)[V]>(r[e]);
+                                if (plus) {
+                                    float a[V];
+                                    unpack<E, V>(o[(c + e) / V], a);
+                                    add_n<V>(v, v, a);
+                                }
+                                st_f<E, V>(o[(c + e) / V].e, v);
+                            }
+                        }
                     } else {
-                        piece = o[c / V + j];
+                        // rows that no wide access fits
+#pragma unroll 1
+                        for (int c = 0; c < cols; c += 16) {
+                            float r[16];
+                            tmem_ld16(from + c, r);
+                            tmem_ld_wait();
+                            narrow.store(r, c, c + 16 < cols);
+                        }
                     }
-                    *reinterpret_cast<Pack<E, V> *>(own + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = piece;
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive_remote(bars + 8 * buf);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    tma_store_2d(&args.out, own, (int)(n0 + c), (int)m0);
-                    bulk_commit();
+                if (!ok) break;
+                if constexpr (kSums) {
+                    if (!wide) {
+#pragma unroll
+                        for (int c = 0; c < kMost; c += 16)
+                            if (c < cols) narrow.store(reinterpret_cast<float (&)[16]>(f[c]), c, c + 16 < cols);
+                    }
+                }
+                if (!wide || m0 >= p.a.rows) continue;
+                // 64 bytes of every row to the buffer (16-byte piece j of row r at j ^ (r / 2 % 4), the
+                // 64-byte swizzle), and from there by a tensor store, which leaves out what is outside
+                constexpr int kStep = 64 / sizeof(E);
+#pragma unroll
+                for (int c = 0; c < kMost; c += kStep) {
+                    if (c >= cols || c >= left) break;
+                    if (lane == 0) bulk_wait_read0();
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        Pack<E, V> piece;
+                        if constexpr (kSums) {
+                            float (&v)[V] = reinterpret_cast<float (&)[V]>(f[c + j * V]);
+                            if (plus) {
+                                float a[V];
+                                unpack<E, V>(ld_row<E, V>(plus + c + j * V, my_row ? (int)min(left - c - j * V, (int64_t)V) : 0), a);
+                                add_n<V>(v, v, a);
+                            }
+                            st_f<E, V>(piece.e, v);
+                        } else {
+                            piece = o[c / V + j];
+                        }
+                        *reinterpret_cast<Pack<E, V> *>(own + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = piece;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&args.out, own, (int)(n0 + c), (int)m0);
+                        bulk_commit();
+                    }
+                }
+            }
+            if (lane == 0) bulk_wait0();
+        }
+    }
+    if constexpr (SPLIT > 1) {
+        // Each store warp sends the sums of the other pairs' columns to the same warp of their CTAs,
+        // into the ring, which is free once every MMA of the cluster has ended, and adds up its own
+        // columns in the order of K.
+        __syncwarp();
+        tc_fence_before();
+        cluster_sync();
+        tc_fence_after();
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        constexpr int kSlice = S::kSlice;
+        const uint32_t from = tmem_addr(acc, quarter * 32, half * S::kMost);
+        float *box = reinterpret_cast<float *>(ring) + (warp - 4) * (SPLIT - 1) * kSlice * 32 + lane;
+        if (warp >= 4 && ok) {
+#pragma unroll 1
+            for (int q = 0; q < SPLIT; ++q) {
+                if (q == part) continue;
+                const uint32_t to = mapa_shared(smem_u32(box + (part < q ? part : part - 1) * kSlice * 32), 2 * q + rank);
+#pragma unroll
+                for (int c = 0; c < kSlice; c += 16) {
+                    float r[16];
+                    tmem_ld16(from + q * kSlice + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) st_cluster(to + (c + e) * 128, r[e]);
                 }
             }
         }
-        if (lane == 0) bulk_wait0();
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 4 && ok) {
+            uint32_t ti, tj;
+            tile_at(pair, down, across, ti, tj);
+            constexpr int V = 16 / sizeof(E);
+            const int64_t m0 = (int64_t)ti * (2 * kRows) + rank * kRows + quarter * 32;
+            const int64_t n0 = (int64_t)tj * BN + half * S::kMost + part * kSlice, left = p.b.rows - n0;
+            const bool my_row = m0 + lane < p.a.rows;
+            E *to = static_cast<E *>(p.out) + (m0 + lane) * p.os + n0;
+            const E *plus = p.add ? static_cast<const E *>(p.add) + (m0 + lane) * p.as + n0 : nullptr;
+            NarrowRows<E> narrow(p, reinterpret_cast<float *>(staging + (warp - 4) * kStoreBuffer), m0, n0, lane);
+            if (!wide) narrow.take_addend(0);
+#pragma unroll 1
+            for (int c = 0; c < kSlice; c += 16) {
+                float r[16], s[16];
+                Pack<E, V> a[16 / V];
+                if (wide && plus) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += V) a[e / V] = ld_row<E, V>(plus + c + e, my_row ? (int)min(left - c - e, (int64_t)V) : 0);
+                }
+                tmem_ld16(from + part * kSlice + c, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[e] = part == 0 ? r[e] : box[(c + e) * 32];
+#pragma unroll
+                for (int q = 1; q < SPLIT; ++q)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[e] += q == part ? r[e] : box[((q < part ? q : q - 1) * kSlice + c + e) * 32];
+                if (!wide) {
+                    narrow.store(s, c, c + 16 < kSlice);
+                    continue;
+                }
+#pragma unroll
+                for (int e = 0; e < 16; e += V) {
+                    float (&v)[V] = reinterpret_cast<float (&)[V]>(s[e]);
+                    if (plus) {
+                        float b[V];
+                        unpack<E, V>(a[e / V], b);
+                        add_n<V>(v, v, b);
+                    }
+                    if (!my_row) continue;
+                    if (left - c - e >= V) {
+                        st_f<E, V>(to + c + e, v);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < V; ++x)
+                            if (x < left - c - e) to[c + e + x] = from_f<E>(v[x]);
+                    }
+                }
+            }
+        }
     }
     if (!ok && p.err) atomicExch(p.err, kErrTimeout);
     __syncwarp();
@@ -771,66 +800,54 @@ cudaError_t run_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
     return cudaLaunchKernelEx(&c, kernel, args, split);
 }
 
-template <typename E, int BN>
+template <typename E, int BN, int SPLIT>
 cudaError_t run_pair(MatmulArgs &args, int sms, cudaStream_t stream) {
-    using S = PairShape<BN>;
-    constexpr auto kernel = mm_pair_kernel<E, BN>;
-    cudaError_t e = allow_smem<kernel>(S::kSmem);
+    using S = PairShape<BN, SPLIT>;
+    constexpr auto kernel = mm_pair_kernel<E, BN, SPLIT>;
+    const cudaError_t e = allow_smem<kernel>(S::kSmem);
     if (e != cudaSuccess) return e;
     const MatmulParams &p = args.p;
     if (!encode_operand(args.a, p.a, p.K, kRows) || !encode_operand(args.b, p.b, p.K, BN / 2)) return cudaErrorInvalidValue;
     constexpr int V = 16 / sizeof(E);
     const int wide = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.os % V == 0 &&
                      (!p.add || (reinterpret_cast<uintptr_t>(p.add) % 16 == 0 && p.as % V == 0));
-    if (wide && !encode_out(args.out, p)) return cudaErrorInvalidValue;
-    if (args.plan.split > 1 && (e = cudaMemsetAsync(args.plan.arrived, 0, args.plan.rest * 2 * kStoreWarps * 4, stream)) != cudaSuccess) return e;
+    if (SPLIT == 1 && wide && !encode_out(args.out, p)) return cudaErrorInvalidValue;
+    const int64_t tiles = ceil_div(p.a.rows, 2 * kRows) * ceil_div(p.b.rows, BN);
     cudaLaunchAttribute at;
-    const int64_t items = args.plan.full + (int64_t)args.plan.rest * args.plan.split;
-    const cudaLaunchConfig_t c = cluster_launch(at, 2 * std::min(items, (int64_t)sms / 2), kPairThreads, S::kSmem, 2, stream);
+    const cudaLaunchConfig_t c =
+        cluster_launch(at, 2 * SPLIT * (SPLIT > 1 ? tiles : std::min(tiles, (int64_t)sms / 2)), kPairThreads, S::kSmem, 2 * SPLIT, stream);
     return cudaLaunchKernelEx(&c, kernel, args, wide);
 }
 
-// How a product is computed: rows of a per tile (tile kernel) or of b (pair kernel), and the plan.
+// How a product is computed: rows of a per tile (tile kernel), or rows of b and parts of K (pair
+// kernel).
 struct Choice {
-    int bt, bn;
-    Plan plan;
-    size_t arrived_bytes, part_bytes;
+    int bt, bn, split;
 };
-// Time of a block of K of a pair's tile of BN rows of b, in ns (8192 x 8192 x 8192).
-int block_ns(int bn) { return bn == 128 ? 272 : bn == 192 ? 298 : 318; }
 
 Choice choose(const MatmulParams &p, int sms) {
-    Choice c = {};
-    if (p.a.rows <= 64) {
-        c.bt = p.a.rows <= 16 ? 16 : p.a.rows <= 32 ? 32 : 64;
-        return c;
-    }
-    const int64_t pairs = sms / 2, blocks = ceil_div(p.K, kFp8Block), groups = ceil_div(blocks, 4);
-    double best = 0;
+    if (p.a.rows <= 64) return {p.a.rows <= 16 ? 16 : p.a.rows <= 32 ? 32 : 64, 0, 0};
+    const int64_t pairs = sms / 2, blocks = ceil_div(p.K, kFp8Block);
+    Choice best = {};
+    double least = 0;
     const char *only = getenv("MM_BN"), *sp = getenv("MM_SPLIT");
-    for (int bn : {224, 192, 128}) {
-        if (only && atoi(only) != bn) continue;
-        const int64_t tiles = ceil_div(p.a.rows, 2 * kRows) * ceil_div(p.b.rows, bn), full = tiles / pairs * pairs, rest = tiles - full;
-        // the tiles of the last, partial round: whole, or shared by several pairs, which costs
-        // about 8 blocks' time for the parts' way through L2, and one for each part
-        const double t = block_ns(bn);
-        int split = 1;
-        double tail = rest ? blocks : 0;
-        for (int s = 2; rest && s <= pairs / rest && s <= groups / 2 && s <= 16; ++s) {
-            const double w = (double)blocks / s + 8 + s;
-            if (w < tail) tail = w, split = s;
-        }
-        if (sp && rest) split = atoi(sp);
-        const double cost = t * (full / pairs * blocks + tail);
-        if (c.bn && cost >= best) continue;
-        best = cost;
-        c.bn = bn;
-        c.plan = Plan{(uint32_t)full, (uint32_t)rest, split, nullptr, nullptr};
-        const int64_t most = (bn / 2 + 31) / 32 * 32;
-        c.arrived_bytes = split > 1 ? (size_t)ceil_div(rest * 2 * kStoreWarps * 4, 256) * 256 : 0;
-        c.part_bytes = split > 1 ? (size_t)(rest * split) * 2 * kStoreWarps * most * 32 * 4 : 0;
+    for (const Choice c : {Choice{0, 224, 1}, Choice{0, 192, 1}, Choice{0, 128, 1}, Choice{0, 256, 2}, Choice{0, 128, 2}, Choice{0, 128, 4}}) {
+        if (p.dtype == kFP32 && c.bn == 224) continue;   // its sums do not fit the registers
+        if (only && atoi(only) != c.bn) continue;
+        if (sp && atoi(sp) != c.split) continue;
+        const int64_t tiles = ceil_div(p.a.rows, 2 * kRows) * ceil_div(p.b.rows, c.bn);
+        // a shared tile's cluster takes 4 or 8 SMs of one part of the GPU: 36 and 15 of them fit 152
+        if (c.split > 1 && (tiles > (c.split == 2 ? sms * 36 / 152 : sms * 15 / 152) || blocks < 8 * c.split)) continue;
+        // fp32 sums of a shared tile's part are not cut into segments
+        if (c.split > 1 && p.dtype == kFP32 && blocks > c.split * kSegment) continue;
+        // in cycles: an SM loads 64 bytes in one, (128 + bn / 2) * 128 for a block; the way into a
+        // pipeline and out of it, and that of the parts through distributed shared memory
+        const double cost = (256 + c.bn) * (c.split > 1 ? ceil_div(blocks, c.split) : ceil_div(tiles, pairs) * blocks) + (c.split > 1 ? 3500 : 0);
+        if (best.bn && cost >= least) continue;
+        least = cost;
+        best = c;
     }
-    return c;
+    return best;
 }
 
 // out = add, where K is 0.
@@ -844,13 +861,7 @@ __global__ void __launch_bounds__(256) mm_add_kernel(MatmulParams p) {
 
 }  // namespace
 
-size_t matmul_scratch_bytes(const MatmulParams &p, int sms) {
-    if (p.K == 0) return 0;
-    const Choice c = choose(p, sms);
-    return c.arrived_bytes + c.part_bytes;
-}
-
-cudaError_t launch_matmul(const MatmulParams &p, unsigned char *ws, int sms, cudaStream_t stream) {
+cudaError_t launch_matmul(const MatmulParams &p, int sms, cudaStream_t stream) {
     return with_dtype(p.dtype, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
         if (p.K == 0) {
@@ -860,18 +871,17 @@ cudaError_t launch_matmul(const MatmulParams &p, unsigned char *ws, int sms, cud
         const Choice c = choose(p, sms);
         MatmulArgs args;
         args.p = p;
-        args.plan = c.plan;
-        args.plan.arrived = reinterpret_cast<unsigned *>(ws);
-        args.plan.parts = reinterpret_cast<float *>(ws + c.arrived_bytes);
         switch (c.bt) {
             case 16: return run_tile<E, 16>(args, sms, stream);
             case 32: return run_tile<E, 32>(args, sms, stream);
             case 64: return run_tile<E, 64>(args, sms, stream);
         }
+        if (c.split == 4) return run_pair<E, 128, 4>(args, sms, stream);
+        if (c.split == 2) return c.bn == 128 ? run_pair<E, 128, 2>(args, sms, stream) : run_pair<E, 256, 2>(args, sms, stream);
         switch (c.bn) {
-            case 128: return run_pair<E, 128>(args, sms, stream);
-            case 192: return run_pair<E, 192>(args, sms, stream);
-            default: return run_pair<E, 224>(args, sms, stream);
+            case 128: return run_pair<E, 128, 1>(args, sms, stream);
+            case 192: return run_pair<E, 192, 1>(args, sms, stream);
+            default: return run_pair<E, 224, 1>(args, sms, stream);
         }
     });
 }

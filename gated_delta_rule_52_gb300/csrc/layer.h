@@ -159,7 +159,6 @@ struct MatmulParams {
     int64_t K;
     int *err;
 };
-size_t matmul_scratch_bytes(const MatmulParams &p, int sms);
-cudaError_t launch_matmul(const MatmulParams &p, unsigned char *ws, int sms, cudaStream_t stream);
+cudaError_t launch_matmul(const MatmulParams &p, int sms, cudaStream_t stream);
 
 }  // namespace kda

@@ -440,11 +440,8 @@ kda_status kda_fp8_matmul(const void *a, int64_t a_stride, int a_dtype, const vo
     p.add = add; p.as = add_stride;
     p.dtype = dtype;
     p.K = K;
-    int sms = 0;
-    if (kda::sm_count(sms) != cudaSuccess || kda::device_error_word(p.err) != cudaSuccess) return KDA_ERR_CUDA;
-    return with_workspace(kda::matmul_scratch_bytes(p, sms), stream, [&](unsigned char *ws, int n, cudaStream_t cs) {
-        return kda::launch_matmul(p, ws, n, cs);
-    });
+    if (kda::device_error_word(p.err) != cudaSuccess) return KDA_ERR_CUDA;
+    return with_workspace(0, stream, [&](unsigned char *, int n, cudaStream_t cs) { return kda::launch_matmul(p, n, cs); });
 }
 
 }  // extern "C"

@@ -406,13 +406,16 @@ __device__ __forceinline__ void mma_mx8_pair(uint32_t d_tmem, uint64_t adesc, ui
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate ? 1u : 0u)
         : "memory");
 }
-// Arrives once on the barrier at this address in both CTAs of the pair when all MMAs and copies
-// that this thread has issued are done.
-__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
+// Arrives once on the barrier at this address in the cluster's CTAs of `mask` (both of the pair) when
+// all MMAs and copies that this thread has issued are done.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar, uint16_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"(mask)
         : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 // One warp of each CTA of the pair executes these.
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst_smem, uint32_t ncols) {
