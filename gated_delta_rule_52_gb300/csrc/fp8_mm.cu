@@ -93,18 +93,17 @@ struct ScaleRows {
 };
 
 // ---- few rows of a: one tile of 128 rows of b by BT rows of a per cluster of `split` CTAs, which
-// share K and join their sums through distributed shared memory.  The rows of b, of which nearly
-// all bytes are, lie along the MMA's M, so that tiles are full however few rows a has.  Two CTAs
-// per SM keep about 170 KB of loads in flight.
+// share K and join their sums through distributed shared memory, each for a part of the rows of a.  The rows of b, of which nearly all bytes are, lie along the MMA's M, so that
+// tiles are full however few rows a has.  Two CTAs per SM keep up to 180 KB of loads in flight.
 template <int BT>
 struct TileShape {
     static constexpr int kStage = (kRows + BT) * kFp8Block;
     static constexpr int kScaleStage = 1024;
     static constexpr int kStages = (113 * 1024 - 2048 - kScaleStage * kScaleStages) / kStage;
     static constexpr int kSmem = 1024 + kStage * kStages + kScaleStage * kScaleStages;
+    static_assert(BT * kRows * 4 <= kStage * kStages, "the sums fit the ring");
     static constexpr int kSet = 8;                     // TMEM columns of scales
     static constexpr int kCols = BT + 2 * kSet <= 32 ? 32 : BT + 2 * kSet <= 64 ? 64 : 128;
-    static_assert(BT * kRows * 4 <= kStage * kStages, "the sums fit the ring");
 };
 
 template <typename E, int BT>
@@ -226,40 +225,60 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
     __syncwarp();
     if (!wait_for<false>(&done, 0, 2 * kWait)) ok = false;
     if (!ok && p.err) atomicExch(p.err, kErrTimeout);
-    __syncthreads();   // the ring is free: every copy and MMA has ended
+    __syncwarp();
     tc_fence_after();
-    // sums to shared memory, [BT][128]
-    float *sums = reinterpret_cast<float *>(ring);
-    for (int c = 0; c < BT; c += 16) {
-        float r[16];
-        tmem_ld16(tmem_addr(acc, warp * 32, c), r);
-        tmem_ld_wait();
+    const int64_t n = n0 + threadIdx.x;
+    E *to = static_cast<E *>(p.out) + m0 * p.os + n;
+    const E *plus = p.add ? static_cast<const E *>(p.add) + m0 * p.as + n : nullptr;
+    const int real = (int)min(p.a.rows - m0, (int64_t)BT), here = n < p.b.rows ? real : 0;   // rows of a: all, and those to store
+    if (split > 1) {
+        // the ring is free: every load and MMA has ended
+        float *sums = reinterpret_cast<float *>(ring) + threadIdx.x;   // [BT][128]
+        for (int c = 0; c < real; c += 16) {
+            float r[16];
+            tmem_ld16(tmem_addr(acc, warp * 32, c), r);
+            tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sums[(c + j) * kRows + threadIdx.x] = r[j];
+            for (int j = 0; j < 16; ++j) sums[(c + j) * kRows] = r[j];
+        }
+        cluster_sync();
+        const int rows = BT / split, c1 = min(rows * (rank + 1), real);
+        const uint32_t mine = smem_u32(sums);
+        for (int c = rows * rank; c < c1; c += 4) {      // 4 rows' sums on their way
+            float v[4][8], add[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = min(c + i, c1 - 1);
+                add[i] = plus && row < here ? to_f(plus[row * p.as]) : 0.f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (q < split) v[i][q] = ld_cluster(mapa_shared(mine + row * kRows * 4, q));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float t = v[i][0];
+#pragma unroll
+                for (int q = 1; q < 8; ++q)
+                    if (q < split) t += v[i][q];
+                if (c + i < min(c1, here)) to[(c + i) * p.os] = from_f<E>(plus ? t + add[i] : t);
+            }
+        }
+    } else {
+        for (int c = 0; c < BT; c += 16) {
+            float r[16], add[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) add[j] = plus && c + j < here ? to_f(plus[(c + j) * p.as]) : 0.f;
+            tmem_ld16(tmem_addr(acc, warp * 32, c), r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (c + j < here) to[(c + j) * p.os] = from_f<E>(plus ? r[j] + add[j] : r[j]);
+        }
     }
     tc_fence_before();
-    if (split > 1) cluster_sync();
+    if (split > 1) cluster_sync();   // the others have read this CTA's sums
     else __syncthreads();
     if (warp == 1) tmem_dealloc(acc, S::kCols);
-    // each CTA's part of the tile's rows of a
-    const int c0 = BT * rank / split, c1 = (int)min((int64_t)(BT * (rank + 1) / split), p.a.rows - m0);
-    const int64_t n = n0 + threadIdx.x;
-    const uint32_t mine = smem_u32(sums) + threadIdx.x * 4;
-#pragma unroll 2
-    for (int c = c0; c < c1; ++c) {
-        const int64_t m = m0 + c;
-        float v[8], t = 0.f;
-        if (p.add && n < p.b.rows) t = to_f(static_cast<const E *>(p.add)[m * p.as + n]);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (q < split) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[q]) : "r"(mapa_shared(mine + c * kRows * 4, q)) : "memory");
-        float u = v[0];
-#pragma unroll
-        for (int q = 1; q < 8; ++q)
-            if (q < split) u += v[q];
-        if (n < p.b.rows) static_cast<E *>(p.out)[m * p.os + n] = from_f<E>(p.add ? u + t : u);
-    }
-    if (split > 1) cluster_sync();   // the others have read this CTA's sums
 }
 
 // ---- tiles of 256 rows of a by BN rows of b, each of a pair of CTAs.
@@ -794,7 +813,9 @@ cudaError_t run_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
     // as many parts of K as two CTAs per SM hold, of 4 blocks or more
     const int64_t tiles = ceil_div(p.b.rows, kRows) * ceil_div(p.a.rows, BT), blocks = ceil_div(p.K, kFp8Block);
     int split = 1;
+    const char *sp = getenv("MM_SPLIT");
     while (split < 8 && tiles * split * 2 <= 2 * sms && blocks >= 8 * split) split *= 2;
+    if (sp) split = atoi(sp);
     cudaLaunchAttribute at;
     const cudaLaunchConfig_t c = cluster_launch(at, tiles * split, 128, S::kSmem, split, stream);
     return cudaLaunchKernelEx(&c, kernel, args, split);
