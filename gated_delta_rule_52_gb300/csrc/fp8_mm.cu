@@ -345,12 +345,18 @@ struct NarrowRows {
     float a[16];
     __device__ __forceinline__ NarrowRows(const MatmulParams &p, float *own, int64_t m0, int64_t n0, int lane)
         : p(p), own(own), m(m0 + (lane >> 4)), n0(n0), lane(lane), rows((int)min(max(p.a.rows - m, (int64_t)0), (int64_t)32)) {}
-    __device__ __forceinline__ void take_addend(int c) {
+    __device__ __forceinline__ void addend(int c, E (&to)[16]) const {
         const int64_t n = n0 + c + (lane & 15);
         const E *plus = static_cast<const E *>(p.add) + m * p.as + n;
         const int some = p.add && n < p.b.rows ? rows : 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) a[i] = 2 * i < some ? to_f(plus[2 * i * p.as]) : 0.f;
+        for (int i = 0; i < 16; ++i) to[i] = 2 * i < some ? plus[2 * i * p.as] : from_f<E>(0.f);
+    }
+    __device__ __forceinline__ void take_addend(int c) {
+        E t[16];
+        addend(c, t);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a[i] = to_f(t[i]);
     }
     // Columns c .. + 15, of which the addend was taken; `next`: it is taken for those behind them.
     __device__ __forceinline__ void store(const float (&r)[16], int c, bool next) {
@@ -398,6 +404,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     const int k_end = SPLIT > 1 ? min(k_begin + 4 * (each + (part < over)), blocks) : blocks;
     const int segment = kSums ? kSegment : blocks;
     if (threadIdx.x == 0) {
+        prefetch_map(&args.a);
+        prefetch_map(&args.b);
         for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         for (int i = 0; i < kScaleStages; ++i) mbar_init(&sfull[i], rank == 0 ? 33 : 32), mbar_init(&sempty[i], 1);
         for (int i = 0; i < S::kBuffers; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 2 * kStoreWarps);
@@ -579,7 +587,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                             if (c < cols) o[c / V] = ld_row<E, V>(plus + c, my_row ? (int)min(left - c, (int64_t)V) : 0);
                     }
                 }
-                if (!wide) narrow.take_addend(0);
+                E (&raw_o)[kSums ? V : kMost] = reinterpret_cast<E (&)[kSums ? V : kMost]>(o);
+                if (!wide) {
+                    if constexpr (kSums) {
+                        narrow.take_addend(0);
+                    } else if (plus) {
+#pragma unroll
+                        for (int c = 0; c < kMost; c += 16)
+                            if (c < cols) narrow.addend(c, reinterpret_cast<E (&)[16]>(raw_o[c]));
+                    }
+                }
                 for (int k = 0; k < blocks; k += segment) {
                     const int buf = sum.at;
                     ok = warp_wait<false>(&tfull[buf], sum.turn);
@@ -622,12 +639,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                         }
                     } else {
                         // rows that no wide access fits
-#pragma unroll 1
-                        for (int c = 0; c < cols; c += 16) {
+#pragma unroll
+                        for (int c = 0; c < kMost; c += 16) {
+                            if (c >= cols) break;
                             float r[16];
                             tmem_ld16(from + c, r);
                             tmem_ld_wait();
-                            narrow.store(r, c, c + 16 < cols);
+                            if (plus) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) narrow.a[i] = to_f(raw_o[c + i]);
+                            }
+                            narrow.store(r, c, false);
                         }
                     }
                     tc_fence_before();
@@ -902,8 +924,9 @@ cudaError_t launch_matmul(const MatmulParams &p, int sms, cudaStream_t stream) {
         switch (c.bn) {
             case 128: return run_pair<E, 128, 1>(args, sms, stream);
             case 192: return run_pair<E, 192, 1>(args, sms, stream);
-            default: return run_pair<E, 224, 1>(args, sms, stream);
         }
+        if constexpr (sizeof(E) == 2) return run_pair<E, 224, 1>(args, sms, stream);
+        return cudaErrorInvalidValue;
     });
 }
 

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(E) == 2 ? 4 : 2) quantiz
             }
             row_top[h][i] = Group::kPairs ? larger<E>(t, t >> 16) : t;
         }
-    const bool special = (any & Group::kSigns) != 0;   // this thread holds infinities or NaN
+    const bool special = __any_sync(0xffffffffu, (any & Group::kSigns) != 0);   // the warp holds infinities or NaN
     if (p.qt || p.tile) {
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
@@ -148,53 +148,60 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(E) == 2 ? 4 : 2) quantiz
             if (p.qt) p.st[bc * p.sts + br] = (uint8_t)tile_scale;
         }
     }
-    if (p.q) {
-        const bool whole = cols == 8 && p.qs % 8 == 0 && reinterpret_cast<uintptr_t>(p.q) % 8 == 0;
-        uint8_t *first = static_cast<uint8_t *>(p.q) + (r0 + 4 * rg) * p.qs + c;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                int e = tile_scale;
-                if (!p.tile) {
-                    uint32_t t = row_top[h][i];
-#pragma unroll
-                    for (int o = 8; o; o >>= 1) t = larger<E>(t, __shfl_xor_sync(0xffffffffu, t, o));
-                    e = scale_byte(number<E>(t), E5M2);
-                }
-                const int r = 64 * h + 4 * rg + i;
-                if (r >= rows || cols == 0) continue;
-                if (!p.tile && cg == 0) p.s[(r0 + r) * p.ss + bc] = (uint8_t)e;
-                float f[8];
-                v[h][i].values(f);
-                scale_n(f, inverse_scale(e));
-                const uint32_t lo = quad_to_fp8<E5M2>(f[0], f[1], f[2], f[3], special), hi = quad_to_fp8<E5M2>(f[4], f[5], f[6], f[7], special);
-                uint8_t *at = first + (64 * h + i) * p.qs;
-                if (whole) {
-                    *reinterpret_cast<uint2 *>(at) = make_uint2(lo, hi);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < cols) at[j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
-                }
-            }
-    }
-    if (!p.qt) return;
-    // four rows of a column are one word; word w of column c stands at place w + 2 (c / 8) of
-    // its line, so that a warp's words lie in 32 banks
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) {
-        constexpr int n = Group::kPairs ? 2 : 1;          // columns of a word
-#pragma unroll
-        for (int j = 0; j < n; ++j) {
-            const int col = 8 * cg + n * w + j;
-            const float inv = inverse_scale(p.tile ? tile_scale : col_scale[col]);
+    // to 8 bits, with a path of its own for infinities and NaN
+    const auto convert = [&](auto with_special) {
+        constexpr bool kSpecial = decltype(with_special)::value;
+        if (p.q) {
+            const bool whole = cols == 8 && p.qs % 8 == 0 && reinterpret_cast<uintptr_t>(p.q) % 8 == 0;
+            uint8_t *first = static_cast<uint8_t *>(p.q) + (r0 + 4 * rg) * p.qs + c;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                turned[col * 32 + ((16 * h + rg + 2 * cg) & 31)] =
-                    quad_to_fp8<E5M2>(v[h][0].value(w, j) * inv, v[h][1].value(w, j) * inv, v[h][2].value(w, j) * inv, v[h][3].value(w, j) * inv, special);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    int e = tile_scale;
+                    if (!p.tile) {
+                        uint32_t t = row_top[h][i];
+#pragma unroll
+                        for (int o = 8; o; o >>= 1) t = larger<E>(t, __shfl_xor_sync(0xffffffffu, t, o));
+                        e = scale_byte(number<E>(t), E5M2);
+                    }
+                    const int r = 64 * h + 4 * rg + i;
+                    if (r >= rows || cols == 0) continue;
+                    if (!p.tile && cg == 0) p.s[(r0 + r) * p.ss + bc] = (uint8_t)e;
+                    float f[8];
+                    v[h][i].values(f);
+                    scale_n(f, inverse_scale(e));
+                    const uint32_t lo = quad_to_fp8<E5M2>(f[0], f[1], f[2], f[3], kSpecial), hi = quad_to_fp8<E5M2>(f[4], f[5], f[6], f[7], kSpecial);
+                    uint8_t *at = first + (64 * h + i) * p.qs;
+                    if (whole) {
+                        *reinterpret_cast<uint2 *>(at) = make_uint2(lo, hi);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j < cols) at[j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
+                    }
+                }
         }
-    }
+        if (!p.qt) return;
+        // four rows of a column are one word; word w of column c stands at place w + 2 (c / 8) of
+        // its line, so that a warp's words lie in 32 banks
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            constexpr int n = Group::kPairs ? 2 : 1;          // columns of a word
+#pragma unroll
+            for (int j = 0; j < n; ++j) {
+                const int col = 8 * cg + n * w + j;
+                const float inv = inverse_scale(p.tile ? tile_scale : col_scale[col]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    turned[col * 32 + ((16 * h + rg + 2 * cg) & 31)] =
+                        quad_to_fp8<E5M2>(v[h][0].value(w, j) * inv, v[h][1].value(w, j) * inv, v[h][2].value(w, j) * inv, v[h][3].value(w, j) * inv, kSpecial);
+            }
+        }
+    };
+    if (special) convert(std::true_type{});
+    else convert(std::false_type{});
+    if (!p.qt) return;
     __syncthreads();
     // 8 lanes to a column, 16 rows each
     const bool words = p.qts % 16 == 0 && reinterpret_cast<uintptr_t>(p.qt) % 16 == 0;

@@ -188,6 +188,10 @@ __device__ __forceinline__ void tc_fence_after() {
 }
 
 // ------------------------------------------------------------------ TMA
+// Brings a tensor map nearer before its first use.
+__device__ __forceinline__ void prefetch_map(const void *tmap) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
 // 3-D tiled tensor load into shared memory, completing on `bar` (tx bytes).
 __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, uint64_t *bar, int c0,
                                             int c1, int c2) {
