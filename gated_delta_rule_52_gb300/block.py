@@ -1,6 +1,6 @@
 """A pre-norm recurrent block from the library's operators, trained and served.
 
-  python -m gated_delta_rule_52_gb300.block [--steps 60] [--width 256] [--tokens 512]
+  python -m gated_delta_rule_52_gb300.block [--steps 60] [--width 256] [--tokens 512] [--eight-bits]
 
 Each block is u + Wout(mix(conv(Win(norm(u))))): layer norm, a projection, the short
 convolution with SiLU on the part of it that is mixed (read in place from the projection's
@@ -8,6 +8,11 @@ output), and as the mixer either the gated linear recurrence or the delta rule (
 whose gate reads another part of the projection.  Training runs the operators' backward
 entry points through autograd; serving carries each block's convolution and recurrent state
 from a prefill to single tokens.  The task is to give back the input of three tokens ago.
+
+With --eight-bits the norm is the RMS norm and the projections are products of 8-bit tensors
+with a scale for each block of 128: in training tokens, weights and gradients are quantised for
+the forward product and for both of the backward pass; in serving the weights are quantised
+once, the norm adds the residual and writes 8 bits itself.
 """
 from __future__ import annotations
 
@@ -22,7 +27,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
-from gated_delta_rule_52_gb300 import build, glr, kda, layer_norm, short_conv  # noqa: E402
+from gated_delta_rule_52_gb300 import build, fp8, glr, kda, layer_norm, rms_norm, short_conv  # noqa: E402
 
 EPS = 1e-5
 LOWER_BOUND = -5.0
@@ -67,6 +72,59 @@ class Norm(torch.autograd.Function):
         x, weight, mean, rstd = ctx.saved_tensors
         r = layer_norm.layer_norm_bwd(dout.contiguous(), x, weight, mean, rstd)
         return r["dx"], r["dweight"], r["dbias"]
+
+
+class RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight):
+        out, rstd = torch.empty_like(x), torch.empty(x.shape[:-1], device=x.device)
+        rms_norm.rms_norm_fwd(x, weight, EPS, out, rstd=rstd)
+        ctx.save_for_backward(x, weight, rstd)
+        return out
+
+    @staticmethod
+    @first_order
+    def backward(ctx, dout):
+        x, weight, rstd = ctx.saved_tensors
+        r = rms_norm.rms_norm_bwd(dout.contiguous(), x, weight, rstd)
+        return r["dx"], r["dweight"]
+
+
+def eight_bits(t, tile=False, rows=True, turned=True, dtype=torch.float8_e4m3fn):
+    """The 8-bit forms of ``t`` [..., cols]: (q, scales), and those of its transpose."""
+    cols = t.shape[-1]
+    m = t.reshape(-1, cols)
+    q, s = fp8.empty(*m.shape, dtype, tile, t.device) if rows else (None, None)
+    qt, st = fp8.empty(cols, m.shape[0], dtype, tile, t.device) if turned else (None, None)
+    fp8.quantize(m, q, s, qt=qt, scales_t=st, tile=tile)
+    return q, s, qt, st
+
+
+class Linear(torch.autograd.Function):
+    """x W (+ add) of x [..., K] and W [K, N], in 8 bits: tokens and gradients with a scale for 128
+    neighbours, the gradients in e5m2 for their range, weights with one for a tile."""
+
+    @staticmethod
+    def forward(ctx, x, w, add):
+        q, s, xt, xts = eight_bits(x)
+        wn, wns, wt, wts = eight_bits(w, tile=True)              # W [K, N], and W^T [N, K]
+        out = torch.empty(*x.shape[:-1], w.shape[1], dtype=x.dtype, device=x.device)
+        fp8.matmul(q, s, wt, wts, out.view(-1, w.shape[1]), add=None if add is None else add.reshape(-1, w.shape[1]))
+        # (x and w themselves for first_order: gradients depend on them, too)
+        ctx.save_for_backward(xt, xts, wn, wns, x, w)
+        ctx.added = add is not None
+        return out
+
+    @staticmethod
+    @first_order
+    def backward(ctx, dout):
+        xt, xts, wn, wns, x, w = ctx.saved_tensors
+        d, ds, dt, dts = eight_bits(dout, dtype=torch.float8_e5m2)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        fp8.matmul(d, ds, wn, wns, dx.view(-1, x.shape[-1]))
+        dw = torch.empty(w.shape, dtype=torch.float32, device=w.device)
+        fp8.matmul(xt, xts, dt, dts, dw)
+        return dx, dw.to(w.dtype), dout if ctx.added else None
 
 
 class Conv(torch.autograd.Function):
@@ -120,10 +178,11 @@ class DeltaRule(torch.autograd.Function):
 
 
 class Block:
-    """One block of ``width`` channels; ``kind`` "glr" or "kda" (heads of 128 channels)."""
+    """One block of ``width`` channels; ``kind`` "glr" or "kda" (heads of 128 channels); ``eight``:
+    RMS norm and projections in 8 bits."""
 
-    def __init__(self, kind, width, gen, dev="cuda"):
-        self.kind, self.width, self.heads = kind, width, width // 128
+    def __init__(self, kind, width, gen, dev="cuda", eight=False):
+        self.kind, self.width, self.heads, self.eight, self.served = kind, width, width // 128, eight, None
         n = lambda *s, std: (torch.randn(s, generator=gen) * std).to(dev)  # noqa: E731
         self.mixed = width if kind == "glr" else 3 * width       # x, or q, k, v: what the convolution reads
         wide = self.mixed + (2 * width if kind == "glr" else width + self.heads)
@@ -133,6 +192,8 @@ class Block:
                   "conv_w": n(self.mixed, 4, std=0.5), "conv_b": torch.zeros(self.mixed, device=dev),
                   "A_log": torch.zeros(self.heads, device=dev),
                   "dt_bias": torch.full((self.heads, 128), -3.0, device=dev)}
+        if eight:
+            del self.p["norm_b"]
         for t in self.p.values():
             t.requires_grad_()
 
@@ -146,11 +207,14 @@ class Block:
         return q, k, v, heads(rest[..., :self.width]), rest[..., self.width:]
 
     def train(self, u):
-        p = self.p
-        z = Norm.apply(u, p["norm_w"], p["norm_b"]) @ p["w_in"]
+        p, self.served = self.p, None
+        if self.eight:
+            z = Linear.apply(RmsNorm.apply(u, p["norm_w"]), p["w_in"], None)
+        else:
+            z = Norm.apply(u, p["norm_w"], p["norm_b"]) @ p["w_in"]
         parts = self._parts(z, Conv.apply(z[..., :self.mixed], p["conv_w"], p["conv_b"]))
         mix = (Recurrence if self.kind == "glr" else DeltaRule).apply(*parts, p["A_log"], p["dt_bias"])
-        return u + mix.flatten(2) @ p["w_out"]
+        return Linear.apply(mix.flatten(2), p["w_out"], u) if self.eight else u + mix.flatten(2) @ p["w_out"]
 
     def state(self, B, dev="cuda"):
         """Zero states for serving: the convolution's last inputs and the recurrent state."""
@@ -163,7 +227,32 @@ class Block:
         p = self.p
         y = torch.empty_like(u)
         layer_norm.layer_norm_fwd(u, p["norm_w"], p["norm_b"], EPS, y)
-        z = y @ p["w_in"]
+        return u + self._mix(y @ p["w_in"], state).flatten(2) @ p["w_out"]
+
+    @torch.no_grad()
+    def serve_eight(self, u, delta, state):
+        """serve() in 8 bits.  ``delta``, what the block before adds to the residual stream ``u``, or
+        None, is added by the norm, u in place; returns what this block adds."""
+        p = self.p
+        if self.served is None:
+            self.served = [eight_bits(p[n], tile=True, rows=False)[2:] for n in ("w_in", "w_out")]
+        (w_in, s_in), (w_out, s_out) = self.served
+        rows = u.view(-1, self.width)
+        q, s = fp8.empty(*rows.shape, device=u.device)
+        if delta is None:
+            rms_norm.rms_norm_fwd(rows, p["norm_w"], EPS, q, scales=s)
+        else:
+            rms_norm.rms_norm_fwd(delta.view(-1, self.width), p["norm_w"], EPS, q, residual=rows, residual_out=rows, scales=s)
+        z = torch.empty(*u.shape[:2], w_in.shape[0], dtype=u.dtype, device=u.device)
+        fp8.matmul(q, s, w_in, s_in, z.view(-1, w_in.shape[0]))
+        fp8.quantize(self._mix(z, state).reshape(rows.shape), q, s)
+        out = torch.empty_like(u)
+        fp8.matmul(q, s, w_out, s_out, out.view(rows.shape))
+        return out
+
+    def _mix(self, z, state):
+        """The mixer's output from the projection's, by way of the convolution."""
+        p, u = self.p, z
         c = torch.empty(*u.shape[:2], self.mixed, dtype=u.dtype, device=u.device)
         short_conv.short_conv_fwd(z[..., :self.mixed], p["conv_w"], p["conv_b"], c, initial_state=state["conv"],
                                   final_state=state["conv"])
@@ -176,7 +265,7 @@ class Block:
             mix, last = torch.empty_like(parts[2]), torch.empty_like(state["mix"])
             kda.kda_fwd(*parts, 128 ** -0.5, mix, p["A_log"], p["dt_bias"], LOWER_BOUND, initial_state=state["mix"], final_state=last)
             state["mix"] = last
-        return u + mix.flatten(2) @ p["w_out"]
+        return mix
 
 
 def train(blocks, steps, B, T, gen, lr=2e-3):
@@ -204,14 +293,19 @@ def train(blocks, steps, B, T, gen, lr=2e-3):
 
 @torch.no_grad()
 def serve(blocks, u, prompt):
-    """The stack's outputs with ``prompt`` tokens in one call and the others one by one."""
+    """The outputs of a stack (all of its blocks in 8 bits, or none) with ``prompt`` tokens in one call
+    and the others one by one."""
     states = [b.state(u.shape[0]) for b in blocks]
     outs = []
     for lo, hi in [(0, prompt)] + [(t, t + 1) for t in range(prompt, u.shape[1])]:
-        h = u[:, lo:hi].contiguous()
+        h = u[:, lo:hi].clone(memory_format=torch.contiguous_format)
+        delta = None
         for b, s in zip(blocks, states):
-            h = b.serve(h, s)
-        outs.append(h)
+            if b.eight:
+                delta = b.serve_eight(h, delta, s)
+            else:
+                h = b.serve(h, s)
+        outs.append(h if delta is None else h + delta)
     return torch.cat(outs, 1)
 
 
@@ -221,10 +315,11 @@ def main(argv=None):
     ap.add_argument("--width", type=int, default=256)
     ap.add_argument("--batch", type=int, default=4)
     ap.add_argument("--tokens", type=int, default=512)
+    ap.add_argument("--eight-bits", action="store_true")
     a = ap.parse_args(argv)
     build.build_library()
     gen = torch.Generator().manual_seed(0)
-    blocks = [Block(kind, a.width, gen) for kind in ("glr", "kda")]
+    blocks = [Block(kind, a.width, gen, eight=a.eight_bits) for kind in ("glr", "kda")]
     losses = train(blocks, a.steps, a.batch, a.tokens, gen)
     u = torch.randn(a.batch, 96, a.width, generator=gen).to("cuda", torch.bfloat16)
     whole, stepped = serve(blocks, u, 96), serve(blocks, u, 80)

@@ -5,7 +5,6 @@
 // block take the same byte.  4 blocks' bytes of a row are one 4-byte word, the unit in which
 // scales are loaded and put into TMEM.
 #include <algorithm>
-#include <cstdlib>
 #include <cuda.h>
 
 #include "kda_chunk.cuh"
@@ -835,9 +834,7 @@ cudaError_t run_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
     // as many parts of K as two CTAs per SM hold, of 4 blocks or more
     const int64_t tiles = ceil_div(p.b.rows, kRows) * ceil_div(p.a.rows, BT), blocks = ceil_div(p.K, kFp8Block);
     int split = 1;
-    const char *sp = getenv("MM_SPLIT");
     while (split < 8 && tiles * split * 2 <= 2 * sms && blocks >= 8 * split) split *= 2;
-    if (sp) split = atoi(sp);
     cudaLaunchAttribute at;
     const cudaLaunchConfig_t c = cluster_launch(at, tiles * split, 128, S::kSmem, split, stream);
     return cudaLaunchKernelEx(&c, kernel, args, split);
@@ -873,11 +870,8 @@ Choice choose(const MatmulParams &p, int sms) {
     const int64_t pairs = sms / 2, blocks = ceil_div(p.K, kFp8Block);
     Choice best = {};
     double least = 0;
-    const char *only = getenv("MM_BN"), *sp = getenv("MM_SPLIT");
     for (const Choice c : {Choice{0, 224, 1}, Choice{0, 192, 1}, Choice{0, 128, 1}, Choice{0, 256, 2}, Choice{0, 128, 2}, Choice{0, 128, 4}}) {
         if (p.dtype == kFP32 && c.bn == 224) continue;   // its sums do not fit the registers
-        if (only && atoi(only) != c.bn) continue;
-        if (sp && atoi(sp) != c.split) continue;
         const int64_t tiles = ceil_div(p.a.rows, 2 * kRows) * ceil_div(p.b.rows, c.bn);
         // a shared tile's cluster takes 4 or 8 SMs of one part of the GPU: 36 and 15 of them fit 152
         if (c.split > 1 && (tiles > (c.split == 2 ? sms * 36 / 152 : sms * 15 / 152) || blocks < 8 * c.split)) continue;

@@ -53,10 +53,10 @@ struct Eight {
             for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
         }
     }
-    __device__ __forceinline__ float value(int i, int j) const {   // element j of word i
-        if constexpr (std::is_same_v<E, __nv_bfloat16>) return __uint_as_float(j ? w[i] & 0xffff0000u : w[i] << 16);
-        else if constexpr (kPairs) return to_f(reinterpret_cast<const E *>(w)[2 * i + j]);
-        else return __uint_as_float(w[i]);
+    __device__ __forceinline__ float2 two(int j) const {   // elements j and j + 1, j even
+        if constexpr (std::is_same_v<E, __nv_bfloat16>) return sm103::bf16x2_to_f2(w[j / 2]);
+        else if constexpr (kPairs) return __half22float2(reinterpret_cast<const __half2 *>(w)[j / 2]);
+        else return make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
     }
     __device__ __forceinline__ uint32_t magnitude(int i) const { return (w[i] & kMask) + kShift; }
 };
@@ -148,6 +148,22 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(E) == 2 ? 4 : 2) quantiz
             if (p.qt) p.st[bc * p.sts + br] = (uint8_t)tile_scale;
         }
     }
+    // maxima of the rows over the 16 lanes that share them, 16-bit ones two rows to a word
+    if (p.q && !p.tile) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            constexpr int n = Group::kPairs ? 2 : 4;
+            uint32_t t[n];
+#pragma unroll
+            for (int i = 0; i < n; ++i) t[i] = Group::kPairs ? (row_top[h][2 * i] & 0xffffu) | row_top[h][(2 * i + 1) & 3] << 16 : row_top[h][i];
+#pragma unroll
+            for (int o = 8; o; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < n; ++i) t[i] = larger<E>(t[i], __shfl_xor_sync(0xffffffffu, t[i], o));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) row_top[h][i] = Group::kPairs ? (i & 1 ? t[i / 2] >> 16 : t[i / 2] & 0xffffu) : t[i % n];
+        }
+    }
     // to 8 bits, with a path of its own for infinities and NaN
     const auto convert = [&](auto with_special) {
         constexpr bool kSpecial = decltype(with_special)::value;
@@ -158,13 +174,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(E) == 2 ? 4 : 2) quantiz
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    int e = tile_scale;
-                    if (!p.tile) {
-                        uint32_t t = row_top[h][i];
-#pragma unroll
-                        for (int o = 8; o; o >>= 1) t = larger<E>(t, __shfl_xor_sync(0xffffffffu, t, o));
-                        e = scale_byte(number<E>(t), E5M2);
-                    }
+                    const int e = p.tile ? tile_scale : scale_byte(number<E>(row_top[h][i]), E5M2);
                     const int r = 64 * h + 4 * rg + i;
                     if (r >= rows || cols == 0) continue;
                     if (!p.tile && cg == 0) p.s[(r0 + r) * p.ss + bc] = (uint8_t)e;
@@ -186,16 +196,18 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(E) == 2 ? 4 : 2) quantiz
         // four rows of a column are one word; word w of column c stands at place w + 2 (c / 8) of
         // its line, so that a warp's words lie in 32 banks
 #pragma unroll
-        for (int w = 0; w < kWords; ++w) {
-            constexpr int n = Group::kPairs ? 2 : 1;          // columns of a word
+        for (int j = 0; j < 8; j += 2) {                      // two columns at a time
+            float2 inv;
+            inv.x = inverse_scale(p.tile ? tile_scale : col_scale[8 * cg + j]);
+            inv.y = inverse_scale(p.tile ? tile_scale : col_scale[8 * cg + j + 1]);
 #pragma unroll
-            for (int j = 0; j < n; ++j) {
-                const int col = 8 * cg + n * w + j;
-                const float inv = inverse_scale(p.tile ? tile_scale : col_scale[col]);
+            for (int h = 0; h < 2; ++h) {
+                float2 f[4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    turned[col * 32 + ((16 * h + rg + 2 * cg) & 31)] =
-                        quad_to_fp8<E5M2>(v[h][0].value(w, j) * inv, v[h][1].value(w, j) * inv, v[h][2].value(w, j) * inv, v[h][3].value(w, j) * inv, kSpecial);
+                for (int i = 0; i < 4; ++i) f[i] = sm103::mul2(v[h][i].two(j), inv);
+                uint32_t *to = &turned[(8 * cg + j) * 32 + ((16 * h + rg + 2 * cg) & 31)];
+                to[0] = quad_to_fp8<E5M2>(f[0].x, f[1].x, f[2].x, f[3].x, kSpecial);
+                to[32] = quad_to_fp8<E5M2>(f[0].y, f[1].y, f[2].y, f[3].y, kSpecial);
             }
         }
     };
@@ -232,30 +244,43 @@ __device__ __forceinline__ float scale_of(int byte) {
     return byte == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)max(byte, 1) << 23);
 }
 
-// V neighbouring elements per thread.
+// A warp takes kTurns pieces of 32 V neighbouring elements of a row, V to a lane.
+template <int V> constexpr int Turns = V == 1 ? 4 : 2;
+
 template <typename E, int V>
-__global__ void __launch_bounds__(256) dequantize_kernel(QuantParams p) {
-    const int64_t groups = ceil_div(p.cols, V), all = groups * p.rows;
+__global__ void __launch_bounds__(256) dequantize_kernel(QuantParams p, uint32_t pieces) {
+    constexpr int kTurns = Turns<V>;
     const bool e5m2 = p.q_dtype == kE5M2;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / groups, c = (i - r * groups) * V;
-        const int byte = p.s[(p.tile ? r / kTile : r) * p.ss + c / kTile];
-        const float s = scale_of(byte), half = byte == 0 ? 0.5f : 1.f;
-        const uint8_t *q = static_cast<const uint8_t *>(p.q) + r * p.qs + c;
-        E *at = static_cast<E *>(const_cast<void *>(p.x)) + r * p.xs + c;
+    const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5), row = item / pieces;
+    if (row >= p.rows) return;
+    const int64_t r = row, first = (int64_t)(item - row * pieces) * (32 * V * kTurns) + (threadIdx.x & 31) * V;
+    const uint8_t *q = static_cast<const uint8_t *>(p.q) + r * p.qs, *s = p.s + (p.tile ? r / kTile : r) * p.ss;
+    E *out = static_cast<E *>(const_cast<void *>(p.x)) + r * p.xs;
+    Pack<uint8_t, V> in[kTurns];
+    uint8_t scale[kTurns];
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int64_t c = first + k * 32 * V;
+        if (c < p.cols) in[k] = *reinterpret_cast<const Pack<uint8_t, V> *>(q + c), scale[k] = s[c / kTile];
+    }
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int64_t c = first + k * 32 * V;
+        if (c >= p.cols) break;
+        const int byte = scale[k];
+        const float f = scale_of(byte), half = byte == 0 ? 0.5f : 1.f;
         if constexpr (V == 1) {
-            at[0] = from_f<E>(pair_from_fp8(q[0], e5m2).x * half * s);
+            out[c] = from_f<E>(pair_from_fp8(in[k].e[0], e5m2).x * half * f);
         } else {
-            const Pack<uint32_t, V / 4> w = *reinterpret_cast<const Pack<uint32_t, V / 4> *>(q);
-            float f[V];
+            float v[V];
 #pragma unroll
             for (int j = 0; j < V; j += 2) {
-                const float2 t = pair_from_fp8(w.e[j / 4] >> (8 * (j & 2)), e5m2);
-                f[j] = t.x * half * s, f[j + 1] = t.y * half * s;
+                const float2 t = pair_from_fp8(reinterpret_cast<const uint16_t *>(in[k].e)[j / 2], e5m2);
+                v[j] = t.x * half * f, v[j + 1] = t.y * half * f;
             }
             constexpr int P = 16 / sizeof(E);
 #pragma unroll
-            for (int j = 0; j < V; j += P) st_f<E, P>(at + j, reinterpret_cast<const float (&)[P]>(f[j]));
+            for (int j = 0; j < V; j += P) st_f<E, P>(out + c + j, reinterpret_cast<const float (&)[P]>(v[j]));
         }
     }
 }
@@ -283,10 +308,9 @@ cudaError_t launch_dequantize(const QuantParams &p, int sms, cudaStream_t stream
         using E = std::remove_pointer_t<decltype(tag)>;
         const bool wide = p.cols % 16 == 0 && p.qs % 16 == 0 && reinterpret_cast<uintptr_t>(p.q) % 16 == 0 &&
                           reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.xs % (16 / sizeof(E)) == 0;
-        const int64_t n = p.rows * ceil_div(p.cols, wide ? 16 : 1);
-        const unsigned grid = (unsigned)std::min(ceil_div(n, 256), (int64_t)sms * 16);
-        if (wide) dequantize_kernel<E, 16><<<grid, 256, 0, stream>>>(p);
-        else dequantize_kernel<E, 1><<<grid, 256, 0, stream>>>(p);
+        const int64_t pieces = ceil_div(p.cols, 32 * (wide ? 16 * Turns<16> : Turns<1>)), grid = ceil_div(pieces * p.rows, 8);
+        if (wide) dequantize_kernel<E, 16><<<(unsigned)grid, 256, 0, stream>>>(p, (uint32_t)pieces);
+        else dequantize_kernel<E, 1><<<(unsigned)grid, 256, 0, stream>>>(p, (uint32_t)pieces);
         return cudaGetLastError();
     });
 }

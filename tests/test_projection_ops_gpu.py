@@ -239,3 +239,236 @@ def test_rms_norm(rows, D, dt, out8, residual, weight, how):
     assert_close("dx", got["dx"], dx, E + 2.0 ** -23 * (0 if dres is None else dres.double().abs()))
     # the columns' sums: rows one after the other in a part, parts in turn
     assert_close("dweight", got["dweight"], dw, (min(rows, 512) + 40) * 2.0 ** -23 * (dy.double() * hat).abs().sum(0))
+
+
+# ------------------------------------------------------------------ calls of other kinds
+def test_norm_product_and_gradients_in_a_row():
+    """A norm in 8 bits, the product that reads it, and the backward pass's: each step against its
+    64-bit reference on what the step before wrote."""
+    M, K, N = 150, 384, 300
+    g = _gen(11)
+    x, res, w = torch.randn(M, K, generator=g).to(BF), torch.randn(M, K, generator=g).to(BF), 1 + 0.2 * torch.randn(K, generator=g)
+    W, dy = torch.randn(N, K, generator=g) * K ** -0.5, torch.randn(M, N, generator=g).to(BF) * 1e-3
+    q, s = fp8.empty(M, K)
+    h, rstd = torch.empty(M, K, dtype=BF, device="cuda"), torch.empty(M, device="cuda")
+    rms_norm.rms_norm_fwd(x.cuda(), w.cuda(), EPS, q, residual=res.cuda(), residual_out=h, rstd=rstd, scales=s)
+    wq, ws = fp8.empty(N, K, tile=True)
+    wt, wts = fp8.empty(K, N, tile=True)
+    fp8.quantize(W.cuda(), wq, ws, qt=wt, scales_t=wts, tile=True)
+    y = torch.empty(M, N, dtype=BF, device="cuda")
+    fp8.matmul(q, s, wq, ws, y)
+    d, ds = fp8.empty(M, N, E5)
+    dt, dts = fp8.empty(N, M, E5)
+    fp8.quantize(dy.cuda(), d, ds, qt=dt, scales_t=dts)
+    xt, xts = fp8.empty(K, M)
+    plain = torch.empty(M, K, dtype=BF, device="cuda")
+    fp8.dequantize(q, s, plain)
+    fp8.quantize(plain, qt=xt, scales_t=xts)
+    dn, dW = torch.empty(M, K, dtype=BF, device="cuda"), torch.ones(N, K, device="cuda")
+    fp8.matmul(d, ds, wt, wts, dn)
+    fp8.matmul(dt, dts, xt, xts, dW, add=dW)
+    r = rms_norm.rms_norm_bwd(dn, h, w.cuda(), rstd, dresidual=h)
+    _status()
+    hh, yy, rr = ref.rms(x, res, w, EPS)
+    _close8("norm", q, s, yy, 2 * _sum_err(K) * yy.abs())
+    for name, got, a, sa, b, sb, add in (("y", y, q, s, wq, ws, None), ("dn", dn, d, ds, wt, wts, None), ("dW", dW, dt, dts, xt, xts, torch.ones(N, K))):
+        want = ref.product(a, sa, b, sb, add)
+        assert_close(name, got, want, ref.product_bound(a, sa, b, sb) + 2.0 ** -23 * want.abs())
+    dx, dw = ref.rms_grads(hh, w.double(), rstd.cpu().double(), dn.cpu().double(), hh)
+    mag = rr[:, None] * (dn.cpu().double() * w.double()).abs() * (1 + (hh * rr[:, None]).abs()) + hh.abs()
+    assert_close("dx", r["dx"], dx, D32 * mag.amax(1, keepdim=True).expand_as(mag))
+
+
+def _everything(M=70, K=640, N=520, big=300):
+    """Every operator on inputs of its own: the call, and the tensors that it writes."""
+    g = _gen(5)
+    c = lambda *s: torch.randn(*s, generator=g).to(BF).cuda()  # noqa: E731
+    x, res, w = c(M, K), c(M, K), c(K).float()
+    q, s = fp8.empty(M, K)
+    h, rstd, y16 = torch.zeros(M, K, dtype=BF, device="cuda"), torch.zeros(M, device="cuda"), torch.zeros(M, K, dtype=BF, device="cuda")
+    qt, st = fp8.empty(K, M)
+    b, sb = fp8.empty(N, K, tile=True)
+    a2, sa2 = fp8.empty(big, K)
+    fp8.quantize(c(N, K), b, sb, tile=True)
+    fp8.quantize(c(big, K), a2, sa2)
+    few, many = torch.zeros(M, N, dtype=BF, device="cuda"), torch.zeros(big, N, device="cuda")
+    one = torch.zeros(1, N, dtype=BF, device="cuda")
+
+    def call(stream=None):
+        rms_norm.rms_norm_fwd(x, w, EPS, q, residual=res, residual_out=h, rstd=rstd, scales=s, stream=stream)
+        fp8.matmul(q, s, b, sb, few, stream=stream)
+        fp8.matmul(q[:1], s[:1], b, sb, one, stream=stream)
+        fp8.matmul(a2, sa2, b, sb, many, stream=stream)
+        fp8.quantize(h, qt=qt, scales_t=st, stream=stream)
+        fp8.dequantize(q, s, y16, stream=stream)
+        return rms_norm.rms_norm_bwd(x, h, w, rstd, dresidual=res, stream=stream)
+
+    return call, (x, res), (q, s, h, rstd, few, one, many, qt, st, y16)
+
+
+def _bits(t):
+    return t.contiguous().view(torch.uint8).clone()
+
+
+def test_same_bits_every_time_and_on_another_stream():
+    call, _, outs = _everything()
+    r = call()
+    want = [_bits(t) for t in (*outs, r["dx"], r["dweight"])]
+    for t in outs:
+        t.view(torch.uint8).zero_() if t.element_size() == 1 else t.zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    r = call(side)
+    torch.cuda.current_stream().wait_stream(side)
+    for t, w in zip((*outs, r["dx"], r["dweight"]), want):
+        assert torch.equal(_bits(t), w)
+    _status()
+
+
+def test_captured_and_replayed_on_new_inputs():
+    call, (x, res), outs = _everything()
+    call()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):                                        # two graphs of the same calls
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r = call()
+        graphs.append((g, r))
+    x.copy_(-2 * x)
+    res.copy_(res.flip(0))
+    for g, r in graphs:
+        g.replay()
+        torch.cuda.synchronize()
+        got = [_bits(t) for t in (*outs, r["dx"], r["dweight"])]
+        e = call()
+        torch.cuda.synchronize()
+        for a, b in zip(got, (*outs, e["dx"], e["dweight"])):
+            assert torch.equal(a, _bits(b))
+    _status()
+
+
+def test_two_streams_at_once():
+    first, second = _everything(), _everything(M=64, K=512, N=1000, big=600)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    want = []
+    for call, _, outs in (first, second):
+        call()
+        want.append([_bits(t) for t in outs])
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, (call, _, _) in zip(streams, (first, second)):
+            call(st)
+    torch.cuda.synchronize()
+    for w, (_, _, outs) in zip(want, (first, second)):
+        for a, b in zip(w, outs):
+            assert torch.equal(a, _bits(b))
+    _status()
+
+
+@pytest.mark.parametrize("M", [1, 40, 200, 600])
+@pytest.mark.parametrize("N", [264, 301])
+def test_addend_in_place_and_rows_of_a_wider_tensor(M, N):
+    g = _gen(M + N)
+    a, sa = _small_operand(M, 300, E4, False, g)
+    b, sb = _small_operand(N, 300, E4, True, g)
+    wide = torch.full((M, N + 24), 7.0, dtype=BF, device="cuda")
+    out = wide[:, 8:8 + N]
+    out.copy_(torch.randint(-5, 6, (M, N), generator=g).to(BF))
+    want = ref.product(a, sa, b, sb, out).float().to(BF)
+    fp8.matmul(a, sa, b, sb, out, add=out)
+    _status()
+    assert torch.equal(out.cpu(), want)
+    assert (wide[:, :8] == 7).all() and (wide[:, 8 + N:] == 7).all()
+
+
+@pytest.mark.parametrize("M", [3, 70, 300])
+def test_rows_that_are_not_finite_stay_alone(M):
+    g = _gen(M)
+    a, sa = _small_operand(M, 200, E4, False, g)
+    b, sb = _small_operand(260, 200, E5, True, g)
+    out = torch.empty(M, 260, device="cuda")
+    want = ref.product(a, sa, b, sb)
+    a.view(torch.uint8)[1, 130] = 0x7f                        # NaN
+    sa.view(torch.uint8)[2, 0] = 255                          # a scale of NaN
+    b.view(torch.uint8)[9, 3] = 0x7c                          # infinity in e5m2
+    fp8.matmul(a, sa, b, sb, out)
+    _status()
+    got = out.cpu()
+    assert got[1:3].isnan().all()
+    keep = [i for i in range(M) if i not in (1, 2)]
+    assert not got[keep][:, 9].isfinite().any()
+    cols = [j for j in range(260) if j != 9]
+    assert torch.equal(got[keep][:, cols].double(), want[keep][:, cols])
+
+
+def test_nothing_to_sum_and_nothing_to_write():
+    for M, N in ((5, 300), (300, 5)):
+        a, sa = fp8.empty(M, 0)
+        b, sb = fp8.empty(N, 0)
+        add = torch.randn(M, N, device="cuda")
+        out = torch.full((M, N), float("nan"), device="cuda")
+        fp8.matmul(a, sa, b, sb, out, add=add)
+        assert torch.equal(out, add)
+        fp8.matmul(a, sa, b, sb, out)
+        assert (out == 0).all()
+    a, sa = fp8.empty(0, 128)
+    b, sb = fp8.empty(4, 128)
+    fp8.matmul(a, sa, b, sb, torch.empty(0, 4, device="cuda"))
+    fp8.quantize(torch.empty(0, 128, device="cuda"), a, sa)
+    r = rms_norm.rms_norm_bwd(torch.empty(0, 8, device="cuda"), torch.empty(0, 8, device="cuda"), torch.ones(8, device="cuda"), torch.empty(0, device="cuda"))
+    assert r["dx"].shape == (0, 8) and (r["dweight"] == 0).all()
+    _status()
+
+
+def test_norm_in_place():
+    g = _gen(3)
+    for D in (512, 333, 20000):
+        x, res, w = torch.randn(6, D, generator=g).to(BF), torch.randn(6, D, generator=g).to(BF), torch.randn(D, generator=g).cuda()
+        out, total = torch.empty(6, D, dtype=BF, device="cuda"), torch.empty(6, D, dtype=BF, device="cuda")
+        rms_norm.rms_norm_fwd(x.cuda(), w, EPS, out, residual=res.cuda(), residual_out=total)
+        a, b = x.cuda(), res.cuda()
+        rms_norm.rms_norm_fwd(a, w, EPS, a, residual=b, residual_out=b)          # out over x, the sum over the residual
+        assert torch.equal(a, out) and torch.equal(b, total)
+        a, b = x.cuda(), res.cuda()
+        rms_norm.rms_norm_fwd(a, w, EPS, b, residual=b, residual_out=a)          # the other way round
+        assert torch.equal(b, out) and torch.equal(a, total)
+        a = x.cuda()
+        rms_norm.rms_norm_fwd(a, w, EPS, a, residual=res.cuda())
+        assert torch.equal(a, out)
+    _status()
+
+
+@pytest.mark.parametrize("M", [2, 129])
+def test_offsets_beyond_32_bits(M):
+    """Rows of a, of the output and of a quantised tensor 2^25 bytes or more apart, so that the last
+    ones lie beyond 2^32."""
+    K, N = 256, 136
+    g = _gen(M)
+    step = (1 << 32) // (M - 1) // 16 * 16 + 4096
+    room = torch.empty(step * (M - 1) + 4096, dtype=torch.uint8, device="cuda")
+    a = room.view(E4).as_strided((M, K), (step, 1))
+    small, sa = _small_operand(M, K, E4, False, g)
+    a.copy_(small)
+    b, sb = _small_operand(N, K, E4, False, g)
+    out = torch.empty(M, N, device="cuda")
+    fp8.matmul(a, sa, b, sb, out)
+    want = ref.product(small, sa, b, sb)
+    assert torch.equal(out.cpu().double(), want)
+    back = torch.empty(M, K, device="cuda")
+    fp8.dequantize(a, sa, back)
+    assert torch.equal(back.cpu().double(), ref.values(small, sa))
+    far = room.view(F).as_strided((M, N), (step // 4, 1))      # the output there
+    fp8.matmul(small, sa, b, sb, far)
+    assert torch.equal(far.cpu().double(), want)
+    q, s = a, fp8.empty(M, K)[1]
+    fp8.quantize(back, q, s)
+    assert torch.equal(ref.values(q, s), ref.quantized(back.cpu().double(), E4)[0])
+    x = room.view(BF).as_strided((M, K), (step // 2, 1))       # the norm's rows
+    x.copy_(torch.randn(M, K, generator=g).to(BF))
+    y = torch.empty(M, K, dtype=BF, device="cuda")
+    rms_norm.rms_norm_fwd(x, None, EPS, y)
+    z = torch.empty_like(y)
+    rms_norm.rms_norm_fwd(x.contiguous(), None, EPS, z)
+    assert torch.equal(y, z)
+    _status()
