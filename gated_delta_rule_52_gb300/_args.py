@@ -8,6 +8,8 @@ A decode step's call costs more on the host than on the GPU, so the checks look 
 contiguous tensor once and take the current stream's handle without building a Stream."""
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import kda
@@ -97,6 +99,17 @@ def rows(name, t, dtype, shape, lead: int, width: int, dev: int | None = None) -
         else:
             raise ValueError(f"{name}: rows must be evenly spaced")
     return width if stride is None else stride
+
+
+def matrix(name, t, dtype, shape, lead: int, dev: int) -> tuple:
+    """Data pointer and row stride of a tensor for ``rows``; one of two dimensions, which costs the
+    host least, with a look at each attribute."""
+    if isinstance(t, torch.Tensor) and len(shape) == 2 and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        step = t.stride()
+        if step[1] == 1:
+            return t.data_ptr(), shape[1] if shape[0] == 1 else step[0]
+    stride = rows(name, t, dtype, shape, lead, math.prod(shape[lead:]), dev)
+    return t.data_ptr(), stride
 
 
 def states(initial_state, final_state, shape, dev: int):

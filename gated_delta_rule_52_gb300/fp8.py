@@ -54,12 +54,19 @@ def _code(name, t):
     return code
 
 
-def _scale_rows(name, s, shape, tile, dev):
-    """Row stride of the scales of an 8-bit tensor of this shape."""
-    n = blocks(shape[-1])
+def _scales(name, s, shape, lead, tile, dev):
+    """Pointer and row stride of the scales of an 8-bit tensor of this shape."""
+    n = -(-shape[-1] // BLOCK)
     if tile:
-        return _args.rows(name, s, SCALE, (blocks(math.prod(shape[:-1])), n), 1, n, dev)
-    return _args.rows(name, s, SCALE, (*shape[:-1], n), len(shape) - 1, n, dev)
+        return _args.matrix(name, s, SCALE, (-(-math.prod(shape[:-1]) // BLOCK), n), 1, dev)
+    return _args.matrix(name, s, SCALE, (shape[0], n) if lead == 1 else (*shape[:-1], n), lead, dev)
+
+
+def _tiled(name, s, shape, lead):
+    """Whether the scales of an 8-bit tensor of this shape are those of tiles."""
+    if not isinstance(s, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return s.dim() != lead + 1 or s.shape[0] != shape[0]
 
 
 def _pair(name, q, s, code, shape, tile, dev):
@@ -73,8 +80,7 @@ def _pair(name, q, s, code, shape, tile, dev):
     if _code(name, q) != code:
         raise ValueError("q and qt must be of one type")
     lead = len(shape) - 1
-    return (q.data_ptr(), _args.rows(name, q, q.dtype, shape, lead, shape[-1], dev), s.data_ptr(),
-            _scale_rows(f"scales of {name}", s, shape, tile, dev))
+    return *_args.matrix(name, q, q.dtype, shape, lead, dev), *_scales(f"scales of {name}", s, shape, lead, tile, dev)
 
 
 def quantize(x, q=None, scales=None, qt=None, scales_t=None, tile=False, stream=None) -> None:
@@ -83,38 +89,34 @@ def quantize(x, q=None, scales=None, qt=None, scales_t=None, tile=False, stream=
     lie along x's columns; one pass over x does both.  Asynchronous on ``stream`` (default: the
     current torch stream)."""
     dt, shape = _args.dtype_code("x", x), x.shape
-    if len(shape) < 2:
+    lead = len(shape) - 1
+    if lead < 1:
         raise ValueError("x must have at least two dimensions")
     if q is None and qt is None:
         raise ValueError("q or qt must be given")
-    cols, lead, dev = shape[-1], len(shape) - 1, _args.device("x", x)
-    stride, rows = _args.rows("x", x, x.dtype, shape, lead, cols, dev), math.prod(shape[:-1])
+    cols, dev = shape[-1], _args.device("x", x)
+    rows = shape[0] if lead == 1 else math.prod(shape[:-1])
+    px, xs = _args.matrix("x", x, x.dtype, shape, lead, dev)
     code = _code("q" if q is not None else "qt", q if q is not None else qt)
     pq, qs, ps, ss = _pair("q", q, scales, code, shape, tile, dev)
     pt, ts, pst, sts = _pair("qt", qt, scales_t, code, (cols, rows), tile, dev)
-    _args.done(_args.entry("kda_fp8_quantize")(x.data_ptr(), stride, dt, pq, qs, ps, ss, pt, ts, pst, sts, code, bool(tile), rows,
-                                               cols, _args.stream_handle(stream, dev)))
-
-
-def _tiled(name, s, shape):
-    """Whether the scales of an 8-bit tensor of this shape are those of tiles."""
-    if not isinstance(s, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    return s.shape != (*shape[:-1], blocks(shape[-1]))
+    _args.done(_args.entry("kda_fp8_quantize")(px, xs, dt, pq, qs, ps, ss, pt, ts, pst, sts, code, bool(tile), rows, cols,
+                                               _args.stream_handle(stream, dev)))
 
 
 def dequantize(q, scales, out, stream=None) -> None:
     """Writes the values that ``q`` [..., cols] with ``scales`` (of rows, or of tiles) stands for
     to ``out`` (bf16, fp16 or fp32, shaped like q)."""
     code, shape = _code("q", q), q.shape
-    if len(shape) < 2:
+    lead = len(shape) - 1
+    if lead < 1:
         raise ValueError("q must have at least two dimensions")
-    cols, lead, dev = shape[-1], len(shape) - 1, _args.device("q", q)
-    dt, tile = _args.dtype_code("out", out), _tiled("scales", scales, shape)
-    _args.done(_args.entry("kda_fp8_dequantize")(
-        q.data_ptr(), _args.rows("q", q, q.dtype, shape, lead, cols, dev), code, scales.data_ptr(),
-        _scale_rows("scales", scales, shape, tile, dev), tile, out.data_ptr(),
-        _args.rows("out", out, out.dtype, shape, lead, cols, dev), dt, math.prod(shape[:-1]), cols, _args.stream_handle(stream, dev)))
+    dev, dt, tile = _args.device("q", q), _args.dtype_code("out", out), _tiled("scales", scales, shape, lead)
+    pq, qs = _args.matrix("q", q, q.dtype, shape, lead, dev)
+    ps, ss = _scales("scales", scales, shape, lead, tile, dev)
+    po, os = _args.matrix("out", out, out.dtype, shape, lead, dev)
+    _args.done(_args.entry("kda_fp8_dequantize")(pq, qs, code, ps, ss, tile, po, os, dt, shape[0] if lead == 1 else math.prod(shape[:-1]),
+                                                 shape[-1], _args.stream_handle(stream, dev)))
 
 
 def matmul(a, a_scales, b, b_scales, out, add=None, stream=None) -> None:
@@ -124,18 +126,18 @@ def matmul(a, a_scales, b, b_scales, out, add=None, stream=None) -> None:
     [..., N] is bf16, fp16 or fp32, ``add`` None or like it (it may be ``out``).  Rows of a and b
     start at multiples of 16 bytes, those of the scales at multiples of 4, as ``empty`` lays them
     out; sums are fp32."""
-    ca, cb, sa, sb = _code("a", a), _code("b", b), a.shape, b.shape
-    if len(sa) < 2 or len(sb) != 2:
+    ca, cb, dt, sa, sb = _code("a", a), _code("b", b), _args.dtype_code("out", out), a.shape, b.shape
+    lead = len(sa) - 1
+    if lead < 1 or len(sb) != 2:
         raise ValueError("a must be [..., K] and b [N, K]")
-    K, N, lead, dev = sa[-1], sb[0], len(sa) - 1, _args.device("a", a)
-    dt, shape = _args.dtype_code("out", out), (*sa[:-1], N)
-    ta, tb = _tiled("a_scales", a_scales, sa), _tiled("b_scales", b_scales, sb)
-    rows = _args.rows
-    _args.done(_args.entry("kda_fp8_matmul")(
-        a.data_ptr(), rows("a", a, a.dtype, sa, lead, K, dev), ca, a_scales.data_ptr(),
-        _scale_rows("a_scales", a_scales, sa, ta, dev), ta,
-        b.data_ptr(), rows("b", b, b.dtype, (N, K), 1, K, dev), cb, b_scales.data_ptr(),
-        _scale_rows("b_scales", b_scales, sb, tb, dev), tb,
-        out.data_ptr(), rows("out", out, out.dtype, shape, lead, N, dev),
-        None if add is None else add.data_ptr(), 0 if add is None else rows("add", add, out.dtype, shape, lead, N, dev), dt,
-        math.prod(sa[:-1]), N, K, _args.stream_handle(stream, dev)))
+    K, N, dev = sa[-1], sb[0], _args.device("a", a)
+    M, shape = (sa[0], (sa[0], N)) if lead == 1 else (math.prod(sa[:-1]), (*sa[:-1], N))
+    ta, tb = _tiled("a_scales", a_scales, sa, lead), _tiled("b_scales", b_scales, sb, 1)
+    pa, as_ = _args.matrix("a", a, a.dtype, sa, lead, dev)
+    psa, sas = _scales("a_scales", a_scales, sa, lead, ta, dev)
+    pb, bs = _args.matrix("b", b, b.dtype, (N, K), 1, dev)
+    psb, sbs = _scales("b_scales", b_scales, sb, 1, tb, dev)
+    po, os = _args.matrix("out", out, out.dtype, shape, lead, dev)
+    pp, ps = (None, 0) if add is None else _args.matrix("add", add, out.dtype, shape, lead, dev)
+    _args.done(_args.entry("kda_fp8_matmul")(pa, as_, ca, psa, sas, ta, pb, bs, cb, psb, sbs, tb, po, os, pp, ps, dt, M, N, K,
+                                             _args.stream_handle(stream, dev)))

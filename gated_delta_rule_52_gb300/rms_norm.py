@@ -20,15 +20,17 @@ from . import _args, fp8
 
 def _shape(x):
     dt, shape = _args.dtype_code("x", x), x.shape
-    if not shape:
+    lead = len(shape) - 1
+    if lead < 0:
         raise ValueError("x must have at least one dimension")
-    D, lead, dev = shape[-1], len(shape) - 1, _args.device("x", x)
-    return dev, dt, shape, lead, D, _args.rows("x", x, x.dtype, shape, lead, D, dev)
+    dev = _args.device("x", x)
+    return dev, dt, shape, lead, shape[-1], shape[0] if lead == 1 else math.prod(shape[:-1]), \
+        *_args.matrix("x", x, x.dtype, shape, lead, dev)
 
 
-def _maybe_rows(name, t, x, shape, lead, D, dev):
+def _maybe(name, t, x, shape, lead, dev):
     """Data pointer and row stride of an optional tensor like ``x``."""
-    return (None, 0) if t is None else (t.data_ptr(), _args.rows(name, t, x.dtype, shape, lead, D, dev))
+    return (None, 0) if t is None else _args.matrix(name, t, x.dtype, shape, lead, dev)
 
 
 def rms_norm_fwd(x, weight, eps, out, residual=None, residual_out=None, rstd=None, scales=None, stream=None) -> None:
@@ -37,26 +39,26 @@ def rms_norm_fwd(x, weight, eps, out, residual=None, residual_out=None, rstd=Non
     stream).  ``out`` is of x's type (it may be ``x`` or ``residual``), or torch.float8_e4m3fn
     or torch.float8_e5m2 with ``scales`` [..., ceil(D/128)] of torch.float8_e8m0fnu;
     ``residual_out`` may be ``x`` or ``residual``."""
-    dev, dt, shape, lead, D, stride = _shape(x)
-    code, f32 = fp8.DTYPES.get(out.dtype) if isinstance(out, torch.Tensor) else None, torch.float32
+    dev, dt, shape, lead, D, rows, px, xs = _shape(x)
+    code, row = fp8.DTYPES.get(out.dtype) if isinstance(out, torch.Tensor) else None, shape[:-1]
     if code is None:
         if scales is not None:
             raise ValueError("scales belong to an 8-bit out")
-        code, out_stride, ps, ss = dt, _args.rows("out", out, x.dtype, shape, lead, D, dev), None, 0
+        code, ps, ss = dt, None, 0
+        pout, os = _args.matrix("out", out, x.dtype, shape, lead, dev)
     else:
         if scales is None:
             raise ValueError("an 8-bit out needs scales")
-        out_stride = _args.rows("out", out, out.dtype, shape, lead, D, dev)
-        ss = _args.rows("scales", scales, fp8.SCALE, (*shape[:-1], fp8.blocks(D)), lead, fp8.blocks(D), dev)
-        ps = scales.data_ptr()
+        pout, os = _args.matrix("out", out, out.dtype, shape, lead, dev)
+        ps, ss = _args.matrix("scales", scales, fp8.SCALE, (*row, fp8.blocks(D)), lead, dev)
     if residual_out is not None and residual is None:
         raise ValueError("residual_out needs a residual")
-    pr, rs = _maybe_rows("residual", residual, x, shape, lead, D, dev)
-    po, ros = _maybe_rows("residual_out", residual_out, x, shape, lead, D, dev)
+    pr, rs = _maybe("residual", residual, x, shape, lead, dev)
+    po, ros = _maybe("residual_out", residual_out, x, shape, lead, dev)
+    f32 = torch.float32
     _args.done(_args.entry("kda_rms_norm_fwd")(
-        x.data_ptr(), stride, pr, rs, _args.optional("weight", weight, f32, (D,), dev), eps, out.data_ptr(), out_stride, code,
-        ps, ss, po, ros, _args.optional("rstd", rstd, f32, shape[:-1], dev), dt, math.prod(shape[:-1]), D,
-        _args.stream_handle(stream, dev)))
+        px, xs, pr, rs, _args.optional("weight", weight, f32, (D,), dev), eps, pout, os, code, ps, ss, po, ros,
+        _args.optional("rstd", rstd, f32, row, dev), dt, rows, D, _args.stream_handle(stream, dev)))
 
 
 def rms_norm_bwd(dout, x, weight, rstd, dresidual=None, want_dweight=None, stream=None) -> dict:
@@ -64,9 +66,9 @@ def rms_norm_bwd(dout, x, weight, rstd, dresidual=None, want_dweight=None, strea
     normed and ``rstd`` what the forward wrote.  Returns a dict of new tensors: dx (like x,
     contiguous: the gradient of the forward's x and of its residual) and fp32 dweight (None
     unless ``want_dweight``, by default where there is a weight)."""
-    dev, dt, shape, lead, D, stride = _shape(x)
-    dout_stride = _args.rows("dout", dout, x.dtype, shape, lead, D, dev)
-    pd, ds = _maybe_rows("dresidual", dresidual, x, shape, lead, D, dev)
+    dev, dt, shape, lead, D, rows, px, xs = _shape(x)
+    pdo, dos = _args.matrix("dout", dout, x.dtype, shape, lead, dev)
+    pd, ds = _maybe("dresidual", dresidual, x, shape, lead, dev)
     f32 = torch.float32
     pw, pr = _args.optional("weight", weight, f32, (D,), dev), _args.tensor("rstd", rstd, f32, shape[:-1], dev)
     if want_dweight is None:
@@ -74,6 +76,6 @@ def rms_norm_bwd(dout, x, weight, rstd, dresidual=None, want_dweight=None, strea
     dx, = _args.new(stream, x, shape)
     dw, = _args.new(stream, rstd, (D,) if want_dweight else None)
     _args.done(_args.entry("kda_rms_norm_bwd")(
-        dout.data_ptr(), dout_stride, x.data_ptr(), stride, pw, pr, pd, ds, dx.data_ptr(), None if dw is None else dw.data_ptr(),
-        dt, math.prod(shape[:-1]), D, _args.stream_handle(stream, dev)))
+        pdo, dos, px, xs, pw, pr, pd, ds, dx.data_ptr(), None if dw is None else dw.data_ptr(), dt, rows, D,
+        _args.stream_handle(stream, dev)))
     return {"dx": dx, "dweight": dw}
