@@ -294,8 +294,8 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
 constexpr int kPairThreads = 384, kStoreWarps = 8;
 constexpr int kSegment = 64;                // blocks of K per segment of an fp32 output
 
-// A store warp's buffer: 32 rows of 64 bytes for a tensor store, or 32 x 17 fp32.
-constexpr int kStoreBuffer = 2560;
+// A store warp's buffers: two of 32 rows of 64 bytes for tensor stores, or one of 32 x 17 fp32.
+constexpr int kStoreBuffer = 4096;
 
 template <int BN, int SPLIT>
 struct PairShape {
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
             // ---- accumulators to out: lanes 32 (warp % 4) .. + 31, one half of the columns
             const int quarter = warp & 3, half = (warp - 4) >> 2;
             constexpr int kMost = S::kMost;              // of the first half; the second may be shorter
-            constexpr int V = 16 / sizeof(E);
+            constexpr int V = 16 / sizeof(E), kStep = 64 / sizeof(E);   // elements of 16 bytes, and of 64
             const int cols = half ? BN - kMost : kMost;
             unsigned char *own = staging + (warp - 4) * kStoreBuffer;
             Slot<S::kBuffers> sum;
@@ -576,124 +576,168 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                 const E *plus = p.add ? static_cast<const E *>(p.add) + (m0 + lane) * p.as + n0 : nullptr;
                 const bool my_row = m0 + lane < p.a.rows;
                 NarrowRows<E> narrow(p, reinterpret_cast<float *>(own), m0, n0, lane);
-                // this lane's row: fp32, or 16-bit values that begin as the addend's
-                float f[kSums ? kMost : 1];
-                Pack<E, V> o[kSums ? 1 : kMost / V];
-                if constexpr (!kSums) {
-                    if (wide && plus) {
-#pragma unroll
-                        for (int c = 0; c < kMost; c += V)
-                            if (c < cols) o[c / V] = ld_row<E, V>(plus + c, my_row ? (int)min(left - c, (int64_t)V) : 0);
-                    }
-                }
-                E (&raw_o)[kSums ? V : kMost] = reinterpret_cast<E (&)[kSums ? V : kMost]>(o);
-                if (!wide) {
-                    if constexpr (kSums) {
-                        narrow.take_addend(0);
-                    } else if (plus) {
-#pragma unroll
-                        for (int c = 0; c < kMost; c += 16)
-                            if (c < cols) narrow.addend(c, reinterpret_cast<E (&)[16]>(raw_o[c]));
-                    }
-                }
-                for (int k = 0; k < blocks; k += segment) {
-                    const int buf = sum.at;
-                    ok = warp_wait<false>(&tfull[buf], sum.turn);
-                    if (!ok) break;
-                    sum.next();
-                    tc_fence_after();
-                    const uint32_t from = tmem_addr(acc, quarter * 32, buf * BN + half * kMost);
-                    if constexpr (kSums) {
-#pragma unroll
-                        for (int c = 0; c < kMost; c += 16) {
-                            if (c >= cols) break;
-                            float r[16];
-                            tmem_ld16(from + c, r);
-                            tmem_ld_wait();
-                            if (k == 0) {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) f[c + e] = r[e];
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) f[c + e] += r[e];
-                            }
-                        }
-                    } else if (wide) {
-#pragma unroll
-                        for (int c = 0; c < kMost; c += 32) {
-                            if (c >= cols) break;
-                            float r[32];
-                            tmem_ld32(from + c, r);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 32; e += V) {
-                                float (&v)[V] = reinterpret_cast<float (&)[V]>(r[e]);
-                                if (plus) {
-                                    float a[V];
-                                    unpack<E, V>(o[(c + e) / V], a);
-                                    add_n<V>(v, v, a);
-                                }
-                                st_f<E, V>(o[(c + e) / V].e, v);
-                            }
-                        }
-                    } else {
-                        // rows that no wide access fits
-#pragma unroll
-                        for (int c = 0; c < kMost; c += 16) {
-                            if (c >= cols) break;
-                            float r[16];
-                            tmem_ld16(from + c, r);
-                            tmem_ld_wait();
-                            if (plus) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) narrow.a[i] = to_f(raw_o[c + i]);
-                            }
-                            narrow.store(r, c, false);
-                        }
-                    }
-                    tc_fence_before();
-                    if (lane == 0) mbar_arrive_remote(bars + 8 * buf);
-                }
-                if (!ok) break;
-                if constexpr (kSums) {
-                    if (!wide) {
-#pragma unroll
-                        for (int c = 0; c < kMost; c += 16)
-                            if (c < cols) narrow.store(reinterpret_cast<float (&)[16]>(f[c]), c, c + 16 < cols);
-                    }
-                }
-                if (!wide || m0 >= p.a.rows) continue;
-                // 64 bytes of every row to the buffer (16-byte piece j of row r at j ^ (r / 2 % 4), the
-                // 64-byte swizzle), and from there by a tensor store, which leaves out what is outside
-                constexpr int kStep = 64 / sizeof(E);
-#pragma unroll
-                for (int c = 0; c < kMost; c += kStep) {
-                    if (c >= cols || c >= left) break;
-                    if (lane == 0) bulk_wait_read0();
+                const auto addend = [&](int c) { return ld_row<E, V>(plus + c, my_row ? (int)min(left - c, (int64_t)V) : 0); };
+                // 64 bytes of every row to one of the two buffers (16-byte piece j of row r at
+                // j ^ (r / 2 % 4), the 64-byte swizzle), and from there by a tensor store, which leaves
+                // out what is outside
+                const auto send = [&](int c, const Pack<E, V> (&piece)[4]) {
+                    if (c >= left || m0 >= p.a.rows) return;
+                    unsigned char *buffer = own + (c / kStep & 1) * 2048;
+                    if (lane == 0) bulk_wait_read1();
                     __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        Pack<E, V> piece;
-                        if constexpr (kSums) {
-                            float (&v)[V] = reinterpret_cast<float (&)[V]>(f[c + j * V]);
-                            if (plus) {
-                                float a[V];
-                                unpack<E, V>(ld_row<E, V>(plus + c + j * V, my_row ? (int)min(left - c - j * V, (int64_t)V) : 0), a);
-                                add_n<V>(v, v, a);
-                            }
-                            st_f<E, V>(piece.e, v);
-                        } else {
-                            piece = o[c / V + j];
-                        }
-                        *reinterpret_cast<Pack<E, V> *>(own + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = piece;
-                    }
+                    for (int j = 0; j < 4; ++j) *reinterpret_cast<Pack<E, V> *>(buffer + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = piece[j];
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_2d(&args.out, own, (int)(n0 + c), (int)m0);
+                        tma_store_2d(&args.out, buffer, (int)(n0 + c), (int)m0);
                         bulk_commit();
                     }
+                };
+                if constexpr (kSums) {
+                    // 16 columns at a time: from TMEM, or where K has several segments from their sum
+                    const auto emit = [&](int c, float (&r)[16], const Pack<E, V> (&add)[4]) {
+                        if (!wide) {
+                            narrow.store(r, c, c + 16 < cols);
+                            return;
+                        }
+                        Pack<E, V> piece[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float (&v)[V] = reinterpret_cast<float (&)[V]>(r[j * V]);
+                            if (plus) {
+                                float a[V];
+                                unpack<E, V>(add[j], a);
+                                add_n<V>(v, v, a);
+                            }
+                            st_f<E, V>(piece[j].e, v);
+                        }
+                        send(c, piece);
+                    };
+                    Pack<E, V> add[4];
+                    const auto take = [&](int c) {
+                        if (wide && plus)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) add[j] = addend(c + j * V);
+                    };
+                    if (!wide) narrow.take_addend(0);
+                    if (blocks <= kSegment) {
+                        const int buf = sum.at;
+                        take(0);
+                        ok = warp_wait<false>(&tfull[buf], sum.turn);
+                        if (!ok) break;
+                        sum.next();
+                        tc_fence_after();
+                        const uint32_t from = tmem_addr(acc, quarter * 32, buf * BN + half * kMost);
+#pragma unroll 1
+                        for (int c = 0; c < cols; c += 16) {
+                            float r[16];
+                            Pack<E, V> now[4];
+                            tmem_ld16(from + c, r);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) now[j] = add[j];
+                            if (c + 16 < cols) take(c + 16);
+                            tmem_ld_wait();
+                            emit(c, r, now);
+                        }
+                        tc_fence_before();
+                        if (lane == 0) mbar_arrive_remote_only(bars + 8 * buf);
+                    } else {
+                        float f[kMost];
+                        for (int k = 0; k < blocks; k += kSegment) {
+                            const int buf = sum.at;
+                            ok = warp_wait<false>(&tfull[buf], sum.turn);
+                            if (!ok) break;
+                            sum.next();
+                            tc_fence_after();
+                            const uint32_t from = tmem_addr(acc, quarter * 32, buf * BN + half * kMost);
+#pragma unroll
+                            for (int c = 0; c < kMost; c += 16) {
+                                if (c >= cols) break;
+                                float r[16];
+                                tmem_ld16(from + c, r);
+                                tmem_ld_wait();
+                                if (k == 0) {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) f[c + e] = r[e];
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) f[c + e] += r[e];
+                                }
+                            }
+                            tc_fence_before();
+                            if (lane == 0) mbar_arrive_remote_only(bars + 8 * buf);
+                        }
+                        if (!ok) break;
+#pragma unroll
+                        for (int c = 0; c < kMost; c += 16) {
+                            if (c >= cols) break;
+                            take(c);
+                            emit(c, reinterpret_cast<float (&)[16]>(f[c]), add);
+                        }
+                    }
+                    continue;
                 }
+                // this lane's row in 16 bits (or where rows are not wide: what it stores of 32 rows),
+                // which begins as the addend's, read while the MMAs run
+                Pack<E, V> o[kMost / V];
+                E (&single)[kMost] = reinterpret_cast<E (&)[kMost]>(o);
+                if (plus) {
+#pragma unroll
+                    for (int c = 0; c < kMost; c += 16) {
+                        if (c >= cols) break;
+                        if (!wide) {
+                            narrow.addend(c, reinterpret_cast<E (&)[16]>(single[c]));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; e += V) o[(c + e) / V] = addend(c + e);
+                        }
+                    }
+                }
+                const int buf = sum.at;
+                ok = warp_wait<false>(&tfull[buf], sum.turn);
+                if (!ok) break;
+                sum.next();
+                tc_fence_after();
+                const uint32_t from = tmem_addr(acc, quarter * 32, buf * BN + half * kMost);
+                if (wide) {
+#pragma unroll
+                    for (int c = 0; c < kMost; c += 32) {
+                        if (c >= cols) break;
+                        float r[32];
+                        tmem_ld32(from + c, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; e += V) {
+                            float (&v)[V] = reinterpret_cast<float (&)[V]>(r[e]);
+                            if (plus) {
+                                float a[V];
+                                unpack<E, V>(o[(c + e) / V], a);
+                                add_n<V>(v, v, a);
+                            }
+                            st_f<E, V>(o[(c + e) / V].e, v);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kMost; c += 16) {
+                        if (c >= cols) break;
+                        float r[16];
+                        tmem_ld16(from + c, r);
+                        tmem_ld_wait();
+                        if (plus) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) narrow.a[i] = to_f(single[c + i]);
+                        }
+                        narrow.store(r, c, false);
+                    }
+                }
+                tc_fence_before();
+                if (lane == 0) mbar_arrive_remote_only(bars + 8 * buf);
+                if (!wide) continue;
+#pragma unroll
+                for (int c = 0; c < kMost; c += 32)
+                    if (c < cols) send(c, reinterpret_cast<const Pack<E, V> (&)[4]>(o[c / V]));
             }
             if (lane == 0) bulk_wait0();
         }

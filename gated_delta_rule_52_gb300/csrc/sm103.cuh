@@ -157,6 +157,12 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster_addr) {
                      bar_cluster_addr)
                  : "memory");
 }
+// The same without publishing global memory to the cluster, for a barrier that hands back something
+// else (tensor memory that has been read): a release for the cluster waits for every store that the
+// thread has under way.
+__device__ __forceinline__ void mbar_arrive_remote_only(uint32_t bar_cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
+}
 // Bulk copy of `bytes` from this CTA's shared memory into another CTA's shared
 // memory, completing as transaction bytes on that CTA's mbarrier.
 __device__ __forceinline__ void bulk_copy_to_peer(uint32_t dst_cluster, uint32_t src_cta,
@@ -237,6 +243,10 @@ __device__ __forceinline__ void bulk_commit() {
 // Waits until the bulk stores' reads of shared memory are done (source reusable).
 __device__ __forceinline__ void bulk_wait_read0() {
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+// The same for all but the latest of this thread's groups.
+__device__ __forceinline__ void bulk_wait_read1() {
+    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 __device__ __forceinline__ void bulk_wait0() {
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");

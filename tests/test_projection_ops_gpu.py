@@ -70,7 +70,13 @@ MM = [  # M, N, K, a, b, a_tile, b_tile, dtype, add
     (1100, 520, 1200, E4, E5, True, True, F, False),
     (400, 264, 640, E4, E4, False, True, BF, True),
     (700, 1000, 384, E5, E4, False, False, HF, True),
-    (520, 1032, 4300, E4, E4, False, False, F, True),        # fp32 sums of several segments
+    (520, 1032, 4300, E4, E4, False, False, F, True),
+    (300, 136, 8400, E4, E4, False, True, F, True),          # fp32 sums of several segments of K
+    (8300, 1033, 8400, E4, E4, False, True, F, True),        # and of more tiles than pairs of SMs
+    (4999, 1920, 16600, E4, E5, False, False, F, False),
+    (4999, 1921, 300, E4, E4, False, True, F, True),
+    (5000, 1928, 300, E4, E4, False, True, BF, True),
+    (3000, 2001, 140, E4, E4, False, True, HF, True),
     (2049, 513, 130, E4, E4, False, True, BF, True),
     (1537, 2048, 256, E4, E4, True, True, HF, False),
 ]
