@@ -92,8 +92,9 @@ struct ScaleRows {
 };
 
 // ---- few rows of a: one tile of 128 rows of b by BT rows of a per cluster of `split` CTAs, which
-// share K and join their sums through distributed shared memory, each for a part of the rows of a.  The rows of b, of which nearly all bytes are, lie along the MMA's M, so that
-// tiles are full however few rows a has.  Two CTAs per SM keep up to 180 KB of loads in flight.
+// share K and join their sums through distributed shared memory, each for a part of the rows of a.
+// The rows of b, of which nearly all bytes are, lie along the MMA's M, so that tiles are full however
+// few rows a has.  Two CTAs per SM keep up to 180 KB of loads in flight.
 template <int BT>
 struct TileShape {
     static constexpr int kStage = (kRows + BT) * kFp8Block;
@@ -136,13 +137,16 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
             for (int i = 0; i < kScaleStages; ++i) mbar_init(&sfull[i], 32), mbar_init(&sempty[i], 1);
             mbar_init(&done, 1);
             fence_mbar_init();
-            for (int i = 0; i < early; ++i) load(k0 + i, i);
         }
     } else if (warp == 1) {
         issuer = elect_one();
         tmem_alloc(&tmem_base, S::kCols);
         tmem_relinquish();
     }
+    wait_for_prior_kernels();
+    allow_next_kernel();
+    if (warp == 0 && issuer)
+        for (int i = 0; i < early; ++i) load(k0 + i, i);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -414,6 +418,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     tc_fence_before();
     __syncthreads();
     cluster_sync();
+    wait_for_prior_kernels();
+    allow_next_kernel();
     tc_fence_after();
     const uint32_t acc = tmem_base, sf = acc + S::kBuffers * BN;
     bool ok = true;
@@ -854,19 +860,6 @@ bool encode_out(CUtensorMap &map, const MatmulParams &p) {
                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaLaunchConfig_t cluster_launch(cudaLaunchAttribute &at, int64_t grid, int threads, int smem, int cluster, cudaStream_t stream) {
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)grid);
-    c.blockDim = dim3(threads);
-    c.dynamicSmemBytes = smem;
-    c.stream = stream;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = cluster, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
-    c.attrs = &at;
-    c.numAttrs = 1;
-    return c;
-}
-
 template <typename E, int BT>
 cudaError_t run_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
     using S = TileShape<BT>;
@@ -875,13 +868,12 @@ cudaError_t run_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const MatmulParams &p = args.p;
     if (!encode_operand(args.a, p.a, p.K, BT) || !encode_operand(args.b, p.b, p.K, kRows)) return cudaErrorInvalidValue;
-    // as many parts of K as two CTAs per SM hold, of 4 blocks or more
+    // as many parts of K as two CTAs per SM hold, of 4 blocks or more; for 32-bit outputs also as many
+    // as leave an accumulator kSegment blocks
     const int64_t tiles = ceil_div(p.b.rows, kRows) * ceil_div(p.a.rows, BT), blocks = ceil_div(p.K, kFp8Block);
     int split = 1;
-    while (split < 8 && tiles * split * 2 <= 2 * sms && blocks >= 8 * split) split *= 2;
-    cudaLaunchAttribute at;
-    const cudaLaunchConfig_t c = cluster_launch(at, tiles * split, 128, S::kSmem, split, stream);
-    return cudaLaunchKernelEx(&c, kernel, args, split);
+    while (split < 8 && ((tiles * split * 2 <= 2 * sms && blocks >= 8 * split) || (p.dtype == kFP32 && blocks > split * kSegment))) split *= 2;
+    return launch_early(kernel, tiles * split, dim3(128), S::kSmem, stream, split, args, split);
 }
 
 template <typename E, int BN, int SPLIT>
@@ -897,10 +889,7 @@ cudaError_t run_pair(MatmulArgs &args, int sms, cudaStream_t stream) {
                      (!p.add || (reinterpret_cast<uintptr_t>(p.add) % 16 == 0 && p.as % V == 0));
     if (SPLIT == 1 && wide && !encode_out(args.out, p)) return cudaErrorInvalidValue;
     const int64_t tiles = ceil_div(p.a.rows, 2 * kRows) * ceil_div(p.b.rows, BN);
-    cudaLaunchAttribute at;
-    const cudaLaunchConfig_t c =
-        cluster_launch(at, 2 * SPLIT * (SPLIT > 1 ? tiles : std::min(tiles, (int64_t)sms / 2)), kPairThreads, S::kSmem, 2 * SPLIT, stream);
-    return cudaLaunchKernelEx(&c, kernel, args, wide);
+    return launch_early(kernel, 2 * SPLIT * (SPLIT > 1 ? tiles : std::min(tiles, (int64_t)sms / 2)), dim3(kPairThreads), S::kSmem, stream, 2 * SPLIT, args, wide);
 }
 
 // How a product is computed: rows of a per tile (tile kernel), or rows of b and parts of K (pair
@@ -934,6 +923,7 @@ Choice choose(const MatmulParams &p, int sms) {
 // out = add, where K is 0.
 template <typename E>
 __global__ void __launch_bounds__(256) mm_add_kernel(MatmulParams p) {
+    wait_for_prior_kernels();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.a.rows * p.b.rows; i += (int64_t)gridDim.x * 256) {
         const int64_t m = i / p.b.rows, n = i % p.b.rows;
         static_cast<E *>(p.out)[m * p.os + n] = p.add ? static_cast<const E *>(p.add)[m * p.as + n] : from_f<E>(0.f);
@@ -946,8 +936,7 @@ cudaError_t launch_matmul(const MatmulParams &p, int sms, cudaStream_t stream) {
     return with_dtype(p.dtype, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
         if (p.K == 0) {
-            mm_add_kernel<E><<<(unsigned)std::min(ceil_div(p.a.rows * p.b.rows, 256), (int64_t)sms * 8), 256, 0, stream>>>(p);
-            return cudaGetLastError();
+            return launch_early(mm_add_kernel<E>, std::min(ceil_div(p.a.rows * p.b.rows, 256), (int64_t)sms * 8), dim3(256), 0, stream, 0, p);
         }
         const Choice c = choose(p, sms);
         MatmulArgs args;

@@ -88,6 +88,8 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(E) == 2 ? 4 : 2) quantiz
     const int64_t r0 = (int64_t)br * kTile, c0 = (int64_t)bc * kTile, c = c0 + 8 * cg;
     const int cols = (int)min(max(p.cols - c, (int64_t)0), (int64_t)8), rows = (int)min(p.rows - r0, (int64_t)kTile);
     Group v[2][4];
+    sm103::wait_for_prior_kernels();
+    sm103::allow_next_kernel();
     {
         const E *at = static_cast<const E *>(p.x) + (r0 + 4 * rg) * p.xs + c;
 #pragma unroll
@@ -250,6 +252,8 @@ template <int V> constexpr int Turns = V == 1 ? 4 : 2;
 template <typename E, int V>
 __global__ void __launch_bounds__(256) dequantize_kernel(QuantParams p, uint32_t pieces) {
     constexpr int kTurns = Turns<V>;
+    sm103::wait_for_prior_kernels();
+    sm103::allow_next_kernel();
     const bool e5m2 = p.q_dtype == kE5M2;
     const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5), row = item / pieces;
     if (row >= p.rows) return;
@@ -290,16 +294,11 @@ __global__ void __launch_bounds__(256) dequantize_kernel(QuantParams p, uint32_t
 cudaError_t launch_quantize(const QuantParams &p, int sms, cudaStream_t stream) {
     return with_dtype(p.dtype, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
-        const unsigned grid = (unsigned)(ceil_div(p.cols, kTile) * ceil_div(p.rows, kTile));
+        const int64_t grid = ceil_div(p.cols, kTile) * ceil_div(p.rows, kTile);
         const bool wide = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.xs % (16 / sizeof(E)) == 0;
-        if (p.q_dtype == kE5M2) {
-            if (wide) quantize_kernel<E, true, true><<<grid, kQuantThreads, 0, stream>>>(p);
-            else quantize_kernel<E, true, false><<<grid, kQuantThreads, 0, stream>>>(p);
-        } else {
-            if (wide) quantize_kernel<E, false, true><<<grid, kQuantThreads, 0, stream>>>(p);
-            else quantize_kernel<E, false, false><<<grid, kQuantThreads, 0, stream>>>(p);
-        }
-        return cudaGetLastError();
+        const auto run = [&](auto kernel) { return launch_early(kernel, grid, dim3(kQuantThreads), 0, stream, 0, p); };
+        if (p.q_dtype == kE5M2) return wide ? run(quantize_kernel<E, true, true>) : run(quantize_kernel<E, true, false>);
+        return wide ? run(quantize_kernel<E, false, true>) : run(quantize_kernel<E, false, false>);
     });
 }
 
@@ -309,9 +308,8 @@ cudaError_t launch_dequantize(const QuantParams &p, int sms, cudaStream_t stream
         const bool wide = p.cols % 16 == 0 && p.qs % 16 == 0 && reinterpret_cast<uintptr_t>(p.q) % 16 == 0 &&
                           reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.xs % (16 / sizeof(E)) == 0;
         const int64_t pieces = ceil_div(p.cols, 32 * (wide ? 16 * Turns<16> : Turns<1>)), grid = ceil_div(pieces * p.rows, 8);
-        if (wide) dequantize_kernel<E, 16><<<(unsigned)grid, 256, 0, stream>>>(p, (uint32_t)pieces);
-        else dequantize_kernel<E, 1><<<(unsigned)grid, 256, 0, stream>>>(p, (uint32_t)pieces);
-        return cudaGetLastError();
+        return wide ? launch_early(dequantize_kernel<E, 16>, grid, dim3(256), 0, stream, 0, p, (uint32_t)pieces)
+                    : launch_early(dequantize_kernel<E, 1>, grid, dim3(256), 0, stream, 0, p, (uint32_t)pieces);
     });
 }
 

@@ -135,6 +135,26 @@ cudaError_t allow_smem(int bytes) {
     return once_per_device(done, [&](int) { return cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
 }
 
+// Launches a kernel that may start while the one before it on the stream ends.  The kernel calls
+// sm103::wait_for_prior_kernels() before it touches global memory: everything up to there, and the
+// way to the GPU, costs nothing then.  (A product in a row of them: 2 us less of 16.)
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), int64_t grid, dim3 block, size_t smem, cudaStream_t stream, int cluster, const Args &...args) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = block;
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster, at[1].val.clusterDim.y = 1, at[1].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = cluster > 0 ? 2 : 1;   // 0: no clusters
+    return cudaLaunchKernelEx(&c, kernel, Params(args)...);
+}
+
 // Sum over j of part[j * width + c], 32 columns per CTA of kSumThreads threads, in a fixed
 // order.  The threads of the CTA's first warp have the sum of column 32 blockIdx.x + lane.
 constexpr int kSumThreads = 256;

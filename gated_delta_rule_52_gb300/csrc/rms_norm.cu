@@ -79,6 +79,8 @@ __device__ __forceinline__ void st_group_fp8(uint8_t *at, uint8_t *scale, float 
 // OUT: 0 = out in E, 4, 5 = in 8 bits (kE4M3, kE5M2).
 template <typename E, int EL, int OUT>
 __global__ void __launch_bounds__(512) rms_fwd_row_kernel(RmsParams p) {
+    sm103::wait_for_prior_kernels();
+    sm103::allow_next_kernel();
     constexpr int V = 16 / sizeof(E), N = EL / V;
     __shared__ float part[32];
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -154,6 +156,8 @@ template <typename E, int EL> constexpr int kBwdStages = std::min(4, 192 * 1024 
 
 template <typename E, int EL>
 __global__ void __launch_bounds__(kBwdThreads, 1) rms_bwd_row_kernel(RmsParams p, float *part_out) {
+    sm103::wait_for_prior_kernels();
+    sm103::allow_next_kernel();
     constexpr int V = 16 / sizeof(E), N = EL / V, kStages = kBwdStages<E, EL>;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float part[2][32];
@@ -336,6 +340,8 @@ __device__ __forceinline__ void st_block_fp8(uint8_t *p, uint8_t *scale, int64_t
 
 template <typename E, int NB, int OUT>
 __global__ void __launch_bounds__(512) rms_fwd_odd_kernel(RmsParams p) {
+    sm103::wait_for_prior_kernels();
+    sm103::allow_next_kernel();
     __shared__ float part[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -382,6 +388,8 @@ __global__ void __launch_bounds__(512) rms_fwd_odd_kernel(RmsParams p) {
 // next row's loads are left to the other CTAs of the SM.
 template <typename E, int NB>
 __global__ void __launch_bounds__(512) rms_bwd_odd_kernel(RmsParams p, float *part_out) {
+    sm103::wait_for_prior_kernels();
+    sm103::allow_next_kernel();
     __shared__ float part[2][32];
     extern __shared__ __align__(16) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -452,6 +460,8 @@ __global__ void __launch_bounds__(512) rms_bwd_odd_kernel(RmsParams p, float *pa
 // ---- rows too long for registers: a CTA each, two passes (the second through L1 and L2)
 template <typename E, bool WIDE>
 __global__ void __launch_bounds__(kRowThreads) rms_fwd_kernel(RmsParams p) {
+    sm103::wait_for_prior_kernels();
+    sm103::allow_next_kernel();
     __shared__ float part[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = kRowThreads / 32;
     const int64_t row = blockIdx.x, D = p.D, blocks = ceil_div(D, kFp8Block);
@@ -501,6 +511,8 @@ __global__ void __launch_bounds__(kRowThreads) rms_fwd_kernel(RmsParams p) {
 
 template <typename E, bool WIDE>
 __global__ void __launch_bounds__(kRowThreads) rms_bwd_kernel(RmsParams p) {
+    sm103::wait_for_prior_kernels();
+    sm103::allow_next_kernel();
     __shared__ float part[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = kRowThreads / 32;
     const int64_t row = blockIdx.x, D = p.D, blocks = ceil_div(D, kFp8Block);
@@ -533,20 +545,25 @@ __global__ void __launch_bounds__(kRowThreads) rms_bwd_kernel(RmsParams p) {
     }
 }
 
-// Sums of dy hat over blocks of rows: a thread per column, blockIdx.y a block.
+// Sums of dy hat over `parts` blocks of rows: a thread per column.
 template <typename E>
-__global__ void __launch_bounds__(128) rms_weight_part_kernel(RmsParams p, int64_t block_rows, float *part) {
-    const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x, r0 = blockIdx.y * block_rows, r1 = min(r0 + block_rows, p.rows);
+__global__ void __launch_bounds__(128) rms_weight_part_kernel(RmsParams p, int parts, float *part) {
+    sm103::wait_for_prior_kernels();
+    sm103::allow_next_kernel();
+    const int at = blockIdx.x % parts;
+    const int64_t c = (int64_t)(blockIdx.x / parts) * 128 + threadIdx.x, each = ceil_div(p.rows, parts), r0 = at * each, r1 = min(r0 + each, p.rows);
     if (c >= p.D) return;
     const E *x = static_cast<const E *>(p.x) + c, *dy = static_cast<const E *>(p.dout) + c;
     float s = 0.f;
 #pragma unroll 4
     for (int64_t row = r0; row < r1; ++row) s = fmaf(to_f(dy[row * p.ds]), to_f(x[row * p.xs]) * p.rstd[row], s);
-    part[blockIdx.y * p.D + c] = s;
+    part[at * p.D + c] = s;
 }
 
 // 32 columns per CTA, the parts in 32 slices, in a fixed order.  (8 slices took 7 us of 152 parts.)
 __global__ void __launch_bounds__(1024) rms_weight_sum_kernel(RmsParams p, int64_t parts, const float *part) {
+    sm103::wait_for_prior_kernels();
+    sm103::allow_next_kernel();
     __shared__ float sums[32][33];
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
@@ -628,21 +645,17 @@ int64_t weight_parts(const RmsParams &p, int sms) {
 template <typename E, int NB>
 cudaError_t run_fwd_odd(const RmsParams &p, cudaStream_t stream) {
     const dim3 block = odd_block(p, NB, 256);
-    const unsigned grid = (unsigned)ceil_div(p.rows, (int64_t)block.y);
-    if (p.out_dtype == p.dtype) rms_fwd_odd_kernel<E, NB, 0><<<grid, block, 0, stream>>>(p);
-    else if (p.out_dtype == kE4M3) rms_fwd_odd_kernel<E, NB, kE4M3><<<grid, block, 0, stream>>>(p);
-    else rms_fwd_odd_kernel<E, NB, kE5M2><<<grid, block, 0, stream>>>(p);
-    return cudaGetLastError();
+    const auto run = [&](auto kernel) { return launch_early(kernel, ceil_div(p.rows, (int64_t)block.y), block, 0, stream, 0, p); };
+    if (p.out_dtype == p.dtype) return run(rms_fwd_odd_kernel<E, NB, 0>);
+    return p.out_dtype == kE4M3 ? run(rms_fwd_odd_kernel<E, NB, kE4M3>) : run(rms_fwd_odd_kernel<E, NB, kE5M2>);
 }
 
 template <typename E, int EL>
 cudaError_t run_fwd(const RmsParams &p, cudaStream_t stream) {
     const dim3 block = row_block(p.D, EL, 256);
-    const unsigned grid = (unsigned)ceil_div(p.rows, (int64_t)block.y);
-    if (p.out_dtype == p.dtype) rms_fwd_row_kernel<E, EL, 0><<<grid, block, 0, stream>>>(p);
-    else if (p.out_dtype == kE4M3) rms_fwd_row_kernel<E, EL, kE4M3><<<grid, block, 0, stream>>>(p);
-    else rms_fwd_row_kernel<E, EL, kE5M2><<<grid, block, 0, stream>>>(p);
-    return cudaGetLastError();
+    const auto run = [&](auto kernel) { return launch_early(kernel, ceil_div(p.rows, (int64_t)block.y), block, 0, stream, 0, p); };
+    if (p.out_dtype == p.dtype) return run(rms_fwd_row_kernel<E, EL, 0>);
+    return p.out_dtype == kE4M3 ? run(rms_fwd_row_kernel<E, EL, kE4M3>) : run(rms_fwd_row_kernel<E, EL, kE5M2>);
 }
 
 template <typename E, int EL>
@@ -653,8 +666,7 @@ cudaError_t run_bwd(const RmsParams &p, float *part, int sms, cudaStream_t strea
     const cudaError_t e = allow_smem<kernel>(kBwdThreads * kBytes);
     if (e != cudaSuccess) return e;
     static_assert(kBytes >= EL * 4, "the sums fit the ring");
-    kernel<<<(unsigned)bwd_grid(p, sms), block, block.x * block.y * kBytes, stream>>>(p, part);
-    return cudaGetLastError();
+    return launch_early(kernel, bwd_grid(p, sms), block, block.x * block.y * kBytes, stream, 0, p, part);
 }
 
 }  // namespace
@@ -676,9 +688,7 @@ cudaError_t launch_rms_fwd(const RmsParams &p, int sms, cudaStream_t stream) {
         }
         const bool wide = aligned_rows(p, 4, {{p.x, p.xs}, {p.res, p.rs}, {p.res_out, p.ros}}) &&
                           (p.out_dtype != p.dtype || aligned_rows(p, 4, {{p.out, p.os}}));
-        if (wide) rms_fwd_kernel<E, true><<<(unsigned)p.rows, kRowThreads, 0, stream>>>(p);
-        else rms_fwd_kernel<E, false><<<(unsigned)p.rows, kRowThreads, 0, stream>>>(p);
-        return cudaGetLastError();
+        return launch_early(wide ? rms_fwd_kernel<E, true> : rms_fwd_kernel<E, false>, p.rows, dim3(kRowThreads), 0, stream, 0, p);
     });
 }
 
@@ -696,19 +706,16 @@ cudaError_t launch_rms_bwd(const RmsParams &p, unsigned char *ws, int sms, cudaS
         }
         if (p.D <= kOddBwdMaxD) {
             const dim3 block = odd_bwd_block(p);
-            rms_bwd_odd_kernel<E, 4><<<(unsigned)odd_bwd_grid(p, sms), block, 16 * block.x * 4, stream>>>(p, part);
-            return cudaGetLastError();
+            return launch_early(rms_bwd_odd_kernel<E, 4>, odd_bwd_grid(p, sms), block, 16 * block.x * 4, stream, 0, p, part);
         }
-        if (aligned_rows(p, 4, {{p.x, p.xs}, {p.dout, p.ds}, {p.dres, p.drs}, {p.dx, p.D}}))
-            rms_bwd_kernel<E, true><<<(unsigned)p.rows, kRowThreads, 0, stream>>>(p);
-        else rms_bwd_kernel<E, false><<<(unsigned)p.rows, kRowThreads, 0, stream>>>(p);
-        if (p.dweight)
-            rms_weight_part_kernel<E><<<dim3((unsigned)ceil_div(p.D, 128), (unsigned)parts), 128, 0, stream>>>(p, ceil_div(p.rows, parts), part);
-        return cudaGetLastError();
+        const bool wide = aligned_rows(p, 4, {{p.x, p.xs}, {p.dout, p.ds}, {p.dres, p.drs}, {p.dx, p.D}});
+        const cudaError_t e =
+            launch_early(wide ? rms_bwd_kernel<E, true> : rms_bwd_kernel<E, false>, p.rows, dim3(kRowThreads), 0, stream, 0, p);
+        if (e != cudaSuccess || !p.dweight) return e;
+        return launch_early(rms_weight_part_kernel<E>, ceil_div(p.D, 128) * parts, dim3(128), 0, stream, 0, p, (int)parts, part);
     });
     if (e != cudaSuccess || !p.dweight) return e;
-    rms_weight_sum_kernel<<<(unsigned)ceil_div(p.D, 32), 1024, 0, stream>>>(p, parts, part);
-    return cudaGetLastError();
+    return launch_early(rms_weight_sum_kernel, ceil_div(p.D, 32), dim3(1024), 0, stream, 0, p, parts, part);
 }
 
 }  // namespace kda

@@ -178,6 +178,11 @@ __device__ __forceinline__ void named_bar(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// A kernel launched with programmatic stream serialisation may start while the one before it ends:
+// what that one wrote (and read) is settled after this wait.
+__device__ __forceinline__ void wait_for_prior_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------------ fences
 // Makes generic-proxy shared-memory writes visible to the async proxy (TMA,
 // tensor core operand reads).
