@@ -247,11 +247,10 @@ __device__ __forceinline__ float scale_of(int byte) {
 }
 
 // A warp takes kTurns pieces of 32 V neighbouring elements of a row, V to a lane.
-template <int V> constexpr int Turns = V == 1 ? 4 : 2;
+constexpr int kTurns = 4;
 
 template <typename E, int V>
 __global__ void __launch_bounds__(256) dequantize_kernel(QuantParams p, uint32_t pieces) {
-    constexpr int kTurns = Turns<V>;
     sm103::wait_for_prior_kernels();
     sm103::allow_next_kernel();
     const bool e5m2 = p.q_dtype == kE5M2;
@@ -305,10 +304,10 @@ cudaError_t launch_quantize(const QuantParams &p, int sms, cudaStream_t stream) 
 cudaError_t launch_dequantize(const QuantParams &p, int sms, cudaStream_t stream) {
     return with_dtype(p.dtype, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
-        const bool wide = p.cols % 16 == 0 && p.qs % 16 == 0 && reinterpret_cast<uintptr_t>(p.q) % 16 == 0 &&
+        const bool wide = p.cols % 8 == 0 && p.qs % 8 == 0 && reinterpret_cast<uintptr_t>(p.q) % 8 == 0 &&
                           reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.xs % (16 / sizeof(E)) == 0;
-        const int64_t pieces = ceil_div(p.cols, 32 * (wide ? 16 * Turns<16> : Turns<1>)), grid = ceil_div(pieces * p.rows, 8);
-        return wide ? launch_early(dequantize_kernel<E, 16>, grid, dim3(256), 0, stream, 0, p, (uint32_t)pieces)
+        const int64_t pieces = ceil_div(p.cols, 32 * kTurns * (wide ? 8 : 1)), grid = ceil_div(pieces * p.rows, 8);
+        return wide ? launch_early(dequantize_kernel<E, 8>, grid, dim3(256), 0, stream, 0, p, (uint32_t)pieces)
                     : launch_early(dequantize_kernel<E, 1>, grid, dim3(256), 0, stream, 0, p, (uint32_t)pieces);
     });
 }
