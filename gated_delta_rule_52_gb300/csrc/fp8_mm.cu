@@ -95,6 +95,11 @@ struct ScaleRows {
 // share K and join their sums through distributed shared memory, each for a part of the rows of a.
 // The rows of b, of which nearly all bytes are, lie along the MMA's M, so that tiles are full however
 // few rows a has.  Two CTAs per SM keep up to 180 KB of loads in flight.
+//
+// Bound by reading b: 1 x 8192 x 8192 takes 14.2 us, 64 rows 17.2 us, and 67 MB more of b 10.7 us more
+// (6.3 TB/s); 3.5 us go to the way into the pipeline and out of it.  With one lane of a warp issuing
+// behind a branch 1 x 8192 x 8192 took 21 us, with one CTA per SM 24 us, with the sums of one row at
+// a time on their way 64 rows took 19.7 us.
 template <int BT>
 struct TileShape {
     static constexpr int kStage = (kRows + BT) * kFp8Block;
@@ -295,6 +300,15 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
 // cost more than fp32's own rounding.
 //   SPLIT = 2, 4: few tiles; a cluster of SPLIT pairs shares a tile's K and joins the sums through
 // distributed shared memory, each pair for its part of the columns.
+//
+// 8192 x 8192 x 8192 e4m3 to bf16: 302 us, 3.64 PFLOP/s, 1.9 times what bf16 products of a library reach
+// on the same card (356 us when they follow one another for a second, under the power cap); the
+// tensor pipe is active for 83% of the time.  A block of 128 of K costs an SM 256 + BN cycles to load
+// at 64 bytes a cycle, and 2 BN to multiply: wide tiles for many, and where tiles are few more of them.
+// What it took: all of a warp at the waits, one elected lane at the issue (4096^3 74 us instead of
+// 80), scales in 8 groups of places with 4 on their way and handed to the other CTA by a warp that has
+// no copies under way (8192^3 453 us, then 384, then 326), polling instead of suspended waits (512 x
+// 2048 x 512 11.3 us, then 7.3), the accumulator's stores behind its return to the MMAs.
 constexpr int kPairThreads = 384, kStoreWarps = 8;
 constexpr int kSegment = 64;                // blocks of K per segment of an fp32 output
 

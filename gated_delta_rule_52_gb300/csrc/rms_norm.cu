@@ -11,6 +11,12 @@
 // Backward, CTAs are persistent: a thread's columns stay the same, so that its weights and their
 // gradients stay in registers, and the next rows are on their way into shared memory.  Rows that
 // are not aligned, or too long for registers, take kernels of their own.
+//
+// 8192 x 8192 bf16 with a residual: forward 80.3 us to 8 bits (5.9 TB/s) and 80.9 us to bf16 (6.6, a
+// plain copy's rate), bound by memory; backward 85.9 us (6.2 TB/s, and 4 us of it the sums over CTAs):
+// issue 57% at 16 warps per SM.  With 16 elements per thread the backward pass took 121 us, as each
+// row costs a thread some 150 instructions beside those of its elements.  4999 x 1537 fp16, unaligned,
+// forward 10.8 us (2.9 TB/s): element-wise loads and stores.
 #include <algorithm>
 #include <initializer_list>
 #include <utility>
