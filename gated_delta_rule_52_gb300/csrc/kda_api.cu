@@ -384,7 +384,7 @@ const char *kda_status_string(int status) {
         case KDA_ERR_DTYPE: return "KDA_ERR_DTYPE: bad state or element dtype";
         case KDA_ERR_SHAPE: return "KDA_ERR_SHAPE: inconsistent sizes";
         case KDA_ERR_UNSUPPORTED: return "KDA_ERR_UNSUPPORTED: only K = V = 128 (delta rule) and 2 to 4 taps (short convolution) are supported";
-        case KDA_ERR_ALIGN: return "KDA_ERR_ALIGN: tensor pointer not aligned (16 bytes; the element for the recurrence, norm and convolution)";
+        case KDA_ERR_ALIGN: return "KDA_ERR_ALIGN: tensor pointer not aligned (16 bytes; the element for the recurrence, norms and convolution), or rows of the 8-bit product's operands not 16 bytes or of their scales not 4 bytes aligned";
         case KDA_ERR_VALUE: return "KDA_ERR_VALUE: lower_bound outside [-5, 0], non-finite scale, bad eps or activation, or workspace too small";
         case KDA_ERR_CUDA: return "KDA_ERR_CUDA: CUDA call or launch failed";
         case KDA_ERR_TIMEOUT: return "KDA_ERR_TIMEOUT: a bounded device wait expired";
@@ -403,6 +403,6 @@ kda_status kda_get_device_status(void *stream) {
     return h == 0 ? KDA_OK : static_cast<kda_status>(h);
 }
 
-int kda_version(void) { return 102; }
+int kda_version(void) { return 103; }
 
 }  // extern "C"

@@ -123,7 +123,8 @@ def matmul(a, a_scales, b, b_scales, out, add=None, stream=None) -> None:
     """Writes out[..., n] = add[..., n] + sum_k a[..., k] b[n, k], of the values that the 8-bit
     tensors ``a`` [..., K] and ``b`` [N, K] stand for, asynchronously on ``stream`` (default: the
     current torch stream).  Scales are those of rows or of tiles, by their shape.  ``out``
-    [..., N] is bf16, fp16 or fp32, ``add`` None or like it (it may be ``out``).  Rows of a and b
+    [..., N] is bf16, fp16 or fp32, ``add`` None or like it (it may be ``out``, or one row
+    expanded to all, a bias).  Rows of a and b
     start at multiples of 16 bytes, those of the scales at multiples of 4, as ``empty`` lays them
     out; sums are fp32."""
     ca, cb, dt, sa, sb = _code("a", a), _code("b", b), _args.dtype_code("out", out), a.shape, b.shape

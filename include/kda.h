@@ -42,7 +42,8 @@ typedef enum {
                                 cu_seqlens, num_seqs < 1 with cu_seqlens, or more than
                                 2^26 - 1 (sequence, head) units (N * H) in one call    */
     KDA_ERR_UNSUPPORTED = 4, /* K != 128 or V != 128 (the only head size supported)    */
-    KDA_ERR_ALIGN = 5,       /* a tensor pointer is not 16-byte aligned                 */
+    KDA_ERR_ALIGN = 5,       /* a tensor pointer is not 16-byte aligned (the operators
+                                below name their own alignments)                       */
     KDA_ERR_VALUE = 6,       /* lower_bound outside [-5, 0], non-finite scale, or (for
                                 kda_fwd_ws) a workspace smaller than required          */
     KDA_ERR_CUDA = 7,        /* a CUDA runtime call or kernel launch failed             */
@@ -485,7 +486,8 @@ kda_status kda_fp8_dequantize(const void *q, int64_t q_stride, int q_dtype, cons
  *                  likewise.  Rows start at multiples of 16 bytes, rows of scales at multiples
  *                  of 4 (else KDA_ERR_ALIGN); what lies between two rows is not read
  *   out            [M, N] of dtype, rows out_stride elements apart
- *   add            [M, N] of dtype, rows add_stride apart (it may be out), or NULL (zero)
+ *   add            [M, N] of dtype, rows add_stride apart (it may be out; stride 0: one row for
+ *                  all, a bias), or NULL (zero)
  * A projection y = x W^T takes a = x, b = W; its gradients dx = dy W and dW = dy^T x take the
  * transposed tensors of kda_fp8_quantize: a = dy, b = W^T, and a = dy^T, b = x^T.
  */

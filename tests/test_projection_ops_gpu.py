@@ -144,6 +144,26 @@ def test_quantize(rows, cols, dt, to, how, tile):
         assert torch.equal(back.cpu().double(), want), name
 
 
+@pytest.mark.parametrize("rows,cols,tile", [(77, 131, False), (140, 264, True), (33, 520, False)])
+def test_quantize_one_way_and_to_rows_of_any_alignment(rows, cols, tile):
+    x = _quant_input(rows, cols, BF, 3).cuda()
+    want, e = ref.quantized(x.cpu().double(), E4, tile)
+    want_t, e_t = ref.quantized(x.cpu().double().T, E4, tile)
+    for off in (0, 1, 8):                                     # dense rows, from some element on
+        room = torch.zeros(rows * cols + 16, dtype=torch.uint8, device="cuda")
+        for q, shape, value, ex in ((True, (rows, cols), want, e), (False, (cols, rows), want_t, e_t)):
+            room.zero_()
+            t = room[off:off + rows * cols].view(shape).view(E4)
+            s = torch.zeros(ex.shape, dtype=torch.uint8, device="cuda").view(E8)
+            fp8.quantize(x, *((t, s) if q else (None, None)), **({} if q else {"qt": t, "scales_t": s}), tile=tile)
+            _status()
+            assert torch.equal(s.cpu().view(torch.uint8), ref.bytes_of(ex)) and torch.equal(ref.values(t, s), value)
+            assert not room[:off].any() and not room[off + rows * cols:].any()
+            back = torch.empty(shape, dtype=BF, device="cuda")
+            fp8.dequantize(t, s, back)
+            assert torch.equal(back.cpu().double(), value)
+
+
 @pytest.mark.parametrize("to", [E4, E5])
 @pytest.mark.parametrize("dt", [BF, HF, F])
 def test_quantize_what_is_not_finite(dt, to):
@@ -443,6 +463,35 @@ def test_norm_in_place():
         rms_norm.rms_norm_fwd(a, w, EPS, a, residual=res.cuda())
         assert torch.equal(a, out)
     _status()
+
+
+def test_norm_of_one_row_and_to_dense_rows_of_8_bits():
+    g = _gen(4)
+    for shape in ((640,), (3, 2, 264), (5, 333), (4, 1004)):
+        x, w = torch.randn(shape, generator=g).to(BF), 1 + 0.2 * torch.randn(shape[-1], generator=g)
+        D, rows = shape[-1], x.numel() // shape[-1]
+        out = torch.zeros(x.numel(), dtype=torch.uint8, device="cuda").view(shape).view(E4)
+        s = torch.zeros(*shape[:-1], ref.blocks(D), dtype=torch.uint8, device="cuda").view(E8)
+        rstd = torch.empty(shape[:-1], device="cuda")
+        rms_norm.rms_norm_fwd(x.cuda(), w.cuda(), EPS, out, rstd=rstd, scales=s)
+        _status()
+        _, y, r = ref.rms(x.view(rows, D), None, w, EPS)
+        assert_close("rstd", rstd.view(rows), r, _sum_err(D) * r)
+        _close8("out", out.view(torch.uint8).view(rows, D).view(E4), s.view(torch.uint8).view(rows, -1).view(E8), y, 2 * _sum_err(D) * y.abs())
+        got = rms_norm.rms_norm_bwd(x.cuda(), x.cuda(), w.cuda(), rstd)
+        assert got["dx"].shape == x.shape and got["dweight"].shape == (D,)
+
+
+@pytest.mark.parametrize("M", [2, 100, 700])
+def test_one_row_added_to_all(M):
+    g = _gen(M)
+    a, sa = _small_operand(M, 256, E4, False, g)
+    b, sb = _small_operand(264, 256, E4, True, g)
+    bias = torch.randint(-5, 6, (264,), generator=g).float().cuda()
+    out = torch.empty(M, 264, device="cuda")
+    fp8.matmul(a, sa, b, sb, out, add=bias.expand(M, 264))
+    _status()
+    assert torch.equal(out.cpu().double(), ref.product(a, sa, b, sb, bias.expand(M, 264)))
 
 
 @pytest.mark.parametrize("M", [2, 129])
