@@ -102,14 +102,17 @@ def rows(name, t, dtype, shape, lead: int, width: int, dev: int | None = None) -
 
 
 def matrix(name, t, dtype, shape, lead: int, dev: int) -> tuple:
-    """Data pointer and row stride of a tensor for ``rows``; one of two dimensions, which costs the
-    host least, with a look at each attribute."""
-    if isinstance(t, torch.Tensor) and len(shape) == 2 and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
-        step = t.stride()
-        if step[1] == 1:
-            return t.data_ptr(), shape[1] if shape[0] == 1 else step[0]
+    """Data pointer and row stride of a tensor for ``rows``."""
     stride = rows(name, t, dtype, shape, lead, math.prod(shape[lead:]), dev)
     return t.data_ptr(), stride
+
+
+def width(t, cols: int) -> int:
+    """Row stride of a matrix of ``cols`` columns whose rows are contiguous, or -1."""
+    if t.is_contiguous():
+        return cols
+    step = t.stride()
+    return step[0] if step[1] == 1 else -1
 
 
 def states(initial_state, final_state, shape, dev: int):

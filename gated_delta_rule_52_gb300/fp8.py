@@ -83,11 +83,94 @@ def _pair(name, q, s, code, shape, tile, dev):
     return *_args.matrix(name, q, q.dtype, shape, lead, dev), *_scales(f"scales of {name}", s, shape, lead, tile, dev)
 
 
+# A short call's time is that of its checks.  The functions with _plain_ in front take matrices on the
+# current stream and look once at each attribute; they make the same checks as the function itself
+# and do nothing and return False where anything is not as it should be, or not this plain: the
+# function then says what.  (A product's call: 7.5 us instead of 10.3.)
+
+
+def _plain_quantize(x, q, scales, qt, scales_t, tile) -> bool:
+    try:
+        dt, (R, C), dev = _args.DTYPES[x.dtype], x.shape, x.get_device()
+        wx, br, bc = _args.width(x, C), -(-R // BLOCK), -(-C // BLOCK)
+        if not dev == _args.current_device() >= 0 or wx < 0:
+            return False
+        code = pq = ps = pt = pst = None
+        wq = ws = wt = wst = 0
+        if q is not None:
+            code = DTYPES[q.dtype]
+            if q.shape != (R, C) or scales.shape != (br if tile else R, bc) or scales.dtype is not SCALE or not q.get_device() == scales.get_device() == dev:
+                return False
+            pq, wq, ps, ws = q.data_ptr(), _args.width(q, C), scales.data_ptr(), _args.width(scales, bc)
+        elif scales is not None:
+            return False
+        if qt is not None:
+            ct = DTYPES[qt.dtype]
+            if (code is not None and ct != code) or qt.shape != (C, R) or scales_t.shape != (bc if tile else C, br) or \
+                    scales_t.dtype is not SCALE or not qt.get_device() == scales_t.get_device() == dev:
+                return False
+            code, pt, wt, pst, wst = ct, qt.data_ptr(), _args.width(qt, R), scales_t.data_ptr(), _args.width(scales_t, br)
+        elif scales_t is not None or code is None:
+            return False
+    except (AttributeError, KeyError, TypeError, ValueError):
+        return False
+    if wq < 0 or ws < 0 or wt < 0 or wst < 0:
+        return False
+    _args.done(_args.entry("kda_fp8_quantize")(x.data_ptr(), wx, dt, pq, wq, ps, ws, pt, wt, pst, wst, code, bool(tile), R, C,
+                                               _args.stream_handle(None, dev)))
+    return True
+
+
+def _plain_dequantize(q, scales, out) -> bool:
+    try:
+        code, dt, (R, C), (Ro, Co), (Rs, Cs), dev = DTYPES[q.dtype], _args.DTYPES[out.dtype], q.shape, out.shape, scales.shape, q.get_device()
+    except (AttributeError, KeyError, TypeError, ValueError):
+        return False
+    tile, n = Rs != R, -(-C // BLOCK)
+    if R != Ro or C != Co or Cs != n or (tile and Rs != -(-R // BLOCK)) or scales.dtype is not SCALE or \
+            not dev == out.get_device() == scales.get_device() == _args.current_device() >= 0:
+        return False
+    wq, ws, wo = _args.width(q, C), _args.width(scales, n), _args.width(out, C)
+    if wq < 0 or ws < 0 or wo < 0:
+        return False
+    _args.done(_args.entry("kda_fp8_dequantize")(q.data_ptr(), wq, code, scales.data_ptr(), ws, tile, out.data_ptr(), wo, dt, R, C,
+                                                 _args.stream_handle(None, dev)))
+    return True
+
+
+def _plain_matmul(a, a_scales, b, b_scales, out, add) -> bool:
+    try:
+        ca, cb, dt = DTYPES[a.dtype], DTYPES[b.dtype], _args.DTYPES[out.dtype]
+        (M, K), (N, L), (Mo, No), (Ma, Ka), (Nb, Kb) = a.shape, b.shape, out.shape, a_scales.shape, b_scales.shape
+        dev, n = a.get_device(), -(-K // BLOCK)
+        pp, wp = None, 0
+        if add is not None:
+            if add.dtype is not out.dtype or add.shape != (M, N) or add.get_device() != dev:
+                return False
+            pp, wp = add.data_ptr(), _args.width(add, N)
+    except (AttributeError, KeyError, TypeError, ValueError):
+        return False
+    ta, tb = Ma != M, Nb != N
+    if (K != L or M != Mo or N != No or Ka != n or Kb != n or (ta and Ma != -(-M // BLOCK)) or (tb and Nb != -(-N // BLOCK))
+            or a_scales.dtype is not SCALE or b_scales.dtype is not SCALE
+            or not dev == b.get_device() == out.get_device() == a_scales.get_device() == b_scales.get_device() == _args.current_device() >= 0):
+        return False
+    wa, wb, wo, was, wbs = _args.width(a, K), _args.width(b, K), _args.width(out, N), _args.width(a_scales, n), _args.width(b_scales, n)
+    if wa < 0 or wb < 0 or wo < 0 or was < 0 or wbs < 0 or wp < 0:
+        return False
+    _args.done(_args.entry("kda_fp8_matmul")(
+        a.data_ptr(), wa, ca, a_scales.data_ptr(), was, ta, b.data_ptr(), wb, cb, b_scales.data_ptr(), wbs, tb, out.data_ptr(), wo, pp, wp,
+        dt, M, N, K, _args.stream_handle(None, dev)))
+    return True
+
+
 def quantize(x, q=None, scales=None, qt=None, scales_t=None, tile=False, stream=None) -> None:
     """Writes ``x`` [..., cols] (bf16, fp16 or fp32, rows evenly spaced) in 8 bits to ``q``, shaped
     like x, and ``scales``, and its transpose to ``qt`` [cols, rows] and ``scales_t``, whose blocks
     lie along x's columns; one pass over x does both.  Asynchronous on ``stream`` (default: the
     current torch stream)."""
+    if stream is None and _plain_quantize(x, q, scales, qt, scales_t, tile):
+        return
     dt, shape = _args.dtype_code("x", x), x.shape
     lead = len(shape) - 1
     if lead < 1:
@@ -107,6 +190,8 @@ def quantize(x, q=None, scales=None, qt=None, scales_t=None, tile=False, stream=
 def dequantize(q, scales, out, stream=None) -> None:
     """Writes the values that ``q`` [..., cols] with ``scales`` (of rows, or of tiles) stands for
     to ``out`` (bf16, fp16 or fp32, shaped like q)."""
+    if stream is None and _plain_dequantize(q, scales, out):
+        return
     code, shape = _code("q", q), q.shape
     lead = len(shape) - 1
     if lead < 1:
@@ -127,6 +212,8 @@ def matmul(a, a_scales, b, b_scales, out, add=None, stream=None) -> None:
     expanded to all, a bias).  Rows of a and b
     start at multiples of 16 bytes, those of the scales at multiples of 4, as ``empty`` lays them
     out; sums are fp32."""
+    if stream is None and _plain_matmul(a, a_scales, b, b_scales, out, add):
+        return
     ca, cb, dt, sa, sb = _code("a", a), _code("b", b), _args.dtype_code("out", out), a.shape, b.shape
     lead = len(sa) - 1
     if lead < 1 or len(sb) != 2:

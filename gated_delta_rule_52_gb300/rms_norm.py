@@ -33,12 +33,51 @@ def _maybe(name, t, x, shape, lead, dev):
     return (None, 0) if t is None else _args.matrix(name, t, x.dtype, shape, lead, dev)
 
 
+def _plain_fwd(x, weight, eps, out, residual, residual_out, rstd, scales) -> bool:
+    """The forward pass of matrices on the current stream, like fp8's _plain_ functions: the same
+    checks, each attribute looked at once; False, and nothing done, where it is not that plain."""
+    try:
+        kind, (R, D), dev = x.dtype, x.shape, x.get_device()
+        dt, ot = _args.DTYPES[kind], out.dtype
+        if out.shape != (R, D) or not out.get_device() == dev == _args.current_device() >= 0:
+            return False
+        wx, wo, ps, ws, pr, wr, po, wro = _args.width(x, D), _args.width(out, D), None, 0, None, 0, None, 0
+        if ot is kind:
+            code = dt
+            if scales is not None:
+                return False
+        else:
+            code, n = fp8.DTYPES[ot], -(-D // 128)
+            if scales.shape != (R, n) or scales.dtype is not fp8.SCALE or scales.get_device() != dev:
+                return False
+            ps, ws = scales.data_ptr(), _args.width(scales, n)
+        if residual is not None:
+            if residual.dtype is not kind or residual.shape != (R, D) or residual.get_device() != dev:
+                return False
+            pr, wr = residual.data_ptr(), _args.width(residual, D)
+        if residual_out is not None:
+            if residual is None or residual_out.dtype is not kind or residual_out.shape != (R, D) or residual_out.get_device() != dev:
+                return False
+            po, wro = residual_out.data_ptr(), _args.width(residual_out, D)
+    except (AttributeError, KeyError, TypeError, ValueError):
+        return False
+    if wx < 0 or wo < 0 or ws < 0 or wr < 0 or wro < 0:
+        return False
+    f32 = torch.float32
+    _args.done(_args.entry("kda_rms_norm_fwd")(
+        x.data_ptr(), wx, pr, wr, _args.optional("weight", weight, f32, (D,), dev), eps, out.data_ptr(), wo, code, ps, ws, po, wro,
+        _args.optional("rstd", rstd, f32, (R,), dev), dt, R, D, _args.stream_handle(None, dev)))
+    return True
+
+
 def rms_norm_fwd(x, weight, eps, out, residual=None, residual_out=None, rstd=None, scales=None, stream=None) -> None:
     """Writes ``out`` [..., D] and, where given, ``residual_out`` (the sum h, like ``x``) and
     ``rstd`` (fp32, one value per row), asynchronously on ``stream`` (default: the current torch
     stream).  ``out`` is of x's type (it may be ``x`` or ``residual``), or torch.float8_e4m3fn
     or torch.float8_e5m2 with ``scales`` [..., ceil(D/128)] of torch.float8_e8m0fnu;
     ``residual_out`` may be ``x`` or ``residual``."""
+    if stream is None and _plain_fwd(x, weight, eps, out, residual, residual_out, rstd, scales):
+        return
     dev, dt, shape, lead, D, rows, px, xs = _shape(x)
     code, row = fp8.DTYPES.get(out.dtype) if isinstance(out, torch.Tensor) else None, shape[:-1]
     if code is None:

@@ -177,6 +177,75 @@ def test_bindings_refuse(name, calls):
         assert not made, bad
 
 
+# matrices on the current stream, whose checks are the short ones
+PLAIN = {
+    "rms_norm_fwd": lambda: {k: v for k, v in CALLS["rms_norm_fwd"][1]().items() if k != "stream"},
+    "fp8_quantize": lambda: {k: v for k, v in CALLS["fp8_quantize"][1]().items() if k != "stream"},
+    "fp8_dequantize": lambda: {k: v for k, v in CALLS["fp8_dequantize"][1]().items() if k != "stream"},
+    "fp8_matmul": lambda: {"a": _t(6, 512, dtype=E5), "a_scales": _t(6, 4, dtype=E8), "b": _t(200, 512, dtype=E4),
+                           "b_scales": _t(2, 4, dtype=E8), "out": _t(6, 200), "add": _t(6, 200)},
+}
+WIDER = {   # strides that the short checks pass on, and those of which they make nothing
+    "rms_norm_fwd": [{"x": _t(6, 300, dtype=BF)[:, 9:265]}, {"out": _t(6, 256, dtype=BF), "scales": None}, {"residual": _t(1, 256, dtype=BF).expand(6, 256)},
+                     {"residual": None, "residual_out": None}, {"weight": None, "rstd": None}],
+    "fp8_quantize": [{"x": _t(6, 300)[:, :256]}, {"q": None, "scales": None}, {"qt": None, "scales_t": None}, {"scales": _t(6, 4, dtype=E8)[:, :2]},
+                     {"tile": True, "scales": _t(1, 2, dtype=E8), "scales_t": _t(2, 1, dtype=E8)}],
+    "fp8_dequantize": [{"q": _t(300, 272, dtype=E5)[:, :256]}, {"scales": _t(300, 2, dtype=E8)}, {"out": _t(300, 999, dtype=BF)[:, 1:257]}],
+    "fp8_matmul": [{"add": None}, {"add": _t(200).expand(6, 200)}, {"out": _t(6, 400)[:, 200:]}, {"b_scales": _t(200, 8, dtype=E8)[:, :4]},
+                   {"a_scales": _t(1, 4, dtype=E8)}, {"a": _t(0, 512, dtype=E5), "a_scales": _t(0, 4, dtype=E8), "out": _t(0, 200), "add": None}],
+}
+WRONG = {
+    "rms_norm_fwd": [b for b in BAD["rms_norm_fwd"]] + [{"x": _t(6, 512, dtype=BF)[:, ::2]}],
+    "fp8_quantize": [b for b in BAD["fp8_quantize"]] + [{"qt": _t(6, 256, dtype=E5).T}, {"scales": _t(6, 4, dtype=E8)[:, ::2]}],
+    "fp8_dequantize": [b for b in BAD["fp8_dequantize"]] + [{"out": _t(256, 300).T}],
+    "fp8_matmul": [{"a": _t(6, 500, dtype=E5)}, {"b": _t(200, 512)}, {"b": _t(199, 512, dtype=E4)}, {"out": _t(6, 200, dtype=E4)}, {"out": _t(5, 200)},
+                   {"add": _t(6, 200, dtype=BF)}, {"add": _t(200)}, {"a_scales": _t(6, 3, dtype=E8)}, {"a_scales": _t(2, 4, dtype=E8)},
+                   {"b_scales": _t(200, 4)}, {"b_scales": None}, {"out": _t(6, 400)[:, ::2]}, {"add": _t(200, 6).T}, {"a": None}],
+}
+
+
+@pytest.fixture
+def passed(calls, monkeypatch):
+    """What reaches the entry points, on the current stream and on a given one."""
+    seen = []
+    monkeypatch.setattr(_args, "entry", lambda name: lambda *a: seen.append((name, *a[:-1])) or 0)
+    monkeypatch.setattr(_args, "stream_handle", lambda stream, dev: 0)
+    return seen
+
+
+@pytest.mark.parametrize("name", PLAIN)
+def test_short_checks_pass_on_what_the_long_ones_do(name, passed):
+    call = CALLS[name][0]
+    for change in ({}, *WIDER[name]):
+        a = {**PLAIN[name](), **change}
+        call(**a)
+        call(**a, stream=_Stream(0))
+        assert len(passed) == 2 and passed[0][0] == "kda_" + name and passed[0] == passed[1], change
+        passed.clear()
+
+
+@pytest.mark.parametrize("name", PLAIN)
+def test_short_checks_refuse(name, passed, calls):
+    call, current = CALLS[name][0], calls[1]
+    for bad in WRONG[name]:
+        for stream in ({}, {"stream": _Stream(0)}):
+            with pytest.raises((ValueError, TypeError)):
+                call(**{**PLAIN[name](), **bad}, **stream)
+        assert not passed, bad
+    for k, v in PLAIN[name]().items():
+        if isinstance(v, torch.Tensor):
+            for gpu in (1, -1):
+                a = PLAIN[name]()
+                a[k].gpu = gpu
+                with pytest.raises(ValueError):
+                    call(**a)
+                assert not passed, k
+    current[0] = 1
+    with pytest.raises(ValueError, match="cuda:1"):
+        call(**PLAIN[name]())
+    assert not passed
+
+
 def test_empty_lays_rows_out_for_the_product():
     q, s = fp8.empty(5, 300, E5, device="cpu")
     assert q.shape == (5, 300) and q.stride() == (304, 1) and q.dtype == E5
