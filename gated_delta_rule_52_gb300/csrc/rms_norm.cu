@@ -160,6 +160,17 @@ constexpr int kBwdThreads = 512;
 template <typename E> constexpr int kBwdMost = sizeof(E) == 4 ? 16 : 32;
 template <typename E, int EL> constexpr int kBwdStages = std::min(4, 192 * 1024 / (kBwdThreads * EL * 3 * (int)sizeof(E)));
 
+// Sum over the CTA's rows side by side, in their order; a thread takes whole columns.  (One row
+// after the other, with a barrier between them, took 6 us of 18 at 4096 x 1024.)
+__device__ __forceinline__ void sum_side_by_side(const float *sums, int stride, int D, float *out) {
+    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < D; c += blockDim.x * blockDim.y) {
+        float t = 0.f;
+#pragma unroll 4
+        for (int y = 0; y < (int)blockDim.y; ++y) t += sums[y * stride + c];
+        out[c] = t;
+    }
+}
+
 template <typename E, int EL>
 __global__ void __launch_bounds__(kBwdThreads, 1) rms_bwd_row_kernel(RmsParams p, float *part_out) {
     sm103::wait_for_prior_kernels();
@@ -267,26 +278,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) rms_bwd_row_kernel(RmsParams p
     }
     copies_wait<0>();
     if (!part_out) return;
-    // over the CTA's rows side by side, one after the other
-    float *sums = reinterpret_cast<float *>(smem);   // [EL][blockDim.x], over the ring
-    for (int y = 0; y < (int)blockDim.y; ++y) {
-        __syncthreads();
-        if ((int)threadIdx.y != y) continue;
+    // Rows side by side: each leaves its gradients over the ring, as groups of 4 columns.
+    __syncthreads();
+    float *sums = reinterpret_cast<float *>(smem);   // [blockDim.y][EL blockDim.x]
 #pragma unroll
-        for (int e = 0; e < EL; ++e) {
-            float *at = sums + e * blockDim.x + threadIdx.x;
-            if (y > 0) dw[e] += *at;
-            if (y + 1 < (int)blockDim.y) *at = dw[e];
-        }
-    }
-    if (threadIdx.y == blockDim.y - 1) {
-        float *at = part_out + (int64_t)blockIdx.x * p.D;
+    for (int k = 0; k < N; ++k)
 #pragma unroll
-        for (int e = 0; e < EL; ++e) {
-            const int c = column<V>(e / V) + e % V;
-            if (c < D) at[c] = dw[e];
+        for (int j = 0; j < V; j += 4) {
+            const float *d = dw + k * V + j;
+            if (column<V>(k) < D)
+                *reinterpret_cast<float4 *>(sums + threadIdx.y * EL * blockDim.x + column<V>(k) + j) = make_float4(d[0], d[1], d[2], d[3]);
         }
-    }
+    __syncthreads();
+    sum_side_by_side(sums, EL * blockDim.x, D, part_out + (int64_t)blockIdx.x * D);
 }
 
 // ---- rows that are not aligned: a warp takes blocks of 128 columns, 4 columns 32 apart to a lane, NB
@@ -445,22 +449,11 @@ __global__ void __launch_bounds__(512) rms_bwd_odd_kernel(RmsParams p, float *pa
         }
     }
     if (!part_out) return;
-    // over the CTA's rows side by side, one after the other
-    float *sums = reinterpret_cast<float *>(smem);   // [4 NB][blockDim.x]
-    for (int y = 0; y < (int)blockDim.y; ++y) {
-        __syncthreads();
-        if ((int)threadIdx.y != y) continue;
+    float *sums = reinterpret_cast<float *>(smem) + threadIdx.y * 4 * NB * blockDim.x;   // [blockDim.y][4 NB blockDim.x]
 #pragma unroll
-        for (int e = 0; e < 4 * NB; ++e) {
-            float *at = sums + e * blockDim.x + threadIdx.x;
-            if (y > 0) dw[e / 4][e % 4] += *at;
-            if (y + 1 < (int)blockDim.y) *at = dw[e / 4][e % 4];
-        }
-    }
-    if (threadIdx.y == blockDim.y - 1) {
-#pragma unroll
-        for (int k = 0; k < NB; ++k) st_block<float, false>(part_out + (int64_t)blockIdx.x * p.D, (int64_t)(warp + k * warps) * kFp8Block, p.D, lane, dw[k]);
-    }
+    for (int k = 0; k < NB; ++k) st_block<float, false>(sums, (int64_t)(warp + k * warps) * kFp8Block, p.D, lane, dw[k]);
+    __syncthreads();
+    sum_side_by_side(reinterpret_cast<float *>(smem), 4 * NB * blockDim.x, (int)p.D, part_out + (int64_t)blockIdx.x * p.D);
 }
 
 // ---- rows too long for registers: a CTA each, two passes (the second through L1 and L2)
@@ -568,6 +561,7 @@ __global__ void __launch_bounds__(128) rms_weight_part_kernel(RmsParams p, int p
 
 // 32 columns per CTA, the parts in 32 slices, in a fixed order.  (8 slices took 7 us of 152 parts.)
 __global__ void __launch_bounds__(1024) rms_weight_sum_kernel(RmsParams p, int64_t parts, const float *part) {
+    constexpr int kAtOnce = 5;   // of 152 parts all
     sm103::wait_for_prior_kernels();
     sm103::allow_next_kernel();
     __shared__ float sums[32][33];
@@ -575,8 +569,13 @@ __global__ void __launch_bounds__(1024) rms_weight_sum_kernel(RmsParams p, int64
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float t = 0.f;
     if (c < p.D) {
-#pragma unroll 8
-        for (int64_t j = slice; j < parts; j += 32) t += part[j * p.D + c];
+        for (int64_t j = slice; j < parts; j += 32 * kAtOnce) {
+            float f[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) f[i] = j + 32 * i < parts ? part[(j + 32 * i) * p.D + c] : 0.f;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) t += f[i];
+        }
     }
     sums[slice][lane] = t;
     __syncthreads();
@@ -712,7 +711,7 @@ cudaError_t launch_rms_bwd(const RmsParams &p, unsigned char *ws, int sms, cudaS
         }
         if (p.D <= kOddBwdMaxD) {
             const dim3 block = odd_bwd_block(p);
-            return launch_early(rms_bwd_odd_kernel<E, 4>, odd_bwd_grid(p, sms), block, 16 * block.x * 4, stream, 0, p, part);
+            return launch_early(rms_bwd_odd_kernel<E, 4>, odd_bwd_grid(p, sms), block, 16 * block.x * block.y * 4, stream, 0, p, part);
         }
         const bool wide = aligned_rows(p, 4, {{p.x, p.xs}, {p.dout, p.ds}, {p.dres, p.drs}, {p.dx, p.D}});
         const cudaError_t e =
