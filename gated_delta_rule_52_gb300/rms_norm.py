@@ -100,11 +100,38 @@ def rms_norm_fwd(x, weight, eps, out, residual=None, residual_out=None, rstd=Non
         _args.optional("rstd", rstd, f32, row, dev), dt, rows, D, _args.stream_handle(stream, dev)))
 
 
+def _plain_bwd(dout, x, weight, rstd, dresidual, want_dweight):
+    """The backward pass, likewise: its result, or None."""
+    try:
+        kind, (R, D), dev = x.dtype, x.shape, x.get_device()
+        dt, wx, wd, pr, wr = _args.DTYPES[kind], _args.width(x, D), _args.width(dout, D), None, 0
+        if dout.dtype is not kind or dout.shape != (R, D) or not dout.get_device() == dev == _args.current_device() >= 0:
+            return None
+        if dresidual is not None:
+            if dresidual.dtype is not kind or dresidual.shape != (R, D) or dresidual.get_device() != dev:
+                return None
+            pr, wr = dresidual.data_ptr(), _args.width(dresidual, D)
+    except (AttributeError, KeyError, TypeError, ValueError):
+        return None
+    if wx < 0 or wd < 0 or wr < 0:
+        return None
+    f32 = torch.float32
+    pw, ps = _args.optional("weight", weight, f32, (D,), dev), _args.tensor("rstd", rstd, f32, (R,), dev)
+    dx, dw = torch.empty_like(x, memory_format=torch.contiguous_format), None
+    if weight is not None if want_dweight is None else want_dweight:
+        dw = rstd.new_empty((D,)) if weight is None else torch.empty_like(weight)
+    _args.done(_args.entry("kda_rms_norm_bwd")(dout.data_ptr(), wd, x.data_ptr(), wx, pw, ps, pr, wr, dx.data_ptr(),
+                                               None if dw is None else dw.data_ptr(), dt, R, D, _args.stream_handle(None, dev)))
+    return {"dx": dx, "dweight": dw}
+
+
 def rms_norm_bwd(dout, x, weight, rstd, dresidual=None, want_dweight=None, stream=None) -> dict:
     """Gradients of sum(dout * out) + sum(dresidual * residual_out); ``x`` is the sum h that was
     normed and ``rstd`` what the forward wrote.  Returns a dict of new tensors: dx (like x,
     contiguous: the gradient of the forward's x and of its residual) and fp32 dweight (None
     unless ``want_dweight``, by default where there is a weight)."""
+    if stream is None and (plain := _plain_bwd(dout, x, weight, rstd, dresidual, want_dweight)):
+        return plain
     dev, dt, shape, lead, D, rows, px, xs = _shape(x)
     pdo, dos = _args.matrix("dout", dout, x.dtype, shape, lead, dev)
     pd, ds = _maybe("dresidual", dresidual, x, shape, lead, dev)
