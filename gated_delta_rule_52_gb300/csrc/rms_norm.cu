@@ -116,6 +116,19 @@ __global__ void __launch_bounds__(512) rms_fwd_row_kernel(RmsParams p) {
                 if (column<V>(k) < D) *reinterpret_cast<Pack<E, V> *>(sum + column<V>(k)) = h[k];
         }
     }
+    // Few rows: the weights are asked for before the row's sum is waited for (64 x 2048 bf16 1.85 us
+    // instead of 2.05; with more in registers it does not pay, nor in fp32).
+    constexpr bool kEarly = EL == 8 && sizeof(E) == 2;
+    float w[kEarly ? EL : V];
+    const auto weights = [&](int k, float (&to)[V]) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) ld_f<float, 4>(p.weight + column<V>(k) + j, reinterpret_cast<float (&)[4]>(to[j]));
+    };
+    if constexpr (kEarly) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (p.weight && column<V>(k) < D) weights(k, reinterpret_cast<float (&)[V]>(w[k * V]));
+    }
     float s[V], t = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) s[j] = 0.f;
@@ -135,16 +148,16 @@ __global__ void __launch_bounds__(512) rms_fwd_row_kernel(RmsParams p) {
         const int c = column<V>(k);
         const bool in = c < D;
         if (OUT == 0 && !in) continue;
-        float a[V], w[V];
+        float a[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) a[j] = 0.f;
         if (in) {
             unpack<E, V>(h[k], a);
             scale_n(a, rstd);
             if (p.weight) {
-#pragma unroll
-                for (int j = 0; j < V; j += 4) ld_f<float, 4>(p.weight + c + j, reinterpret_cast<float (&)[4]>(w[j]));
-                mul_n<V>(a, a, w);
+                float (&f)[V] = reinterpret_cast<float (&)[V]>(w[kEarly ? k * V : 0]);
+                if constexpr (!kEarly) weights(k, f);
+                mul_n<V>(a, a, f);
             }
         }
         if constexpr (OUT == 0) st_f<E, V>(static_cast<E *>(p.out) + row * p.os + c, a);
@@ -204,13 +217,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) rms_bwd_row_kernel(RmsParams p
     };
     float w[EL], dw[EL];
 #pragma unroll
-    for (int k = 0; k < N; ++k)
+    for (int k = 0; k < EL; k += 4) {
+        const int c = column<V>(k / V) + k % V;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = column<V>(k) + j;
-            w[k * V + j] = p.weight && c < D ? p.weight[c] : 1.f;
-            dw[k * V + j] = 0.f;
-        }
+        for (int j = 0; j < 4; ++j) w[k + j] = 1.f, dw[k + j] = 0.f;
+        if (p.weight && c < D) ld_f<float, 4>(p.weight + c, reinterpret_cast<float (&)[4]>(w[k]));
+    }
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) request(i);
     int stage = 0, turn = 0;
@@ -612,20 +624,31 @@ bool bwd_in_registers(const RmsParams &p) {
     return p.D <= bwd_most(p) && p.D % V == 0 && aligned_rows(p, V, {{p.x, p.xs}, {p.dout, p.ds}, {p.dres, p.drs}, {p.dx, p.D}});
 }
 // Elements per thread: a warp to a short row; many of longer ones, as each row costs a thread about
-// 150 instructions beside those of its elements.
-int bwd_el(const RmsParams &p) {
+// 150 instructions beside those of its elements, but few where an SM has up to 4 rows (64 x 4096 bf16
+// 5.6 us with 8, 7.6 with 32; 1200 x 4096 11.3 and 10.5).
+int bwd_el(const RmsParams &p, int sms) {
     const int most = p.dtype == kFP32 ? kBwdMost<float> : kBwdMost<__half>;
+    const bool few = p.rows <= 4 * sms;
+    if (few && p.D <= 8192) return p.D <= 4096 ? 8 : 16;
     return p.D <= 256 ? 8 : p.D <= 512 || most == 16 ? 16 : 32;
 }
+// A few rows, up to `most` KB a tensor, are one CTA's, which has the whole gradient of the weight: no
+// workspace and no second launch, which take the host 5 us.  On the GPU 4 x 4096 bf16 (32 KB) take
+// 6.4 us so and 7.2 us with a CTA each, 8 x 4096 8.1 and 7.4; 8 x 1023 (16 KB) 4.7 and 4.9, 16 x 1023
+// 7.8 and 4.9.
+bool one_cta(const RmsParams &p, int most) { return p.dweight && p.rows * p.D * (int64_t)dtype_bytes(p.dtype) <= most << 10; }
+constexpr int kOneCta = 32, kOneCtaOdd = 16;
 // Rows side by side have barriers of their own, of which a CTA has 15 beside the common one; no
 // more of them than leaves every SM a row.
 dim3 bwd_block(const RmsParams &p, int sms) {
-    dim3 block = row_block(p.D, bwd_el(p), kBwdThreads);
+    dim3 block = row_block(p.D, bwd_el(p, sms), kBwdThreads);
     if (block.x > 32) block.y = std::min(block.y, 15u);
-    block.y = (unsigned)std::min((int64_t)block.y, std::max(ceil_div(p.rows, sms), (int64_t)1));
+    block.y = (unsigned)std::min((int64_t)block.y, std::max(ceil_div(p.rows, one_cta(p, kOneCta) ? 1 : sms), (int64_t)1));
     return block;
 }
-int64_t bwd_grid(const RmsParams &p, int sms) { return std::min(ceil_div(p.rows, (int64_t)bwd_block(p, sms).y), (int64_t)sms); }
+int64_t bwd_grid(const RmsParams &p, int sms) {
+    return std::min(ceil_div(p.rows, (int64_t)bwd_block(p, sms).y), (int64_t)(one_cta(p, kOneCta) ? 1 : sms));
+}
 // Rows that are not aligned: 4 blocks of 128 to a warp, 2 where few rows leave most of the GPU idle.
 int odd_blocks(const RmsParams &p, int sms) { return p.D <= 2 * 128 || p.rows <= 4 * sms ? 2 : 4; }
 dim3 odd_block(const RmsParams &p, int nb, int most) {
@@ -639,6 +662,7 @@ constexpr int64_t kOddFwdMaxD = 4096, kOddBwdMaxD = 8192;
 dim3 odd_bwd_block(const RmsParams &p) { return odd_block(p, 4, 256); }
 int64_t odd_bwd_grid(const RmsParams &p, int sms) {
     const dim3 block = odd_bwd_block(p);
+    if (one_cta(p, kOneCtaOdd)) return 1;
     return std::min(ceil_div(p.rows, (int64_t)block.y), (int64_t)sms * std::max(512 / (int)(block.x * block.y), 1));
 }
 int64_t weight_parts(const RmsParams &p, int sms) {
@@ -676,7 +700,10 @@ cudaError_t run_bwd(const RmsParams &p, float *part, int sms, cudaStream_t strea
 
 }  // namespace
 
-size_t rms_bwd_scratch_bytes(const RmsParams &p, int sms) { return p.dweight ? (size_t)(weight_parts(p, sms) * p.D) * sizeof(float) : 0; }
+size_t rms_bwd_scratch_bytes(const RmsParams &p, int sms) {
+    const int64_t parts = p.dweight ? weight_parts(p, sms) : 0;
+    return parts > 1 ? (size_t)(parts * p.D) * sizeof(float) : 0;
+}
 
 cudaError_t launch_rms_fwd(const RmsParams &p, int sms, cudaStream_t stream) {
     return with_dtype(p.dtype, [&](auto *tag) {
@@ -698,13 +725,13 @@ cudaError_t launch_rms_fwd(const RmsParams &p, int sms, cudaStream_t stream) {
 }
 
 cudaError_t launch_rms_bwd(const RmsParams &p, unsigned char *ws, int sms, cudaStream_t stream) {
-    float *part = p.dweight ? reinterpret_cast<float *>(ws) : nullptr;
     const int64_t parts = weight_parts(p, sms);
+    float *part = parts == 1 || !p.dweight ? p.dweight : reinterpret_cast<float *>(ws);
     const cudaError_t e = with_dtype(p.dtype, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
         if (p.rows == 0) return cudaSuccess;
         if (bwd_in_registers(p)) {
-            const int el = bwd_el(p);
+            const int el = bwd_el(p, sms);
             if (el == 8) return run_bwd<E, 8>(p, part, sms, stream);
             if (el == 16) return run_bwd<E, 16>(p, part, sms, stream);
             if constexpr (sizeof(E) == 2) return run_bwd<E, 32>(p, part, sms, stream);
@@ -719,7 +746,7 @@ cudaError_t launch_rms_bwd(const RmsParams &p, unsigned char *ws, int sms, cudaS
         if (e != cudaSuccess || !p.dweight) return e;
         return launch_early(rms_weight_part_kernel<E>, ceil_div(p.D, 128) * parts, dim3(128), 0, stream, 0, p, (int)parts, part);
     });
-    if (e != cudaSuccess || !p.dweight) return e;
+    if (e != cudaSuccess || part == p.dweight) return e;
     return launch_early(rms_weight_sum_kernel, ceil_div(p.D, 32), dim3(1024), 0, stream, 0, p, parts, part);
 }
 

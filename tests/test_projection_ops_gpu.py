@@ -267,6 +267,17 @@ def test_rms_norm(rows, D, dt, out8, residual, weight, how):
     assert_close("dweight", got["dweight"], dw, (min(rows, 512) + 40) * 2.0 ** -23 * (dy.double() * hat).abs().sum(0))
 
 
+# few rows: one CTA's (up to 32 KB a tensor, 16 where they are not aligned), and one more; few and many
+# elements to a thread
+FEW = [(4, 4096, BF), (5, 4096, BF), (64, 256, HF), (65, 256, HF), (16, 512, F), (17, 512, F), (8, 1023, BF), (9, 1023, BF), (2, 4096, F),
+       (1, 16384, BF), (63, 8, BF), (2048, 8, BF), (2049, 8, BF), (608, 1032, BF), (609, 1032, BF), (300, 4104, HF), (620, 8192, BF)]
+
+
+@pytest.mark.parametrize("rows,D,dt", FEW)
+def test_rms_norm_of_few_rows(rows, D, dt):
+    test_rms_norm(rows, D, dt, None, True, True, "dense")
+
+
 # ------------------------------------------------------------------ calls of other kinds
 def test_norm_product_and_gradients_in_a_row():
     """A norm in 8 bits, the product that reads it, and the backward pass's: each step against its
