@@ -340,6 +340,18 @@ __device__ __forceinline__ void tile_at(uint32_t t, uint32_t down, uint32_t acro
     i = first + in - j * high;
 }
 
+// 32 bytes in one load.
+template <typename P>
+__device__ __forceinline__ void ld_sector(const void *at, P (&to)[2]) {
+    uint32_t u[8];
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "l"(at)
+                 : "memory");
+    static_assert(sizeof(to) == sizeof(u), "two groups of 16 bytes");
+    memcpy(&to, u, sizeof(u));
+}
+
 // The first n of V neighbours (the others 0), in one load where all exist.
 template <typename E, int V>
 __device__ __forceinline__ Pack<E, V> ld_row(const E *p, int n) {
@@ -350,50 +362,68 @@ __device__ __forceinline__ Pack<E, V> ld_row(const E *p, int n) {
     return r;
 }
 
-// 16 columns at a time of 32 rows (one to a lane) to out, with the addend, by single elements:
-// neighbouring lanes take neighbouring columns.  The addend of the next 16 is on its way while these
-// are stored.  `own`: 32 x 17 fp32 of shared memory.
+// One element, where there is one (a branch around each of many would cost more than the access).
+template <typename E>
+__device__ __forceinline__ E ld_one(const E *at, bool there) {
+    if constexpr (sizeof(E) == 4) {
+        float v;
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t@q ld.global.f32 %0, [%1];\n\t}"
+                     : "=f"(v) : "l"(at), "r"((int)there) : "memory");
+        return v;
+    } else {
+        uint16_t v;
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b16 %0, 0;\n\t@q ld.global.b16 %0, [%1];\n\t}"
+                     : "=h"(v) : "l"(at), "r"((int)there) : "memory");
+        return *reinterpret_cast<E *>(&v);
+    }
+}
+template <typename E>
+__device__ __forceinline__ void st_one(E *at, E v, bool there) {
+    if constexpr (sizeof(E) == 4)
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q st.global.f32 [%0], %1;\n\t}" ::"l"(at), "f"(v), "r"((int)there) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q st.global.b16 [%0], %1;\n\t}" ::"l"(at),
+                     "h"(*reinterpret_cast<const uint16_t *>(&v)), "r"((int)there)
+                     : "memory");
+}
+
+// out and its addend by single elements, 16 columns of 32 rows at a time: a lane takes column
+// lane % 16 of every other row, so that neighbours take neighbours.
 template <typename E>
 struct NarrowRows {
-    const MatmulParams &p;
-    float *own;
-    int64_t m, n0;
-    int lane, rows;
-    float a[16];
-    __device__ __forceinline__ NarrowRows(const MatmulParams &p, float *own, int64_t m0, int64_t n0, int lane)
-        : p(p), own(own), m(m0 + (lane >> 4)), n0(n0), lane(lane), rows((int)min(max(p.a.rows - m, (int64_t)0), (int64_t)32)) {}
+    E *out;
+    const E *add;
+    int64_t os, as;   // two rows on
+    int rows, cols;   // from this lane's first row and column on
+    __device__ __forceinline__ NarrowRows(const MatmulParams &p, int64_t m0, int64_t n0, int lane) {
+        const int64_t m = m0 + (lane >> 4), n = n0 + (lane & 15);
+        out = static_cast<E *>(p.out) + m * p.os + n;
+        add = p.add ? static_cast<const E *>(p.add) + m * p.as + n : nullptr;
+        os = 2 * p.os, as = 2 * p.as;
+        rows = (int)min(max(p.a.rows - m, (int64_t)0), (int64_t)32);
+        cols = (int)min(p.b.rows - n, (int64_t)1 << 30);
+    }
+    // Column c of rows 0, 2, ..., 30 from this lane's first on (0 where there is no addend).
     __device__ __forceinline__ void addend(int c, E (&to)[16]) const {
-        const int64_t n = n0 + c + (lane & 15);
-        const E *plus = static_cast<const E *>(p.add) + m * p.as + n;
-        const int some = p.add && n < p.b.rows ? rows : 0;
+        const E *at = add + c;
+        const int some = add && c < cols ? rows : 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) to[i] = 2 * i < some ? plus[2 * i * p.as] : from_f<E>(0.f);
+        for (int i = 0; i < 16; ++i, at += as) to[i] = ld_one(at, 2 * i < some);
     }
-    __device__ __forceinline__ void take_addend(int c) {
-        E t[16];
-        addend(c, t);
+    __device__ __forceinline__ void put(int c, const E (&v)[16]) const {
+        E *at = out + c;
+        const int some = c < cols ? rows : 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) a[i] = to_f(t[i]);
+        for (int i = 0; i < 16; ++i, at += os) st_one(at, v[i], 2 * i < some);
     }
-    // Columns c .. + 15, of which the addend was taken; `next`: it is taken for those behind them.
-    __device__ __forceinline__ void store(const float (&r)[16], int c, bool next) {
+    // From 16 columns of a row to a lane to this order.  `own`: 32 x 17 fp32 of shared memory.
+    static __device__ __forceinline__ void turn(float *own, float *r, int lane) {
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < 16; ++e) own[lane * 17 + e] = r[e];
         __syncwarp();
-        const int64_t n = n0 + c + (lane & 15);
-        const int some = n < p.b.rows ? rows : 0;
-        E *to = static_cast<E *>(p.out) + m * p.os + n;
-        E o[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float v = own[(2 * i + (lane >> 4)) * 17 + (lane & 15)];
-            o[i] = from_f<E>(p.add ? v + a[i] : v);
-        }
-        if (next) take_addend(c + 16);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (2 * i < some) to[2 * i * p.os] = o[i];
+        for (int i = 0; i < 16; ++i) r[i] = own[(2 * i + (lane >> 4)) * 17 + (lane & 15)];
     }
 };
 
@@ -420,6 +450,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     const int k_begin = SPLIT > 1 ? 4 * (each * part + min(part, over)) : 0;
     const int k_end = SPLIT > 1 ? min(k_begin + 4 * (each + (part < over)), blocks) : blocks;
     const int segment = kSums ? kSegment : blocks;
+    const bool narrow_rows = __builtin_expect(wide == 0, 0);   // their code off the others' way
     if (threadIdx.x == 0) {
         prefetch_map(&args.a);
         prefetch_map(&args.b);
@@ -595,8 +626,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                 const int64_t left = p.b.rows - n0;          // columns of out from here on
                 const E *plus = p.add ? static_cast<const E *>(p.add) + (m0 + lane) * p.as + n0 : nullptr;
                 const bool my_row = m0 + lane < p.a.rows;
-                NarrowRows<E> narrow(p, reinterpret_cast<float *>(own), m0, n0, lane);
-                const auto addend = [&](int c) { return ld_row<E, V>(plus + c, my_row ? (int)min(left - c, (int64_t)V) : 0); };
+                // a sector at a time where rows start with one
+                const auto addend = [&](int c, Pack<E, V> (&to)[2]) {
+                    const int n = my_row ? (int)min(left - c, (int64_t)(2 * V)) : 0;
+                    if (kSums && wide == 2 && n >= 2 * V) {
+                        ld_sector(plus + c, to);
+                    } else {
+                        to[0] = ld_row<E, V>(plus + c, n);
+                        to[1] = ld_row<E, V>(plus + c + V, n - V);
+                    }
+                };
                 // 64 bytes of every row to one of the two buffers (16-byte piece j of row r at
                 // j ^ (r / 2 % 4), the 64-byte swizzle), and from there by a tensor store, which leaves
                 // out what is outside
@@ -614,150 +653,82 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                         bulk_commit();
                     }
                 };
-                if constexpr (kSums) {
-                    // 16 columns at a time: from TMEM, or where K has several segments from their sum
-                    const auto emit = [&](int c, float (&r)[16], const Pack<E, V> (&add)[4]) {
-                        if (!wide) {
-                            narrow.store(r, c, c + 16 < cols);
-                            return;
-                        }
-                        Pack<E, V> piece[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float (&v)[V] = reinterpret_cast<float (&)[V]>(r[j * V]);
-                            if (plus) {
-                                float a[V];
-                                unpack<E, V>(add[j], a);
-                                add_n<V>(v, v, a);
-                            }
-                            st_f<E, V>(piece[j].e, v);
-                        }
-                        send(c, piece);
-                    };
-                    Pack<E, V> add[4];
-                    const auto take = [&](int c) {
-                        if (wide && plus)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) add[j] = addend(c + j * V);
-                    };
-                    if (!wide) narrow.take_addend(0);
-                    if (blocks <= kSegment) {
-                        const int buf = sum.at;
-                        take(0);
-                        ok = warp_wait<false>(&tfull[buf], sum.turn);
-                        if (!ok) break;
-                        sum.next();
-                        tc_fence_after();
-                        const uint32_t from = tmem_addr(acc, quarter * 32, buf * BN + half * kMost);
-#pragma unroll 1
-                        for (int c = 0; c < cols; c += 16) {
-                            float r[16];
-                            Pack<E, V> now[4];
-                            tmem_ld16(from + c, r);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) now[j] = add[j];
-                            if (c + 16 < cols) take(c + 16);
-                            tmem_ld_wait();
-                            emit(c, r, now);
-                        }
-                        tc_fence_before();
-                        if (lane == 0) mbar_arrive_remote_only(bars + 8 * buf);
-                    } else {
-                        float f[kMost];
-                        for (int k = 0; k < blocks; k += kSegment) {
-                            const int buf = sum.at;
-                            ok = warp_wait<false>(&tfull[buf], sum.turn);
-                            if (!ok) break;
-                            sum.next();
-                            tc_fence_after();
-                            const uint32_t from = tmem_addr(acc, quarter * 32, buf * BN + half * kMost);
-#pragma unroll
-                            for (int c = 0; c < kMost; c += 16) {
-                                if (c >= cols) break;
-                                float r[16];
-                                tmem_ld16(from + c, r);
-                                tmem_ld_wait();
-                                if (k == 0) {
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) f[c + e] = r[e];
-                                } else {
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) f[c + e] += r[e];
-                                }
-                            }
-                            tc_fence_before();
-                            if (lane == 0) mbar_arrive_remote_only(bars + 8 * buf);
-                        }
-                        if (!ok) break;
-#pragma unroll
-                        for (int c = 0; c < kMost; c += 16) {
-                            if (c >= cols) break;
-                            take(c);
-                            emit(c, reinterpret_cast<float (&)[16]>(f[c]), add);
-                        }
-                    }
-                    continue;
-                }
-                // this lane's row in 16 bits (or where rows are not wide: what it stores of 32 rows),
-                // which begins as the addend's, read while the MMAs run
+                // this lane's row (or where rows are not wide: its share of 32 rows), which begins as the
+                // addend's, read while the MMAs run; the sums of the segments of K are added to it
                 Pack<E, V> o[kMost / V];
                 E (&single)[kMost] = reinterpret_cast<E (&)[kMost]>(o);
-                if (plus) {
+                if (narrow_rows) {
+                    const NarrowRows<E> narrow(p, m0, n0, lane);
 #pragma unroll
-                    for (int c = 0; c < kMost; c += 16) {
-                        if (c >= cols) break;
-                        if (!wide) {
-                            narrow.addend(c, reinterpret_cast<E (&)[16]>(single[c]));
-                        } else {
+                    for (int c = 0; c < kMost; c += 16)
+                        if (c < cols) narrow.addend(c, reinterpret_cast<E (&)[16]>(single[c]));
+                } else if (plus) {
 #pragma unroll
-                            for (int e = 0; e < 16; e += V) o[(c + e) / V] = addend(c + e);
-                        }
-                    }
+                    for (int c = 0; c < kMost; c += 2 * V)
+                        if (c < cols) addend(c, reinterpret_cast<Pack<E, V> (&)[2]>(o[c / V]));
+                } else if (kSums) {
+#pragma unroll
+                    for (int c = 0; c < kMost; ++c) single[c] = from_f<E>(0.f);
                 }
-                const int buf = sum.at;
-                ok = warp_wait<false>(&tfull[buf], sum.turn);
-                if (!ok) break;
-                sum.next();
-                tc_fence_after();
-                const uint32_t from = tmem_addr(acc, quarter * 32, buf * BN + half * kMost);
-                if (wide) {
+                int k = 0;
+                do {
+                    const int buf = sum.at;
+                    ok = warp_wait<false>(&tfull[buf], sum.turn);
+                    if (!ok) break;
+                    sum.next();
+                    tc_fence_after();
+                    const uint32_t from = tmem_addr(acc, quarter * 32, buf * BN + half * kMost);
+// this lane's kStep columns from c on, added to what is held of them
+                    const auto join = [&](int c, float (&r)[kStep]) {
 #pragma unroll
-                    for (int c = 0; c < kMost; c += 32) {
-                        if (c >= cols) break;
-                        float r[32];
-                        tmem_ld32(from + c, r);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; e += V) {
+                        for (int e = 0; e < kStep; e += V) {
                             float (&v)[V] = reinterpret_cast<float (&)[V]>(r[e]);
-                            if (plus) {
+                            if (kSums || plus) {
                                 float a[V];
                                 unpack<E, V>(o[(c + e) / V], a);
                                 add_n<V>(v, v, a);
                             }
                             st_f<E, V>(o[(c + e) / V].e, v);
                         }
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < kMost; c += 16) {
-                        if (c >= cols) break;
-                        float r[16];
-                        tmem_ld16(from + c, r);
+                    };
+                    const auto sums_at = [&](int c, float (&r)[kStep]) {
+                        if constexpr (kStep == 32) tmem_ld32(from + c, r);
+                        else tmem_ld16(from + c, r);
                         tmem_ld_wait();
-                        if (plus) {
+                    };
+                    if (!narrow_rows) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) narrow.a[i] = to_f(single[c + i]);
+                        for (int c = 0; c < kMost; c += kStep) {
+                            if (c >= cols) break;
+                            float r[kStep];
+                            sums_at(c, r);
+                            join(c, r);
                         }
-                        narrow.store(r, c, false);
-                    }
-                }
-                tc_fence_before();
-                if (lane == 0) mbar_arrive_remote_only(bars + 8 * buf);
-                if (!wide) continue;
+                    } else {
 #pragma unroll
-                for (int c = 0; c < kMost; c += 32)
-                    if (c < cols) send(c, reinterpret_cast<const Pack<E, V> (&)[4]>(o[c / V]));
+                        for (int c = 0; c < kMost; c += kStep) {
+                            if (c >= cols) break;
+                            float r[kStep];
+                            sums_at(c, r);
+#pragma unroll
+                            for (int e = 0; e < kStep; e += 16) NarrowRows<E>::turn(reinterpret_cast<float *>(own), r + e, lane);
+                            join(c, r);
+                        }
+                    }
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive_remote_only(bars + 8 * buf);
+                } while (kSums && (k += segment) < blocks);
+                if (!ok) break;
+                if (!narrow_rows) {
+#pragma unroll
+                    for (int c = 0; c < kMost; c += kStep)
+                        if (c < cols) send(c, reinterpret_cast<const Pack<E, V> (&)[4]>(o[c / V]));
+                } else {
+                    const NarrowRows<E> narrow(p, m0, n0, lane);
+#pragma unroll
+                    for (int c = 0; c < kMost; c += 16)
+                        if (c < cols) narrow.put(c, reinterpret_cast<const E (&)[16]>(single[c]));
+                }
             }
             if (lane == 0) bulk_wait0();
         }
@@ -800,16 +771,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
             const bool my_row = m0 + lane < p.a.rows;
             E *to = static_cast<E *>(p.out) + (m0 + lane) * p.os + n0;
             const E *plus = p.add ? static_cast<const E *>(p.add) + (m0 + lane) * p.as + n0 : nullptr;
-            NarrowRows<E> narrow(p, reinterpret_cast<float *>(staging + (warp - 4) * kStoreBuffer), m0, n0, lane);
-            if (!wide) narrow.take_addend(0);
-#pragma unroll 1
-            for (int c = 0; c < kSlice; c += 16) {
-                float r[16], s[16];
-                Pack<E, V> a[16 / V];
-                if (wide && plus) {
-#pragma unroll
-                    for (int e = 0; e < 16; e += V) a[e / V] = ld_row<E, V>(plus + c + e, my_row ? (int)min(left - c - e, (int64_t)V) : 0);
-                }
+            // 16 columns' sums of all parts
+            const auto joined = [&](int c, float (&s)[16]) {
+                float r[16];
                 tmem_ld16(from + part * kSlice + c, r);
                 tmem_ld_wait();
 #pragma unroll
@@ -818,25 +782,48 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                 for (int q = 1; q < SPLIT; ++q)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) s[e] += q == part ? r[e] : box[((q < part ? q : q - 1) * kSlice + c + e) * 32];
-                if (!wide) {
-                    narrow.store(s, c, c + 16 < kSlice);
-                    continue;
+            };
+            if (narrow_rows) {
+                const NarrowRows<E> narrow(p, m0, n0, lane);
+                E next[16];
+                narrow.addend(0, next);
+#pragma unroll 1
+                for (int c = 0; c < kSlice; c += 16) {
+                    float s[16];
+                    E v[16];
+                    joined(c, s);
+                    NarrowRows<E>::turn(reinterpret_cast<float *>(staging + (warp - 4) * kStoreBuffer), s, lane);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = from_f<E>(plus ? s[e] + to_f(next[e]) : s[e]);
+                    if (c + 16 < kSlice) narrow.addend(c + 16, next);
+                    narrow.put(c, v);
                 }
-#pragma unroll
-                for (int e = 0; e < 16; e += V) {
-                    float (&v)[V] = reinterpret_cast<float (&)[V]>(s[e]);
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < kSlice; c += 16) {
+                    float s[16];
+                    Pack<E, V> a[16 / V];
                     if (plus) {
-                        float b[V];
-                        unpack<E, V>(a[e / V], b);
-                        add_n<V>(v, v, b);
-                    }
-                    if (!my_row) continue;
-                    if (left - c - e >= V) {
-                        st_f<E, V>(to + c + e, v);
-                    } else {
 #pragma unroll
-                        for (int x = 0; x < V; ++x)
-                            if (x < left - c - e) to[c + e + x] = from_f<E>(v[x]);
+                        for (int e = 0; e < 16; e += V) a[e / V] = ld_row<E, V>(plus + c + e, my_row ? (int)min(left - c - e, (int64_t)V) : 0);
+                    }
+                    joined(c, s);
+#pragma unroll
+                    for (int e = 0; e < 16; e += V) {
+                        float (&v)[V] = reinterpret_cast<float (&)[V]>(s[e]);
+                        if (plus) {
+                            float b[V];
+                            unpack<E, V>(a[e / V], b);
+                            add_n<V>(v, v, b);
+                        }
+                        if (!my_row) continue;
+                        if (left - c - e >= V) {
+                            st_f<E, V>(to + c + e, v);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < V; ++x)
+                                if (x < left - c - e) to[c + e + x] = from_f<E>(v[x]);
+                        }
                     }
                 }
             }
@@ -899,8 +886,8 @@ cudaError_t run_pair(MatmulArgs &args, int sms, cudaStream_t stream) {
     const MatmulParams &p = args.p;
     if (!encode_operand(args.a, p.a, p.K, kRows) || !encode_operand(args.b, p.b, p.K, BN / 2)) return cudaErrorInvalidValue;
     constexpr int V = 16 / sizeof(E);
-    const int wide = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.os % V == 0 &&
-                     (!p.add || (reinterpret_cast<uintptr_t>(p.add) % 16 == 0 && p.as % V == 0));
+    const auto aligned = [&](const void *t, int64_t stride, int n) { return reinterpret_cast<uintptr_t>(t) % (n * sizeof(E)) == 0 && stride % n == 0; };
+    const int wide = !aligned(p.out, p.os, V) || (p.add && !aligned(p.add, p.as, V)) ? 0 : p.add && aligned(p.add, p.as, 2 * V) ? 2 : 1;
     if (SPLIT == 1 && wide && !encode_out(args.out, p)) return cudaErrorInvalidValue;
     const int64_t tiles = ceil_div(p.a.rows, 2 * kRows) * ceil_div(p.b.rows, BN);
     return launch_early(kernel, 2 * SPLIT * (SPLIT > 1 ? tiles : std::min(tiles, (int64_t)sms / 2)), dim3(kPairThreads), S::kSmem, stream, 2 * SPLIT, args, wide);
