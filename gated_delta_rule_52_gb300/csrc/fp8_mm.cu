@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                     sum.next();
                     tc_fence_after();
                     const uint32_t from = tmem_addr(acc, quarter * 32, buf * BN + half * kMost);
-// this lane's kStep columns from c on, added to what is held of them
+                    // this lane's kStep columns from c on, added to what is held of them
                     const auto join = [&](int c, float (&r)[kStep]) {
 #pragma unroll
                         for (int e = 0; e < kStep; e += V) {
