@@ -169,19 +169,37 @@ __global__ void __launch_bounds__(512) rms_fwd_row_kernel(RmsParams p) {
 // that one row's sums form while another is stored
 
 constexpr int kBwdThreads = 512;
+constexpr int kFewCtas = 8;   // of a cluster that has all rows
 // Most elements per thread, and rows in its ring (up to 4, in 192 KB).
 template <typename E> constexpr int kBwdMost = sizeof(E) == 4 ? 16 : 32;
 template <typename E, int EL> constexpr int kBwdStages = std::min(4, 192 * 1024 / (kBwdThreads * EL * 3 * (int)sizeof(E)));
 
-// Sum over the CTA's rows side by side, in their order; a thread takes whole columns.  (One row
-// after the other, with a barrier between them, took 6 us of 18 at 4096 x 1024.)
-__device__ __forceinline__ void sum_side_by_side(const float *sums, int stride, int D, float *out) {
-    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < D; c += blockDim.x * blockDim.y) {
+// Sum over the CTA's rows side by side, in their order, to its part; a thread takes whole columns.
+// (One row after the other, with a barrier between them, took 6 us of 18 at 4096 x 1024.)  A cluster
+// joins its CTAs' sums through distributed shared memory, and has the gradient.
+__device__ __forceinline__ void sum_side_by_side(float *sums, int stride, int D, float *part_out) {
+    const int threads = blockDim.x * blockDim.y, ctas = (int)sm103::cluster_size();
+    float *out = ctas > 1 ? sums : part_out + (int64_t)blockIdx.x * D;
+    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < D; c += threads) {
         float t = 0.f;
 #pragma unroll 4
         for (int y = 0; y < (int)blockDim.y; ++y) t += sums[y * stride + c];
         out[c] = t;
     }
+    if (ctas == 1) return;
+    __syncwarp();
+    sm103::cluster_sync();
+    const uint32_t at = sm103::smem_u32(sums);
+    for (int c = (int)sm103::cluster_ctarank() * threads + threadIdx.y * blockDim.x + threadIdx.x; c < D; c += ctas * threads) {
+        float v[kFewCtas], t = 0.f;
+#pragma unroll
+        for (int q = 0; q < kFewCtas; ++q) v[q] = q < ctas ? sm103::ld_cluster(sm103::mapa_shared(at + 4 * c, q)) : 0.f;
+#pragma unroll
+        for (int q = 0; q < kFewCtas; ++q) t += v[q];
+        part_out[c] = t;
+    }
+    __syncwarp();
+    sm103::cluster_sync();   // the others have read
 }
 
 template <typename E, int EL>
@@ -302,7 +320,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) rms_bwd_row_kernel(RmsParams p
                 *reinterpret_cast<float4 *>(sums + threadIdx.y * EL * blockDim.x + column<V>(k) + j) = make_float4(d[0], d[1], d[2], d[3]);
         }
     __syncthreads();
-    sum_side_by_side(sums, EL * blockDim.x, D, part_out + (int64_t)blockIdx.x * D);
+    sum_side_by_side(sums, EL * blockDim.x, D, part_out);
 }
 
 // ---- rows that are not aligned: a warp takes blocks of 128 columns, 4 columns 32 apart to a lane, NB
@@ -465,7 +483,7 @@ __global__ void __launch_bounds__(512) rms_bwd_odd_kernel(RmsParams p, float *pa
 #pragma unroll
     for (int k = 0; k < NB; ++k) st_block<float, false>(sums, (int64_t)(warp + k * warps) * kFp8Block, p.D, lane, dw[k]);
     __syncthreads();
-    sum_side_by_side(reinterpret_cast<float *>(smem), 4 * NB * blockDim.x, (int)p.D, part_out + (int64_t)blockIdx.x * p.D);
+    sum_side_by_side(reinterpret_cast<float *>(smem), 4 * NB * blockDim.x, (int)p.D, part_out);
 }
 
 // ---- rows too long for registers: a CTA each, two passes (the second through L1 and L2)
@@ -632,22 +650,28 @@ int bwd_el(const RmsParams &p, int sms) {
     if (few && p.D <= 8192) return p.D <= 4096 ? 8 : 16;
     return p.D <= 256 ? 8 : p.D <= 512 || most == 16 ? 16 : 32;
 }
-// A few rows, up to `most` KB a tensor, are one CTA's, which has the whole gradient of the weight: no
-// workspace and no second launch, which take the host 5 us.  On the GPU 4 x 4096 bf16 (32 KB) take
-// 6.4 us so and 7.2 us with a CTA each, 8 x 4096 8.1 and 7.4; 8 x 1023 (16 KB) 4.7 and 4.9, 16 x 1023
-// 7.8 and 4.9.
-bool one_cta(const RmsParams &p, int most) { return p.dweight && p.rows * p.D * (int64_t)dtype_bytes(p.dtype) <= most << 10; }
-constexpr int kOneCta = 32, kOneCtaOdd = 16;
+// A few rows, up to `most` KB a tensor, are one cluster's or one CTA's, which have the whole gradient of
+// the weight: no workspace and no second launch, which take the host 5 us (a call 13 us instead of 18).
+// On the GPU, with a cluster and without: 64 x 256 bf16 2.7 us and 4.1, 64 x 1024 4.1 and 4.3, 128 x
+// 1024 (256 KB) 5.6 and 4.5; unaligned 32 x 1023 4.5 and 5.1, 16 x 4095 (128 KB) 7.2 and 6.0.  Up to
+// 4 KB one CTA is as fast (2 x 256 2.0 us, a cluster 3.5).
+int few_ctas(const RmsParams &p, int most) {
+    const int64_t bytes = p.rows * p.D * (int64_t)dtype_bytes(p.dtype);
+    return !p.dweight || bytes > most << 10 ? 0 : bytes <= 4 << 10 ? 1 : (int)std::min(p.rows, (int64_t)kFewCtas);
+}
+constexpr int kFew = 256, kFewOdd = 128;
 // Rows side by side have barriers of their own, of which a CTA has 15 beside the common one; no
 // more of them than leaves every SM a row.
 dim3 bwd_block(const RmsParams &p, int sms) {
     dim3 block = row_block(p.D, bwd_el(p, sms), kBwdThreads);
     if (block.x > 32) block.y = std::min(block.y, 15u);
-    block.y = (unsigned)std::min((int64_t)block.y, std::max(ceil_div(p.rows, one_cta(p, kOneCta) ? 1 : sms), (int64_t)1));
+    const int few = few_ctas(p, kFew);
+    block.y = (unsigned)std::min((int64_t)block.y, std::max(ceil_div(p.rows, few ? few : sms), (int64_t)1));
     return block;
 }
 int64_t bwd_grid(const RmsParams &p, int sms) {
-    return std::min(ceil_div(p.rows, (int64_t)bwd_block(p, sms).y), (int64_t)(one_cta(p, kOneCta) ? 1 : sms));
+    const int few = few_ctas(p, kFew);
+    return few ? few : std::min(ceil_div(p.rows, (int64_t)bwd_block(p, sms).y), (int64_t)sms);
 }
 // Rows that are not aligned: 4 blocks of 128 to a warp, 2 where few rows leave most of the GPU idle.
 int odd_blocks(const RmsParams &p, int sms) { return p.D <= 2 * 128 || p.rows <= 4 * sms ? 2 : 4; }
@@ -662,13 +686,13 @@ constexpr int64_t kOddFwdMaxD = 4096, kOddBwdMaxD = 8192;
 dim3 odd_bwd_block(const RmsParams &p) { return odd_block(p, 4, 256); }
 int64_t odd_bwd_grid(const RmsParams &p, int sms) {
     const dim3 block = odd_bwd_block(p);
-    if (one_cta(p, kOneCtaOdd)) return 1;
+    if (const int few = few_ctas(p, kFewOdd)) return few;
     return std::min(ceil_div(p.rows, (int64_t)block.y), (int64_t)sms * std::max(512 / (int)(block.x * block.y), 1));
 }
 int64_t weight_parts(const RmsParams &p, int sms) {
     if (p.rows == 0) return 0;
-    if (bwd_in_registers(p)) return bwd_grid(p, sms);
-    return p.D <= kOddBwdMaxD ? odd_bwd_grid(p, sms) : std::min(ceil_div(p.rows, 64), (int64_t)256);
+    if (bwd_in_registers(p)) return few_ctas(p, kFew) ? 1 : bwd_grid(p, sms);
+    return p.D <= kOddBwdMaxD ? few_ctas(p, kFewOdd) ? 1 : odd_bwd_grid(p, sms) : std::min(ceil_div(p.rows, 64), (int64_t)256);
 }
 
 template <typename E, int NB>
@@ -695,7 +719,8 @@ cudaError_t run_bwd(const RmsParams &p, float *part, int sms, cudaStream_t strea
     const cudaError_t e = allow_smem<kernel>(kBwdThreads * kBytes);
     if (e != cudaSuccess) return e;
     static_assert(kBytes >= EL * 4, "the sums fit the ring");
-    return launch_early(kernel, bwd_grid(p, sms), block, block.x * block.y * kBytes, stream, 0, p, part);
+    const int few = few_ctas(p, kFew);
+    return launch_early(kernel, bwd_grid(p, sms), block, block.x * block.y * kBytes, stream, few > 1 ? few : 0, p, part);
 }
 
 }  // namespace
@@ -738,7 +763,8 @@ cudaError_t launch_rms_bwd(const RmsParams &p, unsigned char *ws, int sms, cudaS
         }
         if (p.D <= kOddBwdMaxD) {
             const dim3 block = odd_bwd_block(p);
-            return launch_early(rms_bwd_odd_kernel<E, 4>, odd_bwd_grid(p, sms), block, 16 * block.x * block.y * 4, stream, 0, p, part);
+            const int few = few_ctas(p, kFewOdd);
+            return launch_early(rms_bwd_odd_kernel<E, 4>, odd_bwd_grid(p, sms), block, 16 * block.x * block.y * 4, stream, few > 1 ? few : 0, p, part);
         }
         const bool wide = aligned_rows(p, 4, {{p.x, p.xs}, {p.dout, p.ds}, {p.dres, p.drs}, {p.dx, p.D}});
         const cudaError_t e =

@@ -267,9 +267,10 @@ def test_rms_norm(rows, D, dt, out8, residual, weight, how):
     assert_close("dweight", got["dweight"], dw, (min(rows, 512) + 40) * 2.0 ** -23 * (dy.double() * hat).abs().sum(0))
 
 
-# few rows: one CTA's (up to 32 KB a tensor, 16 where they are not aligned), and one more; few and many
-# elements to a thread
-FEW = [(4, 4096, BF), (5, 4096, BF), (64, 256, HF), (65, 256, HF), (16, 512, F), (17, 512, F), (8, 1023, BF), (9, 1023, BF), (2, 4096, F),
+# few rows: one CTA's (up to 4 KB a tensor), one cluster's (256 KB, 128 where they are not aligned), and
+# more; few and many elements to a thread
+FEW = [(2, 1024, BF), (3, 1024, BF), (8, 16384, BF), (9, 16384, BF), (7, 96, F), (128, 1024, HF), (129, 1024, HF), (64, 1023, BF), (65, 1023, BF),
+       (3, 8191, HF), (32, 2048, F), (33, 2048, F), (1, 8192, F), (16384, 8, BF), (16385, 8, BF), (4, 4096, BF), (5, 4096, BF), (64, 256, HF), (65, 256, HF), (16, 512, F), (17, 512, F), (8, 1023, BF), (9, 1023, BF), (2, 4096, F),
        (1, 16384, BF), (63, 8, BF), (2048, 8, BF), (2049, 8, BF), (608, 1032, BF), (609, 1032, BF), (300, 4104, HF), (620, 8192, BF)]
 
 
