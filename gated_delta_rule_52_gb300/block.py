@@ -94,6 +94,8 @@ def eight_bits(t, tile=False, rows=True, turned=True, dtype=torch.float8_e4m3fn)
     """The 8-bit forms of ``t`` [..., cols]: (q, scales), and those of its transpose."""
     cols = t.shape[-1]
     m = t.reshape(-1, cols)
+    if cols > 1 and m.stride(1) != 1:          # an expanded gradient, a transposed tensor
+        m = m.contiguous()
     q, s = fp8.empty(*m.shape, dtype, tile, t.device) if rows else (None, None)
     qt, st = fp8.empty(cols, m.shape[0], dtype, tile, t.device) if turned else (None, None)
     fp8.quantize(m, q, s, qt=qt, scales_t=st, tile=tile)
@@ -109,7 +111,7 @@ class Linear(torch.autograd.Function):
         q, s, xt, xts = eight_bits(x)
         wn, wns, wt, wts = eight_bits(w, tile=True)              # W [K, N], and W^T [N, K]
         out = torch.empty(*x.shape[:-1], w.shape[1], dtype=x.dtype, device=x.device)
-        fp8.matmul(q, s, wt, wts, out.view(-1, w.shape[1]), add=None if add is None else add.reshape(-1, w.shape[1]))
+        fp8.matmul(q, s, wt, wts, out.view(-1, w.shape[1]), add=None if add is None else add.contiguous().view(-1, w.shape[1]))
         # (x and w themselves for first_order: gradients depend on them, too)
         ctx.save_for_backward(xt, xts, wn, wns, x, w)
         ctx.added = add is not None
@@ -182,7 +184,7 @@ class Block:
     RMS norm and projections in 8 bits."""
 
     def __init__(self, kind, width, gen, dev="cuda", eight=False):
-        self.kind, self.width, self.heads, self.eight, self.served = kind, width, width // 128, eight, None
+        self.kind, self.width, self.heads, self.eight = kind, width, width // 128, eight
         n = lambda *s, std: (torch.randn(s, generator=gen) * std).to(dev)  # noqa: E731
         self.mixed = width if kind == "glr" else 3 * width       # x, or q, k, v: what the convolution reads
         wide = self.mixed + (2 * width if kind == "glr" else width + self.heads)
@@ -207,7 +209,7 @@ class Block:
         return q, k, v, heads(rest[..., :self.width]), rest[..., self.width:]
 
     def train(self, u):
-        p, self.served = self.p, None
+        p = self.p
         if self.eight:
             z = Linear.apply(RmsNorm.apply(u, p["norm_w"]), p["w_in"], None)
         else:
@@ -217,9 +219,13 @@ class Block:
         return Linear.apply(mix.flatten(2), p["w_out"], u) if self.eight else u + mix.flatten(2) @ p["w_out"]
 
     def state(self, B, dev="cuda"):
-        """Zero states for serving: the convolution's last inputs and the recurrent state."""
+        """Zero states for serving: the convolution's last inputs and the recurrent state; and with
+        8 bits the projections' weights, quantised once for all calls with this state."""
         shape = (B, self.heads, 128) if self.kind == "glr" else (B, self.heads, 128, 128)
-        return {"conv": torch.zeros(B, 3, self.mixed, dtype=torch.bfloat16, device=dev), "mix": torch.zeros(shape, device=dev)}
+        s = {"conv": torch.zeros(B, 3, self.mixed, dtype=torch.bfloat16, device=dev), "mix": torch.zeros(shape, device=dev)}
+        if self.eight:
+            s["weights"] = [eight_bits(self.p[n].detach(), tile=True, rows=False)[2:] for n in ("w_in", "w_out")]
+        return s
 
     @torch.no_grad()
     def serve(self, u, state):
@@ -234,9 +240,7 @@ class Block:
         """serve() in 8 bits.  ``delta``, what the block before adds to the residual stream ``u``, or
         None, is added by the norm, u in place; returns what this block adds."""
         p = self.p
-        if self.served is None:
-            self.served = [eight_bits(p[n], tile=True, rows=False)[2:] for n in ("w_in", "w_out")]
-        (w_in, s_in), (w_out, s_out) = self.served
+        (w_in, s_in), (w_out, s_out) = state["weights"]
         rows = u.view(-1, self.width)
         q, s = fp8.empty(*rows.shape, device=u.device)
         if delta is None:

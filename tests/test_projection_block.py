@@ -24,6 +24,18 @@ def test_second_derivative_is_refused(monkeypatch):
             torch.autograd.grad((first[0].square() + leaves[0].square()).sum(), leaves[0])
 
 
+def test_rows_that_are_not_contiguous_are_laid_out(monkeypatch):
+    """What autograd hands over (an expanded gradient, a transposed tensor) is quantised from contiguous rows."""
+    seen = []
+    monkeypatch.setattr(fp8, "quantize", lambda x, *a, **k: seen.append(x))
+    for t in (torch.ones(()).expand(4, 8), torch.arange(32.).view(8, 4).T, torch.arange(12.)[:, None].expand(2, 12, 8), torch.arange(64.).view(4, 16)[:, ::2]):
+        block.eight_bits(t)
+        assert seen[-1].stride(-1) == 1 and torch.equal(seen[-1], t.reshape(-1, t.shape[-1]))
+    t = torch.arange(64.).view(4, 16)
+    block.eight_bits(t[:, 3:11])             # rows of a wider tensor are read where they are
+    assert seen[-1].data_ptr() == t[:, 3:].data_ptr()
+
+
 def _whole(gen, *shape):
     """Whole numbers that 8 bits hold exactly, whatever their neighbours are: 0 to 3 in magnitude."""
     return torch.randint(-3, 4, shape, generator=gen).to(BF).cuda()
@@ -82,3 +94,27 @@ def test_block_in_eight_bits_trains_and_serves():
     for b in blocks:
         h = b.train(h)
     assert float((whole.float() - h.float()).norm()) <= 2.0 ** -4 * float(whole.float().norm())
+
+
+@pytest.mark.gpu
+def test_gradient_of_a_sum():
+    """An expanded gradient, and an addend that is one: exact on whole numbers."""
+    gen = torch.Generator().manual_seed(5)
+    x, w = _whole(gen, 6, 40).requires_grad_(), _whole(gen, 40, 24).requires_grad_()
+    a = torch.ones((), dtype=BF, device="cuda").expand(6, 24)
+    out = block.Linear.apply(x, w, a)
+    assert torch.equal(out, (x.double() @ w.double() + 1).to(BF))
+    dx, dw = torch.autograd.grad(out.sum(), [x, w])
+    assert torch.equal(dx, w.detach().double().sum(1).expand(6, 40).to(BF)) and torch.equal(dw, x.detach().double().sum(0)[:, None].expand(40, 24).to(BF))
+
+
+@pytest.mark.gpu
+def test_serving_reads_the_weights_as_they_are_at_its_start():
+    gen = torch.Generator().manual_seed(7)
+    b = block.Block("glr", 128, gen, eight=True)
+    u = torch.randn(2, 9, 128, generator=gen).to("cuda", BF)
+    first = block.serve([b], u, 5)
+    with torch.no_grad():
+        b.p["w_out"].zero_()
+    assert torch.equal(block.serve([b], u, 5), u)        # the block adds nothing
+    assert not torch.equal(first, u)
