@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
 // distributed shared memory, each pair for its part of the columns.
 //
 // 8192 x 8192 x 8192 e4m3 to bf16: 302 us, 3.64 PFLOP/s, 1.9 times what bf16 products of a library reach
-// on the same card (356 us when they follow one another for a second, under the power cap); the
+// on the same card (364 us when they follow one another for a second, under the power cap); the
 // tensor pipe is active for 83% of the time.  A block of 128 of K costs an SM 256 + BN cycles to load
 // at 64 bytes a cycle, and 2 BN to multiply: wide tiles for many, and where tiles are few more of them.
 // What it took: all of a warp at the waits, one elected lane at the issue (4096^3 74 us instead of

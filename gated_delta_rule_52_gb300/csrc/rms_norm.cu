@@ -12,9 +12,9 @@
 // gradients stay in registers, and the next rows are on their way into shared memory.  Rows that
 // are not aligned, or too long for registers, take kernels of their own.
 //
-// 8192 x 8192 bf16 with a residual: forward 80.3 us to 8 bits (5.9 TB/s) and 80.9 us to bf16 (6.6, a
-// plain copy's rate), bound by memory; backward 85.9 us (6.2 TB/s, and 4 us of it the sums over CTAs):
-// issue 57% at 16 warps per SM.  With 16 elements per thread the backward pass took 121 us, as each
+// 8192 x 8192 bf16 with a residual: forward 79 us to 8 bits (5.9 TB/s) and 80.9 us to bf16 (6.6, a
+// plain copy's rate), bound by memory; backward 82 us (6.5 TB/s; 76 us without the weight's gradient):
+// issue 53% at 16 warps per SM.  With 16 elements per thread the backward pass took 121 us, as each
 // row costs a thread some 150 instructions beside those of its elements.  4999 x 1537 fp16, unaligned,
 // forward 10.8 us (2.9 TB/s): element-wise loads and stores.
 #include <algorithm>
@@ -589,7 +589,8 @@ __global__ void __launch_bounds__(128) rms_weight_part_kernel(RmsParams p, int p
     part[at * p.D + c] = s;
 }
 
-// 32 columns per CTA, the parts in 32 slices, in a fixed order.  (8 slices took 7 us of 152 parts.)
+// 32 columns per CTA, the parts in 32 slices, in a fixed order.  (A slice's loads one after
+// the other took 1.3 us more.)
 __global__ void __launch_bounds__(1024) rms_weight_sum_kernel(RmsParams p, int64_t parts, const float *part) {
     constexpr int kAtOnce = 5;   // of 152 parts all
     sm103::wait_for_prior_kernels();
