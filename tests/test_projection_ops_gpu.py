@@ -109,6 +109,43 @@ def test_products(M, N, K, ta, tb, a_tile, b_tile, dt, add):
     assert_close("out", out, want, ref.product_bound(a, sa, b, sb) + 2.0 ** -23 * want.abs())
 
 
+# long K of operands beyond the L2: two pairs' tiles share rows of b.  Odd numbers of tiles, one tile
+# above none, rows that end inside a tile and inside a half of the shared rows, both tile widths
+LONG = [
+    (7800, 301, 8300, E5, E4, False, False, F, True),
+    (8192, 256, 8192, E4, E4, False, True, BF, False),
+    (8100, 448, 8192, E4, E5, True, True, HF, True),
+    (300, 8000, 8320, E4, E4, False, True, F, False),
+    (200, 6500, 10240, E5, E5, False, False, F, True),
+    (8192, 2048, 8192, E4, E4, False, True, BF, True),
+]
+
+
+@pytest.mark.parametrize("M,N,K,ta,tb,a_tile,b_tile,dt,add", LONG)
+def test_exact_products_of_long_rows(M, N, K, ta, tb, a_tile, b_tile, dt, add):
+    test_exact_products(M, N, K, ta, tb, a_tile, b_tile, dt, add)
+
+
+def test_shared_rows_back_to_back_and_captured():
+    """The same product three times in a row, and from a graph: the same bits."""
+    g = _gen(77)
+    a, sa = _normal_operand(8000, 8192, E4, False, g)
+    b, sb = _normal_operand(384, 8192, E4, True, g)
+    outs = [torch.full((8000, 384), float("nan"), device="cuda") for _ in range(4)]
+    for o in outs[:3]:
+        fp8.matmul(a, sa, b, sb, o)
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        for _ in range(3):
+            fp8.matmul(a, sa, b, sb, outs[3])
+    graph.replay()
+    graph.replay()
+    _status()
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+
+
 # ------------------------------------------------------------------ 8-bit tensors
 QUANT = [  # rows, cols, dtype, type, how
     (1, 1, BF, E4, "dense"), (1, 128, F, E4, "dense"), (3, 130, HF, E5, "dense"), (128, 128, BF, E4, "dense"),
