@@ -925,7 +925,7 @@ struct Choice {
 // 56, with one round more 4096 x 2560 x 16384 147 and 123).
 bool shares(const MatmulParams &p, int bn, int sms) {
     const int64_t down = ceil_div(p.a.rows, 2 * kRows), across = ceil_div(p.b.rows, bn);
-    return p.K >= 8192 && (p.a.rows + p.b.rows) * p.K >= int64_t(64) << 20 &&
+    return p.K >= 8192 && (p.a.rows + p.b.rows) * (p.K / kFp8Block) >= (int64_t(64) << 20) / kFp8Block &&
            ceil_div(ceil_div(down, 2) * across, clusters_of_4(sms)) <= ceil_div(down * across, (int64_t)sms / 2);
 }
 
