@@ -631,6 +631,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
             constexpr int V = 16 / sizeof(E), kStep = 64 / sizeof(E);   // elements of 16 bytes, and of 64
             const int cols = half ? BN - kMost : kMost;
             unsigned char *own = staging + (warp - 4) * kStoreBuffer;
+            uint32_t turn = 0;                           // of the two store buffers, over all tiles
             Slot<S::kBuffers> sum;
             const uint32_t bars = mapa_shared(smem_u32(tempty), first);
             for (uint32_t t = pair; ok && t < tiles; t += pairs) {
@@ -652,10 +653,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                 };
                 // 64 bytes of every row to one of the two buffers (16-byte piece j of row r at
                 // j ^ (r / 2 % 4), the 64-byte swizzle), and from there by a tensor store, which leaves
-                // out what is outside
+                // out what is outside.  The buffers alternate with the stores, also from a tile to the
+                // next, which may have an odd number: the one store that the wait leaves out is always the
+                // other buffer's.
                 const auto send = [&](int c, const Pack<E, V> (&piece)[4]) {
                     if (c >= left || m0 >= p.a.rows) return;
-                    unsigned char *buffer = own + (c / kStep & 1) * 2048;
+                    unsigned char *buffer = own + turn * 2048;
+                    turn ^= 1;
                     if (lane == 0) bulk_wait_read1();
                     __syncwarp();
 #pragma unroll
