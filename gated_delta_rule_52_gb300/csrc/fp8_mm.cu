@@ -300,8 +300,6 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
 // cost more than fp32's own rounding.
 //   SPLIT = 2, 4: few tiles; a cluster of SPLIT pairs shares a tile's K and joins the sums through
 // distributed shared memory, each pair for its part of the columns.
-//   SHARE = 2: a cluster's two pairs have tiles one above the other and each loads half of the rows of b
-// for both (multicast); a stage is free when both have multiplied it.
 //
 // 8192 x 8192 x 8192 e4m3 to bf16: 302 us, 3.64 PFLOP/s, 1.9 times what bf16 products of a library reach
 // on the same card (364 us when they follow one another for a second, under the power cap); the
@@ -336,9 +334,8 @@ struct PairShape {
 
 // Tile t of a grid of `down` x `across`: 8 tiles down, then across, so that the tiles in flight
 // share rows of both operands in L2.
-template <uint32_t BAND>
 __device__ __forceinline__ void tile_at(uint32_t t, uint32_t down, uint32_t across, uint32_t &i, uint32_t &j) {
-    const uint32_t band = t / (BAND * across), first = band * BAND, high = min(down - first, BAND), in = t - band * BAND * across;
+    const uint32_t band = t / (8 * across), first = band * 8, high = min(down - first, 8u), in = t - band * 8 * across;
     j = in / high;
     i = first + in - j * high;
 }
@@ -430,7 +427,7 @@ struct NarrowRows {
     }
 };
 
-template <typename E, int BN, int SPLIT, int SHARE>
+template <typename E, int BN, int SPLIT>
 __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_constant__ MatmulArgs args, int wide) {
     using S = PairShape<BN, SPLIT>;
     constexpr bool kSums = sizeof(E) == 4 && SPLIT == 1;
@@ -446,13 +443,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     const uint32_t in_cluster = cluster_ctarank(), rank = in_cluster & 1, first = in_cluster & ~1u;
     const uint16_t both_ctas = (uint16_t)(3u << first);
     const int part = SPLIT > 1 ? first >> 1 : 0;
-    // (SHARE: of the cluster's tiles, one above the other)
-    const uint32_t down = (uint32_t)ceil_div(p.a.rows, SHARE * 2 * kRows), across = (uint32_t)ceil_div(p.b.rows, BN), tiles = down * across;
-    const uint32_t pair = blockIdx.x / (2 * SPLIT * SHARE), pairs = gridDim.x / (2 * SPLIT * SHARE);
-    const auto tile_of = [&](uint32_t t, uint32_t &i, uint32_t &j) {
-        tile_at<8 / SHARE>(t, down, across, i, j);
-        if (SHARE > 1) i = i * SHARE + (first >> 1);
-    };
+    const uint32_t down = (uint32_t)ceil_div(p.a.rows, 2 * kRows), across = (uint32_t)ceil_div(p.b.rows, BN), tiles = down * across;
+    const uint32_t pair = blockIdx.x / (2 * SPLIT), pairs = gridDim.x / (2 * SPLIT);
     // blocks of K: all, or this pair's part, which begins at a group of 4
     const int blocks = (int)ceil_div(p.K, kFp8Block), groups = (blocks + 3) / 4, each = groups / SPLIT, over = groups - each * SPLIT;
     const int k_begin = SPLIT > 1 ? 4 * (each * part + min(part, over)) : 0;
@@ -462,7 +454,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     if (threadIdx.x == 0) {
         prefetch_map(&args.a);
         prefetch_map(&args.b);
-        for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], SHARE);
+        for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         for (int i = 0; i < kScaleStages; ++i) mbar_init(&sfull[i], rank == 0 ? 33 : 32), mbar_init(&sempty[i], 1);
         for (int i = 0; i < S::kBuffers; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 2 * kStoreWarps);
         fence_mbar_init();
@@ -484,7 +476,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         const uint32_t bars = mapa_shared(smem_u32(full), first);
         for (uint32_t t = pair; ok && t < tiles; t += pairs) {
             uint32_t ti, tj;
-            tile_of(t, ti, tj);
+            tile_at(t, down, across, ti, tj);
             const int ra = (int)(ti * (2 * kRows) + rank * kRows), rb = (int)(tj * BN + rank * (BN / 2));
             for (int k = k_begin; k < k_end; ++k) {
                 // (a wait for the turn before the first returns at once)
@@ -496,13 +488,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                 if (issuer) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[slot.at], 2 * S::kStage);
                     tma_load_2d_pair(at, &args.a, bars + 8 * slot.at, k * kFp8Block, ra);
-                    unsigned char *to = at + kRows * kFp8Block;
-                    if constexpr (SHARE > 1) {   // a half of these rows of b, for both pairs
-                        const int half = (int)(first >> 1) * (BN / 4);
-                        tma_load_2d_pairs(to + half * kFp8Block, &args.b, bars + 8 * slot.at, k * kFp8Block, rb + half, (uint16_t)(5u << rank));
-                    } else {
-                        tma_load_2d_pair(to, &args.b, bars + 8 * slot.at, k * kFp8Block, rb);
-                    }
+                    tma_load_2d_pair(at + kRows * kFp8Block, &args.b, bars + 8 * slot.at, k * kFp8Block, rb);
                 }
                 slot.next();
                 loads = min(loads + 1, S::kStages);
@@ -524,7 +510,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         const uint32_t idesc = idesc_mx8(2 * kRows, BN, p.a.dtype == kE5M2, p.b.dtype == kE5M2, 0);
         for (uint32_t t = pair; ok && t < tiles; t += pairs) {
             uint32_t ti, tj;
-            tile_of(t, ti, tj);
+            tile_at(t, down, across, ti, tj);
             for (int k0 = k_begin; ok && k0 < k_end; k0 += segment) {
                 if (!warp_wait<false>(&tempty[sum.at], sum.turn ^ 1)) {
                     ok = false;
@@ -562,7 +548,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                     if (issuer) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) mma_mx8_pair(to, ad + 2 * q, bd + 2 * q, id, set, set + 4, k != k0 || q > 0);
-                        mma_commit_pair(&empty[here], SHARE > 1 ? (uint16_t)15 : both_ctas);
+                        mma_commit_pair(&empty[here], both_ctas);
                     }
                     if (k % 4 == 3 || k == blocks - 1) scale.next();
                 }
@@ -577,7 +563,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         const uint32_t bars = mapa_shared(smem_u32(sfull), first);
         for (uint32_t t = pair; ok && t < tiles; t += pairs) {
             uint32_t ti, tj;
-            tile_of(t, ti, tj);
+            tile_at(t, down, across, ti, tj);
             for (int k = k_begin; k < k_end; k += 4) {
                 ok = warp_wait<false>(&sfull[scale.at], scale.turn);
                 if (!ok) break;
@@ -600,7 +586,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         };
         for (uint32_t t = pair; ok && t < tiles; t += pairs) {
             uint32_t ti, tj;
-            tile_of(t, ti, tj);
+            tile_at(t, down, across, ti, tj);
             rows_a.set(p.a, (int64_t)ti * (2 * kRows) + rank * kRows, k_begin, lane);
             rows_b.set(p.b, (int64_t)tj * BN, k_begin, lane);
             for (int k = k_begin; k < k_end; k += 4) {
@@ -636,7 +622,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
             const uint32_t bars = mapa_shared(smem_u32(tempty), first);
             for (uint32_t t = pair; ok && t < tiles; t += pairs) {
                 uint32_t ti, tj;
-                tile_of(t, ti, tj);
+                tile_at(t, down, across, ti, tj);
                 const int64_t m0 = (int64_t)ti * (2 * kRows) + rank * kRows + quarter * 32, n0 = (int64_t)tj * BN + half * kMost;
                 const int64_t left = p.b.rows - n0;          // columns of out from here on
                 const E *plus = p.add ? static_cast<const E *>(p.add) + (m0 + lane) * p.as + n0 : nullptr;
@@ -782,7 +768,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         cluster_sync();
         if (warp >= 4 && ok) {
             uint32_t ti, tj;
-            tile_of(pair, ti, tj);
+            tile_at(pair, down, across, ti, tj);
             constexpr int V = 16 / sizeof(E);
             const int64_t m0 = (int64_t)ti * (2 * kRows) + rank * kRows + quarter * 32;
             const int64_t n0 = (int64_t)tj * BN + half * S::kMost + part * kSlice, left = p.b.rows - n0;
@@ -899,20 +885,20 @@ cudaError_t run_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
 int64_t clusters_of_4(int sms) { return sms * 36 / 152; }
 int64_t clusters_of_8(int sms) { return sms * 15 / 152; }
 
-template <typename E, int BN, int SPLIT, int SHARE = 1>
+template <typename E, int BN, int SPLIT>
 cudaError_t run_pair(MatmulArgs &args, int sms, cudaStream_t stream) {
     using S = PairShape<BN, SPLIT>;
-    constexpr auto kernel = mm_pair_kernel<E, BN, SPLIT, SHARE>;
+    constexpr auto kernel = mm_pair_kernel<E, BN, SPLIT>;
     const cudaError_t e = allow_smem<kernel>(S::kSmem);
     if (e != cudaSuccess) return e;
     const MatmulParams &p = args.p;
-    if (!encode_operand(args.a, p.a, p.K, kRows) || !encode_operand(args.b, p.b, p.K, BN / 2 / SHARE)) return cudaErrorInvalidValue;
+    if (!encode_operand(args.a, p.a, p.K, kRows) || !encode_operand(args.b, p.b, p.K, BN / 2)) return cudaErrorInvalidValue;
     constexpr int V = 16 / sizeof(E);
     const auto aligned = [&](const void *t, int64_t stride, int n) { return reinterpret_cast<uintptr_t>(t) % (n * sizeof(E)) == 0 && stride % n == 0; };
     const int wide = !aligned(p.out, p.os, V) || (p.add && !aligned(p.add, p.as, V)) ? 0 : p.add && aligned(p.add, p.as, 2 * V) ? 2 : 1;
     if (SPLIT == 1 && wide && !encode_out(args.out, p)) return cudaErrorInvalidValue;
-    constexpr int kCtas = 2 * SPLIT * SHARE;
-    const int64_t tiles = ceil_div(p.a.rows, SHARE * 2 * kRows) * ceil_div(p.b.rows, BN), most = SPLIT > 1 ? tiles : SHARE > 1 ? clusters_of_4(sms) : sms / 2;
+    constexpr int kCtas = 2 * SPLIT;
+    const int64_t tiles = ceil_div(p.a.rows, 2 * kRows) * ceil_div(p.b.rows, BN), most = SPLIT > 1 ? tiles : sms / 2;
     return launch_early(kernel, kCtas * std::min(tiles, most), dim3(kPairThreads), S::kSmem, stream, kCtas, args, wide);
 }
 
@@ -920,18 +906,7 @@ cudaError_t run_pair(MatmulArgs &args, int sms, cudaStream_t stream) {
 // kernel).
 struct Choice {
     int bt, bn, split;
-    bool share;
 };
-
-// Pairs that share rows of b read a fifth less, of 72 SM pairs instead of 76: where that leaves as many
-// rounds of tiles, K is long and the operands leave the L2 (2048 x 8192 x 16384 fp32 183 us instead of
-// 195, 8192 x 4096 x 16384 365 and 389, 8192 x 2048 x 8192 bf16 96.5 and 98; 65536 x 512 x 2048 59.5 and
-// 56, with one round more 4096 x 2560 x 16384 147 and 123).
-bool shares(const MatmulParams &p, int bn, int sms) {
-    const int64_t down = ceil_div(p.a.rows, 2 * kRows), across = ceil_div(p.b.rows, bn);
-    return p.K >= 8192 && (p.a.rows + p.b.rows) * (p.K / kFp8Block) >= (int64_t(64) << 20) / kFp8Block &&
-           ceil_div(ceil_div(down, 2) * across, clusters_of_4(sms)) <= ceil_div(down * across, (int64_t)sms / 2);
-}
 
 Choice choose(const MatmulParams &p, int sms) {
     if (p.a.rows <= 64) return {p.a.rows <= 16 ? 16 : p.a.rows <= 32 ? 32 : 64, 0, 0};
@@ -951,7 +926,6 @@ Choice choose(const MatmulParams &p, int sms) {
         least = cost;
         best = c;
     }
-    best.share = best.split == 1 && best.bn > 128 && shares(p, best.bn, sms);
     return best;
 }
 
@@ -984,8 +958,8 @@ cudaError_t launch_matmul(const MatmulParams &p, int sms, cudaStream_t stream) {
         if (c.split == 4) return run_pair<E, 128, 4>(args, sms, stream);
         if (c.split == 2) return c.bn == 128 ? run_pair<E, 128, 2>(args, sms, stream) : run_pair<E, 256, 2>(args, sms, stream);
         if (c.bn == 128) return run_pair<E, 128, 1>(args, sms, stream);
-        if (c.bn == 192) return c.share ? run_pair<E, 192, 1, 2>(args, sms, stream) : run_pair<E, 192, 1>(args, sms, stream);
-        if constexpr (sizeof(E) == 2) return c.share ? run_pair<E, 224, 1, 2>(args, sms, stream) : run_pair<E, 224, 1>(args, sms, stream);
+        if (c.bn == 192) return run_pair<E, 192, 1>(args, sms, stream);
+        if constexpr (sizeof(E) == 2) return run_pair<E, 224, 1>(args, sms, stream);
         return cudaErrorInvalidValue;
     });
 }

@@ -464,16 +464,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const void *tmap, ui
         : "memory");
 }
 
-// The same into that place of every CTA in `ctas` (a mask of the cluster's); the bytes of each count on
-// the barrier at bar's place in its own pair, in the CTA of the same place in the pair as bar's.
-__device__ __forceinline__ void tma_load_2d_pairs(void *dst, const void *tmap, uint32_t bar, int c0, int c1, uint16_t ctas) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(
-            smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "h"(ctas)
-        : "memory");
-}
-
 // Arrives once on `bar` when all previously issued MMAs of this thread finish.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile(

@@ -109,8 +109,8 @@ def test_products(M, N, K, ta, tb, a_tile, b_tile, dt, add):
     assert_close("out", out, want, ref.product_bound(a, sa, b, sb) + 2.0 ** -23 * want.abs())
 
 
-# long K of operands beyond the L2: two pairs' tiles share rows of b.  Odd numbers of tiles, one tile
-# above none, rows that end inside a tile and inside a half of the shared rows, both tile widths
+# long K of operands beyond the L2.  Odd numbers of tiles, one tile above none, rows that end inside a
+# tile and inside a half of it, both tile widths
 LONG = [
     (7800, 301, 8300, E5, E4, False, False, F, True),
     (8192, 256, 8192, E4, E4, False, True, BF, False),
