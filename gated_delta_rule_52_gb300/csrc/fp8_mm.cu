@@ -21,6 +21,10 @@ using namespace sm103;
 constexpr uint64_t kWait = 2000000000ull;   // 2 s per wait
 constexpr int kRows = 128;                  // rows of b per tile: the MMA's M, TMEM's lanes
 constexpr int kScaleStages = 8, kAhead = 4;   // groups of 4 blocks' scales: places, and on their way
+// Blocks of K in one accumulator where the output has 32 bits.  The tensor cores cut an accumulator at
+// each MMA, always towards zero, so that over a long K that would cost more than fp32's own rounding;
+// the sums of the segments are added in registers.
+constexpr int kSegment = 64;
 
 // Waits of the pipelines.  Reading the GPU's timer takes longer than a stage does, so it is read
 // once in many tries only.
@@ -100,6 +104,10 @@ struct ScaleRows {
 // (6.3 TB/s); 3.5 us go to the way into the pipeline and out of it.  With one lane of a warp issuing
 // behind a branch 1 x 8192 x 8192 took 21 us, with one CTA per SM 24 us, with the sums of one row at
 // a time on their way 64 rows took 19.7 us.
+//
+// A long K has an accumulator for each segment, `sums` of them, which are added in registers at the
+// end.  A CTA takes up to half of the SM's TMEM, so that the two of an SM never wait for each other's:
+// CTAs of two clusters that did could wait in a circle.
 template <int BT>
 struct TileShape {
     static constexpr int kStage = (kRows + BT) * kFp8Block;
@@ -108,11 +116,16 @@ struct TileShape {
     static constexpr int kSmem = 1024 + kStage * kStages + kScaleStage * kScaleStages;
     static_assert(BT * kRows * 4 <= kStage * kStages, "the sums fit the ring");
     static constexpr int kSet = 8;                     // TMEM columns of scales
-    static constexpr int kCols = BT + 2 * kSet <= 32 ? 32 : BT + 2 * kSet <= 64 ? 64 : 128;
+    static constexpr int kMostSums = (256 - 2 * kSet) / BT;
+    static int cols(int sums) {                        // TMEM columns, a power of two
+        int n = 32;
+        while (n < sums * BT + 2 * kSet) n *= 2;
+        return n;
+    }
 };
 
 template <typename E, int BT>
-__global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ MatmulArgs args, int split) {
+__global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ MatmulArgs args, int split, int segment, int sums, int cols) {
     using S = TileShape<BT>;
     extern __shared__ unsigned char raw[];
     unsigned char *ring = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -145,7 +158,7 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
         }
     } else if (warp == 1) {
         issuer = elect_one();
-        tmem_alloc(&tmem_base, S::kCols);
+        tmem_alloc(&tmem_base, cols);
         tmem_relinquish();
     }
     wait_for_prior_kernels();
@@ -155,7 +168,7 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t acc = tmem_base, sf = acc + BT;
+    const uint32_t acc = tmem_base, sf = acc + sums * BT;
     if (warp == 0) {
         Slot<S::kStages> slot;
         for (int k = k0 + early; k < k1; ++k) {
@@ -175,8 +188,10 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
         Slot<kScaleStages> scale;
         const uint64_t b0 = sdesc_sw128(smem_u32(ring), 16, 1024), s0 = sdesc_plain(smem_u32(scales), 128);
         const uint32_t idesc = idesc_mx8(kRows, BT, p.b.dtype == kE5M2, p.a.dtype == kE5M2, 0);
-        for (int k = k0; k < k1; ++k) {
+        uint32_t to = acc;
+        for (int k = k0, in = 0; k < k1; ++k, ++in) {
             const uint32_t set = sf + (scale.at & 1) * S::kSet;
+            if (in == segment) in = 0, to += BT;
             if (k % 4 == 0 || k == k0) {
                 ok = warp_wait<false>(&sfull[scale.at], scale.turn);
                 if (!ok) break;
@@ -195,7 +210,7 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
             const uint32_t id = idesc | (k & 3) << 4 | (uint32_t)(k & 3) << 29;
             if (issuer) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) mma_mx8(acc, bd + 2 * q, ad + 2 * q, id, set, set + 4, k != k0 || q > 0);
+                for (int q = 0; q < 4; ++q) mma_mx8(to, bd + 2 * q, ad + 2 * q, id, set, set + 4, in > 0 || q > 0);
                 mma_commit(&empty[slot.at]);
             }
             slot.next();
@@ -239,19 +254,29 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
     E *to = static_cast<E *>(p.out) + m0 * p.os + n;
     const E *plus = p.add ? static_cast<const E *>(p.add) + m0 * p.as + n : nullptr;
     const int real = (int)min(p.a.rows - m0, (int64_t)BT), here = n < p.b.rows ? real : 0;   // rows of a: all, and those to store
+    // 16 rows' sums of all of this CTA's segments, in the order of K
+    const auto summed = [&](int c, float (&r)[16]) {
+        tmem_ld16(tmem_addr(acc, warp * 32, c), r);
+        tmem_ld_wait();
+        for (int k = k0 + segment, at = c + BT; k < k1; k += segment, at += BT) {
+            float more[16];
+            tmem_ld16(tmem_addr(acc, warp * 32, at), more);
+            tmem_ld_wait();
+            add_n<16>(r, r, more);
+        }
+    };
     if (split > 1) {
         // the ring is free: every load and MMA has ended
-        float *sums = reinterpret_cast<float *>(ring) + threadIdx.x;   // [BT][128]
+        float *parts = reinterpret_cast<float *>(ring) + threadIdx.x;   // [BT][128]
         for (int c = 0; c < real; c += 16) {
             float r[16];
-            tmem_ld16(tmem_addr(acc, warp * 32, c), r);
-            tmem_ld_wait();
+            summed(c, r);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sums[(c + j) * kRows] = r[j];
+            for (int j = 0; j < 16; ++j) parts[(c + j) * kRows] = r[j];
         }
         cluster_sync();
         const int rows = BT / split, c1 = min(rows * (rank + 1), real);
-        const uint32_t mine = smem_u32(sums);
+        const uint32_t mine = smem_u32(parts);
         for (int c = rows * rank; c < c1; c += 4) {      // 4 rows' sums on their way
             float v[4][8], add[4];
 #pragma unroll
@@ -276,8 +301,7 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
             float r[16], add[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) add[j] = plus && c + j < here ? to_f(plus[(c + j) * p.as]) : 0.f;
-            tmem_ld16(tmem_addr(acc, warp * 32, c), r);
-            tmem_ld_wait();
+            summed(c, r);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 if (c + j < here) to[(c + j) * p.os] = from_f<E>(plus ? r[j] + add[j] : r[j]);
@@ -286,7 +310,7 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
     tc_fence_before();
     if (split > 1) cluster_sync();   // the others have read this CTA's sums
     else __syncthreads();
-    if (warp == 1) tmem_dealloc(acc, S::kCols);
+    if (warp == 1) tmem_dealloc(acc, cols);
 }
 
 // ---- tiles of 256 rows of a by BN rows of b, each of a pair of CTAs.
@@ -296,8 +320,7 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
 // Warp 0 loads tiles, warp 2 scales, warp 1 issues, warps 4 to 11 empty the accumulators.
 //   SPLIT = 1: pairs are persistent and walk the tiles, with two accumulators in TMEM, so that a
 // tile's MMAs run while the one before is stored.  fp32 outputs take K in segments whose sums are
-// added in registers: the tensor cores cut an accumulator at each step, which over a long K would
-// cost more than fp32's own rounding.
+// added in registers.
 //   SPLIT = 2, 4: few tiles; a cluster of SPLIT pairs shares a tile's K and joins the sums through
 // distributed shared memory, each pair for its part of the columns.
 //
@@ -310,7 +333,6 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
 // no copies under way (8192^3 453 us, then 384, then 326), polling instead of suspended waits (512 x
 // 2048 x 512 11.3 us, then 7.3), the accumulator's stores behind its return to the MMAs.
 constexpr int kPairThreads = 384, kStoreWarps = 8;
-constexpr int kSegment = 64;                // blocks of K per segment of an fp32 output
 
 // A store warp's buffers: two of 32 rows of 64 bytes for tensor stores, or one of 32 x 17 fp32.
 constexpr int kStoreBuffer = 4096;
@@ -874,11 +896,14 @@ cudaError_t run_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
     const MatmulParams &p = args.p;
     if (!encode_operand(args.a, p.a, p.K, BT) || !encode_operand(args.b, p.b, p.K, kRows)) return cudaErrorInvalidValue;
     // as many parts of K as two CTAs per SM hold, of 4 blocks or more; for 32-bit outputs also as many
-    // as leave an accumulator kSegment blocks
+    // as leave a part kSegment blocks
     const int64_t tiles = ceil_div(p.b.rows, kRows) * ceil_div(p.a.rows, BT), blocks = ceil_div(p.K, kFp8Block);
     int split = 1;
     while (split < 8 && ((tiles * split * 2 <= 2 * sms && blocks >= 8 * split) || (p.dtype == kFP32 && blocks > split * kSegment))) split *= 2;
-    return launch_early(kernel, tiles * split, dim3(128), S::kSmem, stream, split, args, split);
+    // longer segments only of 16-bit outputs (choose)
+    const int64_t each = ceil_div(blocks, split), segment = std::max((int64_t)kSegment, ceil_div(each, S::kMostSums));
+    const int sums = (int)ceil_div(each, segment);
+    return launch_early(kernel, tiles * split, dim3(128), S::kSmem, stream, split, args, split, (int)segment, sums, S::cols(sums));
 }
 
 // Clusters of 4 and of 8 SMs of one part of the GPU that fit it: 36 and 15 of 152.
@@ -909,8 +934,11 @@ struct Choice {
 };
 
 Choice choose(const MatmulParams &p, int sms) {
-    if (p.a.rows <= 64) return {p.a.rows <= 16 ? 16 : p.a.rows <= 32 ? 32 : 64, 0, 0};
     const int64_t pairs = sms / 2, blocks = ceil_div(p.K, kFp8Block);
+    // few rows, but not of a K whose segments of 32-bit sums the tile kernel has no accumulators for
+    const int bt = p.a.rows <= 16 ? 16 : p.a.rows <= 32 ? 32 : p.a.rows <= 64 ? 64 : 0;
+    const int64_t most = bt == 16 ? TileShape<16>::kMostSums : bt == 32 ? TileShape<32>::kMostSums : TileShape<64>::kMostSums;
+    if (bt && (p.dtype != kFP32 || blocks <= 8 * most * kSegment)) return {bt, 0, 0};
     Choice best = {};
     double least = 0;
     for (const Choice c : {Choice{0, 224, 1}, Choice{0, 192, 1}, Choice{0, 128, 1}, Choice{0, 256, 2}, Choice{0, 128, 2}, Choice{0, 128, 4}}) {

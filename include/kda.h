@@ -481,7 +481,12 @@ kda_status kda_fp8_dequantize(const void *q, int64_t q_stride, int q_dtype, cons
  *
  *   out[m, n] = add[m, n] + sum_k a[m, k] b[n, k]
  *
- * of the values that they stand for, summed in fp32 and rounded to dtype once.
+ * of the values that they stand for, summed in fp32 and rounded to dtype once.  The tensor
+ * cores cut a sum towards zero at every 32 elements of K.  fp32 outputs let them sum 8192
+ * elements and add such sums with rounding: off by up to 5e-6 of sum |a b| where all products
+ * have one sign, by about 5e-7 of the outputs' size where signs vary, whatever K is.  16-bit
+ * outputs of more than 64 rows let them sum all of K, 4e-6 per 8192 elements of one sign: at
+ * K = 2^20 as much as their own rounding in fp16.
  *   a, a_scales    [M, K] of a_dtype (e4m3 or e5m2) with its scales; b, b_scales [N, K]
  *                  likewise.  Rows start at multiples of 16 bytes, rows of scales at multiples
  *                  of 4 (else KDA_ERR_ALIGN); what lies between two rows is not read
