@@ -93,7 +93,7 @@ def _plain_quantize(x, q, scales, qt, scales_t, tile) -> bool:
     try:
         dt, (R, C), dev = _args.DTYPES[x.dtype], x.shape, x.get_device()
         wx, br, bc = _args.width(x, C), -(-R // BLOCK), -(-C // BLOCK)
-        if not dev == _args.current_device() >= 0 or wx < 0:
+        if not 0 <= dev == _args.current_device() or wx < 0:
             return False
         code = pq = ps = pt = pst = None
         wq = ws = wt = wst = 0
@@ -128,7 +128,7 @@ def _plain_dequantize(q, scales, out) -> bool:
         return False
     tile, n = Rs != R, -(-C // BLOCK)
     if R != Ro or C != Co or Cs != n or (tile and Rs != -(-R // BLOCK)) or scales.dtype is not SCALE or \
-            not dev == out.get_device() == scales.get_device() == _args.current_device() >= 0:
+            not 0 <= dev == out.get_device() == scales.get_device() == _args.current_device():
         return False
     wq, ws, wo = _args.width(q, C), _args.width(scales, n), _args.width(out, C)
     if wq < 0 or ws < 0 or wo < 0:
@@ -153,7 +153,7 @@ def _plain_matmul(a, a_scales, b, b_scales, out, add) -> bool:
     ta, tb = Ma != M, Nb != N
     if (K != L or M != Mo or N != No or Ka != n or Kb != n or (ta and Ma != -(-M // BLOCK)) or (tb and Nb != -(-N // BLOCK))
             or a_scales.dtype is not SCALE or b_scales.dtype is not SCALE
-            or not dev == b.get_device() == out.get_device() == a_scales.get_device() == b_scales.get_device() == _args.current_device() >= 0):
+            or not 0 <= dev == b.get_device() == out.get_device() == a_scales.get_device() == b_scales.get_device() == _args.current_device()):
         return False
     wa, wb, wo, was, wbs = _args.width(a, K), _args.width(b, K), _args.width(out, N), _args.width(a_scales, n), _args.width(b_scales, n)
     if wa < 0 or wb < 0 or wo < 0 or was < 0 or wbs < 0 or wp < 0:

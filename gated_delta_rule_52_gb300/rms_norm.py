@@ -39,7 +39,7 @@ def _plain_fwd(x, weight, eps, out, residual, residual_out, rstd, scales) -> boo
     try:
         kind, (R, D), dev = x.dtype, x.shape, x.get_device()
         dt, ot = _args.DTYPES[kind], out.dtype
-        if out.shape != (R, D) or not out.get_device() == dev == _args.current_device() >= 0:
+        if out.shape != (R, D) or not 0 <= dev == out.get_device() == _args.current_device():
             return False
         wx, wo, ps, ws, pr, wr, po, wro = _args.width(x, D), _args.width(out, D), None, 0, None, 0, None, 0
         if ot is kind:
@@ -105,7 +105,7 @@ def _plain_bwd(dout, x, weight, rstd, dresidual, want_dweight):
     try:
         kind, (R, D), dev = x.dtype, x.shape, x.get_device()
         dt, wx, wd, pr, wr = _args.DTYPES[kind], _args.width(x, D), _args.width(dout, D), None, 0
-        if dout.dtype is not kind or dout.shape != (R, D) or not dout.get_device() == dev == _args.current_device() >= 0:
+        if dout.dtype is not kind or dout.shape != (R, D) or not 0 <= dev == dout.get_device() == _args.current_device():
             return None
         if dresidual is not None:
             if dresidual.dtype is not kind or dresidual.shape != (R, D) or dresidual.get_device() != dev:
