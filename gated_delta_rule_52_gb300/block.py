@@ -297,8 +297,7 @@ def train(blocks, steps, B, T, gen, lr=2e-3):
 
 @torch.no_grad()
 def serve(blocks, u, prompt):
-    """The outputs of a stack (all of its blocks in 8 bits, or none) with ``prompt`` tokens in one call
-    and the others one by one."""
+    """The outputs of a stack with ``prompt`` tokens in one call and the others one by one."""
     states = [b.state(u.shape[0]) for b in blocks]
     outs = []
     for lo, hi in [(0, prompt)] + [(t, t + 1) for t in range(prompt, u.shape[1])]:
@@ -308,6 +307,8 @@ def serve(blocks, u, prompt):
             if b.eight:
                 delta = b.serve_eight(h, delta, s)
             else:
+                if delta is not None:            # what a block in 8 bits has left to add
+                    h, delta = h + delta, None
                 h = b.serve(h, s)
         outs.append(h if delta is None else h + delta)
     return torch.cat(outs, 1)
