@@ -438,6 +438,8 @@ kda_status kda_short_conv_bwd(const void *x, int64_t x_stride, const float *weig
  *                  KDA_DTYPE_E4M3 or KDA_DTYPE_E5M2 with `scales` [rows, ceil(D/128)]
  *   residual_out   [rows, D] of dtype: takes h (it may be x or residual), or NULL
  *   rstd           fp32 [rows] or NULL (not written), for kda_rms_norm_bwd
+ * Squares are summed in fp32: of a row whose sum leaves fp32's range (magnitudes from about 2^60
+ * on), rstd is 0 and so is out.
  * KDA_ERR_VALUE for eps negative or not finite; KDA_ERR_NULL for residual_out without a
  * residual, or 8-bit outputs without scales.
  */
@@ -472,7 +474,8 @@ kda_status kda_fp8_quantize(const void *x, int64_t x_stride, int dtype, void *q,
                             int64_t scales_stride, void *qt, int64_t qt_stride, void *scales_t, int64_t scales_t_stride,
                             int q_dtype, int tile, int64_t rows, int64_t cols, void *stream);
 
-/* kda_fp8_dequantize — the values that an 8-bit tensor stands for, [rows, cols] of dtype. */
+/* kda_fp8_dequantize — the values that an 8-bit tensor stands for, [rows, cols] of dtype.  Values
+   below 2^-126 in magnitude become 0. */
 kda_status kda_fp8_dequantize(const void *q, int64_t q_stride, int q_dtype, const void *scales, int64_t scales_stride, int tile,
                               void *out, int64_t out_stride, int dtype, int64_t rows, int64_t cols, void *stream);
 
