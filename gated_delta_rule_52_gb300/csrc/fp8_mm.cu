@@ -19,6 +19,7 @@ using namespace layer;
 using namespace sm103;
 
 constexpr uint64_t kWait = 2000000000ull;   // 2 s per wait
+constexpr uint64_t kLate = kWait / 100;     // of copies under way where a wait has expired already
 constexpr int kRows = 128;                  // rows of b per tile: the MMA's M, TMEM's lanes
 constexpr int kScaleStages = 8, kAhead = 4;   // groups of 4 blocks' scales: places, and on their way
 // Blocks of K in one accumulator where the output has 32 bits.  The tensor cores cut an accumulator at
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
         // the copies end before the CTA does: the last loads of all slots, in order
         if (early < S::kStages) slot.at = 0;
         for (int i = 0; i < early; ++i) {
-            if (!warp_wait<false>(&full[slot.at], early < S::kStages ? 0 : slot.turn)) ok = false;
+            if (!warp_wait<false>(&full[slot.at], early < S::kStages ? 0 : slot.turn, ok ? kWait : kLate)) ok = false;
             slot.next();
         }
     } else if (warp == 1) {
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
             for (int m = 0; m < loads; ++m) {
                 slot.at = slot.at == 0 ? S::kStages - 1 : slot.at - 1;
                 if (slot.at == S::kStages - 1) slot.turn ^= 1;
-                if (!warp_wait<false>(&full[slot.at], slot.turn)) ok = false;
+                if (!warp_wait<false>(&full[slot.at], slot.turn, ok ? kWait : kLate)) ok = false;
             }
     } else if (warp == 1 && rank == 0) {
         // ---- MMAs of the pair
