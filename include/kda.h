@@ -438,8 +438,8 @@ kda_status kda_short_conv_bwd(const void *x, int64_t x_stride, const float *weig
  *                  KDA_DTYPE_E4M3 or KDA_DTYPE_E5M2 with `scales` [rows, ceil(D/128)]
  *   residual_out   [rows, D] of dtype: takes h (it may be x or residual), or NULL
  *   rstd           fp32 [rows] or NULL (not written), for kda_rms_norm_bwd
- * Squares are summed in fp32: of a row whose sum leaves fp32's range (magnitudes from about 2^60
- * on), rstd is 0 and so is out.
+ * Values below 2^-126 count as 0.  Squares are summed in fp32: of a row whose sum leaves fp32's
+ * range (magnitudes from about 2^57 on), rstd is 0 and so is out.
  * KDA_ERR_VALUE for eps negative or not finite; KDA_ERR_NULL for residual_out without a
  * residual, or 8-bit outputs without scales.
  */
