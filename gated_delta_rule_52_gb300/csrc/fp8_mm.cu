@@ -889,7 +889,7 @@ bool encode_out(CUtensorMap &map, const MatmulParams &p) {
 }
 
 template <typename E, int BT>
-cudaError_t run_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
+cudaError_t launch_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
     using S = TileShape<BT>;
     constexpr auto kernel = mm_tile_kernel<E, BT>;
     const cudaError_t e = allow_smem<kernel>(S::kSmem);
@@ -901,10 +901,29 @@ cudaError_t run_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
     const int64_t tiles = ceil_div(p.b.rows, kRows) * ceil_div(p.a.rows, BT), blocks = ceil_div(p.K, kFp8Block);
     int split = 1;
     while (split < 8 && ((tiles * split * 2 <= 2 * sms && blocks >= 8 * split) || (p.dtype == kFP32 && blocks > split * kSegment))) split *= 2;
-    // longer segments only of 16-bit outputs (choose)
+    // longer segments only of 16-bit outputs (run_tile)
     const int64_t each = ceil_div(blocks, split), segment = std::max((int64_t)kSegment, ceil_div(each, S::kMostSums));
     const int sums = (int)ceil_div(each, segment);
     return launch_early(kernel, tiles * split, dim3(128), S::kSmem, stream, split, args, split, (int)segment, sums, S::cols(sums));
+}
+
+// A 32-bit output of a K with more segments than 8 CTAs have accumulators for takes it a piece at a time, each
+// added to what the ones before have left in out.  (40 x 256 x 262144 with an addend 94 us, by pairs of CTAs, which
+// empty their accumulators after each segment, 508 us.)
+template <typename E, int BT>
+cudaError_t run_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
+    const MatmulParams whole = args.p;
+    const int64_t most = whole.dtype == kFP32 ? int64_t(8) * TileShape<BT>::kMostSums * kSegment * kFp8Block : whole.K;
+    MatmulParams &p = args.p;
+    for (int64_t k = 0; k < whole.K; k += most) {
+        p.K = std::min(most, whole.K - k);
+        p.a.q = static_cast<const uint8_t *>(whole.a.q) + k, p.b.q = static_cast<const uint8_t *>(whole.b.q) + k;
+        p.a.s = whole.a.s + k / kFp8Block, p.b.s = whole.b.s + k / kFp8Block;
+        if (k > 0) p.add = p.out, p.as = p.os;
+        const cudaError_t e = launch_tile<E, BT>(args, sms, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 // Clusters of 4 and of 8 SMs of one part of the GPU that fit it: 36 and 15 of 152.
@@ -935,11 +954,8 @@ struct Choice {
 };
 
 Choice choose(const MatmulParams &p, int sms) {
+    if (p.a.rows <= 64) return {p.a.rows <= 16 ? 16 : p.a.rows <= 32 ? 32 : 64, 0, 0};
     const int64_t pairs = sms / 2, blocks = ceil_div(p.K, kFp8Block);
-    // few rows, but not of a K whose segments of 32-bit sums the tile kernel has no accumulators for
-    const int bt = p.a.rows <= 16 ? 16 : p.a.rows <= 32 ? 32 : p.a.rows <= 64 ? 64 : 0;
-    const int64_t most = bt == 16 ? TileShape<16>::kMostSums : bt == 32 ? TileShape<32>::kMostSums : TileShape<64>::kMostSums;
-    if (bt && (p.dtype != kFP32 || blocks <= 8 * most * kSegment)) return {bt, 0, 0};
     Choice best = {};
     double least = 0;
     for (const Choice c : {Choice{0, 224, 1}, Choice{0, 192, 1}, Choice{0, 128, 1}, Choice{0, 256, 2}, Choice{0, 128, 2}, Choice{0, 128, 4}}) {

@@ -62,3 +62,26 @@ def test_sums_of_a_long_k(M, N, K):
     # each segment added once, and up to 8 parts of K joined
     off = (out.double() - want).abs() / want * 2 ** 24
     assert float(off.max()) <= len(parts) + 8
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 40, 400001), (20, 131, 500003), (1, 33, 2000000)])
+@pytest.mark.parametrize("add", ["own", "row", "out"])
+def test_addends_of_a_long_k(M, N, K, add):
+    """A K that few rows take in pieces: the addend counts once, also in place.  Whole numbers, exact sums."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    a, sa, b, sb = *fp8.empty(M, K, E4), *fp8.empty(N, K, E4)
+    for q, s in ((a, sa), (b, sb)):
+        q.copy_(torch.randint(-3, 4, q.shape, generator=g, device="cuda").float())
+        s.view(torch.uint8).fill_(127)
+    out = torch.full((M, N), float("nan"), device="cuda")
+    plus = torch.randint(-99, 100, (1 if add == "row" else M, N), generator=g, device="cuda").float().expand(M, N)
+    want = a.float() @ b.float().T
+    want = want.double() + plus.double()
+    assert float(want.abs().max()) < 2 ** 20
+    if add == "out":
+        out.copy_(plus)
+        plus = out
+    fp8.matmul(a, sa, b, sb, out, add=plus)
+    torch.cuda.synchronize()
+    assert kda.get_device_status() == kda.KDA_OK
+    assert torch.equal(out.double(), want)
