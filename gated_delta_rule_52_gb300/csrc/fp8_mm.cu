@@ -101,8 +101,8 @@ struct ScaleRows {
 // The rows of b, of which nearly all bytes are, lie along the MMA's M, so that tiles are full however
 // few rows a has.  Two CTAs per SM keep up to 180 KB of loads in flight.
 //
-// Bound by reading b: 1 x 8192 x 8192 takes 14.2 us, 64 rows 17.2 us, and 67 MB more of b 10.7 us more
-// (6.3 TB/s); 3.5 us go to the way into the pipeline and out of it.  With one lane of a warp issuing
+// Bound by reading b: 1 x 8192 x 8192 takes 14.5 us, 16 rows 15.9, 64 rows 17.6 (64 x 8192 x 65536 90
+// us), and 67 MB more of b 10.7 us more (6.3 TB/s); 3.5 us go to the way into the pipeline and out of it.  With one lane of a warp issuing
 // behind a branch 1 x 8192 x 8192 took 21 us, with one CTA per SM 24 us, with the sums of one row at
 // a time on their way 64 rows took 19.7 us.
 //
@@ -325,10 +325,12 @@ __global__ void __launch_bounds__(128) mm_tile_kernel(const __grid_constant__ Ma
 //   SPLIT = 2, 4: few tiles; a cluster of SPLIT pairs shares a tile's K and joins the sums through
 // distributed shared memory, each pair for its part of the columns.
 //
-// 8192 x 8192 x 8192 e4m3 to bf16: 302 us, 3.64 PFLOP/s, 1.9 times what bf16 products of a library reach
-// on the same card (364 us when they follow one another for a second, under the power cap); the
-// tensor pipe is active for 83% of the time.  A block of 128 of K costs an SM 256 + BN cycles to load
-// at 64 bytes a cycle, and 2 BN to multiply: wide tiles for many, and where tiles are few more of them.
+// 8192 x 8192 x 8192 e4m3 to bf16: 363 to 374 us, 3.0 PFLOP/s, where calls follow one another for a
+// second, under the power cap, and 302 us, 3.64 PFLOP/s, in short runs: 1.8 and 1.9 times what bf16
+// products of a library reach on the same card; the tensor pipe is active for 83% of the time.  A weight
+// gradient, 8192 x 2048 x 16384 to fp32 with an addend, 234 us and 212 (2.35 and 2.6 PFLOP/s).  A block
+// of 128 of K costs an SM 256 + BN cycles to load at 64 bytes a cycle, and 2 BN to multiply: wide tiles
+// for many, and where tiles are few more of them.
 // What it took: all of a warp at the waits, one elected lane at the issue (4096^3 74 us instead of
 // 80), scales in 8 groups of places with 4 on their way and handed to the other CTA by a warp that has
 // no copies under way (8192^3 453 us, then 384, then 326), polling instead of suspended waits (512 x

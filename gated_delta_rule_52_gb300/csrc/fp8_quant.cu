@@ -5,9 +5,10 @@
 // results come from there, the transposed one by way of shared memory.
 //
 // 8192 x 8192 bf16: one way 36.7 us (81% of the copy rate), both ways 50.8 us (78%), by tiles 45.4 us
-// (88%); 8192 x 2048 fp32 by tiles both ways 20.5 us (73%).  Bound by issue (74% of the slots: a row's
-// and a column's maximum, two scalings and two conversions per element) and, in 32 bits, by the tiles
-// in flight.  Unaligned rows are loaded and stored element by element (8192 x 8191 both ways 92 us).
+// (88%); 8192 x 2048 fp32 by tiles both ways 20 us (75%), 8192 x 8192 67 us (89%).  Bound by issue (74% of
+// the slots: a row's and a column's maximum, two scalings and two conversions per element); in 32 bits
+// by memory, and of few tiles by rounds: 1024 CTAs on 304 places are 3.4, which take 4, and a CTA loads
+// no further tile while it stores.  Unaligned rows are loaded and stored element by element (8192 x 8191 both ways 92 us).
 // Back: 8192 x 8192 to bf16 31.2 us (96%).
 #include <algorithm>
 
