@@ -102,9 +102,9 @@ struct ScaleRows {
 // few rows a has.  Two CTAs per SM keep up to 180 KB of loads in flight.
 //
 // Bound by reading b: 1 x 8192 x 8192 takes 14.5 us, 16 rows 15.9, 64 rows 17.6 (64 x 8192 x 65536 90
-// us), and 67 MB more of b 10.7 us more (6.3 TB/s); 3.5 us go to the way into the pipeline and out of it.  With one lane of a warp issuing
-// behind a branch 1 x 8192 x 8192 took 21 us, with one CTA per SM 24 us, with the sums of one row at
-// a time on their way 64 rows took 19.7 us.
+// us), and 67 MB more of b 10.7 us more (6.3 TB/s); 3.5 us go to the way into the pipeline and out of
+// it.  With one lane of a warp issuing behind a branch 1 x 8192 x 8192 took 21 us, with one CTA per SM
+// 24 us, with the sums of one row at a time on their way 64 rows took 19.7 us.
 //
 // A long K has an accumulator for each segment, `sums` of them, which are added in registers at the
 // end.  A CTA takes up to half of the SM's TMEM, so that the two of an SM never wait for each other's:
@@ -909,9 +909,9 @@ cudaError_t launch_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
     return launch_early(kernel, tiles * split, dim3(128), S::kSmem, stream, split, args, split, (int)segment, sums, S::cols(sums));
 }
 
-// A 32-bit output of a K with more segments than 8 CTAs have accumulators for takes it a piece at a time, each
-// added to what the ones before have left in out.  (40 x 256 x 262144 with an addend 94 us, by pairs of CTAs, which
-// empty their accumulators after each segment, 508 us.)
+// A 32-bit output of a K with more segments than 8 CTAs have accumulators for takes it a piece at a time,
+// each added to what the ones before have left in out.  (40 x 256 x 262144 with an addend 94 us; by pairs
+// of CTAs, which empty their accumulators after each segment, 508 us.)
 template <typename E, int BT>
 cudaError_t run_tile(MatmulArgs &args, int sms, cudaStream_t stream) {
     const MatmulParams whole = args.p;
