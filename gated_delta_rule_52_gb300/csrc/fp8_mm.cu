@@ -664,23 +664,34 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
                 };
                 // 64 bytes of every row to one of the two buffers (16-byte piece j of row r at
                 // j ^ (r / 2 % 4), the 64-byte swizzle), and from there by a tensor store, which leaves
-                // out what is outside.  The buffers alternate with the stores, also from a tile to the
+                // out rows that are outside and what is outside of a row but for the rest of the last 16
+                // bytes: a row that ends inside of those is stored by single elements.  The buffers alternate with the stores, also from a tile to the
                 // next, which may have an odd number: the one store that the wait leaves out is always the
                 // other buffer's.
                 const auto send = [&](int c, const Pack<E, V> (&piece)[4]) {
                     if (c >= left || m0 >= p.a.rows) return;
                     unsigned char *buffer = own + turn * 2048;
-                    turn ^= 1;
                     if (lane == 0) bulk_wait_read1();
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 4; ++j) *reinterpret_cast<Pack<E, V> *>(buffer + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = piece[j];
+                    if (left - c < kStep && (left - c) % V) {
+                        __syncwarp();
+                        E *to = static_cast<E *>(p.out) + m0 * p.os + n0 + c + lane;
+#pragma unroll 1
+                        for (int r = 0; r < 32; ++r, to += p.os)
+                            if (lane < left - c && m0 + r < p.a.rows)
+                                *to = reinterpret_cast<const E *>(buffer + r * 64 + ((lane / V ^ (r >> 1 & 3)) << 4))[lane % V];
+                        __syncwarp();
+                        return;                              // (no store reads this buffer: it is the next one's, too)
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         tma_store_2d(&args.out, buffer, (int)(n0 + c), (int)m0);
                         bulk_commit();
                     }
+                    turn ^= 1;
                 };
                 // this lane's row (or where rows are not wide: its share of 32 rows), which begins as the
                 // addend's, read while the MMAs run; the sums of the segments of K are added to it
